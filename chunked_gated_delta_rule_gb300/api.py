@@ -17,7 +17,7 @@ import torch
 
 from . import build as _build
 
-GDR_F32, GDR_BF16, GDR_F16 = 0, 1, 2
+GDR_F32, GDR_BF16, GDR_F16, GDR_E4M3, GDR_I8 = 0, 1, 2, 3, 4
 
 
 class gdr_dims(ctypes.Structure):
@@ -43,6 +43,16 @@ class gdr_options(ctypes.Structure):
                 ("grid_limit", ctypes.c_int32)]
 
 
+class gdr_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("dtype", ctypes.c_int32),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3)]
+
+
 # Diagnostic entry points declared in include/gdr_selftest.h.
 SELFTEST_EXPORTS = ("gdr_selftest_umma", "gdr_selftest_tma", "gdr_selftest_inverse",
                     "gdr_selftest_timeout")
@@ -50,7 +60,8 @@ SELFTEST_EXPORTS = ("gdr_selftest_umma", "gdr_selftest_tma", "gdr_selftest_inver
 # Every symbol include/gdr.h declares.
 EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_ex", "gdr_chunk_fwd_host", "gdr_chunk_fwd_noalloc",
            "gdr_workspace_size", "gdr_plan_query", "gdr_recurrent_fwd", "gdr_kernel_name", "gdr_error_string",
-           "gdr_release_cached", "gdr_version", "gdr_chunk_bwd", "gdr_bwd_workspace_size")
+           "gdr_release_cached", "gdr_version", "gdr_chunk_bwd", "gdr_bwd_workspace_size",
+           "gdr_cache_write", "gdr_cache_read", "gdr_paged_attn", "gdr_attn_workspace_size")
 
 _lib = None
 _lock = threading.Lock()
@@ -111,6 +122,15 @@ def load_library():
         lib.gdr_selftest_timeout.restype = ctypes.c_int
         lib.gdr_selftest_inverse.argtypes = [vp, vp, vp]
         lib.gdr_selftest_inverse.restype = ctypes.c_int
+        cache_p = ctypes.POINTER(gdr_paged_cache)
+        for name in ("gdr_cache_write", "gdr_cache_read"):
+            getattr(lib, name).argtypes = [dims_p, cache_p, vp, vp, i32p, vp, vp]
+            getattr(lib, name).restype = ctypes.c_int
+        lib.gdr_paged_attn.argtypes = [dims_p, cache_p, vp, i32p, vp, vp, ctypes.c_int,
+                                       ctypes.c_int64, ctypes.POINTER(gdr_options), vp]
+        lib.gdr_paged_attn.restype = ctypes.c_int
+        lib.gdr_attn_workspace_size.argtypes = [dims_p, cache_p]
+        lib.gdr_attn_workspace_size.restype = ctypes.c_size_t
         lib.gdr_release_cached.argtypes = []
         lib.gdr_release_cached.restype = ctypes.c_int
         lib.gdr_version.argtypes = []
@@ -396,6 +416,176 @@ def gdr_recurrent_fwd(q, k, v, g, beta=None, cu_seqlens=None, *, state, state_in
     if rc != 0:
         raise GdrError(rc)
     return o
+
+
+_CACHE_DTYPES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16, torch.float16: GDR_F16,
+                 torch.float8_e4m3fn: GDR_E4M3, torch.int8: GDR_I8}
+
+
+def _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, dev):
+    """The C struct of a paged cache; sizes, types and devices checked."""
+    fmt = _CACHE_DTYPES.get(k_cache.dtype)
+    if fmt is None or v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must share a dtype: float32, bfloat16, float16, "
+                        f"float8_e4m3fn or int8, got {k_cache.dtype} and {v_cache.dtype}")
+    if k_cache.dim() != 4 or v_cache.dim() != 4 or k_cache.shape[:3] != v_cache.shape[:3]:
+        raise ValueError("k_cache and v_cache must be [pages, page size, heads, K] and [.., V]")
+    P, page, H, _ = k_cache.shape
+    strides = []
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if t.is_contiguous():
+            strides.append((0, 0, 0))
+        elif t.stride(-1) == 1 and min(t.stride()) > 0:
+            strides.append(t.stride()[:3])
+        else:
+            raise ValueError(f"{name} needs a contiguous last dimension")
+    if (fmt >= GDR_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale belong to an 8-bit cache, both of them")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _check(name, t, torch.float32, dev)
+        if t is not None and t.shape != (P, H, page):
+            raise ValueError(f"{name} must be [pages, heads, page size]")
+    _check("page_table", page_table, torch.int32, dev)
+    _check("kv_lens", kv_lens, torch.int32, dev)
+    if page_table.dim() != 2 or page_table.shape[0] != nseq or kv_lens.shape != (nseq,):
+        raise ValueError("page_table must be [sequences, pages a sequence], kv_lens [sequences]")
+    c = gdr_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(),
+                        None if k_scale is None else k_scale.data_ptr(),
+                        None if v_scale is None else v_scale.data_ptr(),
+                        page_table.data_ptr(), kv_lens.data_ptr(), P, page, page_table.shape[1],
+                        H, fmt)
+    c.k_stride[:], c.v_stride[:] = strides
+    return c
+
+
+def _paged_call(fn, dev, stream, *args):
+    """Calls a library function on ``stream`` (default: the current one)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        rc = fn(*args, ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise GdrError(rc)
+
+
+def gdr_cache_write(k, v, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
+                    k_scale=None, v_scale=None, status=None, stream=None):
+    """Stores the new tokens' ``k`` [B, T, H, K] and ``v`` [B, T, H, V] in the
+    paged cache ``k_cache`` [P, page size, H, K], ``v_cache`` [.., V], in place.
+    ``kv_lens`` [N] counts each sequence's tokens including the new ones: token
+    i of the L new ones goes to position ``kv_lens[n] - L + i``, slot ``position
+    % page size`` of page ``page_table[n, position // page size]``.  A cache of
+    q's dtype holds the rows as they are; a float8_e4m3fn or int8 cache holds
+    them quantised, with a scale for each (token, head) row in ``k_scale`` and
+    ``v_scale`` [P, H, page size] (float32)."""
+    lib = load_library()
+    dev = k.device
+    if dev.type != "cuda":
+        raise ValueError("gdr_cache_write takes CUDA tensors")
+    _check("v", v, k.dtype, dev, strided=True)
+    _check_cu(cu_seqlens, dev)
+    dims = _dims_of(k, v, cu_seqlens, k=k)
+    dims.q_stride[:] = (0, 0)
+    if v.shape[:-1] != k.shape[:-1] or k_cache.shape[2:] != k.shape[2:] or \
+            v_cache.shape[-1] != v.shape[-1]:
+        raise ValueError("k, v and the caches must agree in tokens, heads and widths")
+    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale,
+                      dims.N if cu_seqlens is not None else dims.B, dev)
+    _paged_call(lib.gdr_cache_write, dev, stream, ctypes.byref(dims), ctypes.byref(cache), _ptr(k),
+                _ptr(v), _ptr(cu_seqlens), _ptr(status))
+
+
+def gdr_cache_read(k_cache, v_cache, page_table, kv_lens, T, cu_seqlens=None, *, k_scale=None,
+                   v_scale=None, dtype=None, k=None, v=None, status=None, stream=None):
+    """What the paged cache holds for the last tokens of every sequence, as
+    ``(k, v)`` [B, T, H, K] and [B, T, H, V]: ``T`` tokens of each sequence, or
+    with ``cu_seqlens`` the packed lengths (T their sum, B = 1).  ``dtype`` is
+    the cache's own unless that is an 8-bit format (then bfloat16 by default);
+    ``k`` and ``v`` may be given to write into."""
+    lib = load_library()
+    dev = k_cache.device
+    if dev.type != "cuda":
+        raise ValueError("gdr_cache_read takes CUDA tensors")
+    _check_cu(cu_seqlens, dev)
+    if k_cache.dim() != 4 or v_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [pages, page size, heads, K] and [.., V]")
+    B = kv_lens.numel() if cu_seqlens is None else 1
+    if dtype is None:
+        dtype = k.dtype if k is not None else (
+            k_cache.dtype if k_cache.element_size() > 1 else torch.bfloat16)
+    H, K, V = k_cache.shape[2], k_cache.shape[3], v_cache.shape[3]
+    k = torch.empty(B, T, H, K, dtype=dtype, device=dev) if k is None else k
+    v = torch.empty(B, T, H, V, dtype=dtype, device=dev) if v is None else v
+    for name, t, shape in (("k", k, (B, T, H, K)), ("v", v, (B, T, H, V))):
+        _check(name, t, dtype, dev, strided=True)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+    dims = _dims_of(k, v, cu_seqlens, k=k)
+    dims.q_stride[:] = (0, 0)
+    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale,
+                      dims.N if cu_seqlens is not None else dims.B, dev)
+    _paged_call(lib.gdr_cache_read, dev, stream, ctypes.byref(dims), ctypes.byref(cache), _ptr(k),
+                _ptr(v), _ptr(cu_seqlens), _ptr(status))
+    return k, v
+
+
+def gdr_paged_attn(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *, k_scale=None,
+                   v_scale=None, causal=True, window=0, scale=0.0, max_seqlen=None, o=None,
+                   lse=None, force_path=0, grid_limit=0, workspace=None, status=None,
+                   stream=None, timer=None):
+    """Softmax attention of the new tokens ``q`` [B, T, Hq, K] over the paged
+    cache (laid out as for :func:`gdr_cache_write`, which put the new tokens'
+    own keys and values there).  Token i, at position p, sees the positions
+    below ``kv_lens[n]``, up to p when ``causal`` and above ``p - window`` when
+    ``window`` > 0; Hq is a multiple of the cache's heads.  Returns ``(o,
+    lse)``: o [B, T, Hq, V] in q's dtype and the log of the softmax's
+    denominator [B, T, Hq] (float32); a row that sees nothing has o = 0 and lse
+    = -inf.  ``max_seqlen`` is the most new tokens of a sequence when the
+    caller knows it (a planning hint).  Work is enqueued on ``stream`` (default:
+    the current one) and not synchronised."""
+    lib = load_library()
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("gdr_paged_attn takes CUDA tensors")
+    _check_cu(cu_seqlens, dev)
+    if q.dim() != 4 or k_cache.dim() != 4 or v_cache.dim() != 4 or q.shape[-1] != k_cache.shape[-1]:
+        raise ValueError("q must be [B, T, heads, K], the caches [pages, page size, heads, K or V]")
+    shape = (*q.shape[:3], v_cache.shape[3])
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=dev)
+    elif o.shape != shape:
+        raise ValueError("o must be [B, T, heads, V]")
+    if lse is None:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    elif lse.shape != shape[:3]:
+        raise ValueError("lse must be [B, T, heads]")
+    _check("o", o, q.dtype, dev, strided=True)
+    _check("lse", lse, torch.float32, dev)
+    dims = make_dims(*q.shape[:3], q.shape[3], shape[3],
+                     0 if cu_seqlens is None else cu_seqlens.numel() - 1, _dtype_code(q.dtype),
+                     GDR_SEQLENS_I64 if cu_seqlens is not None and cu_seqlens.dtype == torch.int64
+                     else 0, 0 if max_seqlen is None else int(max_seqlen))
+    dims.q_stride[:], dims.o_stride[:] = _row_strides(q), _row_strides(o)
+    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale,
+                      dims.N if cu_seqlens is not None else dims.B, dev)
+    if cache.dtype < GDR_E4M3 and k_cache.dtype != q.dtype:
+        raise TypeError(f"the caches must be {q.dtype} or an 8-bit format, got {k_cache.dtype}")
+    opt = gdr_options(float(scale), int(force_path), 0,
+                      None if workspace is None else workspace.data_ptr(),
+                      0 if workspace is None else workspace.numel() * workspace.element_size(),
+                      None if status is None else status.data_ptr())
+    opt.grid_limit = int(grid_limit)
+    if timer is not None:
+        opt.events = ctypes.cast(timer._handles, ctypes.c_void_p)
+        opt.max_launches = timer.max
+        opt.launch_ids = ctypes.cast(timer._ids, ctypes.c_void_p)
+        opt.n_launches = ctypes.cast(ctypes.pointer(timer._count), ctypes.c_void_p)
+    _paged_call(lib.gdr_paged_attn, dev, stream, ctypes.byref(dims), ctypes.byref(cache), _ptr(q),
+                _ptr(cu_seqlens), _ptr(o), _ptr(lse), int(bool(causal)), int(window),
+                ctypes.byref(opt))
+    return o, lse
 
 
 def gdr_chunk_fwd_host(q, k, v, g, beta=None, cu_seqlens=None, h0=None, *, n_segments=0,

@@ -1,0 +1,149 @@
+// attn_api.cu -- host side of the paged cache and of the attention over it:
+// argument checks, choice of kernel, scratch, launches.
+#include <cmath>
+
+#include "attn.cuh"
+#include "gdr_launch.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int64_t kMaxPagedV = 256;
+
+// The cache against the call's sizes.  `heads` is what the call's k and v
+// have (the cache's own), or its query heads, a multiple of the cache's.
+int check_cache(const gdr_dims &d, const gdr_paged_cache *c, bool attention) {
+    if (!c || !c->k || !c->v || !c->page_table || !c->kv_lens) return GDR_ERR_INVALID;
+    if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->H < 1) return GDR_ERR_INVALID;
+    const bool quant = cache_quantised(c->dtype);
+    if (!quant && c->dtype != d.dtype) return GDR_ERR_INVALID;
+    if (quant && (!c->k_scale || !c->v_scale)) return GDR_ERR_INVALID;
+    if (attention ? d.H % c->H != 0 : d.H != c->H) return GDR_ERR_INVALID;
+    for (const int64_t *s : {c->k_stride, c->v_stride}) {
+        const int zeros = (s[0] == 0) + (s[1] == 0) + (s[2] == 0);
+        if ((zeros != 0 && zeros != 3) || s[0] < 0 || s[1] < 0 || s[2] < 0) return GDR_ERR_INVALID;
+    }
+    if (d.V > kMaxPagedV) return GDR_ERR_UNSUPPORTED;
+    if (c->n_pages > INT32_MAX || c->page_size > INT32_MAX || c->H > 65535 ||
+        c->max_pages > INT32_MAX / c->page_size)
+        return GDR_ERR_UNSUPPORTED;  // positions fit 31 bits
+    return GDR_OK;
+}
+
+int64_t seqs_of(const gdr_dims &d) { return d.N > 0 ? d.N : d.B; }
+
+PagedCache device_cache(const gdr_dims &d, const gdr_paged_cache &c) {
+    PagedCache p{};
+    p.k = c.k; p.v = c.v; p.ks = c.k_scale; p.vs = c.v_scale;
+    p.table = c.page_table; p.kv_lens = c.kv_lens;
+    p.max_pages = c.max_pages;
+    p.n_pages = (int32_t)c.n_pages; p.page_size = (int32_t)c.page_size;
+    p.H = (int32_t)c.H; p.dtype = c.dtype;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t dk[3] = {c.page_size * c.H * d.K, c.H * d.K, d.K};
+        const int64_t dv[3] = {c.page_size * c.H * d.V, c.H * d.V, d.V};
+        p.kst[i] = c.k_stride[0] ? c.k_stride[i] : dk[i];
+        p.vst[i] = c.v_stride[0] ? c.v_stride[i] : dv[i];
+    }
+    return p;
+}
+
+TokenRows token_rows(const gdr_dims &d, const int32_t *cu, int32_t *status) {
+    TokenRows r{};
+    if (cu && (d.flags & GDR_SEQLENS_I64)) r.cu64 = reinterpret_cast<const int64_t *>(cu);
+    else r.cu = cu;
+    r.N = seqs_of(d);
+    r.T = d.T;
+    r.status = status;
+    return r;
+}
+
+int cache_call(bool write, const gdr_dims *dims, const gdr_paged_cache *cache, const void *k,
+               const void *v, const int32_t *cu, int32_t *status, gdr_stream_t stream) {
+    int rc = check_dims(dims);
+    if (rc != GDR_OK) return rc;
+    if (!k || !v || (cu != nullptr) != (dims->N > 0)) return GDR_ERR_INVALID;
+    rc = check_cache(*dims, cache, false);
+    if (rc != GDR_OK) return rc;
+    if (!write) {  // outputs: two rows must not share an address
+        gdr_dims o = *dims;
+        for (int i = 0; i < 2; ++i) o.o_stride[i] = dims->v_stride[i];
+        if (check_dims(&o) != GDR_OK) return GDR_ERR_INVALID;
+        for (int i = 0; i < 2; ++i) o.o_stride[i] = dims->k_stride[i];
+        o.V = dims->K;
+        if (check_dims(&o) != GDR_OK) return GDR_ERR_INVALID;
+    }
+    return cache_rows(write, device_cache(*dims, *cache), token_rows(*dims, cu, status),
+                      dims->dtype, k, v, dims_stride(dims->k_stride, dims->H, dims->K),
+                      dims_stride(dims->v_stride, dims->H, dims->V), (int)dims->K, (int)dims->V,
+                      reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" {
+
+int gdr_cache_write(const gdr_dims *dims, const gdr_paged_cache *cache, const void *k,
+                    const void *v, const int32_t *cu_seqlens, int32_t *status,
+                    gdr_stream_t stream) {
+    return cache_call(true, dims, cache, k, v, cu_seqlens, status, stream);
+}
+
+int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, void *v,
+                   const int32_t *cu_seqlens, int32_t *status, gdr_stream_t stream) {
+    return cache_call(false, dims, cache, k, v, cu_seqlens, status, stream);
+}
+
+size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cache) {
+    if (check_dims(dims) != GDR_OK || check_cache(*dims, cache, true) != GDR_OK) return 0;
+    return 256;
+}
+
+int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const void *q,
+                   const int32_t *cu_seqlens, void *o, float *lse, int causal, int64_t window,
+                   const gdr_options *opt, gdr_stream_t stream) {
+    int rc = check_dims(dims);
+    if (rc != GDR_OK) return rc;
+    if (!q || !o || window < 0 || (cu_seqlens != nullptr) != (dims->N > 0)) return GDR_ERR_INVALID;
+    rc = check_cache(*dims, cache, true);
+    if (rc != GDR_OK) return rc;
+    if (opt && (!(opt->scale >= 0.f) || opt->grid_limit < 0 || opt->force_bv ||
+                opt->force_path < 0 || opt->force_path > 3))
+        return GDR_ERR_INVALID;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    AttnProblem p{};
+    p.c = device_cache(*dims, *cache);
+    p.r = token_rows(*dims, cu_seqlens, opt ? opt->status : nullptr);
+    p.q = q; p.o = o; p.lse = lse;
+    p.sq = dims_stride(dims->q_stride, dims->H, dims->K);
+    p.so = dims_stride(dims->o_stride, dims->H, dims->V);
+    p.Hq = (int)dims->H; p.G = (int)(dims->H / cache->H);
+    p.K = (int)dims->K; p.V = (int)dims->V;
+    p.dtype = dims->dtype;
+    p.causal = causal != 0;
+    p.window = window;
+    p.scale = opt && opt->scale > 0.f ? opt->scale : 1.0f / std::sqrt((float)dims->K);
+    p.grid_limit = opt ? opt->grid_limit : 0;
+    LaunchRecorder rec;
+    rec.st = st;
+    if (opt) {
+        rec.events = reinterpret_cast<cudaEvent_t *>(opt->events);
+        rec.ids = opt->launch_ids;
+        rec.max_launches = opt->events || opt->launch_ids ? opt->max_launches : 0;
+        if (opt->n_launches) *opt->n_launches = 0;
+    }
+    if (seqs_of(*dims) == 0 || dims->T == 0) return GDR_OK;
+    if (opt && opt->force_path > 1) return GDR_ERR_UNSUPPORTED;
+    if (rec.begin(kKAttnSimt) != cudaSuccess || attn_simt(p, st) != cudaSuccess ||
+        rec.end() != cudaSuccess)
+        return GDR_ERR_CUDA;
+    if (opt && opt->n_launches) *opt->n_launches = rec.count;
+    return GDR_OK;
+}
+
+}  // extern "C"

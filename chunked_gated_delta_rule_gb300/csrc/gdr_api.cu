@@ -260,6 +260,12 @@ bool prescan_split_kinds(int64_t segs) { return 2 * segs <= device_sms(); }
 
 }  // namespace
 
+cudaError_t scratch_alloc(void **ptr, size_t bytes, cudaStream_t st) {
+    return lib_malloc(ptr, bytes, st);
+}
+int check_dims(const gdr_dims *d) { return validate_dims(d); }
+TokStride dims_stride(const int64_t (&s)[2], int64_t H, int64_t D) { return stride_of(s, H, D); }
+
 int64_t split_seqs(const gdr_dims &d, int S) {
     const int64_t nseq = n_seqs(d);
     if (S <= 1 || nseq <= 1) return S <= 1 ? 0 : nseq;
@@ -789,6 +795,7 @@ const char *gdr_kernel_name(int id) {
     case kKTcSegRecompute: return "tc_chain_segment_recompute";
     case kKTcBwdPre: return "tc_bwd_scan_prescan";
     case kKTcBwdSegOut: return "tc_bwd_scan_segment_out";
+    case kKAttnSimt: return "attn_simt";
     default: return "?";
     }
 }

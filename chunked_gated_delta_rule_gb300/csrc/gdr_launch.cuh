@@ -87,6 +87,7 @@ enum KernelId {
     kKTcComposeGroups = 32,
     kKTcComposeTop = 33,
     kKTcComposeFill = 34,
+    kKAttnSimt = 35,
     kKNumIds
 };
 
@@ -182,5 +183,23 @@ cudaError_t recurrent_fwd(const Problem &p, float *state, int64_t n_states,
 // tc_chain's mode 1 runs them as separate chains, which is faster while both
 // kinds fit one wave (prescan_split_kinds).
 cudaError_t tc_prescan(const Problem &p, const Workspace &ws, cudaStream_t st);
+
+// ---- the paged cache and the attention over it ----------------------------
+struct PagedCache;
+struct TokenRows;
+struct AttnProblem;
+// Rows k, v of the call's tokens into the cache (write), or out of it.
+cudaError_t cache_rows(bool write, const PagedCache &c, const TokenRows &r, int dtype,
+                       const void *k, const void *v, const TokStride &sk, const TokStride &sv,
+                       int K, int V, cudaStream_t st);
+// Attention on CUDA cores (every type, K and V multiples of 16 up to 256).
+cudaError_t attn_simt(const AttnProblem &p, cudaStream_t st);
+
+// Device scratch from the library's pool, ordered on the stream.
+cudaError_t scratch_alloc(void **ptr, size_t bytes, cudaStream_t st);
+// GDR_OK or the code that a call with these sizes returns.
+int check_dims(const gdr_dims *d);
+// Token and head strides of a tensor (a dims pair, {0, 0} = contiguous).
+TokStride dims_stride(const int64_t (&s)[2], int64_t H, int64_t D);
 
 }  // namespace gdr

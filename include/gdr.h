@@ -70,8 +70,9 @@ extern "C" {
 typedef struct CUstream_st *gdr_stream_t;
 
 /* Element type of q, k, v and o.  GDR_F16 runs on the CUDA-core path (the
- * tensor-core kernels take BF16). */
-enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1, GDR_F16 = 2 };
+ * tensor-core kernels take BF16).  The last two are formats of a paged cache
+ * only (gdr_paged_cache). */
+enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1, GDR_F16 = 2, GDR_E4M3 = 3, GDR_I8 = 4 };
 
 /* Return codes. */
 enum gdr_status {
@@ -82,7 +83,8 @@ enum gdr_status {
     GDR_ERR_TIMEOUT = -4,      /* device status: a bounded wait expired     */
     GDR_ERR_SEQLENS = -5,      /* device status: cu_seqlens malformed       */
     GDR_ERR_WORKSPACE = -6,    /* caller workspace too small                */
-    GDR_ERR_INDEX = -7         /* device status: a state index out of range */
+    GDR_ERR_INDEX = -7         /* device status: a state index out of range,
+                                  or a length or page of a paged cache      */
 };
 
 /* Layout flags of gdr_dims.flags (bitwise OR; 0 = the defaults above). */
@@ -330,6 +332,93 @@ int gdr_chunk_bwd(const gdr_dims *dims, const void *q, const void *k,
                   const void *dout, const float *dht, void *dq, void *dk,
                   void *dv, float *dg, float *dbeta, float *dh0,
                   int n_segments, const gdr_options *opt, gdr_stream_t stream);
+
+/*
+ * A paged cache of keys and values, beside the state pool of
+ * gdr_recurrent_fwd what a server of a model keeps whose gated-delta-rule
+ * layers alternate with softmax attention.  Everything is caller-owned device
+ * memory.  Position p of sequence n is slot p % page_size of page
+ * page_table[n][p / page_size].
+ *   kv_lens   counts each sequence's tokens INCLUDING those of the call, so
+ *             token i of the L_n tokens that a call has of sequence n is at
+ *             position kv_lens[n] - L_n + i.  A position below 0 has no place
+ *             in the cache.
+ *   dtype     the call's own type (GDR_F32, GDR_BF16, GDR_F16: stored as they
+ *             are), or GDR_E4M3 / GDR_I8: each (token, head) row x is stored
+ *             as q = round(x / s) beside its FP32 scale s = max|x| * (1 / 448)
+ *             or max|x| * (1 / 127), one FP32 product (ties to even; q = 0
+ *             where s = 0), and stands for q s.  A row with a NaN or an
+ *             infinity is stored as s = NaN, q = 0 and reads back as NaN.
+ *   strides   in elements: page, slot, head; {0, 0, 0} means contiguous
+ *             ([n_pages, page_size, H, K]).  The last dimension is always
+ *             contiguous, so pages may be head-major or hold keys and values
+ *             side by side.
+ * A length outside [0, max_pages * page_size] or a page outside
+ * [0, n_pages) sets GDR_ERR_INDEX in the status word: nothing outside the
+ * tensors is read or written, such a length counts as the nearest one inside,
+ * and such a page holds no tokens.
+ */
+typedef struct gdr_paged_cache {
+    void *k, *v;               /* pages of keys [.., K] and of values [.., V]  */
+    float *k_scale, *v_scale;  /* [n_pages, H, page_size] FP32 (8-bit formats) */
+    const int32_t *page_table; /* [Nseq, max_pages]                            */
+    const int32_t *kv_lens;    /* [Nseq]                                       */
+    int64_t n_pages, page_size, max_pages;
+    int64_t H;                 /* key (and value) heads                        */
+    int32_t dtype;             /* enum gdr_dtype                               */
+    int64_t k_stride[3], v_stride[3];
+} gdr_paged_cache;
+
+/*
+ * gdr_cache_write -- stores the call's keys and values in the cache.
+ *   dims        B, T, N, K, V, dtype, k_stride, v_stride as for gdr_chunk_fwd;
+ *               H = cache->H; V at most 256.
+ *   k, v        [B, T, H, K], [B, T, H, V].
+ *   status      device int32 word or NULL, zeroed by the caller.
+ * The tokens of one call must have places of their own.  Enqueued on `stream`,
+ * no allocation, no synchronisation.
+ */
+int gdr_cache_write(const gdr_dims *dims, const gdr_paged_cache *cache, const void *k,
+                    const void *v, const int32_t *cu_seqlens, int32_t *status,
+                    gdr_stream_t stream);
+
+/*
+ * gdr_cache_read -- the way back: k and v (dims as above, written through
+ * k_stride and v_stride) get what the cache holds for the call's tokens: the
+ * L_n last positions of each sequence, so L_n = kv_lens[n] reads it whole.
+ * Tokens without a place read as zeros.
+ */
+int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, void *v,
+                   const int32_t *cu_seqlens, int32_t *status, gdr_stream_t stream);
+
+/*
+ * gdr_paged_attn -- softmax attention of the call's tokens over the cache
+ * (which holds their own keys and values already): with s_ij = scale <q_i,
+ * k_j>, o_i = sum_j e^{s_ij - lse_i} v_j and lse_i = log sum_j e^{s_ij} over
+ * the positions j that token i, at position p_i, sees: j < kv_lens[n]; causal
+ * != 0: j <= p_i; window > 0: j > p_i - window.  A row that sees nothing gets
+ * o = 0, lse = -inf.
+ *   dims      B, T, N, K, V (at most 256), dtype, q_stride, o_stride; H the
+ *             query heads, a multiple of cache->H: query head h reads key head
+ *             h / (H / cache->H).  max_len: the most new tokens of a sequence
+ *             (varlen; a hint that picks the kernel, 0 = the mean).
+ *   q, o      [B, T, H, K], [B, T, H, V].   lse  [B, T, H] FP32 or NULL.
+ *   opt       NULL, or gdr_options with scale (0 => 1/sqrt(K)), status,
+ *             workspace (at least gdr_attn_workspace_size bytes, 256-byte
+ *             aligned), the launch events, grid_limit and force_path (0 plan,
+ *             1 CUDA cores, 2 the tensor-core kernel of many rows, 3 that of
+ *             few rows); force_bv must be 0.
+ * FP32 scores, softmax statistics and accumulators.  A masked position never
+ * adds to a row, whatever the cache holds there.  Results are bit-identical
+ * from run to run.
+ */
+int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const void *q,
+                   const int32_t *cu_seqlens, void *o, float *lse, int causal,
+                   int64_t window, const gdr_options *opt, gdr_stream_t stream);
+
+/* Bytes of device scratch gdr_paged_attn needs (whatever its force_path).  0
+ * on invalid arguments. */
+size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cache);
 
 /* Bytes of device scratch gdr_chunk_bwd needs for this problem (beta_free
  * != 0 for the beta-free mode; n_segments as passed to gdr_chunk_bwd),
