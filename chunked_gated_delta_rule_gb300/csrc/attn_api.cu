@@ -2,7 +2,7 @@
 // argument checks, choice of kernel, scratch, launches.
 #include <cmath>
 
-#include "attn.cuh"
+#include "attn_split.cuh"
 #include "gdr_launch.cuh"
 
 namespace gdr {
@@ -81,6 +81,26 @@ int cache_call(bool write, const gdr_dims *dims, const gdr_paged_cache *cache, c
                : GDR_ERR_CUDA;
 }
 
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t split_bytes(const SplitPlan &s, int64_t V) {
+    const size_t rows = (size_t)s.workers * 2 * s.rows;
+    return align256(rows * V * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
+           align256((size_t)s.workers * sizeof(int4));
+}
+
+SplitScratch carve_split(void *base, const SplitPlan &s, int64_t V) {
+    const size_t rows = (size_t)s.workers * 2 * s.rows;
+    char *c = static_cast<char *>(base);
+    SplitScratch ws{};
+    ws.o = reinterpret_cast<float *>(c);
+    c += align256(rows * V * sizeof(float));
+    ws.ml = reinterpret_cast<float *>(c);
+    c += align256(rows * 2 * sizeof(float));
+    ws.rec = reinterpret_cast<int4 *>(c);
+    return ws;
+}
+
 }  // namespace
 }  // namespace gdr
 
@@ -101,7 +121,8 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
 
 size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cache) {
     if (check_dims(dims) != GDR_OK || check_cache(*dims, cache, true) != GDR_OK) return 0;
-    return 256;
+    AttnProblem p{};
+    return split_bytes(attn_rows_plan(p), dims->V);
 }
 
 int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const void *q,
@@ -138,12 +159,36 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
         if (opt->n_launches) *opt->n_launches = 0;
     }
     if (seqs_of(*dims) == 0 || dims->T == 0) return GDR_OK;
-    if (opt && opt->force_path > 1) return GDR_ERR_UNSUPPORTED;
-    if (rec.begin(kKAttnSimt) != cudaSuccess || attn_simt(p, st) != cudaSuccess ||
-        rec.end() != cudaSuccess)
+    const int force = opt ? opt->force_path : 0;
+    if (force == 2) return GDR_ERR_UNSUPPORTED;
+    const bool rows = force != 1 && attn_rows_supported(p);
+    if (force == 3 && !rows) return GDR_ERR_UNSUPPORTED;
+    if (!rows) {
+        if (rec.begin(kKAttnSimt) != cudaSuccess || attn_simt(p, st) != cudaSuccess ||
+            rec.end() != cudaSuccess)
+            return GDR_ERR_CUDA;
+        if (opt && opt->n_launches) *opt->n_launches = rec.count;
+        return GDR_OK;
+    }
+    const SplitPlan plan = attn_rows_plan(p);
+    const size_t need = split_bytes(plan, p.V);
+    void *base = opt ? opt->workspace : nullptr;
+    if (base) {
+        if (opt->workspace_bytes < need) return GDR_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(base) % 256) return GDR_ERR_INVALID;
+    } else if (scratch_alloc(&base, need, st) != cudaSuccess) {
         return GDR_ERR_CUDA;
+    }
+    const SplitScratch ws = carve_split(base, plan, p.V);
+    rc = rec.begin(kKAttnRows) == cudaSuccess && attn_rows(p, ws, plan, st) == cudaSuccess &&
+                 rec.end() == cudaSuccess && rec.begin(kKAttnJoin) == cudaSuccess &&
+                 attn_rows_join(p, ws, plan, st) == cudaSuccess && rec.end() == cudaSuccess
+             ? GDR_OK
+             : GDR_ERR_CUDA;
+    if (!(opt && opt->workspace) && cudaFreeAsync(base, st) != cudaSuccess && rc == GDR_OK)
+        rc = GDR_ERR_CUDA;
     if (opt && opt->n_launches) *opt->n_launches = rec.count;
-    return GDR_OK;
+    return rc;
 }
 
 }  // extern "C"

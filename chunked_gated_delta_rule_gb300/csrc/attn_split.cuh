@@ -1,0 +1,210 @@
+// attn_split.cuh -- how the tensor-core attention kernels share out a call.
+//
+// The work is cut into units, one for each (sequence, tile of M rows, key
+// head), and a unit into steps of BN positions of the keys that its rows see
+// (one step at least, so that rows that see nothing are written too).  All
+// steps of the call form one line, sequence by sequence, and worker w of nw
+// takes the steps [W w / nw, W (w + 1) / nw): equal shares whatever the
+// lengths, known to every worker from the lengths alone, with no plan made on
+// the host (the lengths are device data) and none passed between kernels.
+//
+// A worker's share meets at most two units that it does not do whole: its
+// first (begun before it, slot 0) and its last (begun by it, slot 1).  Their
+// unnormalised sums go to the worker's two scratch slots, and the worker that
+// begins a split unit records how many pieces it has; a second kernel joins
+// them in the order of the axis, so results do not depend on timing.
+#pragma once
+
+#include "attn.cuh"
+
+namespace gdr {
+
+// Scratch of a call: for `workers` workers, two slots each of M rows.
+struct SplitScratch {
+    float *o;      // [workers][2][M][V] sums of e^{s - m} v
+    float *ml;     // [workers][2][M][2] m (base 2) and sum of e^{s - m}
+    int4 *rec;     // [workers] sequence, tile, key head, pieces (0: none split)
+};
+
+constexpr int kSplitSlots = 256;  // groups of sequences whose steps are summed up
+
+struct Unit {
+    int n, tile, head;
+    int step, steps;       // next step, steps of the unit
+    int lo, hi;            // positions that its rows see
+    int t0, len, kv;       // the sequence: first token, new tokens, cached tokens
+};
+
+__device__ __forceinline__ void load_seq(const AttnProblem &p, int64_t n, int &t0, int &len,
+                                         int &kv) {
+    int64_t a, b;
+    seq_span(p.r, n, a, b);
+    t0 = (int)a;
+    len = (int)b;
+    kv = (int)cached_len(p.c, n, p.r.status);
+}
+
+template <int M>
+__device__ __forceinline__ int tiles_of(const AttnProblem &p, int len) {
+    return (int)(((int64_t)len * p.G + (M - 1)) / M);
+}
+
+// Positions [lo, hi) that the rows of a tile see, and its steps.
+template <int M, int BN>
+__device__ __forceinline__ int tile_steps(const AttnProblem &p, int len, int kv, int tile, int &lo,
+                                          int &hi) {
+    const int64_t r0 = (int64_t)tile * M;
+    const int64_t i0 = r0 / p.G;
+    int64_t i1 = (r0 + M - 1) / p.G;
+    if (i1 > len - 1) i1 = len - 1;
+    int64_t a, b, c, d;
+    visible(p, kv, (int64_t)kv - len + i0, a, b);
+    visible(p, kv, (int64_t)kv - len + i1, c, d);
+    lo = (int)a;
+    hi = (int)(d > a ? d : a);
+    const int s = (hi - lo + BN - 1) / BN;
+    return s > 0 ? s : 1;
+}
+
+template <int M, int BN>
+__device__ __forceinline__ int64_t seq_steps(const AttnProblem &p, int len, int kv, int first,
+                                             int stride) {
+    int lo, hi;
+    int64_t s = 0;
+    const int tiles = tiles_of<M>(p, len);
+    for (int t = first; t < tiles; t += stride) s += tile_steps<M, BN>(p, len, kv, t, lo, hi);
+    return s * p.c.H;
+}
+
+// Exclusive prefix sums of the steps of kSplitSlots groups of `per` sequences
+// (per = ceil(N / kSplitSlots)) in pre[0 .. kSplitSlots], by the whole block.
+// Each thread sums a group's short sequences; those of many tiles are left
+// to the block, which shares their tiles out.
+template <int M, int BN, int NT>
+__device__ void split_prefix(const AttnProblem &p, int64_t per, int64_t *pre) {
+    static_assert(NT % 32 == 0 && kSplitSlots % 32 == 0, "whole warps");
+    constexpr int kFew = 8;
+    __shared__ int s_many[kSplitSlots];
+    __shared__ int64_t s_warp[kSplitSlots / 32];
+    __shared__ int s_any;
+    const int tid = threadIdx.x;
+    if (tid == 0) s_any = 0;
+    __syncthreads();
+    for (int e = tid; e < kSplitSlots; e += NT) {
+        int64_t sum = 0;
+        int many = 0;
+        for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
+            int t0, len, kv;
+            load_seq(p, n, t0, len, kv);
+            if (tiles_of<M>(p, len) <= kFew) sum += seq_steps<M, BN>(p, len, kv, 0, 1);
+            else ++many;
+        }
+        pre[e + 1] = sum;
+        s_many[e] = many;
+        if (many) s_any = 1;
+    }
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+    if (s_any) {
+        for (int e = 0; e < kSplitSlots; ++e) {
+            if (!s_many[e]) continue;
+            int64_t sum = 0;
+            for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
+                int t0, len, kv;
+                load_seq(p, n, t0, len, kv);
+                if (tiles_of<M>(p, len) > kFew) sum += seq_steps<M, BN>(p, len, kv, tid, NT);
+            }
+            atomicAdd(reinterpret_cast<unsigned long long *>(&pre[e + 1]), (unsigned long long)sum);
+        }
+        __syncthreads();
+    }
+    for (int e = tid; e < kSplitSlots; e += NT) {  // whole warps: NT and the slots are multiples
+        int64_t x = pre[e + 1];
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if ((e & 31) >= d) x += y;
+        }
+        pre[e + 1] = x;
+        if ((e & 31) == 31) s_warp[e >> 5] = x;
+    }
+    __syncthreads();
+    for (int e = tid; e < kSplitSlots; e += NT) {
+        int64_t add = 0;
+        for (int w = 0; w < (e >> 5); ++w) add += s_warp[w];
+        pre[e + 1] += add;
+    }
+    __syncthreads();
+}
+
+// The sequence, tile and key head that hold step `at` of the line, by a whole
+// warp (0 <= at < pre[kSplitSlots]).
+template <int M, int BN>
+__device__ Unit split_locate(const AttnProblem &p, int64_t per, const int64_t *pre, int64_t at) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = kSplitSlots;  // the last e with pre[e] <= at
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, i < hi && pre[i] <= at);
+        lo += (31 - __clz(m)) * step;
+        if (lo + step < hi) hi = lo + step;
+    }
+    int64_t rem = at - pre[lo];
+    Unit u{};
+    for (int64_t n = lo * per;; ++n) {
+        load_seq(p, n, u.t0, u.len, u.kv);
+        const int tiles = tiles_of<M>(p, u.len);
+        for (int t = 0; t < tiles; t += 32) {
+            int a = 0, b = 0;
+            const int s = t + lane < tiles ? tile_steps<M, BN>(p, u.len, u.kv, t + lane, a, b) : 0;
+            int64_t x = (int64_t)s * p.c.H;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, x > rem);
+            if (m) {
+                const int l = __ffs(m) - 1;
+                u.n = (int)n;
+                u.tile = t + l;
+                u.steps = __shfl_sync(0xffffffffu, s, l);
+                u.lo = __shfl_sync(0xffffffffu, a, l);
+                u.hi = __shfl_sync(0xffffffffu, b, l);
+                rem -= __shfl_sync(0xffffffffu, x, l) - (int64_t)u.steps * p.c.H;
+                u.head = (int)(rem / u.steps);
+                u.step = (int)(rem - (int64_t)u.head * u.steps);
+                return u;
+            }
+            rem -= __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (n + 1 >= p.r.N) return u;  // not reached for a step of the line
+    }
+}
+
+// On to the next unit of the line (there is one).
+template <int M, int BN>
+__device__ __forceinline__ void next_unit(const AttnProblem &p, Unit &u) {
+    u.step = 0;
+    if (++u.head < p.c.H) return;
+    u.head = 0;
+    ++u.tile;
+    while (u.tile >= tiles_of<M>(p, u.len)) {
+        u.tile = 0;
+        if (++u.n >= p.r.N) return;
+        load_seq(p, u.n, u.t0, u.len, u.kv);
+    }
+    u.steps = tile_steps<M, BN>(p, u.len, u.kv, u.tile, u.lo, u.hi);
+}
+
+// First step of worker w of nw.
+__device__ __forceinline__ int64_t share_begin(int64_t total, int64_t w, int64_t nw) {
+    return total / nw * w + total % nw * w / nw;
+}
+// Pieces of the unit whose steps end before `end` on the line, begun by
+// worker w: the workers from w on whose shares begin before it.  Worker j's
+// does iff floor(total j / nw) < end, that is iff total j < end nw.
+__device__ __forceinline__ int pieces_from(int64_t total, int64_t w, int64_t nw, int64_t end) {
+    const int64_t j = (end * nw + total - 1) / total;
+    return (int)((j < nw ? j : nw) - w);
+}
+
+}  // namespace gdr

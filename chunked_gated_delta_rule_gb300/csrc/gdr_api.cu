@@ -796,6 +796,8 @@ const char *gdr_kernel_name(int id) {
     case kKTcBwdPre: return "tc_bwd_scan_prescan";
     case kKTcBwdSegOut: return "tc_bwd_scan_segment_out";
     case kKAttnSimt: return "attn_simt";
+    case kKAttnRows: return "attn_rows";
+    case kKAttnJoin: return "attn_join";
     default: return "?";
     }
 }

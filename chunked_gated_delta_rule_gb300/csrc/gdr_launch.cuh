@@ -88,6 +88,8 @@ enum KernelId {
     kKTcComposeTop = 33,
     kKTcComposeFill = 34,
     kKAttnSimt = 35,
+    kKAttnRows = 36,
+    kKAttnJoin = 37,
     kKNumIds
 };
 
@@ -194,6 +196,19 @@ cudaError_t cache_rows(bool write, const PagedCache &c, const TokenRows &r, int 
                        int K, int V, cudaStream_t st);
 // Attention on CUDA cores (every type, K and V multiples of 16 up to 256).
 cudaError_t attn_simt(const AttnProblem &p, cudaStream_t st);
+// The same on the tensor cores, few rows of queries for each key head: the
+// steps of the call shared out among workers (attn_split.cuh) and the units
+// that were split joined by a second kernel.
+struct SplitScratch;
+struct SplitPlan {
+    int ctas, workers, rows;  // rows: of a tile
+};
+bool attn_rows_supported(const AttnProblem &p);
+SplitPlan attn_rows_plan(const AttnProblem &p);
+cudaError_t attn_rows(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
+                      cudaStream_t st);
+cudaError_t attn_rows_join(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
+                           cudaStream_t st);
 
 // Device scratch from the library's pool, ordered on the stream.
 cudaError_t scratch_alloc(void **ptr, size_t bytes, cudaStream_t st);

@@ -103,6 +103,12 @@ __device__ __forceinline__ int64_t scale_at(const PagedCache &c, int64_t page, i
     return (page * c.H + head) * c.page_size + slot;
 }
 
+// 16-byte loads of a cache's rows: an aligned base and strides.
+inline bool pages_aligned16(const void *p, const int64_t (&st)[3], int es) {
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(st[0] * es) | (uintptr_t)(st[1] * es) |
+             (uintptr_t)(st[2] * es)) & 15u) == 0;
+}
+
 inline bool cache_quantised(int dtype) { return dtype == GDR_E4M3 || dtype == GDR_I8; }
 
 }  // namespace gdr

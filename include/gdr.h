@@ -356,7 +356,8 @@ int gdr_chunk_bwd(const gdr_dims *dims, const void *q, const void *k,
  * A length outside [0, max_pages * page_size] or a page outside
  * [0, n_pages) sets GDR_ERR_INDEX in the status word: nothing outside the
  * tensors is read or written, such a length counts as the nearest one inside,
- * and such a page holds no tokens.
+ * a token of such a page is not stored and reads as zeros, and what the
+ * attention gives for its sequence is unspecified.
  */
 typedef struct gdr_paged_cache {
     void *k, *v;               /* pages of keys [.., K] and of values [.., V]  */
