@@ -81,6 +81,15 @@ int cache_call(bool write, const gdr_dims *dims, const gdr_paged_cache *cache, c
                : GDR_ERR_CUDA;
 }
 
+// New tokens of a sequence, as far as the host knows: the longest (dense, or
+// the caller's hint), else the mean.
+int64_t tile_rows(const gdr_dims &d) {
+    if (d.N == 0) return d.T;
+    return d.max_len > 0 ? d.max_len : (d.T + d.N - 1) / d.N;
+}
+// Rows of a key head up to which the kernel of 16-row tiles is taken.
+constexpr int64_t kFewRows = 16;
+
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t split_bytes(const SplitPlan &s, int64_t V) {
@@ -122,7 +131,9 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
 size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cache) {
     if (check_dims(dims) != GDR_OK || check_cache(*dims, cache, true) != GDR_OK) return 0;
     AttnProblem p{};
-    return split_bytes(attn_rows_plan(p), dims->V);
+    const size_t a = split_bytes(attn_rows_plan(p), dims->V);
+    const size_t b = split_bytes(attn_tiles_plan(p), dims->V);
+    return a > b ? a : b;
 }
 
 int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const void *q,
@@ -160,17 +171,17 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
     }
     if (seqs_of(*dims) == 0 || dims->T == 0) return GDR_OK;
     const int force = opt ? opt->force_path : 0;
-    if (force == 2) return GDR_ERR_UNSUPPORTED;
-    const bool rows = force != 1 && attn_rows_supported(p);
-    if (force == 3 && !rows) return GDR_ERR_UNSUPPORTED;
-    if (!rows) {
+    const bool tensor = force != 1 && attn_rows_supported(p);
+    if (force > 1 && !tensor) return GDR_ERR_UNSUPPORTED;
+    if (!tensor) {
         if (rec.begin(kKAttnSimt) != cudaSuccess || attn_simt(p, st) != cudaSuccess ||
             rec.end() != cudaSuccess)
             return GDR_ERR_CUDA;
         if (opt && opt->n_launches) *opt->n_launches = rec.count;
         return GDR_OK;
     }
-    const SplitPlan plan = attn_rows_plan(p);
+    const bool tiles = force == 2 || (force == 0 && tile_rows(*dims) * p.G > kFewRows);
+    const SplitPlan plan = tiles ? attn_tiles_plan(p) : attn_rows_plan(p);
     const size_t need = split_bytes(plan, p.V);
     void *base = opt ? opt->workspace : nullptr;
     if (base) {
@@ -180,9 +191,10 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
         return GDR_ERR_CUDA;
     }
     const SplitScratch ws = carve_split(base, plan, p.V);
-    rc = rec.begin(kKAttnRows) == cudaSuccess && attn_rows(p, ws, plan, st) == cudaSuccess &&
+    rc = rec.begin(tiles ? kKAttnTiles : kKAttnRows) == cudaSuccess &&
+                 (tiles ? attn_tiles(p, ws, plan, st) : attn_rows(p, ws, plan, st)) == cudaSuccess &&
                  rec.end() == cudaSuccess && rec.begin(kKAttnJoin) == cudaSuccess &&
-                 attn_rows_join(p, ws, plan, st) == cudaSuccess && rec.end() == cudaSuccess
+                 attn_join(p, ws, plan, st) == cudaSuccess && rec.end() == cudaSuccess
              ? GDR_OK
              : GDR_ERR_CUDA;
     if (!(opt && opt->workspace) && cudaFreeAsync(base, st) != cudaSuccess && rc == GDR_OK)

@@ -781,9 +781,9 @@ cudaError_t launch_dim(const AttnProblem &p, const SplitScratch &ws, int ctas, c
 
 template <typename T, int M>
 cudaError_t join_dim(const AttnProblem &p, const SplitScratch &ws, int workers, cudaStream_t st) {
-    // many pieces a unit: a CTA for each row of it; few: the rows share one
-    const int y = workers > 8 * p.r.N * p.c.H ? (p.G < M ? p.G : M) : 1;
-    const dim3 g((unsigned)workers, (unsigned)y);
+    // few pieces a unit: eight rows to a CTA; many: a CTA for each row
+    const int rows = workers > 8 * p.r.N * p.c.H ? (M == 16 && p.G < M ? p.G : M) : (M + 7) / 8;
+    const dim3 g((unsigned)workers, (unsigned)(M == 16 && workers <= 8 * p.r.N * p.c.H ? 1 : rows));
     if (p.V == 64) return launch_pdl(k_attn_join<T, M, 64>, g, dim3(kJoinThreads), 0, st, p, ws);
     return launch_pdl(k_attn_join<T, M, 128>, g, dim3(kJoinThreads), 0, st, p, ws);
 }
@@ -811,10 +811,13 @@ cudaError_t attn_rows(const AttnProblem &p, const SplitScratch &ws, const SplitP
     return p.dtype == GDR_F16 ? launch_dim<__half>(p, ws, s.ctas, st)
                               : launch_dim<__nv_bfloat16>(p, ws, s.ctas, st);
 }
-cudaError_t attn_rows_join(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
-                           cudaStream_t st) {
-    return p.dtype == GDR_F16 ? join_dim<__half, kRowsM>(p, ws, s.workers, st)
-                              : join_dim<__nv_bfloat16, kRowsM>(p, ws, s.workers, st);
+cudaError_t attn_join(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
+                      cudaStream_t st) {
+    if (s.rows == kRowsM)
+        return p.dtype == GDR_F16 ? join_dim<__half, kRowsM>(p, ws, s.workers, st)
+                                  : join_dim<__nv_bfloat16, kRowsM>(p, ws, s.workers, st);
+    return p.dtype == GDR_F16 ? join_dim<__half, 256>(p, ws, s.workers, st)
+                              : join_dim<__nv_bfloat16, 256>(p, ws, s.workers, st);
 }
 
 }  // namespace gdr

@@ -1,0 +1,815 @@
+// attn_tiles.cu -- attention over a paged cache for many new tokens (chunks
+// of a prompt) on tcgen05: tiles of 256 rows (query heads and tokens of one
+// key head) against 128 positions a step.
+//
+// Per step and 128-row half, with the sums of the softmax taken in one pass:
+//   S = Q K^T                        tcgen05, FP32 in TMEM
+//   m' = max(m, max S),  P = e^(S - m')  (base 2, in registers; P back to TMEM
+//                                    as 16-bit operand over S's own columns)
+//   O <- O e^(m - m') + P V          tcgen05, A = P from TMEM
+// O is scaled only when a row's maximum has grown by more than 2^8 since it
+// was last scaled; the weights stay below 2^8 and the factor cancels in O / l.
+//
+// Bound by the tensor pipe while softmax keeps up: a step of a half is 2 x
+// 512 cycles of products and 16384 exponentials (512 cycles of the special
+// function units).  So the two halves run in turns: one half's exponentials
+// beside the other's products.
+//   warps 0-3, 4-7   softmax of rows 0-127, 128-255 (a thread a row)
+//   warps 8-11       loads: page look-up, keys and values into a ring of
+//                    tiles, queries; 8-bit rows are widened to FP16 on the way
+//   warp 12          every tcgen05 product
+// Keys and values come through the page table token by token, so any page
+// size and order will do, as 16-byte asynchronous copies into the 128-byte
+// swizzled layout that the products read.  A position past the last one that
+// the unit sees is filled with zeros.
+// 8-bit caches: see attn_rows.cu for the place of the scales.
+//
+// The steps of the call are shared out equally over one CTA an SM
+// (attn_split.cuh).  Every wait is bounded: on expiry the CTA records
+// GDR_ERR_TIMEOUT, its other roles leave too, and it exits.
+#include <cuda_fp8.h>
+
+#include "attn_split.cuh"
+#include "gdr_launch.cuh"
+#include "tc_common.cuh"
+
+namespace gdr {
+namespace {
+
+using namespace tc;
+
+constexpr int kTM = 256;       // rows of a unit
+constexpr int kTN = 128;       // positions of a step
+constexpr int kTThreads = 512;
+constexpr float kTLog2e = 1.4426950408889634f;
+constexpr float kTLn2 = 0.6931471805599453f;
+constexpr float kTLeast = 7.888609052210118e-31f;  // 2^-100
+
+// Registers a thread of the softmax warps, the loaders and the rest: 128 each
+// at launch, 2 x 184 + 104 + 40 = 4 x 128.
+constexpr int kRegSoftmax = 184, kRegLoad = 104, kRegRest = 40;
+static_assert(2 * kRegSoftmax + kRegLoad + kRegRest <= 4 * 128, "the launch's registers");
+
+template <int D>
+struct TilesCfg {
+    static constexpr uint32_t kTile = kTN * D * 2;     // a 128-row tile of 16-bit values
+    static constexpr int kRing = D == 128 ? 4 : 8;     // tiles of keys and values
+    // steps whose scales are kept: a step's keys are loaded once the products
+    // of the step kRing / 2 before it are done, so that softmax is at most
+    // kRing / 2 steps behind
+    static constexpr int kScales = kRing;
+    static constexpr uint32_t kOffRing = 2 * kTile;    // after the queries
+    static constexpr uint32_t kOffScale = kOffRing + kRing * kTile;  // [kScales][3][128]
+    static constexpr uint32_t kOffOff = kOffScale + kScales * 3 * kTN * 4; // [2 steps][K, V][128]
+    static constexpr uint32_t kOffQf = kOffOff + 2 * 2 * kTN * 8;    // [2 units][256]
+    static constexpr uint32_t kOffBar = kOffQf + 2 * kTM * 4;
+    static constexpr uint32_t kBytes = kOffBar + 512 + 1024;         // and to align
+    static constexpr uint32_t kColS = 0, kColO = 256;  // TMEM: S / P of both halves, O
+};
+
+// mbarriers
+template <int RING>
+struct Bars {
+    static constexpr int kFull = 0, kEmpty = RING, kQFull = 2 * RING, kQEmpty = kQFull + 1,
+                         kS = kQFull + 2, kP = kS + 2, kO = kP + 2, kDrain = kO + 2;
+};
+
+struct TilesArgs {
+    AttnProblem p;
+    SplitScratch ws;
+    int64_t per;
+    int min_steps;
+};
+
+template <int R>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ float2 wide16(uint32_t x) {
+    if constexpr (std::is_same<T, __half>::value)
+        return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    else
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x));
+}
+
+__device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool live) {
+    const int bytes = live ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_wait_but() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Barrier of the loading warps: whether all of them are well.
+__device__ __forceinline__ bool load_sync(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok)
+        : "memory");
+    return r != 0;
+}
+
+// Four 8-bit values as FP16 (exact).
+template <int FMT>
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FMT == 1) {
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> 16), __NV_E4M3);
+        lo = (uint32_t)a.x | (uint32_t)a.y << 16;
+        hi = (uint32_t)b.x | (uint32_t)b.y << 16;
+    } else {
+        const uint32_t u = x ^ 0x80808080u;  // x + 128, the low bits of 1024 + x + 128
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 c = __floats2half2_rn(1152.f, 1152.f);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&a), c);
+        const __half2 z = __hsub2(*reinterpret_cast<const __half2 *>(&b), c);
+        lo = *reinterpret_cast<const uint32_t *>(&y);
+        hi = *reinterpret_cast<const uint32_t *>(&z);
+    }
+}
+
+// Instruction descriptor: A and B of type T, A K-major, FP32 sums, M = 128.
+template <typename T>
+__host__ __device__ constexpr uint32_t tiles_idesc(int N, int b_mn) {
+    const uint32_t f = std::is_same<T, __half>::value ? 0u : 1u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Whether some row of the tile sees a part of the step at `base` only.
+__device__ __forceinline__ bool step_masked(const AttnProblem &p, const Unit &u, int base) {
+    const int i0 = (int)((int64_t)u.tile * kTM / p.G);
+    const int i1 = (int)min((int64_t)u.len - 1, ((int64_t)u.tile * kTM + kTM - 1) / p.G);
+    int64_t l0, h0, l1, h1;
+    visible(p, u.kv, (int64_t)u.kv - u.len + i0, l0, h0);
+    visible(p, u.kv, (int64_t)u.kv - u.len + i1, l1, h1);
+    return base + kTN > h0 || base < l1;
+}
+
+__device__ __forceinline__ int unit_rows(const AttnProblem &p, const Unit &u) {
+    return (int)min((int64_t)kTM, (int64_t)u.len * p.G - (int64_t)u.tile * kTM);
+}
+
+template <typename T, int FMT, int D>
+__global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_constant__ TilesArgs a) {
+    using C = TilesCfg<D>;
+    using B = Bars<C::kRing>;
+    using TP = typename std::conditional<FMT == 0, T, __half>::type;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t s_pre[kSplitSlots + 1];
+    __shared__ Unit s_unit;
+    __shared__ int s_poison[8];  // unit (count, modulo 8) + 1 whose masked values are not finite
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort_flag;
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::kOffBar);
+    volatile int *s_abort = &s_abort_flag;
+    const AttnProblem &p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    pdl_trigger();
+    if (tid == 0) {
+        for (int i = 0; i < C::kRing; ++i) {
+            mbar_init(&bars[B::kFull + i], 128);
+            mbar_init(&bars[B::kEmpty + i], 1);
+        }
+        mbar_init(&bars[B::kQFull], 128);
+        mbar_init(&bars[B::kQEmpty], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[B::kS + i], 1);
+            mbar_init(&bars[B::kP + i], 128);
+            mbar_init(&bars[B::kO + i], 1);
+        }
+        mbar_init(&bars[B::kDrain], 1);
+        mbar_init_fence();
+        s_abort_flag = 0;
+    }
+    if (tid < 8) s_poison[tid] = 0;
+    if (warp == 12) tmem_alloc(&s_tmem, 512);
+    split_prefix<kTM, kTN, kTThreads>(p, a.per, s_pre);
+    const int64_t total = s_pre[kSplitSlots];
+    const int64_t worker = blockIdx.x;
+    int64_t nw = gridDim.x;
+    if (nw * a.min_steps > total) nw = (total + a.min_steps - 1) / a.min_steps;
+    if (tid == 0) a.ws.rec[worker] = make_int4(0, 0, 0, 0);
+    const int64_t begin = worker < nw ? share_begin(total, worker, nw) : 0;
+    const int count = worker < nw ? (int)(share_begin(total, worker + 1, nw) - begin) : 0;
+    if (warp == 0 && count) {
+        const Unit u = split_locate<kTM, kTN>(p, a.per, s_pre, begin);
+        if (lane == 0) s_unit = u;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    auto wait = [&](int b, uint32_t parity) {
+        return mbar_wait_or_abort(&bars[b], parity & 1u, p.r.status, s_abort);
+    };
+    Unit u = s_unit;
+
+    if (count == 0) {
+        // no steps for this CTA
+    } else if (warp < 8) {
+        // ------------------------------------------------------- softmax
+        regs_up<kRegSoftmax>();
+        const int half = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane << 16
+        const uint32_t ts = tmem + lanes + C::kColS + half * 128;
+        const uint32_t to = tmem + lanes + C::kColO + half * D;
+        uint32_t k = 0;  // steps that this half has done
+        int left = count, seg = 0;
+        for (int done = 0; left > 0; ++seg) {
+            const int first = u.step, steps = min(left, u.steps - u.step);
+            left -= steps;
+            const int rows = unit_rows(p, u);
+            const bool begun = first == 0, ends = first + steps == u.steps;
+            if (half == 0 || rows > 128) {
+                const int r = half * 128 + row;
+                const bool live = r < rows;
+                const int64_t ur = (int64_t)u.tile * kTM + r;
+                const int tok = (int)(ur / p.G), hq = u.head * p.G + (int)(ur - (int64_t)tok * p.G);
+                int lo = 0, hi = 0;
+                if (live) {
+                    int64_t x, y;
+                    visible(p, u.kv, (int64_t)u.kv - u.len + tok, x, y);
+                    lo = (int)x;
+                    hi = (int)y;
+                }
+                float m = -INFINITY, l = 0.f;
+                float f = p.scale * kTLog2e;
+                bool ok = true;
+                for (int s = 0; s < steps; ++s, ++k) {
+                    ok = __all_sync(0xffffffffu, wait(B::kS + half, k));
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t sr[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, sr[q]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) reg_fence(sr[q]);
+                    const int base = u.lo + (first + s) * kTN;
+                    const float *scale = nullptr;
+                    if constexpr (FMT != 0) {
+                        if (s == 0) f *= reinterpret_cast<const float *>(sm + C::kOffQf)[(seg & 1) * kTM + r];
+                        scale = reinterpret_cast<const float *>(sm + C::kOffScale) + ((done + s) % C::kScales) * 3 * kTN;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 ks = *reinterpret_cast<const float4 *>(scale + q * 32 + e);
+                                const float4 lg = *reinterpret_cast<const float4 *>(scale + kTN + q * 32 + e);
+                                const float2 ff = make_float2(f, f);
+                                float2 x = make_float2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
+                                float2 y = make_float2(__uint_as_float(sr[q][e + 2]), __uint_as_float(sr[q][e + 3]));
+                                x = fma2(mul2(x, make_float2(ks.x, ks.y)), ff, make_float2(lg.x, lg.y));
+                                y = fma2(mul2(y, make_float2(ks.z, ks.w)), ff, make_float2(lg.z, lg.w));
+                                sr[q][e] = __float_as_uint(x.x);
+                                sr[q][e + 1] = __float_as_uint(x.y);
+                                sr[q][e + 2] = __float_as_uint(y.x);
+                                sr[q][e + 3] = __float_as_uint(y.y);
+                            }
+                    }
+                    const bool masked = __any_sync(0xffffffffu, base < lo || base + kTN > hi);
+                    if (masked) {
+                        const int c0 = lo - base, c1 = hi - base;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (q * 32 + e < c0 || q * 32 + e >= c1) sr[q][e] = 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        mx[q] = max3(__uint_as_float(sr[q][0]), __uint_as_float(sr[q][1]),
+                                     __uint_as_float(sr[q][2]));
+#pragma unroll
+                        for (int e = 3; e + 1 < 32; e += 2)
+                            mx[q] = max3(mx[q], __uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
+                        mx[q] = fmaxf(mx[q], __uint_as_float(sr[q][31]));
+                    }
+                    float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if constexpr (FMT == 0) mn = mn == -INFINITY ? mn : mn * f;
+                    if (__any_sync(0xffffffffu, mn > m + 8.f)) {
+                        const float n = fmaxf(m, mn);
+                        const float c = n == -INFINITY ? 1.f : ex2(m - n);
+                        m = n;
+                        l *= c;
+                        if (s > 0) {  // O holds the steps before
+                            ok = __all_sync(0xffffffffu, wait(B::kO + half, k - 1));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) {
+                                uint32_t o[32];
+                                tmem_ld32(to + 32 * q, o);
+                                tmem_wait_ld();
+                                reg_fence(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
+                                tmem_st32(to + 32 * q, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float2 ff = make_float2(f, f), nm = make_float2(-mu, -mu);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t ph[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 x = make_float2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
+                            if constexpr (FMT == 0) x = fma2(x, ff, nm);
+                            else x = add2(x, nm);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            if constexpr (FMT == 0) {
+                                sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
+                            } else {
+                                float2 iv = *reinterpret_cast<const float2 *>(scale + 2 * kTN + q * 32 + e);
+                                if (masked) {  // what a row does not see may have no scale
+                                    if (x.x == 0.f) iv.x = 0.f;
+                                    if (x.y == 0.f) iv.y = 0.f;
+                                }
+                                sum[(e >> 1) & 1] = fma2(x, iv, sum[(e >> 1) & 1]);
+                            }
+                            ph[e >> 1] = pack16<TP>(x.x, x.y);
+                        }
+                        tmem_st16(ts + 16 * q, ph);
+                    }
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&bars[B::kP + half]);
+                }
+                if (!ok) break;
+                // ------------------------------------------- the piece ends
+                ok = __all_sync(0xffffffffu, wait(B::kO + half, k - 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (FMT == 0 && s_poison[seg & 7] == seg + 1) {
+                    // values that are not finite at masked positions went in
+                    // as zeros: add them to the rows that see them
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(to + 32 * q, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
+                        for (int s = first; s < first + steps; ++s) {
+                            const int base = u.lo + s * kTN;
+                            if (!step_masked(p, u, base)) continue;
+                            for (int j = max(base, lo); j < min(base + kTN, hi); ++j) {
+                                const int page = page_of(p.c, u.n, j / p.c.page_size, p.r.status);
+                                if (page < 0) continue;
+                                const T *v = reinterpret_cast<const T *>(p.c.v) +
+                                             page_at(p.c.vst, page, j % p.c.page_size, u.head) + 32 * q;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float x = (float)v[e];
+                                    if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        tmem_st32(to + 32 * q, o);
+                    }
+                    tmem_wait_st();
+                }
+                const bool whole = begun && ends;
+                const bool empty = l == 0.f;
+                const float inv = whole ? (empty ? 0.f : 1.f / l) : 1.f;
+                T *o16 = reinterpret_cast<T *>(p.o) + (live ? tok_at(p.so, u.t0 + tok, hq) : 0);
+                const int64_t slot = (worker * 2 + (begun ? 1 : 0)) * kTM + r;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(to + 32 * q, o);
+                    tmem_wait_ld();
+                    reg_fence(o);
+                    if (live && whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 x;
+                            x.x = pack16<T>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                            x.y = pack16<T>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                            x.z = pack16<T>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                            x.w = pack16<T>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                            *reinterpret_cast<uint4 *>(o16 + 32 * q + e) = x;
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4 *>(a.ws.o + slot * D + 32 * q + e) =
+                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                tc_fence_before();  // O is read before the next unit's first product is let go
+                if (live && whole && p.lse)
+                    p.lse[(int64_t)(u.t0 + tok) * p.Hq + hq] =
+                        empty ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kTLn2;
+                if (live && !whole) {
+                    a.ws.ml[slot * 2] = m;
+                    a.ws.ml[slot * 2 + 1] = l;
+                }
+            }
+            done += steps;
+            if (begun && !ends && tid == 0)
+                a.ws.rec[worker] = make_int4(u.n, u.tile, u.head,
+                                             pieces_from(total, worker, nw, begin + done + (u.steps - first - steps)));
+            if (left) next_unit<kTM, kTN>(p, u);
+        }
+    } else if (warp < 12) {
+        // --------------------------------------------------------- loads
+        regs_down<kRegLoad>();
+        const int t = tid - 256;
+        constexpr int kES = FMT ? 1 : 2;
+        constexpr int kChunks = D * kES / 16, kPass = 128 / kChunks;  // rows a pass of the 128 threads
+        constexpr int kPasses = kTN / kPass;
+        const int ch = t % kChunks, r0 = t / kChunks;
+        const uint8_t *kc = reinterpret_cast<const uint8_t *>(p.c.k);
+        const uint8_t *vc = reinterpret_cast<const uint8_t *>(p.c.v);
+        int64_t *offs = reinterpret_cast<int64_t *>(sm + C::kOffOff);
+        int page = -1, slot = 0;
+        auto look_up = [&]() {
+            const int pos = u.lo + u.step * kTN + t;
+            page = -1;
+            if (pos < u.hi) {
+                const int pi = pos / p.c.page_size;
+                slot = pos - pi * p.c.page_size;
+                page = page_of(p.c, u.n, pi, p.r.status);
+            }
+        };
+        // copies in flight whose barrier has not been told: their barrier,
+        // the tile to be looked over for values that are not finite, its unit
+        struct Pending {
+            int bar, tile, seg;
+        };
+        Pending pend[2] = {{-1, -1, 0}, {-1, -1, 0}};
+        auto tell = [&](const Pending &x) {
+            if (x.bar < 0) return;
+            if (FMT == 0 && x.tile >= 0) {
+                constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+                uint8_t *tile = sm + C::kOffRing + x.tile * C::kTile;
+                for (int i = 0; i < kPasses; ++i) {
+                    uint32_t *w = reinterpret_cast<uint32_t *>(tile + sw128_chunk(r0 + i * kPass, ch, kTN));
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t y = w[e];
+                        const bool b0 = (y & kExp) == kExp, b1 = (y >> 16 & kExp) == kExp;
+                        if (b0 || b1) {
+                            w[e] = (b0 ? 0u : y & 0xffffu) | (b1 ? 0u : y & 0xffff0000u);
+                            s_poison[x.seg & 7] = x.seg + 1;
+                        }
+                    }
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(&bars[x.bar]);
+        };
+        auto push = [&](int bar, int tile, int seg) {  // the copies since the last push
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            cp_wait_but<2>();
+            tell(pend[0]);
+            pend[0] = pend[1];
+            pend[1] = Pending{bar, tile, seg};
+        };
+        auto flush = [&]() {
+            cp_wait_but<0>();
+            tell(pend[0]);
+            tell(pend[1]);
+            pend[0].bar = pend[1].bar = -1;
+        };
+        // one answer for the warp: some of what follows is done together
+        auto acquire = [&](int bar, uint32_t parity) {
+            bool ok = mbar_try_wait(&bars[bar], parity & 1u);
+            if (!ok) {
+                flush();
+                ok = wait(bar, parity);
+            }
+            return (bool)__all_sync(0xffffffffu, ok);
+        };
+        uint32_t item = 0;
+        bool ok = true;
+        int seg = 0;
+        look_up();
+        for (int it = 0; it < count; ++it) {
+            const Unit cur = u;
+            const bool first = it == 0 || cur.step == 0;
+            if (it > 0 && cur.step == 0) ++seg;
+            const bool masked = step_masked(p, cur, cur.lo + cur.step * kTN);
+            int64_t *ko = offs + (it & 1) * 2 * kTN, *vo = ko + kTN;
+            ko[t] = page < 0 ? -1 : page_at(p.c.kst, page, slot, cur.head) * kES;
+            vo[t] = page < 0 ? -1 : page_at(p.c.vst, page, slot, cur.head) * kES;
+            float ks = 0.f, vs = 1.f;
+            if constexpr (FMT != 0) {
+                if (page >= 0) {
+                    const int64_t so = scale_at(p.c, page, slot, cur.head);
+                    ks = p.c.ks[so];
+                    vs = p.c.vs[so];
+                }
+            }
+            ok = load_sync(ok);
+            if (!ok) break;
+            if (it + 1 < count) {
+                if (++u.step == u.steps) next_unit<kTM, kTN>(p, u);
+                look_up();
+            }
+            auto queries = [&]() {
+                ok = acquire(B::kQEmpty, (uint32_t)seg + 1);
+                if (!ok) return;
+                const int rows = unit_rows(p, cur);
+                constexpr int kQC = D / 8, kQP = 128 / kQC;  // chunks a row, rows a pass
+                const int qc = t % kQC;
+                float *qf = reinterpret_cast<float *>(sm + C::kOffQf) + (seg & 1) * kTM;
+                for (int r = t / kQC; r < kTM; r += kQP) {
+                    if (r >= 128 && rows <= 128) break;
+                    const int64_t ur = (int64_t)cur.tile * kTM + r;
+                    const int tok = (int)(ur / p.G), hq = cur.head * p.G + (int)(ur - (int64_t)tok * p.G);
+                    const bool live = r < rows;
+                    const T *src = reinterpret_cast<const T *>(p.q) +
+                                   (live ? tok_at(p.sq, cur.t0 + tok, hq) + qc * 8 : 0);
+                    const uint32_t dst = (r >> 7) * C::kTile + sw128_chunk(r & 127, qc, 128);
+                    if constexpr (FMT != 0 && std::is_same<T, __nv_bfloat16>::value) {
+                        // FP16 of the row's own power of two (see attn_rows.cu)
+                        uint4 x = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+                        float big = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y = wide16<T>(w[e]);
+                            big = fmaxf(big, fmaxf(fabsf(y.x), fabsf(y.y)));
+                        }
+                        for (int d = 1; d < kQC; d <<= 1)
+                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+                        const int ex = (__float_as_int(big) >> 23) & 255;
+                        const float g = ex > 0 && ex < 254 ? __int_as_float((254 - ex) << 23) : 1.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y = wide16<T>(w[e]);
+                            w[e] = pack16<__half>(y.x * g, y.y * g);
+                        }
+                        *reinterpret_cast<uint4 *>(sm + dst) = x;
+                        if (qc == 0) qf[r] = 1.f / g;
+                    } else {
+                        cp16z(sb + dst, src, live);
+                        if (FMT != 0 && qc == 0) qf[r] = 1.f;
+                    }
+                }
+                push(B::kQFull, -1, 0);
+            };
+            if constexpr (FMT == 0) {
+                for (int kv = 0; kv < 2 && ok; ++kv, ++item) {
+                    const int b = item % C::kRing;
+                    ok = acquire(B::kEmpty + b, item / C::kRing + 1);
+                    if (!ok) break;
+                    const uint32_t dst = sb + C::kOffRing + b * C::kTile;
+                    const uint8_t *src = kv ? vc : kc;
+                    const int64_t *of = kv ? vo : ko;
+#pragma unroll 8
+                    for (int i = 0; i < kPasses; ++i) {
+                        const int r = r0 + i * kPass;
+                        const int64_t o = of[r];
+                        cp16z(dst + sw128_chunk(r, ch, kTN), o < 0 ? src : src + o + ch * 16, o >= 0);
+                    }
+                    push(B::kFull + b, kv && masked ? b : -1, seg);
+                    if (kv == 0 && first) queries();
+                }
+            } else {
+                uint4 x[kPasses], y[kPasses];
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const int64_t o = ko[r0 + i * kPass], q = vo[r0 + i * kPass];
+                    x[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(kc + o + ch * 16);
+                    y[i] = q < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(vc + q + ch * 16);
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++item) {
+                    if (!ok) break;
+                    const int b = item % C::kRing;
+                    ok = acquire(B::kEmpty + b, item / C::kRing + 1);
+                    if (!ok) break;
+                    if (kv == 0) {
+                        float *sc = reinterpret_cast<float *>(sm + C::kOffScale) + (it % C::kScales) * 3 * kTN;
+                        const float v = vs < kTLeast ? kTLeast : vs;
+                        sc[t] = ks;
+                        sc[kTN + t] = __log2f(v);
+                        sc[2 * kTN + t] = __fdividef(1.f, v);
+                    }
+                    uint8_t *tile = sm + C::kOffRing + b * C::kTile;
+#pragma unroll
+                    for (int i = 0; i < kPasses; ++i) {
+                        const uint4 w = kv ? y[i] : x[i];
+                        uint4 e0, e1;
+                        widen4<FMT>(w.x, e0.x, e0.y);
+                        widen4<FMT>(w.y, e0.z, e0.w);
+                        widen4<FMT>(w.z, e1.x, e1.y);
+                        widen4<FMT>(w.w, e1.z, e1.w);
+                        const int r = r0 + i * kPass;
+                        // odd chunks first in the upper columns: the two
+                        // column blocks lie on the same banks
+                        const bool odd = ch >= kChunks / 2 && D == 128;
+                        *reinterpret_cast<uint4 *>(tile + sw128_chunk(r, 2 * ch + (odd ? 1 : 0), kTN)) = odd ? e1 : e0;
+                        *reinterpret_cast<uint4 *>(tile + sw128_chunk(r, 2 * ch + (odd ? 0 : 1), kTN)) = odd ? e0 : e1;
+                    }
+                    fence_async_smem();
+                    mbar_arrive(&bars[B::kFull + b]);
+                    if (kv == 0 && first) {
+                        queries();
+                        flush();
+                    }
+                }
+            }
+        }
+        flush();
+    } else {
+        regs_down<kRegRest>();
+        if (warp == 12 && lane == 0) {
+            // -------------------------------------------------- products
+            constexpr uint32_t kIdS = tiles_idesc<TP>(128, 0), kIdO = tiles_idesc<TP>(D, 1);
+            auto score = [&](int half, int b) {
+                const uint32_t q = sb + half * C::kTile, kt = sb + C::kOffRing + b * C::kTile;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    const uint32_t o = (d >> 2) * 16384 + (d & 3) * 32;
+                    umma_bf16(tmem + C::kColS + half * 128, sdesc_sw128(q + o, 16, 1024),
+                              sdesc_sw128(kt + o, 16, 1024), kIdS, d > 0);
+                }
+            };
+            auto gather = [&](int half, int b, bool fresh) {
+                const uint32_t vt = sb + C::kOffRing + b * C::kTile;
+#pragma unroll
+                for (int j = 0; j < kTN / 16; ++j)
+                    umma_bf16_ts(tmem + C::kColO + half * D, tmem + C::kColS + half * 128 + 8 * j,
+                                 sdesc_sw128(vt + j * 2048, 16384, 1024), kIdO, !(fresh && j == 0));
+            };
+            uint32_t item = 0, kp[2] = {0, 0};
+            bool ok = true;
+            int left = count;
+            for (int seg = 0; left > 0 && ok; ++seg) {
+                const int steps = min(left, u.steps - u.step);
+                left -= steps;
+                const int halves = unit_rows(p, u) > 128 ? 2 : 1;
+                ok = wait(B::kFull + item % C::kRing, item / C::kRing) && wait(B::kQFull, seg);
+                if (!ok) break;
+                tc_fence_after();
+                for (int h = 0; h < halves; ++h) {
+                    score(h, item % C::kRing);
+                    umma_commit(&bars[B::kS + h]);
+                }
+                umma_commit(&bars[B::kEmpty + item % C::kRing]);
+                if (steps == 1) umma_commit(&bars[B::kQEmpty]);
+                for (int s = 0; s < steps && ok; ++s, item += 2) {
+                    const uint32_t iv = item + 1, ik = item + 2;
+                    const bool more = s + 1 < steps;
+                    ok = wait(B::kFull + iv % C::kRing, iv / C::kRing);
+                    if (ok && more) ok = wait(B::kFull + ik % C::kRing, ik / C::kRing);
+                    for (int h = 0; h < halves && ok; ++h) {
+                        ok = wait(B::kP + h, kp[h]++);
+                        if (!ok) break;
+                        tc_fence_after();
+                        gather(h, iv % C::kRing, s == 0);
+                        umma_commit(&bars[B::kO + h]);
+                        if (h + 1 == halves) umma_commit(&bars[B::kEmpty + iv % C::kRing]);
+                        if (more) {
+                            score(h, ik % C::kRing);
+                            umma_commit(&bars[B::kS + h]);
+                            if (h + 1 == halves) {
+                                umma_commit(&bars[B::kEmpty + ik % C::kRing]);
+                                if (s + 2 == steps) umma_commit(&bars[B::kQEmpty]);
+                            }
+                        }
+                    }
+                }
+                if (left) next_unit<kTM, kTN>(p, u);
+            }
+        }
+        if (warp == 12 && lane == 0) {  // nothing is in flight when the memory goes back
+            umma_commit(&bars[B::kDrain]);
+            mbar_wait(&bars[B::kDrain], 0, p.r.status);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) {
+        tmem_relinquish();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int FMT, int D>
+cudaError_t launch_tiles(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
+    using C = TilesCfg<D>;
+    TilesArgs a{p, ws, (p.r.N + kSplitSlots - 1) / kSplitSlots, 1};
+    auto k = k_attn_tiles<T, FMT, D>;
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, k);
+    if (e != cudaSuccess) return e;
+    // the split of the registers draws on what the launch holds
+    if (at.numRegs * 4 < 2 * kRegSoftmax + kRegLoad + kRegRest) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+    if (e != cudaSuccess) return e;
+    k<<<ctas, kTThreads, C::kBytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_fmt(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
+    if (p.c.dtype == GDR_E4M3) return launch_tiles<T, 1, D>(p, ws, ctas, st);
+    if (p.c.dtype == GDR_I8) return launch_tiles<T, 2, D>(p, ws, ctas, st);
+    return launch_tiles<T, 0, D>(p, ws, ctas, st);
+}
+
+template <typename T>
+cudaError_t launch_dim(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
+    return p.K == 64 ? launch_fmt<T, 64>(p, ws, ctas, st) : launch_fmt<T, 128>(p, ws, ctas, st);
+}
+
+}  // namespace
+
+SplitPlan attn_tiles_plan(const AttnProblem &p) {
+    SplitPlan s{};
+    const int g = device_sms();
+    s.ctas = p.grid_limit > 0 && p.grid_limit < g ? p.grid_limit : g;
+    s.workers = s.ctas;
+    s.rows = kTM;
+    return s;
+}
+
+cudaError_t attn_tiles(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
+                       cudaStream_t st) {
+    return p.dtype == GDR_F16 ? launch_dim<__half>(p, ws, s.ctas, st)
+                              : launch_dim<__nv_bfloat16>(p, ws, s.ctas, st);
+}
+
+}  // namespace gdr

@@ -798,6 +798,7 @@ const char *gdr_kernel_name(int id) {
     case kKAttnSimt: return "attn_simt";
     case kKAttnRows: return "attn_rows";
     case kKAttnJoin: return "attn_join";
+    case kKAttnTiles: return "attn_tiles";
     default: return "?";
     }
 }

@@ -90,6 +90,7 @@ enum KernelId {
     kKAttnSimt = 35,
     kKAttnRows = 36,
     kKAttnJoin = 37,
+    kKAttnTiles = 38,
     kKNumIds
 };
 
@@ -207,8 +208,12 @@ bool attn_rows_supported(const AttnProblem &p);
 SplitPlan attn_rows_plan(const AttnProblem &p);
 cudaError_t attn_rows(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
                       cudaStream_t st);
-cudaError_t attn_rows_join(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
-                           cudaStream_t st);
+// Many rows: tiles of 256 on tcgen05, for the same types, widths and strides.
+SplitPlan attn_tiles_plan(const AttnProblem &p);
+cudaError_t attn_tiles(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
+                       cudaStream_t st);
+cudaError_t attn_join(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
+                      cudaStream_t st);
 
 // Device scratch from the library's pool, ordered on the stream.
 cudaError_t scratch_alloc(void **ptr, size_t bytes, cudaStream_t st);

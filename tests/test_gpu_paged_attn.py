@@ -10,7 +10,7 @@ from paged_ref import Batch, check
 
 pytestmark = pytest.mark.gpu
 
-ROUTES = [1, 3]
+ROUTES = [1, 2, 3]
 
 # (new tokens, cached tokens with them): one token, none, odd chunks, a chunk
 # longer than the cache (its first rows see nothing), pages ending in tiles
