@@ -29,6 +29,7 @@ struct AttnProblem {
     int64_t window;       // 0: none
     float scale;
     int grid_limit;
+    int align;            // tiles' first positions are multiples of it (a power of two)
 };
 
 // Positions [lo, hi) that the token at position pos of a sequence of kv

@@ -180,7 +180,10 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
         if (opt && opt->n_launches) *opt->n_launches = rec.count;
         return GDR_OK;
     }
-    const bool tiles = force == 2 || (force == 0 && tile_rows(*dims) * p.G > kFewRows);
+    const bool can = attn_tiles_supported(p);
+    if (force == 2 && !can) return GDR_ERR_UNSUPPORTED;
+    const bool tiles = force == 2 || (force == 0 && can && tile_rows(*dims) * p.G > kFewRows);
+    for (p.align = 1; p.align < 128 && p.c.page_size % (2 * p.align) == 0;) p.align *= 2;
     const SplitPlan plan = tiles ? attn_tiles_plan(p) : attn_rows_plan(p);
     const size_t need = split_bytes(plan, p.V);
     void *base = opt ? opt->workspace : nullptr;

@@ -49,7 +49,8 @@ __device__ __forceinline__ int tiles_of(const AttnProblem &p, int len) {
     return (int)(((int64_t)len * p.G + (M - 1)) / M);
 }
 
-// Positions [lo, hi) that the rows of a tile see, and its steps.
+// Positions [lo, hi) that the rows of a tile see, lo down to a multiple of
+// p.align (a box of a page begins there), and the tile's steps.
 template <int M, int BN>
 __device__ __forceinline__ int tile_steps(const AttnProblem &p, int len, int kv, int tile, int &lo,
                                           int &hi) {
@@ -60,8 +61,8 @@ __device__ __forceinline__ int tile_steps(const AttnProblem &p, int len, int kv,
     int64_t a, b, c, d;
     visible(p, kv, (int64_t)kv - len + i0, a, b);
     visible(p, kv, (int64_t)kv - len + i1, c, d);
-    lo = (int)a;
     hi = (int)(d > a ? d : a);
+    lo = (int)a & -p.align;
     const int s = (hi - lo + BN - 1) / BN;
     return s > 0 ? s : 1;
 }

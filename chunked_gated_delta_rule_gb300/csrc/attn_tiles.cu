@@ -15,13 +15,19 @@
 // function units).  So the two halves run in turns: one half's exponentials
 // beside the other's products.
 //   warps 0-3, 4-7   softmax of rows 0-127, 128-255 (a thread a row)
-//   warps 8-11       loads: page look-up, keys and values into a ring of
-//                    tiles, queries; 8-bit rows are widened to FP16 on the way
+//   warps 8-11       queries into shared memory; 8-bit rows widened to FP16;
+//                    values of masked steps looked over (below)
 //   warp 12          every tcgen05 product
-// Keys and values come through the page table token by token, so any page
-// size and order will do, as 16-byte asynchronous copies into the 128-byte
-// swizzled layout that the products read.  A position past the last one that
-// the unit sees is filled with zeros.
+//   warp 13          page look-up, keys and values by TMA
+// A step's 128 positions come as boxes of gcd(page size, 128) slots, each of
+// one page, into the 128-byte swizzled layout that the products read (page
+// sizes that are no multiple of 8 go to the kernel of few rows).  A box
+// without a page is filled with zeros.
+// A position that some rows see and others do not must not reach the others
+// as 0 * NaN, and what a page holds past the last position is anything: in
+// masked steps (one to three a unit) warps 8-11 clear the values past the end
+// and those that are not finite before the product, and the end of the piece
+// adds the latter to the rows that see them.
 // 8-bit caches: see attn_rows.cu for the place of the scales.
 //
 // The steps of the call are shared out equally over one CTA an SM
@@ -32,6 +38,7 @@
 #include "attn_split.cuh"
 #include "gdr_launch.cuh"
 #include "tc_common.cuh"
+#include "tma_host.cuh"
 
 namespace gdr {
 namespace {
@@ -45,33 +52,35 @@ constexpr float kTLog2e = 1.4426950408889634f;
 constexpr float kTLn2 = 0.6931471805599453f;
 constexpr float kTLeast = 7.888609052210118e-31f;  // 2^-100
 
-// Registers a thread of the softmax warps, the loaders and the rest: 128 each
-// at launch, 2 x 184 + 104 + 40 = 4 x 128.
-constexpr int kRegSoftmax = 184, kRegLoad = 104, kRegRest = 40;
-static_assert(2 * kRegSoftmax + kRegLoad + kRegRest <= 4 * 128, "the launch's registers");
+// Registers a thread of the softmax warps, the helpers and the rest: 128 each
+// at launch, 2 x 184 + 88 + 56 = 4 x 128.
+constexpr int kRegSoftmax = 184, kRegHelp = 88, kRegRest = 56;
+static_assert(2 * kRegSoftmax + kRegHelp + kRegRest <= 4 * 128, "the launch's registers");
 
-template <int D>
+template <int FMT, int D>
 struct TilesCfg {
     static constexpr uint32_t kTile = kTN * D * 2;     // a 128-row tile of 16-bit values
-    static constexpr int kRing = D == 128 ? 4 : 8;     // tiles of keys and values
-    // steps whose scales are kept: a step's keys are loaded once the products
+    static constexpr int kRing = D == 64 ? 8 : FMT ? 3 : 4;  // tiles of keys and values
+    static constexpr int kRaw = FMT ? 3 : 0;                 // 8-bit tiles on their way
+    static constexpr uint32_t kRawTile = kTN * D, kRawSize = kRawTile + 2 * kTN * 4;
+    // steps whose scales are kept: a step's keys are widened once the products
     // of the step kRing / 2 before it are done, so that softmax is at most
-    // kRing / 2 steps behind
-    static constexpr int kScales = kRing;
+    // that far behind
+    static constexpr int kScales = FMT ? (D == 64 ? 8 : 4) : 0;
     static constexpr uint32_t kOffRing = 2 * kTile;    // after the queries
-    static constexpr uint32_t kOffScale = kOffRing + kRing * kTile;  // [kScales][3][128]
-    static constexpr uint32_t kOffOff = kOffScale + kScales * 3 * kTN * 4; // [2 steps][K, V][128]
-    static constexpr uint32_t kOffQf = kOffOff + 2 * 2 * kTN * 8;    // [2 units][256]
+    static constexpr uint32_t kOffRaw = kOffRing + kRing * kTile;    // + scales of keys, values
+    static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawSize; // [kScales][3][128]
+    static constexpr uint32_t kOffQf = kOffScale + kScales * 3 * kTN * 4;  // [2 units][256]
     static constexpr uint32_t kOffBar = kOffQf + 2 * kTM * 4;
     static constexpr uint32_t kBytes = kOffBar + 512 + 1024;         // and to align
     static constexpr uint32_t kColS = 0, kColO = 256;  // TMEM: S / P of both halves, O
-};
-
-// mbarriers
-template <int RING>
-struct Bars {
-    static constexpr int kFull = 0, kEmpty = RING, kQFull = 2 * RING, kQEmpty = kQFull + 1,
-                         kS = kQFull + 2, kP = kS + 2, kO = kP + 2, kDrain = kO + 2;
+    // mbarriers
+    static constexpr int kFull = 0, kEmpty = kRing;    // tiles
+    static constexpr int kLand = 2 * kRing;            // FMT: raw tiles; else masked values, by tile
+    static constexpr int kLands = FMT ? kRaw : kRing, kTaken = kLand + kLands;  // raw tiles read
+    static constexpr int kQFull = kTaken + kRaw, kQEmpty = kQFull + 1, kS = kQFull + 2, kP = kS + 2,
+                         kO = kP + 2, kDrain = kO + 2;
+    static_assert((kDrain + 1) * 8 <= 512, "barriers");
 };
 
 struct TilesArgs {
@@ -79,6 +88,8 @@ struct TilesArgs {
     SplitScratch ws;
     int64_t per;
     int min_steps;
+    int box;             // slots of a TMA box
+    CUtensorMap tk, tv;  // [page][head][slot][column] of the caches
 };
 
 template <int R>
@@ -145,12 +156,17 @@ __device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool live) 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_wait_but() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar,
+                                            int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
 }
-// Barrier of the loading warps: whether all of them are well.
-__device__ __forceinline__ bool load_sync(bool ok) {
+
+// Barrier of the helping warps: whether all of them are well.
+__device__ __forceinline__ bool help_sync(bool ok) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -215,13 +231,15 @@ __device__ __forceinline__ int unit_rows(const AttnProblem &p, const Unit &u) {
 
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_constant__ TilesArgs a) {
-    using C = TilesCfg<D>;
-    using B = Bars<C::kRing>;
+    using C = TilesCfg<FMT, D>;
+    using B = C;  // its barriers
     using TP = typename std::conditional<FMT == 0, T, __half>::type;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_pre[kSplitSlots + 1];
     __shared__ Unit s_unit;
+    __shared__ int64_t s_share[4];  // steps of the call, workers, this one's first step and count
     __shared__ int s_poison[8];  // unit (count, modulo 8) + 1 whose masked values are not finite
+    __shared__ int2 s_piece[8];  // steps and halves of the piece (count, modulo 8), for the products
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort_flag;
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -235,9 +253,11 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     pdl_trigger();
     if (tid == 0) {
         for (int i = 0; i < C::kRing; ++i) {
-            mbar_init(&bars[B::kFull + i], 128);
+            mbar_init(&bars[B::kFull + i], FMT ? 128 : 1);
             mbar_init(&bars[B::kEmpty + i], 1);
         }
+        for (int i = 0; i < C::kLands; ++i) mbar_init(&bars[B::kLand + i], 1);
+        for (int i = 0; i < C::kRaw; ++i) mbar_init(&bars[B::kTaken + i], 128);
         mbar_init(&bars[B::kQFull], 128);
         mbar_init(&bars[B::kQEmpty], 1);
         for (int i = 0; i < 2; ++i) {
@@ -252,16 +272,22 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     if (tid < 8) s_poison[tid] = 0;
     if (warp == 12) tmem_alloc(&s_tmem, 512);
     split_prefix<kTM, kTN, kTThreads>(p, a.per, s_pre);
-    const int64_t total = s_pre[kSplitSlots];
-    const int64_t worker = blockIdx.x;
-    int64_t nw = gridDim.x;
-    if (nw * a.min_steps > total) nw = (total + a.min_steps - 1) / a.min_steps;
-    if (tid == 0) a.ws.rec[worker] = make_int4(0, 0, 0, 0);
-    const int64_t begin = worker < nw ? share_begin(total, worker, nw) : 0;
-    const int count = worker < nw ? (int)(share_begin(total, worker + 1, nw) - begin) : 0;
-    if (warp == 0 && count) {
-        const Unit u = split_locate<kTM, kTN>(p, a.per, s_pre, begin);
-        if (lane == 0) s_unit = u;
+    if (warp == 0) {
+        const int64_t total = s_pre[kSplitSlots], w = blockIdx.x;
+        int64_t nw = gridDim.x;
+        if (nw * a.min_steps > total) nw = (total + a.min_steps - 1) / a.min_steps;
+        const int64_t begin = w < nw ? share_begin(total, w, nw) : 0;
+        const int64_t steps = w < nw ? share_begin(total, w + 1, nw) - begin : 0;
+        Unit u{};
+        if (steps) u = split_locate<kTM, kTN>(p, a.per, s_pre, begin);
+        if (lane == 0) {
+            s_unit = u;
+            s_share[0] = total;
+            s_share[1] = nw;
+            s_share[2] = begin;
+            s_share[3] = steps;
+            a.ws.rec[w] = make_int4(0, 0, 0, 0);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -270,13 +296,15 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     auto wait = [&](int b, uint32_t parity) {
         return mbar_wait_or_abort(&bars[b], parity & 1u, p.r.status, s_abort);
     };
-    Unit u = s_unit;
+    const int count = (int)s_share[3];
 
     if (count == 0) {
         // no steps for this CTA
     } else if (warp < 8) {
         // ------------------------------------------------------- softmax
         regs_up<kRegSoftmax>();
+        Unit u = s_unit;
+        const int64_t worker = blockIdx.x;
         const int half = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane << 16
         const uint32_t ts = tmem + lanes + C::kColS + half * 128;
@@ -365,16 +393,15 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                             ok = __all_sync(0xffffffffu, wait(B::kO + half, k - 1));
                             if (!ok) break;
                             tc_fence_after();
+#pragma unroll 1
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t o[16];
+                                tmem_ld16(to + 16 * q, o);
+                                tmem_wait_ld(o);
 #pragma unroll
-                            for (int q = 0; q < D / 32; ++q) {
-                                uint32_t o[32];
-                                tmem_ld32(to + 32 * q, o);
-                                tmem_wait_ld();
-                                reg_fence(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
-                                tmem_st32(to + 32 * q, o);
+                                tmem_st16(to + 16 * q, o);
                             }
                             tmem_wait_st();
                         }
@@ -485,177 +512,131 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             done += steps;
             if (begun && !ends && tid == 0)
                 a.ws.rec[worker] = make_int4(u.n, u.tile, u.head,
-                                             pieces_from(total, worker, nw, begin + done + (u.steps - first - steps)));
+                                             pieces_from(s_share[0], worker, s_share[1],
+                                                         s_share[2] + done + (u.steps - first - steps)));
             if (left) next_unit<kTM, kTN>(p, u);
         }
     } else if (warp < 12) {
-        // --------------------------------------------------------- loads
-        regs_down<kRegLoad>();
+        // ------------------------------------------------------- helpers
+        regs_down<kRegHelp>();
+        Unit u = s_unit;
         const int t = tid - 256;
-        constexpr int kES = FMT ? 1 : 2;
-        constexpr int kChunks = D * kES / 16, kPass = 128 / kChunks;  // rows a pass of the 128 threads
-        constexpr int kPasses = kTN / kPass;
-        const int ch = t % kChunks, r0 = t / kChunks;
-        const uint8_t *kc = reinterpret_cast<const uint8_t *>(p.c.k);
-        const uint8_t *vc = reinterpret_cast<const uint8_t *>(p.c.v);
-        int64_t *offs = reinterpret_cast<int64_t *>(sm + C::kOffOff);
-        int page = -1, slot = 0;
-        auto look_up = [&]() {
-            const int pos = u.lo + u.step * kTN + t;
-            page = -1;
-            if (pos < u.hi) {
-                const int pi = pos / p.c.page_size;
-                slot = pos - pi * p.c.page_size;
-                page = page_of(p.c, u.n, pi, p.r.status);
-            }
-        };
-        // copies in flight whose barrier has not been told: their barrier,
-        // the tile to be looked over for values that are not finite, its unit
-        struct Pending {
-            int bar, tile, seg;
-        };
-        Pending pend[2] = {{-1, -1, 0}, {-1, -1, 0}};
-        auto tell = [&](const Pending &x) {
-            if (x.bar < 0) return;
-            if (FMT == 0 && x.tile >= 0) {
-                constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-                uint8_t *tile = sm + C::kOffRing + x.tile * C::kTile;
-                for (int i = 0; i < kPasses; ++i) {
-                    uint32_t *w = reinterpret_cast<uint32_t *>(tile + sw128_chunk(r0 + i * kPass, ch, kTN));
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t y = w[e];
-                        const bool b0 = (y & kExp) == kExp, b1 = (y >> 16 & kExp) == kExp;
-                        if (b0 || b1) {
-                            w[e] = (b0 ? 0u : y & 0xffffu) | (b1 ? 0u : y & 0xffff0000u);
-                            s_poison[x.seg & 7] = x.seg + 1;
-                        }
-                    }
-                }
-            }
-            fence_async_smem();
-            mbar_arrive(&bars[x.bar]);
-        };
-        auto push = [&](int bar, int tile, int seg) {  // the copies since the last push
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            cp_wait_but<2>();
-            tell(pend[0]);
-            pend[0] = pend[1];
-            pend[1] = Pending{bar, tile, seg};
-        };
-        auto flush = [&]() {
-            cp_wait_but<0>();
-            tell(pend[0]);
-            tell(pend[1]);
-            pend[0].bar = pend[1].bar = -1;
-        };
-        // one answer for the warp: some of what follows is done together
-        auto acquire = [&](int bar, uint32_t parity) {
-            bool ok = mbar_try_wait(&bars[bar], parity & 1u);
-            if (!ok) {
-                flush();
-                ok = wait(bar, parity);
-            }
-            return (bool)__all_sync(0xffffffffu, ok);
-        };
-        uint32_t item = 0;
         bool ok = true;
         int seg = 0;
-        look_up();
-        for (int it = 0; it < count; ++it) {
-            const Unit cur = u;
-            const bool first = it == 0 || cur.step == 0;
-            if (it > 0 && cur.step == 0) ++seg;
-            const bool masked = step_masked(p, cur, cur.lo + cur.step * kTN);
-            int64_t *ko = offs + (it & 1) * 2 * kTN, *vo = ko + kTN;
-            ko[t] = page < 0 ? -1 : page_at(p.c.kst, page, slot, cur.head) * kES;
-            vo[t] = page < 0 ? -1 : page_at(p.c.vst, page, slot, cur.head) * kES;
-            float ks = 0.f, vs = 1.f;
-            if constexpr (FMT != 0) {
-                if (page >= 0) {
-                    const int64_t so = scale_at(p.c, page, slot, cur.head);
-                    ks = p.c.ks[so];
-                    vs = p.c.vs[so];
-                }
-            }
-            ok = load_sync(ok);
-            if (!ok) break;
-            if (it + 1 < count) {
-                if (++u.step == u.steps) next_unit<kTM, kTN>(p, u);
-                look_up();
-            }
-            auto queries = [&]() {
-                ok = acquire(B::kQEmpty, (uint32_t)seg + 1);
-                if (!ok) return;
-                const int rows = unit_rows(p, cur);
-                constexpr int kQC = D / 8, kQP = 128 / kQC;  // chunks a row, rows a pass
-                const int qc = t % kQC;
-                float *qf = reinterpret_cast<float *>(sm + C::kOffQf) + (seg & 1) * kTM;
-                for (int r = t / kQC; r < kTM; r += kQP) {
-                    if (r >= 128 && rows <= 128) break;
-                    const int64_t ur = (int64_t)cur.tile * kTM + r;
-                    const int tok = (int)(ur / p.G), hq = cur.head * p.G + (int)(ur - (int64_t)tok * p.G);
-                    const bool live = r < rows;
-                    const T *src = reinterpret_cast<const T *>(p.q) +
-                                   (live ? tok_at(p.sq, cur.t0 + tok, hq) + qc * 8 : 0);
-                    const uint32_t dst = (r >> 7) * C::kTile + sw128_chunk(r & 127, qc, 128);
-                    if constexpr (FMT != 0 && std::is_same<T, __nv_bfloat16>::value) {
-                        // FP16 of the row's own power of two (see attn_rows.cu)
-                        uint4 x = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-                        float big = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 y = wide16<T>(w[e]);
-                            big = fmaxf(big, fmaxf(fabsf(y.x), fabsf(y.y)));
-                        }
-                        for (int d = 1; d < kQC; d <<= 1)
-                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-                        const int ex = (__float_as_int(big) >> 23) & 255;
-                        const float g = ex > 0 && ex < 254 ? __int_as_float((254 - ex) << 23) : 1.f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 y = wide16<T>(w[e]);
-                            w[e] = pack16<__half>(y.x * g, y.y * g);
-                        }
-                        *reinterpret_cast<uint4 *>(sm + dst) = x;
-                        if (qc == 0) qf[r] = 1.f / g;
-                    } else {
-                        cp16z(sb + dst, src, live);
-                        if (FMT != 0 && qc == 0) qf[r] = 1.f;
-                    }
-                }
-                push(B::kQFull, -1, 0);
-            };
-            if constexpr (FMT == 0) {
-                for (int kv = 0; kv < 2 && ok; ++kv, ++item) {
-                    const int b = item % C::kRing;
-                    ok = acquire(B::kEmpty + b, item / C::kRing + 1);
-                    if (!ok) break;
-                    const uint32_t dst = sb + C::kOffRing + b * C::kTile;
-                    const uint8_t *src = kv ? vc : kc;
-                    const int64_t *of = kv ? vo : ko;
+        uint32_t item = 0, landed = 0;
+        auto queries = [&]() {
+            ok = __all_sync(0xffffffffu, wait(B::kQEmpty, (uint32_t)seg + 1));
+            if (!ok) return;
+            const int rows = unit_rows(p, u);
+            constexpr int kQC = D / 8, kQP = 128 / kQC;  // chunks a row, rows a pass
+            const int qc = t % kQC, halves = rows > 128 ? 2 : 1;
+            float *qf = reinterpret_cast<float *>(sm + C::kOffQf) + (seg & 1) * kTM;
+            constexpr bool kConvert = FMT != 0 && std::is_same<T, __nv_bfloat16>::value;
 #pragma unroll 8
-                    for (int i = 0; i < kPasses; ++i) {
-                        const int r = r0 + i * kPass;
-                        const int64_t o = of[r];
-                        cp16z(dst + sw128_chunk(r, ch, kTN), o < 0 ? src : src + o + ch * 16, o >= 0);
+            for (int r = t / kQC; r < 128 * halves; r += kQP) {
+                const int64_t ur = (int64_t)u.tile * kTM + r;
+                const int tok = (int)(ur / p.G), hq = u.head * p.G + (int)(ur - (int64_t)tok * p.G);
+                const bool live = r < rows;
+                const T *src = reinterpret_cast<const T *>(p.q) +
+                               (live ? tok_at(p.sq, u.t0 + tok, hq) + qc * 8 : 0);
+                const uint32_t dst = (r >> 7) * C::kTile + sw128_chunk(r & 127, qc, 128);
+                if constexpr (kConvert) {
+                    // FP16 of the row's own power of two (see attn_rows.cu)
+                    uint4 x = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+                    float big = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = wide16<T>(w[e]);
+                        big = fmaxf(big, fmaxf(fabsf(y.x), fabsf(y.y)));
                     }
-                    push(B::kFull + b, kv && masked ? b : -1, seg);
-                    if (kv == 0 && first) queries();
+#pragma unroll
+                    for (int d = 1; d < kQC; d <<= 1)
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+                    const int ex = (__float_as_int(big) >> 23) & 255;
+                    const float g = ex > 0 && ex < 254 ? __int_as_float((254 - ex) << 23) : 1.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = wide16<T>(w[e]);
+                        w[e] = pack16<__half>(y.x * g, y.y * g);
+                    }
+                    *reinterpret_cast<uint4 *>(sm + dst) = x;
+                    if (qc == 0) qf[r] = 1.f / g;
+                } else {
+                    cp16z(sb + dst, src, live);
+                    if (FMT != 0 && qc == 0) qf[r] = 1.f;
+                }
+            }
+            if constexpr (!kConvert) asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            mbar_arrive(&bars[B::kQFull]);
+        };
+        for (int it = 0; it < count; ++it) {
+            ok = help_sync(ok);
+            if (!ok) break;
+            if (it > 0 && u.step == 0) ++seg;
+            if (it == 0 || u.step == 0) {
+                if (t == 0)
+                    s_piece[seg & 7] = make_int2(min(count - it, u.steps - u.step),
+                                                 unit_rows(p, u) > 128 ? 2 : 1);
+                queries();
+            }
+            const int base = u.lo + u.step * kTN, left = u.hi - base;  // positions of the step
+            if constexpr (FMT == 0) {
+                const int b = (item + 1) % C::kRing;
+                item += 2;
+                if (ok && step_masked(p, u, base)) {
+                    ok = __all_sync(0xffffffffu, wait(B::kLand + b, landed >> b));
+                    landed ^= 1u << b;
+                    if (ok) {
+                        constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+                        uint8_t *tile = sm + C::kOffRing + b * C::kTile;
+                        bool bad = false;
+                        for (int i = t; i < kTN * D / 8; i += 128) {
+                            const int r = i / (D / 8);
+                            uint4 *w4 = reinterpret_cast<uint4 *>(tile + sw128_chunk(r, i % (D / 8), kTN));
+                            uint4 x = *w4;
+                            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+                            bool change = r >= left;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t y = w[e];
+                                const bool b0 = (y & kExp) == kExp, b1 = (y >> 16 & kExp) == kExp;
+                                if (r >= left) {
+                                    w[e] = 0;
+                                } else if (b0 || b1) {
+                                    w[e] = (b0 ? 0u : y & 0xffffu) | (b1 ? 0u : y & 0xffff0000u);
+                                    bad = change = true;
+                                }
+                            }
+                            if (change) *w4 = x;
+                        }
+                        if (bad) s_poison[seg & 7] = seg + 1;
+                        fence_async_smem();
+                    }
+                    ok = help_sync(ok);
+                    if (!ok) break;
+                    if (t == 0) mbar_arrive(&bars[B::kFull + b]);
                 }
             } else {
-                uint4 x[kPasses], y[kPasses];
-#pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const int64_t o = ko[r0 + i * kPass], q = vo[r0 + i * kPass];
-                    x[i] = o < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(kc + o + ch * 16);
-                    y[i] = q < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(vc + q + ch * 16);
-                }
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++item) {
+                constexpr int kChunks = D / 16, kPass = 128 / kChunks, kPasses = kTN / kPass;
+                const int ch = t % kChunks, r0 = t / kChunks;
+                for (int kv = 0; kv < 2 && ok; ++kv, ++item) {
+                    const int b = item % C::kRing, w = item % C::kRaw;
+                    const uint8_t *raw = sm + C::kOffRaw + w * C::kRawSize;
+                    ok = __all_sync(0xffffffffu, wait(B::kLand + w, item / C::kRaw));
                     if (!ok) break;
-                    const int b = item % C::kRing;
-                    ok = acquire(B::kEmpty + b, item / C::kRing + 1);
+                    uint4 x[kPasses];
+#pragma unroll
+                    for (int i = 0; i < kPasses; ++i)
+                        x[i] = *reinterpret_cast<const uint4 *>(raw + (r0 + i * kPass) * D + ch * 16);
+                    float ks = 0.f, vs = 1.f;
+                    if (kv == 0 && t < left) {
+                        ks = reinterpret_cast<const float *>(raw + C::kRawTile)[t];
+                        vs = reinterpret_cast<const float *>(raw + C::kRawTile)[kTN + t];
+                    }
+                    mbar_arrive(&bars[B::kTaken + w]);
+                    ok = __all_sync(0xffffffffu, wait(B::kEmpty + b, item / C::kRing + 1));
                     if (!ok) break;
                     if (kv == 0) {
                         float *sc = reinterpret_cast<float *>(sm + C::kOffScale) + (it % C::kScales) * 3 * kTN;
@@ -667,13 +648,13 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     uint8_t *tile = sm + C::kOffRing + b * C::kTile;
 #pragma unroll
                     for (int i = 0; i < kPasses; ++i) {
-                        const uint4 w = kv ? y[i] : x[i];
-                        uint4 e0, e1;
-                        widen4<FMT>(w.x, e0.x, e0.y);
-                        widen4<FMT>(w.y, e0.z, e0.w);
-                        widen4<FMT>(w.z, e1.x, e1.y);
-                        widen4<FMT>(w.w, e1.z, e1.w);
                         const int r = r0 + i * kPass;
+                        uint4 e0, e1;
+                        if (r >= left) x[i] = make_uint4(0, 0, 0, 0);  // past the end: anything
+                        widen4<FMT>(x[i].x, e0.x, e0.y);
+                        widen4<FMT>(x[i].y, e0.z, e0.w);
+                        widen4<FMT>(x[i].z, e1.x, e1.y);
+                        widen4<FMT>(x[i].w, e1.z, e1.w);
                         // odd chunks first in the upper columns: the two
                         // column blocks lie on the same banks
                         const bool odd = ch >= kChunks / 2 && D == 128;
@@ -682,58 +663,59 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     }
                     fence_async_smem();
                     mbar_arrive(&bars[B::kFull + b]);
-                    if (kv == 0 && first) {
-                        queries();
-                        flush();
-                    }
                 }
             }
+            if (it + 1 < count && ++u.step == u.steps) next_unit<kTM, kTN>(p, u);
         }
-        flush();
     } else {
         regs_down<kRegRest>();
         if (warp == 12 && lane == 0) {
             // -------------------------------------------------- products
             constexpr uint32_t kIdS = tiles_idesc<TP>(128, 0), kIdO = tiles_idesc<TP>(D, 1);
+            // descriptors as a base plus a constant for each product: the
+            // address is their low 14 bits, in units of 16 bytes
+            const uint64_t dk0 = sdesc_sw128(sb, 16, 1024), dv0 = sdesc_sw128(sb, 16384, 1024);
             auto score = [&](int half, int b) {
-                const uint32_t q = sb + half * C::kTile, kt = sb + C::kOffRing + b * C::kTile;
+                const uint64_t q = dk0 + half * (C::kTile >> 4);
+                const uint64_t kt = dk0 + ((C::kOffRing + b * C::kTile) >> 4);
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
-                    const uint32_t o = (d >> 2) * 16384 + (d & 3) * 32;
-                    umma_bf16(tmem + C::kColS + half * 128, sdesc_sw128(q + o, 16, 1024),
-                              sdesc_sw128(kt + o, 16, 1024), kIdS, d > 0);
+                    const uint64_t o = ((d >> 2) * 16384 + (d & 3) * 32) >> 4;
+                    umma_bf16(tmem + C::kColS + half * 128, q + o, kt + o, kIdS, d > 0);
                 }
             };
             auto gather = [&](int half, int b, bool fresh) {
-                const uint32_t vt = sb + C::kOffRing + b * C::kTile;
+                const uint64_t vt = dv0 + ((C::kOffRing + b * C::kTile) >> 4);
 #pragma unroll
                 for (int j = 0; j < kTN / 16; ++j)
                     umma_bf16_ts(tmem + C::kColO + half * D, tmem + C::kColS + half * 128 + 8 * j,
-                                 sdesc_sw128(vt + j * 2048, 16384, 1024), kIdO, !(fresh && j == 0));
+                                 vt + ((j * 2048) >> 4), kIdO, !(fresh && j == 0));
             };
-            uint32_t item = 0, kp[2] = {0, 0};
+            uint32_t item = 0, kp = 0, kp1 = 0;
             bool ok = true;
             int left = count;
             for (int seg = 0; left > 0 && ok; ++seg) {
-                const int steps = min(left, u.steps - u.step);
-                left -= steps;
-                const int halves = unit_rows(p, u) > 128 ? 2 : 1;
                 ok = wait(B::kFull + item % C::kRing, item / C::kRing) && wait(B::kQFull, seg);
                 if (!ok) break;
                 tc_fence_after();
+                const int steps = s_piece[seg & 7].x, halves = s_piece[seg & 7].y;
+                left -= steps;
+#pragma unroll 1
                 for (int h = 0; h < halves; ++h) {
                     score(h, item % C::kRing);
                     umma_commit(&bars[B::kS + h]);
                 }
                 umma_commit(&bars[B::kEmpty + item % C::kRing]);
                 if (steps == 1) umma_commit(&bars[B::kQEmpty]);
+#pragma unroll 1
                 for (int s = 0; s < steps && ok; ++s, item += 2) {
                     const uint32_t iv = item + 1, ik = item + 2;
                     const bool more = s + 1 < steps;
                     ok = wait(B::kFull + iv % C::kRing, iv / C::kRing);
                     if (ok && more) ok = wait(B::kFull + ik % C::kRing, ik / C::kRing);
+#pragma unroll 1
                     for (int h = 0; h < halves && ok; ++h) {
-                        ok = wait(B::kP + h, kp[h]++);
+                        ok = wait(B::kP + h, h ? kp1++ : kp++);
                         if (!ok) break;
                         tc_fence_after();
                         gather(h, iv % C::kRing, s == 0);
@@ -749,7 +731,80 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         }
                     }
                 }
-                if (left) next_unit<kTM, kTN>(p, u);
+            }
+        }
+        __syncwarp();
+        if (warp == 13) {
+            // ----------------------------------------------------- loads
+            Unit u = s_unit;
+            const int box = a.box, boxes = kTN / box;
+            // the page of this lane's box of the step that is loaded next; a
+            // page past the cache reads as zeros
+            int page = 0, slot = 0;
+            bool there = false;
+            auto look_up = [&]() {
+                const int pos = u.lo + u.step * kTN + lane * box;
+                there = lane < boxes && pos < u.hi;
+                page = p.c.n_pages;
+                slot = 0;
+                if (there) {
+                    const int pi = pos / p.c.page_size;
+                    slot = pos - pi * p.c.page_size;
+                    const int x = page_of(p.c, u.n, pi, p.r.status);
+                    there = x >= 0;
+                    if (there) page = x;
+                }
+            };
+            uint32_t item = 0;
+            bool ok = true;
+            look_up();
+            for (int it = 0; it < count && ok; ++it) {
+                const int pg = page, sl = slot, head = u.head;
+                const bool here = there;
+                const bool masked = FMT == 0 && step_masked(p, u, u.lo + u.step * kTN);
+                if (it + 1 < count) {
+                    if (++u.step == u.steps) next_unit<kTM, kTN>(p, u);
+                    look_up();
+                }
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++item) {
+                    const CUtensorMap *map = kv ? &a.tv : &a.tk;
+                    int bar;
+                    uint32_t dst, bytes;
+                    if constexpr (FMT == 0) {
+                        const int b = item % C::kRing;
+                        ok = __all_sync(0xffffffffu, wait(B::kEmpty + b, item / C::kRing + 1));
+                        bar = kv && masked ? B::kLand + b : B::kFull + b;
+                        dst = C::kOffRing + b * C::kTile;
+                        bytes = C::kTile;
+                    } else {
+                        const int w = item % C::kRaw;
+                        ok = __all_sync(0xffffffffu, wait(B::kTaken + w, item / C::kRaw + 1));
+                        bar = B::kLand + w;
+                        dst = C::kOffRaw + w * C::kRawSize;
+                        bytes = C::kRawTile;
+                        if (kv == 0) bytes += __popc(__ballot_sync(0xffffffffu, here)) * box * 8;
+                    }
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars[bar], bytes);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        if constexpr (FMT == 0) {
+#pragma unroll
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_4d(sb + dst + c * 16384 + lane * box * 128, map, &bars[bar],
+                                            c * 64, sl, head, pg);
+                        } else {
+                            tma_load_4d(sb + dst + lane * box * D, map, &bars[bar], 0, sl, head, pg);
+                            if (kv == 0 && here) {
+                                const int64_t so = scale_at(p.c, pg, sl, head);
+                                uint8_t *sc = sm + dst + C::kRawTile + lane * box * 4;
+                                bulk_load(sc, p.c.ks + so, box * 4, &bars[bar]);
+                                bulk_load(sc + kTN * 4, p.c.vs + so, box * 4, &bars[bar]);
+                            }
+                        }
+                    }
+                }
             }
         }
         if (warp == 12 && lane == 0) {  // nothing is in flight when the memory goes back
@@ -767,16 +822,40 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     }
 }
 
+// Pages of a cache as a tensor of boxes of `box` slots by 128 bytes (16 bits,
+// 64 columns, swizzled) or by a row (8 bits).
+bool page_map(CUtensorMap *map, const AttnProblem &p, const void *base, const int64_t (&st)[3],
+              int D, int box) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const bool raw = cache_quantised(p.c.dtype);
+    const uint64_t es = raw ? 1 : 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.c.page_size, (cuuint64_t)p.c.H,
+                                (cuuint64_t)p.c.n_pages};
+    const cuuint64_t strides[3] = {st[1] * es, st[2] * es, st[0] * es};
+    const cuuint32_t bx[4] = {raw ? (cuuint32_t)D : 64u, (cuuint32_t)box, 1, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const auto type = raw                       ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                      : p.dtype == GDR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return enc(map, type, 4, const_cast<void *>(base), dims, strides, bx, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               raw ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int FMT, int D>
 cudaError_t launch_tiles(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
-    using C = TilesCfg<D>;
-    TilesArgs a{p, ws, (p.r.N + kSplitSlots - 1) / kSplitSlots, 1};
+    using C = TilesCfg<FMT, D>;
+    TilesArgs a{p, ws, (p.r.N + kSplitSlots - 1) / kSplitSlots, 1, p.align};
+    if (!page_map(&a.tk, p, p.c.k, p.c.kst, D, a.box) || !page_map(&a.tv, p, p.c.v, p.c.vst, D, a.box))
+        return cudaErrorInvalidValue;
     auto k = k_attn_tiles<T, FMT, D>;
     cudaFuncAttributes at;
     cudaError_t e = cudaFuncGetAttributes(&at, k);
     if (e != cudaSuccess) return e;
     // the split of the registers draws on what the launch holds
-    if (at.numRegs * 4 < 2 * kRegSoftmax + kRegLoad + kRegRest) return cudaErrorInvalidConfiguration;
+    if (at.numRegs * 4 < 2 * kRegSoftmax + kRegHelp + kRegRest) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
     if (e != cudaSuccess) return e;
     k<<<ctas, kTThreads, C::kBytes, st>>>(a);
@@ -804,6 +883,12 @@ SplitPlan attn_tiles_plan(const AttnProblem &p) {
     s.workers = s.ctas;
     s.rows = kTM;
     return s;
+}
+
+// Boxes of 8 slots and more, and scales on 16-byte boundaries.
+bool attn_tiles_supported(const AttnProblem &p) {
+    return attn_rows_supported(p) && p.c.page_size % 8 == 0 &&
+           ((reinterpret_cast<uintptr_t>(p.c.ks) | reinterpret_cast<uintptr_t>(p.c.vs)) & 15u) == 0;
 }
 
 cudaError_t attn_tiles(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,

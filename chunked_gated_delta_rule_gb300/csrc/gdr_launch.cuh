@@ -208,7 +208,9 @@ bool attn_rows_supported(const AttnProblem &p);
 SplitPlan attn_rows_plan(const AttnProblem &p);
 cudaError_t attn_rows(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
                       cudaStream_t st);
-// Many rows: tiles of 256 on tcgen05, for the same types, widths and strides.
+// Many rows: tiles of 256 on tcgen05, for the same types, widths and strides
+// and pages of a multiple of 8 slots.
+bool attn_tiles_supported(const AttnProblem &p);
 SplitPlan attn_tiles_plan(const AttnProblem &p);
 cudaError_t attn_tiles(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
                        cudaStream_t st);
