@@ -26,18 +26,17 @@ struct AttnProblem {
     float *lse;           // [tokens, Hq] or nullptr
     TokStride sq, so;
     int Hq, G, K, V, dtype, causal;
-    int64_t window;       // 0: none
+    int window;           // 0: none
     float scale;
     int grid_limit;
     int align;            // tiles' first positions are multiples of it (a power of two)
 };
 
-// Positions [lo, hi) that the token at position pos of a sequence of kv
-// cached tokens sees.
-__device__ __forceinline__ void visible(const AttnProblem &p, int64_t kv, int64_t pos,
-                                        int64_t &lo, int64_t &hi) {
-    hi = p.causal ? (pos + 1 < kv ? pos + 1 : kv) : kv;
-    lo = p.window && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
+// Positions [lo, hi) that the token at position pos (below 0: before the
+// cache) of a sequence of kv cached tokens sees.  Positions fit 31 bits.
+__device__ __forceinline__ void visible(const AttnProblem &p, int kv, int pos, int &lo, int &hi) {
+    hi = p.causal && pos + 1 < kv ? pos + 1 : kv;
+    lo = p.window && pos >= p.window ? pos - p.window + 1 : 0;
     if (hi < lo) hi = lo;
 }
 

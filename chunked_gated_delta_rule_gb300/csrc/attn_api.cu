@@ -95,7 +95,7 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t split_bytes(const SplitPlan &s, int64_t V) {
     const size_t rows = (size_t)s.workers * 2 * s.rows;
     return align256(rows * V * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
-           align256((size_t)s.workers * sizeof(int4));
+           align256((size_t)s.workers * 2 * sizeof(int4));
 }
 
 SplitScratch carve_split(void *base, const SplitPlan &s, int64_t V) {
@@ -158,7 +158,7 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
     p.K = (int)dims->K; p.V = (int)dims->V;
     p.dtype = dims->dtype;
     p.causal = causal != 0;
-    p.window = window;
+    p.window = window < INT32_MAX ? (int)window : INT32_MAX;
     p.scale = opt && opt->scale > 0.f ? opt->scale : 1.0f / std::sqrt((float)dims->K);
     p.grid_limit = opt ? opt->grid_limit : 0;
     LaunchRecorder rec;

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
     const int64_t worker = (int64_t)blockIdx.x * kRowsWarps + warp;
     int64_t nw = (int64_t)gridDim.x * kRowsWarps;
     if (nw * a.min_steps > total) nw = (total + a.min_steps - 1) / a.min_steps;
-    if (lane == 0) a.ws.rec[worker] = make_int4(0, 0, 0, 0);
+    if (lane == 0) a.ws.rec[worker * 2] = make_int4(0, 0, 0, 0);
     if (worker >= nw) return;
     const int64_t begin = share_begin(total, worker, nw);
     const int count = (int)(share_begin(total, worker + 1, nw) - begin);
@@ -259,13 +259,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
             f.first = u.step == 0;
             f.steps_left = u.steps - 1 - u.step;
             f.last = f.steps_left == 0;
-            // some row of the tile sees a part of the step only
-            const int r0 = u.tile * kRowsM, i0 = r0 / p.G;
-            const int i1 = min(u.len - 1, (r0 + kRowsM - 1) / p.G);
-            int64_t l0, h0, l1, h1;
-            visible(p, u.kv, (int64_t)u.kv - u.len + i0, l0, h0);
-            visible(p, u.kv, (int64_t)u.kv - u.len + i1, l1, h1);
-            f.mask = f.base + C::kBN > h0 || f.base < l1;
+            f.mask = step_masked<C::kBN>(u, f.base);
             info[s] = f;
         }
         if (++u.step == u.steps) next_unit<kRowsM, C::kBN>(p, u);
@@ -309,20 +303,15 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
             const int ra = f.tile * kRowsM + qr, ia = ra / p.G, ib = (ra + 8) / p.G;
             several = ia != f.tile * kRowsM / p.G || rows > p.G;
             several = __any_sync(0xffffffffu, several);
-            int64_t x, y;
             lo0 = hi0 = lo1 = hi1 = 0;
             const T *qa = nullptr, *qb = nullptr;
             if (qr < rows) {
-                visible(p, f.kv, (int64_t)f.kv - f.len + ia, x, y);
-                lo0 = (int)x;
-                hi0 = (int)y;
+                visible(p, f.kv, f.kv - f.len + ia, lo0, hi0);
                 qa = reinterpret_cast<const T *>(p.q) +
                      tok_at(p.sq, f.t0 + ia, f.head * p.G + ra - ia * p.G);
             }
             if (qr + 8 < rows) {
-                visible(p, f.kv, (int64_t)f.kv - f.len + ib, x, y);
-                lo1 = (int)x;
-                hi1 = (int)y;
+                visible(p, f.kv, f.kv - f.len + ib, lo1, hi1);
                 qb = reinterpret_cast<const T *>(p.q) +
                      tok_at(p.sq, f.t0 + ib, f.head * p.G + ra + 8 - ib * p.G);
             }
@@ -675,10 +664,11 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
                     }
                 }
             }
-            if (begun && !f.last && lane == 0)
-                a.ws.rec[worker] = make_int4(f.n, f.tile, f.head,
-                                             pieces_from(total, worker, nw,
-                                                         begin + it + 1 + f.steps_left));
+            if (begun && !f.last && lane == 0) {
+                a.ws.rec[worker * 2] = make_int4(
+                    pieces_from(total, worker, nw, begin + it + 1 + f.steps_left), f.t0, f.len, f.tile);
+                a.ws.rec[worker * 2 + 1].x = f.head;
+            }
         }
         __syncwarp();  // the stage is free
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
@@ -687,16 +677,17 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
 }
 
 // ---- joining split units --------------------------------------------------
-// CTA w joins the unit that worker w begins and others go on with:
+// The unit that worker w begins and others go on with, row by row:
 //   m = max_j m_j,  o = sum_j 2^(m_j - m) O_j / sum_j 2^(m_j - m) l_j
 // over its pieces j, in an order that only their number fixes: up to kW
-// pieces by one warp a row, more by all warps, each taking every kW-th.
+// pieces by one warp, R rows at a time; more by all warps of the CTA, each
+// taking every kW-th piece of one row.
 constexpr int kJoinThreads = 256;
 
 template <int V>
 struct Joined {
     float m = -INFINITY, l = 0.f, o[V] = {};
-    __device__ __forceinline__ void add(float mj, float lj, const float *oj) {
+    __device__ __forceinline__ void add(float mj, float lj, const float (&oj)[V]) {
         const float n = fmaxf(m, mj), nu = n == -INFINITY ? 0.f : n;
         const float c = exp2f(m - nu), cj = exp2f(mj - nu);
         m = n;
@@ -706,53 +697,91 @@ struct Joined {
     }
 };
 
+// A lane's V = D / 32 consecutive columns.
+template <int V>
+__device__ __forceinline__ void load_cols(float (&o)[V], const float *p) {
+    if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2 *>(p);
+        o[0] = x.x; o[1] = x.y;
+    }
+}
+
 template <typename T, int M, int D>
 __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnProblem p,
                                                             SplitScratch ws) {
-    constexpr int kW = kJoinThreads / 32, kV = D / 32;
-    __shared__ float s_o[kW][D], s_ml[kW][2];
+    constexpr int kW = kJoinThreads / 32, kV = D / 32, kR = M > 16 ? 4 : 1;
+    __shared__ __align__(16) float s_o[kW][D];
+    __shared__ float s_ml[kW][2];
     pdl_wait();
     const int64_t w = blockIdx.x;
-    const int4 rec = ws.rec[w];
-    if (rec.w == 0) return;
-    int t0, len, kv;
-    load_seq(p, rec.x, t0, len, kv);
-    const int rows = min(M, len * p.G - rec.y * M);
+    const int4 rec = ws.rec[w * 2];
+    const int pieces = rec.x;
+    if (pieces == 0) return;
+    const int head = ws.rec[w * 2 + 1].x, t0 = rec.y, tile = rec.w;
+    const int rows = min(M, rec.z * p.G - tile * M);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool few = rec.w <= kW;
-    for (int r = few ? blockIdx.y * kW + warp : blockIdx.y; r < rows;
-         r += few ? gridDim.y * kW : gridDim.y) {
-        Joined<kV> a;
-#pragma unroll 4
-        for (int j = few ? 0 : warp; j < rec.w; j += few ? 1 : kW) {
-            const int64_t at = ((w + j) * 2 + (j == 0 ? 1 : 0)) * M + r;
-            float oj[kV];
-#pragma unroll
-            for (int i = 0; i < kV; ++i) oj[i] = ws.o[at * D + lane * kV + i];
-            a.add(ws.ml[at * 2], ws.ml[at * 2 + 1], oj);
-        }
-        if (!few) {
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kV; ++i) s_o[warp][lane * kV + i] = a.o[i];
-            if (lane == 0) {
-                s_ml[warp][0] = a.m;
-                s_ml[warp][1] = a.l;
-            }
-            __syncthreads();
-            if (warp) continue;
-            a = Joined<kV>();
-            for (int j = 0; j < kW; ++j) a.add(s_ml[j][0], s_ml[j][1], &s_o[j][lane * kV]);
-        }
+    auto slot = [&](int j, int r) { return ((w + j) * 2 + (j == 0 ? 1 : 0)) * M + r; };
+    auto write = [&](const Joined<kV> &a, int r) {
         const bool empty = a.l == 0.f;
         const float inv = empty ? 0.f : 1.f / a.l;
-        const int row = rec.y * M + r, i = row / p.G, hq = rec.z * p.G + row - i * p.G;
+        const int row = tile * M + r, i = row / p.G, hq = head * p.G + row - i * p.G;
         T *o = reinterpret_cast<T *>(p.o) + tok_at(p.so, t0 + i, hq) + lane * kV;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) o[e] = (T)(a.o[e] * inv);
+        for (int e = 0; e < kV; e += 2)
+            *reinterpret_cast<uint32_t *>(o + e) = pack2<T>(a.o[e] * inv, a.o[e + 1] * inv);
         if (p.lse && lane == 0)
             p.lse[(int64_t)(t0 + i) * p.Hq + hq] =
                 empty ? -INFINITY : ((a.m == -INFINITY ? 0.f : a.m) + log2f(a.l)) * kLn2;
+    };
+    if (pieces <= kW) {
+        for (int r = (blockIdx.y * kW + warp) * kR; r < rows; r += gridDim.y * kW * kR) {
+            Joined<kV> a[kR];
+            for (int j = 0; j < pieces; ++j) {
+                float oj[kR][kV], ml[kR][2];
+#pragma unroll
+                for (int e = 0; e < kR; ++e) {
+                    const int64_t at = slot(j, min(r + e, rows - 1));
+                    load_cols<kV>(oj[e], ws.o + at * D + lane * kV);
+                    ml[e][0] = ws.ml[at * 2];
+                    ml[e][1] = ws.ml[at * 2 + 1];
+                }
+#pragma unroll
+                for (int e = 0; e < kR; ++e) a[e].add(ml[e][0], ml[e][1], oj[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < kR; ++e)
+                if (r + e < rows) write(a[e], r + e);
+        }
+        return;
+    }
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        Joined<kV> a;
+#pragma unroll 4
+        for (int j = warp; j < pieces; j += kW) {
+            const int64_t at = slot(j, r);
+            float oj[kV];
+            load_cols<kV>(oj, ws.o + at * D + lane * kV);
+            a.add(ws.ml[at * 2], ws.ml[at * 2 + 1], oj);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kV; ++i) s_o[warp][lane * kV + i] = a.o[i];
+        if (lane == 0) {
+            s_ml[warp][0] = a.m;
+            s_ml[warp][1] = a.l;
+        }
+        __syncthreads();
+        if (warp) continue;
+        a = Joined<kV>();
+        for (int j = 0; j < kW; ++j) {
+            float oj[kV];
+            load_cols<kV>(oj, &s_o[j][lane * kV]);
+            a.add(s_ml[j][0], s_ml[j][1], oj);
+        }
+        write(a, r);
     }
 }
 
@@ -781,9 +810,11 @@ cudaError_t launch_dim(const AttnProblem &p, const SplitScratch &ws, int ctas, c
 
 template <typename T, int M>
 cudaError_t join_dim(const AttnProblem &p, const SplitScratch &ws, int workers, cudaStream_t st) {
-    // few pieces a unit: eight rows to a CTA; many: a CTA for each row
-    const int rows = workers > 8 * p.r.N * p.c.H ? (M == 16 && p.G < M ? p.G : M) : (M + 7) / 8;
-    const dim3 g((unsigned)workers, (unsigned)(M == 16 && workers <= 8 * p.r.N * p.c.H ? 1 : rows));
+    // many pieces a unit: a CTA for each row of it; few: 8 rows (of 16-row
+    // tiles) or 32 share one
+    const bool many = workers > 8 * p.r.N * p.c.H;
+    const int y = M == 16 ? (many ? (p.G < M ? p.G : M) : 1) : (many ? 64 : M / 32);
+    const dim3 g((unsigned)workers, (unsigned)y);
     if (p.V == 64) return launch_pdl(k_attn_join<T, M, 64>, g, dim3(kJoinThreads), 0, st, p, ws);
     return launch_pdl(k_attn_join<T, M, 128>, g, dim3(kJoinThreads), 0, st, p, ws);
 }
@@ -802,6 +833,7 @@ SplitPlan attn_rows_plan(const AttnProblem &p) {
 bool attn_rows_supported(const AttnProblem &p) {
     const int ec = cache_quantised(p.c.dtype) ? 1 : 2;
     return (p.dtype == GDR_BF16 || p.dtype == GDR_F16) && p.K == p.V && (p.K == 64 || p.K == 128) &&
+           p.r.T * p.G < INT32_MAX - 512 &&  // rows are counted in 32 bits
            rows_aligned16(p.q, p.sq, 2) && rows_aligned16(p.o, p.so, 2) &&
            pages_aligned16(p.c.k, p.c.kst, ec) && pages_aligned16(p.c.v, p.c.vst, ec);
 }

@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(32 * kAWarps) k_attn_simt(AttnProblem p) {
     int64_t t0, len;
     seq_span(p.r, n, t0, len);
     const int64_t kv = cached_len(p.c, n, p.r.status);
-    int64_t lo = 0, hi = 0;
-    if (t >= t0 && t < t0 + len) visible(p, kv, kv - len + (t - t0), lo, hi);
+    int lo = 0, hi = 0;
+    if (t >= t0 && t < t0 + len) visible(p, (int)kv, (int)(kv - len + (t - t0)), lo, hi);
 
     const Tio *q = reinterpret_cast<const Tio *>(p.q) + tok_at(p.sq, t, h);
     for (int d = lane; d < p.K; d += 32) sq[warp][d] = (float)q[d] * p.scale;
@@ -43,13 +43,13 @@ __global__ void __launch_bounds__(32 * kAWarps) k_attn_simt(AttnProblem p) {
 
     float m = -INFINITY, l = 0.f;
     float acc[kAMaxD / 32] = {};
-    for (int64_t j0 = lo; j0 < hi; j0 += 32) {
-        const int64_t j = j0 + lane;
+    for (int j0 = lo; j0 < hi; j0 += 32) {
+        const int j = j0 + lane;
         int64_t ko = 0, vo = 0;
         float s = -INFINITY, vs = 1.f;
         bool live = j < hi;
         if (live) {
-            const int pi = (int)(j / p.c.page_size), slot = (int)(j - (int64_t)pi * p.c.page_size);
+            const int pi = j / p.c.page_size, slot = j - pi * p.c.page_size;
             const int page = page_of(p.c, n, pi, p.r.status);
             live = page >= 0;
             if (live) {

@@ -23,7 +23,9 @@ namespace gdr {
 struct SplitScratch {
     float *o;      // [workers][2][M][V] sums of e^{s - m} v
     float *ml;     // [workers][2][M][2] m (base 2) and sum of e^{s - m}
-    int4 *rec;     // [workers] sequence, tile, key head, pieces (0: none split)
+    // [workers][2] the unit that the worker begins and others go on with:
+    // {pieces (0: there is none), first token, new tokens, tile}, {key head}
+    int4 *rec;
 };
 
 constexpr int kSplitSlots = 256;  // groups of sequences whose steps are summed up
@@ -31,7 +33,8 @@ constexpr int kSplitSlots = 256;  // groups of sequences whose steps are summed 
 struct Unit {
     int n, tile, head;
     int step, steps;       // next step, steps of the unit
-    int lo, hi;            // positions that its rows see
+    int lo, hi;            // positions that some row of it sees
+    int in_lo, in_hi;      // positions that every row sees
     int t0, len, kv;       // the sequence: first token, new tokens, cached tokens
 };
 
@@ -46,34 +49,38 @@ __device__ __forceinline__ void load_seq(const AttnProblem &p, int64_t n, int &t
 
 template <int M>
 __device__ __forceinline__ int tiles_of(const AttnProblem &p, int len) {
-    return (int)(((int64_t)len * p.G + (M - 1)) / M);
+    return (len * p.G + (M - 1)) / M;  // the host sees to it that this fits
 }
 
-// Positions [lo, hi) that the rows of a tile see, lo down to a multiple of
-// p.align (a box of a page begins there), and the tile's steps.
+// Positions [u.lo, u.hi) that the rows of tile u.tile see, lo down to a
+// multiple of p.align (a box of a page begins there), and the tile's steps.
 template <int M, int BN>
-__device__ __forceinline__ int tile_steps(const AttnProblem &p, int len, int kv, int tile, int &lo,
-                                          int &hi) {
-    const int64_t r0 = (int64_t)tile * M;
-    const int64_t i0 = r0 / p.G;
-    int64_t i1 = (r0 + M - 1) / p.G;
-    if (i1 > len - 1) i1 = len - 1;
-    int64_t a, b, c, d;
-    visible(p, kv, (int64_t)kv - len + i0, a, b);
-    visible(p, kv, (int64_t)kv - len + i1, c, d);
-    hi = (int)(d > a ? d : a);
-    lo = (int)a & -p.align;
-    const int s = (hi - lo + BN - 1) / BN;
+__device__ __forceinline__ int tile_steps(const AttnProblem &p, Unit &u) {
+    const int r0 = u.tile * M, i0 = r0 / p.G;
+    const int i1 = min((r0 + M - 1) / p.G, u.len - 1);
+    int a, d;
+    visible(p, u.kv, u.kv - u.len + i0, a, u.in_hi);
+    visible(p, u.kv, u.kv - u.len + i1, u.in_lo, d);
+    u.hi = d > a ? d : a;
+    u.lo = a & -p.align;
+    const int s = (u.hi - u.lo + BN - 1) / BN;
     return s > 0 ? s : 1;
 }
+// Whether some row of the unit sees a part only of the BN positions at `base`.
+template <int BN>
+__device__ __forceinline__ bool step_masked(const Unit &u, int base) {
+    return base < u.in_lo || base + BN > u.in_hi;
+}
+template <int M>
+__device__ __forceinline__ int unit_rows(const AttnProblem &p, const Unit &u) {
+    return min(M, u.len * p.G - u.tile * M);
+}
 
 template <int M, int BN>
-__device__ __forceinline__ int64_t seq_steps(const AttnProblem &p, int len, int kv, int first,
-                                             int stride) {
-    int lo, hi;
+__device__ __forceinline__ int64_t seq_steps(const AttnProblem &p, Unit &u, int first, int stride) {
     int64_t s = 0;
-    const int tiles = tiles_of<M>(p, len);
-    for (int t = first; t < tiles; t += stride) s += tile_steps<M, BN>(p, len, kv, t, lo, hi);
+    const int tiles = tiles_of<M>(p, u.len);
+    for (u.tile = first; u.tile < tiles; u.tile += stride) s += tile_steps<M, BN>(p, u);
     return s * p.c.H;
 }
 
@@ -95,9 +102,9 @@ __device__ void split_prefix(const AttnProblem &p, int64_t per, int64_t *pre) {
         int64_t sum = 0;
         int many = 0;
         for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
-            int t0, len, kv;
-            load_seq(p, n, t0, len, kv);
-            if (tiles_of<M>(p, len) <= kFew) sum += seq_steps<M, BN>(p, len, kv, 0, 1);
+            Unit u;
+            load_seq(p, n, u.t0, u.len, u.kv);
+            if (tiles_of<M>(p, u.len) <= kFew) sum += seq_steps<M, BN>(p, u, 0, 1);
             else ++many;
         }
         pre[e + 1] = sum;
@@ -111,9 +118,9 @@ __device__ void split_prefix(const AttnProblem &p, int64_t per, int64_t *pre) {
             if (!s_many[e]) continue;
             int64_t sum = 0;
             for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
-                int t0, len, kv;
-                load_seq(p, n, t0, len, kv);
-                if (tiles_of<M>(p, len) > kFew) sum += seq_steps<M, BN>(p, len, kv, tid, NT);
+                Unit u;
+                load_seq(p, n, u.t0, u.len, u.kv);
+                if (tiles_of<M>(p, u.len) > kFew) sum += seq_steps<M, BN>(p, u, tid, NT);
             }
             atomicAdd(reinterpret_cast<unsigned long long *>(&pre[e + 1]), (unsigned long long)sum);
         }
@@ -155,8 +162,8 @@ __device__ Unit split_locate(const AttnProblem &p, int64_t per, const int64_t *p
         load_seq(p, n, u.t0, u.len, u.kv);
         const int tiles = tiles_of<M>(p, u.len);
         for (int t = 0; t < tiles; t += 32) {
-            int a = 0, b = 0;
-            const int s = t + lane < tiles ? tile_steps<M, BN>(p, u.len, u.kv, t + lane, a, b) : 0;
+            u.tile = t + lane;
+            const int s = t + lane < tiles ? tile_steps<M, BN>(p, u) : 0;
             int64_t x = (int64_t)s * p.c.H;
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
@@ -167,9 +174,7 @@ __device__ Unit split_locate(const AttnProblem &p, int64_t per, const int64_t *p
                 const int l = __ffs(m) - 1;
                 u.n = (int)n;
                 u.tile = t + l;
-                u.steps = __shfl_sync(0xffffffffu, s, l);
-                u.lo = __shfl_sync(0xffffffffu, a, l);
-                u.hi = __shfl_sync(0xffffffffu, b, l);
+                u.steps = tile_steps<M, BN>(p, u);
                 rem -= __shfl_sync(0xffffffffu, x, l) - (int64_t)u.steps * p.c.H;
                 u.head = (int)(rem / u.steps);
                 u.step = (int)(rem - (int64_t)u.head * u.steps);
@@ -193,7 +198,7 @@ __device__ __forceinline__ void next_unit(const AttnProblem &p, Unit &u) {
         if (++u.n >= p.r.N) return;
         load_seq(p, u.n, u.t0, u.len, u.kv);
     }
-    u.steps = tile_steps<M, BN>(p, u.len, u.kv, u.tile, u.lo, u.hi);
+    u.steps = tile_steps<M, BN>(p, u);
 }
 
 // First step of worker w of nw.

@@ -61,6 +61,9 @@ template <int FMT, int D>
 struct TilesCfg {
     static constexpr uint32_t kTile = kTN * D * 2;     // a 128-row tile of 16-bit values
     static constexpr int kRing = D == 64 ? 8 : FMT ? 3 : 4;  // tiles of keys and values
+    // tiles given back in pairs, a step's keys and the values before them
+    // (one commit a step instead of two); 0: one by one
+    static constexpr int kPairs = FMT ? 0 : kRing / 2;
     static constexpr int kRaw = FMT ? 3 : 0;                 // 8-bit tiles on their way
     static constexpr uint32_t kRawTile = kTN * D, kRawSize = kRawTile + 2 * kTN * 4;
     // steps whose scales are kept: a step's keys are widened once the products
@@ -206,6 +209,44 @@ __host__ __device__ constexpr uint32_t tiles_idesc(int N, int b_mn) {
            ((uint32_t)(128 >> 4) << 24);
 }
 
+// tcgen05 products and commits for a warp that stays together: every lane goes
+// through them and one issues (lead != 0).  The operands are then uniform, and
+// the compiler keeps them so; issued from a branch of one lane, each product
+// is a dozen instructions more, which beside eight busy warps take longer than
+// the product (a product of 64 cycles every 68 cycles, against 290).
+__device__ __forceinline__ uint32_t elect_lead() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+                 : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void lead_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t add, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void lead_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t add, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void lead_commit(uint64_t *bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -213,20 +254,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-
-// Whether some row of the tile sees a part of the step at `base` only.
-__device__ __forceinline__ bool step_masked(const AttnProblem &p, const Unit &u, int base) {
-    const int i0 = (int)((int64_t)u.tile * kTM / p.G);
-    const int i1 = (int)min((int64_t)u.len - 1, ((int64_t)u.tile * kTM + kTM - 1) / p.G);
-    int64_t l0, h0, l1, h1;
-    visible(p, u.kv, (int64_t)u.kv - u.len + i0, l0, h0);
-    visible(p, u.kv, (int64_t)u.kv - u.len + i1, l1, h1);
-    return base + kTN > h0 || base < l1;
-}
-
-__device__ __forceinline__ int unit_rows(const AttnProblem &p, const Unit &u) {
-    return (int)min((int64_t)kTM, (int64_t)u.len * p.G - (int64_t)u.tile * kTM);
 }
 
 template <typename T, int FMT, int D>
@@ -286,7 +313,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             s_share[1] = nw;
             s_share[2] = begin;
             s_share[3] = steps;
-            a.ws.rec[w] = make_int4(0, 0, 0, 0);
+            a.ws.rec[w * 2] = make_int4(0, 0, 0, 0);
         }
     }
     tc_fence_before();
@@ -309,25 +336,19 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, lane << 16
         const uint32_t ts = tmem + lanes + C::kColS + half * 128;
         const uint32_t to = tmem + lanes + C::kColO + half * D;
-        uint32_t k = 0;  // steps that this half has done
+        uint32_t k = 0, pieces = 0;  // steps and pieces that this half has done
         int left = count, seg = 0;
         for (int done = 0; left > 0; ++seg) {
             const int first = u.step, steps = min(left, u.steps - u.step);
             left -= steps;
-            const int rows = unit_rows(p, u);
+            const int rows = unit_rows<kTM>(p, u);
             const bool begun = first == 0, ends = first + steps == u.steps;
             if (half == 0 || rows > 128) {
                 const int r = half * 128 + row;
                 const bool live = r < rows;
-                const int64_t ur = (int64_t)u.tile * kTM + r;
-                const int tok = (int)(ur / p.G), hq = u.head * p.G + (int)(ur - (int64_t)tok * p.G);
+                const int ur = u.tile * kTM + r, tok = ur / p.G, hq = u.head * p.G + ur - tok * p.G;
                 int lo = 0, hi = 0;
-                if (live) {
-                    int64_t x, y;
-                    visible(p, u.kv, (int64_t)u.kv - u.len + tok, x, y);
-                    lo = (int)x;
-                    hi = (int)y;
-                }
+                if (live) visible(p, u.kv, u.kv - u.len + tok, lo, hi);
                 float m = -INFINITY, l = 0.f;
                 float f = p.scale * kTLog2e;
                 bool ok = true;
@@ -389,10 +410,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         const float c = n == -INFINITY ? 1.f : ex2(m - n);
                         m = n;
                         l *= c;
-                        if (s > 0) {  // O holds the steps before
-                            ok = __all_sync(0xffffffffu, wait(B::kO + half, k - 1));
-                            if (!ok) break;
-                            tc_fence_after();
+                        if (s > 0) {  // O holds the steps before: they are done, as this S is
 #pragma unroll 1
                             for (int q = 0; q < D / 16; ++q) {
                                 uint32_t o[16];
@@ -441,7 +459,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 }
                 if (!ok) break;
                 // ------------------------------------------- the piece ends
-                ok = __all_sync(0xffffffffu, wait(B::kO + half, k - 1));
+                ok = __all_sync(0xffffffffu, wait(B::kO + half, pieces++));
                 if (!ok) break;
                 tc_fence_after();
                 if (FMT == 0 && s_poison[seg & 7] == seg + 1) {
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         reg_fence(o);
                         for (int s = first; s < first + steps; ++s) {
                             const int base = u.lo + s * kTN;
-                            if (!step_masked(p, u, base)) continue;
+                            if (!step_masked<kTN>(u, base)) continue;
                             for (int j = max(base, lo); j < min(base + kTN, hi); ++j) {
                                 const int page = page_of(p.c, u.n, j / p.c.page_size, p.r.status);
                                 if (page < 0) continue;
@@ -510,10 +528,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 }
             }
             done += steps;
-            if (begun && !ends && tid == 0)
-                a.ws.rec[worker] = make_int4(u.n, u.tile, u.head,
-                                             pieces_from(s_share[0], worker, s_share[1],
-                                                         s_share[2] + done + (u.steps - first - steps)));
+            if (begun && !ends && tid == 0) {
+                const int pieces = pieces_from(s_share[0], worker, s_share[1],
+                                               s_share[2] + done + (u.steps - first - steps));
+                a.ws.rec[worker * 2] = make_int4(pieces, u.t0, u.len, u.tile);
+                a.ws.rec[worker * 2 + 1].x = u.head;
+            }
             if (left) next_unit<kTM, kTN>(p, u);
         }
     } else if (warp < 12) {
@@ -527,15 +547,14 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
         auto queries = [&]() {
             ok = __all_sync(0xffffffffu, wait(B::kQEmpty, (uint32_t)seg + 1));
             if (!ok) return;
-            const int rows = unit_rows(p, u);
+            const int rows = unit_rows<kTM>(p, u);
             constexpr int kQC = D / 8, kQP = 128 / kQC;  // chunks a row, rows a pass
             const int qc = t % kQC, halves = rows > 128 ? 2 : 1;
             float *qf = reinterpret_cast<float *>(sm + C::kOffQf) + (seg & 1) * kTM;
             constexpr bool kConvert = FMT != 0 && std::is_same<T, __nv_bfloat16>::value;
 #pragma unroll 8
             for (int r = t / kQC; r < 128 * halves; r += kQP) {
-                const int64_t ur = (int64_t)u.tile * kTM + r;
-                const int tok = (int)(ur / p.G), hq = u.head * p.G + (int)(ur - (int64_t)tok * p.G);
+                const int ur = u.tile * kTM + r, tok = ur / p.G, hq = u.head * p.G + ur - tok * p.G;
                 const bool live = r < rows;
                 const T *src = reinterpret_cast<const T *>(p.q) +
                                (live ? tok_at(p.sq, u.t0 + tok, hq) + qc * 8 : 0);
@@ -578,14 +597,14 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             if (it == 0 || u.step == 0) {
                 if (t == 0)
                     s_piece[seg & 7] = make_int2(min(count - it, u.steps - u.step),
-                                                 unit_rows(p, u) > 128 ? 2 : 1);
+                                                 unit_rows<kTM>(p, u) > 128 ? 2 : 1);
                 queries();
             }
             const int base = u.lo + u.step * kTN, left = u.hi - base;  // positions of the step
             if constexpr (FMT == 0) {
                 const int b = (item + 1) % C::kRing;
                 item += 2;
-                if (ok && step_masked(p, u, base)) {
+                if (ok && step_masked<kTN>(u, base)) {
                     ok = __all_sync(0xffffffffu, wait(B::kLand + b, landed >> b));
                     landed ^= 1u << b;
                     if (ok) {
@@ -669,67 +688,81 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
         }
     } else {
         regs_down<kRegRest>();
-        if (warp == 12 && lane == 0) {
+        if (warp == 12) {
             // -------------------------------------------------- products
+            // loops and conditions go by votes, so that they are uniform
             constexpr uint32_t kIdS = tiles_idesc<TP>(128, 0), kIdO = tiles_idesc<TP>(D, 1);
+            const uint32_t lead = elect_lead();
+            auto all_wait = [&](int b, uint32_t parity) {
+                return (bool)__all_sync(0xffffffffu, wait(b, parity));
+            };
             // descriptors as a base plus a constant for each product: the
             // address is their low 14 bits, in units of 16 bytes
             const uint64_t dk0 = sdesc_sw128(sb, 16, 1024), dv0 = sdesc_sw128(sb, 16384, 1024);
-            auto score = [&](int half, int b) {
+            auto score = [&](int half, uint32_t b) {
                 const uint64_t q = dk0 + half * (C::kTile >> 4);
                 const uint64_t kt = dk0 + ((C::kOffRing + b * C::kTile) >> 4);
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
                     const uint64_t o = ((d >> 2) * 16384 + (d & 3) * 32) >> 4;
-                    umma_bf16(tmem + C::kColS + half * 128, q + o, kt + o, kIdS, d > 0);
+                    lead_mma(tmem + C::kColS + half * 128, q + o, kt + o, kIdS, d > 0, lead);
                 }
+                lead_commit(&bars[B::kS + half], lead);
             };
-            auto gather = [&](int half, int b, bool fresh) {
+            auto gather = [&](int half, uint32_t b, uint32_t add) {
                 const uint64_t vt = dv0 + ((C::kOffRing + b * C::kTile) >> 4);
 #pragma unroll
                 for (int j = 0; j < kTN / 16; ++j)
-                    umma_bf16_ts(tmem + C::kColO + half * D, tmem + C::kColS + half * 128 + 8 * j,
-                                 vt + ((j * 2048) >> 4), kIdO, !(fresh && j == 0));
+                    lead_mma_ts(tmem + C::kColO + half * D, tmem + C::kColS + half * 128 + 8 * j,
+                                vt + ((j * 2048) >> 4), kIdO, j ? 1u : add, lead);
             };
-            uint32_t item = 0, kp = 0, kp1 = 0;
-            bool ok = true;
+            // the keys of item 2 k, and with them the values before, are done
+            auto release_k = [&](uint32_t i) {
+                if constexpr (C::kPairs > 0) lead_commit(&bars[B::kEmpty + (i >> 1) % C::kPairs], lead);
+                else lead_commit(&bars[B::kEmpty + i % C::kRing], lead);
+            };
+            uint32_t item = 0, kp0 = 0, kp1 = 0, seg = 0;
             int left = count;
-            for (int seg = 0; left > 0 && ok; ++seg) {
-                ok = wait(B::kFull + item % C::kRing, item / C::kRing) && wait(B::kQFull, seg);
+            bool ok = true;
+            while (ok && __any_sync(0xffffffffu, left > 0)) {
+                ok = all_wait(B::kFull + item % C::kRing, item / C::kRing) && all_wait(B::kQFull, seg);
                 if (!ok) break;
                 tc_fence_after();
-                const int steps = s_piece[seg & 7].x, halves = s_piece[seg & 7].y;
+                const int steps = s_piece[seg & 7].x;
+                const bool two = __any_sync(0xffffffffu, s_piece[seg & 7].y == 2);
+                ++seg;
                 left -= steps;
-#pragma unroll 1
-                for (int h = 0; h < halves; ++h) {
-                    score(h, item % C::kRing);
-                    umma_commit(&bars[B::kS + h]);
-                }
-                umma_commit(&bars[B::kEmpty + item % C::kRing]);
-                if (steps == 1) umma_commit(&bars[B::kQEmpty]);
-#pragma unroll 1
-                for (int s = 0; s < steps && ok; ++s, item += 2) {
-                    const uint32_t iv = item + 1, ik = item + 2;
-                    const bool more = s + 1 < steps;
-                    ok = wait(B::kFull + iv % C::kRing, iv / C::kRing);
-                    if (ok && more) ok = wait(B::kFull + ik % C::kRing, ik / C::kRing);
-#pragma unroll 1
-                    for (int h = 0; h < halves && ok; ++h) {
-                        ok = wait(B::kP + h, h ? kp1++ : kp++);
+                score(0, item % C::kRing);
+                if (two) score(1, item % C::kRing);
+                release_k(item);
+                uint32_t add = 0;
+                for (int s = 1;; ++s) {
+                    const bool more = __any_sync(0xffffffffu, s < steps);
+                    if (!more) lead_commit(&bars[B::kQEmpty], lead);
+                    const uint32_t iv = (item + 1) % C::kRing, ik = (item + 2) % C::kRing;
+                    ok = all_wait(B::kFull + iv, (item + 1) / C::kRing);
+                    if (ok && more) ok = all_wait(B::kFull + ik, (item + 2) / C::kRing);
+                    ok = ok && all_wait(B::kP, kp0++);
+                    if (!ok) break;
+                    tc_fence_after();
+                    gather(0, iv, add);
+                    if (more) score(0, ik);
+                    else lead_commit(&bars[B::kO], lead);
+                    if (two) {
+                        ok = all_wait(B::kP + 1, kp1++);
                         if (!ok) break;
                         tc_fence_after();
-                        gather(h, iv % C::kRing, s == 0);
-                        umma_commit(&bars[B::kO + h]);
-                        if (h + 1 == halves) umma_commit(&bars[B::kEmpty + iv % C::kRing]);
-                        if (more) {
-                            score(h, ik % C::kRing);
-                            umma_commit(&bars[B::kS + h]);
-                            if (h + 1 == halves) {
-                                umma_commit(&bars[B::kEmpty + ik % C::kRing]);
-                                if (s + 2 == steps) umma_commit(&bars[B::kQEmpty]);
-                            }
-                        }
+                        gather(1, iv, add);
+                        if (C::kPairs == 0) lead_commit(&bars[B::kEmpty + iv], lead);
+                        if (more) score(1, ik);
+                        else lead_commit(&bars[B::kO + 1], lead);
+                    } else if (C::kPairs == 0) {
+                        lead_commit(&bars[B::kEmpty + iv], lead);
                     }
+                    if (more) release_k(item + 2);
+                    item += 2;
+                    add = 1;
+                    if (!more) break;
                 }
             }
         }
@@ -738,34 +771,28 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             // ----------------------------------------------------- loads
             Unit u = s_unit;
             const int box = a.box, boxes = kTN / box;
-            // the page of this lane's box of the step that is loaded next; a
-            // page past the cache reads as zeros
-            int page = 0, slot = 0;
-            bool there = false;
+            // the page-table entry and slot of this lane's box of the step that
+            // is loaded next, asked for a step ahead
+            int entry = -1, slot = 0;
+            bool asked = false;
             auto look_up = [&]() {
                 const int pos = u.lo + u.step * kTN + lane * box;
-                there = lane < boxes && pos < u.hi;
-                page = p.c.n_pages;
-                slot = 0;
-                if (there) {
+                asked = lane < boxes && pos < u.hi;
+                if (asked) {
                     const int pi = pos / p.c.page_size;
                     slot = pos - pi * p.c.page_size;
-                    const int x = page_of(p.c, u.n, pi, p.r.status);
-                    there = x >= 0;
-                    if (there) page = x;
+                    entry = p.c.table[u.n * p.c.max_pages + pi];
                 }
             };
             uint32_t item = 0;
             bool ok = true;
             look_up();
             for (int it = 0; it < count && ok; ++it) {
-                const int pg = page, sl = slot, head = u.head;
-                const bool here = there;
-                const bool masked = FMT == 0 && step_masked(p, u, u.lo + u.step * kTN);
-                if (it + 1 < count) {
-                    if (++u.step == u.steps) next_unit<kTM, kTN>(p, u);
-                    look_up();
-                }
+                // a page past the cache reads as zeros
+                const bool here = asked && (unsigned)entry < (unsigned)p.c.n_pages;
+                if (asked && !here) report(p.r.status, GDR_ERR_INDEX);
+                const int pg = here ? entry : p.c.n_pages, sl = here ? slot : 0, head = u.head;
+                const bool masked = FMT == 0 && step_masked<kTN>(u, u.lo + u.step * kTN);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++item) {
                     const CUtensorMap *map = kv ? &a.tv : &a.tk;
@@ -773,7 +800,10 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     uint32_t dst, bytes;
                     if constexpr (FMT == 0) {
                         const int b = item % C::kRing;
-                        ok = __all_sync(0xffffffffu, wait(B::kEmpty + b, item / C::kRing + 1));
+                        // values s and keys s + 1 go into the tiles of values
+                        // s - kPairs and keys s + 1 - kPairs
+                        const int e = (int)((item + 1) >> 1) - C::kPairs;
+                        if (e >= 0) ok = __all_sync(0xffffffffu, wait(B::kEmpty + e % C::kPairs, e / C::kPairs));
                         bar = kv && masked ? B::kLand + b : B::kFull + b;
                         dst = C::kOffRing + b * C::kTile;
                         bytes = C::kTile;
@@ -804,6 +834,10 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                             }
                         }
                     }
+                }
+                if (it + 1 < count) {
+                    if (++u.step == u.steps) next_unit<kTM, kTN>(p, u);
+                    look_up();
                 }
             }
         }
