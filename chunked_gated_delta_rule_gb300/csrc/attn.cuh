@@ -18,6 +18,22 @@
 
 namespace gdr {
 
+// Division by a number d that a call does not change, of x < 2^31: with l =
+// ceil(log2 d) and m = ceil(2^(31 + l) / d), floor(x m / 2^(31 + l)) is
+// floor(x / d), as m d - 2^(31 + l) < d <= 2^l.
+struct Divisor {
+    uint32_t m;
+    int s;
+    __device__ __forceinline__ int operator()(int x) const {
+        return (int)(((uint64_t)(uint32_t)x * m) >> s);
+    }
+};
+inline Divisor divisor(uint32_t d) {
+    int l = 0;
+    while ((uint64_t(1) << l) < d) ++l;
+    return Divisor{(uint32_t)(((uint64_t(1) << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 struct AttnProblem {
     PagedCache c;
     TokenRows r;
@@ -29,6 +45,7 @@ struct AttnProblem {
     int window;           // 0: none
     float scale;
     int grid_limit;
+    Divisor by_G, by_page;
     int align;            // tiles' first positions are multiples of it (a power of two)
 };
 

@@ -183,6 +183,8 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
     const bool can = attn_tiles_supported(p);
     if (force == 2 && !can) return GDR_ERR_UNSUPPORTED;
     const bool tiles = force == 2 || (force == 0 && can && tile_rows(*dims) * p.G > kFewRows);
+    p.by_G = divisor((uint32_t)p.G);
+    p.by_page = divisor((uint32_t)p.c.page_size);
     for (p.align = 1; p.align < 128 && p.c.page_size % (2 * p.align) == 0;) p.align *= 2;
     const SplitPlan plan = tiles ? attn_tiles_plan(p) : attn_rows_plan(p);
     const size_t need = split_bytes(plan, p.V);

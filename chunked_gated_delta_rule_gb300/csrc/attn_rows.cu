@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qr = lane >> 2, qc = lane & 3;
     pdl_trigger();
-    split_prefix<kRowsM, C::kBN, 32 * kRowsWarps>(p, a.per, s_pre);
+    split_prefix<kRowsM, C::kBN, 0, 32 * kRowsWarps>(p, a.per, s_pre, nullptr);
 
     const int64_t total = s_pre[kSplitSlots];
     const int64_t worker = (int64_t)blockIdx.x * kRowsWarps + warp;
@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
     if (worker >= nw) return;
     const int64_t begin = share_begin(total, worker, nw);
     const int count = (int)(share_begin(total, worker + 1, nw) - begin);
-    Unit u = split_locate<kRowsM, C::kBN>(p, a.per, s_pre, begin);
+    int64_t real;
+    Unit u = split_locate<kRowsM, C::kBN, 0>(p, a.per, s_pre, nullptr, begin, real);
 
     uint8_t *ring = smem + warp * C::kRing;
     const uint32_t ring_u = tc::smem_u32(ring);
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
         const int pos = u.lo + u.step * C::kBN + lane;
         page = -1;
         if (lane < C::kBN && pos < u.hi) {
-            const int pi = pos / p.c.page_size;
+            const int pi = p.by_page(pos);
             slot = pos - pi * p.c.page_size;
             page = page_of(p.c, u.n, pi, p.r.status);
         }
@@ -300,8 +301,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
             begun = f.first;
             const int rows = min(kRowsM, f.len * p.G - f.tile * kRowsM);
             two = rows > 8;
-            const int ra = f.tile * kRowsM + qr, ia = ra / p.G, ib = (ra + 8) / p.G;
-            several = ia != f.tile * kRowsM / p.G || rows > p.G;
+            const int ra = f.tile * kRowsM + qr, ia = p.by_G(ra), ib = p.by_G(ra + 8);
+            several = rows > p.G || (qr == 0 && p.by_G(ra + rows - 1) != ia);
             several = __any_sync(0xffffffffu, several);
             lo0 = hi0 = lo1 = hi1 = 0;
             const T *qa = nullptr, *qb = nullptr;
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
                 if (whole) {
                     const bool empty = l == 0.f;
                     const float inv = empty ? 0.f : 1.f / l;
-                    const int row = f.tile * kRowsM + r, i = row / p.G;
+                    const int row = f.tile * kRowsM + r, i = p.by_G(row);
                     const int hq = f.head * p.G + row - i * p.G;
                     T *o = reinterpret_cast<T *>(p.o) + tok_at(p.so, f.t0 + i, hq);
                     if constexpr (FMT == 0) {
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
     auto write = [&](const Joined<kV> &a, int r) {
         const bool empty = a.l == 0.f;
         const float inv = empty ? 0.f : 1.f / a.l;
-        const int row = tile * M + r, i = row / p.G, hq = head * p.G + row - i * p.G;
+        const int row = tile * M + r, i = p.by_G(row), hq = head * p.G + row - i * p.G;
         T *o = reinterpret_cast<T *>(p.o) + tok_at(p.so, t0 + i, hq) + lane * kV;
 #pragma unroll
         for (int e = 0; e < kV; e += 2)

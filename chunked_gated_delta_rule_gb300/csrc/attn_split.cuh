@@ -8,6 +8,10 @@
 // lengths, known to every worker from the lengths alone, with no plan made on
 // the host (the lengths are device data) and none passed between kernels.
 //
+// A unit also costs what comes before its first step and after its last; it
+// stands for U0 steps more on the line, ahead of its own.  A share that holds
+// only such steps of a unit does nothing of it.
+//
 // A worker's share meets at most two units that it does not do whole: its
 // first (begun before it, slot 0) and its last (begun by it, slot 1).  Their
 // unnormalised sums go to the worker's two scratch slots, and the worker that
@@ -56,8 +60,8 @@ __device__ __forceinline__ int tiles_of(const AttnProblem &p, int len) {
 // multiple of p.align (a box of a page begins there), and the tile's steps.
 template <int M, int BN>
 __device__ __forceinline__ int tile_steps(const AttnProblem &p, Unit &u) {
-    const int r0 = u.tile * M, i0 = r0 / p.G;
-    const int i1 = min((r0 + M - 1) / p.G, u.len - 1);
+    const int r0 = u.tile * M, i0 = p.by_G(r0);
+    const int i1 = min(p.by_G(r0 + M - 1), u.len - 1);
     int a, d;
     visible(p, u.kv, u.kv - u.len + i0, a, u.in_hi);
     visible(p, u.kv, u.kv - u.len + i1, u.in_lo, d);
@@ -76,78 +80,99 @@ __device__ __forceinline__ int unit_rows(const AttnProblem &p, const Unit &u) {
     return min(M, u.len * p.G - u.tile * M);
 }
 
-template <int M, int BN>
-__device__ __forceinline__ int64_t seq_steps(const AttnProblem &p, Unit &u, int first, int stride) {
+// Length on the line of a sequence's tiles first, first + stride, ...
+template <int M, int BN, int U0>
+__device__ __forceinline__ int64_t seq_line(const AttnProblem &p, Unit &u, int first, int stride) {
     int64_t s = 0;
     const int tiles = tiles_of<M>(p, u.len);
-    for (u.tile = first; u.tile < tiles; u.tile += stride) s += tile_steps<M, BN>(p, u);
+    for (u.tile = first; u.tile < tiles; u.tile += stride) s += tile_steps<M, BN>(p, u) + U0;
     return s * p.c.H;
 }
 
-// Exclusive prefix sums of the steps of kSplitSlots groups of `per` sequences
-// (per = ceil(N / kSplitSlots)) in pre[0 .. kSplitSlots], by the whole block.
-// Each thread sums a group's short sequences; those of many tiles are left
-// to the block, which shares their tiles out.
-template <int M, int BN, int NT>
-__device__ void split_prefix(const AttnProblem &p, int64_t per, int64_t *pre) {
+// Exclusive prefix sums, by the whole block, over kSplitSlots groups of `per`
+// sequences (per = ceil(N / kSplitSlots)): lengths on the line in pre[0 ..
+// kSplitSlots], and units in units[] where U0 > 0.  Each thread sums up a
+// group's short sequences; those of many tiles are left to the block, which
+// shares their tiles out.
+template <int M, int BN, int U0, int NT>
+__device__ void split_prefix(const AttnProblem &p, int64_t per, int64_t *pre, int64_t *units) {
     static_assert(NT % 32 == 0 && kSplitSlots % 32 == 0, "whole warps");
-    constexpr int kFew = 8;
-    __shared__ int s_many[kSplitSlots];
-    __shared__ int64_t s_warp[kSplitSlots / 32];
-    __shared__ int s_any;
+    constexpr int kFew = 4;
+    __shared__ int64_t s_warp[2][kSplitSlots / 32];
+    __shared__ int s_long[kSplitSlots], s_longs;  // groups with long sequences
     const int tid = threadIdx.x;
-    if (tid == 0) s_any = 0;
+    if (tid == 0) s_longs = 0;
     __syncthreads();
     for (int e = tid; e < kSplitSlots; e += NT) {
-        int64_t sum = 0;
-        int many = 0;
+        int64_t sum = 0, un = 0;
+        bool any = false;
         for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
             Unit u;
             load_seq(p, n, u.t0, u.len, u.kv);
-            if (tiles_of<M>(p, u.len) <= kFew) sum += seq_steps<M, BN>(p, u, 0, 1);
-            else ++many;
+            const int tiles = tiles_of<M>(p, u.len);
+            un += tiles;
+            if (tiles <= kFew) sum += seq_line<M, BN, U0>(p, u, 0, 1);
+            else any = true;
         }
         pre[e + 1] = sum;
-        s_many[e] = many;
-        if (many) s_any = 1;
+        if (U0) units[e + 1] = un * p.c.H;
+        if (any) s_long[atomicAdd(&s_longs, 1)] = e;
     }
-    if (tid == 0) pre[0] = 0;
+    if (tid == 0) {
+        pre[0] = 0;
+        if (U0) units[0] = 0;
+    }
     __syncthreads();
-    if (s_any) {
-        for (int e = 0; e < kSplitSlots; ++e) {
-            if (!s_many[e]) continue;
-            int64_t sum = 0;
-            for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
-                Unit u;
-                load_seq(p, n, u.t0, u.len, u.kv);
-                if (tiles_of<M>(p, u.len) > kFew) sum += seq_steps<M, BN>(p, u, tid, NT);
-            }
-            atomicAdd(reinterpret_cast<unsigned long long *>(&pre[e + 1]), (unsigned long long)sum);
+    const int longs = s_longs;
+    for (int i = 0; i < longs; ++i) {
+        const int e = s_long[i];
+        int64_t sum = 0;
+        for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
+            Unit u;
+            load_seq(p, n, u.t0, u.len, u.kv);
+            if (tiles_of<M>(p, u.len) > kFew) sum += seq_line<M, BN, U0>(p, u, tid, NT);
         }
-        __syncthreads();
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if ((tid & 31) == 0 && sum)
+            atomicAdd(reinterpret_cast<unsigned long long *>(&pre[e + 1]), (unsigned long long)sum);
     }
+    if (longs) __syncthreads();
     for (int e = tid; e < kSplitSlots; e += NT) {  // whole warps: NT and the slots are multiples
-        int64_t x = pre[e + 1];
+        int64_t x = pre[e + 1], y = U0 ? units[e + 1] : 0;
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-            if ((e & 31) >= d) x += y;
+            const int64_t a = __shfl_up_sync(0xffffffffu, x, d);
+            const int64_t b = U0 ? __shfl_up_sync(0xffffffffu, y, d) : 0;
+            if ((e & 31) >= d) {
+                x += a;
+                y += b;
+            }
         }
         pre[e + 1] = x;
-        if ((e & 31) == 31) s_warp[e >> 5] = x;
+        if (U0) units[e + 1] = y;
+        if ((e & 31) == 31) {
+            s_warp[0][e >> 5] = x;
+            s_warp[1][e >> 5] = y;
+        }
     }
     __syncthreads();
     for (int e = tid; e < kSplitSlots; e += NT) {
-        int64_t add = 0;
-        for (int w = 0; w < (e >> 5); ++w) add += s_warp[w];
-        pre[e + 1] += add;
+        int64_t x = 0, y = 0;
+        for (int w = 0; w < (e >> 5); ++w) {
+            x += s_warp[0][w];
+            y += s_warp[1][w];
+        }
+        pre[e + 1] += x;
+        if (U0) units[e + 1] += y;
     }
     __syncthreads();
 }
 
-// The sequence, tile and key head that hold step `at` of the line, by a whole
-// warp (0 <= at < pre[kSplitSlots]).
-template <int M, int BN>
-__device__ Unit split_locate(const AttnProblem &p, int64_t per, const int64_t *pre, int64_t at) {
+// The unit and the step of it that a worker begins with whose share begins at
+// `at` on the line (0 <= at < pre[kSplitSlots]), and the steps of all units
+// before that one in `real`; by a whole warp.
+template <int M, int BN, int U0>
+__device__ Unit split_locate(const AttnProblem &p, int64_t per, const int64_t *pre,
+                             const int64_t *units, int64_t at, int64_t &real) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = kSplitSlots;  // the last e with pre[e] <= at
     while (hi - lo > 1) {
@@ -157,14 +182,15 @@ __device__ Unit split_locate(const AttnProblem &p, int64_t per, const int64_t *p
         if (lo + step < hi) hi = lo + step;
     }
     int64_t rem = at - pre[lo];
+    real = pre[lo] - (U0 ? U0 * units[lo] : 0);
     Unit u{};
     for (int64_t n = lo * per;; ++n) {
         load_seq(p, n, u.t0, u.len, u.kv);
         const int tiles = tiles_of<M>(p, u.len);
         for (int t = 0; t < tiles; t += 32) {
             u.tile = t + lane;
-            const int s = t + lane < tiles ? tile_steps<M, BN>(p, u) : 0;
-            int64_t x = (int64_t)s * p.c.H;
+            const int s = t + lane < tiles ? tile_steps<M, BN>(p, u) : -U0;
+            int64_t x = (int64_t)(s + U0) * p.c.H;
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
                 if (lane >= d) x += y;
@@ -175,14 +201,19 @@ __device__ Unit split_locate(const AttnProblem &p, int64_t per, const int64_t *p
                 u.n = (int)n;
                 u.tile = t + l;
                 u.steps = tile_steps<M, BN>(p, u);
-                rem -= __shfl_sync(0xffffffffu, x, l) - (int64_t)u.steps * p.c.H;
-                u.head = (int)(rem / u.steps);
-                u.step = (int)(rem - (int64_t)u.head * u.steps);
+                const int64_t before = __shfl_sync(0xffffffffu, x, l) - (int64_t)(u.steps + U0) * p.c.H;
+                rem -= before;
+                u.head = (int)(rem / (u.steps + U0));
+                const int v = (int)(rem - (int64_t)u.head * (u.steps + U0)) - U0;
+                u.step = v > 0 ? v : 0;
+                real += before - (int64_t)U0 * p.c.H * l + (int64_t)u.head * u.steps;
                 return u;
             }
-            rem -= __shfl_sync(0xffffffffu, x, 31);
+            const int64_t all = __shfl_sync(0xffffffffu, x, 31);
+            rem -= all;
+            real += all - (int64_t)U0 * p.c.H * min(32, tiles - t);
         }
-        if (n + 1 >= p.r.N) return u;  // not reached for a step of the line
+        if (n + 1 >= p.r.N) return u;  // not reached for a point of the line
     }
 }
 
@@ -201,12 +232,11 @@ __device__ __forceinline__ void next_unit(const AttnProblem &p, Unit &u) {
     u.steps = tile_steps<M, BN>(p, u);
 }
 
-// First step of worker w of nw.
+// Where the share of worker w of nw begins.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int64_t w, int64_t nw) {
     return total / nw * w + total % nw * w / nw;
 }
-// Pieces of the unit whose steps end before `end` on the line, begun by
-// worker w: the workers from w on whose shares begin before it.  Worker j's
+// Pieces of the unit that ends at `end` on the line, begun by worker w: the workers from w on whose shares begin before it.  Worker j's
 // does iff floor(total j / nw) < end, that is iff total j < end nw.
 __device__ __forceinline__ int pieces_from(int64_t total, int64_t w, int64_t nw, int64_t end) {
     const int64_t j = (end * nw + total - 1) / total;

@@ -48,6 +48,7 @@ using namespace tc;
 constexpr int kTM = 256;       // rows of a unit
 constexpr int kTN = 128;       // positions of a step
 constexpr int kTThreads = 512;
+constexpr int kTUnit = 2;      // what a unit costs beside its steps, in steps
 constexpr float kTLog2e = 1.4426950408889634f;
 constexpr float kTLn2 = 0.6931471805599453f;
 constexpr float kTLeast = 7.888609052210118e-31f;  // 2^-100
@@ -92,7 +93,9 @@ struct TilesArgs {
     int64_t per;
     int min_steps;
     int box;             // slots of a TMA box
+    int q_box;           // queries by TMA: tokens of a half (0: by the helpers)
     CUtensorMap tk, tv;  // [page][head][slot][column] of the caches
+    CUtensorMap tq;      // [token][head][column]
 };
 
 template <int R>
@@ -264,7 +267,9 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_pre[kSplitSlots + 1];
     __shared__ Unit s_unit;
-    __shared__ int64_t s_share[4];  // steps of the call, workers, this one's first step and count
+    __shared__ int64_t s_units[kSplitSlots + 1];
+    __shared__ int64_t s_share[3];  // length of the line, workers, where this one's share ends
+    __shared__ int64_t s_real[2];   // steps of the call before this worker's, and with them
     __shared__ int s_poison[8];  // unit (count, modulo 8) + 1 whose masked values are not finite
     __shared__ int2 s_piece[8];  // steps and halves of the piece (count, modulo 8), for the products
     __shared__ uint32_t s_tmem;
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
         }
         for (int i = 0; i < C::kLands; ++i) mbar_init(&bars[B::kLand + i], 1);
         for (int i = 0; i < C::kRaw; ++i) mbar_init(&bars[B::kTaken + i], 128);
-        mbar_init(&bars[B::kQFull], 128);
+        mbar_init(&bars[B::kQFull], a.q_box ? 1 : 128);
         mbar_init(&bars[B::kQEmpty], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[B::kS + i], 1);
@@ -298,22 +303,26 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     }
     if (tid < 8) s_poison[tid] = 0;
     if (warp == 12) tmem_alloc(&s_tmem, 512);
-    split_prefix<kTM, kTN, kTThreads>(p, a.per, s_pre);
-    if (warp == 0) {
+    split_prefix<kTM, kTN, kTUnit, kTThreads>(p, a.per, s_pre, s_units);
+    if (warp < 2) {  // where the share begins, and where it ends
         const int64_t total = s_pre[kSplitSlots], w = blockIdx.x;
         int64_t nw = gridDim.x;
         if (nw * a.min_steps > total) nw = (total + a.min_steps - 1) / a.min_steps;
-        const int64_t begin = w < nw ? share_begin(total, w, nw) : 0;
-        const int64_t steps = w < nw ? share_begin(total, w + 1, nw) - begin : 0;
-        Unit u{};
-        if (steps) u = split_locate<kTM, kTN>(p, a.per, s_pre, begin);
+        const int64_t at = w < nw ? share_begin(total, w + warp, nw) : total;
+        int64_t real = total - kTUnit * s_units[kSplitSlots];  // of the whole line
+        if (at < total) {
+            const Unit u = split_locate<kTM, kTN, kTUnit>(p, a.per, s_pre, s_units, at, real);
+            real += u.step;
+            if (warp == 0 && lane == 0) s_unit = u;
+        }
         if (lane == 0) {
-            s_unit = u;
-            s_share[0] = total;
-            s_share[1] = nw;
-            s_share[2] = begin;
-            s_share[3] = steps;
-            a.ws.rec[w * 2] = make_int4(0, 0, 0, 0);
+            s_real[warp] = real;
+            if (warp == 1) {
+                s_share[0] = total;
+                s_share[1] = nw;
+                s_share[2] = at;
+                a.ws.rec[w * 2] = make_int4(0, 0, 0, 0);
+            }
         }
     }
     tc_fence_before();
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     auto wait = [&](int b, uint32_t parity) {
         return mbar_wait_or_abort(&bars[b], parity & 1u, p.r.status, s_abort);
     };
-    const int count = (int)s_share[3];
+    const int count = (int)(s_real[1] - s_real[0]);
 
     if (count == 0) {
         // no steps for this CTA
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             if (half == 0 || rows > 128) {
                 const int r = half * 128 + row;
                 const bool live = r < rows;
-                const int ur = u.tile * kTM + r, tok = ur / p.G, hq = u.head * p.G + ur - tok * p.G;
+                const int ur = u.tile * kTM + r, tok = p.by_G(ur), hq = u.head * p.G + ur - tok * p.G;
                 int lo = 0, hi = 0;
                 if (live) visible(p, u.kv, u.kv - u.len + tok, lo, hi);
                 float m = -INFINITY, l = 0.f;
@@ -365,7 +374,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     const int base = u.lo + (first + s) * kTN;
                     const float *scale = nullptr;
                     if constexpr (FMT != 0) {
-                        if (s == 0) f *= reinterpret_cast<const float *>(sm + C::kOffQf)[(seg & 1) * kTM + r];
+                        if (s == 0 && std::is_same<T, __nv_bfloat16>::value)
+                            f *= reinterpret_cast<const float *>(sm + C::kOffQf)[(seg & 1) * kTM + r];
                         scale = reinterpret_cast<const float *>(sm + C::kOffScale) + ((done + s) % C::kScales) * 3 * kTN;
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                             const int base = u.lo + s * kTN;
                             if (!step_masked<kTN>(u, base)) continue;
                             for (int j = max(base, lo); j < min(base + kTN, hi); ++j) {
-                                const int page = page_of(p.c, u.n, j / p.c.page_size, p.r.status);
+                                const int page = page_of(p.c, u.n, p.by_page(j), p.r.status);
                                 if (page < 0) continue;
                                 const T *v = reinterpret_cast<const T *>(p.c.v) +
                                              page_at(p.c.vst, page, j % p.c.page_size, u.head) + 32 * q;
@@ -530,7 +540,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             done += steps;
             if (begun && !ends && tid == 0) {
                 const int pieces = pieces_from(s_share[0], worker, s_share[1],
-                                               s_share[2] + done + (u.steps - first - steps));
+                                               s_share[2] + (u.steps - first - steps));
                 a.ws.rec[worker * 2] = make_int4(pieces, u.t0, u.len, u.tile);
                 a.ws.rec[worker * 2 + 1].x = u.head;
             }
@@ -554,7 +564,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             constexpr bool kConvert = FMT != 0 && std::is_same<T, __nv_bfloat16>::value;
 #pragma unroll 8
             for (int r = t / kQC; r < 128 * halves; r += kQP) {
-                const int ur = u.tile * kTM + r, tok = ur / p.G, hq = u.head * p.G + ur - tok * p.G;
+                const int ur = u.tile * kTM + r, tok = p.by_G(ur), hq = u.head * p.G + ur - tok * p.G;
                 const bool live = r < rows;
                 const T *src = reinterpret_cast<const T *>(p.q) +
                                (live ? tok_at(p.sq, u.t0 + tok, hq) + qc * 8 : 0);
@@ -583,7 +593,6 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     if (qc == 0) qf[r] = 1.f / g;
                 } else {
                     cp16z(sb + dst, src, live);
-                    if (FMT != 0 && qc == 0) qf[r] = 1.f;
                 }
             }
             if constexpr (!kConvert) asm volatile("cp.async.wait_all;" ::: "memory");
@@ -594,12 +603,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             ok = help_sync(ok);
             if (!ok) break;
             if (it > 0 && u.step == 0) ++seg;
-            if (it == 0 || u.step == 0) {
-                if (t == 0)
-                    s_piece[seg & 7] = make_int2(min(count - it, u.steps - u.step),
-                                                 unit_rows<kTM>(p, u) > 128 ? 2 : 1);
-                queries();
-            }
+            if (!a.q_box && (it == 0 || u.step == 0)) queries();
             const int base = u.lo + u.step * kTN, left = u.hi - base;  // positions of the step
             if constexpr (FMT == 0) {
                 const int b = (item + 1) % C::kRing;
@@ -611,24 +615,31 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
                         uint8_t *tile = sm + C::kOffRing + b * C::kTile;
                         bool bad = false;
+#pragma unroll 4
                         for (int i = t; i < kTN * D / 8; i += 128) {
                             const int r = i / (D / 8);
                             uint4 *w4 = reinterpret_cast<uint4 *>(tile + sw128_chunk(r, i % (D / 8), kTN));
+                            if (r >= left) {
+                                *w4 = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
                             uint4 x = *w4;
+                            // a half word whose exponent is all ones, less
+                            // the ones below: its top bit is set by the borrow
+                            auto odd = [](uint32_t y) {
+                                y = (y & (kExp | kExp << 16)) ^ (kExp | kExp << 16);
+                                return (y - 0x00010001u) & ~y & 0x80008000u;
+                            };
+                            if (!(odd(x.x) | odd(x.y) | odd(x.z) | odd(x.w))) continue;
                             uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-                            bool change = r >= left;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const uint32_t y = w[e];
                                 const bool b0 = (y & kExp) == kExp, b1 = (y >> 16 & kExp) == kExp;
-                                if (r >= left) {
-                                    w[e] = 0;
-                                } else if (b0 || b1) {
-                                    w[e] = (b0 ? 0u : y & 0xffffu) | (b1 ? 0u : y & 0xffff0000u);
-                                    bad = change = true;
-                                }
+                                w[e] = (b0 ? 0u : y & 0xffffu) | (b1 ? 0u : y & 0xffff0000u);
+                                bad |= b0 || b1;
                             }
-                            if (change) *w4 = x;
+                            *w4 = x;
                         }
                         if (bad) s_poison[seg & 7] = seg + 1;
                         fence_async_smem();
@@ -779,15 +790,19 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 const int pos = u.lo + u.step * kTN + lane * box;
                 asked = lane < boxes && pos < u.hi;
                 if (asked) {
-                    const int pi = pos / p.c.page_size;
+                    const int pi = p.by_page(pos);
                     slot = pos - pi * p.c.page_size;
                     entry = p.c.table[u.n * p.c.max_pages + pi];
                 }
             };
-            uint32_t item = 0;
+            uint32_t item = 0, seg = 0;
             bool ok = true;
             look_up();
             for (int it = 0; it < count && ok; ++it) {
+                const bool first = it == 0 || u.step == 0;
+                if (first && lane == 0)
+                    s_piece[seg & 7] = make_int2(min(count - it, u.steps - u.step),
+                                                 unit_rows<kTM>(p, u) > 128 ? 2 : 1);
                 // a page past the cache reads as zeros
                 const bool here = asked && (unsigned)entry < (unsigned)p.c.n_pages;
                 if (asked && !here) report(p.r.status, GDR_ERR_INDEX);
@@ -834,7 +849,22 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                             }
                         }
                     }
+                    if (first && kv == 0 && a.q_box) {
+                        // rows past the unit's are those of other tokens, or
+                        // zeros; they see nothing
+                        ok = __all_sync(0xffffffffu, wait(B::kQEmpty, seg + 1));
+                        if (!ok) break;
+                        const int halves = unit_rows<kTM>(p, u) > 128 ? 2 : 1;
+                        if (lane == 0) mbar_arrive_expect_tx(&bars[B::kQFull], halves * C::kTile);
+                        __syncwarp();
+                        if (lane < halves * (D / 64)) {
+                            const int h = lane / (D / 64), c = lane % (D / 64);
+                            tma_load_3d(sm + h * C::kTile + c * 16384, &a.tq, &bars[B::kQFull], c * 64,
+                                        u.head * p.G, u.t0 + (u.tile * 2 + h) * a.q_box);
+                        }
+                    }
                 }
+                seg += first;
                 if (it + 1 < count) {
                     if (++u.step == u.steps) next_unit<kTM, kTN>(p, u);
                     look_up();
@@ -884,6 +914,21 @@ cudaError_t launch_tiles(const AttnProblem &p, const SplitScratch &ws, int ctas,
     TilesArgs a{p, ws, (p.r.N + kSplitSlots - 1) / kSplitSlots, 1, p.align};
     if (!page_map(&a.tk, p, p.c.k, p.c.kst, D, a.box) || !page_map(&a.tv, p, p.c.v, p.c.vst, D, a.box))
         return cudaErrorInvalidValue;
+    // a half's rows are whole tokens: its queries are one box of 128 / G
+    // tokens by G heads
+    constexpr bool kConvert = FMT != 0 && std::is_same<T, __nv_bfloat16>::value;
+    if (!kConvert && p.G <= 128 && 128 % p.G == 0) {
+        auto enc = tensor_map_encoder();
+        const uint64_t tokens = rows_packed(p.r) ? p.r.T : p.r.N * p.r.T;
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)tokens};
+        const cuuint64_t strides[2] = {(cuuint64_t)p.sq.h * 2, (cuuint64_t)p.sq.t * 2};
+        const cuuint32_t bx[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)}, one[3] = {1, 1, 1};
+        if (enc(&a.tq, p.dtype == GDR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                3, const_cast<void *>(p.q), dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+            a.q_box = 128 / p.G;
+    }
     auto k = k_attn_tiles<T, FMT, D>;
     cudaFuncAttributes at;
     cudaError_t e = cudaFuncGetAttributes(&at, k);
