@@ -180,7 +180,6 @@ __device__ __forceinline__ int dim_of(int nt, int n) {
 struct RowsArgs {
     AttnProblem p;
     SplitScratch ws;
-    int64_t per;     // sequences a group of the prefix sums
     int min_steps;   // least steps a worker
 };
 
@@ -195,24 +194,23 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
     // the output's own
     constexpr bool kSplitP = std::is_same<T, TP>::value;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_pre[kSplitSlots + 1];
     __shared__ StepInfo s_info[kRowsWarps][C::kStages];
     const AttnProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qr = lane >> 2, qc = lane & 3;
     pdl_trigger();
-    split_prefix<kRowsM, C::kBN, 0, 32 * kRowsWarps>(p, a.per, s_pre, nullptr);
-
-    const int64_t total = s_pre[kSplitSlots];
+    SplitLine<kRowsM, C::kBN, 0> line;
+    line.measure(p);
+    const int64_t total = line.total;
     const int64_t worker = (int64_t)blockIdx.x * kRowsWarps + warp;
     int64_t nw = (int64_t)gridDim.x * kRowsWarps;
-    if (nw * a.min_steps > total) nw = (total + a.min_steps - 1) / a.min_steps;
+    if (nw * a.min_steps > total) nw = quotient(total + a.min_steps - 1, a.min_steps);
     if (lane == 0) a.ws.rec[worker * 2] = make_int4(0, 0, 0, 0);
     if (worker >= nw) return;
     const int64_t begin = share_begin(total, worker, nw);
     const int count = (int)(share_begin(total, worker + 1, nw) - begin);
     int64_t real;
-    Unit u = split_locate<kRowsM, C::kBN, 0>(p, a.per, s_pre, nullptr, begin, real);
+    Unit u = line.locate(p, begin, real);
 
     uint8_t *ring = smem + warp * C::kRing;
     const uint32_t ring_u = tc::smem_u32(ring);
@@ -789,7 +787,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
 template <typename T, int FMT, int D>
 cudaError_t launch_rows(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
     using C = RowsCfg<FMT, D>;
-    RowsArgs a{p, ws, (p.r.N + kSplitSlots - 1) / kSplitSlots, 4};
+    RowsArgs a{p, ws, 4};
     auto k = k_attn_rows<T, FMT, D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;

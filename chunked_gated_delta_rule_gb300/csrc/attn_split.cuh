@@ -32,8 +32,6 @@ struct SplitScratch {
     int4 *rec;
 };
 
-constexpr int kSplitSlots = 256;  // groups of sequences whose steps are summed up
-
 struct Unit {
     int n, tile, head;
     int step, steps;       // next step, steps of the unit
@@ -42,13 +40,25 @@ struct Unit {
     int t0, len, kv;       // the sequence: first token, new tokens, cached tokens
 };
 
-__device__ __forceinline__ void load_seq(const AttnProblem &p, int64_t n, int &t0, int &len,
-                                         int &kv) {
-    int64_t a, b;
-    seq_span(p.r, n, a, b);
-    t0 = (int)a;
-    len = (int)b;
-    kv = (int)cached_len(p.c, n, p.r.status);
+// The sequence's part of a unit.  Returns 0 or the code to report; nothing
+// outside the call's tokens and the page table's row is addressed after it.
+__device__ __forceinline__ int load_seq(const AttnProblem &p, int64_t n, Unit &u) {
+    const int64_t t0 = row_bound(p.r, n), end = row_bound(p.r, n + 1);
+    const int kv = p.c.kv_lens[n];
+    const int cap = (int)(p.c.max_pages * p.c.page_size);
+    int code = 0;
+    u.t0 = (int)t0;
+    u.len = (int)(end - t0);
+    u.kv = kv;
+    if (rows_packed(p.r) && (t0 < 0 || end < t0 || end > p.r.T)) {
+        code = GDR_ERR_SEQLENS;
+        u.t0 = u.len = 0;
+    }
+    if (kv < 0 || kv > cap) {
+        code = GDR_ERR_INDEX;
+        u.kv = kv < 0 ? 0 : cap;
+    }
+    return code;
 }
 
 template <int M>
@@ -80,6 +90,17 @@ __device__ __forceinline__ int unit_rows(const AttnProblem &p, const Unit &u) {
     return min(M, u.len * p.G - u.tile * M);
 }
 
+// x / y, for 0 <= x and 0 < y: in 32 bits where both fit, as they do but for
+// calls of many millions of steps.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    if (((uint64_t)(x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+    return x / y;
+}
+// Where the share of worker w of nw begins.
+__device__ __forceinline__ int64_t share_begin(int64_t total, int64_t w, int64_t nw) {
+    const int64_t q = quotient(total, nw);
+    return q * w + quotient((total - q * nw) * w, nw);
+}
 // Length on the line of a sequence's tiles first, first + stride, ...
 template <int M, int BN, int U0>
 __device__ __forceinline__ int64_t seq_line(const AttnProblem &p, Unit &u, int first, int stride) {
@@ -89,133 +110,107 @@ __device__ __forceinline__ int64_t seq_line(const AttnProblem &p, Unit &u, int f
     return s * p.c.H;
 }
 
-// Exclusive prefix sums, by the whole block, over kSplitSlots groups of `per`
-// sequences (per = ceil(N / kSplitSlots)): lengths on the line in pre[0 ..
-// kSplitSlots], and units in units[] where U0 > 0.  Each thread sums up a
-// group's short sequences; those of many tiles are left to the block, which
-// shares their tiles out.
-template <int M, int BN, int U0, int NT>
-__device__ void split_prefix(const AttnProblem &p, int64_t per, int64_t *pre, int64_t *units) {
-    static_assert(NT % 32 == 0 && kSplitSlots % 32 == 0, "whole warps");
-    constexpr int kFew = 4;
-    __shared__ int64_t s_warp[2][kSplitSlots / 32];
-    __shared__ int s_long[kSplitSlots], s_longs;  // groups with long sequences
-    const int tid = threadIdx.x;
-    if (tid == 0) s_longs = 0;
-    __syncthreads();
-    for (int e = tid; e < kSplitSlots; e += NT) {
-        int64_t sum = 0, un = 0;
-        bool any = false;
-        for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
-            Unit u;
-            load_seq(p, n, u.t0, u.len, u.kv);
+// Where a worker begins: the length of the whole line, and, once the caller
+// has told where on the line its share begins, the unit and the step of it.
+// A warp's work: lane l holds the sequences [l per, (l + 1) per), per =
+// ceil(N / 32), sums them up, and the sums of the lanes are scanned.
+template <int M, int BN, int U0>
+struct SplitLine {
+    int64_t total, units;      // length, units of the call
+    int64_t line0, units0;     // those of the lanes before this one
+    int64_t per;
+
+    __device__ __forceinline__ void measure(const AttnProblem &p) {
+        const int lane = threadIdx.x & 31;
+        constexpr int kFew = 16;  // more tiles are shared out among the lanes
+        per = (p.r.N + 31) >> 5;
+        int64_t x = 0, y = 0;
+        int code = 0;
+#pragma unroll 4
+        for (int64_t k = 0; k < per; ++k) {
+            const int64_t n = lane * per + k;
+            Unit u{};
+            if (n < p.r.N) {
+                const int c = load_seq(p, n, u);
+                code = c ? c : code;
+            }
             const int tiles = tiles_of<M>(p, u.len);
-            un += tiles;
-            if (tiles <= kFew) sum += seq_line<M, BN, U0>(p, u, 0, 1);
-            else any = true;
+            y += tiles;
+            if (tiles <= kFew) x += seq_line<M, BN, U0>(p, u, 0, 1);
+            for (unsigned m = __ballot_sync(0xffffffffu, tiles > kFew); m; m &= m - 1) {
+                const int l = __ffs(m) - 1;
+                Unit v{};
+                v.len = __shfl_sync(0xffffffffu, u.len, l);
+                v.kv = __shfl_sync(0xffffffffu, u.kv, l);
+                int64_t sum = seq_line<M, BN, U0>(p, v, lane, 32);
+#pragma unroll
+                for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (lane == l) x += sum;
+            }
         }
-        pre[e + 1] = sum;
-        if (U0) units[e + 1] = un * p.c.H;
-        if (any) s_long[atomicAdd(&s_longs, 1)] = e;
-    }
-    if (tid == 0) {
-        pre[0] = 0;
-        if (U0) units[0] = 0;
-    }
-    __syncthreads();
-    const int longs = s_longs;
-    for (int i = 0; i < longs; ++i) {
-        const int e = s_long[i];
-        int64_t sum = 0;
-        for (int64_t n = e * per; n < (e + 1) * per && n < p.r.N; ++n) {
-            Unit u;
-            load_seq(p, n, u.t0, u.len, u.kv);
-            if (tiles_of<M>(p, u.len) > kFew) sum += seq_line<M, BN, U0>(p, u, tid, NT);
-        }
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if ((tid & 31) == 0 && sum)
-            atomicAdd(reinterpret_cast<unsigned long long *>(&pre[e + 1]), (unsigned long long)sum);
-    }
-    if (longs) __syncthreads();
-    for (int e = tid; e < kSplitSlots; e += NT) {  // whole warps: NT and the slots are multiples
-        int64_t x = pre[e + 1], y = U0 ? units[e + 1] : 0;
+        if (code) report(p.r.status, code);
+        y *= p.c.H;
+        line0 = x;
+        units0 = y;
+#pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t a = __shfl_up_sync(0xffffffffu, x, d);
             const int64_t b = U0 ? __shfl_up_sync(0xffffffffu, y, d) : 0;
-            if ((e & 31) >= d) {
+            if (lane >= d) {
                 x += a;
                 y += b;
             }
         }
-        pre[e + 1] = x;
-        if (U0) units[e + 1] = y;
-        if ((e & 31) == 31) {
-            s_warp[0][e >> 5] = x;
-            s_warp[1][e >> 5] = y;
-        }
+        total = __shfl_sync(0xffffffffu, x, 31);
+        units = U0 ? __shfl_sync(0xffffffffu, y, 31) : 0;
+        line0 = x - line0;
+        units0 = y - units0;
     }
-    __syncthreads();
-    for (int e = tid; e < kSplitSlots; e += NT) {
-        int64_t x = 0, y = 0;
-        for (int w = 0; w < (e >> 5); ++w) {
-            x += s_warp[0][w];
-            y += s_warp[1][w];
-        }
-        pre[e + 1] += x;
-        if (U0) units[e + 1] += y;
-    }
-    __syncthreads();
-}
 
-// The unit and the step of it that a worker begins with whose share begins at
-// `at` on the line (0 <= at < pre[kSplitSlots]), and the steps of all units
-// before that one in `real`; by a whole warp.
-template <int M, int BN, int U0>
-__device__ Unit split_locate(const AttnProblem &p, int64_t per, const int64_t *pre,
-                             const int64_t *units, int64_t at, int64_t &real) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = kSplitSlots;  // the last e with pre[e] <= at
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
-        const unsigned m = __ballot_sync(0xffffffffu, i < hi && pre[i] <= at);
-        lo += (31 - __clz(m)) * step;
-        if (lo + step < hi) hi = lo + step;
-    }
-    int64_t rem = at - pre[lo];
-    real = pre[lo] - (U0 ? U0 * units[lo] : 0);
-    Unit u{};
-    for (int64_t n = lo * per;; ++n) {
-        load_seq(p, n, u.t0, u.len, u.kv);
-        const int tiles = tiles_of<M>(p, u.len);
-        for (int t = 0; t < tiles; t += 32) {
-            u.tile = t + lane;
-            const int s = t + lane < tiles ? tile_steps<M, BN>(p, u) : -U0;
-            int64_t x = (int64_t)(s + U0) * p.c.H;
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
+    // The unit and step at `at` (0 <= at < total), and the steps of the call
+    // before that unit in `real`.
+    __device__ __forceinline__ Unit locate(const AttnProblem &p, int64_t at, int64_t &real) const {
+        const int lane = threadIdx.x & 31;
+        // the last lane that begins at or before it
+        const int g = 31 - __clz(__ballot_sync(0xffffffffu, line0 <= at));
+        int64_t rem = at - __shfl_sync(0xffffffffu, line0, g);
+        real = __shfl_sync(0xffffffffu, line0, g) - (U0 ? U0 * __shfl_sync(0xffffffffu, units0, g) : 0);
+        Unit u{};
+        for (int64_t n = g * per;; ++n) {
+            load_seq(p, n, u);
+            const int tiles = tiles_of<M>(p, u.len);
+            for (int t = 0; t < tiles; t += 32) {
+                u.tile = t + lane;
+                const int s = t + lane < tiles ? tile_steps<M, BN>(p, u) : -U0;
+                int64_t x = (int64_t)(s + U0) * p.c.H;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+                    if (lane >= d) x += y;
+                }
+                const unsigned m = __ballot_sync(0xffffffffu, x > rem);
+                if (m) {
+                    const int l = __ffs(m) - 1;
+                    u.n = (int)n;
+                    u.tile = t + l;
+                    u.steps = tile_steps<M, BN>(p, u);
+                    const int64_t before =
+                        __shfl_sync(0xffffffffu, x, l) - (int64_t)(u.steps + U0) * p.c.H;
+                    rem -= before;
+                    u.head = (int)quotient(rem, u.steps + U0);
+                    const int v = (int)(rem - (int64_t)u.head * (u.steps + U0)) - U0;
+                    u.step = v > 0 ? v : 0;
+                    real += before - (int64_t)U0 * p.c.H * l + (int64_t)u.head * u.steps;
+                    return u;
+                }
+                const int64_t all = __shfl_sync(0xffffffffu, x, 31);
+                rem -= all;
+                real += all - (int64_t)U0 * p.c.H * min(32, tiles - t);
             }
-            const unsigned m = __ballot_sync(0xffffffffu, x > rem);
-            if (m) {
-                const int l = __ffs(m) - 1;
-                u.n = (int)n;
-                u.tile = t + l;
-                u.steps = tile_steps<M, BN>(p, u);
-                const int64_t before = __shfl_sync(0xffffffffu, x, l) - (int64_t)(u.steps + U0) * p.c.H;
-                rem -= before;
-                u.head = (int)(rem / (u.steps + U0));
-                const int v = (int)(rem - (int64_t)u.head * (u.steps + U0)) - U0;
-                u.step = v > 0 ? v : 0;
-                real += before - (int64_t)U0 * p.c.H * l + (int64_t)u.head * u.steps;
-                return u;
-            }
-            const int64_t all = __shfl_sync(0xffffffffu, x, 31);
-            rem -= all;
-            real += all - (int64_t)U0 * p.c.H * min(32, tiles - t);
+            if (n + 1 >= p.r.N) return u;  // not reached for a point of the line
         }
-        if (n + 1 >= p.r.N) return u;  // not reached for a point of the line
     }
-}
+};
 
 // On to the next unit of the line (there is one).
 template <int M, int BN>
@@ -227,19 +222,15 @@ __device__ __forceinline__ void next_unit(const AttnProblem &p, Unit &u) {
     while (u.tile >= tiles_of<M>(p, u.len)) {
         u.tile = 0;
         if (++u.n >= p.r.N) return;
-        load_seq(p, u.n, u.t0, u.len, u.kv);
+        load_seq(p, u.n, u);
     }
     u.steps = tile_steps<M, BN>(p, u);
 }
 
-// Where the share of worker w of nw begins.
-__device__ __forceinline__ int64_t share_begin(int64_t total, int64_t w, int64_t nw) {
-    return total / nw * w + total % nw * w / nw;
-}
 // Pieces of the unit that ends at `end` on the line, begun by worker w: the workers from w on whose shares begin before it.  Worker j's
 // does iff floor(total j / nw) < end, that is iff total j < end nw.
 __device__ __forceinline__ int pieces_from(int64_t total, int64_t w, int64_t nw, int64_t end) {
-    const int64_t j = (end * nw + total - 1) / total;
+    const int64_t j = quotient(end * nw + total - 1, total);
     return (int)((j < nw ? j : nw) - w);
 }
 

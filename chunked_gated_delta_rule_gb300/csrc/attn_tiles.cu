@@ -90,8 +90,7 @@ struct TilesCfg {
 struct TilesArgs {
     AttnProblem p;
     SplitScratch ws;
-    int64_t per;
-    int min_steps;
+    int min_steps;       // least length of a share
     int box;             // slots of a TMA box
     int q_box;           // queries by TMA: tokens of a half (0: by the helpers)
     CUtensorMap tk, tv;  // [page][head][slot][column] of the caches
@@ -265,9 +264,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     using B = C;  // its barriers
     using TP = typename std::conditional<FMT == 0, T, __half>::type;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t s_pre[kSplitSlots + 1];
     __shared__ Unit s_unit;
-    __shared__ int64_t s_units[kSplitSlots + 1];
     __shared__ int64_t s_share[3];  // length of the line, workers, where this one's share ends
     __shared__ int64_t s_real[2];   // steps of the call before this worker's, and with them
     __shared__ int s_poison[8];  // unit (count, modulo 8) + 1 whose masked values are not finite
@@ -303,15 +300,16 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     }
     if (tid < 8) s_poison[tid] = 0;
     if (warp == 12) tmem_alloc(&s_tmem, 512);
-    split_prefix<kTM, kTN, kTUnit, kTThreads>(p, a.per, s_pre, s_units);
     if (warp < 2) {  // where the share begins, and where it ends
-        const int64_t total = s_pre[kSplitSlots], w = blockIdx.x;
+        SplitLine<kTM, kTN, kTUnit> line;
+        line.measure(p);
+        const int64_t total = line.total, w = blockIdx.x;
         int64_t nw = gridDim.x;
-        if (nw * a.min_steps > total) nw = (total + a.min_steps - 1) / a.min_steps;
+        if (nw * a.min_steps > total) nw = quotient(total + a.min_steps - 1, a.min_steps);
         const int64_t at = w < nw ? share_begin(total, w + warp, nw) : total;
-        int64_t real = total - kTUnit * s_units[kSplitSlots];  // of the whole line
+        int64_t real = total - kTUnit * line.units;  // of the whole line
         if (at < total) {
-            const Unit u = split_locate<kTM, kTN, kTUnit>(p, a.per, s_pre, s_units, at, real);
+            const Unit u = line.locate(p, at, real);
             real += u.step;
             if (warp == 0 && lane == 0) s_unit = u;
         }
@@ -911,7 +909,7 @@ bool page_map(CUtensorMap *map, const AttnProblem &p, const void *base, const in
 template <typename T, int FMT, int D>
 cudaError_t launch_tiles(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
     using C = TilesCfg<FMT, D>;
-    TilesArgs a{p, ws, (p.r.N + kSplitSlots - 1) / kSplitSlots, 1, p.align};
+    TilesArgs a{p, ws, 1, p.align};
     if (!page_map(&a.tk, p, p.c.k, p.c.kst, D, a.box) || !page_map(&a.tv, p, p.c.v, p.c.vst, D, a.box))
         return cudaErrorInvalidValue;
     // a half's rows are whole tokens: its queries are one box of 128 / G
