@@ -28,7 +28,13 @@
 // masked steps (one to three a unit) warps 8-11 clear the values past the end
 // and those that are not finite before the product, and the end of the piece
 // adds the latter to the rows that see them.
-// 8-bit caches: see attn_rows.cu for the place of the scales.
+// 8-bit caches: under FP16 queries the scales go where attn_rows.cu puts them,
+// to scores and weights, which costs a thread three loads a column (393 KB of
+// shared-memory traffic a step).  Under BF16 queries o is rounded to 8 bits, so
+// that FP16's 11 are as good as exact for the values: there the products see q
+// s / s_max in FP16, s_max the largest scale of the step's 128 positions, and
+// s_max alone is left to the weights.  The keys' scales stay with the scores:
+// lse is FP32.
 //
 // The steps of the call are shared out equally over one CTA an SM
 // (attn_split.cuh).  Every wait is bounded: on expiry the CTA records
@@ -65,7 +71,7 @@ struct TilesCfg {
     // tiles given back in pairs, a step's keys and the values before them
     // (one commit a step instead of two); 0: one by one
     static constexpr int kPairs = FMT ? 0 : kRing / 2;
-    static constexpr int kRaw = FMT ? 3 : 0;                 // 8-bit tiles on their way
+    static constexpr int kRaw = FMT ? 2 : 0;                 // 8-bit tiles on their way
     static constexpr uint32_t kRawTile = kTN * D, kRawSize = kRawTile + 2 * kTN * 4;
     // steps whose scales are kept: a step's keys are widened once the products
     // of the step kRing / 2 before it are done, so that softmax is at most
@@ -137,7 +143,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -263,12 +273,15 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     using C = TilesCfg<FMT, D>;
     using B = C;  // its barriers
     using TP = typename std::conditional<FMT == 0, T, __half>::type;
+    constexpr bool kFold = FMT != 0 && std::is_same<T, __nv_bfloat16>::value;  // values' scales in them
     extern __shared__ uint8_t smem_raw[];
     __shared__ Unit s_unit;
     __shared__ int64_t s_share[3];  // length of the line, workers, where this one's share ends
     __shared__ int64_t s_real[2];   // steps of the call before this worker's, and with them
     __shared__ int s_poison[8];  // unit (count, modulo 8) + 1 whose masked values are not finite
     __shared__ int2 s_piece[8];  // steps and halves of the piece (count, modulo 8), for the products
+    __shared__ float s_most[4];          // largest scale of a step's values, by warp
+    __shared__ uint2 s_ratio[kTN];       // scale / largest: FP16 hi and lo, each twice
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort_flag;
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -371,25 +384,38 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     for (int q = 0; q < 4; ++q) reg_fence(sr[q]);
                     const int base = u.lo + (first + s) * kTN;
                     const float *scale = nullptr;
+                    float fs = f, lgs = 0.f, invs = 1.f;  // of the step
                     if constexpr (FMT != 0) {
-                        if (s == 0 && std::is_same<T, __nv_bfloat16>::value)
-                            f *= reinterpret_cast<const float *>(sm + C::kOffQf)[(seg & 1) * kTM + r];
+                        if (s == 0 && kFold)
+                            fs = f *= reinterpret_cast<const float *>(sm + C::kOffQf)[(seg & 1) * kTM + r];
                         scale = reinterpret_cast<const float *>(sm + C::kOffScale) + ((done + s) % C::kScales) * 3 * kTN;
+                        if constexpr (kFold) {
+                            lgs = scale[kTN];
+                            invs = scale[2 * kTN];
+                        }
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 const float4 ks = *reinterpret_cast<const float4 *>(scale + q * 32 + e);
-                                const float4 lg = *reinterpret_cast<const float4 *>(scale + kTN + q * 32 + e);
+                                const float4 lg = kFold ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                        : *reinterpret_cast<const float4 *>(scale + kTN + q * 32 + e);
                                 const float2 ff = make_float2(f, f);
                                 float2 x = make_float2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
                                 float2 y = make_float2(__uint_as_float(sr[q][e + 2]), __uint_as_float(sr[q][e + 3]));
-                                x = fma2(mul2(x, make_float2(ks.x, ks.y)), ff, make_float2(lg.x, lg.y));
-                                y = fma2(mul2(y, make_float2(ks.z, ks.w)), ff, make_float2(lg.z, lg.w));
+                                x = mul2(x, make_float2(ks.x, ks.y));
+                                y = mul2(y, make_float2(ks.z, ks.w));
+                                if constexpr (!kFold) {
+                                    x = fma2(x, ff, make_float2(lg.x, lg.y));
+                                    y = fma2(y, ff, make_float2(lg.z, lg.w));
+                                }
                                 sr[q][e] = __float_as_uint(x.x);
                                 sr[q][e + 1] = __float_as_uint(x.y);
                                 sr[q][e + 2] = __float_as_uint(y.x);
                                 sr[q][e + 3] = __float_as_uint(y.y);
+                                // no more than eight columns' loads ahead: the
+                                // registers are full of scores
+                                if (e & 4) asm volatile("" ::: "memory");
                             }
                     }
                     const bool masked = __any_sync(0xffffffffu, base < lo || base + kTN > hi);
@@ -412,7 +438,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         mx[q] = fmaxf(mx[q], __uint_as_float(sr[q][31]));
                     }
                     float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if constexpr (FMT == 0) mn = mn == -INFINITY ? mn : mn * f;
+                    if constexpr (FMT == 0 || kFold) mn = mn == -INFINITY ? mn : fmaf(mn, fs, lgs);
                     if (__any_sync(0xffffffffu, mn > m + 8.f)) {
                         const float n = fmaxf(m, mn);
                         const float c = n == -INFINITY ? 1.f : ex2(m - n);
@@ -434,18 +460,18 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     }
                     const float mu = m == -INFINITY ? 0.f : m;
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    const float2 ff = make_float2(f, f), nm = make_float2(-mu, -mu);
+                    const float2 ff = make_float2(fs, fs), nm = make_float2(lgs - mu, lgs - mu);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t ph[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float2 x = make_float2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
-                            if constexpr (FMT == 0) x = fma2(x, ff, nm);
+                            if constexpr (FMT == 0 || kFold) x = fma2(x, ff, nm);
                             else x = add2(x, nm);
                             x.x = ex2(x.x);
                             x.y = ex2(x.y);
-                            if constexpr (FMT == 0) {
+                            if constexpr (FMT == 0 || kFold) {
                                 sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], x);
                             } else {
                                 float2 iv = *reinterpret_cast<const float2 *>(scale + 2 * kTN + q * 32 + e);
@@ -460,7 +486,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         tmem_st16(ts + 16 * q, ph);
                     }
                     sum[0] = add2(sum[0], sum[1]);
-                    l += sum[0].x + sum[0].y;
+                    l = fmaf(sum[0].x + sum[0].y, invs, l);
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(&bars[B::kP + half]);
@@ -470,7 +496,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 ok = __all_sync(0xffffffffu, wait(B::kO + half, pieces++));
                 if (!ok) break;
                 tc_fence_after();
-                if (FMT == 0 && s_poison[seg & 7] == seg + 1) {
+                if ((FMT == 0 || kFold) && s_poison[seg & 7] == seg + 1) {
                     // values that are not finite at masked positions went in
                     // as zeros: add them to the rows that see them
                     for (int q = 0; q < D / 32; ++q) {
@@ -484,12 +510,18 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                             for (int j = max(base, lo); j < min(base + kTN, hi); ++j) {
                                 const int page = page_of(p.c, u.n, p.by_page(j), p.r.status);
                                 if (page < 0) continue;
-                                const T *v = reinterpret_cast<const T *>(p.c.v) +
-                                             page_at(p.c.vst, page, j % p.c.page_size, u.head) + 32 * q;
+                                const int at = j - p.by_page(j) * p.c.page_size;
+                                if constexpr (FMT == 0) {
+                                    const T *v = reinterpret_cast<const T *>(p.c.v) +
+                                                 page_at(p.c.vst, page, at, u.head) + 32 * q;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float x = (float)v[e];
-                                    if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                                    for (int e = 0; e < 32; ++e) {
+                                        const float x = (float)v[e];
+                                        if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                                    }
+                                } else if (!isfinite(p.c.vs[scale_at(p.c, page, at, u.head)])) {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = 0x7fc00000u;
                                 }
                             }
                         }
@@ -597,9 +629,16 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             fence_async_smem();
             mbar_arrive(&bars[B::kQFull]);
         };
-        for (int it = 0; it < count; ++it) {
+        // a warp that gives up says so at the next barrier of the others, the
+        // last of which is at the end; one that has heard it comes to none
+        bool heard = false;
+        auto together = [&]() {
             ok = help_sync(ok);
-            if (!ok) break;
+            heard = !ok;
+            return ok;
+        };
+        for (int it = 0; it < count && ok; ++it) {
+            if (!together()) break;
             if (it > 0 && u.step == 0) ++seg;
             if (!a.q_box && (it == 0 || u.step == 0)) queries();
             const int base = u.lo + u.step * kTN, left = u.hi - base;  // positions of the step
@@ -642,31 +681,47 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         if (bad) s_poison[seg & 7] = seg + 1;
                         fence_async_smem();
                     }
-                    ok = help_sync(ok);
-                    if (!ok) break;
+                    if (!ok || !together()) break;
                     if (t == 0) mbar_arrive(&bars[B::kFull + b]);
                 }
             } else {
                 constexpr int kChunks = D / 16, kPass = 128 / kChunks, kPasses = kTN / kPass;
                 const int ch = t % kChunks, r0 = t / kChunks;
+                const bool masked = step_masked<kTN>(u, base);
                 for (int kv = 0; kv < 2 && ok; ++kv, ++item) {
                     const int b = item % C::kRing, w = item % C::kRaw;
                     const uint8_t *raw = sm + C::kOffRaw + w * C::kRawSize;
                     ok = __all_sync(0xffffffffu, wait(B::kLand + w, item / C::kRaw));
                     if (!ok) break;
-                    uint4 x[kPasses];
-#pragma unroll
-                    for (int i = 0; i < kPasses; ++i)
-                        x[i] = *reinterpret_cast<const uint4 *>(raw + (r0 + i * kPass) * D + ch * 16);
-                    float ks = 0.f, vs = 1.f;
+                    float ks = 0.f, vs = kFold ? 0.f : 1.f;
                     if (kv == 0 && t < left) {
                         ks = reinterpret_cast<const float *>(raw + C::kRawTile)[t];
                         vs = reinterpret_cast<const float *>(raw + C::kRawTile)[kTN + t];
                     }
-                    mbar_arrive(&bars[B::kTaken + w]);
                     ok = __all_sync(0xffffffffu, wait(B::kEmpty + b, item / C::kRing + 1));
                     if (!ok) break;
-                    if (kv == 0) {
+                    if (kFold && kv == 0) {
+                        // the values' largest scale, and every row's part of it
+                        float vm = isfinite(vs) ? vs : 0.f;
+#pragma unroll
+                        for (int d = 16; d; d >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
+                        if (lane == 0) s_most[warp - 8] = vm;
+                        float *sc = reinterpret_cast<float *>(sm + C::kOffScale) + (it % C::kScales) * 3 * kTN;
+                        sc[t] = ks;
+                        if (!together()) break;
+                        vm = fmaxf(kTLeast, fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3])));
+                        const float part = __fdividef(vs, vm);
+                        const __half2 hi = __float2half2_rn(part);
+                        const __half2 lo = __float2half2_rn(part - __low2float(hi));
+                        s_ratio[t] = make_uint2(*reinterpret_cast<const uint32_t *>(&hi),
+                                                *reinterpret_cast<const uint32_t *>(&lo));
+                        if (t == 0) {
+                            sc[kTN] = __log2f(vm);
+                            sc[2 * kTN] = __fdividef(1.f, vm);
+                        }
+                        if (!together()) break;
+                    }
+                    if (!kFold && kv == 0) {
                         float *sc = reinterpret_cast<float *>(sm + C::kOffScale) + (it % C::kScales) * 3 * kTN;
                         const float v = vs < kTLeast ? kTLeast : vs;
                         sc[t] = ks;
@@ -674,27 +729,45 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         sc[2 * kTN + t] = __fdividef(1.f, v);
                     }
                     uint8_t *tile = sm + C::kOffRing + b * C::kTile;
-#pragma unroll
+#pragma unroll 2
                     for (int i = 0; i < kPasses; ++i) {
                         const int r = r0 + i * kPass;
-                        uint4 e0, e1;
-                        if (r >= left) x[i] = make_uint4(0, 0, 0, 0);  // past the end: anything
-                        widen4<FMT>(x[i].x, e0.x, e0.y);
-                        widen4<FMT>(x[i].y, e0.z, e0.w);
-                        widen4<FMT>(x[i].z, e1.x, e1.y);
-                        widen4<FMT>(x[i].w, e1.z, e1.w);
+                        uint4 x = *reinterpret_cast<const uint4 *>(raw + r * D + ch * 16), e0, e1;
+                        if (r >= left) x = make_uint4(0, 0, 0, 0);  // past the end: anything
+                        widen4<FMT>(x.x, e0.x, e0.y);
+                        widen4<FMT>(x.y, e0.z, e0.w);
+                        widen4<FMT>(x.z, e1.x, e1.y);
+                        widen4<FMT>(x.w, e1.z, e1.w);
+                        if (kFold && kv) {  // times hi + lo, rounded once
+                            const uint2 ra = s_ratio[r];
+                            const __half2 hi = *reinterpret_cast<const __half2 *>(&ra.x);
+                            const __half2 lo = *reinterpret_cast<const __half2 *>(&ra.y);
+                            // a value row without a scale, in a step that some
+                            // rows see a part of: added at the end
+                            const bool out = masked && __hisnan(__low2half(hi));
+                            if (out) s_poison[seg & 7] = seg + 1;
+                            uint32_t *w[8] = {&e0.x, &e0.y, &e0.z, &e0.w, &e1.x, &e1.y, &e1.z, &e1.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const __half2 y = *reinterpret_cast<const __half2 *>(w[e]);
+                                const __half2 z = __hfma2(y, hi, __hmul2(y, lo));
+                                *w[e] = out ? 0u : *reinterpret_cast<const uint32_t *>(&z);
+                            }
+                        }
                         // odd chunks first in the upper columns: the two
                         // column blocks lie on the same banks
                         const bool odd = ch >= kChunks / 2 && D == 128;
                         *reinterpret_cast<uint4 *>(tile + sw128_chunk(r, 2 * ch + (odd ? 1 : 0), kTN)) = odd ? e1 : e0;
                         *reinterpret_cast<uint4 *>(tile + sw128_chunk(r, 2 * ch + (odd ? 0 : 1), kTN)) = odd ? e0 : e1;
                     }
+                    mbar_arrive(&bars[B::kTaken + w]);
                     fence_async_smem();
                     mbar_arrive(&bars[B::kFull + b]);
                 }
             }
             if (it + 1 < count && ++u.step == u.steps) next_unit<kTM, kTN>(p, u);
         }
+        if (!heard) help_sync(ok);
     } else {
         regs_down<kRegRest>();
         if (warp == 12) {

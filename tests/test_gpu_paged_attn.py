@@ -111,6 +111,30 @@ def test_masked_places_never_reach_a_row(route):
 
 
 @pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_rows_without_a_scale(route, dtype, fmt):
+    """8-bit rows stored without a scale (they held a NaN): the rows that see
+    them are NaN, the others exact; scales that differ by 2^40 between tokens,
+    and rows of zeros."""
+    b = Batch([50], [150], heads=2, kv_heads=1, dtype=dtype, fmt=fmt, page=16)
+    tokens = torch.arange(150)
+    pages, slots = b.table[0, tokens // 16].long(), tokens % 16
+    b.vs[pages, 0, slots] *= 2.0 ** ((tokens % 5) * -10).float()
+    b.vs[pages[7:9], 0, slots[7:9]] = 0
+    b.ks[pages[9], 0, slots[9]] = 0
+    ref_o, ref_lse = b.attention()
+    for which in ("vs", "ks"):
+        keep = getattr(b, which).clone()
+        getattr(b, which)[pages[120], 0, slots[120]] = math.nan
+        o, lse = b.run(force_path=route)
+        check(b, o[:20], lse[:20], ref_o[:20], ref_lse[:20], label=f"{which} before")
+        assert o[20:].isnan().all()
+        setattr(b, which, keep)
+    check(b, *b.run(force_path=route), ref_o, ref_lse, label="all")
+
+
+@pytest.mark.parametrize("route", ROUTES)
 def test_strides_layouts_and_outputs(route):
     """q a slice of a fused projection, o a slice of a wider tensor, head-major
     pages; bits equal to the contiguous call's."""
