@@ -131,6 +131,8 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
 size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cache) {
     if (check_dims(dims) != GDR_OK || check_cache(*dims, cache, true) != GDR_OK) return 0;
     AttnProblem p{};
+    p.K = (int)dims->K;
+    p.c.dtype = cache->dtype;
     const size_t a = split_bytes(attn_rows_plan(p), dims->V);
     const size_t b = split_bytes(attn_tiles_plan(p), dims->V);
     return a > b ? a : b;

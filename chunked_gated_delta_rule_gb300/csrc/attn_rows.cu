@@ -8,10 +8,13 @@
 // part in eight of work), and the design goes to keeping loads in flight:
 //   * every warp is a worker of its own with an equal share of the call's
 //     steps (attn_split.cuh), its own ring of kStages steps in shared memory
-//     filled by 16-byte asynchronous copies, and its own running maximum, sum
-//     and accumulators in registers; warps never wait for each other;
-//   * the page of each token of the step after the next load is looked up one
-//     load ahead, so a load never waits for the page table;
+//     and its own running maximum, sum and accumulators in registers; warps
+//     never wait for each other;
+//   * a step of 32 positions comes by TMA as boxes of gcd(page size, 32) slots,
+//     each of one page, a lane a box (16-byte asynchronous copies where pages
+//     are no multiple of 8 slots: 200 instructions a step more);
+//   * the pages of the step after the next load are looked up one load ahead,
+//     so a load never waits for the page table;
 //   * the ring runs across the ends of units (sequences, heads).
 // 8-bit caches stay 8-bit in shared memory.  The values q of a row times its
 // FP32 scale s would not fit 16 bits, so scales are applied in FP32: keys'
@@ -25,6 +28,7 @@
 // products cost nothing beside the loads.
 #include <cuda_fp8.h>
 
+#include "attn_map.cuh"
 #include "attn_split.cuh"
 #include "gdr_launch.cuh"
 #include "tc_common.cuh"
@@ -33,7 +37,6 @@ namespace gdr {
 namespace {
 
 constexpr int kRowsM = 16;
-constexpr int kRowsWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100
@@ -43,22 +46,28 @@ constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100
 template <int FMT, int D>
 struct RowsCfg {
     static constexpr int kES = FMT ? 1 : 2;
-    static constexpr int kBN = FMT ? 32 : 16;        // positions a step
+    static constexpr int kBN = 32;                   // positions a step
     static constexpr int kRow = D * kES;             // bytes of a row
+    static constexpr int kLine = kRow < 128 ? kRow : 128;  // bytes of a row of a box
+    static constexpr int kBlocks = kRow / kLine;     // boxes beside each other
     static constexpr int kKV = kBN * kRow;           // bytes of a step's keys
     static constexpr int kScale = FMT ? kBN * 4 : 0;
-    static constexpr int kStage = 2 * kKV + 2 * kScale;
-    static constexpr int kStages = D == 64 ? 5 : 3;
+    // tiles start on the swizzle's period
+    static constexpr int kStage = (2 * kKV + 2 * kScale + 1023) / 1024 * 1024;
+    static constexpr int kStages = kStage > 12288 ? 2 : kStage > 6144 ? 3 : 4;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kSmem = kRowsWarps * kRing;
+    // warps an SM: a ring each
+    static constexpr int kWarps = kRing > 28672 ? 6 : 8;
+    static constexpr int kSmem = kWarps * kRing + 1024;
 };
 
 // What a step in the ring is.
 struct StepInfo {
-    int n, tile, head, t0, len, kv, base, hi;
-    int first, last, mask;
-    int steps_left;  // of the unit, after this step
+    int base, flags;               // first position; bits below
+    int tile, head, t0, len, kv, hi;
+    int steps_left;                // of the unit, after this step
 };
+constexpr int kFirst = 1, kLast = 2, kMask = 4;  // of the unit; some row sees a part
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
     const int bytes = live ? 16 : 0;
@@ -69,11 +78,6 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool live) {
     const int bytes = live ? 4 : 0;
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -135,40 +139,27 @@ __device__ __forceinline__ uint32_t widen2(uint32_t x) {
     }
 }
 
-// Shared-memory byte offsets of 16-byte chunk `c` of token `t` in a step's
-// keys and values, permuted so that the reads below meet no bank twice.
-// 16 bits: ldmatrix takes one chunk of eight tokens.  8 bits: the keys' reads
-// take four chunks of tokens t, t + 1; the values' reads the same chunks of
-// tokens t, t + 4, t + 8, t + 12.
+// Shared-memory byte offset of 16-byte chunk `c` of token `t` in a step's keys
+// or values: what TMA writes with the 128-byte swizzle (64-byte for rows of 64
+// bytes).  ldmatrix, which takes one chunk of eight tokens, meets no bank
+// twice, nor do the reads of 8-bit rows below.
 template <int FMT, int D>
-__device__ __forceinline__ uint32_t k_off(int t, int c) {
+__device__ __forceinline__ uint32_t kv_off(int t, int c) {
     using C = RowsCfg<FMT, D>;
-    if constexpr (FMT == 0) return t * C::kRow + ((c ^ (t & 7)) << 4);
-    else if constexpr (D >= 128) return t * C::kRow + ((c ^ ((t & 1) << 2)) << 4);
-    else return t * C::kRow + (c << 4);
-}
-template <int FMT, int D>
-__device__ __forceinline__ uint32_t v_off(int t, int c) {
-    using C = RowsCfg<FMT, D>;
-    if constexpr (FMT == 0) {
-        return t * C::kRow + ((c ^ (t & 7)) << 4);
-    } else if constexpr (D == 64) {
-        const int row = (t & ~15) + (t & 3) * 4 + ((t >> 2) & 3);
-        return row * C::kRow + ((c ^ ((t >> 3 & 1) << 1)) << 4);
-    } else if constexpr (D == 128) {
-        return t * C::kRow + ((c ^ ((t >> 2 & 3) << 1)) << 4);
-    } else {
-        return t * C::kRow + ((c ^ ((t >> 2 & 1) | (t >> 3 & 1) << 2)) << 4);
-    }
+    if constexpr (C::kLine == 128)
+        return (c >> 3) * (C::kBN * 128) + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+    else
+        return t * 64 + ((c ^ (t >> 1 & 3)) << 4);
 }
 
-// Token of column n of score tile nt.  8 bits: a thread's four weights of a
-// 16-token product are those of four consecutive tokens, whose value bytes
-// it reads.
+// Token of column n of score tile nt.  8 bits: the keys' reads take chunks 0-3
+// or 4-7 of the tokens of columns n, n + 1 (n even), the values' reads one
+// chunk or two of the tokens of columns n, n + 2, n + 4, n + 6; the order below
+// puts either on different banks.
 template <int FMT>
 __device__ __forceinline__ int token_of(int nt, int n) {
     if constexpr (FMT == 0) return nt * 8 + n;
-    else return (nt >> 1) * 16 + 4 * (n >> 1) + 2 * (nt & 1) + (n & 1);
+    else return nt * 8 + (n & 1 ? ((n - 1) ^ 4) | 1 : n);
 }
 
 // Output column of column n of product tile nt.
@@ -180,11 +171,14 @@ __device__ __forceinline__ int dim_of(int nt, int n) {
 struct RowsArgs {
     AttnProblem p;
     SplitScratch ws;
-    int min_steps;   // least steps a worker
+    int min_steps;       // least steps a worker
+    int box;             // slots of a TMA box (0: asynchronous copies)
+    CUtensorMap tk, tv;  // [page][head][slot][column] of the caches
 };
 
 template <typename T, int FMT, int D>
-__global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
+    k_attn_rows(const __grid_constant__ RowsArgs a) {
     using C = RowsCfg<FMT, D>;
     using TP = typename std::conditional<FMT == 0, T, __half>::type;  // of the products
     constexpr int kNT = C::kBN / 8;        // score tiles
@@ -193,8 +187,9 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
     // weights in two halves, where one rounding of them would be as large as
     // the output's own
     constexpr bool kSplitP = std::is_same<T, TP>::value;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ StepInfo s_info[kRowsWarps][C::kStages];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ StepInfo s_info[C::kWarps][C::kStages];
+    __shared__ uint64_t s_bar[C::kWarps][C::kStages];
     const AttnProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qr = lane >> 2, qc = lane & 3;
@@ -202,8 +197,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
     SplitLine<kRowsM, C::kBN, 0> line;
     line.measure(p);
     const int64_t total = line.total;
-    const int64_t worker = (int64_t)blockIdx.x * kRowsWarps + warp;
-    int64_t nw = (int64_t)gridDim.x * kRowsWarps;
+    const int64_t worker = (int64_t)blockIdx.x * C::kWarps + warp;
+    int64_t nw = (int64_t)gridDim.x * C::kWarps;
     if (nw * a.min_steps > total) nw = quotient(total + a.min_steps - 1, a.min_steps);
     if (lane == 0) a.ws.rec[worker * 2] = make_int4(0, 0, 0, 0);
     if (worker >= nw) return;
@@ -212,66 +207,100 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
     int64_t real;
     Unit u = line.locate(p, begin, real);
 
-    uint8_t *ring = smem + warp * C::kRing;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023)) + warp * C::kRing;
     const uint32_t ring_u = tc::smem_u32(ring);
     StepInfo *info = s_info[warp];
-    const uint8_t *kc = reinterpret_cast<const uint8_t *>(p.c.k);
-    const uint8_t *vc = reinterpret_cast<const uint8_t *>(p.c.v);
+    uint64_t *bars = s_bar[warp];
+    if (lane == 0) {
+        for (int i = 0; i < C::kStages; ++i) tc::mbar_init(&bars[i], a.box ? 1 : 32);
+        tc::mbar_init_fence();
+    }
+    __syncwarp();
 
-    // the page of this lane's token of the step that is loaded next, and the
-    // token's slot; page -1: no such token
-    int page = -1, slot = 0;
+    // what this lane asks of the step that is loaded next: the page-table entry
+    // and slot of its box (boxes first, then keys and values, then columns) or
+    // of its token, a step ahead
+    const int per = a.box ? a.box : 1, boxes = a.box ? C::kBN / a.box : 32;
+    const int bx = lane & (boxes - 1), part = a.box ? lane / boxes : 0;
+    int entry = -1, slot = 0;
+    bool asked = false;
     auto look_up = [&]() {
-        const int pos = u.lo + u.step * C::kBN + lane;
-        page = -1;
-        if (lane < C::kBN && pos < u.hi) {
+        const int pos = u.lo + u.step * C::kBN + bx * per;
+        asked = pos < u.hi;
+        if (asked) {
             const int pi = p.by_page(pos);
             slot = pos - pi * p.c.page_size;
-            page = page_of(p.c, u.n, pi, p.r.status);
+            entry = p.c.table[u.n * p.c.max_pages + pi];
         }
     };
     auto load_step = [&](int s) {
         const uint32_t st = ring_u + s * C::kStage;
-        const int64_t ko = page_at(p.c.kst, page, slot, u.head) * C::kES;
-        const int64_t vo = page_at(p.c.vst, page, slot, u.head) * C::kES;
-        constexpr int kChunks = C::kRow / 16, kPer = 32 / kChunks;  // chunks a row, rows a load
-#pragma unroll
-        for (int i = 0; i < C::kBN / kPer; ++i) {
-            const int t = i * kPer + lane / kChunks, c = lane % kChunks;
-            const int64_t kof = __shfl_sync(0xffffffffu, ko, t);
-            const int64_t vof = __shfl_sync(0xffffffffu, vo, t);
-            const bool live = __shfl_sync(0xffffffffu, page, t) >= 0;
-            cp16(st + k_off<FMT, D>(t, c), live ? kc + kof + c * 16 : kc, live);
-            cp16(st + C::kKV + v_off<FMT, D>(t, c), live ? vc + vof + c * 16 : vc, live);
-        }
-        if constexpr (FMT) {
-            const int64_t so = page >= 0 ? scale_at(p.c, page, slot, u.head) : 0;
-            cp4(st + 2 * C::kKV + lane * 4, p.c.ks + so, page >= 0);
-            cp4(st + 2 * C::kKV + C::kScale + lane * 4, p.c.vs + so, page >= 0);
+        const bool here = asked && (unsigned)entry < (unsigned)p.c.n_pages;
+        if (asked && !here) report(p.r.status, GDR_ERR_INDEX);
+        if (a.box) {
+            // a page past the cache reads as zeros
+            const int page = here ? entry : p.c.n_pages, sl = here ? slot : 0;
+            uint32_t bytes = 2 * C::kKV;
+            if constexpr (FMT) bytes += __popc(__ballot_sync(0xffffffffu, here && part == 0)) * a.box * 8;
+            if (lane == 0) tc::mbar_arrive_expect_tx(&bars[s], bytes);
+            __syncwarp();
+            if (part < 2 * C::kBlocks) {
+                const int kv = part & 1, c = part >> 1;
+                const uint32_t dst = st + kv * C::kKV + c * (C::kBN * 128) + bx * a.box * C::kLine;
+                tma_page(dst, kv ? &a.tv : &a.tk, &bars[s], c * (C::kLine / C::kES), sl, u.head, page);
+                if constexpr (FMT) {
+                    if (here)
+                        tc::bulk_load(ring + s * C::kStage + 2 * C::kKV + kv * C::kScale + bx * a.box * 4,
+                                      (kv ? p.c.vs : p.c.ks) + scale_at(p.c, page, sl, u.head),
+                                      a.box * 4, &bars[s]);
+                }
+            }
+        } else {
+            const uint8_t *kc = reinterpret_cast<const uint8_t *>(p.c.k);
+            const uint8_t *vc = reinterpret_cast<const uint8_t *>(p.c.v);
+            const int64_t ko = here ? page_at(p.c.kst, entry, slot, u.head) * C::kES : 0;
+            const int64_t vo = here ? page_at(p.c.vst, entry, slot, u.head) * C::kES : 0;
+            constexpr int kChunks = C::kRow / 16, kPer = 32 / kChunks;  // chunks a row, rows a load
+#pragma unroll 2
+            for (int i = 0; i < C::kBN / kPer; ++i) {
+                const int t = i * kPer + lane / kChunks, c = lane % kChunks;
+                const int64_t kof = __shfl_sync(0xffffffffu, ko, t);
+                const int64_t vof = __shfl_sync(0xffffffffu, vo, t);
+                const bool live = __shfl_sync(0xffffffffu, here, t);
+                cp16(st + kv_off<FMT, D>(t, c), kc + kof + (live ? c * 16 : 0), live);
+                cp16(st + C::kKV + kv_off<FMT, D>(t, c), vc + vof + (live ? c * 16 : 0), live);
+            }
+            if constexpr (FMT) {
+                const int64_t so = here ? scale_at(p.c, entry, slot, u.head) : 0;
+                cp4(st + 2 * C::kKV + lane * 4, p.c.ks + so, here);
+                cp4(st + 2 * C::kKV + C::kScale + lane * 4, p.c.vs + so, here);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                             tc::smem_u32(&bars[s]))
+                         : "memory");
         }
         if (lane == 0) {
-            StepInfo f;
-            f.n = u.n; f.tile = u.tile; f.head = u.head;
-            f.t0 = u.t0; f.len = u.len; f.kv = u.kv;
+            StepInfo &f = info[s];
             f.base = u.lo + u.step * C::kBN;
-            f.hi = u.hi;
-            f.first = u.step == 0;
             f.steps_left = u.steps - 1 - u.step;
-            f.last = f.steps_left == 0;
-            f.mask = step_masked<C::kBN>(u, f.base);
-            info[s] = f;
+            f.flags = (u.step == 0 ? kFirst : 0) | (f.steps_left == 0 ? kLast : 0) |
+                      (step_masked<C::kBN>(u, f.base) ? kMask : 0);
+            f.tile = u.tile;
+            f.head = u.head;
+            f.t0 = u.t0;
+            f.len = u.len;
+            f.kv = u.kv;
+            f.hi = u.hi;
         }
         if (++u.step == u.steps) next_unit<kRowsM, C::kBN>(p, u);
     };
 
     look_up();
 #pragma unroll 1
-    for (int s = 0; s < C::kStages - 1; ++s) {
-        if (s < count) {
-            load_step(s);
-            if (s + 1 < count) look_up();
-        }
-        cp_commit();
+    for (int s = 0; s < C::kStages && s < count; ++s) {
+        load_step(s);
+        if (s + 1 < count) look_up();
     }
 
     uint32_t qf[kKS][4];
@@ -280,28 +309,28 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
     float f0 = 0.f, f1 = 0.f;  // base-2 score of a unit of product, rows qr and qr + 8
     int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
     bool begun = false, two = false, several = false;
-    int stage = 0, ahead = C::kStages - 1;
+    int stage = 0;
+    uint32_t phase = 0;
 
 #pragma unroll 1
     for (int it = 0; it < count; ++it) {
-        if (it + C::kStages - 1 < count) {
-            load_step(ahead);
-            if (it + C::kStages < count) look_up();
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[stage], phase, p.r.status))) {
+            for (int s = 0; s < C::kStages; ++s)  // its own copies first, for 10 ms
+                tc::mbar_wait(&bars[s], s < stage ? phase ^ 1u : phase, nullptr, 10000000ull);
+            return;
         }
-        cp_commit();
-        cp_wait<C::kStages - 1>();
         __syncwarp();
-        const StepInfo f = info[stage];
+        const int base = info[stage].base, flags = info[stage].flags;
         const uint32_t ks_u = ring_u + stage * C::kStage, vs_u = ks_u + C::kKV;
         uint8_t *st = ring + stage * C::kStage;
 
-        if (it == 0 || f.first) {  // a piece begins: its queries, zero sums
-            begun = f.first;
+        if (it == 0 || (flags & kFirst)) {  // a piece begins: its queries, zero sums
+            const StepInfo f = info[stage];
+            begun = flags & kFirst;
             const int rows = min(kRowsM, f.len * p.G - f.tile * kRowsM);
             two = rows > 8;
             const int ra = f.tile * kRowsM + qr, ia = p.by_G(ra), ib = p.by_G(ra + 8);
-            several = rows > p.G || (qr == 0 && p.by_G(ra + rows - 1) != ia);
-            several = __any_sync(0xffffffffu, several);
+            several = __any_sync(0xffffffffu, rows > p.G || (qr == 0 && p.by_G(ra + rows - 1) != ia));
             lo0 = hi0 = lo1 = hi1 = 0;
             const T *qa = nullptr, *qb = nullptr;
             if (qr < rows) {
@@ -376,11 +405,14 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
         if constexpr (FMT == 0) {
 #pragma unroll
             for (int k = 0; k < kKS; ++k) {
-                uint32_t b[4];  // tokens 0-7 and 8-15, both halves of the columns
-                const int t = (lane & 7) + ((lane >> 4) << 3), c = 2 * k + (lane >> 3 & 1);
-                ldsm4(b, ks_u + k_off<FMT, D>(t, c));
-                mma16<TP>(sc[0], qf[k], b[0], b[1]);
-                mma16<TP>(sc[1], qf[k], b[2], b[3]);
+#pragma unroll
+                for (int h = 0; h < kNT / 2; ++h) {
+                    uint32_t b[4];  // tokens 0-7 and 8-15 of 16, both halves of the columns
+                    const int t = h * 16 + (lane & 7) + ((lane >> 4) << 3), c = 2 * k + (lane >> 3 & 1);
+                    ldsm4(b, ks_u + kv_off<FMT, D>(t, c));
+                    mma16<TP>(sc[2 * h], qf[k], b[0], b[1]);
+                    mma16<TP>(sc[2 * h + 1], qf[k], b[2], b[3]);
+                }
             }
         } else {
 #pragma unroll
@@ -388,7 +420,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt) {
                     const int t = token_of<FMT>(nt, qr);
-                    const uint4 w = *reinterpret_cast<const uint4 *>(st + k_off<FMT, D>(t, g * 4 + qc));
+                    const uint4 w = *reinterpret_cast<const uint4 *>(st + kv_off<FMT, D>(t, g * 4 + qc));
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -402,14 +434,13 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
         for (int nt = 0; nt < kNT; ++nt) {
             float ks2[2] = {1.f, 1.f}, lg[2] = {0.f, 0.f};
             if constexpr (FMT) {
-                const int t = token_of<FMT>(nt, 2 * qc);
-                const float2 kk = *reinterpret_cast<const float2 *>(st + 2 * C::kKV + t * 4);
-                const float2 vv = *reinterpret_cast<const float2 *>(st + 2 * C::kKV + C::kScale + t * 4);
-                ks2[0] = kk.x;
-                ks2[1] = kk.y;
+                const float *sk = reinterpret_cast<const float *>(st + 2 * C::kKV), *sv = sk + C::kBN;
+                const int ta = token_of<FMT>(nt, 2 * qc), tb = token_of<FMT>(nt, 2 * qc + 1);
+                ks2[0] = sk[ta];
+                ks2[1] = sk[tb];
                 // no smaller than 2^-100, so that 1 / s is finite: a scale of
                 // 0 stands for a row of zeros, for which any other will do
-                const float v0 = vv.x < kLeast ? kLeast : vv.x, v1 = vv.y < kLeast ? kLeast : vv.y;
+                const float v0 = sv[ta] < kLeast ? kLeast : sv[ta], v1 = sv[tb] < kLeast ? kLeast : sv[tb];
                 lg[0] = __log2f(v0);
                 lg[1] = __log2f(v1);
                 inv_s[nt][0] = __fdividef(1.f, v0);
@@ -426,12 +457,12 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
                 }
             }
         }
-        if (f.mask) {
+        if (flags & kMask) {
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int pos = f.base + token_of<FMT>(nt, 2 * qc + e);
+                    const int pos = base + token_of<FMT>(nt, 2 * qc + e);
                     const bool see0 = pos >= lo0 && pos < hi0, see1 = pos >= lo1 && pos < hi1;
                     if (!see0) sc[nt][e] = -INFINITY;
                     if (!see1) sc[nt][2 + e] = -INFINITY;
@@ -455,8 +486,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
         }
         if (__any_sync(0xffffffffu, x0 > m0 + 4.f || x1 > m1 + 4.f)) {
             const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-            const float c0 = n0 == -INFINITY ? 1.f : exp2f(m0 - n0);
-            const float c1 = n1 == -INFINITY ? 1.f : exp2f(m1 - n1);
+            const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+            const float c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
             m0 = n0;
             m1 = n1;
             l0 *= c0;
@@ -475,8 +506,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                sc[nt][e] = exp2f(sc[nt][e] - u0);
-                sc[nt][2 + e] = two ? exp2f(sc[nt][2 + e] - u1) : 0.f;
+                sc[nt][e] = ex2(sc[nt][e] - u0);
+                sc[nt][2 + e] = two ? ex2(sc[nt][2 + e] - u1) : 0.f;
                 if constexpr (FMT) {
                     // a row that does not see the token has weight 0 there
                     // and takes nothing of its scale, NaN or not
@@ -497,10 +528,22 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
             }
         }
 
+        // what lies past the last position is anything
+        if ((flags & kMask) && base + C::kBN > info[stage].hi) {
+            const int left = info[stage].hi - base;
+            for (int i = lane; i < C::kBN * (C::kRow / 16); i += 32) {
+                const int t = i / (C::kRow / 16);
+                if (t >= left)
+                    *reinterpret_cast<uint4 *>(st + C::kKV + kv_off<FMT, D>(t, i % (C::kRow / 16))) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+        }
         if constexpr (FMT == 0) {
             // a value that some rows see and others do not must not reach the
             // others as 0 * NaN: where one is not finite it is added by hand
-            if (f.mask && several) {
+            if ((flags & kMask) && several) {
                 constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
                 auto bad = [](uint32_t x) {
                     return (x & kExp) == kExp || (x >> 16 & kExp) == kExp;
@@ -522,12 +565,12 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
                                 w1 = a1;
                             }
                         }
-                        const int pos = f.base + t;
+                        const int pos = base + t;
                         const bool see0 = pos >= lo0 && pos < hi0, see1 = pos >= lo1 && pos < hi1;
 #pragma unroll
                         for (int i = 0; i < kDT; ++i) {
                             const uint32_t x = *reinterpret_cast<uint32_t *>(
-                                st + C::kKV + v_off<FMT, D>(t, i) + qc * 4);
+                                st + C::kKV + kv_off<FMT, D>(t, i) + qc * 4);
                             const float2 v = unpack2<T>(x);
                             if (!isfinite(v.x)) {
                                 if (see0) acc[i][0] += w0 * v.x;
@@ -544,19 +587,21 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
                         T *e = reinterpret_cast<T *>(st + C::kKV) + i;
                         if (!isfinite((float)*e)) *e = (T)0.f;
                     }
+                    tc::fence_async_smem();
                     __syncwarp();
                 }
             }
-            const uint32_t ah[4] = {ph[0][0], ph[0][1], ph[1][0], ph[1][1]};
 #pragma unroll
-            for (int i = 0; i < kDT; i += 2) {
-                uint32_t b[4];  // columns 8 i .. and 8 (i + 1) .., tokens 0-7 and 8-15
-                const int t = lane & 15, c = i + (lane >> 4);
-                ldsm4t(b, vs_u + v_off<FMT, D>(t, c));
-                mma16<TP>(acc[i], ah, b[0], b[1]);
-                mma16<TP>(acc[i + 1], ah, b[2], b[3]);
-                if constexpr (kSplitP) {
-                    const uint32_t al[4] = {pl[0][0], pl[0][1], pl[1][0], pl[1][1]};
+            for (int h = 0; h < kNT / 2; ++h) {
+                const uint32_t ah[4] = {ph[2 * h][0], ph[2 * h][1], ph[2 * h + 1][0], ph[2 * h + 1][1]};
+                const uint32_t al[4] = {pl[2 * h][0], pl[2 * h][1], pl[2 * h + 1][0], pl[2 * h + 1][1]};
+#pragma unroll
+                for (int i = 0; i < kDT; i += 2) {
+                    uint32_t b[4];  // columns 8 i .. and 8 (i + 1) .., tokens 0-7 and 8-15 of 16
+                    const int t = h * 16 + (lane & 15), c = i + (lane >> 4);
+                    ldsm4t(b, vs_u + kv_off<FMT, D>(t, c));
+                    mma16<TP>(acc[i], ah, b[0], b[1]);
+                    mma16<TP>(acc[i + 1], ah, b[2], b[3]);
                     mma16<TP>(acc[i], al, b[0], b[1]);
                     mma16<TP>(acc[i + 1], al, b[2], b[3]);
                 }
@@ -572,17 +617,17 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
                 uint32_t w[4][kB / 4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int t = kk * 16 + 4 * qc + j;
+                    const int t = token_of<FMT>(2 * kk + (j >> 1), 2 * qc + (j & 1));
                     if constexpr (kB == 8) {
                         const uint2 x = *reinterpret_cast<const uint2 *>(
-                            st + C::kKV + v_off<FMT, D>(t, qr >> 1) + (qr & 1) * 8);
+                            st + C::kKV + kv_off<FMT, D>(t, qr >> 1) + (qr & 1) * 8);
                         w[j][0] = x.x;
                         w[j][1] = x.y;
                     } else {
 #pragma unroll
                         for (int h = 0; h < kB / 16; ++h) {
                             const uint4 x = *reinterpret_cast<const uint4 *>(
-                                st + C::kKV + v_off<FMT, D>(t, qr * (kB / 16) + h));
+                                st + C::kKV + kv_off<FMT, D>(t, qr * (kB / 16) + h));
                             w[j][h * 4] = x.x;
                             w[j][h * 4 + 1] = x.y;
                             w[j][h * 4 + 2] = x.z;
@@ -608,7 +653,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
             }
         }
 
-        if (f.last || it + 1 == count) {  // the piece ends
+        if ((flags & kLast) || it + 1 == count) {  // the piece ends
+            const StepInfo f = info[stage];
             float s0 = l0, s1 = l1;
 #pragma unroll
             for (int d = 1; d < 4; d <<= 1) {
@@ -616,7 +662,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
                 s1 += __shfl_xor_sync(0xffffffffu, s1, d);
             }
             const int rows = min(kRowsM, f.len * p.G - f.tile * kRowsM);
-            const bool whole = begun && f.last;
+            const bool whole = begun && (flags & kLast);
             float *po = a.ws.o + ((worker * 2 + (begun ? 1 : 0)) * kRowsM) * D;
             float *pm = a.ws.ml + ((worker * 2 + (begun ? 1 : 0)) * kRowsM) * 2;
 #pragma unroll
@@ -663,15 +709,21 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_attn_rows(const __grid_cons
                     }
                 }
             }
-            if (begun && !f.last && lane == 0) {
+            if (begun && !(flags & kLast) && lane == 0) {
                 a.ws.rec[worker * 2] = make_int4(
                     pieces_from(total, worker, nw, begin + it + 1 + f.steps_left), f.t0, f.len, f.tile);
                 a.ws.rec[worker * 2 + 1].x = f.head;
             }
         }
         __syncwarp();  // the stage is free
-        stage = stage + 1 == C::kStages ? 0 : stage + 1;
-        ahead = ahead + 1 == C::kStages ? 0 : ahead + 1;
+        if (it + C::kStages < count) {
+            load_step(stage);
+            if (it + C::kStages + 1 < count) look_up();
+        }
+        if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
     }
 }
 
@@ -787,11 +839,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
 template <typename T, int FMT, int D>
 cudaError_t launch_rows(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
     using C = RowsCfg<FMT, D>;
-    RowsArgs a{p, ws, 4};
+    RowsArgs a{p, ws, 2};
+    const int box = p.align < C::kBN ? p.align : C::kBN;
+    if (box >= 8 && scales_aligned16(p.c) && page_map(&a.tk, p, p.c.k, p.c.kst, D, box, kPageSwizzled) &&
+        page_map(&a.tv, p, p.c.v, p.c.vst, D, box, kPageSwizzled))
+        a.box = box;
     auto k = k_attn_rows<T, FMT, D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    k<<<ctas, 32 * kRowsWarps, C::kSmem, st>>>(a);
+    k<<<ctas, 32 * C::kWarps, C::kSmem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -820,11 +876,18 @@ cudaError_t join_dim(const AttnProblem &p, const SplitScratch &ws, int workers, 
 
 }  // namespace
 
+// Warps a CTA of the configuration that a call takes.
+static int rows_warps(const AttnProblem &p) {
+    if (cache_quantised(p.c.dtype))
+        return p.K == 64 ? RowsCfg<1, 64>::kWarps : RowsCfg<1, 128>::kWarps;
+    return p.K == 64 ? RowsCfg<0, 64>::kWarps : RowsCfg<0, 128>::kWarps;
+}
+
 SplitPlan attn_rows_plan(const AttnProblem &p) {
     SplitPlan s{};
-    const int64_t g = 2 * (int64_t)device_sms();
-    s.ctas = (int)(p.grid_limit > 0 && p.grid_limit < g ? p.grid_limit : g);
-    s.workers = s.ctas * kRowsWarps;
+    const int g = device_sms();
+    s.ctas = p.grid_limit > 0 && p.grid_limit < g ? p.grid_limit : g;
+    s.workers = s.ctas * rows_warps(p);
     s.rows = kRowsM;
     return s;
 }

@@ -41,10 +41,9 @@
 // GDR_ERR_TIMEOUT, its other roles leave too, and it exits.
 #include <cuda_fp8.h>
 
+#include "attn_map.cuh"
 #include "attn_split.cuh"
 #include "gdr_launch.cuh"
-#include "tc_common.cuh"
-#include "tma_host.cuh"
 
 namespace gdr {
 namespace {
@@ -111,11 +110,6 @@ template <int R>
 __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
     asm("{\n\t.reg .b64 x, y, z, w;\n\t"
@@ -171,15 +165,6 @@ __device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool live) 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar,
-                                            int c0, int c1, int c2, int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
-
 // Barrier of the helping warps: whether all of them are well.
 __device__ __forceinline__ bool help_sync(bool ok) {
     uint32_t r;
@@ -908,10 +893,10 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         if constexpr (FMT == 0) {
 #pragma unroll
                             for (int c = 0; c < D / 64; ++c)
-                                tma_load_4d(sb + dst + c * 16384 + lane * box * 128, map, &bars[bar],
+                                tma_page(sb + dst + c * 16384 + lane * box * 128, map, &bars[bar],
                                             c * 64, sl, head, pg);
                         } else {
-                            tma_load_4d(sb + dst + lane * box * D, map, &bars[bar], 0, sl, head, pg);
+                            tma_page(sb + dst + lane * box * D, map, &bars[bar], 0, sl, head, pg);
                             if (kv == 0 && here) {
                                 const int64_t so = scale_at(p.c, pg, sl, head);
                                 uint8_t *sc = sm + dst + C::kRawTile + lane * box * 4;
@@ -957,33 +942,12 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     }
 }
 
-// Pages of a cache as a tensor of boxes of `box` slots by 128 bytes (16 bits,
-// 64 columns, swizzled) or by a row (8 bits).
-bool page_map(CUtensorMap *map, const AttnProblem &p, const void *base, const int64_t (&st)[3],
-              int D, int box) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    const bool raw = cache_quantised(p.c.dtype);
-    const uint64_t es = raw ? 1 : 2;
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.c.page_size, (cuuint64_t)p.c.H,
-                                (cuuint64_t)p.c.n_pages};
-    const cuuint64_t strides[3] = {st[1] * es, st[2] * es, st[0] * es};
-    const cuuint32_t bx[4] = {raw ? (cuuint32_t)D : 64u, (cuuint32_t)box, 1, 1};
-    const cuuint32_t one[4] = {1, 1, 1, 1};
-    const auto type = raw                       ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                      : p.dtype == GDR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return enc(map, type, 4, const_cast<void *>(base), dims, strides, bx, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE,
-               raw ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename T, int FMT, int D>
 cudaError_t launch_tiles(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
     using C = TilesCfg<FMT, D>;
     TilesArgs a{p, ws, 1, p.align};
-    if (!page_map(&a.tk, p, p.c.k, p.c.kst, D, a.box) || !page_map(&a.tv, p, p.c.v, p.c.vst, D, a.box))
+    if (!page_map(&a.tk, p, p.c.k, p.c.kst, D, a.box, kPagePlain) ||
+        !page_map(&a.tv, p, p.c.v, p.c.vst, D, a.box, kPagePlain))
         return cudaErrorInvalidValue;
     // a half's rows are whole tokens: its queries are one box of 128 / G
     // tokens by G heads
@@ -1037,8 +1001,7 @@ SplitPlan attn_tiles_plan(const AttnProblem &p) {
 
 // Boxes of 8 slots and more, and scales on 16-byte boundaries.
 bool attn_tiles_supported(const AttnProblem &p) {
-    return attn_rows_supported(p) && p.c.page_size % 8 == 0 &&
-           ((reinterpret_cast<uintptr_t>(p.c.ks) | reinterpret_cast<uintptr_t>(p.c.vs)) & 15u) == 0;
+    return attn_rows_supported(p) && p.c.page_size % 8 == 0 && scales_aligned16(p.c);
 }
 
 cudaError_t attn_tiles(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
