@@ -131,9 +131,7 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
 size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cache) {
     if (check_dims(dims) != GDR_OK || check_cache(*dims, cache, true) != GDR_OK) return 0;
     AttnProblem p{};
-    p.K = (int)dims->K;
-    p.c.dtype = cache->dtype;
-    const size_t a = split_bytes(attn_rows_plan(p), dims->V);
+    const size_t a = split_bytes(attn_rows_plan(p, kFewRows), dims->V);
     const size_t b = split_bytes(attn_tiles_plan(p), dims->V);
     return a > b ? a : b;
 }
@@ -188,7 +186,7 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
     p.by_G = divisor((uint32_t)p.G);
     p.by_page = divisor((uint32_t)p.c.page_size);
     for (p.align = 1; p.align < 128 && p.c.page_size % (2 * p.align) == 0;) p.align *= 2;
-    const SplitPlan plan = tiles ? attn_tiles_plan(p) : attn_rows_plan(p);
+    const SplitPlan plan = tiles ? attn_tiles_plan(p) : attn_rows_plan(p, tile_rows(*dims) * p.G);
     const size_t need = split_bytes(plan, p.V);
     void *base = opt ? opt->workspace : nullptr;
     if (base) {

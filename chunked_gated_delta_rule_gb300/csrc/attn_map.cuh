@@ -1,5 +1,5 @@
-// attn_map.cuh -- a paged cache as a TMA tensor: boxes of slots of one page and
-// one head.
+// attn_map.cuh -- what the tensor-core kernels share: a paged cache as a TMA
+// tensor (boxes of slots of one page and one head), and its 8-bit values as FP16.
 #pragma once
 
 #include "attn.cuh"
@@ -56,6 +56,25 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Four 8-bit values (FMT 1: E4M3, 2: integers) as FP16, exact.
+template <int FMT>
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FMT == 1) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(x));
+    } else {
+        const uint32_t u = x ^ 0x80808080u;  // x + 128, the low bits of 1024 + x + 128
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 c = __floats2half2_rn(1152.f, 1152.f);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&a), c);
+        const __half2 z = __hsub2(*reinterpret_cast<const __half2 *>(&b), c);
+        lo = *reinterpret_cast<const uint32_t *>(&y);
+        hi = *reinterpret_cast<const uint32_t *>(&z);
+    }
 }
 
 }  // namespace gdr

@@ -39,8 +39,6 @@
 // The steps of the call are shared out equally over one CTA an SM
 // (attn_split.cuh).  Every wait is bounded: on expiry the CTA records
 // GDR_ERR_TIMEOUT, its other roles leave too, and it exits.
-#include <cuda_fp8.h>
-
 #include "attn_map.cuh"
 #include "attn_split.cuh"
 #include "gdr_launch.cuh"
@@ -177,25 +175,6 @@ __device__ __forceinline__ bool help_sync(bool ok) {
         : "r"((uint32_t)ok)
         : "memory");
     return r != 0;
-}
-
-// Four 8-bit values as FP16 (exact).
-template <int FMT>
-__device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi) {
-    if constexpr (FMT == 1) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> 16), __NV_E4M3);
-        lo = (uint32_t)a.x | (uint32_t)a.y << 16;
-        hi = (uint32_t)b.x | (uint32_t)b.y << 16;
-    } else {
-        const uint32_t u = x ^ 0x80808080u;  // x + 128, the low bits of 1024 + x + 128
-        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 c = __floats2half2_rn(1152.f, 1152.f);
-        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&a), c);
-        const __half2 z = __hsub2(*reinterpret_cast<const __half2 *>(&b), c);
-        lo = *reinterpret_cast<const uint32_t *>(&y);
-        hi = *reinterpret_cast<const uint32_t *>(&z);
-    }
 }
 
 // Instruction descriptor: A and B of type T, A K-major, FP32 sums, M = 128.

@@ -205,7 +205,7 @@ struct SplitPlan {
     int ctas, workers, rows;  // rows: of a tile
 };
 bool attn_rows_supported(const AttnProblem &p);
-SplitPlan attn_rows_plan(const AttnProblem &p);
+SplitPlan attn_rows_plan(const AttnProblem &p, int64_t rows);  // rows: of a key head, expected
 cudaError_t attn_rows(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
                       cudaStream_t st);
 // Many rows: tiles of 256 on tcgen05, for the same types, widths and strides
