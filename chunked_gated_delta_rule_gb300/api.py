@@ -75,6 +75,8 @@ def load_library():
     """Open ``libgdr.so``.  Raises if it has not been built: there is no
     fallback implementation."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -422,52 +424,100 @@ _CACHE_DTYPES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16, torch.float16
                  torch.float8_e4m3fn: GDR_E4M3, torch.int8: GDR_I8}
 
 
-def _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, dev):
+def _on(index, **tensors):
+    """Every given tensor lies on CUDA device ``index``, contiguous, and has the
+    dtype it is paired with (None: any)."""
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, index):
     """The C struct of a paged cache; sizes, types and devices checked."""
-    fmt = _CACHE_DTYPES.get(k_cache.dtype)
-    if fmt is None or v_cache.dtype != k_cache.dtype:
+    dtype = k_cache.dtype
+    fmt = _CACHE_DTYPES.get(dtype)
+    if fmt is None or v_cache.dtype is not dtype:
         raise TypeError("k_cache and v_cache must share a dtype: float32, bfloat16, float16, "
-                        f"float8_e4m3fn or int8, got {k_cache.dtype} and {v_cache.dtype}")
-    if k_cache.dim() != 4 or v_cache.dim() != 4 or k_cache.shape[:3] != v_cache.shape[:3]:
+                        f"float8_e4m3fn or int8, got {dtype} and {v_cache.dtype}")
+    if k_cache.dim() != 4 or v_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [pages, page size, heads, K] and [.., V]")
     P, page, H, _ = k_cache.shape
-    strides = []
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-        if t.is_contiguous():
-            strides.append((0, 0, 0))
-        elif t.stride(-1) == 1 and min(t.stride()) > 0:
-            strides.append(t.stride()[:3])
-        else:
-            raise ValueError(f"{name} needs a contiguous last dimension")
-    if (fmt >= GDR_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale belong to an 8-bit cache, both of them")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _check(name, t, torch.float32, dev)
-        if t is not None and t.shape != (P, H, page):
-            raise ValueError(f"{name} must be [pages, heads, page size]")
-    _check("page_table", page_table, torch.int32, dev)
-    _check("kv_lens", kv_lens, torch.int32, dev)
-    if page_table.dim() != 2 or page_table.shape[0] != nseq or kv_lens.shape != (nseq,):
+    if (P, page, H) != v_cache.shape[:3]:
+        raise ValueError("k_cache and v_cache must share pages, page size and heads")
+    if k_cache.get_device() != index or v_cache.get_device() != index:
+        raise ValueError(f"k_cache and v_cache must be on cuda:{index}")
+    if k_scale is None:
+        if fmt >= GDR_E4M3 or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to an 8-bit cache, both of them")
+        ks = vs = None
+    else:
+        if fmt < GDR_E4M3 or v_scale is None:
+            raise ValueError("k_scale and v_scale belong to an 8-bit cache, both of them")
+        _on(index, k_scale=(k_scale, torch.float32), v_scale=(v_scale, torch.float32))
+        if k_scale.shape != (P, H, page) or v_scale.shape != (P, H, page):
+            raise ValueError("k_scale and v_scale must be [pages, heads, page size]")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    if page_table.dtype is not torch.int32 or kv_lens.dtype is not torch.int32:
+        raise TypeError("page_table and kv_lens must be int32")
+    if page_table.get_device() != index or kv_lens.get_device() != index or \
+            not page_table.is_contiguous() or not kv_lens.is_contiguous():
+        raise ValueError(f"page_table and kv_lens must be contiguous and on cuda:{index}")
+    if page_table.dim() != 2 or page_table.size(0) != nseq or kv_lens.shape != (nseq,):
         raise ValueError("page_table must be [sequences, pages a sequence], kv_lens [sequences]")
-    c = gdr_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(),
-                        None if k_scale is None else k_scale.data_ptr(),
-                        None if v_scale is None else v_scale.data_ptr(),
-                        page_table.data_ptr(), kv_lens.data_ptr(), P, page, page_table.shape[1],
-                        H, fmt)
-    c.k_stride[:], c.v_stride[:] = strides
+    c = gdr_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, page_table.data_ptr(),
+                        kv_lens.data_ptr(), P, page, page_table.size(1), H, fmt)
+    if not k_cache.is_contiguous():
+        c.k_stride[:] = _page_strides(k_cache)
+    if not v_cache.is_contiguous():
+        c.v_stride[:] = _page_strides(v_cache)
     return c
 
 
-def _paged_call(fn, dev, stream, *args):
+def _page_strides(t):
+    if t.stride(-1) != 1 or min(t.stride()) < 1:
+        raise ValueError("k_cache and v_cache need a contiguous last dimension")
+    return t.stride()[:3]
+
+
+def _paged_dims(B, T, H, K, V, cu_seqlens, dtype, index, max_seqlen=None):
+    """gdr_dims of a call on a paged cache, and its number of sequences."""
+    if cu_seqlens is None:
+        n, flags = 0, 0
+    else:
+        if cu_seqlens.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"cu_seqlens must be int32 or int64, got {cu_seqlens.dtype}")
+        _on(index, cu_seqlens=(cu_seqlens, None))
+        n = cu_seqlens.numel() - 1
+        flags = GDR_SEQLENS_I64 if cu_seqlens.dtype == torch.int64 else 0
+    return gdr_dims(B, T, H, K, V, n, _dtype_code(dtype), flags,
+                    0 if max_seqlen is None else int(max_seqlen)), B if cu_seqlens is None else n
+
+
+def _set_strides(field, t):
+    if not t.is_contiguous():
+        field[:] = _row_strides(t)
+
+
+def _paged_call(fn, index, stream, *args):
     """Calls a library function on ``stream`` (default: the current one)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        rc = fn(*args, ctypes.c_void_p(stream.cuda_stream))
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
     if rc != 0:
         raise GdrError(rc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def gdr_cache_write(k, v, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
@@ -477,24 +527,24 @@ def gdr_cache_write(k, v, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None
     ``kv_lens`` [N] counts each sequence's tokens including the new ones: token
     i of the L new ones goes to position ``kv_lens[n] - L + i``, slot ``position
     % page size`` of page ``page_table[n, position // page size]``.  A cache of
-    q's dtype holds the rows as they are; a float8_e4m3fn or int8 cache holds
+    k's dtype holds the rows as they are; a float8_e4m3fn or int8 cache holds
     them quantised, with a scale for each (token, head) row in ``k_scale`` and
     ``v_scale`` [P, H, page size] (float32)."""
     lib = load_library()
-    dev = k.device
-    if dev.type != "cuda":
+    index = k.get_device()
+    if index < 0:
         raise ValueError("gdr_cache_write takes CUDA tensors")
-    _check("v", v, k.dtype, dev, strided=True)
-    _check_cu(cu_seqlens, dev)
-    dims = _dims_of(k, v, cu_seqlens, k=k)
-    dims.q_stride[:] = (0, 0)
+    if v.get_device() != index or v.dtype != k.dtype:
+        raise ValueError("k and v must share a device and a dtype")
     if v.shape[:-1] != k.shape[:-1] or k_cache.shape[2:] != k.shape[2:] or \
             v_cache.shape[-1] != v.shape[-1]:
         raise ValueError("k, v and the caches must agree in tokens, heads and widths")
-    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale,
-                      dims.N if cu_seqlens is not None else dims.B, dev)
-    _paged_call(lib.gdr_cache_write, dev, stream, ctypes.byref(dims), ctypes.byref(cache), _ptr(k),
-                _ptr(v), _ptr(cu_seqlens), _ptr(status))
+    dims, nseq = _paged_dims(*k.shape, v.shape[3], cu_seqlens, k.dtype, index)
+    _set_strides(dims.k_stride, k)
+    _set_strides(dims.v_stride, v)
+    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, index)
+    _paged_call(lib.gdr_cache_write, index, stream, dims, cache, k.data_ptr(), v.data_ptr(),
+                _addr(cu_seqlens), _addr(status))
 
 
 def gdr_cache_read(k_cache, v_cache, page_table, kv_lens, T, cu_seqlens=None, *, k_scale=None,
@@ -505,10 +555,9 @@ def gdr_cache_read(k_cache, v_cache, page_table, kv_lens, T, cu_seqlens=None, *,
     the cache's own unless that is an 8-bit format (then bfloat16 by default);
     ``k`` and ``v`` may be given to write into."""
     lib = load_library()
-    dev = k_cache.device
-    if dev.type != "cuda":
+    index = k_cache.get_device()
+    if index < 0:
         raise ValueError("gdr_cache_read takes CUDA tensors")
-    _check_cu(cu_seqlens, dev)
     if k_cache.dim() != 4 or v_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [pages, page size, heads, K] and [.., V]")
     B = kv_lens.numel() if cu_seqlens is None else 1
@@ -516,18 +565,19 @@ def gdr_cache_read(k_cache, v_cache, page_table, kv_lens, T, cu_seqlens=None, *,
         dtype = k.dtype if k is not None else (
             k_cache.dtype if k_cache.element_size() > 1 else torch.bfloat16)
     H, K, V = k_cache.shape[2], k_cache.shape[3], v_cache.shape[3]
-    k = torch.empty(B, T, H, K, dtype=dtype, device=dev) if k is None else k
-    v = torch.empty(B, T, H, V, dtype=dtype, device=dev) if v is None else v
-    for name, t, shape in (("k", k, (B, T, H, K)), ("v", v, (B, T, H, V))):
-        _check(name, t, dtype, dev, strided=True)
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}")
-    dims = _dims_of(k, v, cu_seqlens, k=k)
-    dims.q_stride[:] = (0, 0)
-    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale,
-                      dims.N if cu_seqlens is not None else dims.B, dev)
-    _paged_call(lib.gdr_cache_read, dev, stream, ctypes.byref(dims), ctypes.byref(cache), _ptr(k),
-                _ptr(v), _ptr(cu_seqlens), _ptr(status))
+    for name, t, D in (("k", k, K), ("v", v, V)):
+        if t is not None and (t.get_device() != index or t.dtype != dtype or
+                              t.shape != (B, T, H, D)):
+            raise ValueError(f"{name} must be {[B, T, H, D]}, {dtype}, on cuda:{index}")
+    k = kv_lens.new_empty((B, T, H, K), dtype=dtype) if k is None else k
+    v = (torch.empty_like(k) if V == K and k.is_contiguous()
+         else kv_lens.new_empty((B, T, H, V), dtype=dtype)) if v is None else v
+    dims, nseq = _paged_dims(B, T, H, K, V, cu_seqlens, dtype, index)
+    _set_strides(dims.k_stride, k)
+    _set_strides(dims.v_stride, v)
+    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, index)
+    _paged_call(lib.gdr_cache_read, index, stream, dims, cache, k.data_ptr(), v.data_ptr(),
+                _addr(cu_seqlens), _addr(status))
     return k, v
 
 
@@ -546,45 +596,42 @@ def gdr_paged_attn(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
     caller knows it (a planning hint).  Work is enqueued on ``stream`` (default:
     the current one) and not synchronised."""
     lib = load_library()
-    dev = q.device
-    if dev.type != "cuda":
+    index = q.get_device()
+    if index < 0:
         raise ValueError("gdr_paged_attn takes CUDA tensors")
-    _check_cu(cu_seqlens, dev)
-    if q.dim() != 4 or k_cache.dim() != 4 or v_cache.dim() != 4 or q.shape[-1] != k_cache.shape[-1]:
+    if q.dim() != 4 or k_cache.dim() != 4 or v_cache.dim() != 4 or q.shape[3] != k_cache.shape[3]:
         raise ValueError("q must be [B, T, heads, K], the caches [pages, page size, heads, K or V]")
-    shape = (*q.shape[:3], v_cache.shape[3])
+    B, T, H, K = q.shape
+    V = v_cache.shape[3]
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=dev)
-    elif o.shape != shape:
-        raise ValueError("o must be [B, T, heads, V]")
+        o = torch.empty_like(q) if V == K and q.is_contiguous() else q.new_empty((B, T, H, V))
+    elif o.shape != (B, T, H, V) or o.dtype != q.dtype or o.get_device() != index:
+        raise ValueError(f"o must be {[B, T, H, V]}, {q.dtype}, on cuda:{index}")
     if lse is None:
-        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
-    elif lse.shape != shape[:3]:
-        raise ValueError("lse must be [B, T, heads]")
-    _check("o", o, q.dtype, dev, strided=True)
-    _check("lse", lse, torch.float32, dev)
-    dims = make_dims(*q.shape[:3], q.shape[3], shape[3],
-                     0 if cu_seqlens is None else cu_seqlens.numel() - 1, _dtype_code(q.dtype),
-                     GDR_SEQLENS_I64 if cu_seqlens is not None and cu_seqlens.dtype == torch.int64
-                     else 0, 0 if max_seqlen is None else int(max_seqlen))
-    dims.q_stride[:], dims.o_stride[:] = _row_strides(q), _row_strides(o)
-    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale,
-                      dims.N if cu_seqlens is not None else dims.B, dev)
+        lse = q.new_empty((B, T, H), dtype=torch.float32)
+    else:
+        _on(index, lse=(lse, torch.float32))
+        if lse.shape != (B, T, H):
+            raise ValueError("lse must be [B, T, heads]")
+    dims, nseq = _paged_dims(B, T, H, K, V, cu_seqlens, q.dtype, index, max_seqlen)
+    _set_strides(dims.q_stride, q)
+    _set_strides(dims.o_stride, o)
+    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, index)
     if cache.dtype < GDR_E4M3 and k_cache.dtype != q.dtype:
         raise TypeError(f"the caches must be {q.dtype} or an 8-bit format, got {k_cache.dtype}")
-    opt = gdr_options(float(scale), int(force_path), 0,
-                      None if workspace is None else workspace.data_ptr(),
-                      0 if workspace is None else workspace.numel() * workspace.element_size(),
-                      None if status is None else status.data_ptr())
-    opt.grid_limit = int(grid_limit)
-    if timer is not None:
-        opt.events = ctypes.cast(timer._handles, ctypes.c_void_p)
-        opt.max_launches = timer.max
-        opt.launch_ids = ctypes.cast(timer._ids, ctypes.c_void_p)
-        opt.n_launches = ctypes.cast(ctypes.pointer(timer._count), ctypes.c_void_p)
-    _paged_call(lib.gdr_paged_attn, dev, stream, ctypes.byref(dims), ctypes.byref(cache), _ptr(q),
-                _ptr(cu_seqlens), _ptr(o), _ptr(lse), int(bool(causal)), int(window),
-                ctypes.byref(opt))
+    opt = None
+    if scale or force_path or grid_limit or workspace is not None or status is not None or timer:
+        opt = gdr_options(float(scale), int(force_path), 0, _addr(workspace),
+                          0 if workspace is None else workspace.numel() * workspace.element_size(),
+                          _addr(status))
+        opt.grid_limit = int(grid_limit)
+        if timer is not None:
+            opt.events = ctypes.cast(timer._handles, ctypes.c_void_p)
+            opt.max_launches = timer.max
+            opt.launch_ids = ctypes.cast(timer._ids, ctypes.c_void_p)
+            opt.n_launches = ctypes.cast(ctypes.pointer(timer._count), ctypes.c_void_p)
+    _paged_call(lib.gdr_paged_attn, index, stream, dims, cache, q.data_ptr(), _addr(cu_seqlens),
+                o.data_ptr(), lse.data_ptr(), 1 if causal else 0, int(window), opt)
     return o, lse
 
 

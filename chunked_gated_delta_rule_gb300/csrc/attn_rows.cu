@@ -803,6 +803,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
     if (pieces <= kW) {
         for (int r = (blockIdx.y * kW + warp) * kR; r < rows; r += gridDim.y * kW * kR) {
             Joined<kV> a[kR];
+#pragma unroll 4
             for (int j = 0; j < pieces; ++j) {
                 float oj[kR][kV], ml[kR][2];
 #pragma unroll
@@ -823,7 +824,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
     }
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         Joined<kV> a;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = warp; j < pieces; j += kW) {
             const int64_t at = slot(j, r);
             float oj[kV];
@@ -858,7 +859,10 @@ cudaError_t launch_rows(const AttnProblem &p, const SplitScratch &ws, int ctas, 
         page_map(&a.tv, p, p.c.v, p.c.vst, D, box, kPageSwizzled))
         a.box = box;
     auto k = k_attn_rows<T, FMT, D, NR>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_a_device(done, [&] {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
     if (e != cudaSuccess) return e;
     k<<<ctas, 32 * C::kWarps, C::kSmem, st>>>(a);
     return cudaGetLastError();
@@ -880,10 +884,10 @@ cudaError_t launch_dim(const AttnProblem &p, const SplitScratch &ws, const Split
 
 template <typename T, int M>
 cudaError_t join_dim(const AttnProblem &p, const SplitScratch &ws, int workers, cudaStream_t st) {
-    // many pieces a unit: a CTA for each row of it; few: the rows of a 16-row
-    // tile, or 32 of a larger one, share one
+    // many pieces a unit: a CTA for each row of it; few: 8 rows of a small
+    // tile (a warp a row), or 32 of a larger one, share one
     const bool many = workers > 8 * p.r.N * p.c.H;
-    const int y = M <= kRowsMost ? (many ? (p.G < M ? p.G : M) : 1) : (many ? 64 : M / 32);
+    const int y = M <= kRowsMost ? (many ? (p.G < M ? p.G : M) : M / 8) : (many ? 64 : M / 32);
     const dim3 g((unsigned)workers, (unsigned)y);
     if (p.V == 64) return launch_pdl(k_attn_join<T, M, 64>, g, dim3(kJoinThreads), 0, st, p, ws);
     return launch_pdl(k_attn_join<T, M, 128>, g, dim3(kJoinThreads), 0, st, p, ws);

@@ -944,12 +944,15 @@ cudaError_t launch_tiles(const AttnProblem &p, const SplitScratch &ws, int ctas,
             a.q_box = 128 / p.G;
     }
     auto k = k_attn_tiles<T, FMT, D>;
-    cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, k);
-    if (e != cudaSuccess) return e;
-    // the split of the registers draws on what the launch holds
-    if (at.numRegs * 4 < 2 * kRegSoftmax + kRegHelp + kRegRest) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = once_a_device(done, [&] {
+        cudaFuncAttributes at;
+        const cudaError_t x = cudaFuncGetAttributes(&at, k);
+        if (x != cudaSuccess) return x;
+        // the split of the registers draws on what the launch holds
+        if (at.numRegs * 4 < 2 * kRegSoftmax + kRegHelp + kRegRest) return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+    });
     if (e != cudaSuccess) return e;
     k<<<ctas, kTThreads, C::kBytes, st>>>(a);
     return cudaGetLastError();

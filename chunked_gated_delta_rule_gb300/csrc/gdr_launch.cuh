@@ -5,6 +5,8 @@
 // the kernels' sources untouched.
 #pragma once
 
+#include <atomic>
+
 #include "gdr_internal.cuh"
 
 namespace gdr {
@@ -216,6 +218,20 @@ cudaError_t attn_tiles(const AttnProblem &p, const SplitScratch &ws, const Split
                        cudaStream_t st);
 cudaError_t attn_join(const AttnProblem &p, const SplitScratch &ws, const SplitPlan &s,
                       cudaStream_t st);
+
+// Runs `set` (which sets a kernel's attributes) the first time that it is
+// called on the current device; `done` is the caller's, one bit a device.
+template <typename F>
+cudaError_t once_a_device(std::atomic<uint64_t> &done, F set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Device scratch from the library's pool, ordered on the stream.
 cudaError_t scratch_alloc(void **ptr, size_t bytes, cudaStream_t st);

@@ -120,7 +120,7 @@ def test_binding_checks_caches():
     c = torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16)
     table, lens = torch.zeros(1, 3, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     good = dict(k_cache=c, v_cache=c, page_table=table, kv_lens=lens, k_scale=None, v_scale=None,
-                nseq=1, dev=c.device)
+                nseq=1, index=-1)
     api._cache_of(**good)
     scale = torch.zeros(3, 2, 16)
     for bad, err in ((dict(v_cache=c.float()), TypeError), (dict(k_cache=c.double()), TypeError),
