@@ -95,7 +95,7 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t split_bytes(const SplitPlan &s, int64_t V) {
     const size_t rows = (size_t)s.workers * 2 * s.rows;
     return align256(rows * V * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
-           align256((size_t)s.workers * 2 * sizeof(int4));
+           align256((size_t)s.workers * sizeof(int4));
 }
 
 SplitScratch carve_split(void *base, const SplitPlan &s, int64_t V) {

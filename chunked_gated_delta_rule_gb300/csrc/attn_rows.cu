@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
     const int64_t worker = (int64_t)blockIdx.x * C::kWarps + warp;
     int64_t nw = (int64_t)gridDim.x * C::kWarps;
     if (nw * a.min_steps > total) nw = quotient(total + a.min_steps - 1, a.min_steps);
-    if (lane == 0) a.ws.rec[worker * 2] = make_int4(0, 0, 0, 0);
+    if (lane == 0) a.ws.rec[worker] = make_int4(0, 0, 0, 0);
     if (worker >= nw) return;
     // where the share ends, then where it begins
     const int64_t end = share_begin(total, worker + 1, nw);
@@ -730,11 +730,10 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
                     }
                 }
             }
-            if (begun && !(flags & kLast) && lane == 0) {
-                a.ws.rec[worker * 2] = make_int4(
-                    pieces_from(total, worker, nw, end + fi->steps_left), fi->t0, fi->len, fi->tile);
-                a.ws.rec[worker * 2 + 1].x = fi->head;
-            }
+            if (begun && !(flags & kLast) && lane == 0)
+                a.ws.rec[worker] = make_int4(
+                    fi->head << 16 | pieces_from(total, worker, nw, end + fi->steps_left), fi->t0,
+                    fi->len, fi->tile);
         }
         next_tile();
     }
@@ -743,23 +742,12 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
 // ---- joining split units --------------------------------------------------
 // The unit that worker w begins and others go on with, row by row:
 //   m = max_j m_j,  o = sum_j 2^(m_j - m) O_j / sum_j 2^(m_j - m) l_j
-// over its pieces j, in an order that only their number fixes: up to kW
-// pieces by one warp, R rows at a time; more by all warps of the CTA, each
-// taking every kW-th piece of one row.
+// over its pieces j, in an order that only their number fixes: up to kBatch
+// pieces by one warp a row; more by all warps of the CTA, each taking every
+// kW-th piece of one row.  What a CTA waits for is loads, one behind the other
+// (15 us a CTA when pieces came one by one), so a batch of pieces is asked for
+// at once.
 constexpr int kJoinThreads = 256;
-
-template <int V>
-struct Joined {
-    float m = -INFINITY, l = 0.f, o[V] = {};
-    __device__ __forceinline__ void add(float mj, float lj, const float (&oj)[V]) {
-        const float n = fmaxf(m, mj), nu = n == -INFINITY ? 0.f : n;
-        const float c = exp2f(m - nu), cj = exp2f(mj - nu);
-        m = n;
-        l = l * c + lj * cj;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = o[i] * c + oj[i] * cj;
-    }
-};
 
 // A lane's V = D / 32 consecutive columns.
 template <int V>
@@ -773,21 +761,62 @@ __device__ __forceinline__ void load_cols(float (&o)[V], const float *p) {
     }
 }
 
+constexpr int kBatch = 8;
+template <int V>
+struct Joined {
+    float m = -INFINITY, l = 0.f, o[V] = {};
+    // Pieces first, first + stride, ... below `pieces`, a batch of them; at(j)
+    // gives piece j's row of the scratch.
+    template <typename F>
+    __device__ __forceinline__ void add(const SplitScratch &ws, int D, int lane, int first, int stride,
+                                        int pieces, F at) {
+        float oj[kBatch][V], mj[kBatch], lj[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int j = first + b * stride;
+            mj[b] = -INFINITY;
+            lj[b] = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) oj[b][i] = 0.f;
+            if (j < pieces) {
+                const int64_t r = at(j);
+                const float2 ml = *reinterpret_cast<const float2 *>(ws.ml + r * 2);
+                mj[b] = ml.x;
+                lj[b] = ml.y;
+                load_cols<V>(oj[b], ws.o + r * D + lane * V);
+            }
+        }
+        float n = m;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) n = fmaxf(n, mj[b]);
+        const float nu = n == -INFINITY ? 0.f : n, c = ex2(m - nu);
+        m = n;
+        l *= c;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= c;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const float cj = ex2(mj[b] - nu);
+            l += lj[b] * cj;
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] += oj[b][i] * cj;
+        }
+    }
+};
+
 template <typename T, int M, int D>
-__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnProblem p,
-                                                            SplitScratch ws) {
-    constexpr int kW = kJoinThreads / 32, kV = D / 32, kR = M > kRowsMost ? 4 : 1;
+__global__ void __launch_bounds__(kJoinThreads, 4) k_attn_join(const __grid_constant__ AttnProblem p,
+                                                               SplitScratch ws) {
+    constexpr int kW = kJoinThreads / 32, kV = D / 32;
     __shared__ __align__(16) float s_o[kW][D];
-    __shared__ float s_ml[kW][2];
+    __shared__ __align__(8) float s_ml[kW][2];
     pdl_wait();
     const int64_t w = blockIdx.x;
-    const int4 rec = ws.rec[w * 2];
-    const int pieces = rec.x;
+    const int4 rec = ws.rec[w];
+    const int pieces = rec.x & 0xffff, head = (int)((unsigned)rec.x >> 16);
     if (pieces == 0) return;
-    const int head = ws.rec[w * 2 + 1].x, t0 = rec.y, tile = rec.w;
-    const int rows = min(M, rec.z * p.G - tile * M);
+    const int t0 = rec.y, tile = rec.w, rows = min(M, rec.z * p.G - tile * M);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto slot = [&](int j, int r) { return ((w + j) * 2 + (j == 0 ? 1 : 0)) * M + r; };
     auto write = [&](const Joined<kV> &a, int r) {
         const bool empty = a.l == 0.f;
         const float inv = empty ? 0.f : 1.f / a.l;
@@ -800,37 +829,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
             p.lse[(int64_t)(t0 + i) * p.Hq + hq] =
                 empty ? -INFINITY : ((a.m == -INFINITY ? 0.f : a.m) + log2f(a.l)) * kLn2;
     };
-    if (pieces <= kW) {
-        for (int r = (blockIdx.y * kW + warp) * kR; r < rows; r += gridDim.y * kW * kR) {
-            Joined<kV> a[kR];
-#pragma unroll 4
-            for (int j = 0; j < pieces; ++j) {
-                float oj[kR][kV], ml[kR][2];
-#pragma unroll
-                for (int e = 0; e < kR; ++e) {
-                    const int64_t at = slot(j, min(r + e, rows - 1));
-                    load_cols<kV>(oj[e], ws.o + at * D + lane * kV);
-                    ml[e][0] = ws.ml[at * 2];
-                    ml[e][1] = ws.ml[at * 2 + 1];
-                }
-#pragma unroll
-                for (int e = 0; e < kR; ++e) a[e].add(ml[e][0], ml[e][1], oj[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < kR; ++e)
-                if (r + e < rows) write(a[e], r + e);
+    auto piece = [&](int r) {
+        return [=](int j) { return ((w + j) * 2 + (j == 0 ? 1 : 0)) * M + r; };
+    };
+    if (pieces <= kBatch) {
+        for (int r = blockIdx.y * kW + warp; r < rows; r += gridDim.y * kW) {
+            Joined<kV> a;
+            a.add(ws, D, lane, 0, 1, pieces, piece(r));
+            write(a, r);
         }
         return;
     }
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         Joined<kV> a;
-#pragma unroll 8
-        for (int j = warp; j < pieces; j += kW) {
-            const int64_t at = slot(j, r);
-            float oj[kV];
-            load_cols<kV>(oj, ws.o + at * D + lane * kV);
-            a.add(ws.ml[at * 2], ws.ml[at * 2 + 1], oj);
-        }
+        for (int j = warp; j < pieces; j += kW * kBatch) a.add(ws, D, lane, j, kW, pieces, piece(r));
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kV; ++i) s_o[warp][lane * kV + i] = a.o[i];
@@ -840,13 +852,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
         }
         __syncthreads();
         if (warp) continue;
-        a = Joined<kV>();
-        for (int j = 0; j < kW; ++j) {
-            float oj[kV];
-            load_cols<kV>(oj, &s_o[j][lane * kV]);
-            a.add(s_ml[j][0], s_ml[j][1], oj);
-        }
-        write(a, r);
+        Joined<kV> all;
+        all.add(SplitScratch{&s_o[0][0], &s_ml[0][0], nullptr}, D, lane, 0, 1, kW,
+                [](int j) { return (int64_t)j; });
+        write(all, r);
     }
 }
 
@@ -884,10 +893,9 @@ cudaError_t launch_dim(const AttnProblem &p, const SplitScratch &ws, const Split
 
 template <typename T, int M>
 cudaError_t join_dim(const AttnProblem &p, const SplitScratch &ws, int workers, cudaStream_t st) {
-    // many pieces a unit: a CTA for each row of it; few: 8 rows of a small
-    // tile (a warp a row), or 32 of a larger one, share one
+    // many pieces a unit: a CTA for each row of it; few: 8 rows share one
     const bool many = workers > 8 * p.r.N * p.c.H;
-    const int y = M <= kRowsMost ? (many ? (p.G < M ? p.G : M) : M / 8) : (many ? 64 : M / 32);
+    const int y = !many ? M / 8 : M <= kRowsMost ? (p.G < M ? p.G : M) : 64;
     const dim3 g((unsigned)workers, (unsigned)y);
     if (p.V == 64) return launch_pdl(k_attn_join<T, M, 64>, g, dim3(kJoinThreads), 0, st, p, ws);
     return launch_pdl(k_attn_join<T, M, 128>, g, dim3(kJoinThreads), 0, st, p, ws);

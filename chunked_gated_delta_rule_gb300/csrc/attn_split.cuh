@@ -27,8 +27,8 @@ namespace gdr {
 struct SplitScratch {
     float *o;      // [workers][2][M][V] sums of e^{s - m} v
     float *ml;     // [workers][2][M][2] m (base 2) and sum of e^{s - m}
-    // [workers][2] the unit that the worker begins and others go on with:
-    // {pieces (0: there is none), first token, new tokens, tile}, {key head}
+    // [workers] the unit that the worker begins and others go on with: key head
+    // << 16 | pieces (0: there is none), first token, new tokens, tile
     int4 *rec;
 };
 
@@ -119,10 +119,10 @@ struct SplitLine {
     int64_t total, units;      // length, units of the call
     int64_t line0, units0;     // those of the lanes before this one
     int64_t per;
+    static constexpr int kFew = 16;  // more tiles of a sequence are shared out among the lanes
 
     __device__ __forceinline__ void measure(const AttnProblem &p) {
         const int lane = threadIdx.x & 31;
-        constexpr int kFew = 16;  // more tiles are shared out among the lanes
         per = (p.r.N + 31) >> 5;
         int64_t x = 0, y = 0;
         int code = 0;
@@ -176,7 +176,37 @@ struct SplitLine {
         int64_t rem = at - __shfl_sync(0xffffffffu, line0, g);
         real = __shfl_sync(0xffffffffu, line0, g) - (U0 ? U0 * __shfl_sync(0xffffffffu, units0, g) : 0);
         Unit u{};
-        for (int64_t n = g * per;; ++n) {
+        // of the lane's sequences, 32 at a time: a lane a sequence, down to the
+        // one that holds it (if they are all short, as many sequences are)
+        int64_t n = g * per;
+        for (; per > 1 && n < (g + 1) * per; n += 32) {
+            Unit v{};
+            if (n + lane < (g + 1) * per && n + lane < p.r.N) load_seq(p, n + lane, v);
+            const int tiles = tiles_of<M>(p, v.len);
+            if (__any_sync(0xffffffffu, tiles > kFew)) break;
+            const int64_t own = seq_line<M, BN, U0>(p, v, 0, 1);
+            int64_t x = own;
+            int un = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+                const int z = __shfl_up_sync(0xffffffffu, un, d);
+                if (lane >= d) {
+                    x += y;
+                    un += z;
+                }
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, x > rem);
+            const int l = m ? __ffs(m) - 1 : 31;  // none: all 32 lie before it
+            const int64_t before = __shfl_sync(0xffffffffu, m ? x - own : x, l);
+            rem -= before;
+            real += before - (int64_t)U0 * p.c.H * __shfl_sync(0xffffffffu, m ? un - tiles : un, l);
+            if (m) {
+                n += l;
+                break;
+            }
+        }
+        for (;; ++n) {
             load_seq(p, n, u);
             const int tiles = tiles_of<M>(p, u.len);
             for (int t = 0; t < tiles; t += 32) {

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 s_share[0] = total;
                 s_share[1] = nw;
                 s_share[2] = at;
-                a.ws.rec[w * 2] = make_int4(0, 0, 0, 0);
+                a.ws.rec[w] = make_int4(0, 0, 0, 0);
             }
         }
     }
@@ -535,8 +535,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             if (begun && !ends && tid == 0) {
                 const int pieces = pieces_from(s_share[0], worker, s_share[1],
                                                s_share[2] + (u.steps - first - steps));
-                a.ws.rec[worker * 2] = make_int4(pieces, u.t0, u.len, u.tile);
-                a.ws.rec[worker * 2 + 1].x = u.head;
+                a.ws.rec[worker] = make_int4(u.head << 16 | pieces, u.t0, u.len, u.tile);
             }
             if (left) next_unit<kTM, kTN>(p, u);
         }
