@@ -50,16 +50,25 @@ struct RowsCfg {
     static constexpr int kRow = D * kES;             // bytes of a row
     static constexpr int kLine = kRow < 128 ? kRow : 128;  // bytes of a row of a box
     static constexpr int kBlocks = kRow / kLine;     // boxes beside each other
-    static constexpr int kRows = kBN * kRow;         // bytes of a tile's rows
-    static constexpr int kScale = FMT ? kBN * 4 : 0; // after a tile of keys: both scales
-    // tiles start on the swizzle's period
-    static constexpr int kTile = (kRows + 2 * kScale + 1023) / 1024 * 1024;
-    static constexpr int kTiles = kTile > 6144 ? 3 : 5;
-    static constexpr int kRing = kTiles * kTile;
+    static constexpr int kRows = kBN * kRow;         // bytes of a tile
+    static constexpr int kScale = FMT ? kBN * 4 : 0; // of a step's scales of keys, of values
+    // 16 bits: three tiles (192 KB an SM), each loaded again as soon as it is
+    // read.  8 bits: three or more pairs, keys and values of a step (the swizzle's
+    // period apart) and both scales, loaded again together: there instructions
+    // are what bounds the kernel, half of them waiting to be fetched, and the
+    // loads then stand in the loop once.
+    static constexpr bool kPairs = FMT != 0;
+    static constexpr int kPair = (2 * kRows + 2 * kScale + 1023) / 1024 * 1024;
+    static constexpr int kTiles = !kPairs ? (D == 64 ? 5 : 3) : D == 64 ? 8 : 6;
+    static constexpr int kRing = kPairs ? kTiles / 2 * kPair : kTiles * kRows;
     static constexpr int kWarps = 8;
     static constexpr int kSmem = kWarps * kRing + 1024;
     static constexpr int kInfos = 4;                 // steps in the ring, at most
-    static_assert(kTiles / 2 + 2 <= kInfos, "steps in the ring");
+    static_assert(kPairs ? kTiles / 2 <= kInfos : kTiles / 2 + 2 <= kInfos, "steps in the ring");
+    __host__ __device__ static constexpr int tile_at(int i) {
+        return kPairs ? (i >> 1) * kPair + (i & 1) * kRows : i * kRows;
+    }
+    __host__ __device__ static constexpr int scale_at(int i) { return (i >> 1) * kPair + 2 * kRows; }
 };
 
 // What a step in the ring is.
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
     int load_item = 0, load_tile = 0;
     auto load = [&]() {
         const int kv = load_item & 1;
-        const uint32_t st = ring_u + load_tile * C::kTile;
+        const uint32_t st = ring_u + C::tile_at(load_tile);
         uint64_t *bar = &bars[load_tile];
         const bool here = asked && (unsigned)entry < (unsigned)p.c.n_pages;
         if (a.box) {
@@ -252,8 +261,8 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
                 tma_page(st + part * (C::kBN * 128) + bx * a.box * C::kLine, kv ? &a.tv : &a.tk, bar,
                          part * (C::kLine / C::kES), sl, u.head, page);
             if (FMT && !kv && here && part < 2)
-                tc::bulk_load(ring + load_tile * C::kTile + C::kRows + part * C::kScale + bx * a.box * 4,
-                              (part ? p.c.vs : p.c.ks) + scale_at(p.c, page, sl, u.head), a.box * 4, bar);
+                tc::bulk_load(ring + C::scale_at(load_tile) + part * C::kScale + bx * a.box * 4,
+                              (part ? p.c.vs : p.c.ks) + gdr::scale_at(p.c, page, sl, u.head), a.box * 4, bar);
         } else {
             const uint8_t *base = reinterpret_cast<const uint8_t *>(kv ? p.c.v : p.c.k);
             const int64_t at = !here ? 0 : kv ? page_at(p.c.vst, entry, slot, u.head) * C::kES
@@ -267,9 +276,10 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
                 cp16(st + kv_off<FMT, D>(t, c), base + of + (live ? c * 16 : 0), live);
             }
             if (FMT && !kv) {
-                const int64_t so = here ? scale_at(p.c, entry, slot, u.head) : 0;
-                cp4(st + C::kRows + lane * 4, p.c.ks + so, here);
-                cp4(st + C::kRows + C::kScale + lane * 4, p.c.vs + so, here);
+                const int64_t so = here ? gdr::scale_at(p.c, entry, slot, u.head) : 0;
+                const uint32_t sc = ring_u + C::scale_at(load_tile);
+                cp4(sc + lane * 4, p.c.ks + so, here);
+                cp4(sc + C::kScale + lane * 4, p.c.vs + so, here);
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar))
                          : "memory");
@@ -298,8 +308,10 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
     };
 
     look_up();
+    if constexpr (!C::kPairs) {
 #pragma unroll 1
-    for (int i = 0; i < C::kTiles && i < 2 * count; ++i) load();
+        for (int i = 0; i < C::kTiles && i < 2 * count; ++i) load();
+    }
 
     uint32_t qf[kKS][NR][2];
     float acc[kDT][NR][4];
@@ -317,16 +329,25 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
         return false;
     };
     auto next_tile = [&]() {
-        __syncwarp();  // the tile is free
-        if (load_item < 2 * count) load();
+        if constexpr (!C::kPairs) {
+            __syncwarp();  // the tile is free
+            if (load_item < 2 * count) load();
+        }
         if (++tile == C::kTiles) {
             tile = 0;
             phase ^= 1;
         }
     };
 
+    // pairs: the first turns only load
 #pragma unroll 1
-    for (int it = 0; it < count; ++it) {
+    for (int it = C::kPairs ? 1 - C::kTiles / 2 : 0; it < count; ++it) {
+        if constexpr (C::kPairs) {
+            __syncwarp();  // the pair before is free
+#pragma unroll 1
+            for (int i = 0; i < 2 && load_item < 2 * count; ++i) load();
+            if (it < 0) continue;
+        }
         if (!arrived()) return;
         __syncwarp();
         const StepInfo *fi = &info[it % C::kInfos];
@@ -396,7 +417,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
 
         // scores: sc[t][n][.] of tokens 16 t + token_of(qr) (and + 8: 2, 3) and
         // queries 8 n + 2 qc (and + 1: 1, 3)
-        const uint8_t *kt = ring + tile * C::kTile;
+        const uint8_t *kt = ring + C::tile_at(tile);
         float sc[kMT][NR][4];
 #pragma unroll
         for (int t = 0; t < kMT; ++t)
@@ -405,7 +426,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[t][n][e] = 0.f;
         if constexpr (FMT == 0) {
-            const uint32_t kt_u = ring_u + tile * C::kTile;
+            const uint32_t kt_u = ring_u + C::tile_at(tile);
 #pragma unroll
             for (int k = 0; k < kKS; ++k)
 #pragma unroll
@@ -444,7 +465,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
             for (int h = 0; h < 2; ++h) {
                 float ks = 1.f, lg = 0.f;
                 if constexpr (FMT) {
-                    const float *s = reinterpret_cast<const float *>(kt + C::kRows) + t * 16 + h * 8 +
+                    const float *s = reinterpret_cast<const float *>(ring + C::scale_at(tile)) + t * 16 + h * 8 +
                                      token_of<FMT>(qr);
                     ks = s[0];
                     // no smaller than 2^-100, so that 1 / s is finite: a scale of
@@ -541,7 +562,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
                 }
 
         if (!arrived()) return;
-        uint8_t *vt = ring + tile * C::kTile;
+        uint8_t *vt = ring + C::tile_at(tile);
         // what lies past the last position is anything
         if ((flags & kMask) && base + C::kBN > fi->hi) {
             const int left = fi->hi - base;
@@ -603,7 +624,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
                     __syncwarp();
                 }
             }
-            const uint32_t vt_u = ring_u + tile * C::kTile;
+            const uint32_t vt_u = ring_u + C::tile_at(tile);
 #pragma unroll
             for (int t = 0; t < kMT; ++t)
 #pragma unroll
