@@ -87,8 +87,20 @@ int64_t tile_rows(const gdr_dims &d) {
     if (d.N == 0) return d.T;
     return d.max_len > 0 ? d.max_len : (d.T + d.N - 1) / d.N;
 }
-// Rows of a key head up to which the kernel of 16-row tiles is taken.
-constexpr int64_t kFewRows = 16;
+// Rows of a key head (new tokens x G) up to which the kernel of small tiles is
+// taken, which reads every key for each 16 of them, against that of 256-row
+// tiles.  Measured, small against large, head width 128, 4 key heads:
+//   32 sequences of 4K tokens, BF16:  16 rows 55 / 60 us, 32: 65 / 60, 64: 100 / 60
+//   128 of 512 tokens, BF16:          32 rows 47 / 53 us, 64: 69 / 56
+//   32 of 4K, E4M3:                   32 rows 65 / 100 us, 64: 107 / 106
+//   one of 32K, BF16:                  8 rows 27 / 29 us, 16: 40 / 29
+//   one of 32K, E4M3:                  8 rows 31 / 44 us, 16: 50 / 44
+// so with few (sequence, key head) pairs, where each is shared by many workers,
+// the limit is lower.
+int64_t few_rows(const gdr_dims &d, const gdr_paged_cache &c) {
+    if (seqs_of(d) * c.H < 32) return 8;
+    return cache_quantised(c.dtype) ? 64 : 32;
+}
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -131,7 +143,7 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
 size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cache) {
     if (check_dims(dims) != GDR_OK || check_cache(*dims, cache, true) != GDR_OK) return 0;
     AttnProblem p{};
-    const size_t a = split_bytes(attn_rows_plan(p, kFewRows), dims->V);
+    const size_t a = split_bytes(attn_rows_plan(p, 16), dims->V);
     const size_t b = split_bytes(attn_tiles_plan(p), dims->V);
     return a > b ? a : b;
 }
@@ -182,7 +194,7 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
     }
     const bool can = attn_tiles_supported(p);
     if (force == 2 && !can) return GDR_ERR_UNSUPPORTED;
-    const bool tiles = force == 2 || (force == 0 && can && tile_rows(*dims) * p.G > kFewRows);
+    const bool tiles = force == 2 || (force == 0 && can && tile_rows(*dims) * p.G > few_rows(*dims, *cache));
     p.by_G = divisor((uint32_t)p.G);
     p.by_page = divisor((uint32_t)p.c.page_size);
     for (p.align = 1; p.align < 128 && p.c.page_size % (2 * p.align) == 0;) p.align *= 2;

@@ -463,34 +463,36 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 if ((FMT == 0 || kFold) && s_poison[seg & 7] == seg + 1) {
                     // values that are not finite at masked positions went in
                     // as zeros: add them to the rows that see them
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tmem_ld32(to + 32 * q, o);
-                        tmem_wait_ld();
-                        reg_fence(o);
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(to + 16 * q, o);
+                        tmem_wait_ld(o);
+#pragma unroll 1
                         for (int s = first; s < first + steps; ++s) {
                             const int base = u.lo + s * kTN;
                             if (!step_masked<kTN>(u, base)) continue;
+#pragma unroll 1
                             for (int j = max(base, lo); j < min(base + kTN, hi); ++j) {
                                 const int page = page_of(p.c, u.n, p.by_page(j), p.r.status);
                                 if (page < 0) continue;
                                 const int at = j - p.by_page(j) * p.c.page_size;
                                 if constexpr (FMT == 0) {
                                     const T *v = reinterpret_cast<const T *>(p.c.v) +
-                                                 page_at(p.c.vst, page, at, u.head) + 32 * q;
+                                                 page_at(p.c.vst, page, at, u.head) + 16 * q;
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) {
+                                    for (int e = 0; e < 16; ++e) {
                                         const float x = (float)v[e];
                                         if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
                                     }
                                 } else if (!isfinite(p.c.vs[scale_at(p.c, page, at, u.head)])) {
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = 0x7fc00000u;
+                                    for (int e = 0; e < 16; ++e) o[e] = 0x7fc00000u;
                                 }
                             }
                         }
                         __syncwarp();
-                        tmem_st32(to + 32 * q, o);
+                        tmem_st16(to + 16 * q, o);
                     }
                     tmem_wait_st();
                 }
@@ -555,37 +557,64 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             const int qc = t % kQC, halves = rows > 128 ? 2 : 1;
             float *qf = reinterpret_cast<float *>(sm + C::kOffQf) + (seg & 1) * kTM;
             constexpr bool kConvert = FMT != 0 && std::is_same<T, __nv_bfloat16>::value;
-#pragma unroll 8
-            for (int r = t / kQC; r < 128 * halves; r += kQP) {
-                const int ur = u.tile * kTM + r, tok = p.by_G(ur), hq = u.head * p.G + ur - tok * p.G;
+            // rows in steps of kQP from this thread's first: token and head move
+            // by the same amounts
+            const int dt = p.by_G(kQP), dh = kQP - dt * p.G;
+            int tok = p.by_G(u.tile * kTM + t / kQC), hq = u.tile * kTM + t / kQC - tok * p.G;
+            auto place = [&](int r, const T *&src) {  // whether the unit has the row, and where
                 const bool live = r < rows;
-                const T *src = reinterpret_cast<const T *>(p.q) +
-                               (live ? tok_at(p.sq, u.t0 + tok, hq) + qc * 8 : 0);
-                const uint32_t dst = (r >> 7) * C::kTile + sw128_chunk(r & 127, qc, 128);
-                if constexpr (kConvert) {
-                    // FP16 of the row's own power of two (see attn_rows.cu)
-                    uint4 x = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-                    float big = 0.f;
+                src = reinterpret_cast<const T *>(p.q) +
+                      (live ? tok_at(p.sq, u.t0 + tok, u.head * p.G + hq) + qc * 8 : 0);
+                tok += dt;
+                hq += dh;
+                if (hq >= p.G) {
+                    hq -= p.G;
+                    ++tok;
+                }
+                return live;
+            };
+            auto dst = [&](int r) { return (r >> 7) * C::kTile + sw128_chunk(r & 127, qc, 128); };
+            if constexpr (kConvert) {
+                // FP16 of the row's own power of two (see attn_rows.cu), four
+                // rows' loads at a time
+                #pragma unroll 1
+                for (int r0 = t / kQC; r0 < 128 * halves; r0 += 4 * kQP) {
+                    uint4 x[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = wide16<T>(w[e]);
-                        big = fmaxf(big, fmaxf(fabsf(y.x), fabsf(y.y)));
+                    for (int i = 0; i < 4; ++i) {
+                        const T *src;
+                        const bool live = place(r0 + i * kQP, src);
+                        x[i] = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int d = 1; d < kQC; d <<= 1)
-                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-                    const int ex = (__float_as_int(big) >> 23) & 255;
-                    const float g = ex > 0 && ex < 254 ? __int_as_float((254 - ex) << 23) : 1.f;
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        // the largest magnitude's bits: they are in its order
+                        uint32_t big = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                                __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = wide16<T>(w[e]);
-                        w[e] = pack16<__half>(y.x * g, y.y * g);
+                        for (int d = 1; d < kQC; d <<= 1)
+                            big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, d));
+                        big = max(big & 0xffffu, big >> 16);
+                        const int ex = (int)(big >> 7);
+                        const bool normal = ex > 0 && ex < 254;
+                        const float g = normal ? __int_as_float((254 - ex) << 23) : 1.f;
+                        const float back = normal ? __int_as_float(ex << 23) : 1.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack16<__half>(__uint_as_float(w[e] << 16) * g,
+                                                  __uint_as_float(w[e] & 0xffff0000u) * g);
+                        const int r = r0 + i * kQP;
+                        *reinterpret_cast<uint4 *>(sm + dst(r)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (qc == 0) qf[r] = back;
                     }
-                    *reinterpret_cast<uint4 *>(sm + dst) = x;
-                    if (qc == 0) qf[r] = 1.f / g;
-                } else {
-                    cp16z(sb + dst, src, live);
+                }
+            } else {
+#pragma unroll 8
+                for (int r = t / kQC; r < 128 * halves; r += kQP) {
+                    const T *src;
+                    const bool live = place(r, src);
+                    cp16z(sb + dst(r), src, live);
                 }
             }
             if constexpr (!kConvert) asm volatile("cp.async.wait_all;" ::: "memory");
@@ -692,7 +721,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         sc[2 * kTN + t] = __fdividef(1.f, v);
                     }
                     uint8_t *tile = sm + C::kOffRing + b * C::kTile;
-#pragma unroll 2
+#pragma unroll 4
                     for (int i = 0; i < kPasses; ++i) {
                         const int r = r0 + i * kPass;
                         uint4 x = *reinterpret_cast<const uint4 *>(raw + r * D + ch * 16), e0, e1;
