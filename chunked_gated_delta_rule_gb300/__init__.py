@@ -1,4 +1,5 @@
-"""GB300-native chunked gated-delta-rule forward and backward passes.
+"""GB300-native chunked gated-delta-rule forward and backward passes, and the
+paged cache and attention of the softmax layers beside them.
 
 The compute path is a C-ABI CUDA library (``include/gdr.h``, built in-tree
 into ``_build/libgdr.so``); this package is its thin ctypes binding plus the

@@ -409,8 +409,14 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
  *             aligned), the launch events, grid_limit and force_path (0 plan,
  *             1 CUDA cores, 2 the tensor-core kernel of many rows, 3 that of
  *             few rows); force_bv must be 0.
- * FP32 scores, softmax statistics and accumulators.  A masked position never
- * adds to a row, whatever the cache holds there.  Results are bit-identical
+ * Routes: the tensor cores take BF16 and FP16 queries with K = V = 64 or 128
+ * and 16-byte aligned q, o and pages (bases and strides), pages of any size
+ * (the kernel of many rows: of a multiple of 8 slots); everything else, FP32
+ * among it, runs on CUDA cores.
+ * FP32 scores, softmax statistics and accumulators; weights are rounded to 16
+ * bits for the product with the values (few rows: as two halves).  A masked
+ * position never adds to a row, whatever the cache holds there (E4M3 caches: as
+ * gdr_cache_write stores them, without NaN bytes).  Results are bit-identical
  * from run to run.
  */
 int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const void *q,
