@@ -445,13 +445,12 @@ def _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, ind
     if fmt is None or v_cache.dtype is not dtype:
         raise TypeError("k_cache and v_cache must share a dtype: float32, bfloat16, float16, "
                         f"float8_e4m3fn or int8, got {dtype} and {v_cache.dtype}")
-    if k_cache.dim() != 4 or v_cache.dim() != 4:
+    shape, v_shape, t_shape = k_cache.shape, v_cache.shape, page_table.shape
+    if len(shape) != 4 or len(v_shape) != 4:
         raise ValueError("k_cache and v_cache must be [pages, page size, heads, K] and [.., V]")
-    P, page, H, _ = k_cache.shape
-    if (P, page, H) != v_cache.shape[:3]:
+    P, page, H, _ = shape
+    if v_shape[0] != P or v_shape[1] != page or v_shape[2] != H:
         raise ValueError("k_cache and v_cache must share pages, page size and heads")
-    if k_cache.get_device() != index or v_cache.get_device() != index:
-        raise ValueError(f"k_cache and v_cache must be on cuda:{index}")
     if k_scale is None:
         if fmt >= GDR_E4M3 or v_scale is not None:
             raise ValueError("k_scale and v_scale belong to an 8-bit cache, both of them")
@@ -465,13 +464,15 @@ def _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, ind
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     if page_table.dtype is not torch.int32 or kv_lens.dtype is not torch.int32:
         raise TypeError("page_table and kv_lens must be int32")
-    if page_table.get_device() != index or kv_lens.get_device() != index or \
-            not page_table.is_contiguous() or not kv_lens.is_contiguous():
-        raise ValueError(f"page_table and kv_lens must be contiguous and on cuda:{index}")
-    if page_table.dim() != 2 or page_table.size(0) != nseq or kv_lens.shape != (nseq,):
+    if not (index == k_cache.get_device() == v_cache.get_device() == page_table.get_device()
+            == kv_lens.get_device()):
+        raise ValueError(f"the caches, page_table and kv_lens must be on cuda:{index}")
+    if not (page_table.is_contiguous() and kv_lens.is_contiguous()):
+        raise ValueError("page_table and kv_lens must be contiguous")
+    if len(t_shape) != 2 or t_shape[0] != nseq or kv_lens.shape != (nseq,):
         raise ValueError("page_table must be [sequences, pages a sequence], kv_lens [sequences]")
     c = gdr_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, page_table.data_ptr(),
-                        kv_lens.data_ptr(), P, page, page_table.size(1), H, fmt)
+                        kv_lens.data_ptr(), P, page, t_shape[1], H, fmt)
     if not k_cache.is_contiguous():
         c.k_stride[:] = _page_strides(k_cache)
     if not v_cache.is_contiguous():
@@ -507,7 +508,7 @@ def _set_strides(field, t):
 def _paged_call(fn, index, stream, *args):
     """Calls a library function on ``stream`` (default: the current one)."""
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:  # torch holds a tensor there: it is initialised
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -569,9 +570,11 @@ def gdr_cache_read(k_cache, v_cache, page_table, kv_lens, T, cu_seqlens=None, *,
         if t is not None and (t.get_device() != index or t.dtype != dtype or
                               t.shape != (B, T, H, D)):
             raise ValueError(f"{name} must be {[B, T, H, D]}, {dtype}, on cuda:{index}")
-    k = kv_lens.new_empty((B, T, H, K), dtype=dtype) if k is None else k
-    v = (torch.empty_like(k) if V == K and k.is_contiguous()
-         else kv_lens.new_empty((B, T, H, V), dtype=dtype)) if v is None else v
+    if k is None:
+        k = torch.empty((B, T, H, K), dtype=dtype, device=k_cache.device)
+    if v is None:
+        v = (torch.empty_like(k) if V == K and k.is_contiguous()
+             else torch.empty((B, T, H, V), dtype=dtype, device=k_cache.device))
     dims, nseq = _paged_dims(B, T, H, K, V, cu_seqlens, dtype, index)
     _set_strides(dims.k_stride, k)
     _set_strides(dims.v_stride, v)
@@ -599,16 +602,17 @@ def gdr_paged_attn(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
     index = q.get_device()
     if index < 0:
         raise ValueError("gdr_paged_attn takes CUDA tensors")
-    if q.dim() != 4 or k_cache.dim() != 4 or v_cache.dim() != 4 or q.shape[3] != k_cache.shape[3]:
+    shape, k_shape, v_shape = q.shape, k_cache.shape, v_cache.shape
+    if len(shape) != 4 or len(k_shape) != 4 or len(v_shape) != 4 or shape[3] != k_shape[3]:
         raise ValueError("q must be [B, T, heads, K], the caches [pages, page size, heads, K or V]")
-    B, T, H, K = q.shape
-    V = v_cache.shape[3]
+    B, T, H, K = shape
+    V = v_shape[3]
     if o is None:
         o = torch.empty_like(q) if V == K and q.is_contiguous() else q.new_empty((B, T, H, V))
     elif o.shape != (B, T, H, V) or o.dtype != q.dtype or o.get_device() != index:
         raise ValueError(f"o must be {[B, T, H, V]}, {q.dtype}, on cuda:{index}")
     if lse is None:
-        lse = q.new_empty((B, T, H), dtype=torch.float32)
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
     else:
         _on(index, lse=(lse, torch.float32))
         if lse.shape != (B, T, H):
