@@ -51,7 +51,7 @@ using namespace tc;
 constexpr int kTM = 256;       // rows of a unit
 constexpr int kTN = 128;       // positions of a step
 constexpr int kTThreads = 512;
-constexpr int kTUnit = 2;      // what a unit costs beside its steps, in steps
+constexpr int kTUnit = 4;      // what a unit costs beside its steps, in steps
 constexpr float kTLog2e = 1.4426950408889634f;
 constexpr float kTLn2 = 0.6931471805599453f;
 constexpr float kTLeast = 7.888609052210118e-31f;  // 2^-100
@@ -95,6 +95,7 @@ struct TilesArgs {
     SplitScratch ws;
     int min_steps;       // least length of a share
     int box;             // slots of a TMA box
+    int wide_o;          // rows of o lie on 32-byte boundaries
     int q_box;           // queries by TMA: tokens of a half (0: by the helpers)
     CUtensorMap tk, tv;  // [page][head][slot][column] of the caches
     CUtensorMap tq;      // [token][head][column]
@@ -175,6 +176,13 @@ __device__ __forceinline__ bool help_sync(bool ok) {
         : "r"((uint32_t)ok)
         : "memory");
     return r != 0;
+}
+
+// 32 bytes, a whole sector, by one lane (aligned).
+__device__ __forceinline__ void store32(void *p, const uint32_t (&x)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
+                 "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
 }
 
 // Instruction descriptor: A and B of type T, A K-major, FP32 sums, M = 128.
@@ -501,27 +509,27 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 const float inv = whole ? (empty ? 0.f : 1.f / l) : 1.f;
                 T *o16 = reinterpret_cast<T *>(p.o) + (live ? tok_at(p.so, u.t0 + tok, hq) : 0);
                 const int64_t slot = (worker * 2 + (begun ? 1 : 0)) * kTM + r;
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    tmem_ld32(to + 32 * q, o);
-                    tmem_wait_ld();
-                    reg_fence(o);
+                // not unrolled: this runs once a unit, and code that is not in the
+                // instruction cache costs as much as what it does
+#pragma unroll 1
+                for (int q = 0; q < D / 16; ++q) {
+                    uint32_t o[16];
+                    tmem_ld16(to + 16 * q, o);
+                    tmem_wait_ld(o);
                     if (live && whole) {
+                        uint32_t x[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 x;
-                            x.x = pack16<T>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                            x.y = pack16<T>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                            x.z = pack16<T>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                            x.w = pack16<T>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                            *reinterpret_cast<uint4 *>(o16 + 32 * q + e) = x;
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = pack16<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        if (a.wide_o) {
+                            store32(o16 + 16 * q, x);
+                        } else {
+                            reinterpret_cast<uint4 *>(o16 + 16 * q)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+                            reinterpret_cast<uint4 *>(o16 + 16 * q)[1] = make_uint4(x[4], x[5], x[6], x[7]);
                         }
                     } else if (live) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4 *>(a.ws.o + slot * D + 32 * q + e) =
-                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        store32(a.ws.o + slot * D + 16 * q, *reinterpret_cast<const uint32_t(*)[8]>(&o[0]));
+                        store32(a.ws.o + slot * D + 16 * q + 8, *reinterpret_cast<const uint32_t(*)[8]>(&o[8]));
                     }
                 }
                 tc_fence_before();  // O is read before the next unit's first product is let go
@@ -953,6 +961,7 @@ template <typename T, int FMT, int D>
 cudaError_t launch_tiles(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
     using C = TilesCfg<FMT, D>;
     TilesArgs a{p, ws, 1, p.align};
+    a.wide_o = ((reinterpret_cast<uintptr_t>(p.o) | (uintptr_t)(p.so.t * 2) | (uintptr_t)(p.so.h * 2)) & 31u) == 0;
     if (!page_map(&a.tk, p, p.c.k, p.c.kst, D, a.box, kPagePlain) ||
         !page_map(&a.tv, p, p.c.v, p.c.vst, D, a.box, kPagePlain))
         return cudaErrorInvalidValue;
