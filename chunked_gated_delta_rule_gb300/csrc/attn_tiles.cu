@@ -35,6 +35,20 @@
 // s / s_max in FP16, s_max the largest scale of the step's 128 positions, and
 // s_max alone is left to the weights.  The keys' scales stay with the scores:
 // lse is FP32.
+// E4M3 keys of 128 columns under BF16 queries are not widened at all: a row of
+// queries, scaled by a power of two to have its largest magnitude in [2^7, 2^8),
+// is split into two E4M3 parts, x = hi + lo.  hi takes four of BF16's eight bits
+// and leaves at most four, so the split is exact for components down to 2^-9 of
+// the row's largest; what smaller ones lose is at most 2^-17 of the largest, 2^-8
+// of what BF16 itself rounded off that one.  S = hi K^T + lo K^T takes two E4M3
+// products at twice the rate of one FP16 product, so no longer, and the keys go
+// from the cache into the products as they are: 490 us for 4096 new tokens over
+// 16K (4 key heads), 691 with widened keys.
+// Measured (4 key heads of 128, 4 query heads each, BF16, replayed from a graph):
+// 4096 new tokens over 32K: 615 us, 1678 TFLOP/s, 0.86 of a library product's
+// rate; over 16K in E4M3: 490 us, bound by softmax and the helpers, which share
+// the paths to shared memory (every thread reads 128 scales a step); 32 prompts of
+// 128 to 512 tokens: 71 us, of which a unit costs 6 us beside 1.4 us a step.
 //
 // The steps of the call are shared out equally over one CTA an SM
 // (attn_split.cuh).  Every wait is bounded: on expiry the CTA records
@@ -51,20 +65,28 @@ using namespace tc;
 constexpr int kTM = 256;       // rows of a unit
 constexpr int kTN = 128;       // positions of a step
 constexpr int kTThreads = 512;
-constexpr int kTUnit = 4;      // what a unit costs beside its steps, in steps
+// What a unit costs beside its steps, in steps: 6 us of 1.4 us (32 prompts: 71 us,
+// with two 79).
+constexpr int kTUnit = 4;
 constexpr float kTLog2e = 1.4426950408889634f;
 constexpr float kTLn2 = 0.6931471805599453f;
 constexpr float kTLeast = 7.888609052210118e-31f;  // 2^-100
 
 // Registers a thread of the softmax warps, the helpers and the rest: 128 each
-// at launch, 2 x 184 + 88 + 56 = 4 x 128.
-constexpr int kRegSoftmax = 184, kRegHelp = 88, kRegRest = 56;
+// at launch, 2 x 192 + 72 + 56 = 4 x 128
+// (184 / 88 / 56: 515 us instead of 490 for 4096 new tokens over 16K in E4M3,
+// where softmax spills more).
+constexpr int kRegSoftmax = 192, kRegHelp = 72, kRegRest = 56;
 static_assert(2 * kRegSoftmax + kRegHelp + kRegRest <= 4 * 128, "the launch's registers");
 
-template <int FMT, int D>
+template <typename T, int FMT, int D>
 struct TilesCfg {
+    // E4M3 keys as they are, the queries in two E4M3 parts (above)
+    static constexpr bool kSplit = FMT == 1 && D == 128 && std::is_same<T, __nv_bfloat16>::value;
     static constexpr uint32_t kTile = kTN * D * 2;     // a 128-row tile of 16-bit values
-    static constexpr int kRing = D == 64 ? 8 : FMT ? 3 : 4;  // tiles of keys and values
+    // tiles of keys and values, or of values alone beside kKeys of keys
+    static constexpr int kRing = D == 64 ? 8 : kSplit ? 2 : FMT ? 3 : 4;
+    static constexpr int kKeys = kSplit ? 2 : 0;
     // tiles given back in pairs, a step's keys and the values before them
     // (one commit a step instead of two); 0: one by one
     static constexpr int kPairs = FMT ? 0 : kRing / 2;
@@ -75,7 +97,8 @@ struct TilesCfg {
     // that far behind
     static constexpr int kScales = FMT ? (D == 64 ? 8 : 4) : 0;
     static constexpr uint32_t kOffRing = 2 * kTile;    // after the queries
-    static constexpr uint32_t kOffRaw = kOffRing + kRing * kTile;    // + scales of keys, values
+    static constexpr uint32_t kOffKeys = kOffRing + kRing * kTile;
+    static constexpr uint32_t kOffRaw = kOffKeys + kKeys * kRawTile; // + scales of keys, values
     static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawSize; // [kScales][3][128]
     static constexpr uint32_t kOffQf = kOffScale + kScales * 3 * kTN * 4;  // [2 units][256]
     static constexpr uint32_t kOffBar = kOffQf + 2 * kTM * 4;
@@ -85,9 +108,27 @@ struct TilesCfg {
     static constexpr int kFull = 0, kEmpty = kRing;    // tiles
     static constexpr int kLand = 2 * kRing;            // FMT: raw tiles; else masked values, by tile
     static constexpr int kLands = FMT ? kRaw : kRing, kTaken = kLand + kLands;  // raw tiles read
-    static constexpr int kQFull = kTaken + kRaw, kQEmpty = kQFull + 1, kS = kQFull + 2, kP = kS + 2,
+    static constexpr int kKeyFull = kTaken + kRaw, kKeyEmpty = kKeyFull + kKeys;
+    static constexpr int kQFull = kKeyEmpty + kKeys, kQEmpty = kQFull + 1, kS = kQFull + 2, kP = kS + 2,
                          kO = kP + 2, kDrain = kO + 2;
     static_assert((kDrain + 1) * 8 <= 512, "barriers");
+    // Item 2 s is the keys of step s and 2 s + 1 its values: its tile, how often
+    // the tile was used before, its barriers.
+    __device__ static uint32_t turns(uint32_t item) {
+        return !kSplit ? item / kRing : (item >> 1) / (item & 1 ? kRing : kKeys);
+    }
+    __device__ static uint32_t slot(uint32_t item) {
+        return !kSplit ? item % kRing : (item >> 1) % (item & 1 ? kRing : kKeys);
+    }
+    __device__ static int full(uint32_t item) {
+        return (kSplit && !(item & 1) ? kKeyFull : kFull) + slot(item);
+    }
+    __device__ static int empty(uint32_t item) {
+        return (kSplit && !(item & 1) ? kKeyEmpty : kEmpty) + slot(item);
+    }
+    __device__ static uint32_t tile(uint32_t item) {
+        return kSplit && !(item & 1) ? kOffKeys + slot(item) * kRawTile : kOffRing + slot(item) * kTile;
+    }
 };
 
 struct TilesArgs {
@@ -178,6 +219,29 @@ __device__ __forceinline__ bool help_sync(bool ok) {
     return r != 0;
 }
 
+// Four values in E4M3, in order, to nearest even; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
+    uint32_t y;
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
+        : "=r"(y)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+    return y;
+}
+
+// Two BF16 values of a row that holds an infinity or a NaN: an infinity becomes
+// +-1, a NaN stays, anything finite is nothing beside them.
+__device__ __forceinline__ uint32_t signs_of_infinities(uint32_t w) {
+    uint32_t y = 0;
+#pragma unroll
+    for (int i = 0; i < 32; i += 16) {
+        const uint32_t x = w >> i & 0x7fffu;
+        if (x == 0x7f80u) y |= (0x3f80u | (w >> i & 0x8000u)) << i;
+        else if (x > 0x7f80u) y |= 0x7fc0u << i;
+    }
+    return y;
+}
+
 // 32 bytes, a whole sector, by one lane (aligned).
 __device__ __forceinline__ void store32(void *p, const uint32_t (&x)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
@@ -186,6 +250,7 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&x)[8]) {
 }
 
 // Instruction descriptor: A and B of type T, A K-major, FP32 sums, M = 128.
+// E4M3 operands have FP16's number.
 template <typename T>
 __host__ __device__ constexpr uint32_t tiles_idesc(int N, int b_mn) {
     const uint32_t f = std::is_same<T, __half>::value ? 0u : 1u;
@@ -203,6 +268,16 @@ __device__ __forceinline__ uint32_t elect_lead() {
     asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
                  : "=r"(r));
     return r;
+}
+// E4M3 operands: 32 columns a product instead of 16.
+__device__ __forceinline__ void lead_mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t add, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ void lead_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t add, uint32_t lead) {
@@ -242,7 +317,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_constant__ TilesArgs a) {
-    using C = TilesCfg<FMT, D>;
+    using C = TilesCfg<T, FMT, D>;
     using B = C;  // its barriers
     using TP = typename std::conditional<FMT == 0, T, __half>::type;
     constexpr bool kFold = FMT != 0 && std::is_same<T, __nv_bfloat16>::value;  // values' scales in them
@@ -272,6 +347,10 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
         }
         for (int i = 0; i < C::kLands; ++i) mbar_init(&bars[B::kLand + i], 1);
         for (int i = 0; i < C::kRaw; ++i) mbar_init(&bars[B::kTaken + i], 128);
+        for (int i = 0; i < C::kKeys; ++i) {
+            mbar_init(&bars[B::kKeyFull + i], 129);  // the keys, and the helpers with their scales
+            mbar_init(&bars[B::kKeyEmpty + i], 1);
+        }
         mbar_init(&bars[B::kQFull], a.q_box ? 1 : 128);
         mbar_init(&bars[B::kQEmpty], 1);
         for (int i = 0; i < 2; ++i) {
@@ -412,7 +491,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if constexpr (FMT == 0 || kFold) mn = mn == -INFINITY ? mn : fmaf(mn, fs, lgs);
                     if (__any_sync(0xffffffffu, mn > m + 8.f)) {
-                        const float n = fmaxf(m, mn);
+                        const float n = mn > m + 8.f ? mn : m;  // each row by its own scores alone
                         const float c = n == -INFINITY ? 1.f : ex2(m - n);
                         m = n;
                         l *= c;
@@ -604,16 +683,47 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         for (int d = 1; d < kQC; d <<= 1)
                             big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, d));
                         big = max(big & 0xffffu, big >> 16);
-                        const int ex = (int)(big >> 7);
-                        const bool normal = ex > 0 && ex < 254;
-                        const float g = normal ? __int_as_float((254 - ex) << 23) : 1.f;
-                        const float back = normal ? __int_as_float(ex << 23) : 1.f;
+                        const int ex = (int)(big >> 7), r = r0 + i * kQP;
+                        float back;
+                        if constexpr (C::kSplit) {
+                            // the largest magnitude into [2^7, 2^8); a row with an
+                            // infinity is its infinities' signs, times infinity
+                            const int at = max(ex, 8);
+                            const float g = __int_as_float((261 - at) << 23);
+                            back = ex == 255 ? INFINITY : __int_as_float((at - 7) << 23);
+                            uint32_t hi[2], lo[2];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack16<__half>(__uint_as_float(w[e] << 16) * g,
-                                                  __uint_as_float(w[e] & 0xffff0000u) * g);
-                        const int r = r0 + i * kQP;
-                        *reinterpret_cast<uint4 *>(sm + dst(r)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int e = 0; e < 2; ++e) {
+                                uint2 y = make_uint2(w[2 * e], w[2 * e + 1]);
+                                if (ex == 255) {
+                                    y.x = signs_of_infinities(y.x);
+                                    y.y = signs_of_infinities(y.y);
+                                }
+                                const float x0 = __uint_as_float(y.x << 16) * (ex == 255 ? 1.f : g);
+                                const float x1 = __uint_as_float(y.x & 0xffff0000u) * (ex == 255 ? 1.f : g);
+                                const float x2 = __uint_as_float(y.y << 16) * (ex == 255 ? 1.f : g);
+                                const float x3 = __uint_as_float(y.y & 0xffff0000u) * (ex == 255 ? 1.f : g);
+                                hi[e] = e4m3x4(x0, x1, x2, x3);
+                                uint32_t a0, a1;
+                                widen4<1>(hi[e], a0, a1);
+                                const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&a0));
+                                const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&a1));
+                                lo[e] = e4m3x4(x0 - f0.x, x1 - f0.y, x2 - f1.x, x3 - f1.y);
+                            }
+                            // first the 128 columns of hi, then those of lo
+                            const uint32_t row = (r >> 7) * C::kTile + (qc & 1) * 8;
+                            *reinterpret_cast<uint2 *>(sm + row + sw128_chunk(r & 127, qc >> 1, 128)) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2 *>(sm + row + sw128_chunk(r & 127, 8 + (qc >> 1), 128)) = make_uint2(lo[0], lo[1]);
+                        } else {
+                            const bool normal = ex > 0 && ex < 254;
+                            const float g = normal ? __int_as_float((254 - ex) << 23) : 1.f;
+                            back = normal ? __int_as_float(ex << 23) : 1.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack16<__half>(__uint_as_float(w[e] << 16) * g,
+                                                      __uint_as_float(w[e] & 0xffff0000u) * g);
+                            *reinterpret_cast<uint4 *>(sm + dst(r)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                         if (qc == 0) qf[r] = back;
                     }
                 }
@@ -688,19 +798,24 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 constexpr int kChunks = D / 16, kPass = 128 / kChunks, kPasses = kTN / kPass;
                 const int ch = t % kChunks, r0 = t / kChunks;
                 const bool masked = step_masked<kTN>(u, base);
-                for (int kv = 0; kv < 2 && ok; ++kv, ++item) {
-                    const int b = item % C::kRing, w = item % C::kRaw;
+                for (int kv = C::kSplit ? 1 : 0; kv < 2 && ok; ++kv, ++item) {
+                    // scales come with the first 8-bit tile of a step
+                    const bool scales = C::kSplit || kv == 0;
+                    const uint32_t tile_item = C::kSplit ? 2 * item + 1 : item;
+                    const int w = item % C::kRaw;
                     const uint8_t *raw = sm + C::kOffRaw + w * C::kRawSize;
                     ok = __all_sync(0xffffffffu, wait(B::kLand + w, item / C::kRaw));
                     if (!ok) break;
                     float ks = 0.f, vs = kFold ? 0.f : 1.f;
-                    if (kv == 0 && t < left) {
+                    if (scales && t < left) {
                         ks = reinterpret_cast<const float *>(raw + C::kRawTile)[t];
                         vs = reinterpret_cast<const float *>(raw + C::kRawTile)[kTN + t];
                     }
-                    ok = __all_sync(0xffffffffu, wait(B::kEmpty + b, item / C::kRing + 1));
-                    if (!ok) break;
-                    if (kFold && kv == 0) {
+                    if (!C::kSplit) {
+                        ok = __all_sync(0xffffffffu, wait(C::empty(tile_item), C::turns(tile_item) + 1));
+                        if (!ok) break;
+                    }
+                    if (kFold && scales) {
                         // the values' largest scale, and every row's part of it
                         float vm = isfinite(vs) ? vs : 0.f;
 #pragma unroll
@@ -719,16 +834,21 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                             sc[kTN] = __log2f(vm);
                             sc[2 * kTN] = __fdividef(1.f, vm);
                         }
+                        if (C::kSplit) mbar_arrive(&bars[C::full(2 * item)]);
                         if (!together()) break;
                     }
-                    if (!kFold && kv == 0) {
+                    if (C::kSplit) {
+                        ok = __all_sync(0xffffffffu, wait(C::empty(tile_item), C::turns(tile_item) + 1));
+                        if (!ok) break;
+                    }
+                    if (!kFold && scales) {
                         float *sc = reinterpret_cast<float *>(sm + C::kOffScale) + (it % C::kScales) * 3 * kTN;
                         const float v = vs < kTLeast ? kTLeast : vs;
                         sc[t] = ks;
                         sc[kTN + t] = __log2f(v);
                         sc[2 * kTN + t] = __fdividef(1.f, v);
                     }
-                    uint8_t *tile = sm + C::kOffRing + b * C::kTile;
+                    uint8_t *tile = sm + C::tile(tile_item);
 #pragma unroll 4
                     for (int i = 0; i < kPasses; ++i) {
                         const int r = r0 + i * kPass;
@@ -762,7 +882,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     }
                     mbar_arrive(&bars[B::kTaken + w]);
                     fence_async_smem();
-                    mbar_arrive(&bars[B::kFull + b]);
+                    mbar_arrive(&bars[C::full(tile_item)]);
                 }
             }
             if (it + 1 < count && ++u.step == u.steps) next_unit<kTM, kTN>(p, u);
@@ -781,18 +901,25 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             // descriptors as a base plus a constant for each product: the
             // address is their low 14 bits, in units of 16 bytes
             const uint64_t dk0 = sdesc_sw128(sb, 16, 1024), dv0 = sdesc_sw128(sb, 16384, 1024);
-            auto score = [&](int half, uint32_t b) {
+            auto score = [&](int half, uint32_t i) {
                 const uint64_t q = dk0 + half * (C::kTile >> 4);
-                const uint64_t kt = dk0 + ((C::kOffRing + b * C::kTile) >> 4);
+                const uint64_t kt = dk0 + (C::tile(i) >> 4);
+                if constexpr (C::kSplit) {  // hi, then lo, with the same keys
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    const uint64_t o = ((d >> 2) * 16384 + (d & 3) * 32) >> 4;
-                    lead_mma(tmem + C::kColS + half * 128, q + o, kt + o, kIdS, d > 0, lead);
+                    for (int d = 0; d < 8; ++d)
+                        lead_mma8(tmem + C::kColS + half * 128, q + (((d >> 2) * 16384 + (d & 3) * 32) >> 4),
+                                  kt + (((d & 3) * 32) >> 4), kIdS, d > 0, lead);
+                } else {
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        const uint64_t o = ((d >> 2) * 16384 + (d & 3) * 32) >> 4;
+                        lead_mma(tmem + C::kColS + half * 128, q + o, kt + o, kIdS, d > 0, lead);
+                    }
                 }
                 lead_commit(&bars[B::kS + half], lead);
             };
-            auto gather = [&](int half, uint32_t b, uint32_t add) {
-                const uint64_t vt = dv0 + ((C::kOffRing + b * C::kTile) >> 4);
+            auto gather = [&](int half, uint32_t i, uint32_t add) {
+                const uint64_t vt = dv0 + (C::tile(i) >> 4);
 #pragma unroll
                 for (int j = 0; j < kTN / 16; ++j)
                     lead_mma_ts(tmem + C::kColO + half * D, tmem + C::kColS + half * 128 + 8 * j,
@@ -801,29 +928,29 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             // the keys of item 2 k, and with them the values before, are done
             auto release_k = [&](uint32_t i) {
                 if constexpr (C::kPairs > 0) lead_commit(&bars[B::kEmpty + (i >> 1) % C::kPairs], lead);
-                else lead_commit(&bars[B::kEmpty + i % C::kRing], lead);
+                else lead_commit(&bars[C::empty(i)], lead);
             };
             uint32_t item = 0, kp0 = 0, kp1 = 0, seg = 0;
             int left = count;
             bool ok = true;
             while (ok && __any_sync(0xffffffffu, left > 0)) {
-                ok = all_wait(B::kFull + item % C::kRing, item / C::kRing) && all_wait(B::kQFull, seg);
+                ok = all_wait(C::full(item), C::turns(item)) && all_wait(B::kQFull, seg);
                 if (!ok) break;
                 tc_fence_after();
                 const int steps = s_piece[seg & 7].x;
                 const bool two = __any_sync(0xffffffffu, s_piece[seg & 7].y == 2);
                 ++seg;
                 left -= steps;
-                score(0, item % C::kRing);
-                if (two) score(1, item % C::kRing);
+                score(0, item);
+                if (two) score(1, item);
                 release_k(item);
                 uint32_t add = 0;
                 for (int s = 1;; ++s) {
                     const bool more = __any_sync(0xffffffffu, s < steps);
                     if (!more) lead_commit(&bars[B::kQEmpty], lead);
-                    const uint32_t iv = (item + 1) % C::kRing, ik = (item + 2) % C::kRing;
-                    ok = all_wait(B::kFull + iv, (item + 1) / C::kRing);
-                    if (ok && more) ok = all_wait(B::kFull + ik, (item + 2) / C::kRing);
+                    const uint32_t iv = item + 1, ik = item + 2;
+                    ok = all_wait(C::full(iv), C::turns(iv));
+                    if (ok && more) ok = all_wait(C::full(ik), C::turns(ik));
                     ok = ok && all_wait(B::kP, kp0++);
                     if (!ok) break;
                     tc_fence_after();
@@ -835,11 +962,11 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         if (!ok) break;
                         tc_fence_after();
                         gather(1, iv, add);
-                        if (C::kPairs == 0) lead_commit(&bars[B::kEmpty + iv], lead);
+                        if (C::kPairs == 0) lead_commit(&bars[C::empty(iv)], lead);
                         if (more) score(1, ik);
                         else lead_commit(&bars[B::kO + 1], lead);
                     } else if (C::kPairs == 0) {
-                        lead_commit(&bars[B::kEmpty + iv], lead);
+                        lead_commit(&bars[C::empty(iv)], lead);
                     }
                     if (more) release_k(item + 2);
                     item += 2;
@@ -879,6 +1006,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 if (asked && !here) report(p.r.status, GDR_ERR_INDEX);
                 const int pg = here ? entry : p.c.n_pages, sl = here ? slot : 0, head = u.head;
                 const bool masked = FMT == 0 && step_masked<kTN>(u, u.lo + u.step * kTN);
+                constexpr int kScaled = C::kSplit ? 1 : 0;  // the scales come with the keys or the values
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++item) {
                     const CUtensorMap *map = kv ? &a.tv : &a.tk;
@@ -893,13 +1021,19 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         bar = kv && masked ? B::kLand + b : B::kFull + b;
                         dst = C::kOffRing + b * C::kTile;
                         bytes = C::kTile;
+                    } else if (C::kSplit && kv == 0) {
+                        ok = __all_sync(0xffffffffu, wait(C::empty(item), C::turns(item) + 1));
+                        bar = C::full(item);
+                        dst = C::tile(item);
+                        bytes = C::kRawTile;
                     } else {
-                        const int w = item % C::kRaw;
-                        ok = __all_sync(0xffffffffu, wait(B::kTaken + w, item / C::kRaw + 1));
+                        const uint32_t i = C::kSplit ? item >> 1 : item;
+                        const int w = i % C::kRaw;
+                        ok = __all_sync(0xffffffffu, wait(B::kTaken + w, i / C::kRaw + 1));
                         bar = B::kLand + w;
                         dst = C::kOffRaw + w * C::kRawSize;
                         bytes = C::kRawTile;
-                        if (kv == 0) bytes += __popc(__ballot_sync(0xffffffffu, here)) * box * 8;
+                        if (kv == kScaled) bytes += __popc(__ballot_sync(0xffffffffu, here)) * box * 8;
                     }
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(&bars[bar], bytes);
@@ -912,7 +1046,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                                             c * 64, sl, head, pg);
                         } else {
                             tma_page(sb + dst + lane * box * D, map, &bars[bar], 0, sl, head, pg);
-                            if (kv == 0 && here) {
+                            if (kv == kScaled && here) {
                                 const int64_t so = scale_at(p.c, pg, sl, head);
                                 uint8_t *sc = sm + dst + C::kRawTile + lane * box * 4;
                                 bulk_load(sc, p.c.ks + so, box * 4, &bars[bar]);
@@ -959,10 +1093,10 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
 
 template <typename T, int FMT, int D>
 cudaError_t launch_tiles(const AttnProblem &p, const SplitScratch &ws, int ctas, cudaStream_t st) {
-    using C = TilesCfg<FMT, D>;
+    using C = TilesCfg<T, FMT, D>;
     TilesArgs a{p, ws, 1, p.align};
     a.wide_o = ((reinterpret_cast<uintptr_t>(p.o) | (uintptr_t)(p.so.t * 2) | (uintptr_t)(p.so.h * 2)) & 31u) == 0;
-    if (!page_map(&a.tk, p, p.c.k, p.c.kst, D, a.box, kPagePlain) ||
+    if (!page_map(&a.tk, p, p.c.k, p.c.kst, D, a.box, C::kSplit ? kPageSwizzled : kPagePlain) ||
         !page_map(&a.tv, p, p.c.v, p.c.vst, D, a.box, kPagePlain))
         return cudaErrorInvalidValue;
     // a half's rows are whole tokens: its queries are one box of 128 / G
