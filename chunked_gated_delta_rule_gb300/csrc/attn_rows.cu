@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
             for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float y = fmaxf(m[n][e], x[n][e]);
+                    // each row by its own scores alone
+                    const float y = x[n][e] > m[n][e] + 4.f ? x[n][e] : m[n][e];
                     const float c = y == -INFINITY ? 1.f : ex2(m[n][e] - y);
                     m[n][e] = y;
                     l[n][e] *= c;

@@ -90,6 +90,30 @@ def test_sharp_and_flat_softmax(route, size):
 
 
 @pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt", ["same", "e4m3", "int8"])
+def test_uneven_query_rows(route, dtype, fmt):
+    """One column 2^6 times the others, rows near the least and the largest
+    magnitudes, rows of zeros: the same bounds."""
+    b = Batch([70], [300], heads=4, kv_heads=1, dtype=dtype, fmt=fmt, page=16)
+    b.q[:, 0::5, :, 9] *= 64
+    b.q[:, 0::5] /= 16
+    b.q[:, 1::5] *= 2.0 ** (-120 if dtype == "bf16" else -20)
+    b.q[:, 2::5] = 0
+    o, lse = b.run(force_path=route)
+    check(b, o, lse, *b.attention(), label=f"{route} {dtype} {fmt}")
+    b.q[:, 3, 1, 7], b.q[:, 4, 2, 7], b.q[:, 8, 3, 0] = math.nan, math.inf, -math.inf
+    bad, _ = b.run(force_path=route)
+    rows = [(3, 1), (4, 2), (8, 3)]
+    for t, h in rows:
+        assert bad[t, h].isnan().all() or not torch.isfinite(bad[t, h]).all()
+    keep = torch.ones(70, 4, dtype=torch.bool)
+    for t, h in rows:
+        keep[t, h] = False
+    assert torch.equal(bad.cpu()[keep], o.cpu()[keep])
+
+
+@pytest.mark.parametrize("route", ROUTES)
 def test_masked_places_never_reach_a_row(route):
     """NaN and infinities at positions that only later rows see: the rows
     before them are exact, the rows that see them are not finite."""
