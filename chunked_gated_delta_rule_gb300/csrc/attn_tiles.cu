@@ -46,8 +46,9 @@
 // 16K (4 key heads), 691 with widened keys.
 // Measured (4 key heads of 128, 4 query heads each, BF16, replayed from a graph):
 // 4096 new tokens over 32K: 615 us, 1678 TFLOP/s, 0.86 of a library product's
-// rate; over 16K in E4M3: 490 us, bound by softmax and the helpers, which share
-// the paths to shared memory (every thread reads 128 scales a step); 32 prompts of
+// rate; over 16K in E4M3: 490 us, bound by latency (no
+// unit above 41 %): the chain of a half's softmax, 3K cycles of which a third
+// applies the step's 128 scales, and its products; 32 prompts of
 // 128 to 512 tokens: 71 us, of which a unit costs 6 us beside 1.4 us a step.
 //
 // The steps of the call are shared out equally over one CTA an SM
