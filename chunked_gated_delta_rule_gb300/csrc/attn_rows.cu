@@ -915,9 +915,13 @@ cudaError_t launch_dim(const AttnProblem &p, const SplitScratch &ws, const Split
 
 template <typename T, int M>
 cudaError_t join_dim(const AttnProblem &p, const SplitScratch &ws, int workers, cudaStream_t st) {
-    // many pieces a unit: a CTA for each row of it; few: 8 rows share one
-    const bool many = workers > 8 * p.r.N * p.c.H;
-    const int y = !many ? M / 8 : M <= kRowsMost ? (p.G < M ? p.G : M) : 64;
+    // many pieces a unit (of which there are at least so many): a CTA for each
+    // row of it; few: 8 rows share one, or 32 of a 256-row unit (4096 new tokens
+    // over 16K in E4M3: 484 us the whole call, 486 with 8, 489 with 64 CTAs a
+    // unit, half of them idle)
+    const int64_t tokens = rows_packed(p.r) ? p.r.T : p.r.N * p.r.T, tiles = tokens * p.G / M;
+    const bool many = workers > 8 * (p.r.N > tiles ? p.r.N : tiles) * p.c.H;
+    const int y = !many ? (M > kRowsMost ? M / 32 : M / 8) : M <= kRowsMost ? (p.G < M ? p.G : M) : 64;
     const dim3 g((unsigned)workers, (unsigned)y);
     if (p.V == 64) return launch_pdl(k_attn_join<T, M, 64>, g, dim3(kJoinThreads), 0, st, p, ws);
     return launch_pdl(k_attn_join<T, M, 128>, g, dim3(kJoinThreads), 0, st, p, ws);
