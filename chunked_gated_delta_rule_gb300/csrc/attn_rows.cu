@@ -564,12 +564,13 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
 
         if (!arrived()) return;
         uint8_t *vt = ring + C::tile_at(tile);
-        // what lies past the last position is anything
-        if ((flags & kMask) && base + C::kBN > fi->hi) {
-            const int left = fi->hi - base;
+        // what lies past the last position, or before the first that the tile's
+        // first row sees (steps begin where a box of a page does), is anything
+        const int left = fi->hi - base, before = __shfl_sync(0xffffffffu, lo[0][0], 0) - base;
+        if ((flags & kMask) && (left < C::kBN || before > 0)) {
             for (int i = lane; i < C::kBN * (C::kRow / 16); i += 32) {
                 const int t = i / (C::kRow / 16);
-                if (t >= left)
+                if (t >= left || t < before)
                     *reinterpret_cast<uint4 *>(vt + kv_off<FMT, D>(t, i % (C::kRow / 16))) =
                         make_uint4(0, 0, 0, 0);
             }
