@@ -32,9 +32,12 @@
 // to scores and weights, which costs a thread three loads a column (393 KB of
 // shared-memory traffic a step).  Under BF16 queries o is rounded to 8 bits, so
 // that FP16's 11 are as good as exact for the values: there the products see q
-// s / s_max in FP16, s_max the largest scale of the step's 128 positions, and
-// s_max alone is left to the weights.  The keys' scales stay with the scores:
-// lse is FP32.
+// s / s' in FP16, s' a power of two for the step's 128 positions that brings the
+// largest of them to [2^6, 2^7), and s' alone is left to the weights.  That is
+// as exact for every position down to 2^-18 of the largest; a step of wider
+// spread (a scale whose position a row does not see, or gives no weight, must
+// not cost that row its own values) takes the way of FP16 queries.  The keys'
+// scales stay with the scores: lse is FP32.
 // E4M3 keys of 128 columns under BF16 queries are not widened at all: a row of
 // queries, scaled by a power of two to have its largest magnitude in [2^7, 2^8),
 // is split into two E4M3 parts, x = hi + lo.  hi takes four of BF16's eight bits
@@ -72,6 +75,12 @@ constexpr int kTUnit = 4;
 constexpr float kTLog2e = 1.4426950408889634f;
 constexpr float kTLn2 = 0.6931471805599453f;
 constexpr float kTLeast = 7.888609052210118e-31f;  // 2^-100
+// Values' scales in FP16, less than 2^7 by choice: below this a step is wide.
+// They keep 13 bits there (a part and what it leaves, both above 2^-25).
+constexpr float kTNarrow = 0x1p-12f;
+// log2 s' of a wide step: above any maximum, so that softmax comes to where it
+// rescales its sums (a rare place) and finds the mark there.
+constexpr float kTWide = 0x1p100f;
 
 // Registers a thread of the softmax warps, the helpers and the rest: 128 each
 // at launch, 2 x 192 + 72 + 56 = 4 x 128
@@ -316,6 +325,81 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// A row's maximum m to that of a step's scores, its sum l and its output (at
+// `to`, where there is one) with it.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t to, float mn, float &m, float &l, bool begun) {
+    const float n = mn > m + 8.f ? mn : m;  // each row by its own scores alone
+    const float c = n == -INFINITY ? 1.f : ex2(m - n);
+    m = n;
+    l *= c;
+    if (!begun) return;
+    // O holds the steps before: they are done, as this step's S is
+#pragma unroll 1
+    for (int q = 0; q < D / 16; ++q) {
+        uint32_t o[16];
+        tmem_ld16(to + 16 * q, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
+        tmem_st16(to + 16 * q, o);
+    }
+    tmem_wait_st();
+}
+
+// Softmax of a wide step, from its S at `ts`: t + log2 s over it, the sum of e^t
+// by itself, then the weights, 32 columns at a time (they lie below the columns
+// that they come from).  Columns [c0, c1) are seen; gives {m, l}.  Not inlined, and
+// with a tail of its own: in the middle of the softmax's loop it cost 4096 new
+// tokens over 16K 30 us of 480 without being run once, so 16.
+template <typename TP, int D>
+__device__ __noinline__ float2 wide_step(uint32_t ts, uint32_t to, const float *scale, int c0, int c1, float f,
+                                         float m, float l, bool begun) {
+    const float *lg = scale + kTN + 1;
+    float tm = -INFINITY, mn = -INFINITY, sum = 0.f;
+#pragma unroll 1
+    for (int j0 = 0; j0 < kTN; j0 += 16) {
+        uint32_t x[16];
+        tmem_ld16(ts + j0, x);
+        tmem_wait_ld(x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float t = __uint_as_float(x[e]) * scale[j0 + e] * f;
+            const bool see = j0 + e >= c0 && j0 + e < c1;
+            const float z = see ? t + lg[j0 + e] : -INFINITY;
+            tm = fmaxf(tm, see ? t : -INFINITY);
+            mn = fmaxf(mn, z);
+            x[e] = __float_as_uint(z);
+        }
+        tmem_st16(ts + j0, x);
+    }
+    tmem_wait_st();
+    rescale<D>(to, mn, m, l, begun);
+    const float mu = m == -INFINITY ? 0.f : m, tu = tm == -INFINITY ? 0.f : tm;
+#pragma unroll 1
+    for (int j0 = 0; j0 < kTN; j0 += 32) {
+        uint32_t ph[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t x[16];
+            tmem_ld16(ts + j0 + 16 * h, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float z = __uint_as_float(x[e]);
+                // what a row does not see may have no scale
+                sum += z == -INFINITY ? 0.f : ex2(z - lg[j0 + 16 * h + e] - tu);
+                x[e] = __float_as_uint(ex2(z - mu));
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+                ph[8 * h + (e >> 1)] = pack16<TP>(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        }
+        tmem_st16(ts + j0 / 2, ph);
+    }
+    return make_float2(m, sum == 0.f ? l : l + sum * ex2(tu - mu));
+}
+
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_constant__ TilesArgs a) {
     using C = TilesCfg<T, FMT, D>;
@@ -328,8 +412,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     __shared__ int64_t s_real[2];   // steps of the call before this worker's, and with them
     __shared__ int s_poison[8];  // unit (count, modulo 8) + 1 whose masked values are not finite
     __shared__ int2 s_piece[8];  // steps and halves of the piece (count, modulo 8), for the products
-    __shared__ float s_most[4];          // largest scale of a step's values, by warp
-    __shared__ uint2 s_ratio[kTN];       // scale / largest: FP16 hi and lo, each twice
+    __shared__ uint2 s_span[4];          // largest and least scale of a step's values, by warp
+    __shared__ uint2 s_ratio[kTN];       // scales in the values: FP16 hi and lo, each twice
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort_flag;
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -443,7 +527,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         scale = reinterpret_cast<const float *>(sm + C::kOffScale) + ((done + s) % C::kScales) * 3 * kTN;
                         if constexpr (kFold) {
                             lgs = scale[kTN];
-                            invs = scale[2 * kTN];
+                            invs = scale[2 * kTN + 1];
                         }
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
@@ -492,23 +576,16 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if constexpr (FMT == 0 || kFold) mn = mn == -INFINITY ? mn : fmaf(mn, fs, lgs);
                     if (__any_sync(0xffffffffu, mn > m + 8.f)) {
-                        const float n = mn > m + 8.f ? mn : m;  // each row by its own scores alone
-                        const float c = n == -INFINITY ? 1.f : ex2(m - n);
-                        m = n;
-                        l *= c;
-                        if (s > 0) {  // O holds the steps before: they are done, as this S is
-#pragma unroll 1
-                            for (int q = 0; q < D / 16; ++q) {
-                                uint32_t o[16];
-                                tmem_ld16(to + 16 * q, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * c);
-                                tmem_st16(to + 16 * q, o);
-                            }
+                        if (kFold && lgs == kTWide) {
+                            const float2 ml = wide_step<TP, D>(ts, to, scale, lo - base, hi - base, f, m, l, s > 0);
+                            m = ml.x;
+                            l = ml.y;
                             tmem_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(&bars[B::kP + half]);
+                            continue;
                         }
+                        rescale<D>(to, mn, m, l, s > 0);
                     }
                     const float mu = m == -INFINITY ? 0.f : m;
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -817,24 +894,38 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         if (!ok) break;
                     }
                     if (kFold && scales) {
-                        // the values' largest scale, and every row's part of it
-                        float vm = isfinite(vs) ? vs : 0.f;
-#pragma unroll
-                        for (int d = 16; d; d >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
-                        if (lane == 0) s_most[warp - 8] = vm;
+                        // the span of the values' scales, and every row's part of
+                        // the largest (rows of zeros and rows without a scale aside)
+                        const bool some = vs > 0.f && isfinite(vs);
+                        const uint32_t bits = __float_as_uint(vs);  // in their values' order
+                        const uint32_t most = __reduce_max_sync(0xffffffffu, some ? bits : 0u);
+                        const uint32_t least = __reduce_min_sync(0xffffffffu, some ? bits : 0x7f800000u);
+                        if (lane == 0) s_span[warp - 8] = make_uint2(most, least);
                         float *sc = reinterpret_cast<float *>(sm + C::kOffScale) + (it % C::kScales) * 3 * kTN;
                         sc[t] = ks;
                         if (!together()) break;
-                        vm = fmaxf(kTLeast, fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3])));
-                        const float part = __fdividef(vs, vm);
+                        const uint2 s0 = s_span[0], s1 = s_span[1], s2 = s_span[2], s3 = s_span[3];
+                        const uint32_t vm = max(max(s0.x, s1.x), max(s2.x, s3.x));
+                        const float vl = __uint_as_float(min(min(s0.y, s1.y), min(s2.y, s3.y)));
+                        // s' = 2^(at - 127): the largest, rounded up to a power of
+                        // two, over 2^7; 2^-100 at least, so that 1 / s' leaves room
+                        const int at = max((int)(vm >> 23) - 6, 27);
+                        const float inv = __int_as_float((254 - at) << 23);
+                        float part = vs * inv, lgs = (float)(at - 127), invs = inv;
+                        if (__builtin_expect(vl * inv < kTNarrow, 0)) {  // wide
+                            sc[kTN + 1 + t] = __log2f(vs < kTLeast ? kTLeast : vs);
+                            part = fminf(vs * 0x1p100f, 1.f);  // what 2^-100 leaves of smaller ones
+                            lgs = kTWide;
+                            invs = 0.f;
+                        }
+                        if (t == 0) {
+                            sc[kTN] = lgs;
+                            sc[2 * kTN + 1] = invs;
+                        }
                         const __half2 hi = __float2half2_rn(part);
                         const __half2 lo = __float2half2_rn(part - __low2float(hi));
                         s_ratio[t] = make_uint2(*reinterpret_cast<const uint32_t *>(&hi),
                                                 *reinterpret_cast<const uint32_t *>(&lo));
-                        if (t == 0) {
-                            sc[kTN] = __log2f(vm);
-                            sc[2 * kTN] = __fdividef(1.f, vm);
-                        }
                         if (C::kSplit) mbar_arrive(&bars[C::full(2 * item)]);
                         if (!together()) break;
                     }

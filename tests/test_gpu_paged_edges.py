@@ -33,3 +33,37 @@ def test_positions_that_left_the_window(route, dtype, fmt, q_len, heads):
             b.ks[page, :, slot] = math.nan
     check(b, *b.run(force_path=route, window=37), *b.attention(window=37),
           label=f"{route} {dtype} {fmt} {q_len} {heads}")
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt,K", [("e4m3", 128), ("int8", 128), ("e4m3", 64)])
+@pytest.mark.parametrize("bits", [8, 16, 20, 24, 30, 60])
+def test_one_value_far_larger_than_the_others(route, dtype, fmt, K, bits):
+    """A value 2^bits times the others: of a later token, of one below the
+    window, of one with next to no weight.  The rows that do not take it keep
+    their own values."""
+    b = Batch([50], [150], heads=2, kv_heads=1, K=K, dtype=dtype, fmt=fmt, page=16)
+
+    def place(at):
+        return int(b.table[0, at // 16]), 0, at % 16
+
+    vs, kc, ks = b.vs.clone(), b.kc.clone(), b.ks.clone()
+    most = float(vs.nan_to_num().max()) * (127 if fmt == "int8" else 448)
+    big = min(2.0 ** bits, torch.finfo(b.q.dtype).max / (4 * most))  # the output fits its type
+    b.vs[place(149)] *= big
+    check(b, *b.run(force_path=route), *b.attention(), label=f"later {bits}")
+    b.vs = vs.clone()
+    b.vs[place(75)] *= big
+    ref_o, ref_lse = b.attention(window=40)
+    check(b, *b.run(force_path=route, window=40), ref_o, ref_lse, label=f"window {bits}")
+    # queries above 0, a key of equal and very negative columns
+    b.vs = vs.clone()
+    b.vs[place(90)] *= big
+    b.q = b.q.abs()
+    page, _, slot = place(90)
+    b.kc[page, slot, 0] = torch.full((K,), -120.0).to(kc.dtype)
+    b.ks[place(90)] = 0.5
+    ref_o, ref_lse = b.attention()
+    assert float(ref_o.abs().max()) < 100  # the value takes no part
+    check(b, *b.run(force_path=route), ref_o, ref_lse, label=f"weightless {bits}")
