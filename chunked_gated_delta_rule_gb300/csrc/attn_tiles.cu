@@ -39,20 +39,23 @@
 // not cost that row its own values) takes the way of FP16 queries.  The keys'
 // scales stay with the scores: lse is FP32.
 // E4M3 keys of 128 columns under BF16 queries are not widened at all: a row of
-// queries, scaled by a power of two to have its largest magnitude in [2^7, 2^8),
-// is split into two E4M3 parts, x = hi + lo.  hi takes four of BF16's eight bits
-// and leaves at most four, so the split is exact for components down to 2^-9 of
-// the row's largest; what smaller ones lose is at most 2^-17 of the largest, 2^-8
-// of what BF16 itself rounded off that one.  S = hi K^T + lo K^T takes two E4M3
-// products at twice the rate of one FP16 product, so no longer, and the keys go
-// from the cache into the products as they are: 490 us for 4096 new tokens over
-// 16K (4 key heads), 691 with widened keys.
+// queries, scaled by a power of two to have its largest magnitude in [2^14, 2^15),
+// is split into three E5M2 parts, each what the ones before it leave.  Rounded to
+// nearest, the first takes three of BF16's eight bits and leaves at most four, the
+// second three of those and leaves one, so the split is exact for components down
+// to 2^-23 of the row's largest (FP16 queries: 2^-17), however little the largest,
+// an outlier channel say, has to do with the softmax.  Two E4M3 parts are exact
+// down to 2^-9 only: with one channel of 2^10 where the keys do not vary, o was
+// 4.9e-3 off.  S = (a + b + c) K^T takes three 8-bit products at twice the rate of
+// one FP16 product, and the keys go from the cache into the products as they are:
+// 525 us for 4096 new tokens over 16K (4 key heads; two parts: 524), 691 with
+// widened keys.  The third part's room is that of a second 8-bit tile of values.
 // Measured (4 key heads of 128, 4 query heads each, BF16, replayed from a graph):
 // 4096 new tokens over 32K: 615 us, 1678 TFLOP/s, 0.86 of a library product's
-// rate; over 16K in E4M3: 490 us, bound by latency (no
-// unit above 41 %): the chain of a half's softmax, 3K cycles of which a third
-// applies the step's 128 scales, and its products; 32 prompts of
-// 128 to 512 tokens: 71 us, of which a unit costs 6 us beside 1.4 us a step.
+// rate; over 16K in E4M3: 525 us, bound by latency: the chain of a half's
+// softmax, 3K cycles of which a third applies the step's 128 scales, and its
+// products; 32 prompts of 128 to 512 tokens: 71 us, of which a unit costs 6 us
+// beside 1.4 us a step.
 //
 // The steps of the call are shared out equally over one CTA an SM
 // (attn_split.cuh).  Every wait is bounded: on expiry the CTA records
@@ -84,29 +87,30 @@ constexpr float kTWide = 0x1p100f;
 
 // Registers a thread of the softmax warps, the helpers and the rest: 128 each
 // at launch, 2 x 192 + 72 + 56 = 4 x 128
-// (184 / 88 / 56: 515 us instead of 490 for 4096 new tokens over 16K in E4M3,
-// where softmax spills more).
+// (4096 new tokens over 16K in E4M3: 525 us; 184 / 88 / 56 spills more in the
+// softmax, 200 / 64 / 48 in the helpers: 556).
 constexpr int kRegSoftmax = 192, kRegHelp = 72, kRegRest = 56;
 static_assert(2 * kRegSoftmax + kRegHelp + kRegRest <= 4 * 128, "the launch's registers");
 
 template <typename T, int FMT, int D>
 struct TilesCfg {
-    // E4M3 keys as they are, the queries in two E4M3 parts (above)
+    // E4M3 keys as they are, the queries in three E5M2 parts (above)
     static constexpr bool kSplit = FMT == 1 && D == 128 && std::is_same<T, __nv_bfloat16>::value;
     static constexpr uint32_t kTile = kTN * D * 2;     // a 128-row tile of 16-bit values
+    static constexpr uint32_t kQTile = kSplit ? kTN * D * 3 : kTile;  // a half's queries
     // tiles of keys and values, or of values alone beside kKeys of keys
     static constexpr int kRing = D == 64 ? 8 : kSplit ? 2 : FMT ? 3 : 4;
     static constexpr int kKeys = kSplit ? 2 : 0;
     // tiles given back in pairs, a step's keys and the values before them
     // (one commit a step instead of two); 0: one by one
     static constexpr int kPairs = FMT ? 0 : kRing / 2;
-    static constexpr int kRaw = FMT ? 2 : 0;                 // 8-bit tiles on their way
+    static constexpr int kRaw = !FMT ? 0 : kSplit ? 1 : 2;                 // 8-bit tiles on their way
     static constexpr uint32_t kRawTile = kTN * D, kRawSize = kRawTile + 2 * kTN * 4;
     // steps whose scales are kept: a step's keys are widened once the products
     // of the step kRing / 2 before it are done, so that softmax is at most
     // that far behind
     static constexpr int kScales = FMT ? (D == 64 ? 8 : 4) : 0;
-    static constexpr uint32_t kOffRing = 2 * kTile;    // after the queries
+    static constexpr uint32_t kOffRing = 2 * kQTile;   // after the queries
     static constexpr uint32_t kOffKeys = kOffRing + kRing * kTile;
     static constexpr uint32_t kOffRaw = kOffKeys + kKeys * kRawTile; // + scales of keys, values
     static constexpr uint32_t kOffScale = kOffRaw + kRaw * kRawSize; // [kScales][3][128]
@@ -229,14 +233,24 @@ __device__ __forceinline__ bool help_sync(bool ok) {
     return r != 0;
 }
 
-// Four values in E4M3, in order, to nearest even; NaN stays NaN.
-__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
+// Four values in E5M2, in order, to nearest even (NaN stays NaN), and back.
+__device__ __forceinline__ uint32_t e5m2x4(float x0, float x1, float x2, float x3) {
     uint32_t y;
-    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e5m2x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
         : "=r"(y)
         : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
     return y;
+}
+__device__ __forceinline__ float4 wide5(uint32_t x) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e5m2x2 %0, a;\n\tcvt.rn.f16x2.e5m2x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // Two BF16 values of a row that holds an infinity or a NaN: an infinity becomes
@@ -260,7 +274,7 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&x)[8]) {
 }
 
 // Instruction descriptor: A and B of type T, A K-major, FP32 sums, M = 128.
-// E4M3 operands have FP16's number.
+// E4M3 operands have FP16's number, E5M2 ones BF16's.
 template <typename T>
 __host__ __device__ constexpr uint32_t tiles_idesc(int N, int b_mn) {
     const uint32_t f = std::is_same<T, __half>::value ? 0u : 1u;
@@ -738,7 +752,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                 }
                 return live;
             };
-            auto dst = [&](int r) { return (r >> 7) * C::kTile + sw128_chunk(r & 127, qc, 128); };
+            auto dst = [&](int r) { return (r >> 7) * C::kQTile + sw128_chunk(r & 127, qc, 128); };
             if constexpr (kConvert) {
                 // FP16 of the row's own power of two (see attn_rows.cu), four
                 // rows' loads at a time
@@ -764,34 +778,34 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         const int ex = (int)(big >> 7), r = r0 + i * kQP;
                         float back;
                         if constexpr (C::kSplit) {
-                            // the largest magnitude into [2^7, 2^8); a row with an
+                            // the largest magnitude into [2^14, 2^15); a row with an
                             // infinity is its infinities' signs, times infinity
-                            const int at = max(ex, 8);
-                            const float g = __int_as_float((261 - at) << 23);
-                            back = ex == 255 ? INFINITY : __int_as_float((at - 7) << 23);
-                            uint32_t hi[2], lo[2];
-#pragma unroll
+                            const int at = max(ex, 15);
+                            const float g = ex == 255 ? 1.f : __int_as_float((268 - at) << 23);
+                            back = ex == 255 ? INFINITY : __int_as_float((at - 14) << 23);
+                            // first the 128 columns of the first part, then the next's
+                            const uint32_t row = (r >> 7) * C::kQTile + (qc & 1) * 8;
+#pragma unroll 1
                             for (int e = 0; e < 2; ++e) {
-                                uint2 y = make_uint2(w[2 * e], w[2 * e + 1]);
+                                uint2 v = e ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
                                 if (ex == 255) {
-                                    y.x = signs_of_infinities(y.x);
-                                    y.y = signs_of_infinities(y.y);
+                                    v.x = signs_of_infinities(v.x);
+                                    v.y = signs_of_infinities(v.y);
                                 }
-                                const float x0 = __uint_as_float(y.x << 16) * (ex == 255 ? 1.f : g);
-                                const float x1 = __uint_as_float(y.x & 0xffff0000u) * (ex == 255 ? 1.f : g);
-                                const float x2 = __uint_as_float(y.y << 16) * (ex == 255 ? 1.f : g);
-                                const float x3 = __uint_as_float(y.y & 0xffff0000u) * (ex == 255 ? 1.f : g);
-                                hi[e] = e4m3x4(x0, x1, x2, x3);
-                                uint32_t a0, a1;
-                                widen4<1>(hi[e], a0, a1);
-                                const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&a0));
-                                const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&a1));
-                                lo[e] = e4m3x4(x0 - f0.x, x1 - f0.y, x2 - f1.x, x3 - f1.y);
+                                float f0 = __uint_as_float(v.x << 16) * g, f1 = __uint_as_float(v.x & 0xffff0000u) * g;
+                                float f2 = __uint_as_float(v.y << 16) * g, f3 = __uint_as_float(v.y & 0xffff0000u) * g;
+#pragma unroll
+                                for (int i = 0; i < 3; ++i) {
+                                    const uint32_t y = e5m2x4(f0, f1, f2, f3);
+                                    *reinterpret_cast<uint32_t *>(sm + row + sw128_chunk(r & 127, 8 * i + (qc >> 1), 128) +
+                                                                  4 * e) = y;
+                                    const float4 h = wide5(y);
+                                    f0 -= h.x;
+                                    f1 -= h.y;
+                                    f2 -= h.z;
+                                    f3 -= h.w;
+                                }
                             }
-                            // first the 128 columns of hi, then those of lo
-                            const uint32_t row = (r >> 7) * C::kTile + (qc & 1) * 8;
-                            *reinterpret_cast<uint2 *>(sm + row + sw128_chunk(r & 127, qc >> 1, 128)) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2 *>(sm + row + sw128_chunk(r & 127, 8 + (qc >> 1), 128)) = make_uint2(lo[0], lo[1]);
                         } else {
                             const bool normal = ex > 0 && ex < 254;
                             const float g = normal ? __int_as_float((254 - ex) << 23) : 1.f;
@@ -985,7 +999,8 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
         if (warp == 12) {
             // -------------------------------------------------- products
             // loops and conditions go by votes, so that they are uniform
-            constexpr uint32_t kIdS = tiles_idesc<TP>(128, 0), kIdO = tiles_idesc<TP>(D, 1);
+            constexpr uint32_t kIdS = tiles_idesc<TP>(128, 0) | (C::kSplit ? 1u << 7 : 0u);  // E5M2 times E4M3
+            constexpr uint32_t kIdO = tiles_idesc<TP>(D, 1);
             const uint32_t lead = elect_lead();
             auto all_wait = [&](int b, uint32_t parity) {
                 return (bool)__all_sync(0xffffffffu, wait(b, parity));
@@ -994,11 +1009,11 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             // address is their low 14 bits, in units of 16 bytes
             const uint64_t dk0 = sdesc_sw128(sb, 16, 1024), dv0 = sdesc_sw128(sb, 16384, 1024);
             auto score = [&](int half, uint32_t i) {
-                const uint64_t q = dk0 + half * (C::kTile >> 4);
+                const uint64_t q = dk0 + half * (C::kQTile >> 4);
                 const uint64_t kt = dk0 + (C::tile(i) >> 4);
-                if constexpr (C::kSplit) {  // hi, then lo, with the same keys
+                if constexpr (C::kSplit) {  // the parts one by one, with the same keys
 #pragma unroll
-                    for (int d = 0; d < 8; ++d)
+                    for (int d = 0; d < 12; ++d)
                         lead_mma8(tmem + C::kColS + half * 128, q + (((d >> 2) * 16384 + (d & 3) * 32) >> 4),
                                   kt + (((d & 3) * 32) >> 4), kIdS, d > 0, lead);
                 } else {
@@ -1152,11 +1167,11 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         ok = __all_sync(0xffffffffu, wait(B::kQEmpty, seg + 1));
                         if (!ok) break;
                         const int halves = unit_rows<kTM>(p, u) > 128 ? 2 : 1;
-                        if (lane == 0) mbar_arrive_expect_tx(&bars[B::kQFull], halves * C::kTile);
+                        if (lane == 0) mbar_arrive_expect_tx(&bars[B::kQFull], halves * C::kQTile);
                         __syncwarp();
                         if (lane < halves * (D / 64)) {
                             const int h = lane / (D / 64), c = lane % (D / 64);
-                            tma_load_3d(sm + h * C::kTile + c * 16384, &a.tq, &bars[B::kQFull], c * 64,
+                            tma_load_3d(sm + h * C::kQTile + c * 16384, &a.tq, &bars[B::kQFull], c * 64,
                                         u.head * p.G, u.t0 + (u.tile * 2 + h) * a.q_box);
                         }
                     }

@@ -67,3 +67,21 @@ def test_one_value_far_larger_than_the_others(route, dtype, fmt, K, bits):
     ref_o, ref_lse = b.attention()
     assert float(ref_o.abs().max()) < 100  # the value takes no part
     check(b, *b.run(force_path=route), ref_o, ref_lse, label=f"weightless {bits}")
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt,K", [("e4m3", 128), ("int8", 128), ("e4m3", 64)])
+@pytest.mark.parametrize("bits", [6, 9, 10, 12, 14])
+def test_outlier_channel_of_the_queries(route, dtype, fmt, K, bits):
+    """One channel of the queries 2^bits, where the keys do not vary: it adds the
+    same to every score, and the softmax is that of the other channels."""
+    b = Batch([70], [300], heads=4, kv_heads=1, K=K, dtype=dtype, fmt=fmt, page=16)
+    g = torch.Generator().manual_seed(7)
+    size = 60.0 if fmt == "e4m3" else 20.0
+    b.kc = (size * torch.randn(b.kc.shape, generator=g)).clamp(-120, 120)
+    b.kc = (b.kc if fmt == "e4m3" else b.kc.round()).to(b.vc.dtype)
+    b.kc[..., 9] = torch.full(b.kc.shape[:-1], 32.0).to(b.kc.dtype)
+    b.ks[:] = 1 / size
+    b.q[..., 9] = 2.0 ** bits
+    check(b, *b.run(force_path=route), *b.attention(), label=f"{route} {dtype} {fmt} {K} {bits}")
