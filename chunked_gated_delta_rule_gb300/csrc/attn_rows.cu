@@ -193,10 +193,11 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
     const int qr = lane >> 2, qc = lane & 3;
     pdl_trigger();
     SplitLine<kM, C::kBN, kRowsUnit> line;
-    line.measure(p);
+    const bool formed = line.measure(p);
     const int64_t total = line.total;
     const int64_t worker = (int64_t)blockIdx.x * C::kWarps + warp;
     int64_t nw = (int64_t)gridDim.x * C::kWarps;
+    if (!formed) clear_unheld(p, worker, nw);
     if (nw * a.min_steps > total) nw = quotient(total + a.min_steps - 1, a.min_steps);
     if (lane == 0) a.ws.rec[worker] = make_int4(0, 0, 0, 0);
     if (worker >= nw) return;

@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(32 * kAWarps) k_attn_simt(AttnProblem p) {
     const int64_t kv = cached_len(p.c, n, p.r.status);
     int lo = 0, hi = 0;
     if (t >= t0 && t < t0 + len) visible(p, (int)kv, (int)(kv - len + (t - t0)), lo, hi);
+    if (row == 0) check_offsets(p.r);
 
     const Tio *q = reinterpret_cast<const Tio *>(p.q) + tok_at(p.sq, t, h);
     for (int d = lane; d < p.K; d += 32) sq[warp][d] = (float)q[d] * p.scale;

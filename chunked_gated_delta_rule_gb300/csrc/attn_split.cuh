@@ -41,7 +41,9 @@ struct Unit {
 };
 
 // The sequence's part of a unit.  Returns 0 or the code to report; nothing
-// outside the call's tokens and the page table's row is addressed after it.
+// outside the call's tokens and the page table's row is addressed after it.  A
+// packed table that does not begin at 0 or end at T is malformed, though each of
+// its sequences may be well.
 __device__ __forceinline__ int load_seq(const AttnProblem &p, int64_t n, Unit &u) {
     const int64_t t0 = row_bound(p.r, n), end = row_bound(p.r, n + 1);
     const int kv = p.c.kv_lens[n];
@@ -50,15 +52,43 @@ __device__ __forceinline__ int load_seq(const AttnProblem &p, int64_t n, Unit &u
     u.t0 = (int)t0;
     u.len = (int)(end - t0);
     u.kv = kv;
-    if (rows_packed(p.r) && (t0 < 0 || end < t0 || end > p.r.T)) {
-        code = GDR_ERR_SEQLENS;
-        u.t0 = u.len = 0;
-    }
     if (kv < 0 || kv > cap) {
         code = GDR_ERR_INDEX;
         u.kv = kv < 0 ? 0 : cap;
     }
+    if (rows_packed(p.r)) {
+        if (t0 < 0 || end < t0 || end > p.r.T) {
+            code = GDR_ERR_SEQLENS;
+            u.t0 = u.len = 0;
+        } else if ((n == 0 && t0 != 0) || (n == p.r.N - 1 && end != p.r.T)) {
+            code = GDR_ERR_SEQLENS;
+        }
+    }
     return code;
+}
+
+// The tokens that no sequence of a malformed table holds have o = 0 and lse = -inf.
+// Warp w of nw takes every nw-th token; 16-bit o, rows on 16-byte boundaries.
+__device__ __forceinline__ void clear_unheld(const AttnProblem &p, int64_t w, int64_t nw) {
+    const int lane = threadIdx.x & 31, chunks = p.V / 8;
+#pragma unroll 1
+    for (int64_t t = w; t < p.r.T; t += nw) {
+        bool held = false;
+#pragma unroll 1
+        for (int64_t n = lane; n < p.r.N; n += 32) {
+            const int64_t t0 = row_bound(p.r, n), end = row_bound(p.r, n + 1);
+            held |= t0 >= 0 && end <= p.r.T && t0 <= t && t < end;
+        }
+        if (__any_sync(0xffffffffu, held)) continue;
+#pragma unroll 1
+        for (int i = lane; i < p.Hq * chunks; i += 32) {
+            const int h = i / chunks;
+            uint16_t *o = reinterpret_cast<uint16_t *>(p.o) + tok_at(p.so, t, h);
+            reinterpret_cast<uint4 *>(o)[i - h * chunks] = make_uint4(0, 0, 0, 0);
+        }
+        if (p.lse)
+            for (int h = lane; h < p.Hq; h += 32) p.lse[t * p.Hq + h] = -INFINITY;
+    }
 }
 
 template <int M>
@@ -121,11 +151,13 @@ struct SplitLine {
     int64_t per;
     static constexpr int kFew = 16;  // more tiles of a sequence are shared out among the lanes
 
-    __device__ __forceinline__ void measure(const AttnProblem &p) {
+    // Whether the table of offsets is well formed.
+    __device__ __forceinline__ bool measure(const AttnProblem &p) {
         const int lane = threadIdx.x & 31;
         per = (p.r.N + 31) >> 5;
         int64_t x = 0, y = 0;
         int code = 0;
+        bool malformed = false;
 #pragma unroll 4
         for (int64_t k = 0; k < per; ++k) {
             const int64_t n = lane * per + k;
@@ -133,6 +165,7 @@ struct SplitLine {
             if (n < p.r.N) {
                 const int c = load_seq(p, n, u);
                 code = c ? c : code;
+                malformed |= c == GDR_ERR_SEQLENS;
             }
             const int tiles = tiles_of<M>(p, u.len);
             y += tiles;
@@ -165,6 +198,7 @@ struct SplitLine {
         units = U0 ? __shfl_sync(0xffffffffu, y, 31) : 0;
         line0 = x - line0;
         units0 = y - units0;
+        return !__any_sync(0xffffffffu, malformed);
     }
 
     // The unit and step at `at` (0 <= at < total), and the steps of the call

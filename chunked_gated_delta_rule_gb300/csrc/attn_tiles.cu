@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
     if (warp == 12) tmem_alloc(&s_tmem, 512);
     if (warp < 2) {  // where the share begins, and where it ends
         SplitLine<kTM, kTN, kTUnit> line;
-        line.measure(p);
+        if (!line.measure(p)) clear_unheld(p, (int64_t)blockIdx.x * 2 + warp, (int64_t)gridDim.x * 2);
         const int64_t total = line.total, w = blockIdx.x;
         int64_t nw = gridDim.x;
         if (nw * a.min_steps > total) nw = quotient(total + a.min_steps - 1, a.min_steps);

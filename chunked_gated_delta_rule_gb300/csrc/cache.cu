@@ -193,7 +193,7 @@ __device__ __forceinline__ void find_places(const RowArgs &a, int64_t first, int
             len = a.c.kv_lens[seq];
         }
         int page = -1, slot = 0;
-        if (rows_packed(a.r) && (t < begin || t >= end || end > a.r.T)) {
+        if (rows_packed(a.r) && (begin < 0 || t < begin || t >= end || end > a.r.T)) {
             report(a.r.status, GDR_ERR_SEQLENS);
         } else {
             const int64_t pos = (int64_t)len - (end - t);
@@ -255,7 +255,8 @@ __device__ __forceinline__ void write_row(const Eight<Tin> &x, bool live, Tc *ds
     }
 }
 
-// Both kernels: a warp takes every so-manieth chunk of rows.
+// Both kernels: a warp takes every so-manieth chunk of rows.  The table of offsets
+// is looked over by a warp that calls of few rows leave idle.
 template <typename Tin, typename Tc, bool VEC>
 __global__ void __launch_bounds__(kCThreads, kBlocksPerSm) k_cache_write(RowArgs a) {
     __shared__ Place s_places[kWarps][32];
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kCThreads, kBlocksPerSm) k_cache_write(RowArgs
     const int groups = 32 / a.lanes, group = (threadIdx.x & 31) / a.lanes;
     const int sub = threadIdx.x & (a.lanes - 1), d = sub * 8;
     const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (warp == kWarps - 1) check_offsets(a.r);
     for (int64_t first = warp * a.chunk; first < a.rows; first += (int64_t)gridDim.x * kWarps * a.chunk) {
         const int n = (int)(a.rows - first < a.chunk ? a.rows - first : a.chunk);
         __syncwarp();
@@ -317,6 +319,7 @@ __global__ void __launch_bounds__(kCThreads, kBlocksPerSm) k_cache_read(RowArgs 
     const int groups = 32 / a.lanes, group = (threadIdx.x & 31) / a.lanes;
     const int sub = threadIdx.x & (a.lanes - 1), d = sub * 8;
     const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (warp == kWarps - 1) check_offsets(a.r);
     Tout *ko = const_cast<Tout *>(reinterpret_cast<const Tout *>(a.k));
     Tout *vo = const_cast<Tout *>(reinterpret_cast<const Tout *>(a.v));
     for (int64_t first = warp * a.chunk; first < a.rows; first += (int64_t)gridDim.x * kWarps * a.chunk) {

@@ -54,6 +54,16 @@ __device__ __forceinline__ void seq_span(const TokenRows &r, int64_t n, int64_t 
     }
 }
 
+// Reports a packed table that does not run from 0 to T without a step back.  A
+// warp's work; the kernels whose warps each look at a few sequences have one do it.
+__device__ __forceinline__ void check_offsets(const TokenRows &r) {
+    if (!rows_packed(r)) return;
+    bool bad = row_bound(r, 0) != 0 || row_bound(r, r.N) != r.T;
+#pragma unroll 4
+    for (int64_t n = threadIdx.x & 31; n < r.N; n += 32) bad |= row_bound(r, n + 1) < row_bound(r, n);
+    if (bad) report(r.status, GDR_ERR_SEQLENS);
+}
+
 // Cached tokens of sequence n, cut to what its row of the page table holds.
 __device__ __forceinline__ int64_t cached_len(const PagedCache &c, int64_t n, int32_t *status) {
     const int64_t cap = c.max_pages * c.page_size;

@@ -358,6 +358,9 @@ int gdr_chunk_bwd(const gdr_dims *dims, const void *q, const void *k,
  * tensors is read or written, such a length counts as the nearest one inside,
  * a token of such a page is not stored and reads as zeros, and what the
  * attention gives for its sequence is unspecified.
+ * A malformed cu_seqlens sets GDR_ERR_SEQLENS, and the sequences that lie within
+ * [0, T) are still done (where they overlap, in any order).  A token that none of
+ * them holds is not stored, reads as zeros and gets o = 0, lse = -inf.
  */
 typedef struct gdr_paged_cache {
     void *k, *v;               /* pages of keys [.., K] and of values [.., V]  */

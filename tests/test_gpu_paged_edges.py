@@ -85,3 +85,57 @@ def test_outlier_channel_of_the_queries(route, dtype, fmt, K, bits):
     b.ks[:] = 1 / size
     b.q[..., 9] = 2.0 ** bits
     check(b, *b.run(force_path=route), *b.attention(), label=f"{route} {dtype} {fmt} {K} {bits}")
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("cu,held", [([3, 7, 8], [(3, 7), (7, 8)]), ([0, 4, 6], [(0, 4), (4, 6)]),
+                                     ([0, 6, 2, 8], None),
+                                     ([0, 4, 100], [(0, 4)]), ([-4, 4, 8], [(4, 8)]), ([0, 9, 8], [])])
+def test_tokens_that_no_sequence_holds(route, cu, held):
+    """Offsets that do not run from 0 to T: reported; the tokens of sequences
+    that are within T get their results, the others o = 0 and lse = -inf."""
+    b = Batch([8], [30], heads=2, kv_heads=1, dtype="bf16", page=16)
+    table = b.table.repeat(len(cu) - 1, 1).cuda()
+    lens = torch.full((len(cu) - 1,), 30, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = torch.full((1, 8, 2, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, 8, 2), math.nan, device="cuda")
+    pkg.gdr_paged_attn(b.on("q"), b.on("kc"), b.on("vc"), table, lens,
+                       torch.tensor(cu, dtype=torch.int32, device="cuda"), force_path=route,
+                       status=status, o=o, lse=lse)
+    assert int(status) == -5
+    if held is None:  # sequences that overlap: in any order
+        return
+    loose = torch.ones(8, dtype=torch.bool)
+    for t0, t1 in held:
+        part = Batch([t1 - t0], [30], heads=2, kv_heads=1, dtype="bf16", page=16)
+        part.table, part.kc, part.vc, part.q = b.table, b.kc, b.vc, b.q[:, t0:t1]
+        check(part, o[0, t0:t1], lse[0, t0:t1], *part.attention(), label=f"{cu} {t0}")
+        loose[t0:t1] = False
+    assert (o[0].cpu()[loose] == 0).all() and (lse[0].cpu()[loose] == -math.inf).all()
+
+
+@pytest.mark.parametrize("cu,held", [([3, 7, 8], [3, 4, 5, 6, 7]), ([0, 4, 6], [0, 1, 2, 3, 4, 5]),
+                                     ([0, 4, 100], [0, 1, 2, 3]), ([-4, 4, 8], [4, 5, 6, 7]),
+                                     ([0, 9, 8], []), ([0, 6, 2, 8], None)])
+def test_cache_rows_that_no_sequence_holds(cu, held):
+    """The same tables: such tokens are not stored and read as zeros."""
+    n = len(cu) - 1
+    b = Batch([8], [8], heads=1, kv_heads=1, K=32, page=8, dtype="bf16")
+    kc, vc = (torch.full((n, 8, 1, 32), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[:, None]
+    lens = torch.full((n,), 8, dtype=torch.int32, device="cuda")
+    cu_dev = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    pkg.gdr_cache_write(b.on("k"), b.on("v"), kc, vc, table, lens, cu_dev, status=status[:1])
+    k, v = pkg.gdr_cache_read(kc, vc, table, lens, 8, cu_dev, status=status[1:])
+    assert status.tolist() == [-5, -5]
+    if held is None:
+        return
+    for got, cache, x in ((k, kc, b.k), (v, vc, b.v)):
+        want, pages = torch.zeros_like(x), torch.full((n, 8, 1, 32), 7.0, dtype=torch.bfloat16)
+        for t in held:
+            seq = max(i for i in range(n) if cu[i] <= t < cu[i + 1])
+            want[0, t] = x[0, t]
+            pages[seq, 8 - (cu[seq + 1] - t)] = x[0, t]
+        assert torch.equal(got.cpu(), want) and torch.equal(cache.cpu(), pages)
