@@ -197,7 +197,7 @@ __device__ __forceinline__ void find_places(const RowArgs &a, int64_t first, int
             report(a.r.status, GDR_ERR_SEQLENS);
         } else {
             const int64_t pos = (int64_t)len - (end - t);
-            if (pos >= a.c.max_pages * a.c.page_size) {
+            if (len < 0 || len > a.c.max_pages * a.c.page_size) {  // no token has a place
                 report(a.r.status, GDR_ERR_INDEX);
             } else if (pos >= 0) {
                 const unsigned pi = (unsigned)pos / (unsigned)a.c.page_size;

@@ -355,9 +355,10 @@ int gdr_chunk_bwd(const gdr_dims *dims, const void *q, const void *k,
  *             side by side.
  * A length outside [0, max_pages * page_size] or a page outside
  * [0, n_pages) sets GDR_ERR_INDEX in the status word: nothing outside the
- * tensors is read or written, such a length counts as the nearest one inside,
- * a token of such a page is not stored and reads as zeros, and what the
- * attention gives for its sequence is unspecified.
+ * tensors is read or written.  The tokens of a sequence of such a length, and
+ * those of such a page, are not stored and read as zeros; the attention takes
+ * the nearest length inside, and what it gives for a sequence with such a page
+ * is unspecified.
  * A malformed cu_seqlens sets GDR_ERR_SEQLENS, and the sequences that lie within
  * [0, T) are still done (where they overlap, in any order).  A token that none of
  * them holds is not stored, reads as zeros and gets o = 0, lse = -inf.

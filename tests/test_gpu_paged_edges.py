@@ -139,3 +139,31 @@ def test_cache_rows_that_no_sequence_holds(cu, held):
             want[0, t] = x[0, t]
             pages[seq, 8 - (cu[seq + 1] - t)] = x[0, t]
         assert torch.equal(got.cpu(), want) and torch.equal(cache.cpu(), pages)
+
+
+@pytest.mark.parametrize("length,stands_for", [(-5, 0), (65, 64), (1 << 30, 64), (-(1 << 31), 0)])
+def test_lengths_outside_the_table(length, stands_for):
+    """Reported; the sequence's tokens are neither stored nor read, the attention
+    takes the nearest length inside; the other sequence is untouched by it."""
+    b = Batch([4, 4], [64, 30], heads=2, kv_heads=1, K=64, page=16, dtype="bf16")
+    cu, table = b.on("cu"), b.on("table")
+    kc, vc = b.on("kc").nan_to_num(0.5), b.on("vc").nan_to_num(0.5)
+    before = kc.clone(), vc.clone()
+    lens, near = (torch.tensor([x, 30], dtype=torch.int32, device="cuda") for x in (length, stands_for))
+    status = torch.zeros(3, dtype=torch.int32, device="cuda")
+    pkg.gdr_cache_write(b.on("k"), b.on("v"), kc, vc, table, lens, cu, status=status[:1])
+    at = torch.arange(26, 30)
+    for c, old, x in ((kc, before[0], b.k), (vc, before[1], b.v)):
+        want = old.cpu()
+        want[b.table[1, at // 16].long(), at % 16] = x[0, 4:]
+        assert torch.equal(c.cpu(), want)
+    k, v = pkg.gdr_cache_read(kc, vc, table, lens, 8, cu, status=status[1:2])
+    for got, x in ((k, b.k), (v, b.v)):
+        assert (got[0, :4] == 0).all() and torch.equal(got[0, 4:].cpu(), x[0, 4:])
+    for route in ROUTES:
+        status[2] = 0
+        o, lse = pkg.gdr_paged_attn(b.on("q"), kc, vc, table, lens, cu, status=status[2:],
+                                    force_path=route)
+        assert status.tolist() == [-7, -7, -7]
+        o2, lse2 = pkg.gdr_paged_attn(b.on("q"), kc, vc, table, near, cu, force_path=route)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
