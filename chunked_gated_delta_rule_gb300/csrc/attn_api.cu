@@ -62,7 +62,8 @@ int cache_call(bool write, const gdr_dims *dims, const gdr_paged_cache *cache, c
                const void *v, const int32_t *cu, int32_t *status, gdr_stream_t stream) {
     int rc = check_dims(dims);
     if (rc != GDR_OK) return rc;
-    if (!k || !v || (cu != nullptr) != (dims->N > 0)) return GDR_ERR_INVALID;
+    // tensors without elements may have no address
+    if (((!k || !v) && dims->T > 0) || (cu != nullptr) != (dims->N > 0)) return GDR_ERR_INVALID;
     rc = check_cache(*dims, cache, false);
     if (rc != GDR_OK) return rc;
     if (!write) {  // outputs: two rows must not share an address
@@ -153,7 +154,8 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
                    const gdr_options *opt, gdr_stream_t stream) {
     int rc = check_dims(dims);
     if (rc != GDR_OK) return rc;
-    if (!q || !o || window < 0 || (cu_seqlens != nullptr) != (dims->N > 0)) return GDR_ERR_INVALID;
+    if (((!q || !o) && dims->T > 0) || window < 0 || (cu_seqlens != nullptr) != (dims->N > 0))
+        return GDR_ERR_INVALID;
     rc = check_cache(*dims, cache, true);
     if (rc != GDR_OK) return rc;
     if (opt && (!(opt->scale >= 0.f) || opt->grid_limit < 0 || opt->force_bv ||

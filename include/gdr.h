@@ -378,7 +378,8 @@ typedef struct gdr_paged_cache {
  * gdr_cache_write -- stores the call's keys and values in the cache.
  *   dims        B, T, N, K, V, dtype, k_stride, v_stride as for gdr_chunk_fwd;
  *               H = cache->H; V at most 256.
- *   k, v        [B, T, H, K], [B, T, H, V].
+ *   k, v        [B, T, H, K], [B, T, H, V]; NULL will do where T = 0 (here and
+ *               below: such a call does nothing).
  *   status      device int32 word or NULL, zeroed by the caller.
  * The tokens of one call must have places of their own.  Enqueued on `stream`,
  * no allocation, no synchronisation.

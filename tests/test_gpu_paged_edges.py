@@ -167,3 +167,21 @@ def test_lengths_outside_the_table(length, stands_for):
         assert status.tolist() == [-7, -7, -7]
         o2, lse2 = pkg.gdr_paged_attn(b.on("q"), kc, vc, table, near, cu, force_path=route)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_calls_without_tokens(packed):
+    """A step with no new tokens: nothing to do, and no error."""
+    b = Batch([3, 2], [30, 20], heads=4, kv_heads=2, K=64, dtype="bf16", page=16)
+    kc, vc = b.on("kc"), b.on("vc")
+    lead = (1, 0) if packed else (2, 0)
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda") if packed else None
+    k = torch.empty(*lead, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.empty(*lead, 4, 64, dtype=torch.bfloat16, device="cuda")
+    pkg.gdr_cache_write(k, k, kc, vc, b.on("table"), b.on("lens"), cu)
+    k2, v2 = pkg.gdr_cache_read(kc, vc, b.on("table"), b.on("lens"), 0, cu)
+    o, lse = pkg.gdr_paged_attn(q, kc, vc, b.on("table"), b.on("lens"), cu)
+    torch.cuda.synchronize()
+    assert k2.shape == v2.shape == (*lead, 2, 64)
+    assert o.shape == q.shape and lse.shape == q.shape[:-1]
+    assert torch.equal(kc.nan_to_num(), b.on("kc").nan_to_num())

@@ -135,3 +135,14 @@ def test_binding_checks_caches():
                      (dict(kv_lens=lens.float()), TypeError)):
         with pytest.raises(err):
             api._cache_of(**{**good, **bad})
+
+
+def test_empty_tensors_need_no_address(lib):
+    """A tensor without elements has none."""
+    c = _cache()
+    assert _attn(lib, api.make_dims(1, 0, 4, 64, 64), c, q=None, o=None) == 0
+    assert _attn(lib, api.make_dims(1, 0, 4, 64, 64, N=2), c, q=None, o=None, cu=3) == 0
+    assert _attn(lib, api.make_dims(1, 0, 3, 64, 64), c, q=None, o=None) == -1  # 3 heads over 2
+    for name in ("gdr_cache_write", "gdr_cache_read"):
+        assert _rows(lib, name, api.make_dims(1, 0, 2, 64, 64), c, k=None, v=None) == 0
+        assert _rows(lib, name, api.make_dims(1, 0, 2, 64, 64), None, k=None, v=None) == -1
