@@ -58,6 +58,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The scale s that a row of values is weighed with, 2^(t + log2 s - m): its own,
+// but no smaller than 2^-100, so that the sum of the 2^(t + log2 s - m) / s stays
+// finite.  A row of zeros has none, and any will do that neither loses its weight
+// in that sum (below 2^-126 beside the largest) nor drives the others out of FP16.
+constexpr float kLeastScale = 0x1p-100f, kScaleOfZeros = 0x1p-60f;
+__device__ __forceinline__ float weighed_scale(float s) {
+    return s < kLeastScale ? (s == 0.f ? kScaleOfZeros : kLeastScale) : s;
+}
+
 // Four 8-bit values (FMT 1: E4M3, 2: integers) as FP16, exact.
 template <int FMT>
 __device__ __forceinline__ void widen4(uint32_t x, uint32_t &lo, uint32_t &hi) {

@@ -39,7 +39,6 @@ constexpr int kRowsMost = 16;  // rows of a tile: 8 or 16
 constexpr int kRowsUnit = 2;   // what a unit costs beside its steps, in steps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100
 
 // Sizes of one configuration.  FMT: 0 the call's own 16-bit type, 1 E4M3,
 // 2 8-bit integers.
@@ -469,9 +468,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
                     const float *s = reinterpret_cast<const float *>(ring + C::scale_at(tile)) + t * 16 + h * 8 +
                                      token_of<FMT>(qr);
                     ks = s[0];
-                    // no smaller than 2^-100, so that 1 / s is finite: a scale of
-                    // 0 stands for a row of zeros, for which any other will do
-                    const float vs = s[C::kBN] < kLeast ? kLeast : s[C::kBN];
+                    const float vs = weighed_scale(s[C::kBN]);
                     lg = __log2f(vs);
                     inv_s[t][h] = __fdividef(1.f, vs);
                 }

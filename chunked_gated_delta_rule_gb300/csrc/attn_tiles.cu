@@ -77,7 +77,6 @@ constexpr int kTThreads = 512;
 constexpr int kTUnit = 4;
 constexpr float kTLog2e = 1.4426950408889634f;
 constexpr float kTLn2 = 0.6931471805599453f;
-constexpr float kTLeast = 7.888609052210118e-31f;  // 2^-100
 // Values' scales in FP16, less than 2^7 by choice: below this a step is wide.
 // They keep 13 bits there (a part and what it leaves, both above 2^-25).
 constexpr float kTNarrow = 0x1p-12f;
@@ -927,7 +926,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         const float inv = __int_as_float((254 - at) << 23);
                         float part = vs * inv, lgs = (float)(at - 127), invs = inv;
                         if (__builtin_expect(vl * inv < kTNarrow, 0)) {  // wide
-                            sc[kTN + 1 + t] = __log2f(vs < kTLeast ? kTLeast : vs);
+                            sc[kTN + 1 + t] = __log2f(weighed_scale(vs));
                             part = fminf(vs * 0x1p100f, 1.f);  // what 2^-100 leaves of smaller ones
                             lgs = kTWide;
                             invs = 0.f;
@@ -949,7 +948,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     }
                     if (!kFold && scales) {
                         float *sc = reinterpret_cast<float *>(sm + C::kOffScale) + (it % C::kScales) * 3 * kTN;
-                        const float v = vs < kTLeast ? kTLeast : vs;
+                        const float v = weighed_scale(vs);
                         sc[t] = ks;
                         sc[kTN + t] = __log2f(v);
                         sc[2 * kTN + t] = __fdividef(1.f, v);

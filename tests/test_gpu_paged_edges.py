@@ -185,3 +185,21 @@ def test_calls_without_tokens(packed):
     assert k2.shape == v2.shape == (*lead, 2, 64)
     assert o.shape == q.shape and lse.shape == q.shape[:-1]
     assert torch.equal(kc.nan_to_num(), b.on("kc").nan_to_num())
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("fmt,K", [("e4m3", 128), ("int8", 128), ("int8", 64)])
+@pytest.mark.parametrize("bits", [-40, 0, 40])
+@pytest.mark.parametrize("spread", [False, True])
+def test_rows_of_zeros_keep_their_weight(route, fmt, K, bits, spread):
+    """Values of zeros (their scale is 0) beside values of about 2^bits, some of
+    them 2^-20 of that: they take their part of the softmax's sum."""
+    b = Batch([50], [150], heads=2, kv_heads=1, K=K, dtype="bf16", fmt=fmt, page=16)
+    b.vs *= 2.0 ** bits
+    at = torch.arange(150)
+    pages, slots = b.table[0, at // 16].long(), at % 16
+    if spread:
+        b.vs[pages[1::3], 0, slots[1::3]] *= 2.0 ** -20
+    b.vs[pages[::2], 0, slots[::2]] = 0
+    b.vc[pages[::2], slots[::2]] = torch.zeros(K).to(b.vc.dtype)
+    check(b, *b.run(force_path=route), *b.attention(), label=f"{route} {fmt} {K} {bits} {spread}")
