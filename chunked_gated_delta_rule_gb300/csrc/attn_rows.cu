@@ -184,6 +184,8 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
     // weights in two halves, where one rounding of them would be as large as
     // the output's own
     constexpr bool kSplitP = std::is_same<T, TP>::value;
+    // whose o holds values of the least scales
+    constexpr bool kBf = FMT != 0 && std::is_same<T, __nv_bfloat16>::value;
     extern __shared__ uint8_t smem_raw[];
     __shared__ StepInfo s_info[C::kWarps][C::kInfos];
     __shared__ uint64_t s_bar[C::kWarps][C::kTiles];
@@ -459,6 +461,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
 
         // base-2 scores; 8 bits: with the values' scales in them
         float inv_s[kMT][2];
+        bool small = false;  // some value's scale is weighed as 2^-100
 #pragma unroll
         for (int t = 0; t < kMT; ++t)
 #pragma unroll
@@ -469,6 +472,7 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
                                      token_of<FMT>(qr);
                     ks = s[0];
                     const float vs = weighed_scale(s[C::kBN]);
+                    if (kBf) small |= s[C::kBN] < kLeastScale && s[C::kBN] > 0.f;
                     lg = __log2f(vs);
                     inv_s[t][h] = __fdividef(1.f, vs);
                 }
@@ -552,6 +556,28 @@ __global__ void __launch_bounds__(32 * RowsCfg<FMT, D>::kWarps, 1)
                         // and takes nothing of its scale, NaN or not
                         l[n][e] += FMT ? (w == 0.f ? 0.f : w * inv_s[t][h]) : w;
                     }
+                }
+        if (kBf && __any_sync(0xffffffffu, small)) {
+            // what 2^-100 leaves of their scales goes to their weights
+#pragma unroll
+            for (int t = 0; t < kMT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float s = reinterpret_cast<const float *>(ring + C::scale_at(tile))[
+                        C::kBN + t * 16 + h * 8 + token_of<FMT>(qr)];
+                    const float rest = s >= 0.f && s < kLeastScale ? s * (1.f / kLeastScale) : 1.f;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) sc[t][n][2 * h + e] *= rest;
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     const uint32_t w2 = pack2<TP>(sc[t][n][2 * h], sc[t][n][2 * h + 1]);
                     ph[t][n][h] = transpose8(w2);
                     if constexpr (kSplitP) {

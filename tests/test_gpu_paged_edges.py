@@ -203,3 +203,21 @@ def test_rows_of_zeros_keep_their_weight(route, fmt, K, bits, spread):
     b.vs[pages[::2], 0, slots[::2]] = 0
     b.vc[pages[::2], slots[::2]] = torch.zeros(K).to(b.vc.dtype)
     check(b, *b.run(force_path=route), *b.attention(), label=f"{route} {fmt} {K} {bits} {spread}")
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("fmt,K", [("e4m3", 128), ("int8", 128), ("int8", 64)])
+@pytest.mark.parametrize("some", [False, True])
+def test_values_near_the_least_magnitudes(route, fmt, K, some):
+    """Scales of values about 2^-110 (BF16 goes down to 2^-133): of all tokens,
+    or of all but a few whose weight is nothing beside the others'."""
+    b = Batch([50], [150], heads=2, kv_heads=1, K=K, dtype="bf16", fmt=fmt, page=16)
+    b.vs *= 2.0 ** -103
+    if some:
+        b.q = b.q.abs()
+        for at in (40, 90):
+            page, slot = int(b.table[0, at // 16]), at % 16
+            b.vs[page, 0, slot] = 1e-30
+            b.kc[page, slot, 0] = torch.full((K,), -120.0).to(b.kc.dtype)
+            b.ks[page, 0, slot] = 0.5
+    check(b, *b.run(force_path=route), *b.attention(), label=f"{route} {fmt} {K} {some}")
