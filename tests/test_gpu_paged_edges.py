@@ -221,3 +221,45 @@ def test_values_near_the_least_magnitudes(route, fmt, K, some):
             b.kc[page, slot, 0] = torch.full((K,), -120.0).to(b.kc.dtype)
             b.ks[page, 0, slot] = 0.5
     check(b, *b.run(force_path=route), *b.attention(), label=f"{route} {fmt} {K} {some}")
+
+
+@pytest.mark.parametrize("route", [1, 3, 0])
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "same"), ("f16", "same"), ("bf16", "e4m3"),
+                                       ("bf16", "int8"), ("f16", "e4m3"), ("f16", "int8")])
+@pytest.mark.parametrize("page,K", [(1, 128), (5, 64), (12, 128), (4, 64)])
+def test_pages_that_no_box_fits(route, dtype, fmt, page, K):
+    """Pages of no multiple of 8 slots: gathered row by row."""
+    b = Batch([3, 0, 1, 70, 5], [3, 9, 131, 200, 0], heads=4, kv_heads=2, K=K, page=page,
+              dtype=dtype, fmt=fmt)
+    check(b, *b.run(force_path=route), *b.attention(), label=f"{route} {dtype} {fmt} {page}")
+    check(b, *b.run(force_path=route, window=33), *b.attention(window=33), label="window")
+    with pytest.raises(pkg.GdrError):  # boxes of 8 slots at least
+        b.run(force_path=2)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("K", [64, 128])
+def test_scales_off_16_bytes(fmt, K):
+    b = Batch([1, 20], [131, 200], heads=4, kv_heads=2, K=K, page=16, dtype="bf16", fmt=fmt)
+    ref = b.attention()
+    for name in ("ks", "vs"):
+        keep = getattr(b, name)
+        flat = torch.zeros(keep.numel() + 1, device="cuda")
+        flat[1:] = keep.reshape(-1).cuda()
+        moved = flat[1:].view(keep.shape)
+        setattr(b, name, moved)
+        b_on = b.on
+        b.on = lambda n, m=moved, f=b_on, name=name: m if n == name else f(n)
+        for route in (0, 1, 3):
+            check(b, *b.run(force_path=route), *ref, label=f"{name} {route}")
+        b.on = b_on
+        setattr(b, name, keep)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("K,V", [(16, 16), (48, 208), (256, 256), (128, 64), (64, 128)])
+def test_other_widths_in_16_bits(dtype, fmt, K, V):
+    b = Batch([3, 40, 1], [50, 40, 300], heads=4, kv_heads=2, K=K, V=V, dtype=dtype, fmt=fmt,
+              page=16)
+    check(b, *b.run(), *b.attention(), label=f"{dtype} {fmt} {K} {V}")
