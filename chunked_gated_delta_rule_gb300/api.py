@@ -521,6 +521,14 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _check_status(status, index):
+    """The status word is written on the device."""
+    if status is not None:
+        _on(index, status=(status, torch.int32))
+        if status.numel() < 1:
+            raise ValueError("status must have an element")
+
+
 def gdr_cache_write(k, v, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
                     k_scale=None, v_scale=None, status=None, stream=None):
     """Stores the new tokens' ``k`` [B, T, H, K] and ``v`` [B, T, H, V] in the
@@ -537,6 +545,7 @@ def gdr_cache_write(k, v, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None
         raise ValueError("gdr_cache_write takes CUDA tensors")
     if v.get_device() != index or v.dtype != k.dtype:
         raise ValueError("k and v must share a device and a dtype")
+    _check_status(status, index)
     if v.shape[:-1] != k.shape[:-1] or k_cache.shape[2:] != k.shape[2:] or \
             v_cache.shape[-1] != v.shape[-1]:
         raise ValueError("k, v and the caches must agree in tokens, heads and widths")
@@ -559,6 +568,7 @@ def gdr_cache_read(k_cache, v_cache, page_table, kv_lens, T, cu_seqlens=None, *,
     index = k_cache.get_device()
     if index < 0:
         raise ValueError("gdr_cache_read takes CUDA tensors")
+    _check_status(status, index)
     if k_cache.dim() != 4 or v_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [pages, page size, heads, K] and [.., V]")
     B = kv_lens.numel() if cu_seqlens is None else 1
@@ -602,6 +612,8 @@ def gdr_paged_attn(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
     index = q.get_device()
     if index < 0:
         raise ValueError("gdr_paged_attn takes CUDA tensors")
+    _check_status(status, index)
+    _on(index, workspace=(workspace, None))
     shape, k_shape, v_shape = q.shape, k_cache.shape, v_cache.shape
     if len(shape) != 4 or len(k_shape) != 4 or len(v_shape) != 4 or shape[3] != k_shape[3]:
         raise ValueError("q must be [B, T, heads, K], the caches [pages, page size, heads, K or V]")

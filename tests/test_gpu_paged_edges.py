@@ -263,3 +263,19 @@ def test_other_widths_in_16_bits(dtype, fmt, K, V):
     b = Batch([3, 40, 1], [50, 40, 300], heads=4, kv_heads=2, K=K, V=V, dtype=dtype, fmt=fmt,
               page=16)
     check(b, *b.run(), *b.attention(), label=f"{dtype} {fmt} {K} {V}")
+
+
+def test_status_and_workspace_must_be_on_the_device():
+    b = Batch([3], [30], heads=2, kv_heads=1, K=64, dtype="bf16", page=16)
+    args = [b.on(x) for x in ("kc", "vc", "table", "lens")]
+    host = torch.zeros(1, dtype=torch.int32)
+    for bad in (host, host.cuda().long()):
+        with pytest.raises((ValueError, TypeError)):
+            pkg.gdr_paged_attn(b.on("q"), *args, b.on("cu"), status=bad)
+        with pytest.raises((ValueError, TypeError)):
+            pkg.gdr_cache_write(b.on("k"), b.on("v"), *args, b.on("cu"), status=bad)
+        with pytest.raises((ValueError, TypeError)):
+            pkg.gdr_cache_read(*args, 3, b.on("cu"), status=bad)
+    with pytest.raises(ValueError):
+        pkg.gdr_paged_attn(b.on("q"), *args, b.on("cu"),
+                           workspace=torch.zeros(1 << 24, dtype=torch.uint8))
