@@ -11,7 +11,7 @@ missing.
 from .api import (GdrError, LaunchTimer, gdr_chunk_fwd, gdr_chunk_fwd_host,  # noqa: F401
                   gdr_chunk_bwd, gdr_bwd_workspace_size,
                   gdr_chunk_fwd_noalloc, gdr_recurrent_fwd,
-                  gdr_cache_write, gdr_cache_read, gdr_paged_attn,
+                  gdr_cache_write, gdr_cache_read, gdr_paged_attn, gdr_attn_workspace_size,
                   gdr_error_string, gdr_kernel_name, gdr_plan_query, gdr_release_cached,
                   gdr_version,
                   gdr_workspace_size, load_library)

@@ -606,8 +606,9 @@ def gdr_paged_attn(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
     lse)``: o [B, T, Hq, V] in q's dtype and the log of the softmax's
     denominator [B, T, Hq] (float32); a row that sees nothing has o = 0 and lse
     = -inf.  ``max_seqlen`` is the most new tokens of a sequence when the
-    caller knows it (a planning hint).  Work is enqueued on ``stream`` (default:
-    the current one) and not synchronised."""
+    caller knows it (a planning hint).  ``workspace`` may hold the call's scratch
+    (:func:`gdr_attn_workspace_size` bytes, 256-byte aligned).  Work is enqueued on
+    ``stream`` (default: the current one) and not synchronised."""
     lib = load_library()
     index = q.get_device()
     if index < 0:
@@ -649,6 +650,19 @@ def gdr_paged_attn(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
     _paged_call(lib.gdr_paged_attn, index, stream, dims, cache, q.data_ptr(), _addr(cu_seqlens),
                 o.data_ptr(), lse.data_ptr(), 1 if causal else 0, int(window), opt)
     return o, lse
+
+
+def gdr_attn_workspace_size(q, k_cache, v_cache, page_table, kv_lens, cu_seqlens=None, *,
+                            k_scale=None, v_scale=None) -> int:
+    """Bytes of device scratch that :func:`gdr_paged_attn` needs for these tensors,
+    whatever its route."""
+    index = q.get_device()
+    if index < 0:
+        raise ValueError("gdr_attn_workspace_size takes CUDA tensors")
+    dims, nseq = _paged_dims(*q.shape, v_cache.shape[3], cu_seqlens, q.dtype, index)
+    cache = _cache_of(k_cache, v_cache, page_table, kv_lens, k_scale, v_scale, nseq, index)
+    with torch.cuda.device(index):
+        return int(load_library().gdr_attn_workspace_size(ctypes.byref(dims), ctypes.byref(cache)))
 
 
 def gdr_chunk_fwd_host(q, k, v, g, beta=None, cu_seqlens=None, h0=None, *, n_segments=0,

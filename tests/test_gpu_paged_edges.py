@@ -279,3 +279,23 @@ def test_status_and_workspace_must_be_on_the_device():
     with pytest.raises(ValueError):
         pkg.gdr_paged_attn(b.on("q"), *args, b.on("cu"),
                            workspace=torch.zeros(1 << 24, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("route", ROUTES)
+@pytest.mark.parametrize("fmt", ["same", "e4m3"])
+def test_workspace_of_the_caller(route, fmt):
+    """The bits of the call that takes its own scratch, and nothing written past
+    the size that the library asks for."""
+    b = Batch([5, 130, 1], [900, 400, 1500], heads=8, kv_heads=2, dtype="bf16", fmt=fmt, page=16)
+    need = pkg.gdr_attn_workspace_size(*(b.on(x) for x in ("q", "kc", "vc", "table", "lens", "cu")),
+                                       k_scale=b.on("ks"), v_scale=b.on("vs"))
+    o, lse = b.run(force_path=route)
+    room = torch.full((need + 256,), 91, dtype=torch.uint8, device="cuda")
+    o2, lse2 = b.run(force_path=route, workspace=room[:need])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert (room[need:] == 91).all()
+    if route > 1:
+        with pytest.raises(pkg.GdrError):
+            b.run(force_path=route, workspace=room[:256])
+        with pytest.raises(pkg.GdrError):
+            b.run(force_path=route, workspace=room[16:need + 16])
