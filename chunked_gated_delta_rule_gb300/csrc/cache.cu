@@ -244,8 +244,11 @@ __device__ __forceinline__ void write_row(const Eight<Tin> &x, bool live, Tc *ds
                 f[i] = fmaf(fmaf(-q, s, f[i]), r, q);
             }
         } else {
+            // a scale of a few of FP32's least units may be a third too small
+            constexpr float kMost = std::is_same<Tc, int8_t>::value ? 127.f : 448.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = s > 0.f ? __fdiv_rn(f[i], s) : 0.f;
+            for (int i = 0; i < 8; ++i)
+                f[i] = s > 0.f ? fminf(fmaxf(__fdiv_rn(f[i], s), -kMost), kMost) : 0.f;
         }
         Eight<Tc> y;
         y.narrow(f);

@@ -346,8 +346,8 @@ int gdr_chunk_bwd(const gdr_dims *dims, const void *q, const void *k,
  *   dtype     the call's own type (GDR_F32, GDR_BF16, GDR_F16: stored as they
  *             are), or GDR_E4M3 / GDR_I8: each (token, head) row x is stored
  *             as q = round(x / s) beside its FP32 scale s = max|x| * (1 / 448)
- *             or max|x| * (1 / 127), one FP32 product (ties to even; q = 0
- *             where s = 0), and stands for q s.  A row with a NaN or an
+ *             or max|x| * (1 / 127), one FP32 product (ties to even, at most
+ *             448 or 127; q = 0 where s = 0), and stands for q s.  A row with a NaN or an
  *             infinity is stored as s = NaN, q = 0 and reads back as NaN.
  *   strides   in elements: page, slot, head; {0, 0, 0} means contiguous
  *             ([n_pages, page_size, H, K]).  The last dimension is always

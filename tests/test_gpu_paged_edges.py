@@ -299,3 +299,24 @@ def test_workspace_of_the_caller(route, fmt):
             b.run(force_path=route, workspace=room[:256])
         with pytest.raises(pkg.GdrError):
             b.run(force_path=route, workspace=room[16:need + 16])
+
+
+@pytest.mark.parametrize("fmt,most", [("int8", 127.0), ("e4m3", 448.0)])
+def test_rows_whose_scale_is_rounded_far(fmt, most):
+    """FP32 rows so small that their scale is a few of the type's smallest
+    units: quotients past the format's largest value are its largest value."""
+    b = Batch([40], [40], heads=1, kv_heads=1, K=32, page=16, dtype="f32", fmt=fmt)
+    units = 1 + 23 * torch.arange(40, dtype=torch.float64)  # of 2^-149
+    b.k[0] = (units[:, None, None] * torch.linspace(-1, 1, 32, dtype=torch.float64)
+              ).round().mul(2.0 ** -149).float()
+    kc, vc, ks, vs = (b.on(x) for x in ("kc", "vc", "ks", "vs"))
+    pkg.gdr_cache_write(b.on("k"), b.on("v"), kc, vc, b.on("table"), b.on("lens"), b.on("cu"),
+                        k_scale=ks, v_scale=vs)
+    at = torch.arange(40)
+    pages, slots = b.table[0, at // 16].long(), at % 16
+    got, scale = kc.cpu().float()[pages, slots, 0].double(), ks.cpu()[pages, 0, slots].double()
+    assert float(got.abs().max()) == most
+    x = b.k[0, :, 0].double()
+    want = torch.where(scale[:, None] > 0, x / scale[:, None], torch.zeros_like(x)).clamp(-most, most)
+    step = 1.0 if fmt == "int8" else 32.0
+    assert ((got - want).abs() <= step / 2).all() and (got * want >= 0).all()
