@@ -27,6 +27,8 @@ int check_cache(const gdr_dims &d, const gdr_paged_cache *c, bool attention) {
     if (c->n_pages > INT32_MAX || c->page_size > INT32_MAX || c->H > 65535 ||
         c->max_pages > INT32_MAX / c->page_size)
         return GDR_ERR_UNSUPPORTED;  // positions fit 31 bits
+    // those of the attention's steps as well, which pass the last by up to 127
+    if (attention && c->max_pages > (INT32_MAX - 1023) / c->page_size) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
 

@@ -404,6 +404,7 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
  * the positions j that token i, at position p_i, sees: j < kv_lens[n]; causal
  * != 0: j <= p_i; window > 0: j > p_i - window.  A row that sees nothing gets
  * o = 0, lse = -inf.
+ * The page table has at most 2^31 - 1024 positions a sequence.
  *   dims      B, T, N, K, V (at most 256), dtype, q_stride, o_stride; H the
  *             query heads, a multiple of cache->H: query head h reads key head
  *             h / (H / cache->H).  max_len: the most new tokens of a sequence

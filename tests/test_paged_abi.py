@@ -146,3 +146,11 @@ def test_empty_tensors_need_no_address(lib):
     for name in ("gdr_cache_write", "gdr_cache_read"):
         assert _rows(lib, name, api.make_dims(1, 0, 2, 64, 64), c, k=None, v=None) == 0
         assert _rows(lib, name, api.make_dims(1, 0, 2, 64, 64), None, k=None, v=None) == -1
+
+
+def test_attention_refuses_positions_that_steps_would_pass(lib):
+    """A step's positions are 32-bit numbers too, up to 127 past the last: tables
+    of more than 2^31 - 1024 positions are refused."""
+    dims = api.make_dims(1, 8, 2, 64, 64)
+    for page, pages in ((1, (1 << 31) - 1), (16, (1 << 27) - 1), ((1 << 31) - 1, 1)):
+        assert _attn(lib, dims, _cache(page_size=page, max_pages=pages)) == -2
