@@ -59,7 +59,8 @@
 //
 // The steps of the call are shared out equally over one CTA an SM
 // (attn_split.cuh).  Every wait is bounded: on expiry the CTA records
-// GDR_ERR_TIMEOUT, its other roles leave too, and it exits.
+// GDR_ERR_TIMEOUT, its other roles leave too, and it exits once its loads in
+// flight have landed.
 #include "attn_map.cuh"
 #include "attn_split.cuh"
 #include "gdr_launch.cuh"
@@ -1099,7 +1100,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     entry = p.c.table[u.n * p.c.max_pages + pi];
                 }
             };
-            uint32_t item = 0, seg = 0;
+            uint32_t item = 0, seg = 0, landed = 0;  // landed: by tile, whether kLand has had an odd number
             bool ok = true;
             look_up();
             for (int it = 0; it < count && ok; ++it) {
@@ -1125,6 +1126,7 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         const int e = (int)((item + 1) >> 1) - C::kPairs;
                         if (e >= 0) ok = __all_sync(0xffffffffu, wait(B::kEmpty + e % C::kPairs, e / C::kPairs));
                         bar = kv && masked ? B::kLand + b : B::kFull + b;
+                        landed ^= (uint32_t)(kv && masked) << b;
                         dst = C::kOffRing + b * C::kTile;
                         bytes = C::kTile;
                     } else if (C::kSplit && kv == 0) {
@@ -1164,7 +1166,10 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                         // rows past the unit's are those of other tokens, or
                         // zeros; they see nothing
                         ok = __all_sync(0xffffffffu, wait(B::kQEmpty, seg + 1));
-                        if (!ok) break;
+                        if (!ok) {
+                            ++item;  // it is on its way
+                            break;
+                        }
                         const int halves = unit_rows<kTM>(p, u) > 128 ? 2 : 1;
                         if (lane == 0) mbar_arrive_expect_tx(&bars[B::kQFull], halves * C::kQTile);
                         __syncwarp();
@@ -1181,6 +1186,19 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                     look_up();
                 }
             }
+            // Whether or not anybody still waits for them, the loads land before the
+            // memory goes back: the last turn of every barrier (turn -1, of one not
+            // used, is over).  10 ms, as a turn may need others who gave up.
+            auto land = [&](int bar, uint32_t turns) { mbar_wait(&bars[bar], (turns - 1) & 1u, nullptr, 10000000ull); };
+            auto used = [](uint32_t n, uint32_t i, uint32_t of) { return (n + of - 1 - i) / of; };  // i < of
+            if (FMT == 0 && lane < C::kRing) {
+                land(B::kFull + lane, used(item, lane, C::kRing));
+                land(B::kLand + lane, landed >> lane);
+            }
+            if (FMT != 0 && lane < C::kRaw)
+                land(B::kLand + lane, used(C::kSplit ? item >> 1 : item, lane, C::kRaw));
+            if (C::kSplit && lane < C::kKeys) land(B::kKeyFull + lane, used((item + 1) >> 1, lane, C::kKeys));
+            if (a.q_box && lane == 0) land(B::kQFull, seg);
         }
         if (warp == 12 && lane == 0) {  // nothing is in flight when the memory goes back
             umma_commit(&bars[B::kDrain]);
