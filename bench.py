@@ -10,16 +10,19 @@ fits one GPU, one 65,536-token sequence with 8 heads (K = V = 128, BF16
 q/k/v, near non-contracting decay), at the plan's segment count.  L2 is
 flushed (a 256 MiB write) between timed steps, outside the timed events.
 
-The same JSON line carries a sub-record per configuration ("configs"): ms
-per call, tokens/s, the call's roofline fraction, per-kernel times; serial
+The same JSON line carries the ms per call of every configuration
+("configs").  --records FILE writes the whole record there, with a sub-record
+for each: tokens/s, the call's roofline fraction, per-kernel times; serial
 beside split at 64K tokens (8 heads and 1); at 16K tokens every split count
 with its error against the FP64 oracle on sampled (sequence, head) pairs;
 the plan's pick beside serial on a batch with one long sequence; and the
 backward pass (gdr_chunk_bwd, at its plan's route) on the wide varlen batch,
-16K tokens and 64K tokens x 8 heads ("backward_<workload>").
+16K tokens and 64K tokens x 8 heads ("backward_<workload>").  The line itself
+stays short: where the end of a program's output is all that is kept, a
+longer one is lost.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl gdr|reference]
-                  [--workload NAME] [--no-configs]
+                  [--workload NAME] [--no-configs] [--records FILE]
 
 --impl reference times the FP64 CPU oracle (the slow reference program) on
 bounded samples of the same workload, drawn by the same sampler as the
@@ -67,12 +70,55 @@ def parse_args():
     ap.add_argument("--cpu-seconds", type=float, default=10.0)
     ap.add_argument("--no-configs", action="store_true",
                     help="skip the per-configuration sub-records")
+    ap.add_argument("--records", help="write the whole record to this file as well")
     ap.add_argument("--pass", dest="which", choices=["fwd", "bwd"], default="fwd",
                     help="bwd times gdr_chunk_bwd (the backward pass) instead")
     args = ap.parse_args()
     if args.workload is None:
         args.workload = DEFAULT_WORKLOAD_BWD if args.which == "bwd" else DEFAULT_WORKLOAD
     return args
+
+
+# ----------------------------------------------------------------------------
+# the result line
+# ----------------------------------------------------------------------------
+LINE_LIMIT = 2800  # characters
+
+
+def short_line(record):
+    """The record as one line of at most LINE_LIMIT characters: configurations
+    by their ms per call, numbers to five digits, and as few of the notes and
+    of the per-kernel numbers dropped as that takes."""
+    def brief(x):
+        if isinstance(x, float):
+            return float(f"{x:.5g}") if math.isfinite(x) else None
+        if isinstance(x, dict):
+            return {k: brief(v) for k, v in x.items()}
+        return [brief(v) for v in x] if isinstance(x, (list, tuple)) else x
+
+    line = brief(record)
+    for k in ("value", "ms_per_step"):  # as they were measured
+        if k in record:
+            line[k] = record[k]
+    if record.get("configs"):
+        line["configs"] = {k: brief(v["ms_per_call"]) for k, v in record["configs"].items()}
+    for part, notes in (("roofline", ("basis", "timing")), ("scan_roofline", ("basis", "timing")),
+                        ("call_roofline", ("basis",))):
+        for note in notes:
+            if isinstance(line.get(part), dict):
+                line[part].pop(note, None)
+    for k in ("scan_roofline", "kernels", "step_ms", "configs"):
+        if len(json.dumps(line)) <= LINE_LIMIT:
+            break
+        line.pop(k, None)
+    return json.dumps(line)
+
+
+def emit(record, path=None):
+    if path:
+        with open(path, "w") as f:
+            json.dump(record, f)
+    print(short_line(record), flush=True)
 
 
 # ----------------------------------------------------------------------------
@@ -943,7 +989,7 @@ def run_gdr(args):
                             "p10": sorted(step_ms)[len(step_ms) // 10],
                             "p90": sorted(step_ms)[(9 * len(step_ms)) // 10]},
                 "configs": configs}
-        print(json.dumps(line), flush=True)
+        emit(line, args.records)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
@@ -1064,7 +1110,7 @@ def run_decode(args):
                 "step_ms": {"median": statistics.median(step_ms), "min": min(step_ms),
                             "p10": sorted(step_ms)[len(step_ms) // 10],
                             "p90": sorted(step_ms)[(9 * len(step_ms)) // 10]}}
-        print(json.dumps(line), flush=True)
+        emit(line, args.records)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
@@ -1233,7 +1279,7 @@ def run_bwd(args):
                 "step_ms": {"median": statistics.median(step_ms), "min": min(step_ms),
                             "p10": sorted(step_ms)[len(step_ms) // 10],
                             "p90": sorted(step_ms)[(9 * len(step_ms)) // 10]}}
-        print(json.dumps(line), flush=True)
+        emit(line, args.records)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()

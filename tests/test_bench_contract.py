@@ -157,3 +157,35 @@ def test_segment_counts_under_both_cutting_rules():
     # or every non-empty one's (own length)
     assert common["split_seq_heads"] == 2 * 2
     assert own["split_seq_heads"] == 2 * 5
+
+
+def test_result_line_is_short():
+    """A record with every configuration's kernels still gives a line that the end
+    of a program's output holds whole, with every key that is asked for."""
+    b = _bench()
+    roof = {"kernel": "tc_gla_segment_out", "bound": "hbm", "achieved": 1426.6491234567, "peak": 6671.2,
+            "unit": "GB/s", "frac": 0.2138767769713503, "traffic": 238754944.0,
+            "algorithmic_bytes_per_launch": 295755776, "avg_launch_ms": 0.06878080070018769,
+            "timing": "CUDA events " * 8, "basis": "the whole call's bytes " * 10,
+            "peak_source": "measured (hbm_gbs, copy bandwidth)"}
+    kernels = {f"tc_chain_segment_recompute_{i}": {"launches": 20, "avg_ms": 0.12797440141439437,
+                                                   "share": 0.45095304590831625} for i in range(6)}
+    line = dict.fromkeys(REQUIRED)
+    line.update(metric=b.METRIC, value=139856733.12345678, unit="tokens/s", ms_per_step=0.46859123456789,
+                roofline=dict(roof), scan_roofline=dict(roof), call_roofline=dict(roof), kernels=kernels,
+                config={f"key_{i}": "a value of some length" for i in range(12)},
+                cpu_baseline={"value": 24900.65349166815, "sample": "groups of sequences " * 8},
+                e2e={"value": 11065524.258715358, "unit": "tokens/s", "h2d_bytes_per_step": 129821828,
+                     "d2h_bytes_per_step": 76382208, "ms_per_step": 0.944916820526123},
+                step_ms={k: 0.13318400084972382 for k in ("median", "min", "p10", "p90")},
+                configs={f"backward_stress_64k_h8_bf16_{i}": {"ms_per_call": 0.4685912345, "kernels": kernels,
+                                                              "roofline": roof} for i in range(12)})
+    text = b.short_line(line)
+    assert len(text) <= b.LINE_LIMIT and "\n" not in text
+    short = json.loads(text)
+    assert REQUIRED <= set(short)
+    assert short["value"] == line["value"] and short["ms_per_step"] == line["ms_per_step"]
+    assert short["e2e"]["h2d_bytes_per_step"] == 129821828
+    assert abs(short["roofline"]["frac"] / roof["frac"] - 1) < 1e-4
+    line["configs"], line["kernels"] = None, {}
+    assert json.loads(b.short_line(line))["scan_roofline"]["kernel"] == roof["kernel"]
