@@ -40,19 +40,18 @@
 // scales stay with the scores: lse is FP32.
 // E4M3 keys of 128 columns under BF16 queries are not widened at all: a row of
 // queries, scaled by a power of two to have its largest magnitude in [2^14, 2^15),
-// is split into three E5M2 parts, each what the ones before it leave.  Rounded to
-// nearest, the first takes three of BF16's eight bits and leaves at most four, the
-// second three of those and leaves one, so the split is exact for components down
-// to 2^-23 of the row's largest (FP16 queries: 2^-17), however little the largest,
+// is split into three E5M2 parts, the upper three bits of what the ones before it
+// leave.  They hold BF16's eight, so the split is exact for components down to
+// 2^-23 of the row's largest (FP16 queries: 2^-17), however little the largest,
 // an outlier channel say, has to do with the softmax.  Two E4M3 parts are exact
 // down to 2^-9 only: with one channel of 2^10 where the keys do not vary, o was
 // 4.9e-3 off.  S = (a + b + c) K^T takes three 8-bit products at twice the rate of
 // one FP16 product, and the keys go from the cache into the products as they are:
-// 525 us for 4096 new tokens over 16K (4 key heads; two parts: 524), 691 with
-// widened keys.  The third part's room is that of a second 8-bit tile of values.
+// 507 us for 4096 new tokens over 16K (4 key heads), 691 with widened keys.  The
+// third part's room is that of a second 8-bit tile of values (2 us).
 // Measured (4 key heads of 128, 4 query heads each, BF16, replayed from a graph):
 // 4096 new tokens over 32K: 615 us, 1678 TFLOP/s, 0.86 of a library product's
-// rate; over 16K in E4M3: 525 us, bound by latency: the chain of a half's
+// rate; over 16K in E4M3: 507 us, bound by latency: the chain of a half's
 // softmax, 3K cycles of which a third applies the step's 128 scales, and its
 // products; 32 prompts of 128 to 512 tokens: 71 us, of which a unit costs 6 us
 // beside 1.4 us a step.
@@ -87,8 +86,8 @@ constexpr float kTWide = 0x1p100f;
 
 // Registers a thread of the softmax warps, the helpers and the rest: 128 each
 // at launch, 2 x 192 + 72 + 56 = 4 x 128
-// (4096 new tokens over 16K in E4M3: 525 us; 184 / 88 / 56 spills more in the
-// softmax, 200 / 64 / 48 in the helpers: 556).
+// (184 / 88 / 56 spills more in the softmax, 200 / 64 / 48 in the helpers: 4096
+// new tokens over 16K in E4M3 took 571 and 556 us beside 525).
 constexpr int kRegSoftmax = 192, kRegHelp = 72, kRegRest = 56;
 static_assert(2 * kRegSoftmax + kRegHelp + kRegRest <= 4 * 128, "the launch's registers");
 
@@ -231,26 +230,6 @@ __device__ __forceinline__ bool help_sync(bool ok) {
         : "r"((uint32_t)ok)
         : "memory");
     return r != 0;
-}
-
-// Four values in E5M2, in order, to nearest even (NaN stays NaN), and back.
-__device__ __forceinline__ uint32_t e5m2x4(float x0, float x1, float x2, float x3) {
-    uint32_t y;
-    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e5m2x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e5m2x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
-        : "=r"(y)
-        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
-    return y;
-}
-__device__ __forceinline__ float4 wide5(uint32_t x) {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e5m2x2 %0, a;\n\tcvt.rn.f16x2.e5m2x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(x));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // Two BF16 values of a row that holds an infinity or a NaN: an infinity becomes
@@ -754,19 +733,21 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
             };
             auto dst = [&](int r) { return (r >> 7) * C::kQTile + sw128_chunk(r & 127, qc, 128); };
             if constexpr (kConvert) {
-                // FP16 of the row's own power of two (see attn_rows.cu), four
-                // rows' loads at a time
-                #pragma unroll 1
-                for (int r0 = t / kQC; r0 < 128 * halves; r0 += 4 * kQP) {
-                    uint4 x[4];
+                // FP16 of the row's own power of two (see attn_rows.cu), or the
+                // parts of it, two rows at a time (4096 tokens over 16K in E4M3:
+                // 507 us; four rows 513, eight 542)
+                const uint32_t first8 = sw128_chunk(t / kQC, qc >> 1, 128) + (qc & 1) * 8;
+#pragma unroll 1
+                for (int r0 = t / kQC; r0 < 128 * halves; r0 += 2 * kQP) {
+                    uint4 x[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const T *src;
                         const bool live = place(r0 + i * kQP, src);
                         x[i] = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                         // the largest magnitude's bits: they are in its order
                         uint32_t big = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
@@ -781,29 +762,33 @@ __global__ void __launch_bounds__(kTThreads, 1) k_attn_tiles(const __grid_consta
                             // the largest magnitude into [2^14, 2^15); a row with an
                             // infinity is its infinities' signs, times infinity
                             const int at = max(ex, 15);
-                            const float g = ex == 255 ? 1.f : __int_as_float((268 - at) << 23);
-                            back = ex == 255 ? INFINITY : __int_as_float((at - 14) << 23);
-                            // first the 128 columns of the first part, then the next's
-                            const uint32_t row = (r >> 7) * C::kQTile + (qc & 1) * 8;
-#pragma unroll 1
-                            for (int e = 0; e < 2; ++e) {
-                                uint2 v = e ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
-                                if (ex == 255) {
-                                    v.x = signs_of_infinities(v.x);
-                                    v.y = signs_of_infinities(v.y);
-                                }
-                                float f0 = __uint_as_float(v.x << 16) * g, f1 = __uint_as_float(v.x & 0xffff0000u) * g;
-                                float f2 = __uint_as_float(v.y << 16) * g, f3 = __uint_as_float(v.y & 0xffff0000u) * g;
+                            float g = __int_as_float((268 - at) << 23);
+                            back = __int_as_float((at - 14) << 23);
+                            if (__any_sync(0xffffffffu, ex == 255)) {
+                                g = ex == 255 ? 1.f : g;
+                                back = ex == 255 ? INFINITY : back;
 #pragma unroll
-                                for (int i = 0; i < 3; ++i) {
-                                    const uint32_t y = e5m2x4(f0, f1, f2, f3);
-                                    *reinterpret_cast<uint32_t *>(sm + row + sw128_chunk(r & 127, 8 * i + (qc >> 1), 128) +
-                                                                  4 * e) = y;
-                                    const float4 h = wide5(y);
-                                    f0 -= h.x;
-                                    f1 -= h.y;
-                                    f2 -= h.z;
-                                    f3 -= h.w;
+                                for (int e = 0; e < 4; ++e) w[e] = ex == 255 ? signs_of_infinities(w[e]) : w[e];
+                            }
+                            // FP16 holds what the parts do, and E5M2 is its upper byte
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                h[e] = pack16<__half>(__uint_as_float(w[e] << 16) * g,
+                                                      __uint_as_float(w[e] & 0xffff0000u) * g);
+                            // first the 128 columns of the first part, then the next's;
+                            // the swizzle is that of the thread's first row
+                            uint8_t *to = sm + first8 + (r >> 7) * C::kQTile + (r & 127) / 8 * 1024;
+#pragma unroll
+                            for (int i = 0; i < 3; ++i) {
+                                *reinterpret_cast<uint2 *>(to + i * 16384) =
+                                    make_uint2(__byte_perm(h[0], h[1], 0x7531), __byte_perm(h[2], h[3], 0x7531));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t top = h[e] & 0xff00ff00u;
+                                    const __half2 left = __hsub2(*reinterpret_cast<const __half2 *>(&h[e]),
+                                                                 *reinterpret_cast<const __half2 *>(&top));
+                                    h[e] = *reinterpret_cast<const uint32_t *>(&left);
                                 }
                             }
                         } else {
