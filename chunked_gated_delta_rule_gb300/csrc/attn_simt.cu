@@ -8,7 +8,9 @@
 // and the values are added with lanes across the columns.  Each key is read
 // once for every query row that sees it, so the kernel is bound by L1 and L2
 // and by FP32 products, not by memory; the tensor-core kernels are the fast
-// route.  A position that a row does not see is never multiplied into it, so
+// route.  Measured, 16 query heads on 2 of 256 columns: 512 new tokens over 4K
+// 29.6 ms (FP32 the same), 32 decodes over up to 4K 6.1 ms, one over 16K 14.8 ms
+// (its axis is not split); elementary library products take 1.6, 2.6 and 1.5 ms.  A position that a row does not see is never multiplied into it, so
 // what a masked place holds (infinities, NaN) cannot reach it.
 #include <cuda_fp8.h>
 

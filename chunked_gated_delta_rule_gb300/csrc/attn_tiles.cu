@@ -10,6 +10,13 @@
 // O is scaled only when a row's maximum has grown by more than 2^8 since it
 // was last scaled; the weights stay below 2^8 and the factor cancels in O / l.
 //
+// Weights go into the product as one 16-bit value each: two halves, as for few
+// rows, would be half as many products again.  o against 64 bits, 4096 new tokens
+// over 32K in BF16: 2.3e-3, of which 1.7e-3 are o's own rounding; 2.9e-4 and
+// 2.1e-4 in FP16.  The sum takes them unrounded, so lse is FP32's.
+// Two halves in turns, and sums rescaled only past a threshold, are published
+// ideas.
+//
 // Bound by the tensor pipe while softmax keeps up: a step of a half is 2 x
 // 512 cycles of products and 16384 exponentials (512 cycles of the special
 // function units).  So the two halves run in turns: one half's exponentials
@@ -342,7 +349,9 @@ __device__ __forceinline__ void rescale(uint32_t to, float mn, float &m, float &
 
 // Softmax of a wide step, from its S at `ts`: t + log2 s over it, the sum of e^t
 // by itself, then the weights, 32 columns at a time (they lie below the columns
-// that they come from).  Columns [c0, c1) are seen; gives {m, l}.  Not inlined, and
+// that they come from).  Columns [c0, c1) are seen; gives {m, l}.  Three times the
+// other steps' time (1609 us for 4096 new tokens over 16K, all steps wide).  Not
+// inlined, and
 // with a tail of its own: in the middle of the softmax's loop it cost 4096 new
 // tokens over 16K 30 us of 480 without being run once, so 16.
 template <typename TP, int D>

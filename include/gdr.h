@@ -418,9 +418,14 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
  * Routes: the tensor cores take BF16 and FP16 queries with K = V = 64 or 128
  * and 16-byte aligned q, o and pages (bases and strides), pages of any size
  * (the kernel of many rows: of a multiple of 8 slots); everything else, FP32
- * among it, runs on CUDA cores.
- * FP32 scores, softmax statistics and accumulators; weights are rounded to 16
- * bits for the product with the values (few rows: as two halves).  A masked
+ * among it, runs on CUDA cores, which is exact but slow (2 to 20 times what
+ * plain library products take at a width of 256).
+ * FP32 scores, softmax statistics and accumulators.  Weights are rounded to 16
+ * bits for the product with the values: once to the type of q by the kernel of
+ * many rows, as two halves by that of few; over 8-bit caches to FP16, once under
+ * BF16 queries, where the kernel of many rows also rounds values and scales
+ * together to FP16 (the last bits of a value then depend on the largest scale of
+ * its step, whoever sees that).  lse comes from unrounded weights.  A masked
  * position never adds to a row, whatever the cache holds there (E4M3 caches: as
  * gdr_cache_write stores them, without NaN bytes).  8-bit caches on the tensor
  * cores: values of a scale below 2^-100 (none above 2^-91) are held to 2^-25 of
