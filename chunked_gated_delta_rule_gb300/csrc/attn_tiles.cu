@@ -110,7 +110,7 @@ struct TilesCfg {
     // tiles given back in pairs, a step's keys and the values before them
     // (one commit a step instead of two); 0: one by one
     static constexpr int kPairs = FMT ? 0 : kRing / 2;
-    static constexpr int kRaw = !FMT ? 0 : kSplit ? 1 : 2;                 // 8-bit tiles on their way
+    static constexpr int kRaw = !FMT ? 0 : kSplit ? 1 : 2;  // 8-bit tiles on their way
     static constexpr uint32_t kRawTile = kTN * D, kRawSize = kRawTile + 2 * kTN * 4;
     // steps whose scales are kept: a step's keys are widened once the products
     // of the step kRing / 2 before it are done, so that softmax is at most
@@ -351,9 +351,8 @@ __device__ __forceinline__ void rescale(uint32_t to, float mn, float &m, float &
 // by itself, then the weights, 32 columns at a time (they lie below the columns
 // that they come from).  Columns [c0, c1) are seen; gives {m, l}.  Three times the
 // other steps' time (1609 us for 4096 new tokens over 16K, all steps wide).  Not
-// inlined, and
-// with a tail of its own: in the middle of the softmax's loop it cost 4096 new
-// tokens over 16K 30 us of 480 without being run once, so 16.
+// inlined, and with a tail of its own: in the middle of the softmax's loop it cost
+// 4096 new tokens over 16K 30 us of 480 without being run once, so 16.
 template <typename TP, int D>
 __device__ __noinline__ float2 wide_step(uint32_t ts, uint32_t to, const float *scale, int c0, int c1, float f,
                                          float m, float l, bool begun) {
