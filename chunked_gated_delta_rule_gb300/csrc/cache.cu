@@ -15,7 +15,8 @@
 // value they were 39 to write one and 17 to read one (64K tokens x 8 heads to
 // E4M3 and back: 337 us).  So
 //   * the quotients come from one reciprocal a row: r = rn(1 / s), p = rn(x r),
-//     then twice p <- rn(p + r (x - p s)), products and sums fused.  The first
+//     then twice p <- rn(p - r (p s - x)), products and sums fused (with the signs
+//     so, a zero keeps its own).  The first
 //     step makes p faithful (p is within two units in the last place at the
 //     start), and a faithful p is then rounded correctly (Markstein, "Computation
 //     of elementary functions on the IBM RISC System/6000 processor", 1990), as
@@ -240,8 +241,8 @@ __device__ __forceinline__ void write_row(const Eight<Tin> &x, bool live, Tc *ds
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float q = f[i] * r;
-                q = fmaf(fmaf(-q, s, f[i]), r, q);
-                f[i] = fmaf(fmaf(-q, s, f[i]), r, q);
+                q = fmaf(fmaf(q, s, -f[i]), -r, q);
+                f[i] = fmaf(fmaf(q, s, -f[i]), -r, q);
             }
         } else {
             // a scale of a few of FP32's least units may be a third too small

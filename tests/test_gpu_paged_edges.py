@@ -320,3 +320,20 @@ def test_rows_whose_scale_is_rounded_far(fmt, most):
     want = torch.where(scale[:, None] > 0, x / scale[:, None], torch.zeros_like(x)).clamp(-most, most)
     step = 1.0 if fmt == "int8" else 32.0
     assert ((got - want).abs() <= step / 2).all() and (got * want >= 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_zeros_keep_their_sign(dtype):
+    """E4M3 has a zero of either sign, and -0 / s is -0."""
+    b = Batch([20], [20], heads=1, kv_heads=1, K=32, page=16, dtype=dtype, fmt="e4m3")
+    b.k[0, ::2, 0, 3] = -0.0
+    b.k[0, 1::2, 0, 3] = 0.0
+    kc, vc, ks, vs = (b.on(x) for x in ("kc", "vc", "ks", "vs"))
+    pkg.gdr_cache_write(b.on("k"), b.on("v"), kc, vc, b.on("table"), b.on("lens"), b.on("cu"),
+                        k_scale=ks, v_scale=vs)
+    at = torch.arange(20)
+    got = kc.cpu().view(torch.uint8)[b.table[0, at // 16].long(), at % 16, 0, 3]
+    assert got.tolist() == [128, 0] * 10
+    k, _ = pkg.gdr_cache_read(kc, vc, b.on("table"), b.on("lens"), 20, b.on("cu"), k_scale=ks,
+                              v_scale=vs, dtype=b.k.dtype)
+    assert torch.equal(torch.signbit(k[0, :, 0, 3]).cpu(), torch.arange(20) % 2 == 0)
