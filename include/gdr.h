@@ -430,7 +430,8 @@ int gdr_cache_read(const gdr_dims *dims, const gdr_paged_cache *cache, void *k, 
  * gdr_cache_write stores them, without NaN bytes).  8-bit caches on the tensor
  * cores: values of a scale below 2^-100 (none above 2^-91) are held to 2^-25 of
  * what 2^-100 would give, and the values' scales that matter to one row lie
- * within 2^100 of each other.  Results are bit-identical from run to run.
+ * within 2^100 of each other.  An infinity among the values that a row sees gives
+ * it an infinity or a NaN there.  Results are bit-identical from run to run.
  */
 int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const void *q,
                    const int32_t *cu_seqlens, void *o, float *lse, int causal,
