@@ -1,10 +1,12 @@
-"""GB300-native chunked gated-delta-rule forward and backward passes, and the
-paged cache and attention of the softmax layers beside them.
+"""GB300-native chunked gated-delta-rule forward and backward passes, the
+paged cache and attention of the softmax layers beside them, and the operators
+of state-space layers (short convolution, selective scan, norm).
 
 The compute path is a C-ABI CUDA library (``include/gdr.h``, built in-tree
 into ``_build/libgdr.so``); this package is its thin ctypes binding plus the
-seeded synthetic input generator, and ``chunk_gated_delta_rule``, a torch
-autograd function over the library's forward and backward entry points.
+seeded synthetic input generator, and torch autograd functions over the
+library's forward and backward entry points: ``chunk_gated_delta_rule``,
+``short_conv``, ``selective_scan`` and ``rms_norm``.
 There is no CPU fallback: every entry point raises if the CUDA library is
 missing.
 """
@@ -16,7 +18,13 @@ from .api import (GdrError, LaunchTimer, gdr_chunk_fwd, gdr_chunk_fwd_host,  # n
                   gdr_version,
                   gdr_workspace_size, load_library)
 
-from .autograd import chunk_gated_delta_rule  # noqa: F401,E402
+from .layer import (gdr_short_conv_fwd, gdr_short_conv_bwd,  # noqa: F401
+                    gdr_short_conv_bwd_workspace_size,
+                    gdr_selective_scan_fwd, gdr_selective_scan_bwd,
+                    gdr_selective_scan_workspace_size,
+                    gdr_rms_norm_fwd, gdr_rms_norm_bwd, gdr_rms_norm_bwd_workspace_size)
+from .autograd import (chunk_gated_delta_rule, rms_norm, selective_scan,  # noqa: F401,E402
+                       short_conv)
 
 # gdr_chunk_fwd_ex's options (scale, forced plan, workspace, status word) are
 # keyword arguments of gdr_chunk_fwd in Python.

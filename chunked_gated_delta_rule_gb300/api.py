@@ -57,11 +57,51 @@ class gdr_paged_cache(ctypes.Structure):
 SELFTEST_EXPORTS = ("gdr_selftest_umma", "gdr_selftest_tma", "gdr_selftest_inverse",
                     "gdr_selftest_timeout")
 
+class gdr_conv_dims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("C", ctypes.c_int64),
+                ("W", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("max_len", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
+class gdr_scan_dims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("C", ctypes.c_int64),
+                ("S", ctypes.c_int64), ("G", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("softplus", ctypes.c_int32), ("max_len", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64 * 2), ("c_stride", ctypes.c_int64 * 2)]
+
+
+class gdr_scan_tensors(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias")]
+
+
+class gdr_scan_grads(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz",
+                                                     "ddt_bias", "dh0")]
+
+
+class gdr_norm_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("group", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("sum_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
 # Every symbol include/gdr.h declares.
 EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_ex", "gdr_chunk_fwd_host", "gdr_chunk_fwd_noalloc",
            "gdr_workspace_size", "gdr_plan_query", "gdr_recurrent_fwd", "gdr_kernel_name", "gdr_error_string",
            "gdr_release_cached", "gdr_version", "gdr_chunk_bwd", "gdr_bwd_workspace_size",
-           "gdr_cache_write", "gdr_cache_read", "gdr_paged_attn", "gdr_attn_workspace_size")
+           "gdr_cache_write", "gdr_cache_read", "gdr_paged_attn", "gdr_attn_workspace_size",
+           "gdr_short_conv_fwd", "gdr_short_conv_bwd", "gdr_short_conv_bwd_workspace_size",
+           "gdr_selective_scan_fwd", "gdr_selective_scan_bwd", "gdr_selective_scan_workspace_size",
+           "gdr_selective_scan_bwd_workspace_size", "gdr_rms_norm_fwd", "gdr_rms_norm_bwd",
+           "gdr_rms_norm_bwd_workspace_size")
 
 _lib = None
 _lock = threading.Lock()
@@ -133,6 +173,25 @@ def load_library():
         lib.gdr_paged_attn.restype = ctypes.c_int
         lib.gdr_attn_workspace_size.argtypes = [dims_p, cache_p]
         lib.gdr_attn_workspace_size.restype = ctypes.c_size_t
+        opt_p, i64 = ctypes.POINTER(gdr_options), ctypes.c_int64
+        conv_p, norm_p = ctypes.POINTER(gdr_conv_dims), ctypes.POINTER(gdr_norm_dims)
+        scan_p, in_p = ctypes.POINTER(gdr_scan_dims), ctypes.POINTER(gdr_scan_tensors)
+        for name, args in (
+                ("gdr_short_conv_fwd", [conv_p, vp, vp, vp, i32p, vp, vp, i64, i32p, vp]),
+                ("gdr_short_conv_bwd", [conv_p, vp, vp, vp, i32p, vp, vp, vp, vp, vp, vp, vp]),
+                ("gdr_selective_scan_fwd", [scan_p, in_p, i32p, vp, vp, i64, i32p, vp, ctypes.c_int]),
+                ("gdr_selective_scan_bwd", [scan_p, in_p, i32p, vp, vp, vp,
+                                            ctypes.POINTER(gdr_scan_grads)]),
+                ("gdr_rms_norm_fwd", [norm_p, vp, vp, vp, vp, vp, vp]),
+                ("gdr_rms_norm_bwd", [norm_p, vp, vp, vp, vp, vp, vp])):
+            getattr(lib, name).argtypes = args + [opt_p, vp]
+            getattr(lib, name).restype = ctypes.c_int
+        for name, args in (("gdr_short_conv_bwd_workspace_size", [conv_p]),
+                           ("gdr_selective_scan_workspace_size", [scan_p, ctypes.c_int]),
+                           ("gdr_selective_scan_bwd_workspace_size", [scan_p]),
+                           ("gdr_rms_norm_bwd_workspace_size", [norm_p])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ctypes.c_size_t
         lib.gdr_release_cached.argtypes = []
         lib.gdr_release_cached.restype = ctypes.c_int
         lib.gdr_version.argtypes = []

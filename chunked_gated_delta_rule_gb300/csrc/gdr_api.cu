@@ -799,6 +799,23 @@ const char *gdr_kernel_name(int id) {
     case kKAttnRows: return "attn_rows";
     case kKAttnJoin: return "attn_join";
     case kKAttnTiles: return "attn_tiles";
+    case kKConv: return "short_conv";
+    case kKConvStep: return "short_conv_step";
+    case kKConvState: return "short_conv_state";
+    case kKConvBwd: return "short_conv_bwd";
+    case kKConvParams: return "short_conv_params";
+    case kKConvDh0: return "short_conv_dh0";
+    case kKNorm: return "rms_norm";
+    case kKNormBwd: return "rms_norm_bwd";
+    case kKNormWeight: return "rms_norm_weight";
+    case kKScan: return "scan";
+    case kKScanStep: return "scan_step";
+    case kKScanEnds: return "scan_ends";
+    case kKScanJoin: return "scan_join";
+    case kKScanBwdEnds: return "scan_bwd_ends";
+    case kKScanBwd: return "scan_bwd";
+    case kKScanBwdBC: return "scan_bwd_bc";
+    case kKScanBwdParams: return "scan_bwd_params";
     default: return "?";
     }
 }

@@ -93,6 +93,23 @@ enum KernelId {
     kKAttnRows = 36,
     kKAttnJoin = 37,
     kKAttnTiles = 38,
+    kKConv = 39,
+    kKConvStep = 40,
+    kKConvState = 41,
+    kKConvBwd = 42,
+    kKConvParams = 43,
+    kKConvDh0 = 44,
+    kKNorm = 45,
+    kKNormBwd = 46,
+    kKNormWeight = 47,
+    kKScan = 48,
+    kKScanStep = 49,
+    kKScanEnds = 50,
+    kKScanJoin = 51,
+    kKScanBwdEnds = 52,
+    kKScanBwd = 53,
+    kKScanBwdBC = 54,
+    kKScanBwdParams = 55,
     kKNumIds
 };
 

@@ -71,7 +71,7 @@ typedef struct CUstream_st *gdr_stream_t;
 
 /* Element type of q, k, v and o.  GDR_F16 runs on the CUDA-core path (the
  * tensor-core kernels take BF16).  The last two are formats of a paged cache
- * only (gdr_paged_cache). */
+ * (gdr_paged_cache) and of a norm's output (gdr_rms_norm_fwd) only. */
 enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1, GDR_F16 = 2, GDR_E4M3 = 3, GDR_I8 = 4 };
 
 /* Return codes. */
@@ -440,6 +440,156 @@ int gdr_paged_attn(const gdr_dims *dims, const gdr_paged_cache *cache, const voi
 /* Bytes of device scratch gdr_paged_attn needs (whatever its force_path).  0
  * on invalid arguments. */
 size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cache);
+
+/*
+ * The operators of a state-space layer, and of what lies around a layer of the
+ * rule: the short causal convolution of the projections, the selective scan (a
+ * diagonal state for each channel, where the rule has a matrix for each head) and
+ * the norm in front of a layer.  Token rows as above: B rows of T tokens, or N
+ * sequences packed along T with cu_seqlens; rows of channels, the last
+ * dimension contiguous, token strides in elements (0 = contiguous).  A call has
+ * at most 2^31 - 1 tokens.
+ * A token that no sequence holds (before cu[0], from cu[N] on) gets zeros as its
+ * outputs and gradients; such a table is reported as GDR_ERR_SEQLENS all the
+ * same.  Where offsets step back or leave [0, T], what the tokens get is
+ * unspecified; nothing outside the tensors is read or written.
+ * opt may hold status, workspace (256-byte aligned) and the launch events; the
+ * rest is zero.  Results are bit-identical from run to run.
+ */
+
+/*
+ * gdr_short_conv_fwd -- a filter of W taps (2 to 4) along each channel:
+ *   u[t, c] = bias[c] + sum_k weight[c, k] x[t - (W - 1) + k, c],
+ *   y = u (activation 0) or u / (1 + e^-u) (activation 1, SiLU).
+ *   x, y       [B, T, C] of dtype; sums in FP32.
+ *   weight     [C, W], bias [C] or NULL, of weight_dtype: dtype or GDR_F32.
+ *   h0, ht     [n_states, W - 1, C] of dtype: the W - 1 inputs before a
+ *              sequence's first token, oldest first (h0 NULL: zeros), and
+ *              those before the token that will follow its last (ht NULL: not
+ *              written).  ht == h0 moves the states on in place.
+ *   state_indices  [Nseq] row of each sequence, distinct within a call, or NULL
+ *              for row n.  An index outside [0, n_states) sets GDR_ERR_INDEX in
+ *              the status word: the sequence's outputs are zeros, no state is
+ *              touched.
+ *   max_len    as in gdr_dims: with at most 8 tokens a sequence (decode steps) a
+ *              thread takes a whole sequence, reading and writing its states
+ *              beside it.
+ */
+typedef struct gdr_conv_dims {
+    int64_t B, T, C, W, N;
+    int32_t dtype, flags;             /* GDR_F32, GDR_BF16, GDR_F16; GDR_SEQLENS_I64 */
+    int32_t weight_dtype, activation;
+    int64_t max_len;
+    int64_t x_stride, y_stride;       /* token strides; backward: y_stride is dy's    */
+} gdr_conv_dims;
+int gdr_short_conv_fwd(const gdr_conv_dims *dims, const void *x, const void *weight,
+                       const void *bias, const int32_t *cu_seqlens, const void *h0, void *ht,
+                       int64_t n_states, const int32_t *state_indices, void *y,
+                       const gdr_options *opt, gdr_stream_t stream);
+
+/*
+ * gdr_short_conv_bwd -- gradients of <dy, y> + <dht, ht> (h0, dht, dh0: row n for
+ * sequence n; each may be NULL).  dx [B, T, C] and dh0 of dtype, contiguous;
+ * dweight [C, W] and dbias [C] (NULL: not wanted) in FP32.
+ */
+int gdr_short_conv_bwd(const gdr_conv_dims *dims, const void *x, const void *weight,
+                       const void *bias, const int32_t *cu_seqlens, const void *h0,
+                       const void *dy, const void *dht, void *dx, float *dweight, float *dbias,
+                       void *dh0, const gdr_options *opt, gdr_stream_t stream);
+size_t gdr_short_conv_bwd_workspace_size(const gdr_conv_dims *dims);
+
+/*
+ * gdr_selective_scan_fwd -- for every channel c and state s (channel c belongs to
+ * group c / (C / G) of B and C):
+ *   d_t = log(1 + e^(dt_t + dt_bias))   (softplus 0: d_t = dt_t + dt_bias)
+ *   h_t = e^(d_t A) h_{t-1} + d_t x_t B_t
+ *   y_t = (sum_s C_t h_t + D x_t) z_t / (1 + e^-z_t)   (z NULL: without the gate)
+ *   x, dt, z, y    [B, T, C] of dtype.   B, C  [B, T, G, S] of dtype, S at most 64.
+ *   A              [C, S] FP32 (negative for states that decay).
+ *   D, dt_bias     [C] FP32, or NULL for zeros.
+ *   h0, ht, n_states, state_indices   as for gdr_short_conv_fwd, [n_states, C, S]
+ *                  FP32.
+ *   n_segments     0: the plan chooses; 1: sequences are run whole; S > 1: in
+ *                  pieces of about the S-th part of the longest (max_len), all
+ *                  at once, each from the state that a first pass finds for it.
+ * FP32 time steps, states and sums; an output is rounded once.
+ */
+typedef struct gdr_scan_dims {
+    int64_t B, T, C, S, G, N;
+    int32_t dtype, flags, softplus;
+    int64_t max_len;
+    int64_t x_stride, dt_stride, z_stride;  /* token strides                          */
+    int64_t y_stride;                       /* ... of y; backward: of dy              */
+    int64_t b_stride[2], c_stride[2];       /* token and group strides, or {0, 0}     */
+} gdr_scan_dims;
+typedef struct gdr_scan_tensors {
+    const void *x, *dt;
+    const float *A;
+    const void *B, *C;
+    const float *D;
+    const void *z;
+    const float *dt_bias;
+} gdr_scan_tensors;
+int gdr_selective_scan_fwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in,
+                           const int32_t *cu_seqlens, const float *h0, float *ht,
+                           int64_t n_states, const int32_t *state_indices, void *y,
+                           int n_segments, const gdr_options *opt, gdr_stream_t stream);
+size_t gdr_selective_scan_workspace_size(const gdr_scan_dims *dims, int n_segments);
+
+/*
+ * gdr_selective_scan_bwd -- gradients of <dy, y> + <dht, ht> (h0, dht: row n for
+ * sequence n, or NULL).  All outputs are contiguous: dx, ddt, dz of dtype like
+ * their inputs (dz exactly when z is given), dB and dC [B, T, G, S] of dtype; dA,
+ * dD, ddt_bias and dh0 FP32, dD, ddt_bias and dh0 NULL where not wanted.
+ */
+typedef struct gdr_scan_grads {
+    void *dx, *ddt;
+    float *dA;
+    void *dB, *dC;
+    float *dD;
+    void *dz;
+    float *ddt_bias, *dh0;
+} gdr_scan_grads;
+int gdr_selective_scan_bwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in,
+                           const int32_t *cu_seqlens, const float *h0, const void *dy,
+                           const float *dht, const gdr_scan_grads *out, const gdr_options *opt,
+                           gdr_stream_t stream);
+size_t gdr_selective_scan_bwd_workspace_size(const gdr_scan_dims *dims);
+
+/*
+ * gdr_rms_norm_fwd -- rows of D values (at most 16384):
+ *   r = x + residual, rounded to dtype and written to `sum` (without a residual
+ *   r = x, and both are NULL);  n = r / sqrt(mean(r^2) + eps);  y = n weight.
+ *   x, residual, sum  [rows, D] of dtype.  sum may be residual or x itself.
+ *   weight            [D] of weight_dtype (dtype or GDR_F32), or NULL for ones.
+ *   y                 [rows, D] of out_dtype: dtype; or GDR_E4M3 / GDR_I8 with a
+ *                     scale a row (group 0: scale [rows]) or each 128 columns
+ *                     (group 128: scale [rows, ceil(D / 128)]), as a paged cache
+ *                     stores its rows: s = max|y| * (1 / 448) or (1 / 127), q =
+ *                     round(y / s), 0 where s = 0; s = NaN and q = 0 where a y is
+ *                     not finite.  y may be x in place (same dtype).
+ * FP32 sums: rows whose sum of squares passes FP32's range get zeros.
+ */
+typedef struct gdr_norm_dims {
+    int64_t rows, D;
+    int32_t dtype, weight_dtype, out_dtype, group;
+    float eps;
+    int64_t x_stride, residual_stride, sum_stride, y_stride;  /* row strides; 0 = D */
+} gdr_norm_dims;
+int gdr_rms_norm_fwd(const gdr_norm_dims *dims, const void *x, const void *residual,
+                     const void *weight, void *sum, void *y, float *scale,
+                     const gdr_options *opt, gdr_stream_t stream);
+
+/*
+ * gdr_rms_norm_bwd -- from r (the forward's sum, or its x; x_stride) and dy
+ * (y_stride): dx = rstd (weight dy - n mean(weight dy n)) + dsum, the gradient of x and of the
+ * residual alike, with dsum (residual_stride) that of `sum` or NULL; dx is
+ * contiguous, of dtype.  dweight [D] FP32, or NULL.  out_dtype is dtype.
+ */
+int gdr_rms_norm_bwd(const gdr_norm_dims *dims, const void *r, const void *weight,
+                     const void *dy, const void *dsum, void *dx, float *dweight,
+                     const gdr_options *opt, gdr_stream_t stream);
+size_t gdr_rms_norm_bwd_workspace_size(const gdr_norm_dims *dims);
 
 /* Bytes of device scratch gdr_chunk_bwd needs for this problem (beta_free
  * != 0 for the beta-free mode; n_segments as passed to gdr_chunk_bwd),
