@@ -61,19 +61,21 @@ struct ScanArgs {
     float *E, *sd;            // [slots][C][S] states, [slots][C] sums of the time steps
     float *R, *part;          // backward: [slots][C][S]; [tiles][tokens][2 S]
     float *pd;                // backward: [slots][2 C] of D and dt_bias
-    int bytes, bc_bytes, out_bytes;
+    int bytes, bc_bytes;      // alignment: x, dt, z, y, dy; B and C
+    int st_bytes, out_bytes;  // A, h0, ht, dht, dh0; dx, ddt, dz
 };
 cudaError_t scan_step(const ScanArgs &a, int dtype, cudaStream_t st);
 cudaError_t scan_pieces(const ScanArgs &a, int dtype, bool summary, cudaStream_t st);
 cudaError_t scan_join(const ScanArgs &a, bool backward, cudaStream_t st);
-cudaError_t scan_bwd_summary(const ScanArgs &a, int dtype, cudaStream_t st);
+cudaError_t scan_bwd_ends(const ScanArgs &a, int dtype, cudaStream_t st);
 cudaError_t scan_bwd(const ScanArgs &a, int dtype, cudaStream_t st);
 cudaError_t scan_bwd_bc(const ScanArgs &a, int dtype, cudaStream_t st);
 cudaError_t scan_bwd_params(const ScanArgs &a, cudaStream_t st);
-// Channels that a block of the scan takes, and the blocks that all channels take.
-int scan_tile(int S);
-int64_t scan_tiles(int64_t C, int S, int G);
-// The backward's piece.
-constexpr int kScanBwdPiece = 128;
+// Channels that a block of the forward and of the backward scan takes, and the blocks (each within
+// a group) that all channels take.
+int scan_channels(int S);
+int scan_bwd_channels(int S);
+inline int64_t scan_tiles(int64_t C, int channels, int G) { return G * ((C / G + channels - 1) / channels); }
+constexpr int kScanBwdPiece = 64;  // the backward's
 
 }  // namespace gdr

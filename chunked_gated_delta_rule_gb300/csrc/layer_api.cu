@@ -151,7 +151,7 @@ int check_scan(const gdr_scan_dims *d) {
         return GDR_ERR_INVALID;
     if (d->S > 64 || d->C > INT32_MAX / 64) return GDR_ERR_UNSUPPORTED;
     // blocks of a launch: every piece (of 32 tokens at least) of every tile of channels
-    const int64_t seqs = d->N > 0 ? d->N : d->B, tiles = scan_tiles(d->C, (int)d->S, (int)d->G);
+    const int64_t seqs = d->N > 0 ? d->N : d->B, tiles = scan_tiles(d->C, scan_bwd_channels((int)d->S), (int)d->G);
     if (tokens_of(*d) / 32 + seqs + 1 > INT32_MAX / tiles ||
         seqs > INT32_MAX * (int64_t)256 / (d->C * d->S) - 1)
         return GDR_ERR_UNSUPPORTED;
@@ -167,10 +167,17 @@ int64_t scan_piece(const gdr_scan_dims &d, int n_segments) {
     if (n_segments > 1) {
         piece = ceil_div(longest, n_segments);
     } else if (n_segments == 0) {
-        const int64_t tiles = scan_tiles(d.C, (int)d.S, (int)d.G), sms = device_sms();
+        const int64_t tiles = scan_tiles(d.C, scan_channels((int)d.S), (int)d.G), sms = device_sms();
         const int64_t seqs = d.N > 0 ? d.N : d.B;
-        if (seqs * tiles < sms * 2) piece = ceil_div(tokens * tiles, sms * 4);
-        if (piece >= longest) piece = 0;
+        // Cycles of an SM.  Whole sequences: a token of the longest takes 187 where an SM has one
+        // block, 50 more for each other until they fill it, then 100 a block.  Pieces: 163 a token
+        // of a block in both passes, four blocks an SM, and the join.  (2048 channels of 16 states,
+        // whole / in pieces: one sequence of 16384 tokens 1530 / 278 us, 4 of 4096 389 / 287, 5 of
+        // 2048 245 / 191, 8 of 2048 245 / 287, 32 of 320 112 / 197.)
+        const int64_t mine = ceil_div(seqs * tiles, sms), slow = 187 + 50 * (mine - 1);
+        const int64_t whole = longest * (slow > 100 * mine ? slow : 100 * mine);
+        const int64_t cut = tokens * tiles / sms * 163 + 25000;
+        if (cut < whole) piece = ceil_div(tokens * tiles, sms * 4);
     }
     if (piece == 0) return 0;
     piece = ceil_div(piece, kPieceUnit) * kPieceUnit;
@@ -197,7 +204,7 @@ ScanScratch scan_scratch(const gdr_scan_dims &d, int64_t piece, bool backward) {
     if (backward) {
         s.R = take(slots * C * S);
         s.pd = take(slots * 2 * C);
-        s.part = take((size_t)scan_tiles(d.C, (int)d.S, (int)d.G) * (size_t)tokens_of(d) * 2 * S);
+        s.part = take((size_t)scan_tiles(d.C, scan_bwd_channels((int)d.S), (int)d.G) * (size_t)tokens_of(d) * 2 * S);
     }
     s.total = at;
     return s;
@@ -347,7 +354,7 @@ int gdr_selective_scan_fwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
     a.n_states = n_states;
     a.idx = state_indices;
     a.bytes = (int)common_bytes({(uint64_t)a.bytes, addr(y)});
-    a.out_bytes = common_bytes({addr(h0), addr(ht), addr(in->A)});
+    a.st_bytes = common_bytes({addr(h0), addr(ht), addr(in->A)});
     Call call(opt, stream);
     if (n_segments == 0 && longest_of(d) <= kFewTokens) {
         call.run(kKScanStep, [&] { return scan_step(a, d.dtype, call.st); });
@@ -395,6 +402,7 @@ int gdr_selective_scan_bwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
     a.dA = out->dA; a.dD = out->dD; a.dbias = out->ddt_bias; a.dh0 = out->dh0;
     const uint64_t es = (uint64_t)size_of(d.dtype), group = (uint64_t)(d.C / d.G) * es;
     a.bytes = (int)common_bytes({(uint64_t)a.bytes, addr(dy)});
+    a.st_bytes = common_bytes({addr(in->A), addr(h0), addr(dht), addr(out->dh0)});
     a.out_bytes = common_bytes({addr(out->dx), addr(out->ddt), addr(out->dz), d.C * es, d.G > 1 ? group : 0});
     a.piece = kScanBwdPiece;
     a.slots = slots_of(d, kScanBwdPiece);
@@ -407,7 +415,7 @@ int gdr_selective_scan_bwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
     a.sd = reinterpret_cast<float *>(call.base + s.sd);
     a.pd = reinterpret_cast<float *>(call.base + s.pd);
     a.part = reinterpret_cast<float *>(call.base + s.part);
-    call.run(kKScanBwdEnds, [&] { return scan_bwd_summary(a, d.dtype, call.st); });
+    call.run(kKScanBwdEnds, [&] { return scan_bwd_ends(a, d.dtype, call.st); });
     call.run(kKScanJoin, [&] { return scan_join(a, true, call.st); });
     call.run(kKScanBwd, [&] { return scan_bwd(a, d.dtype, call.st); });
     if (tokens) call.run(kKScanBwdBC, [&] { return scan_bwd_bc(a, d.dtype, call.st); });

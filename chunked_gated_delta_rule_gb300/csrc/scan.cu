@@ -24,42 +24,31 @@
 namespace gdr {
 namespace {
 
-// Tokens of a tile, and channels that a loading thread takes of one token.
+constexpr int kPS = 8;  // states of a thread
+
+// Channels of a block, tokens of a tile, channels that a loading thread takes of one token.
 template <int LPC>
-struct FwdLay : Lay<LPC> {
-    static constexpr int kT = 8 * LPC < 32 ? 8 * LPC : 32;
-    static constexpr int kV = kT * Lay<LPC>::kC / kNT;
-    static constexpr int kBC = kT * LPC * 2;                       // 4-state vectors of B and C
+struct Lay {
+    static constexpr int kC = kNT / LPC;
+    static constexpr int kT = LPC == 1 ? 8 : 16;
+    static constexpr int kV = kT * kC / kNT, kRows = kC / kV;
+    static constexpr int kBC = kT * LPC * 2;  // vectors of kPS states of B and C
     static constexpr int kBCper = (kBC + kNT - 1) / kNT;
 };
-
-// The sums of LPC tokens over a channel's LPC lanes: lane q ends with token q's.
-template <int LPC>
-__device__ __forceinline__ float fold(float (&v)[LPC], int q) {
-#pragma unroll
-    for (int m = LPC / 2; m >= 1; m >>= 1) {
-        const bool up = q & m;
-#pragma unroll
-        for (int i = 0; i < m; ++i) {
-            const float keep = up ? v[i + m] : v[i], send = up ? v[i] : v[i + m];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-        }
-    }
-    return v[0];
-}
 
 // SUM: leave a piece's end from a zero start (E) and the sum of its time steps (sd).  Else: the
 // outputs, from E (pieces) or from h0 (whole sequences), and the last state into ht.
 template <typename T, int LPC, bool SUM>
-__global__ void __launch_bounds__(kNT) k_scan(ScanArgs a, int tiles) {
-    using L = FwdLay<LPC>;
+__global__ void __launch_bounds__(kNT, 4) k_scan(ScanArgs a, int tiles) {
+    using L = Lay<LPC>;
     constexpr int kT = L::kT, V = L::kV, kC = L::kC;
-    __shared__ float2 sdx[kT][kC];  // time step and its product with x; the sums over states
-    __shared__ float4 sbc[2][kT][LPC];
+    using O = Order<V, L::kRows>;
+    __shared__ float2 sdx[kT][kC + O::kPad];  // time step and its product with x; the sums over states
+    __shared__ float4 sbc[2][kT][LPC][2];
     const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC;
     const int64_t slot = blockIdx.x / tiles;
-    const Tile tile = tile_of<LPC>(a, (int)(blockIdx.x % tiles));
-    const int tr = tid / (kC / V), cv = tid % (kC / V) * V;
+    const Tile tile = tile_of<kC>(a, (int)(blockIdx.x % tiles));
+    const int tr = tid / L::kRows, lv = tid % L::kRows, cv = lv * V;
     pdl_wait();
     if (!SUM && slot == a.slots) {  // tokens of no sequence
         if (!rows_packed(a.r)) return;
@@ -73,24 +62,32 @@ __global__ void __launch_bounds__(kNT) k_scan(ScanArgs a, int tiles) {
             zero.store((T *)a.y + t * a.ys + tile.c0 + cv, a.bytes, valid);
         return;
     }
-    if (!(SUM && a.piece == 0) && blockIdx.x == 0 && tid < 32) check_offsets(a.r);
+    if ((SUM || !a.piece) && blockIdx.x == 0 && tid < 32) check_offsets(a.r);
     const Piece p = piece_of(a, slot);
     if (p.n < 0) return;
     int64_t row = 0;
     if (!SUM && (a.h0 || a.ht)) row = state_row(a.idx, a.n_states, p.n, a.r.status);
-    const int64_t c = tile.c0 + cl;
-    const bool mine = cl < tile.valid;
+    const int ch = O::channel(cl);
+    const int64_t c = tile.c0 + ch, at_state = c * a.S + q * kPS;
+    const bool mine = ch < tile.valid;
 
-    float A2[kPS], h[kPS];
+    F2 A2[kPS / 2], h[kPS / 2];
+    {
+        const float *from = SUM || row < 0 ? nullptr
+                            : a.piece      ? a.E + slot * a.C * a.S
+                            : a.h0         ? a.h0 + row * a.C * a.S
+                                           : nullptr;
+        float fa[kPS], fh[kPS];
 #pragma unroll
-    for (int i = 0; i < kPS; ++i) {
-        const int s = q * kPS + i;
-        const bool in = mine && s < a.S;
-        A2[i] = in ? a.A[c * a.S + s] * kLog2e : 0.f;
-        h[i] = 0.f;
-        if (!SUM && in && row >= 0) {
-            if (a.piece) h[i] = a.E[(slot * a.C + c) * a.S + s];
-            else if (a.h0) h[i] = a.h0[(row * a.C + c) * a.S + s];
+        for (int i = 0; i < kPS; ++i) {
+            const bool in = mine && q * kPS + i < a.S;
+            fa[i] = in ? a.A[at_state + i] * kLog2e : 0.f;
+            fh[i] = in && from ? from[at_state + i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kPS / 2; ++i) {
+            A2[i] = f2(fa[2 * i], fa[2 * i + 1]);
+            h[i] = f2(fh[2 * i], fh[2 * i + 1]);
         }
     }
     float bias[V], skip[V];
@@ -102,7 +99,8 @@ __global__ void __launch_bounds__(kNT) k_scan(ScanArgs a, int tiles) {
     }
 
     Row<T, V> nx, nd, nz;
-    Row<T, 4> nbc[L::kBCper];
+    Row<T, kPS> nbc[L::kBCper];
+    constexpr int kLoadBC = SUM ? kT * LPC : L::kBC;
     auto fetch = [&](int at) {
         const int64_t t0 = p.t0 + at;
         const int len = p.len - at;
@@ -112,52 +110,58 @@ __global__ void __launch_bounds__(kNT) k_scan(ScanArgs a, int tiles) {
 #pragma unroll
         for (int k = 0; k < L::kBCper; ++k) {
             const int id = k * kNT + tid, which = id / (kT * LPC), t = id / LPC % kT, v = id % LPC;
-            if (id < (SUM ? kT * LPC : L::kBC))
-                load_bc<T>(nbc[k], which ? a.Cm : a.Bm, which ? a.cs : a.bs, tile.g, t0, t, len, 4 * v,
-                           a.S, a.bc_bytes);
+            if (id < kLoadBC)
+                load_bc<T, kPS>(nbc[k], which ? a.Cm : a.Bm, which ? a.cs : a.bs, tile.g, t0, t, len,
+                                kPS * v, a.S, a.bc_bytes);
         }
     };
     fetch(0);
     float total = 0.f;
     for (int at = 0; at < p.len; at += kT) {
-        Row<T, V> cx = nx, cz = nz;
+        const Row<T, V> cx = nx, cz = nz;
         {
-            float x[V], d[V];
+            float x[V], raw[V], d[V];
             nx.widen(x);
-            nd.widen(d);
+            nd.widen(raw);
+            time_steps<V>(a, raw, bias, d);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                // past the end a time step of zero leaves the states as they are
-                const float dt = at + tr < p.len ? time_step(a, d[j] + bias[j]) : 0.f;
-                sdx[tr][cv + j] = make_float2(dt, dt * x[j]);
+                if (at + tr >= p.len) d[j] = 0.f;  // past the end the states stay as they are
+                sdx[tr][O::place(lv, j)] = make_float2(d[j], d[j] * x[j]);
             }
         }
 #pragma unroll
         for (int k = 0; k < L::kBCper; ++k) {
             const int id = k * kNT + tid;
-            if (id < (SUM ? kT * LPC : L::kBC)) {
-                float f[4];
+            if (id < kLoadBC) {
+                float f[kPS];
                 nbc[k].widen(f);
-                sbc[id / (kT * LPC)][id / LPC % kT][id % LPC] = make_float4(f[0], f[1], f[2], f[3]);
+                float4 *to = sbc[id / (kT * LPC)][id / LPC % kT][id % LPC];
+                to[0] = make_float4(f[0], f[1], f[2], f[3]);
+                to[1] = make_float4(f[4], f[5], f[6], f[7]);
             }
         }
         __syncthreads();
         if (at + kT < p.len) fetch(at + kT);
-#pragma unroll 2
+#pragma unroll
         for (int t0 = 0; t0 < kT; t0 += LPC) {
             float y[LPC];
 #pragma unroll
             for (int k = 0; k < LPC; ++k) {
                 const float2 d = sdx[t0 + k][cl];
-                const float4 B = sbc[0][t0 + k][q];
-                const float b[4] = {B.x, B.y, B.z, B.w};
+                const F2 dd = f2(d.x), dx = f2(d.y);
+                const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(sbc[0][t0 + k][q]);
+                const ulonglong2 *C = reinterpret_cast<const ulonglong2 *>(sbc[1][t0 + k][q]);
+                const ulonglong2 b0 = B[0], b1 = B[1];
+                const F2 b[4] = {{b0.x}, {b0.y}, {b1.x}, {b1.y}};
 #pragma unroll
-                for (int i = 0; i < kPS; ++i) h[i] = fmaf(ex2(d.x * A2[i]), h[i], d.y * b[i]);
+                for (int i = 0; i < kPS / 2; ++i) h[i] = fma2(ex2(dd * A2[i]), h[i], dx * b[i]);
                 if constexpr (SUM) {
                     total += d.x;
                 } else {
-                    const float4 C = sbc[1][t0 + k][q];
-                    y[k] = fmaf(h[0], C.x, fmaf(h[1], C.y, fmaf(h[2], C.z, h[3] * C.w)));
+                    const ulonglong2 c0 = C[0], c1 = C[1];
+                    y[k] = both(fma2(h[0], F2{c0.x}, h[1] * F2{c0.y}) +
+                                fma2(h[2], F2{c1.x}, h[3] * F2{c1.y}));
                 }
             }
             if constexpr (!SUM) {
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kNT) k_scan(ScanArgs a, int tiles) {
             float x[V], y[V];
             cx.widen(x);
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = fmaf(skip[j], x[j], sdx[tr][cv + j].x);
+            for (int j = 0; j < V; ++j) y[j] = fmaf(skip[j], x[j], sdx[tr][O::place(lv, j)].x);
             if (a.z) {
                 float z[V];
                 cz.widen(z);
@@ -190,82 +194,96 @@ __global__ void __launch_bounds__(kNT) k_scan(ScanArgs a, int tiles) {
     if constexpr (SUM) {
         if (q == 0) a.sd[slot * a.C + c] = total;
     }
-    float *to = SUM ? a.E + (slot * a.C + c) * a.S
-                    : (a.ht && p.last && row >= 0 ? a.ht + (row * a.C + c) * a.S : nullptr);
+    float *to = SUM ? a.E + slot * a.C * a.S : (a.ht && p.last && row >= 0 ? a.ht + row * a.C * a.S : nullptr);
     if (to) {
 #pragma unroll
-        for (int i = 0; i < kPS; ++i)
-            if (q * kPS + i < a.S) to[q * kPS + i] = h[i];
+        for (int i = 0; i < kPS / 2; ++i) {
+            float lo, hi;
+            split(h[i], lo, hi);
+            if (q * kPS + 2 * i < a.S) to[at_state + 2 * i] = lo;
+            if (q * kPS + 2 * i + 1 < a.S) to[at_state + 2 * i + 1] = hi;
+        }
     }
 }
 
 // Ends of pieces into their starts, in place: h <- exp(A sd) h + E.  Backward (blockIdx.y = 1):
-// the gradients that enter the pieces' starts into those that reach their ends.
-__global__ void __launch_bounds__(256) k_scan_join(ScanArgs a) {
-    const int64_t per = a.C * a.S, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t n = id / per, i = id % per, c = i / a.S;
+// the gradients that enter the pieces' starts into those that reach their ends.  A thread has V
+// states of a channel (4, where S is a multiple), and the loads of several pieces in flight: the
+// pieces of a sequence follow one another, so what counts is what is asked for at once.
+template <int V>
+__global__ void __launch_bounds__(128) k_scan_join(ScanArgs a) {
+    const int per = (int)(a.C * a.S) / V;  // below 2^31
+    const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    const int64_t n = id / per, states = a.C * a.S;
+    const int at = (int)(id % per) * V, c = at / a.S;
     pdl_wait();
     if (n >= a.r.N) return;
     int64_t s, len;
     seq_span(a.r, n, s, len);
     const int64_t L = a.piece, first = s / L + n, pieces = max((int64_t)1, (len + L - 1) / L);
-    const float A2 = a.A[i] * kLog2e;
-    constexpr int kU = 8;  // pieces whose loads are in flight
-    if (blockIdx.y == 0) {
-        float h = 0.f;
-        if (a.h0) {
-            const int64_t row = state_row(a.idx, a.n_states, n, a.r.status);
-            if (row >= 0) h = a.h0[row * per + i];
-        }
-        for (int64_t j = 0; j < pieces; j += kU) {
-            float e[kU], d[kU];
+    const bool back = blockIdx.y;
+    float *const part = (back ? a.R : a.E) + first * states + at;
+    const float *const sd = a.sd + first * a.C + c;
+    float A2[V], h[V];
+    Row<float, V> r;
+    r.load(a.A + at, a.st_bytes, V);
+    r.widen(A2);
 #pragma unroll
-            for (int k = 0; k < kU; ++k)
-                if (j + k < pieces) {
-                    e[k] = a.E[(first + j + k) * per + i];
-                    d[k] = a.sd[(first + j + k) * a.C + c];
-                }
-#pragma unroll
-            for (int k = 0; k < kU; ++k)
-                if (j + k < pieces) {
-                    a.E[(first + j + k) * per + i] = h;
-                    h = fmaf(ex2(A2 * d[k]), h, e[k]);
-                }
-        }
-        return;
+    for (int k = 0; k < V; ++k) A2[k] *= kLog2e;
+    r.zero();
+    if (back) {
+        if (a.dht) r.load(a.dht + n * states + at, a.st_bytes, V);
+    } else if (a.h0) {
+        const int64_t row = state_row(a.idx, a.n_states, n, a.r.status);
+        if (row >= 0) r.load(a.h0 + row * states + at, a.st_bytes, V);
     }
-    float g = a.dht ? a.dht[n * per + i] : 0.f;
-    for (int64_t j = pieces - 1; j >= 0; j -= kU) {
-        float e[kU], d[kU];
+    r.widen(h);
+    constexpr int kU = 8;
+    for (int64_t j = 0; j < pieces; j += kU) {
+        Row<float, V> e[kU];
+        float d[kU];
 #pragma unroll
         for (int k = 0; k < kU; ++k)
-            if (j - k >= 0) {
-                e[k] = a.R[(first + j - k) * per + i];
-                d[k] = a.sd[(first + j - k) * a.C + c];
+            if (j + k < pieces) {
+                const int64_t i = back ? pieces - 1 - j - k : j + k;
+                e[k].load(part + i * states, 16, V);
+                d[k] = sd[i * a.C];
             }
 #pragma unroll
         for (int k = 0; k < kU; ++k)
-            if (j - k >= 0) {
-                a.R[(first + j - k) * per + i] = g;
-                g = fmaf(ex2(A2 * d[k]), g, e[k]);
+            if (j + k < pieces) {
+                const int64_t i = back ? pieces - 1 - j - k : j + k;
+                float f[V];
+                e[k].widen(f);
+                r.narrow(h);
+                r.store(part + i * states, 16, V);
+#pragma unroll
+                for (int v = 0; v < V; ++v) h[v] = fmaf(ex2(A2[v] * d[k]), h[v], f[v]);
             }
     }
-    if (a.dh0) a.dh0[n * per + i] = g;
+    if (back && a.dh0) {
+        r.narrow(h);
+        r.store(a.dh0 + n * states + at, a.st_bytes, V);
+    }
 }
 
-// Sequences of few tokens, a thread four states of a channel as above but straight from memory:
-// what counts is the states' row, read and written once.
+// Sequences of few tokens, straight from memory: what counts is the states' row, read and
+// written once.  A warp has 32 channels of a sequence: a lane four states of LPC of them (lane l
+// those of channels i (32 / LPC) + l / LPC), and with its own token values of channel l, whose time
+// step it forms for the others.
 template <typename T, int LPC>
 __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, int tiles) {
-    const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC;
-    const int64_t n = blockIdx.x / tiles;
-    const Tile tile = tile_of<LPC>(a, (int)(blockIdx.x % tiles));
-    const int64_t c = tile.c0 + cl;
-    if (blockIdx.x == 0 && tid < 32) check_offsets(a.r);
-    const bool mine = cl < tile.valid;
-    T *y = (T *)a.y + c;
+    constexpr int kCh = 32 / LPC;
+    const int lane = threadIdx.x & 31, q = lane % LPC, cl = lane / LPC;
+    const int64_t id = (int64_t)blockIdx.x * (kNT / 32) + (threadIdx.x >> 5);
+    const int64_t n = id / tiles;
+    if (blockIdx.x == 0 && threadIdx.x < 32) check_offsets(a.r);
+    if (n > a.r.N) return;
+    const Tile tile = tile_of<32>(a, (int)(id % tiles));
+    const bool mine = lane < tile.valid;
+    T *y = (T *)a.y + tile.c0 + lane;
     if (n == a.r.N) {  // tokens of no sequence
-        if (!rows_packed(a.r) || !mine || q) return;
+        if (!rows_packed(a.r) || !mine) return;
         const int64_t first = min(max(row_bound(a.r, 0), (int64_t)0), a.r.T);
         for (int64_t t = 0; t < first; ++t) y[t * a.ys] = from_f32<T>(0.f);
         for (int64_t t = max(row_bound(a.r, n), (int64_t)0); t < a.r.T; ++t)
@@ -276,96 +294,111 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, int tiles) {
     seq_span(a.r, n, s, len);
     if (a.h0 || a.ht) row = state_row(a.idx, a.n_states, n, a.r.status);
     if (row < 0) {
-        if (mine && q == 0)
+        if (mine)
             for (int64_t t = s; t < s + len; ++t) y[t * a.ys] = from_f32<T>(0.f);
         return;
     }
-    const int s0 = q * kPS;
-    const int have = mine ? max(0, min(kPS, a.S - s0)) : 0;
-    float A2[kPS], h[kPS];
-    {
-        Row<float, 4> ra, rh;
-        ra.load(a.A + c * a.S + s0, a.S % 4 ? 4 : a.out_bytes, have);
-        rh.zero();
-        if (a.h0) rh.load(a.h0 + (row * a.C + c) * a.S + s0, a.S % 4 ? 4 : a.out_bytes, have);
-        ra.widen(A2);
-        rh.widen(h);
-    }
+    const int s0 = q * 4, wide = a.S % 4 ? 4 : a.st_bytes;
+    const int64_t at_state = (tile.c0 + cl) * a.S + s0;
+    auto have = [&](int i) { return i * kCh + cl < tile.valid ? max(0, min(4, a.S - s0)) : 0; };
+    Row<float, 4> A[LPC], h[LPC];
 #pragma unroll
-    for (int i = 0; i < kPS; ++i) A2[i] *= kLog2e;
-    const float bias = a.dt_bias && mine ? a.dt_bias[c] : 0.f, skip = a.D && mine ? a.D[c] : 0.f;
+    for (int i = 0; i < LPC; ++i) {
+        const int64_t at = at_state + (int64_t)i * kCh * a.S;
+        h[i].zero();
+        if (a.h0) h[i].load(a.h0 + row * a.C * a.S + at, wide, have(i));
+        A[i].load(a.A + at, wide, have(i));
+    }
+    const float bias = a.dt_bias && mine ? a.dt_bias[tile.c0 + lane] : 0.f;
+    const float skip = a.D && mine ? a.D[tile.c0 + lane] : 0.f;
     for (int64_t t = s; t < s + len; ++t) {
         Row<T, 4> rb, rc;
-        rb.load((const T *)a.Bm + t * a.bs[0] + tile.g * a.bs[1] + s0, a.bc_bytes, have);
-        rc.load((const T *)a.Cm + t * a.cs[0] + tile.g * a.cs[1] + s0, a.bc_bytes, have);
-        float x = 0.f, d = 0.f, z = 0.f, b[4], cc[4];
+        const int states = max(0, min(4, a.S - s0));
+        rb.load((const T *)a.Bm + t * a.bs[0] + tile.g * a.bs[1] + s0, a.bc_bytes, states);
+        rc.load((const T *)a.Cm + t * a.cs[0] + tile.g * a.cs[1] + s0, a.bc_bytes, states);
+        float x = 0.f, d = 0.f, z = 0.f, b[4], cc[4], v[LPC];
         if (mine) {
-            x = to_f32(((const T *)a.x)[t * a.xs + c]);
-            d = time_step(a, to_f32(((const T *)a.dt)[t * a.dts + c]) + bias);
-            if (a.z) z = to_f32(((const T *)a.z)[t * a.zs + c]);
+            x = to_f32(((const T *)a.x)[t * a.xs + tile.c0 + lane]);
+            d = to_f32(((const T *)a.dt)[t * a.dts + tile.c0 + lane]) + bias;
+            if (a.z) z = to_f32(((const T *)a.z)[t * a.zs + tile.c0 + lane]);
+        }
+        if (a.softplus) {
+            float unused;
+            split(softplus2(f2(d)), d, unused);
         }
         rb.widen(b);
         rc.widen(cc);
-        float v = 0.f;
+        const float dx = d * x;
 #pragma unroll
-        for (int i = 0; i < kPS; ++i) {
-            h[i] = fmaf(ex2(d * A2[i]), h[i], d * x * b[i]);
-            v = fmaf(h[i], cc[i], v);
+        for (int i = 0; i < LPC; ++i) {
+            const float di = __shfl_sync(0xffffffffu, d, i * kCh + cl) * kLog2e;
+            const float dxi = __shfl_sync(0xffffffffu, dx, i * kCh + cl);
+            float A4[4], h4[4];
+            A[i].widen(A4);
+            h[i].widen(h4);
+            v[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h4[k] = fmaf(ex2(di * A4[k]), h4[k], dxi * b[k]);
+                v[i] = fmaf(h4[k], cc[k], v[i]);
+            }
+            h[i].narrow(h4);
         }
+        // lane q of a channel's lanes has the sum of the q-th of its channels
+        float sum = __shfl_sync(0xffffffffu, fold<LPC>(v, q), lane % kCh * LPC + lane / kCh);
+        sum = fmaf(skip, x, sum);
+        if (a.z) sum *= z * sigmoid_f(z);
+        if (mine) y[t * a.ys] = from_f32<T>(sum);
+    }
+    if (!a.ht) return;
 #pragma unroll
-        for (int m = LPC / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-        v = fmaf(skip, x, v);
-        if (a.z) v *= z * sigmoid_f(z);
-        if (mine && q == 0) y[t * a.ys] = from_f32<T>(v);
-    }
-    if (a.ht && have) {
-        Row<float, 4> r;
-        r.narrow(h);
-        r.store(a.ht + (row * a.C + c) * a.S + s0, a.S % 4 ? 4 : a.out_bytes, have);
-    }
+    for (int i = 0; i < LPC; ++i)
+        h[i].store(a.ht + row * a.C * a.S + at_state + (int64_t)i * kCh * a.S, wide, have(i));
 }
 
 }  // namespace
 
-int scan_tile(int S) { return kNT / (S <= 4 ? 1 : S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16); }
-int64_t scan_tiles(int64_t C, int S, int G) {
-    const int64_t per = C / G, kC = scan_tile(S);
-    return G * ((per + kC - 1) / kC);
-}
+// Channels of a block of k_scan.
+int scan_channels(int S) { return kNT / (S <= 8 ? 1 : S <= 16 ? 2 : S <= 32 ? 4 : 8); }
 
 cudaError_t scan_step(const ScanArgs &a, int dtype, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, a.S, a.G);
+    const int64_t tiles = scan_tiles(a.C, 32, a.G), warps = kNT / 32;
     return scan_type(dtype, [&](auto t) {
-        return scan_lanes(a.S, [&](auto l) {
+        return scan_lanes(a.S, 4, [&](auto l) {
             k_scan_step<decltype(t), decltype(l)::value>
-                <<<(unsigned)((a.r.N + 1) * tiles), kNT, 0, st>>>(a, (int)tiles);
+                <<<(unsigned)(((a.r.N + 1) * tiles + warps - 1) / warps), kNT, 0, st>>>(a, (int)tiles);
             return cudaGetLastError();
         });
     });
 }
 
 cudaError_t scan_pieces(const ScanArgs &a, int dtype, bool summary, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, a.S, a.G);
+    const int64_t tiles = scan_tiles(a.C, scan_channels(a.S), a.G);
     return scan_type(dtype, [&](auto t) {
-        return scan_lanes(a.S, [&](auto l) {
+        return scan_lanes(a.S, kPS, [&](auto l) {
             using T = decltype(t);
             constexpr int LPC = decltype(l)::value;
-            if (summary) {
-                k_scan<T, LPC, true><<<(unsigned)(a.slots * tiles), kNT, 0, st>>>(a, (int)tiles);
-                return cudaGetLastError();
+            if constexpr (LPC <= 8) {  // S is at most 64
+                if (summary) {
+                    k_scan<T, LPC, true><<<(unsigned)(a.slots * tiles), kNT, 0, st>>>(a, (int)tiles);
+                    return cudaGetLastError();
+                }
+                const dim3 grid((unsigned)((a.slots + 1) * tiles));
+                if (a.piece)
+                    return launch_pdl(k_scan<T, LPC, false>, grid, dim3(kNT), 0, st, a, (int)tiles);
+                k_scan<T, LPC, false><<<grid, kNT, 0, st>>>(a, (int)tiles);
             }
-            const dim3 grid((unsigned)((a.slots + 1) * tiles));
-            if (a.piece) return launch_pdl(k_scan<T, LPC, false>, grid, dim3(kNT), 0, st, a, (int)tiles);
-            k_scan<T, LPC, false><<<grid, kNT, 0, st>>>(a, (int)tiles);
             return cudaGetLastError();
         });
     });
 }
 
 cudaError_t scan_join(const ScanArgs &a, bool backward, cudaStream_t st) {
-    const int64_t all = a.r.N * a.C * a.S;
-    return launch_pdl(k_scan_join, dim3((unsigned)((all + 255) / 256), backward ? 2 : 1), dim3(256), 0,
-                      st, a);
+    const int V = a.S % 4 ? 1 : 4;
+    const int64_t all = a.r.N * a.C * a.S / V;
+    const dim3 grid((unsigned)((all + 127) / 128), backward ? 2 : 1);
+    if (V == 4) return launch_pdl(k_scan_join<4>, grid, dim3(128), 0, st, a);
+    return launch_pdl(k_scan_join<1>, grid, dim3(128), 0, st, a);
 }
 
 }  // namespace gdr

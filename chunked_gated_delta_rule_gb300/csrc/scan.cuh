@@ -1,10 +1,10 @@
 // scan.cuh -- what the selective scan's kernels share: how channels and states
-// lie over a block, how sequences are cut into pieces, and the staging of a
-// tile of tokens.
+// lie over a block, how sequences are cut into pieces, pairs of FP32 values, and
+// the time step.
 //
-// A thread holds four states of one channel; LPC neighbouring lanes (a power of
-// two, S <= 4 LPC) hold a channel's states, a block kNT / LPC channels.  States
-// past S have A = B = C = 0, so they stay zero.
+// A thread holds some neighbouring states of one or two channels; LPC
+// neighbouring lanes (a power of two) hold a channel's states.  States past S
+// have A = B = C = 0, so they stay zero.
 //
 // Pieces: sequence n is cut into ceil(len / L) pieces of L tokens.  Piece j of
 // it is slot floor(cu[n] / L) + n + j: since floor((a + len) / L) + 1 - floor(a /
@@ -17,15 +17,8 @@
 
 namespace gdr {
 
-constexpr int kNT = 256;     // threads of a block
-constexpr int kPS = 4;       // states of a thread
-constexpr float kLog2e = 1.4426950408889634f;
-
-template <int LPC>
-struct Lay {
-    static constexpr int kC = kNT / LPC;       // channels of a block
-    static constexpr int kS = kPS * LPC;       // states, padded
-};
+constexpr int kNT = 128;  // threads of a block
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -33,12 +26,83 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// log(1 + e^x)
-__device__ __forceinline__ float softplus_f(float x) {
-    return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x)));
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-__device__ __forceinline__ float time_step(const ScanArgs &a, float raw) {
-    return a.softplus ? softplus_f(raw) : raw;
+
+// Two FP32 values in a register pair: one instruction for both, at the same
+// rate of operations but half the issue slots, which the scan is short of.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 ex2(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return f2(ex2(lo), ex2(hi));
+}
+__device__ __forceinline__ float both(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return lo + hi;
+}
+
+// log(1 + e^x) = max(x, 0) + log(1 + u), u = e^-|x|, for two values.  u is 2^-t with what rounding
+// t = |x| log2(e) lost put back.  log(1 + u) = 2 artanh(s) with 2 s = u / (1 + u / 2); artanh(s) / s
+// is a polynomial in (2 s)^2 <= 4 / 9 (fitted here, off by 5e-9 at most).
+__device__ __forceinline__ F2 softplus2(F2 x) {
+    float a, b, ta, tb, va, vb;
+    split(x, a, b);
+    // from 100 on u counts for nothing; NaN stays
+    const F2 m = f2(fabsf(a) > 100.f ? 100.f : fabsf(a), fabsf(b) > 100.f ? 100.f : fabsf(b));
+    const F2 t = m * f2(kLog2e), lost = fma2(m, f2(-kLog2e), t);
+    split(t, ta, tb);
+    F2 u = f2(ex2(-ta), ex2(-tb));
+    u = fma2(u, lost * f2(kLn2), u);
+    split(fma2(u, f2(0.5f), f2(1.f)), va, vb);
+    const F2 s = u * f2(rcp(va), rcp(vb)), w = s * s;
+    F2 p = fma2(w, f2(0.00054710911f), f2(0.00218764110f));
+    p = fma2(w, p, f2(0.01250672713f));
+    p = fma2(w, p, f2(0.08333302289f));
+    p = fma2(w, p, f2(1.f));
+    return fma2(s, p, f2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+
+// Time steps of V channels from dt and its bias.
+template <int V>
+__device__ __forceinline__ void time_steps(const ScanArgs &a, const float (&raw)[V], const float (&bias)[V],
+                                           float (&d)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+        F2 x = f2(raw[j], raw[j + 1]) + f2(bias[j], bias[j + 1]);
+        if (a.softplus) x = softplus2(x);
+        split(x, d[j], d[j + 1]);
+    }
 }
 
 // The channels of tile `tile`: a tile lies within one group of B and C.
@@ -46,14 +110,14 @@ struct Tile {
     int64_t c0;
     int valid, g;
 };
-template <int LPC>
+template <int C>
 __device__ __forceinline__ Tile tile_of(const ScanArgs &a, int tile) {
-    const int per = (int)(a.C / a.G), tiles = (per + Lay<LPC>::kC - 1) / Lay<LPC>::kC;
+    const int per = (int)(a.C / a.G), tiles = (per + C - 1) / C;
     Tile t;
     t.g = tile / tiles;
-    const int at = tile % tiles * Lay<LPC>::kC;
+    const int at = tile % tiles * C;
     t.c0 = (int64_t)t.g * per + at;
-    t.valid = min(Lay<LPC>::kC, per - at);
+    t.valid = min(C, per - at);
     return t;
 }
 
@@ -108,22 +172,49 @@ __device__ __forceinline__ void load_row(Row<T, V> &r, const void *base, int64_t
     r.load((const T *)base + (t0 + tr) * stride + tile.c0 + cv, bytes, valid);
 }
 
-// Four states of B or C of token row t0 + tr, zeros past the ends.
-template <typename T>
-__device__ __forceinline__ void load_bc(Row<T, 4> &r, const void *base, const int64_t (&st)[2], int g,
+// K states of B or C of token row t0 + tr, zeros past the ends.
+template <typename T, int K>
+__device__ __forceinline__ void load_bc(Row<T, K> &r, const void *base, const int64_t (&st)[2], int g,
                                         int64_t t0, int tr, int len, int s0, int S, int bytes) {
-    const int valid = tr < len ? max(0, min(4, S - s0)) : 0;
+    const int valid = tr < len ? max(0, min(K, S - s0)) : 0;
     r.load((const T *)base + (t0 + tr) * st[0] + g * st[1] + s0, bytes, valid);
 }
 
+// The sums of LPC tokens over a channel's LPC lanes: lane q ends with token q's.
+template <int LPC>
+__device__ __forceinline__ float fold(float (&v)[LPC], int q) {
+#pragma unroll
+    for (int m = LPC / 2; m >= 1; m >>= 1) {
+        const bool up = q & m;
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+            const float keep = up ? v[i + m] : v[i], send = up ? v[i] : v[i + m];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        }
+    }
+    return v[0];
+}
+
+// Calls f(LPC) for lanes of `states` states each.
 template <typename F>
-cudaError_t scan_lanes(int S, F f) {
-    if (S <= 4) return f(std::integral_constant<int, 1>{});
-    if (S <= 8) return f(std::integral_constant<int, 2>{});
-    if (S <= 16) return f(std::integral_constant<int, 4>{});
-    if (S <= 32) return f(std::integral_constant<int, 8>{});
+cudaError_t scan_lanes(int S, int states, F f) {
+    if (S <= states) return f(std::integral_constant<int, 1>{});
+    if (S <= 2 * states) return f(std::integral_constant<int, 2>{});
+    if (S <= 4 * states) return f(std::integral_constant<int, 4>{});
+    if (S <= 8 * states) return f(std::integral_constant<int, 8>{});
     return f(std::integral_constant<int, 16>{});
 }
+// Where a tile's channels lie in a row of shared memory.  A loading thread has V neighbouring ones,
+// R threads a token's; its j-th value lies R behind its first, so that threads of a warp write side
+// by side, and rows are kPad apart more than they hold, so that its four rows do not meet in the
+// same banks.  (With channels in their order a store took 16 cycles for 2, which bound the scan.)
+template <int V, int R>
+struct Order {
+    static constexpr int kPad = R < 16 ? R : 0;
+    static __device__ __forceinline__ int channel(int place) { return place % R * V + place / R; }
+    static __device__ __forceinline__ int place(int lane, int j) { return j * R + lane; }
+};
+
 template <typename F>
 cudaError_t scan_type(int dtype, F f) {
     if (dtype == GDR_BF16) return f(__nv_bfloat16{});

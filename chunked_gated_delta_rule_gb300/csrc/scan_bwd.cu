@@ -13,32 +13,48 @@
 //      product of the decays so far, R = sum_t P_t C_t dv_t;
 //   2. the join turns ends into starts, forward for E and backward for R;
 //   3. the main pass runs the piece forward from its start, keeping the state in
-//      front of every 8 tokens, then backward 8 tokens at a time: their decays and
-//      states are formed again in registers and the gradients follow from the last
-//      to the first.
+//      front of every 8 tokens, then backward 4 tokens at a time: their states are
+//      formed again in registers and the gradients follow from the last token to
+//      the first.
 //   4. sums over channels (dB, dC) and over pieces (dA, dD, dbias), in a fixed order.
-// The exponentials are taken three times, which bounds the pass together with
-// the sums across lanes: over a channel's states for dx, dd and <C, h>, over the
-// channels for dB and dC.  Both fold several tokens, or the eight values of a
-// thread, at once, so that a shuffle carries a value that is still wanted.
+// What bounds the main pass is the number of instructions, most of them for the
+// sums across lanes: over a channel's states for dx, dd and <C, h>, over the
+// channels for dB and dC.  A thread therefore has two channels of four states (the
+// channels' sums begin in its registers), and lanes fold eight values at once, so
+// that a shuffle carries a value that is still wanted.  The decays are formed a
+// third time on the way back: an exponential costs less than the registers.
 #include "scan.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kU = 8;                          // tokens formed again at once
-constexpr int kKeep = kScanBwdPiece / kU;      // states kept of a piece
+constexpr int kU = 8;                      // tokens from one kept state to the next
+constexpr int kG = 4;                      // tokens whose states are in registers at once
+constexpr int kKeep = kScanBwdPiece / kU;  // states kept of a piece
+constexpr int kWarps = kNT / 32;
 
-template <int LPC>
-struct BwdLay : Lay<LPC> {
-    static constexpr int kT = LPC == 1 ? 8 : 16;  // tokens of a tile
-    static constexpr int kVals = kT * Lay<LPC>::kC;
-    static constexpr int kV = kVals / kNT >= 2 ? kVals / kNT : 2;
-    static constexpr int kLoad = kVals / kV;      // threads that load rows
-    static constexpr int kRows = Lay<LPC>::kC / kV;      // ... of one token
+// CH channels and STATES states of a thread: channels of a block, tokens of a tile, and what a
+// loading thread takes of it.
+template <int LPC, int CH, int STATES, int TOKENS>
+struct Lay {
+    static constexpr int kC = CH * kNT / LPC, kS = STATES * LPC;
+    static constexpr int kT = TOKENS;
+    static constexpr int kV = kT * kC / kNT;
+    static constexpr int kRows = kC / kV;     // loading threads of one token
+    static constexpr int kVec = STATES;       // states of a vector of B or C
     static constexpr int kBC = kT * LPC * 2;
     static constexpr int kBCper = (kBC + kNT - 1) / kNT;
+    using O = Order<kV, kRows>;
+    static constexpr int kPitch = kC + O::kPad;  // of a row of shared memory
+    static_assert(kV <= 8 && kV >= 2, "");
 };
+
+template <int LPC>
+using Ends = Lay<LPC, 1, 8, LPC == 1 ? 8 : 16>;
+// Few tokens a tile: a thread then loads few channels of one, and what it has loaded stays in its
+// registers until the tile's gradients are written (loading it again took a quarter of the pass).
+template <int LPC>
+using Main = Lay<LPC, 2, 4, LPC == 16 ? 16 : kU>;
 
 // dv = dout silu(z), or dout.
 template <int V>
@@ -49,122 +65,146 @@ __device__ __forceinline__ void gate_grad(const float (&g)[V], const float (&z)[
 }
 
 // Stages tokens [t0, t0 + kT) of the piece: time steps and their products with x, dv, B and C.
-template <typename T, int LPC>
+template <typename T, typename L>
 struct Stage {
-    using L = BwdLay<LPC>;
-    static constexpr int kT = L::kT, V = L::kV, kC = L::kC;
+    static constexpr int kT = L::kT, V = L::kV, kP = L::kPitch, LPC = L::kS / L::kVec;
+    using O = typename L::O;
     Row<T, V> x, dt, z, dy;
-    Row<T, 4> bc[L::kBCper];
+    Row<T, L::kVec> bc[L::kBCper];
 
     template <bool GRAD>
     __device__ __forceinline__ void fetch(const ScanArgs &a, const Tile &tile, int64_t t0, int len) {
         const int tid = threadIdx.x, tr = tid / L::kRows, cv = tid % L::kRows * V;
-        if (tid < L::kLoad) {
-            load_row<T, V>(x, a.x, a.xs, t0, tr, len, tile, cv, a.bytes);
-            load_row<T, V>(dt, a.dt, a.dts, t0, tr, len, tile, cv, a.bytes);
-            if constexpr (GRAD) {
-                load_row<T, V>(dy, a.dy, a.ys, t0, tr, len, tile, cv, a.bytes);
-                if (a.z) load_row<T, V>(z, a.z, a.zs, t0, tr, len, tile, cv, a.bytes);
-            }
+        load_row<T, V>(x, a.x, a.xs, t0, tr, len, tile, cv, a.bytes);
+        load_row<T, V>(dt, a.dt, a.dts, t0, tr, len, tile, cv, a.bytes);
+        if constexpr (GRAD) {
+            load_row<T, V>(dy, a.dy, a.ys, t0, tr, len, tile, cv, a.bytes);
+            if (a.z) load_row<T, V>(z, a.z, a.zs, t0, tr, len, tile, cv, a.bytes);
         }
 #pragma unroll
         for (int k = 0; k < L::kBCper; ++k) {
             const int id = k * kNT + tid, which = id / (kT * LPC), t = id / LPC % kT, v = id % LPC;
             if (id < (GRAD ? L::kBC : kT * LPC))
-                load_bc<T>(bc[k], which ? a.Cm : a.Bm, which ? a.cs : a.bs, tile.g, t0, t, len, 4 * v,
-                           a.S, a.bc_bytes);
+                load_bc<T, L::kVec>(bc[k], which ? a.Cm : a.Bm, which ? a.cs : a.bs, tile.g, t0, t, len,
+                                    L::kVec * v, a.S, a.bc_bytes);
         }
     }
+    // sbc: [2][kT][kS]; bias: of the tile's channels, in the order of their places
     template <bool GRAD>
-    __device__ __forceinline__ void put(const ScanArgs &a, const float (&bias)[V], int len,
-                                        float2 (*sdx)[kC], float (*sdv)[kC], float4 (*sbc)[kT][LPC]) {
-        const int tid = threadIdx.x, tr = tid / L::kRows, cv = tid % L::kRows * V;
-        if (tid < L::kLoad) {
-            float fx[V], fd[V];
-            x.widen(fx);
-            dt.widen(fd);
+    __device__ __forceinline__ void put(const ScanArgs &a, const float *bias, int len, float2 (*sdx)[kP],
+                                        float (*sdv)[kP], float *sbc) const {
+        const int tid = threadIdx.x, tr = tid / L::kRows, lv = tid % L::kRows;
+        float fx[V], raw[V], fb[V], d[V];
+        x.widen(fx);
+        dt.widen(raw);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = tr < len ? time_step(a, fd[j] + bias[j]) : 0.f;
-                sdx[tr][cv + j] = make_float2(d, d * fx[j]);
-            }
-            if constexpr (GRAD) {
-                float g[V], fz[V], dv[V];
-                dy.widen(g);
-                if (a.z) z.widen(fz);
-                gate_grad<V>(g, fz, a.z != nullptr, dv);
+        for (int j = 0; j < V; ++j) fb[j] = bias[O::place(lv, j)];
+        time_steps<V>(a, raw, fb, d);
 #pragma unroll
-                for (int j = 0; j < V; ++j) sdv[tr][cv + j] = dv[j];
-            }
+        for (int j = 0; j < V; ++j) {
+            if (tr >= len) d[j] = 0.f;  // past the end the states stay as they are
+            sdx[tr][O::place(lv, j)] = make_float2(d[j], d[j] * fx[j]);
+        }
+        if constexpr (GRAD) {
+            float g[V], fz[V], dv[V];
+            dy.widen(g);
+            if (a.z) z.widen(fz);
+            gate_grad<V>(g, fz, a.z != nullptr, dv);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sdv[tr][O::place(lv, j)] = dv[j];
         }
 #pragma unroll
         for (int k = 0; k < L::kBCper; ++k) {
             const int id = k * kNT + tid;
             if (id < (GRAD ? L::kBC : kT * LPC)) {
-                float f[4];
+                float f[L::kVec];
                 bc[k].widen(f);
-                sbc[id / (kT * LPC)][id / LPC % kT][id % LPC] = make_float4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+                for (int i = 0; i < L::kVec; i += 4)
+                    *reinterpret_cast<float4 *>(sbc + id * L::kVec + i) =
+                        make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
             }
         }
     }
 };
 
-template <int LPC>
-__device__ __forceinline__ void load_A2(const ScanArgs &a, int64_t c, bool mine, int q, float (&A2)[kPS]) {
-#pragma unroll
-    for (int i = 0; i < kPS; ++i) {
-        const int s = q * kPS + i;
-        A2[i] = mine && s < a.S ? a.A[c * a.S + s] * kLog2e : 0.f;
+// The bias of the tile's channels in the order of their places, and D behind it.
+template <typename L>
+__device__ __forceinline__ void load_channels(const ScanArgs &a, const Tile &tile, float *to) {
+    for (int i = threadIdx.x; i < L::kC; i += kNT) {
+        const int ch = L::O::channel(i);
+        to[i] = a.dt_bias && ch < tile.valid ? a.dt_bias[tile.c0 + ch] : 0.f;
+        to[L::kC + i] = a.D && ch < tile.valid ? a.D[tile.c0 + ch] : 0.f;
     }
 }
-template <int V>
-__device__ __forceinline__ void load_channel(const float *p, const Tile &tile, int cv, float (&f)[V]) {
+
+// 2 P values of A or of a state, zeros past S and the tile.
+template <int P>
+__device__ __forceinline__ void load_states(const float *p, int64_t at, int s0, int S, bool mine, float by,
+                                            F2 (&to)[P]) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = p && cv + j < tile.valid ? p[tile.c0 + cv + j] : 0.f;
+    for (int i = 0; i < P; ++i)
+        to[i] = f2(p && mine && s0 + 2 * i < S ? p[at + 2 * i] * by : 0.f,
+                   p && mine && s0 + 2 * i + 1 < S ? p[at + 2 * i + 1] * by : 0.f);
+}
+template <int P>
+__device__ __forceinline__ void store_states(float *p, int64_t at, int s0, int S, const F2 (&from)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        float lo, hi;
+        split(from[i], lo, hi);
+        if (s0 + 2 * i < S) p[at + 2 * i] = lo;
+        if (s0 + 2 * i + 1 < S) p[at + 2 * i + 1] = hi;
+    }
 }
 
-// 1. E, sd and R of a piece.
+// 1. E, sd and R of a piece.  A thread has eight states of a channel.
 template <typename T, int LPC>
-__global__ void __launch_bounds__(kNT) k_scan_bwd_sum(ScanArgs a, int tiles) {
-    using L = BwdLay<LPC>;
-    constexpr int kT = L::kT, V = L::kV, kC = L::kC;
-    __shared__ float2 sdx[kT][kC];
-    __shared__ float sdv[kT][kC];
-    __shared__ float4 sbc[2][kT][LPC];
+__global__ void __launch_bounds__(kNT) k_scan_bwd_ends(ScanArgs a, int tiles) {
+    using L = Ends<LPC>;
+    constexpr int kT = L::kT, kC = L::kC, P = 4;
+    __shared__ __align__(16) float2 sdx[kT][L::kPitch];
+    __shared__ float sdv[kT][L::kPitch], sch[2 * kC];
+    __shared__ __align__(16) float sbc[2 * kT * L::kS];
     const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC;
     const int64_t slot = blockIdx.x / tiles;
-    const Tile tile = tile_of<LPC>(a, (int)(blockIdx.x % tiles));
+    const Tile tile = tile_of<kC>(a, (int)(blockIdx.x % tiles));
     if (blockIdx.x == 0 && tid < 32) check_offsets(a.r);
     const Piece p = piece_of(a, slot);
     if (p.n < 0) return;
-    const int64_t c = tile.c0 + cl;
-    const bool mine = cl < tile.valid;
-    float A2[kPS], h[kPS], P[kPS], R[kPS], bias[V], total = 0.f;
-    load_A2<LPC>(a, c, mine, q, A2);
-    load_channel<V>(a.dt_bias, tile, tid % L::kRows * V, bias);
+    const int ch = L::O::channel(cl);
+    const int64_t c = tile.c0 + ch, at_state = c * a.S + q * 8;
+    const bool mine = ch < tile.valid;
+    F2 A2[P], h[P], D[P], R[P];
+    float total = 0.f;
+    load_states<P>(a.A, at_state, q * 8, a.S, mine, kLog2e, A2);
 #pragma unroll
-    for (int i = 0; i < kPS; ++i) {
-        h[i] = R[i] = 0.f;
-        P[i] = 1.f;
+    for (int i = 0; i < P; ++i) {
+        h[i] = R[i] = f2(0.f);
+        D[i] = f2(1.f);
     }
-    Stage<T, LPC> s;
+    Stage<T, L> s;
     s.template fetch<true>(a, tile, p.t0, p.len);
+    load_channels<L>(a, tile, sch);
+    __syncthreads();
     for (int at = 0; at < p.len; at += kT) {
-        s.template put<true>(a, bias, p.len - at, sdx, sdv, sbc);
+        s.template put<true>(a, sch, p.len - at, sdx, sdv, sbc);
         __syncthreads();
         if (at + kT < p.len) s.template fetch<true>(a, tile, p.t0 + at + kT, p.len - at - kT);
 #pragma unroll 4
         for (int t = 0; t < kT; ++t) {
             const float2 d = sdx[t][cl];
-            const float dv = sdv[t][cl];
-            const float4 B = sbc[0][t][q], C = sbc[1][t][q];
-            const float b[4] = {B.x, B.y, B.z, B.w}, cc[4] = {C.x, C.y, C.z, C.w};
+            const F2 dd = f2(d.x), dx = f2(d.y), dv = f2(sdv[t][cl]);
+            const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(sbc + t * L::kS + q * 8);
+            const ulonglong2 *C = reinterpret_cast<const ulonglong2 *>(sbc + (kT + t) * L::kS + q * 8);
+            const ulonglong2 b0 = B[0], b1 = B[1], c0 = C[0], c1 = C[1];
+            const F2 b[P] = {{b0.x}, {b0.y}, {b1.x}, {b1.y}}, cc[P] = {{c0.x}, {c0.y}, {c1.x}, {c1.y}};
 #pragma unroll
-            for (int i = 0; i < kPS; ++i) {
-                const float w = ex2(d.x * A2[i]);
-                h[i] = fmaf(w, h[i], d.y * b[i]);
-                P[i] *= w;
-                R[i] = fmaf(P[i], cc[i] * dv, R[i]);
+            for (int i = 0; i < P; ++i) {
+                const F2 w = ex2(dd * A2[i]);
+                h[i] = fma2(w, h[i], dx * b[i]);
+                D[i] = D[i] * w;
+                R[i] = fma2(D[i], cc[i] * dv, R[i]);
             }
             total += d.x;
         }
@@ -172,26 +212,22 @@ __global__ void __launch_bounds__(kNT) k_scan_bwd_sum(ScanArgs a, int tiles) {
     }
     if (!mine) return;
     if (q == 0) a.sd[slot * a.C + c] = total;
-#pragma unroll
-    for (int i = 0; i < kPS; ++i)
-        if (q * kPS + i < a.S) {
-            a.E[(slot * a.C + c) * a.S + q * kPS + i] = h[i];
-            a.R[(slot * a.C + c) * a.S + q * kPS + i] = R[i];
-        }
+    store_states<P>(a.E + slot * a.C * a.S, at_state, q * 8, a.S, h);
+    store_states<P>(a.R + slot * a.C * a.S, at_state, q * 8, a.S, R);
 }
 
-// Sums of v[token] over a channel's LPC lanes.  A lane ends with kU / LPC tokens (at least one),
-// those from first_token<LPC>(q) on.
+// Sums of eight values over a channel's LPC lanes.  A lane ends with 8 / LPC of them (at least
+// one), those from first_of<LPC>(q) on; with LPC = 16 two lanes end with the same.
 template <int LPC>
-__device__ __forceinline__ void fold_states(float (&v)[kU], int q) {
-    int n = kU;
+__device__ __forceinline__ void fold_states(float (&v)[8], int q) {
+    int n = 8;
 #pragma unroll
     for (int m = LPC / 2; m >= 1; m >>= 1) {
         if (n > 1) {
             n >>= 1;
             const bool up = q & m;
 #pragma unroll
-            for (int i = 0; i < kU / 2; ++i)
+            for (int i = 0; i < 4; ++i)
                 if (i < n) {
                     const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
                     v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
@@ -202,12 +238,12 @@ __device__ __forceinline__ void fold_states(float (&v)[kU], int q) {
     }
 }
 template <int LPC>
-__device__ __forceinline__ int first_token(int q) {
-    return LPC <= kU ? q * (kU / LPC) : q / (LPC / kU);
+__device__ __forceinline__ int first_of(int q) {
+    return LPC <= 8 ? q * (8 / LPC) : q / 2;
 }
 
-// Sums of v[8] (four states of B, four of C) over the warp's 32 / LPC channels.  A lane ends
-// with 8 / channels of them (at least one), from first_value<LPC>(channel) on.
+// Sums of eight values (four states of B, four of C) over the warp's 32 / LPC lanes of one state.
+// A lane ends with 8 / lanes of them (at least one).
 template <int LPC>
 __device__ __forceinline__ void fold_channels(float (&v)[8], int lane) {
     int n = 8;
@@ -229,28 +265,43 @@ __device__ __forceinline__ void fold_channels(float (&v)[8], int lane) {
 }
 
 template <int LPC>
-constexpr size_t bwd_smem() {
-    using L = BwdLay<LPC>;
-    return sizeof(float4) * kKeep * kNT + sizeof(float2) * L::kT * L::kC + sizeof(float) * L::kT * L::kC +
-           sizeof(float4) * 2 * L::kT * LPC + sizeof(float) * (kNT / 32) * L::kT * 2 * L::kS;
+struct Smem {
+    using L = Main<LPC>;
+    float4 keep[kKeep][2][kNT];        // states in front of every kU tokens
+    float sbc[2 * L::kT * L::kS];
+    float2 sdx[L::kT][L::kPitch];      // time step, and its product with x
+    float2 res[L::kT][L::kPitch];      // <dh, B>, <e, A> / ln 2
+    float sdv[L::kT][L::kPitch];       // dv, then <C, h>
+    float red[kWarps][L::kT][2 * L::kS];
+    float sch[2 * L::kC];
+};
+
+// Four states of two channels, forward by a token; y: <C, h> of the two.
+template <bool OUT>
+__device__ __forceinline__ void step(const float4 &d, const ulonglong2 &B, const ulonglong2 &C,
+                                     const F2 (&A2)[2][2], F2 (&h)[2][2], float *y) {
+    const float dd[2] = {d.x, d.z}, dx[2] = {d.y, d.w};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const F2 dk = f2(dd[k]), xk = f2(dx[k]);
+        h[k][0] = fma2(ex2(dk * A2[k][0]), h[k][0], xk * F2{B.x});
+        h[k][1] = fma2(ex2(dk * A2[k][1]), h[k][1], xk * F2{B.y});
+        if constexpr (OUT) y[k] = both(fma2(h[k][0], F2{C.x}, h[k][1] * F2{C.y}));
+    }
 }
 
 // 3. The gradients of a piece.  At the end E's slot holds its part of dA.
 template <typename T, int LPC>
-__global__ void __launch_bounds__(kNT, 2) k_scan_bwd(ScanArgs a, int tiles) {
-    using L = BwdLay<LPC>;
+__global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, int tiles) {
+    using L = Main<LPC>;
     constexpr int kT = L::kT, V = L::kV, kC = L::kC, kS = L::kS;
-    extern __shared__ float4 smem[];
-    float4(*keep)[kNT] = reinterpret_cast<float4(*)[kNT]>(smem);
-    float4(*sbc)[kT][LPC] = reinterpret_cast<float4(*)[kT][LPC]>(smem + kKeep * kNT);
-    float2(*sdx)[kC] = reinterpret_cast<float2(*)[kC]>(smem + kKeep * kNT + 2 * kT * LPC);
-    float(*sdv)[kC] = reinterpret_cast<float(*)[kC]>(sdx + kT);
-    float(*red)[kT][2 * kS] = reinterpret_cast<float(*)[kT][2 * kS]>(sdv + kT);
+    extern __shared__ __align__(16) uint8_t raw_smem[];
+    Smem<LPC> &sm = *reinterpret_cast<Smem<LPC> *>(raw_smem);
     const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC, lane = tid & 31, warp = tid >> 5;
     const int64_t slot = blockIdx.x / tiles;
     const int tile_id = (int)(blockIdx.x % tiles);
-    const Tile tile = tile_of<LPC>(a, tile_id);
-    const int tr = tid / L::kRows, cv = tid % L::kRows * V;
+    const Tile tile = tile_of<kC>(a, tile_id);
+    const int tr = tid / L::kRows, lv = tid % L::kRows, cv = lv * V;
     const int64_t all = total_tokens(a.r);
     float *part = a.part + (int64_t)tile_id * all * 2 * a.S;
     T *dx = (T *)a.dx, *ddt = (T *)a.ddt, *dz = (T *)a.dz;
@@ -261,12 +312,11 @@ __global__ void __launch_bounds__(kNT, 2) k_scan_bwd(ScanArgs a, int tiles) {
         zero.zero();
         const int valid = max(0, min(V, tile.valid - cv));
         auto clear = [&](int64_t from, int64_t to) {
-            if (tid < L::kLoad)
-                for (int64_t t = from + tr; t < to; t += kT) {
-                    zero.store(dx + t * a.C + tile.c0 + cv, a.out_bytes, valid);
-                    zero.store(ddt + t * a.C + tile.c0 + cv, a.out_bytes, valid);
-                    if (a.z) zero.store(dz + t * a.C + tile.c0 + cv, a.out_bytes, valid);
-                }
+            for (int64_t t = from + tr; t < to; t += kT) {
+                zero.store(dx + t * a.C + tile.c0 + cv, a.out_bytes, valid);
+                zero.store(ddt + t * a.C + tile.c0 + cv, a.out_bytes, valid);
+                if (a.z) zero.store(dz + t * a.C + tile.c0 + cv, a.out_bytes, valid);
+            }
             for (int64_t i = from * 2 * a.S + tid; i < to * 2 * a.S; i += kNT) part[i] = 0.f;
         };
         clear(0, min(max(row_bound(a.r, 0), (int64_t)0), a.r.T));
@@ -274,115 +324,140 @@ __global__ void __launch_bounds__(kNT, 2) k_scan_bwd(ScanArgs a, int tiles) {
         return;
     }
     const Piece p = piece_of(a, slot);
-    const int64_t c = tile.c0 + cl, at_state = (slot * a.C + c) * a.S + q * kPS;
-    const bool mine = cl < tile.valid;
     const int len = p.n < 0 ? 0 : p.len;
-    float A[kPS], A2[kPS], h[kPS], dh[kPS], dA[kPS], bias[V], skip[V], dD[V], db[V];
+    const int s0 = q * 4;
+    int64_t at_state[2];
+    bool mine[2];
+    F2 A2[2][2], h[2][2], dh[2][2], dA[2][2];
 #pragma unroll
-    for (int i = 0; i < kPS; ++i) {
-        const bool in = mine && q * kPS + i < a.S;
-        A[i] = in ? a.A[c * a.S + q * kPS + i] : 0.f;
-        A2[i] = A[i] * kLog2e;
-        h[i] = in && len ? a.E[at_state + i] : 0.f;
-        dh[i] = in && len ? a.R[at_state + i] : 0.f;
-        dA[i] = 0.f;
+    for (int k = 0; k < 2; ++k) {
+        const int ch = L::O::channel(2 * cl + k);
+        at_state[k] = (tile.c0 + ch) * a.S + s0;
+        mine[k] = ch < tile.valid;
+        load_states<2>(a.A, at_state[k], s0, a.S, mine[k], kLog2e, A2[k]);
+        load_states<2>(len ? a.E + slot * a.C * a.S : nullptr, at_state[k], s0, a.S, mine[k], 1.f, h[k]);
+        load_states<2>(len ? a.R + slot * a.C * a.S : nullptr, at_state[k], s0, a.S, mine[k], 1.f, dh[k]);
+        dA[k][0] = dA[k][1] = f2(0.f);
     }
-    load_channel<V>(a.dt_bias, tile, cv, bias);
-    load_channel<V>(a.D, tile, cv, skip);
+    float dD[V], db[V];  // of the channels that the thread loads
 #pragma unroll
     for (int j = 0; j < V; ++j) dD[j] = db[j] = 0.f;
+    load_channels<L>(a, tile, sm.sch);
+    auto B_at = [&](int t) { return *reinterpret_cast<const ulonglong2 *>(sm.sbc + t * kS + s0); };
+    auto C_at = [&](int t) { return *reinterpret_cast<const ulonglong2 *>(sm.sbc + (kT + t) * kS + s0); };
+    auto d_at = [&](int t) { return *reinterpret_cast<const float4 *>(&sm.sdx[t][2 * cl]); };
 
-    Stage<T, LPC> s;
+    Stage<T, L> s;
     if (len) s.template fetch<false>(a, tile, p.t0, len);
+    __syncthreads();
     for (int at = 0; at < len; at += kT) {
-        s.template put<false>(a, bias, len - at, sdx, sdv, sbc);
+        s.template put<false>(a, sm.sch, len - at, sm.sdx, sm.sdv, sm.sbc);
         __syncthreads();
         if (at + kT < len) s.template fetch<false>(a, tile, p.t0 + at + kT, len - at - kT);
         else s.template fetch<true>(a, tile, p.t0 + at, len - at);  // the backward's first
 #pragma unroll
         for (int u = 0; u < kT; u += kU) {
-            keep[(at + u) / kU][tid] = make_float4(h[0], h[1], h[2], h[3]);
 #pragma unroll
-            for (int t = u; t < u + kU; ++t) {
-                const float2 d = sdx[t][cl];
-                const float4 B = sbc[0][t][q];
-                const float b[4] = {B.x, B.y, B.z, B.w};
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<ulonglong2 *>(&sm.keep[(at + u) / kU][k][tid]) =
+                    make_ulonglong2(h[k][0].v, h[k][1].v);
 #pragma unroll
-                for (int i = 0; i < kPS; ++i) h[i] = fmaf(ex2(d.x * A2[i]), h[i], d.y * b[i]);
-            }
+            for (int t = u; t < u + kU; ++t) step<false>(d_at(t), B_at(t), ulonglong2{}, A2, h, nullptr);
         }
         __syncthreads();
     }
     for (int at = (len - 1) / kT * kT; at >= 0 && len; at -= kT) {
-        Row<T, V> cx = s.x, cd = s.dt, cz = s.z, cy = s.dy;
-        s.template put<true>(a, bias, len - at, sdx, sdv, sbc);
+        const Row<T, V> cx = s.x, cd = s.dt, cz = s.z, cy = s.dy;
+        s.template put<true>(a, sm.sch, len - at, sm.sdx, sm.sdv, sm.sbc);
         __syncthreads();
         if (at) s.template fetch<true>(a, tile, p.t0 + at - kT, len - at + kT);
 #pragma unroll 1
-        for (int u = kT - kU; u >= 0; u -= kU) {
-            float w[kU][kPS], hs[kU][kPS], v[kU], hb[kU], ea[kU], h0[kPS];
-            const float4 k0 = keep[(at + u) / kU][tid];
-            h0[0] = k0.x; h0[1] = k0.y; h0[2] = k0.z; h0[3] = k0.w;
+        for (int u = kT - kG; u >= 0; u -= kG) {
+            F2 hs[kG][2][2], before[2][2];
 #pragma unroll
-            for (int t = 0; t < kU; ++t) {
-                const float2 d = sdx[u + t][cl];
-                const float4 B = sbc[0][u + t][q], C = sbc[1][u + t][q];
-                const float b[4] = {B.x, B.y, B.z, B.w}, cc[4] = {C.x, C.y, C.z, C.w};
-                v[t] = 0.f;
-#pragma unroll
-                for (int i = 0; i < kPS; ++i) {
-                    w[t][i] = ex2(d.x * A2[i]);
-                    hs[t][i] = fmaf(w[t][i], t ? hs[t - 1][i] : h0[i], d.y * b[i]);
-                    v[t] = fmaf(hs[t][i], cc[i], v[t]);
-                }
+            for (int k = 0; k < 2; ++k) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sm.keep[(at + u) / kU][k][tid]);
+                before[k][0] = F2{x.x};
+                before[k][1] = F2{x.y};
             }
+            if (u % kU) {  // the second half of what was kept
 #pragma unroll
-            for (int t = kU - 1; t >= 0; --t) {
-                const float2 d = sdx[u + t][cl];
-                const float dv = sdv[u + t][cl];
-                const float4 B = sbc[0][u + t][q], C = sbc[1][u + t][q];
-                const float b[4] = {B.x, B.y, B.z, B.w}, cc[4] = {C.x, C.y, C.z, C.w};
+                for (int t = kG; t > 0; --t) step<false>(d_at(u - t), B_at(u - t), ulonglong2{}, A2, before, nullptr);
+            }
+            float y[2 * kG], hb[2 * kG], ea[2 * kG];  // of token t and channel k in 2 t + k
+#pragma unroll
+            for (int t = 0; t < kG; ++t) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) hs[t][k][j] = t ? hs[t ? t - 1 : 0][k][j] : before[k][j];
+                step<true>(d_at(u + t), B_at(u + t), C_at(u + t), A2, hs[t], y + 2 * t);
+            }
+            if (a.z) fold_states<LPC>(y, q);
+            // so that nothing of the way there is kept in registers for the way back
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int t = kG - 1; t >= 0; --t) {
+                const float4 d = d_at(u + t);
+                const float2 dv2 = *reinterpret_cast<const float2 *>(&sm.sdv[u + t][2 * cl]);
+                const ulonglong2 B = B_at(u + t), C = C_at(u + t);
+                const F2 b[2] = {{B.x}, {B.y}}, cc[2] = {{C.x}, {C.y}};
+                const float ds[2] = {d.x, d.z}, dxs[2] = {d.y, d.w}, dvs[2] = {dv2.x, dv2.y};
+                F2 dB[2], dC[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const F2 dd = f2(ds[k]), dx2 = f2(dxs[k]), dv = f2(dvs[k]);
+                    F2 e[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        F2 &g = dh[k][j];
+                        g = fma2(dv, cc[j], g);
+                        dB[j] = k ? fma2(g, dx2, dB[j]) : g * dx2;
+                        dC[j] = k ? fma2(dv, hs[t][k][j], dC[j]) : dv * hs[t][k][j];
+                        e[j] = g * b[j];
+                    }
+                    hb[2 * t + k] = both(e[0] + e[1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        F2 &g = dh[k][j];
+                        g = g * ex2(dd * A2[k][j]);
+                        e[j] = g * (t ? hs[t ? t - 1 : 0][k][j] : before[k][j]);
+                        dA[k][j] = fma2(e[j], dd, dA[k][j]);
+                    }
+                    ea[2 * t + k] = both(fma2(e[0], A2[k][0], e[1] * A2[k][1]));
+                }
                 float bc[8];
-                hb[t] = ea[t] = 0.f;
 #pragma unroll
-                for (int i = 0; i < kPS; ++i) {
-                    dh[i] = fmaf(dv, cc[i], dh[i]);
-                    bc[i] = dh[i] * d.y;
-                    bc[4 + i] = dv * hs[t][i];
-                    hb[t] = fmaf(dh[i], b[i], hb[t]);
-                    dh[i] *= w[t][i];
-                    const float e = dh[i] * (t ? hs[t - 1][i] : h0[i]);
-                    ea[t] = fmaf(e, A[i], ea[t]);
-                    dA[i] = fmaf(e, d.x, dA[i]);
+                for (int j = 0; j < 2; ++j) {
+                    split(dB[j], bc[2 * j], bc[2 * j + 1]);
+                    split(dC[j], bc[4 + 2 * j], bc[5 + 2 * j]);
                 }
                 fold_channels<LPC>(bc, lane);
-                // the channel's number among the warp's 32 / LPC names the values a lane has
+                // the lane's number among those of its states names the values that it has
                 constexpr int kCh = 32 / LPC, kHas = kCh >= 8 ? 1 : 8 / kCh, kDup = kCh > 8 ? kCh / 8 : 1;
                 const int ch = lane / LPC;
                 if (ch % kDup == 0) {
 #pragma unroll
                     for (int i = 0; i < kHas; ++i) {
                         const int idx = ch / kDup * kHas + i;  // B's four, C's four
-                        red[warp][u + t][idx / 4 * kS + q * kPS + idx % 4] = bc[i];
+                        sm.red[warp][u + t][idx / 4 * kS + s0 + idx % 4] = bc[i];
                     }
                 }
             }
-            fold_states<LPC>(v, q);
             fold_states<LPC>(hb, q);
             fold_states<LPC>(ea, q);
-            __syncwarp();
-            constexpr int kMine = kU / LPC >= 1 ? kU / LPC : 1;
+            __syncwarp();  // dv of these tokens has been read
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int t = u + first_token<LPC>(q) + i;
-                if (LPC <= kU || q % (LPC / kU ? LPC / kU : 1) == 0) {
-                    sdx[t][cl] = make_float2(hb[i], ea[i]);
-                    sdv[t][cl] = v[i];
+            for (int i = 0; i < (LPC <= 8 ? 8 / LPC : 1); ++i) {
+                const int idx = first_of<LPC>(q) + i, t = u + idx / 2, place = 2 * cl + idx % 2;
+                if (LPC <= 8 || q % 2 == 0) {
+                    sm.res[t][place] = make_float2(hb[i], ea[i]);
+                    if (a.z) sm.sdv[t][place] = y[i];
                 }
             }
         }
         __syncthreads();
-        if (tid < L::kLoad && at + tr < len) {
+        if (at + tr < len) {
             const int valid = max(0, min(V, tile.valid - cv));
             float x[V], raw[V], g[V], z[V], dv[V], ox[V], ot[V], oz[V];
             cx.widen(x);
@@ -392,16 +467,17 @@ __global__ void __launch_bounds__(kNT, 2) k_scan_bwd(ScanArgs a, int tiles) {
             gate_grad<V>(g, z, a.z != nullptr, dv);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float2 r = sdx[tr][cv + j];  // <dh, B>, <e, A>
-                const float pre = raw[j] + bias[j], d = time_step(a, pre);
-                ox[j] = fmaf(r.x, d, dv[j] * skip[j]);
-                ot[j] = fmaf(r.x, x[j], r.y);
-                if (a.softplus) ot[j] *= sigmoid_f(pre);
+                const int at_j = L::O::place(lv, j);
+                const float2 r = sm.res[tr][at_j];
+                const float skip = sm.sch[kC + at_j];
+                ox[j] = fmaf(r.x, sm.sdx[tr][at_j].x, dv[j] * skip);
+                ot[j] = fmaf(r.x, x[j], r.y * kLn2);
+                if (a.softplus) ot[j] *= sigmoid_f(raw[j] + sm.sch[at_j]);
                 dD[j] = fmaf(dv[j], x[j], dD[j]);
                 db[j] += ot[j];
                 if (a.z) {
                     const float sg = sigmoid_f(z[j]);
-                    oz[j] = g[j] * fmaf(skip[j], x[j], sdv[tr][cv + j]) * sg * fmaf(z[j], 1.f - sg, 1.f);
+                    oz[j] = g[j] * fmaf(skip, x[j], sm.sdv[tr][at_j]) * sg * fmaf(z[j], 1.f - sg, 1.f);
                 }
             }
             const int64_t to = (p.t0 + at + tr) * a.C + tile.c0 + cv;
@@ -420,31 +496,28 @@ __global__ void __launch_bounds__(kNT, 2) k_scan_bwd(ScanArgs a, int tiles) {
             if (at + t >= len || st >= a.S) continue;
             float sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < kNT / 32; ++k) sum += red[k][t][w * kS + st];
+            for (int k = 0; k < kWarps; ++k) sum += sm.red[k][t][w * kS + st];
             part[((p.t0 + at + t) * 2 + w) * a.S + st] = sum;
         }
         __syncthreads();
     }
-    if (mine) {
 #pragma unroll
-        for (int i = 0; i < kPS; ++i)
-            if (q * kPS + i < a.S) a.E[at_state + i] = dA[i];
-    }
+    for (int k = 0; k < 2; ++k)
+        if (mine[k]) store_states<2>(a.E + slot * a.C * a.S, at_state[k], s0, a.S, dA[k]);
     // dD and dbias: the sums of the loading threads' rows, one behind the other
-    float(*sum)[2][kC] = reinterpret_cast<float(*)[2][kC]>(smem);
+    float(*sum)[2][kC] = reinterpret_cast<float(*)[2][kC]>(&sm.keep);  // [kT]
     __syncthreads();
-    if (tid < L::kLoad) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            sum[tr][0][cv + j] = dD[j];
-            sum[tr][1][cv + j] = db[j];
-        }
+    for (int j = 0; j < V; ++j) {
+        sum[tr][0][cv + j] = dD[j];
+        sum[tr][1][cv + j] = db[j];
     }
     __syncthreads();
     for (int i = tid; i < 2 * kC; i += kNT) {
         const int w = i / kC, ch = i % kC;
         if (ch >= tile.valid) continue;
         float f = 0.f;
+#pragma unroll
         for (int t = 0; t < kT; ++t) f += sum[t][w][ch];
         a.pd[(slot * 2 + w) * a.C + tile.c0 + ch] = f;
     }
@@ -487,24 +560,30 @@ __global__ void __launch_bounds__(256) k_scan_bwd_params(ScanArgs a) {
 
 }  // namespace
 
-cudaError_t scan_bwd_summary(const ScanArgs &a, int dtype, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, a.S, a.G);
+// Channels of a block of the main pass.
+int scan_bwd_channels(int S) { return 2 * kNT / (S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16); }
+
+cudaError_t scan_bwd_ends(const ScanArgs &a, int dtype, cudaStream_t st) {
     return scan_type(dtype, [&](auto t) {
-        return scan_lanes(a.S, [&](auto l) {
-            k_scan_bwd_sum<decltype(t), decltype(l)::value>
-                <<<(unsigned)(a.slots * tiles), kNT, 0, st>>>(a, (int)tiles);
+        return scan_lanes(a.S, 8, [&](auto l) {
+            constexpr int LPC = decltype(l)::value;
+            if constexpr (LPC <= 8) {  // S is at most 64
+                using T = decltype(t);
+                const int64_t tiles = scan_tiles(a.C, Ends<LPC>::kC, a.G);
+                k_scan_bwd_ends<T, LPC><<<(unsigned)(a.slots * tiles), kNT, 0, st>>>(a, (int)tiles);
+            }
             return cudaGetLastError();
         });
     });
 }
 
 cudaError_t scan_bwd(const ScanArgs &a, int dtype, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, a.S, a.G);
+    const int64_t tiles = scan_tiles(a.C, scan_bwd_channels(a.S), a.G);
     return scan_type(dtype, [&](auto t) {
-        return scan_lanes(a.S, [&](auto l) {
+        return scan_lanes(a.S, 4, [&](auto l) {
             using T = decltype(t);
-            constexpr int LPC = decltype(l)::value;
-            constexpr size_t smem = bwd_smem<LPC>();
+            constexpr int LPC = decltype(l)::value < 2 ? 2 : decltype(l)::value;
+            constexpr size_t smem = sizeof(Smem<LPC>);
             static std::atomic<uint64_t> done{0};
             cudaError_t e = once_a_device(done, [] {
                 return cudaFuncSetAttribute(k_scan_bwd<T, LPC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -518,7 +597,7 @@ cudaError_t scan_bwd(const ScanArgs &a, int dtype, cudaStream_t st) {
 }
 
 cudaError_t scan_bwd_bc(const ScanArgs &a, int dtype, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, a.S, a.G);
+    const int64_t tiles = scan_tiles(a.C, scan_bwd_channels(a.S), a.G);
     const int64_t all = rows_packed(a.r) ? a.r.T : a.r.N * a.r.T, outs = all * a.G * 2 * a.S;
     return scan_type(dtype, [&](auto t) {
         return launch_pdl(k_scan_bwd_bc<decltype(t)>, dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, st,
