@@ -9,17 +9,19 @@
 // sum_t du[t] x[t - (W - 1) + k], db = sum_t du[t].
 //
 // Bound by memory: 2 W + 4 operations a value against the 4 bytes that it moves
-// forward.  A thread takes 16 bytes of neighbouring channels and walks a run of
-// tokens with the last W - 1 inputs in registers, so every row is read once but
-// for the W - 1 before a run.  Sequences lie behind one another: a thread looks
-// up which one its run starts in and goes from there.
+// forward.  A thread takes neighbouring channels and walks a run of tokens with
+// the last W - 1 inputs in registers, so every row is read once but for the W - 1
+// before a run.  The rows to come are on their way to shared memory meanwhile, each
+// thread's to places of its own: in registers they would leave too few threads to
+// keep the memory busy.  Sequences lie behind one another: a thread looks up which
+// one its run starts in and goes from there.
 #include "layer.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 8;  // rows that a thread has in flight
+constexpr int kAhead = 4;  // tokens that a thread asks for at once
 
 // Channels of a thread: 16 bytes, where rows start at multiples of that and C is
 // a multiple; else one.
@@ -27,8 +29,8 @@ template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
 template <typename T, int W, int V>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int64_t c, float (&w)[W][V],
-                                          float (&b)[V]) {
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int64_t c, F2 (&w)[W][kPairs<V>],
+                                          F2 (&b)[kPairs<V>]) {
     float flat[V * W];
     if (V % 4 == 0 && a.w_bytes >= 16) {  // a multiple of 16 bytes lies at a multiple of 16
         if (a.w.f32) {
@@ -54,45 +56,44 @@ __device__ __forceinline__ void load_taps(const ConvArgs &a, int64_t c, float (&
         for (int i = 0; i < V * W; ++i) flat[i] = param_at<T>(a.w, c * W + i);
     }
 #pragma unroll
-    for (int k = 0; k < W; ++k)
+    for (int j = 0; j < kPairs<V>; ++j) {
+        const int hi = 2 * j + 1 < V ? 2 * j + 1 : 2 * j;
 #pragma unroll
-        for (int j = 0; j < V; ++j) w[k][j] = flat[j * W + k];
-#pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = a.b.p ? param_at<T>(a.b, c + j) : 0.f;
+        for (int k = 0; k < W; ++k) w[k][j] = f2(flat[2 * j * W + k], flat[hi * W + k]);
+        b[j] = a.b.p ? f2(param_at<T>(a.b, c + 2 * j), param_at<T>(a.b, c + hi)) : f2(0.f);
+    }
 }
 
 // The W - 1 inputs before token t of sequence [s, ..), oldest first; those before s from row
 // `row` of h0.
 template <typename T, int W, int V>
 __device__ __forceinline__ void load_window(const ConvArgs &a, int64_t t, int64_t s, int64_t row,
-                                            int64_t c, float (&win)[W - 1][V]) {
+                                            int64_t c, F2 (&win)[W - 1][kPairs<V>]) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         const int64_t p = t - (W - 1) + k;
         Row<T, V> r;
         if (p >= s) r.load((const T *)a.x + p * a.xs + c, 16, V);
-        else if (a.h0)
-            r.load((const T *)a.h0 + (row * (W - 1) + (W - 1) + (p - s)) * a.C + c, 16, V);
+        else if (a.h0) r.load((const T *)a.h0 + (row * (W - 1) + (W - 1) + (p - s)) * a.C + c, 16, V);
         else r.zero();
-        r.widen(win[k]);
+        widen2<T, V>(r, win[k]);
     }
 }
 
-template <int W, int V>
-__device__ __forceinline__ void taps(const float (&w)[W][V], const float (&b)[V],
-                                     const float (&win)[W - 1][V], const float (&x)[V],
-                                     float (&u)[V]) {
+template <int W, int P>
+__device__ __forceinline__ void taps(const F2 (&w)[W][P], const F2 (&b)[P], const F2 (&win)[W - 1][P],
+                                     const F2 (&x)[P], F2 (&u)[P]) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        u[j] = fmaf(w[W - 1][j], x[j], b[j]);
+    for (int j = 0; j < P; ++j) {
+        u[j] = fma2(w[W - 1][j], x[j], b[j]);
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) u[j] = fmaf(w[k][j], win[k][j], u[j]);
+        for (int k = 0; k < W - 1; ++k) u[j] = fma2(w[k][j], win[k][j], u[j]);
     }
 }
-template <int W, int V>
-__device__ __forceinline__ void shift(float (&win)[W - 1][V], const float (&x)[V]) {
+template <int W, int P>
+__device__ __forceinline__ void shift(F2 (&win)[W - 1][P], const F2 (&x)[P]) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < P; ++j) {
 #pragma unroll
         for (int k = 0; k + 1 < W - 1; ++k) win[k][j] = win[k + 1][j];
         win[W - 2][j] = x[j];
@@ -100,36 +101,93 @@ __device__ __forceinline__ void shift(float (&win)[W - 1][V], const float (&x)[V
 }
 
 template <typename T, int W, int V>
-__device__ __forceinline__ void one_token(const ConvArgs &a, const Row<T, V> &r, int64_t t,
-                                          int64_t c, const float (&w)[W][V],
-                                          const float (&b)[V], float (&win)[W - 1][V]) {
-    float x[V], u[V];
-    r.widen(x);
-    taps<W, V>(w, b, win, x, u);
-    shift<W, V>(win, x);
+__device__ __forceinline__ void one_token(const ConvArgs &a, const Row<T, V> &r, int64_t t, int64_t c,
+                                          const F2 (&w)[W][kPairs<V>], const F2 (&b)[kPairs<V>],
+                                          F2 (&win)[W - 1][kPairs<V>]) {
+    constexpr int P = kPairs<V>;
+    F2 x[P], u[P];
+    widen2<T, V>(r, x);
+    taps<W, P>(w, b, win, x, u);
+    shift<W, P>(win, x);
     if (a.silu) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) u[j] *= sigmoid_f(u[j]);
+        for (int j = 0; j < P; ++j) u[j] = u[j] * sigmoid2(u[j]);
     }
-    Row<T, V> y;
-    y.narrow(u);
-    y.store((T *)a.y + t * a.ys + c, 16, V);
+    store2<T, V>((T *)a.y + t * a.ys + c, u);
 }
+
+// Rows of N tensors on their way to shared memory, in batches of kAhead tokens.  A thread reads only
+// what it has asked for, so it waits for its own copies and for nobody else.  Single values
+// (V = 1) are loaded when they are wanted.
+template <typename T, int V, int N>
+struct Feed {
+    static constexpr bool kRing = V > 1;
+    using Slot = T[kThreads][V];
+    // batches that are on their way or worked on, within 48 KB
+    static constexpr int kDepth = kAhead * N * (int)sizeof(Slot) <= 12288 ? 4 : 3;
+    static constexpr int kBytes = kRing ? kDepth * kAhead * N * (int)sizeof(Slot) : 16;
+    Slot *ring;  // [kDepth * kAhead * N]
+    const T *p[N];
+    int64_t stride[N];
+
+    __device__ __forceinline__ T *slot(int64_t batch, int i, int n) const {
+        return ring[((int)(batch % kDepth) * kAhead + i) * N + n][threadIdx.x];
+    }
+    // Asks for batch `batch` from token t on, if it exists.
+    __device__ __forceinline__ void ask(int64_t batch, int64_t batches, int64_t t) const {
+        if constexpr (kRing) {
+            if (batch < batches) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot(batch, i, n));
+                        const T *from = p[n] + (t + batch * kAhead + i) * stride[n];
+                        if constexpr (V * sizeof(T) == 16)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+                        else
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from),
+                                         "n"(V * sizeof(T)) : "memory");
+                    }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ void start(int64_t batches, int64_t t) const {
+#pragma unroll
+        for (int k = 0; k < kDepth - 1; ++k) ask(k, batches, t);
+    }
+    // The rows of batch `batch`, and the one that its place is free for behind it.
+    __device__ __forceinline__ void take(int64_t batch, int64_t batches, int64_t t, Row<T, V> (&r)[kAhead][N]) const {
+        if constexpr (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                r[i][n].load(kRing ? slot(batch, i, n) : p[n] + (t + batch * kAhead + i) * stride[n], 16, V);
+        ask(batch + kDepth - 1, batches, t);
+    }
+};
 
 // A thread: V channels of a run of tokens.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads) k_conv(ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, kConvThreads / kThreads) k_conv(ConvArgs a) {
+    constexpr int P = kPairs<V>;
     const int64_t nv = a.C / V, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t total = total_tokens(a.r), run = id / nv, c = id % nv * V;
     int64_t t = run * a.run;
+    const bool together = same_in_warp(run);
+    pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x < 32) check_offsets(a.r);
     if (t >= total) return;
     const int64_t t1 = min(t + a.run, total);
-    float w[W][V], b[V], win[W - 1][V];
+    using F = Feed<T, V, 1>;
+    __shared__ __align__(16) uint8_t ring[F::kBytes];
+    const F feed{reinterpret_cast<typename F::Slot *>(ring), {(const T *)a.x + c}, {a.xs}};
+    F2 w[W][P], b[P], win[W - 1][P];
     load_taps<T, W, V>(a, c, w, b);
-    Seq q{-1, 0, t};
     while (t < t1) {
-        q = seq_at(a.r, t);
+        const Seq q = seq_at(a.r, t, together);
         int64_t row = 0;
         if (q.n >= 0 && a.h0) row = state_row(a.idx, a.n_states, q.n, a.r.status);
         const int64_t end = min(q.e, t1);
@@ -140,13 +198,13 @@ __global__ void __launch_bounds__(kThreads) k_conv(ConvArgs a) {
             continue;
         }
         load_window<T, W, V>(a, t, q.s, row, c, win);
-        for (; t + kAhead <= end; t += kAhead) {
-            Row<T, V> r[kAhead];
+        const int64_t batches = (end - t) / kAhead, t0 = t;
+        feed.start(batches, t0);
+        for (int64_t k = 0; k < batches; ++k) {
+            Row<T, V> r[kAhead][1];
+            feed.take(k, batches, t0, r);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                r[i].load((const T *)a.x + (t + i) * a.xs + c, 16, V);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) one_token<T, W, V>(a, r[i], t + i, c, w, b, win);
+            for (int i = 0; i < kAhead; ++i, ++t) one_token<T, W, V>(a, r[i][0], t, c, w, b, win);
         }
         for (; t < end; ++t) {
             Row<T, V> r;
@@ -168,14 +226,10 @@ __global__ void __launch_bounds__(kThreads) k_conv_state(ConvArgs a) {
     seq_span(a.r, n, s, len);
     const int64_t row = state_row(a.idx, a.n_states, n, a.r.status);
     if (row < 0) return;
-    float win[W - 1][V];
+    F2 win[W - 1][kPairs<V>];
     load_window<T, W, V>(a, s + len, s, row, c, win);
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        Row<T, V> r;
-        r.narrow(win[k]);
-        r.store((T *)a.ht + (row * (W - 1) + k) * a.C + c, 16, V);
-    }
+    for (int k = 0; k < W - 1; ++k) store2<T, V>((T *)a.ht + (row * (W - 1) + k) * a.C + c, win[k]);
 }
 
 // A thread: V channels of a whole sequence, for sequences of few tokens, from and into its row
@@ -203,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_step(ConvArgs a) {
         for (int64_t t = s; t < s + len; ++t) zero.store((T *)a.y + t * a.ys + c, 16, V);
         return;
     }
-    float w[W][V], b[V], win[W - 1][V];
+    F2 w[W][kPairs<V>], b[kPairs<V>], win[W - 1][kPairs<V>];
     load_taps<T, W, V>(a, c, w, b);
     load_window<T, W, V>(a, s, s, row, c, win);
     for (int64_t t = s; t < s + len; ++t) {
@@ -213,26 +267,21 @@ __global__ void __launch_bounds__(kThreads) k_conv_step(ConvArgs a) {
     }
     if (a.ht) {
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) {
-            Row<T, V> r;
-            r.narrow(win[k]);
-            r.store((T *)a.ht + (row * (W - 1) + k) * a.C + c, 16, V);
-        }
+        for (int k = 0; k < W - 1; ++k) store2<T, V>((T *)a.ht + (row * (W - 1) + k) * a.C + c, win[k]);
     }
 }
 
 // du of one token from its inputs and dy.
-template <int W, int V>
-__device__ __forceinline__ void grad_u(bool silu, const float (&w)[W][V], const float (&b)[V],
-                                       const float (&win)[W - 1][V], const float (&x)[V],
-                                       float (&du)[V]) {
+template <int W, int P>
+__device__ __forceinline__ void grad_u(bool silu, const F2 (&w)[W][P], const F2 (&b)[P],
+                                       const F2 (&win)[W - 1][P], const F2 (&x)[P], F2 (&du)[P]) {
     if (!silu) return;
-    float u[V];
-    taps<W, V>(w, b, win, x, u);
+    F2 u[P];
+    taps<W, P>(w, b, win, x, u);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const float g = sigmoid_f(u[j]);
-        du[j] *= g * fmaf(u[j], 1.f - g, 1.f);
+    for (int j = 0; j < P; ++j) {  // g (1 + u (1 - g)), g = sigmoid(u)
+        const F2 g = sigmoid2(u[j]);
+        du[j] = du[j] * (g * fma2(u[j], fma2(g, f2(-1.f), f2(1.f)), f2(1.f)));
     }
 }
 
@@ -240,23 +289,29 @@ __device__ __forceinline__ void grad_u(bool silu, const float (&w)[W][V], const 
 // gradient needs the W - 1 after it), with the sums that these still lack in registers.  dw and
 // db of the run go to part[run][(W + 1) C].
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads) k_conv_bwd(ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, kConvThreads / kThreads) k_conv_bwd(ConvArgs a) {
     const int64_t nv = a.C / V, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t total = total_tokens(a.r), run = id / nv, c = id % nv * V;
     const int64_t t0 = run * a.run;
+    const bool together = same_in_warp(run);
+    pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x < 32) check_offsets(a.r);
     if (t0 >= total) return;
     const int64_t t1 = min(t0 + a.run, total);
-    float w[W][V], b[V], dw[W + 1][V];
+    constexpr int P = kPairs<V>;
+    using F = Feed<T, V, 2>;
+    __shared__ __align__(16) uint8_t ring[F::kBytes];
+    const F feed{reinterpret_cast<typename F::Slot *>(ring), {(const T *)a.x + c, (const T *)a.dy + c}, {a.xs, a.ys}};
+    F2 w[W][P], b[P], dw[W + 1][P];
     load_taps<T, W, V>(a, c, w, b);
 #pragma unroll
     for (int k = 0; k <= W; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) dw[k][j] = 0.f;
+        for (int j = 0; j < P; ++j) dw[k][j] = f2(0.f);
 
     int64_t t = t0;
     while (t < t1) {
-        const Seq q = seq_at(a.r, t);
+        const Seq q = seq_at(a.r, t, together);
         const int64_t row = q.n;
         if (q.n < 0) {
             Row<T, V> zero;
@@ -265,47 +320,40 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(ConvArgs a) {
                 zero.store((T *)a.dx + t * a.C + c, 16, V);
             continue;
         }
-        float win[W - 1][V], pend[W][V];  // pend[k]: dx of token t - k, so far
+        F2 win[W - 1][P], pend[W][P];  // pend[k]: dx of token t - k, so far
         load_window<T, W, V>(a, t, q.s, row, c, win);
 #pragma unroll
         for (int k = 0; k < W; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) pend[k][j] = 0.f;
+            for (int j = 0; j < P; ++j) pend[k][j] = f2(0.f);
         const int64_t mine = min(q.e, t1), stop = min(q.e, t1 + W - 1), first = t;
         auto token = [&](const Row<T, V> &rx, const Row<T, V> &rd, int64_t p) {
-            float x[V], du[V];
-            rx.widen(x);
-            rd.widen(du);
-            grad_u<W, V>(a.silu, w, b, win, x, du);
+            F2 x[P], du[P];
+            widen2<T, V>(rx, x);
+            widen2<T, V>(rd, du);
+            grad_u<W, P>(a.silu, w, b, win, x, du);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
+            for (int j = 0; j < P; ++j) {
                 if (p < mine) {
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k) dw[k][j] = fmaf(du[j], win[k][j], dw[k][j]);
-                    dw[W - 1][j] = fmaf(du[j], x[j], dw[W - 1][j]);
-                    dw[W][j] += du[j];
+                    for (int k = 0; k < W - 1; ++k) dw[k][j] = fma2(du[j], win[k][j], dw[k][j]);
+                    dw[W - 1][j] = fma2(du[j], x[j], dw[W - 1][j]);
+                    dw[W][j] = dw[W][j] + du[j];
                 }
 #pragma unroll
-                for (int k = W - 1; k > 0; --k) pend[k][j] = fmaf(w[W - 1 - k][j], du[j], pend[k - 1][j]);
+                for (int k = W - 1; k > 0; --k) pend[k][j] = fma2(w[W - 1 - k][j], du[j], pend[k - 1][j]);
                 pend[0][j] = w[W - 1][j] * du[j];
             }
-            shift<W, V>(win, x);
-            if (p - (W - 1) >= first) {
-                Row<T, V> r;
-                r.narrow(pend[W - 1]);
-                r.store((T *)a.dx + (p - (W - 1)) * a.C + c, 16, V);
-            }
+            shift<W, P>(win, x);
+            if (p - (W - 1) >= first) store2<T, V>((T *)a.dx + (p - (W - 1)) * a.C + c, pend[W - 1]);
         };
-        constexpr int kU = 4;
-        for (; t + kU <= stop; t += kU) {
-            Row<T, V> rx[kU], rd[kU];
+        const int64_t batches = (stop - t) / kAhead;
+        feed.start(batches, first);
+        for (int64_t k = 0; k < batches; ++k) {
+            Row<T, V> r[kAhead][2];
+            feed.take(k, batches, first, r);
 #pragma unroll
-            for (int i = 0; i < kU; ++i) {
-                rx[i].load((const T *)a.x + (t + i) * a.xs + c, 16, V);
-                rd[i].load((const T *)a.dy + (t + i) * a.ys + c, 16, V);
-            }
-#pragma unroll
-            for (int i = 0; i < kU; ++i) token(rx[i], rd[i], t + i);
+            for (int i = 0; i < kAhead; ++i, ++t) token(r[i][0], r[i][1], t);
         }
         for (; t < stop; ++t) {
             Row<T, V> rx, rd;
@@ -320,25 +368,20 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(ConvArgs a) {
                 if (p < first || p >= mine) continue;
                 if (a.dht) {
                     Row<T, V> r;
-                    float d[V];
+                    F2 d[P];
                     r.load((const T *)a.dht + (row * (W - 1) + W - 2 - k) * a.C + c, 16, V);
-                    r.widen(d);
+                    widen2<T, V>(r, d);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) pend[k][j] += d[j];
+                    for (int j = 0; j < P; ++j) pend[k][j] = pend[k][j] + d[j];
                 }
-                Row<T, V> r;
-                r.narrow(pend[k]);
-                r.store((T *)a.dx + p * a.C + c, 16, V);
+                store2<T, V>((T *)a.dx + p * a.C + c, pend[k]);
             }
         }
         t = mine;
     }
     float *part = a.part + run * (W + 1) * a.C;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-#pragma unroll
-        for (int k = 0; k <= W; ++k) part[k * a.C + c + j] = dw[k][j];
-    }
+    for (int k = 0; k <= W; ++k) store2<float, V>(part + k * a.C + c, dw[k]);
 }
 
 // Gradient of the states that the sequences started from: dh0[k] = sum over the first tokens
@@ -350,56 +393,43 @@ __global__ void __launch_bounds__(kThreads) k_conv_dh0(ConvArgs a) {
     if (n >= a.r.N) return;
     int64_t s, len;
     seq_span(a.r, n, s, len);
-    float w[W][V], b[V], win[W - 1][V], d[W - 1][V];
+    constexpr int P = kPairs<V>;
+    F2 w[W][P], b[P], win[W - 1][P], d[W - 1][P];
     load_taps<T, W, V>(a, c, w, b);
     load_window<T, W, V>(a, s, s, n, c, win);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) d[k][j] = 0.f;
-        if (a.dht && k >= len) {
-            Row<T, V> r;
-            r.load((const T *)a.dht + (n * (W - 1) + k - len) * a.C + c, 16, V);
-            r.widen(d[k]);
-        }
+        Row<T, V> r;
+        r.zero();
+        if (a.dht && k >= len) r.load((const T *)a.dht + (n * (W - 1) + k - len) * a.C + c, 16, V);
+        widen2<T, V>(r, d[k]);
     }
 #pragma unroll
     for (int q = 0; q < W - 1; ++q) {
         if (q >= len) break;
         Row<T, V> rx, rd;
-        float x[V], du[V];
+        F2 x[P], du[P];
         rx.load((const T *)a.x + (s + q) * a.xs + c, 16, V);
         rd.load((const T *)a.dy + (s + q) * a.ys + c, 16, V);
-        rx.widen(x);
-        rd.widen(du);
-        grad_u<W, V>(a.silu, w, b, win, x, du);
-        shift<W, V>(win, x);
+        widen2<T, V>(rx, x);
+        widen2<T, V>(rd, du);
+        grad_u<W, P>(a.silu, w, b, win, x, du);
+        shift<W, P>(win, x);
 #pragma unroll
         for (int k = q; k < W - 1; ++k)
 #pragma unroll
-            for (int j = 0; j < V; ++j) d[k][j] = fmaf(w[k - q][j], du[j], d[k][j]);
+            for (int j = 0; j < P; ++j) d[k][j] = fma2(w[k - q][j], du[j], d[k][j]);
     }
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        Row<T, V> r;
-        r.narrow(d[k]);
-        r.store((T *)a.dh0 + (n * (W - 1) + k) * a.C + c, 16, V);
-    }
+    for (int k = 0; k < W - 1; ++k) store2<T, V>((T *)a.dh0 + (n * (W - 1) + k) * a.C + c, d[k]);
 }
 
-// dw[c, k] and db[c]: the sums of the runs, in their order within each of 8 strands.
-__global__ void __launch_bounds__(256) k_conv_params(ConvArgs a, int64_t runs, int W) {
-    __shared__ float sum[8][33];
-    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + lane, cols = (W + 1) * a.C;
+// dw[c, k] and db[c]: the sums of the runs.
+__global__ void __launch_bounds__(kColumnThreads) k_conv_params(ConvArgs a, int W) {
+    const int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31), cols = (W + 1) * a.C;
     pdl_wait();
-    float s = 0.f;
-    if (i < cols)
-        for (int64_t r = strand; r < runs; r += 8) s += a.part[r * cols + i];
-    sum[strand][lane] = s;
-    __syncthreads();
-    if (strand || i >= cols) return;
-    for (int j = 1; j < 8; ++j) s += sum[j][lane];
+    const float s = column_sum(a.part + i, cols, a.runs, i < cols);
+    if (threadIdx.x >= 32 || i >= cols) return;
     const int64_t k = i / a.C, c = i % a.C;
     if (k < W) a.dw[c * W + k] = s;
     else if (a.db) a.db[c] = s;
@@ -463,8 +493,7 @@ cudaError_t conv_dh0(const ConvArgs &a, int W, int dtype, cudaStream_t st) {
 
 cudaError_t conv_params(const ConvArgs &a, int W, cudaStream_t st) {
     const int64_t cols = (W + 1) * a.C;
-    return launch_pdl(k_conv_params, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st, a, a.runs,
-                      W);
+    return launch_pdl(k_conv_params, dim3((unsigned)((cols + 31) / 32)), dim3(kColumnThreads), 0, st, a, W);
 }
 
 }  // namespace gdr

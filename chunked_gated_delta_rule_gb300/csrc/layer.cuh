@@ -23,6 +23,7 @@ struct ConvArgs {
     bool wide;               // 16 bytes of channels a thread
     int w_bytes;             // alignment of the weights
 };
+constexpr int kConvThreads = 512;  // of k_conv and k_conv_bwd on an SM: so many registers they take
 // step: a thread a sequence, from h0 and into ht; else runs of tokens, and conv_state after it.
 cudaError_t conv_fwd(const ConvArgs &a, int W, int dtype, bool step, cudaStream_t st);
 cudaError_t conv_state(const ConvArgs &a, int W, int dtype, cudaStream_t st);

@@ -43,58 +43,76 @@ __device__ __forceinline__ float row_sum(float x, float *sh) {
     __syncthreads();
     return warp_sum(lane < n ? sh[lane] : 0.f);
 }
+// The largest of magnitudes, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+    for (int k = 1; k < LANES; k <<= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, k));
+    return x;
+}
 template <bool WARP>
-__device__ __forceinline__ uint32_t row_max(uint32_t x, float *sh) {
-    x = __reduce_max_sync(0xffffffffu, x);
+__device__ __forceinline__ float row_max(float x, float *sh) {
+    x = lanes_max<32>(x);
     if constexpr (WARP) return x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
     __syncthreads();
-    if (lane == 0) sh[warp] = __uint_as_float(x);
+    if (lane == 0) sh[warp] = x;
     __syncthreads();
-    return __reduce_max_sync(0xffffffffu, lane < n ? __float_as_uint(sh[lane]) : 0u);
+    return lanes_max<32>(lane < n ? sh[lane] : 0.f);
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void load_weights(const NormArgs &a, int64_t c, float (&w)[V]) {
+__device__ __forceinline__ void load_weights(const NormArgs &a, int64_t c, F2 (&w)[kPairs<V>]) {
     if (!a.w.p || c >= a.D) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) w[j] = 1.f;
+        for (int j = 0; j < kPairs<V>; ++j) w[j] = f2(1.f);
     } else if (a.w.f32) {
         Row<float, V> r;
         r.load((const float *)a.w.p + c, 16, V);
-        r.widen(w);
+        widen2<float, V>(r, w);
     } else {
         Row<T, V> r;
         r.load((const T *)a.w.p + c, 16, V);
-        r.widen(w);
+        widen2<T, V>(r, w);
     }
 }
 
-// round(y / s), from one reciprocal: its product with y, corrected twice, is the rounded quotient
-// (Markstein, 1990) unless y - p s underflows, which the division is for.
-__device__ __forceinline__ float quotient(float y, float s, float inv) {
-    if (s < 0x1p-60f) return s > 0.f ? __fdiv_rn(y, s) : 0.f;
-    float p = y * inv;
-    p = fmaf(-inv, fmaf(p, s, -y), p);
-    return fmaf(-inv, fmaf(p, s, -y), p);
-}
-
-// V values y as 8-bit values, stored at p.
+// V values y as 8-bit values, stored at p: round(y / s) from one reciprocal, whose product with y,
+// corrected twice, is the rounded quotient (Markstein, 1990) unless y - p s underflows, which the
+// division is for.
 template <int V, bool E4M3>
-__device__ __forceinline__ void store8(uint8_t *p, const float (&y)[V], float s) {
-    const float inv = s >= 0x1p-60f ? __frcp_rn(s) : 0.f;
+__device__ __forceinline__ void store8(uint8_t *p, const F2 (&y)[kPairs<V>], float s) {
+    constexpr int P = kPairs<V>;
     uint32_t w[(V + 3) / 4] = {};
-    if (s == s) {
+    if (s > 0.f) {  // not NaN
+        const float inv = __frcp_rn(s);
+        const F2 s2 = f2(s), r = f2(inv), nr = f2(-inv), m1 = f2(-1.f);
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-            const float lo = quotient(y[i], s, inv), hi = i + 1 < V ? quotient(y[i + 1 < V ? i + 1 : i], s, inv) : 0.f;
+        for (int i = 0; i < P; ++i) {
+            float lo, hi;
+            if (s >= 0x1p-60f) {
+                const F2 minus = y[i] * m1;
+                F2 q = y[i] * r;
+                q = fma2(nr, fma2(q, s2, minus), q);
+                q = fma2(nr, fma2(q, s2, minus), q);
+                split(q, lo, hi);
+            } else {
+                split(y[i], lo, hi);
+                lo = __fdiv_rn(lo, s);
+                hi = __fdiv_rn(hi, s);
+            }
             uint32_t two;
             if constexpr (E4M3) {
                 two = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
             } else {
                 two = (__float2int_rn(lo) & 0xff) | (__float2int_rn(hi) & 0xff) << 8;
             }
-            w[i / 4] |= two << 8 * (i % 4);
+            w[i / 2] |= two << 16 * (i % 2);
         }
     }
     if constexpr (V == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
@@ -103,9 +121,8 @@ __device__ __forceinline__ void store8(uint8_t *p, const float (&y)[V], float s)
     else *p = (uint8_t)w[0];
 }
 
-__device__ __forceinline__ float scale_of(uint32_t most, float inv_max) {
-    return most >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
-                               : __fmul_rn(__uint_as_float(most), inv_max);
+__device__ __forceinline__ float scale_of(float most, float inv_max) {
+    return most < __uint_as_float(0x7f800000u) ? __fmul_rn(most, inv_max) : __uint_as_float(0x7fffffffu);
 }
 
 // Where a thread's i-th vector of V values lies in its row (D: none).  A warp's neighbouring
@@ -124,72 +141,77 @@ struct Columns {
 // OUT: 0 the call's type, 1 E4M3, 2 8-bit integers.  V: values of a thread's load; D is a multiple.
 template <typename T, int V, int NV, bool WARP, int OUT>
 __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a) {
+    constexpr int P = kPairs<V>;
     __shared__ float sh[32];
     const Columns<V, WARP> col;
     const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.rows) return;  // whole warps
     const int64_t D = a.D;
     Row<T, V> r[NV];
-    float sum = 0.f;
+    F2 sum2 = f2(0.f);
     {
+        const T *x = (const T *)a.x + row * a.xs, *res = (const T *)a.res + row * a.ress;
         Row<T, V> s[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = col(i);
-            r[i].load((const T *)a.x + row * a.xs + c, 16, c < D ? V : 0);
-            if (a.res) s[i].load((const T *)a.res + row * a.ress + c, 16, c < D ? V : 0);
+            r[i].load(x + c, 16, c < D ? V : 0);
+            if (a.res) s[i].load(res + c, 16, c < D ? V : 0);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[V];
-            r[i].widen(f);
+            F2 f[P];
+            widen2<T, V>(r[i], f);
             if (a.res) {
-                float g[V];
-                s[i].widen(g);
+                F2 g[P];
+                widen2<T, V>(s[i], g);
 #pragma unroll
-                for (int j = 0; j < V; ++j) f[j] += g[j];
-                r[i].narrow(f);
+                for (int j = 0; j < P; ++j) f[j] = f[j] + g[j];
+                narrow2<T, V>(f, r[i]);
                 const int64_t c = col(i);
                 if (c < D) r[i].store((T *)a.r + row * a.rs + c, 16, V);
-                r[i].widen(f);
+                widen2<T, V>(r[i], f);
             }
 #pragma unroll
-            for (int j = 0; j < V; ++j) sum = fmaf(f[j], f[j], sum);
+            for (int j = 0; j < P; ++j) sum2 = fma2(f[j], f[j], sum2);
         }
     }
-    sum = row_sum<WARP>(sum, sh);
-    const float rstd = rsqrtf(sum / (float)D + a.eps);
-    auto normed = [&](int i, float(&y)[V]) {
-        float w[V];
-        r[i].widen(y);
+    const float sum = row_sum<WARP>(both(sum2), sh);
+    const F2 rstd = f2(rsqrtf(sum / (float)D + a.eps));
+    auto normed = [&](int i, F2(&y)[P]) {
+        F2 w[P];
+        widen2<T, V>(r[i], y);
         load_weights<T, V>(a, col(i), w);
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = y[j] * rstd * w[j];
+        for (int j = 0; j < P; ++j) y[j] = y[j] * rstd * w[j];
     };
-    auto largest = [](const float(&y)[V], uint32_t m) {
+    auto largest = [](const F2(&y)[P], float m) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
+        for (int j = 0; j < P; ++j) {
+            float lo, hi;
+            split(y[j], lo, hi);
+            m = max_nan(m, fabsf(lo));
+            if (V > 1) m = max_nan(m, fabsf(hi));
+        }
         return m;
     };
     if constexpr (OUT == 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = col(i);
-            float y[V];
+            F2 y[P];
             normed(i, y);
-            Row<T, V> out;
-            out.narrow(y);
-            if (c < D) out.store((T *)a.y + row * a.ys + c, 16, V);
+            if (c < D) store2<T, V>((T *)a.y + row * a.ys + c, y);
         }
     } else {
-        // a row without a finite rstd has NaN where its values are zeros past D: masked by c < D
+        // values past D are zeros and, in a row without a finite rstd, NaN: they do not count
         const float inv_max = OUT == 1 ? 1.f / 448.f : 1.f / 127.f;
         const int64_t groups = a.group ? (D + 127) / 128 : 1;
-        uint32_t most = 0;
+        float most = 0.f;
         if (!a.group) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float y[V];
+                F2 y[P];
                 normed(i, y);
                 if (col(i) < D) most = largest(y, most);
             }
@@ -198,18 +220,14 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a)
         constexpr int kRun = Columns<V, WARP>::kRun;
 #pragma unroll
         for (int i0 = 0; i0 < NV; i0 += kRun) {
-            float y[kRun][V];
-            uint32_t m = 0;
+            F2 y[kRun][P];
+            float m = 0.f;
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
                 normed(i0 + k, y[k]);
                 if (col(i0 + k) < D) m = largest(y[k], m);
             }
-            if (a.group) {
-#pragma unroll
-                for (int k = 1; k < 32 && k < 128 / V; k <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
-                most = m;
-            }
+            if (a.group) most = lanes_max<(V >= 4 ? 128 / V : 32)>(m);
             const float s = scale_of(most, inv_max);
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
@@ -226,15 +244,16 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a)
 // sums of dy n of its columns; part gets those of the whole block.
 template <typename T, int V, int NV, bool WARP>
 __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArgs a) {
+    constexpr int P = kPairs<V>;
     extern __shared__ float acc[];  // WARP: [kWarpRows][D]
     __shared__ float sh[32];
     const Columns<V, WARP> col;
     const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x, D = a.D;
-    float dw[NV][V];
+    F2 dw[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
+        for (int j = 0; j < P; ++j) dw[i][j] = f2(0.f);
     for (int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
          row < a.rows; row += step) {
         Row<T, V> r[NV], dy[NV], dr[NV];
@@ -247,40 +266,37 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
             if (a.dres) dr[i].load((const T *)a.dres + row * a.dress + c, 16, valid);
             else dr[i].zero();
         }
-        float sum = 0.f, dot = 0.f;
+        F2 sum2 = f2(0.f), dot2 = f2(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[V], g[V], w[V];
-            r[i].widen(f);
-            dy[i].widen(g);
+            F2 f[P], g[P], w[P];
+            widen2<T, V>(r[i], f);
+            widen2<T, V>(dy[i], g);
             load_weights<T, V>(a, col(i), w);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                sum = fmaf(f[j], f[j], sum);
-                dot = fmaf(f[j], g[j] * w[j], dot);
+            for (int j = 0; j < P; ++j) {
+                sum2 = fma2(f[j], f[j], sum2);
+                dot2 = fma2(f[j], g[j] * w[j], dot2);
             }
         }
-        sum = row_sum<WARP>(sum, sh);
-        dot = row_sum<WARP>(dot, sh);
+        const float sum = row_sum<WARP>(both(sum2), sh), dot = row_sum<WARP>(both(dot2), sh);
         const float rstd = rsqrtf(sum / (float)D + a.eps);
-        const float k = dot * rstd / (float)D;  // mean(w dy n)
+        const F2 rs = f2(rstd), k = f2(-dot * rstd / (float)D);  // -mean(w dy n)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = col(i);
-            float f[V], g[V], w[V], e[V];
-            r[i].widen(f);
-            dy[i].widen(g);
-            dr[i].widen(e);
+            F2 f[P], g[P], w[P], e[P];
+            widen2<T, V>(r[i], f);
+            widen2<T, V>(dy[i], g);
+            widen2<T, V>(dr[i], e);
             load_weights<T, V>(a, c, w);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float n = f[j] * rstd;
-                dw[i][j] = fmaf(g[j], n, dw[i][j]);
-                e[j] = fmaf(rstd, fmaf(-n, k, g[j] * w[j]), e[j]);
+            for (int j = 0; j < P; ++j) {
+                const F2 n = f[j] * rs;
+                dw[i][j] = fma2(g[j], n, dw[i][j]);
+                e[j] = fma2(rs, fma2(n, k, g[j] * w[j]), e[j]);
             }
-            Row<T, V> out;
-            out.narrow(e);
-            if (c < D) out.store((T *)a.dx + row * D + c, 16, V);
+            if (c < D) store2<T, V>((T *)a.dx + row * D + c, e);
         }
     }
     if (!a.dw) return;
@@ -288,9 +304,15 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t c = col(i);
+        if (c < D) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (c < D) to[c + j] = dw[i][j];
+            for (int j = 0; j < P; ++j) {
+                float lo, hi;
+                split(dw[i][j], lo, hi);
+                to[c + 2 * j] = lo;
+                if (V > 1) to[c + 2 * j + 1] = hi;
+            }
+        }
     }
     if constexpr (WARP) {  // the block's warps join their sums
         __syncthreads();
@@ -303,19 +325,11 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
     }
 }
 
-__global__ void __launch_bounds__(256) k_norm_weight(NormArgs a, int64_t blocks) {
-    __shared__ float sum[8][33];
-    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+__global__ void __launch_bounds__(kColumnThreads) k_norm_weight(NormArgs a, int64_t blocks) {
+    const int64_t c = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     pdl_wait();
-    float s = 0.f;
-    if (c < a.D)
-        for (int64_t b = strand; b < blocks; b += 8) s += a.part[b * a.D + c];
-    sum[strand][lane] = s;
-    __syncthreads();
-    if (strand || c >= a.D) return;
-    for (int j = 1; j < 8; ++j) s += sum[j][lane];
-    a.dw[c] = s;
+    const float s = column_sum(a.part + c, a.D, blocks, c < a.D);
+    if (threadIdx.x < 32 && c < a.D) a.dw[c] = s;
 }
 
 // Threads of a row (32: a warp) and vectors of a thread.  With rows enough a
@@ -421,7 +435,7 @@ cudaError_t norm_bwd(const NormArgs &a, int dtype, int64_t blocks, cudaStream_t 
 }
 
 cudaError_t norm_weight_grad(const NormArgs &a, int64_t blocks, cudaStream_t st) {
-    return launch_pdl(k_norm_weight, dim3((unsigned)((a.D + 31) / 32)), dim3(256), 0, st, a, blocks);
+    return launch_pdl(k_norm_weight, dim3((unsigned)((a.D + 31) / 32)), dim3(kColumnThreads), 0, st, a, blocks);
 }
 
 }  // namespace gdr

@@ -142,21 +142,51 @@ __device__ __forceinline__ int64_t total_tokens(const TokenRows &r) {
     return rows_packed(r) ? r.T : r.N * r.T;
 }
 
-// The sequence n = [s, e) that holds token t, found by a thread on its own.  A
-// token that none holds lies in a hole: n = -1, and the hole reaches to e.
+// Sum of the n values p[0], p[step], ..: a block takes 32 of them side by side (thread l + 32 k the
+// k-th strand of column l), a row of each strand at once, the strands joined in their order.
+// Threads 0 to 31 get the sums.
+constexpr int kColumnThreads = 512;
+__device__ __forceinline__ float column_sum(const float *p, int64_t step, int64_t n, bool in) {
+    constexpr int kStrands = kColumnThreads / 32;
+    __shared__ float sum[kStrands][33];
+    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
+    float s = 0.f;
+    if (in) {
+#pragma unroll 8
+        for (int64_t i = strand; i < n; i += kStrands) s += p[i * step];
+    }
+    sum[strand][lane] = s;
+    __syncthreads();
+    if (strand == 0)
+#pragma unroll
+        for (int k = 1; k < kStrands; ++k) s += sum[k][lane];
+    return s;
+}
+
+__device__ __forceinline__ bool same_in_warp(int64_t x) {
+    return __all_sync(0xffffffffu, x == __shfl_sync(0xffffffffu, x, 0));
+}
+
+// The sequence n = [s, e) that holds token t, found by a warp whose lanes all look for the same
+// one (`together`: every lane takes part), or by a thread on its own.  A token that none holds lies
+// in a hole: n = -1, and the hole reaches to e.
 struct Seq {
     int64_t n, s, e;
 };
-__device__ __forceinline__ Seq seq_at(const TokenRows &r, int64_t t) {
+__device__ __forceinline__ Seq seq_at(const TokenRows &r, int64_t t, bool together) {
     if (!rows_packed(r)) {
         const int64_t n = t / r.T;
         return Seq{n, n * r.T, (n + 1) * r.T};
     }
     int64_t lo = 0, hi = r.N;
-    while (hi - lo > 1) {  // the last n with cu[n] <= t
-        const int64_t mid = (lo + hi) >> 1;
-        if (row_bound(r, mid) <= t) lo = mid;
-        else hi = mid;
+    if (together) {
+        lo = find_seq(r, t);
+    } else {
+        while (hi - lo > 1) {  // the last n with cu[n] <= t
+            const int64_t mid = (lo + hi) >> 1;
+            if (row_bound(r, mid) <= t) lo = mid;
+            else hi = mid;
+        }
     }
     const int64_t s = row_bound(r, lo), e = row_bound(r, lo + 1);
     if (s >= 0 && s <= t && t < e && e <= r.T) return Seq{lo, s, e};
@@ -172,6 +202,97 @@ __device__ __forceinline__ int64_t state_row(const int32_t *idx, int64_t n_state
     return -1;
 }
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two FP32 values in a register pair: one instruction for both, at the same
+// rate of operations but half the issue slots, which these kernels are short of.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 ex2(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return f2(ex2(lo), ex2(hi));
+}
+__device__ __forceinline__ float both(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return lo + hi;
+}
+
+// V values as pairs (one value: a pair with nothing beside it).
+template <int V>
+constexpr int kPairs = (V + 1) / 2;
+
+template <typename T, int V>
+__device__ __forceinline__ void widen2(const Row<T, V> &r, F2 (&x)[kPairs<V>]) {
+    float f[V];
+    r.widen(f);
+    if constexpr (V == 1) {
+        x[0] = f2(f[0], 0.f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) x[j] = f2(f[2 * j], f[2 * j + 1]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void narrow2(const F2 (&x)[kPairs<V>], Row<T, V> &r) {
+    float f[2 * kPairs<V>], g[V];
+#pragma unroll
+    for (int j = 0; j < kPairs<V>; ++j) split(x[j], f[2 * j], f[2 * j + 1]);
+#pragma unroll
+    for (int j = 0; j < V; ++j) g[j] = f[j];
+    r.narrow(g);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store2(T *p, const F2 (&x)[kPairs<V>]) {
+    Row<T, V> r;
+    narrow2<T, V>(x, r);
+    r.store(p, 16, V);
+}
+
+// 1 / (1 + e^-x)
+__device__ __forceinline__ F2 sigmoid2(F2 x) {
+    float a, b;
+    split(ex2(x * f2(-kLog2e)) + f2(1.f), a, b);
+    return f2(rcp(a), rcp(b));
+}
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 }  // namespace gdr

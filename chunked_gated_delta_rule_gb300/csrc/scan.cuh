@@ -18,59 +18,6 @@
 namespace gdr {
 
 constexpr int kNT = 128;  // threads of a block
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two FP32 values in a register pair: one instruction for both, at the same
-// rate of operations but half the issue slots, which the scan is short of.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
-__device__ __forceinline__ void split(F2 a, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 ex2(F2 a) {
-    float lo, hi;
-    split(a, lo, hi);
-    return f2(ex2(lo), ex2(hi));
-}
-__device__ __forceinline__ float both(F2 a) {
-    float lo, hi;
-    split(a, lo, hi);
-    return lo + hi;
-}
 
 // log(1 + e^x) = max(x, 0) + log(1 + u), u = e^-|x|, for two values.  u is 2^-t with what rounding
 // t = |x| log2(e) lost put back.  log(1 + u) = 2 artanh(s) with 2 s = u / (1 + u / 2); artanh(s) / s

@@ -538,21 +538,14 @@ __global__ void __launch_bounds__(256) k_scan_bwd_bc(ScanArgs a, int tiles) {
     to[(t * a.G + g) * a.S + s] = from_f32<T>(f);
 }
 
-// 4b. dA, dD and dbias: the sums of the slots, in eight strands.
-__global__ void __launch_bounds__(256) k_scan_bwd_params(ScanArgs a) {
-    __shared__ float sum[8][33];
-    const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
-    const int64_t states = a.C * a.S, cols = states + 2 * a.C, i = (int64_t)blockIdx.x * 32 + lane;
+// 4b. dA, dD and dbias: the sums of the slots.
+__global__ void __launch_bounds__(kColumnThreads) k_scan_bwd_params(ScanArgs a) {
+    const int64_t states = a.C * a.S, cols = states + 2 * a.C;
+    const int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     pdl_wait();
-    const float *p = i < states ? a.E + i : a.pd + (i - states);
-    const int64_t step = i < states ? states : 2 * a.C;
-    float f = 0.f;
-    if (i < cols)
-        for (int64_t k = strand; k < a.slots; k += 8) f += p[k * step];
-    sum[strand][lane] = f;
-    __syncthreads();
-    if (strand || i >= cols) return;
-    for (int j = 1; j < 8; ++j) f += sum[j][lane];
+    const float f = column_sum(i < states ? a.E + i : a.pd + (i - states), i < states ? states : 2 * a.C,
+                               a.slots, i < cols);
+    if (threadIdx.x >= 32 || i >= cols) return;
     if (i < states) a.dA[i] = f;
     else if (i < states + a.C) { if (a.dD) a.dD[i - states] = f; }
     else if (a.dbias) a.dbias[i - states - a.C] = f;
@@ -607,7 +600,7 @@ cudaError_t scan_bwd_bc(const ScanArgs &a, int dtype, cudaStream_t st) {
 
 cudaError_t scan_bwd_params(const ScanArgs &a, cudaStream_t st) {
     const int64_t cols = a.C * a.S + 2 * a.C;
-    return launch_pdl(k_scan_bwd_params, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st, a);
+    return launch_pdl(k_scan_bwd_params, dim3((unsigned)((cols + 31) / 32)), dim3(kColumnThreads), 0, st, a);
 }
 
 }  // namespace gdr

@@ -6,20 +6,19 @@ import ctypes
 
 import torch
 
-from .api import (GDR_E4M3, GDR_I8, GDR_SEQLENS_I64, _addr, _check_status, _dtype_code, _on,
-                  _paged_call, gdr_conv_dims, gdr_norm_dims, gdr_options, gdr_scan_dims,
-                  gdr_scan_grads, gdr_scan_tensors, load_library)
+from .api import (GDR_BF16, GDR_E4M3, GDR_F16, GDR_F32, GDR_I8, GDR_SEQLENS_I64, GdrError,
+                  _check_status, _dtype_code, _on, gdr_conv_dims, gdr_norm_dims, gdr_options,
+                  gdr_scan_dims, gdr_scan_grads, gdr_scan_tensors, load_library)
+
+# A decode step's time is the time of its calls, most of it here: so what is usually right is
+# tested in line, and a function that names what is wrong is called only where something is.
+
+_CODES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16, torch.float16: GDR_F16}
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _index_of(name, x):
-    index = x.get_device()
-    if index < 0:
-        raise ValueError(f"{name} takes CUDA tensors")
-    return index
-
-
-def _like(index, dtype, shape, **tensors):
-    """Every given tensor lies on CUDA device ``index`` and has this dtype and shape."""
+def _refuse(index, dtype, shape, **tensors):
+    """Raises for the first tensor that is not on CUDA device ``index``, of this dtype and shape."""
     for name, t in tensors.items():
         if t is None:
             continue
@@ -31,47 +30,72 @@ def _like(index, dtype, shape, **tensors):
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _token_stride(name, t):
+def _like(index, dtype, shape, name, t, contiguous=False):
+    """The tensor's address, None without one: it lies on CUDA device ``index`` and has this dtype
+    and shape."""
+    if t is None:
+        return None
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape:
+        _refuse(index, dtype, shape, **{name: t})
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _new(like):
+    """A contiguous tensor of the same shape, type and device."""
+    if like.is_contiguous():
+        return torch.empty_like(like)  # the quickest of torch's ways
+    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
+def _stride(name, t):
     """Elements from one token of [B, T, C] to the next, 0 when contiguous."""
     if t.is_contiguous() or t.numel() == 0:
         return 0
     B, T, C = t.shape
-    step = t.stride(1) if T > 1 else t.stride(0) if B > 1 else C
-    if (C > 1 and t.stride(2) != 1) or (B > 1 and T > 1 and t.stride(0) != T * step) or step < 1:
+    b, step, c = t.stride()
+    if T == 1:
+        step = b if B > 1 else C
+    if (C > 1 and c != 1) or (B > 1 and T > 1 and b != T * step) or step < 1:
         raise ValueError(f"{name} needs contiguous channels and batch rows T token strides apart")
     return step
 
 
 def _group_strides(name, t):
-    """Token and group strides of [B, T, G, S], (0, 0) when contiguous."""
+    """Token and group strides of [B, T, G, S], None when contiguous."""
     if t.is_contiguous() or t.numel() == 0:
-        return (0, 0)
+        return None
     B, T, G, S = t.shape
-    step = t.stride(1) if T > 1 else t.stride(0) if B > 1 else G * S
-    group = t.stride(2) if G > 1 else S
-    if (S > 1 and t.stride(3) != 1) or (B > 1 and T > 1 and t.stride(0) != T * step) or \
-            min(step, group) < 1:
+    b, step, group, c = t.stride()
+    if T == 1:
+        step = b if B > 1 else G * S
+    if G == 1:
+        group = S
+    if (S > 1 and c != 1) or (B > 1 and T > 1 and b != T * step) or min(step, group) < 1:
         raise ValueError(f"{name} needs contiguous states and batch rows T token strides apart")
     return (step, group)
 
 
 def _seqs(B, cu_seqlens, index):
-    """(N, flags, sequences) of a call."""
+    """(N, flags, sequences, address of the offsets) of a call."""
     if cu_seqlens is None:
-        return 0, 0, B
-    if cu_seqlens.dtype not in (torch.int32, torch.int64):
+        return 0, 0, B, None
+    wide = cu_seqlens.dtype is torch.int64
+    if not wide and cu_seqlens.dtype is not torch.int32:
         raise TypeError(f"cu_seqlens must be int32 or int64, got {cu_seqlens.dtype}")
-    _on(index, cu_seqlens=(cu_seqlens, None))
     n = cu_seqlens.numel() - 1
-    return n, GDR_SEQLENS_I64 if cu_seqlens.dtype == torch.int64 else 0, n
+    return (n, GDR_SEQLENS_I64 if wide else 0, n,
+            _like(index, cu_seqlens.dtype, (n + 1,), "cu_seqlens", cu_seqlens, True))
 
 
 def _options(index, workspace, status, timer):
-    _check_status(status, index)
     if workspace is None and status is None and timer is None:
         return None
+    _check_status(status, index)
     _on(index, workspace=(workspace, None))
-    opt = gdr_options(workspace=_addr(workspace), status=_addr(status),
+    opt = gdr_options(workspace=None if workspace is None else workspace.data_ptr(),
+                      status=None if status is None else status.data_ptr(),
                       workspace_bytes=0 if workspace is None
                       else workspace.numel() * workspace.element_size())
     if timer is not None:
@@ -83,60 +107,72 @@ def _options(index, workspace, status, timer):
 
 
 def _call(fn, index, stream, tensors, *args):
-    """The library's call; the memory of ``tensors`` is not handed out again before ``stream``
-    is through with them, whatever stream they were made on."""
-    _paged_call(fn, index, stream, *args)
+    """The library's call on ``stream`` (default: the current one).  The memory of ``tensors`` is
+    not handed out again before ``stream`` is through with them, whatever stream they were made
+    on."""
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:  # torch holds a tensor there: it is initialised
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != 0:
+        raise GdrError(rc)
     if stream is not None:
         for t in tensors:
             if t is not None and t.numel():
                 t.record_stream(stream)
 
 
-def _states(index, nseq, tail, dtype, h0, ht, state, state_indices, want, device):
-    """(h0, ht, rows) of a call that goes on from ``h0`` [N, ...] or moves the pool ``state`` on in
-    place."""
+def _states(index, nseq, tail, dtype, h0, ht, state, state_indices, want, x):
+    """(ht, rows, addresses of h0, ht and the indices) of a call that goes on from ``h0`` [N, ...],
+    or moves the pool ``state`` on in place."""
     if state is not None:
         if h0 is not None or ht is not None:
             raise ValueError("state is read and written in place: h0 and ht do not go with it")
-        _like(index, dtype, (state.shape[0],) + tail, state=state)
-        _on(index, state=(state, None), state_indices=(state_indices, torch.int32))
-        if state_indices is not None and state_indices.shape != (nseq,):
-            raise ValueError(f"state_indices must be [{nseq}], got {list(state_indices.shape)}")
-        if state_indices is None and state.shape[0] < nseq:
+        rows = state.shape[0]
+        p = _like(index, dtype, (rows,) + tail, "state", state, True)
+        if state_indices is None and rows < nseq:
             raise ValueError(f"state must have a row for each of {nseq} sequences")
-        return state, state, state.shape[0]
+        return state, rows, p, p, _like(index, torch.int32, (nseq,), "state_indices",
+                                        state_indices, True)
     if state_indices is not None:
         raise ValueError("state_indices belong to state")
+    shape = (nseq,) + tail
     if ht is None and want:
-        ht = torch.empty((nseq,) + tail, dtype=dtype, device=device)
-    _like(index, dtype, (nseq,) + tail, h0=h0, ht=ht)
-    _on(index, h0=(h0, None), ht=(ht, None))
-    return h0, ht, nseq
+        ht = torch.empty(shape, dtype=dtype, device=x.device)
+    return (ht, nseq, _like(index, dtype, shape, "h0", h0, True),
+            _like(index, dtype, shape, "ht", ht, True), None)
 
 
-def _weight_code(name, t, dtype):
-    if t.dtype != dtype and t.dtype != torch.float32:
-        raise TypeError(f"{name} must be {dtype} or float32, got {t.dtype}")
-    return _dtype_code(t.dtype)
+def _weight(index, dtype, shape, t, name="weight"):
+    """(type, address) of a parameter of x's dtype or float32."""
+    wt = t.dtype
+    if wt is not dtype and wt is not torch.float32:
+        raise TypeError(f"{name} must be {dtype} or float32, got {wt}")
+    return _CODES[wt], _like(index, wt, shape, name, t, True)
 
 
 _ACTIVATIONS = {None: 0, "silu": 1}
 
 
-def _conv_dims(x, weight, bias, cu_seqlens, activation, max_seqlen, index):
-    if x.dim() != 3 or weight.dim() != 2 or weight.shape[0] != x.shape[2]:
+def _conv_call(name, x, weight, bias, cu_seqlens, activation, max_seqlen):
+    """What both directions of the convolution share: (index, gdr_conv_dims, sequences, addresses
+    of weight, bias and offsets)."""
+    index, dtype = x.get_device(), x.dtype
+    if index < 0:
+        raise ValueError(f"{name} takes CUDA tensors")
+    if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("x must be [B, T, C], weight [C, W]")
+    B, T, C = x.shape
+    W = weight.shape[1]
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
-    B, T, C = x.shape
-    wd = _weight_code("weight", weight, x.dtype)
-    _on(index, weight=(weight, None))
-    _like(index, weight.dtype, (C,), bias=bias)
-    _on(index, bias=(bias, None))
-    n, flags, nseq = _seqs(B, cu_seqlens, index)
-    return gdr_conv_dims(B, T, C, weight.shape[1], n, _dtype_code(x.dtype), flags, wd,
-                         _ACTIVATIONS[activation], 0 if max_seqlen is None else int(max_seqlen),
-                         _token_stride("x", x)), nseq
+    wd, w = _weight(index, dtype, (C, W), weight)
+    n, flags, nseq, cu = _seqs(B, cu_seqlens, index)
+    return index, gdr_conv_dims(B, T, C, W, n, _dtype_code(dtype), flags, wd, _ACTIVATIONS[activation],
+                                0 if max_seqlen is None else max_seqlen, _stride("x", x)), nseq, w, \
+        _like(index, weight.dtype, (C,), "bias", bias, True), cu
 
 
 def gdr_short_conv_fwd(x, weight, bias=None, cu_seqlens=None, h0=None, *, activation="silu",
@@ -151,20 +187,19 @@ def gdr_short_conv_fwd(x, weight, bias=None, cu_seqlens=None, h0=None, *, activa
     wanted.  ``max_seqlen`` is a planning hint, as everywhere.  Work is enqueued on ``stream``
     (default: the current one) and not synchronised."""
     lib = load_library()
-    index = _index_of("gdr_short_conv_fwd", x)
-    dims, nseq = _conv_dims(x, weight, bias, cu_seqlens, activation, max_seqlen, index)
+    index, dims, nseq, w, b, cu = _conv_call("gdr_short_conv_fwd", x, weight, bias, cu_seqlens,
+                                             activation, max_seqlen)
     opt = _options(index, None, status, timer)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _new(x)
     else:
-        _like(index, x.dtype, x.shape, y=y)
-        dims.y_stride = _token_stride("y", y)
-    h0, ht, rows = _states(index, nseq, (dims.W - 1, dims.C), x.dtype, h0, ht, state,
-                           state_indices, output_final_state, x.device)
+        _like(index, x.dtype, x.shape, "y", y)
+        dims.y_stride = _stride("y", y)
+    ht, rows, p0, pt, idx = _states(index, nseq, (weight.shape[1] - 1, x.shape[2]), x.dtype, h0, ht,
+                                    state, state_indices, output_final_state, x)
     _call(lib.gdr_short_conv_fwd, index, stream,
-          (x, weight, bias, cu_seqlens, h0, ht, state_indices, y), dims, x.data_ptr(),
-          weight.data_ptr(), _addr(bias), _addr(cu_seqlens), _addr(h0), _addr(ht), rows,
-          _addr(state_indices), y.data_ptr(), opt)
+          (x, weight, bias, cu_seqlens, h0, ht, state_indices, y), dims, x.data_ptr(), w, b, cu, p0,
+          pt, rows, idx, y.data_ptr(), opt)
     return y, ht
 
 
@@ -175,43 +210,53 @@ def gdr_short_conv_bwd(x, weight, dy, bias=None, cu_seqlens=None, h0=None, dht=N
     ``(dx, dweight, dbias, dh0)``, dx and dh0 in x's dtype, dweight and dbias float32; dbias is None
     without a bias, dh0 unless ``want_dh0``."""
     lib = load_library()
-    index = _index_of("gdr_short_conv_bwd", x)
-    dims, nseq = _conv_dims(x, weight, bias, cu_seqlens, activation, max_seqlen, index)
+    index, dims, nseq, w, b, cu = _conv_call("gdr_short_conv_bwd", x, weight, bias, cu_seqlens,
+                                             activation, max_seqlen)
     opt = _options(index, workspace, status, timer)
-    _like(index, x.dtype, x.shape, dy=dy)
-    dims.y_stride = _token_stride("dy", dy)
-    tail = (nseq, dims.W - 1, dims.C)
-    _like(index, x.dtype, tail, h0=h0, dht=dht)
-    _on(index, h0=(h0, None), dht=(dht, None))
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    g = _like(index, x.dtype, x.shape, "dy", dy)
+    dims.y_stride = _stride("dy", dy)
+    tail = (nseq, weight.shape[1] - 1, x.shape[2])
+    p0 = _like(index, x.dtype, tail, "h0", h0, True)
+    gt = _like(index, x.dtype, tail, "dht", dht, True)
+    dx = _new(x)
     dw = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
-    db = None if bias is None else torch.empty(x.shape[2], device=x.device)
+    db = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=x.device)
     dh0 = torch.empty(tail, dtype=x.dtype, device=x.device) if want_dh0 else None
     _call(lib.gdr_short_conv_bwd, index, stream,
           (x, weight, dy, bias, cu_seqlens, h0, dht, dx, dw, db, dh0, workspace), dims,
-          x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(cu_seqlens), _addr(h0),
-          dy.data_ptr(), _addr(dht), dx.data_ptr(), dw.data_ptr(), _addr(db), _addr(dh0), opt)
+          x.data_ptr(), w, b, cu, p0, g, gt, dx.data_ptr(), dw.data_ptr(),
+          None if db is None else db.data_ptr(), None if dh0 is None else dh0.data_ptr(), opt)
     return dx, dw, db, dh0
 
 
-def _scan_dims(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, softplus, max_seqlen, index):
-    if x.dim() != 3 or A.dim() != 2 or A.shape[0] != x.shape[2] or B.dim() != 4 or \
-            B.shape[:2] != x.shape[:2] or B.shape[3] != A.shape[1]:
+def _scan_call(name, x, dt, A, B, C, D, z, dt_bias, cu_seqlens, softplus, max_seqlen):
+    """What both directions of the scan share: (index, gdr_scan_dims, sequences, gdr_scan_tensors,
+    address of the offsets)."""
+    index, dtype = x.get_device(), x.dtype
+    if index < 0:
+        raise ValueError(f"{name} takes CUDA tensors")
+    if x.dim() != 3 or A.dim() != 2 or B.dim() != 4:
         raise ValueError("x must be [B, T, C], A [C, S], B and C [B, T, groups, S]")
-    nb, T, ch = x.shape
-    _like(index, x.dtype, x.shape, dt=dt, z=z)
-    _like(index, x.dtype, B.shape, B=B, C=C)
-    _like(index, torch.float32, (ch,), D=D, dt_bias=dt_bias)
-    _on(index, A=(A, torch.float32), D=(D, None), dt_bias=(dt_bias, None))
-    n, flags, nseq = _seqs(nb, cu_seqlens, index)
-    dims = gdr_scan_dims(nb, T, ch, A.shape[1], B.shape[2], n, _dtype_code(x.dtype), flags,
-                         1 if softplus else 0, 0 if max_seqlen is None else int(max_seqlen),
-                         _token_stride("x", x), _token_stride("dt", dt),
-                         0 if z is None else _token_stride("z", z))
-    dims.b_stride[:] = _group_strides("B", B)
-    dims.c_stride[:] = _group_strides("C", C)
-    return dims, nseq, gdr_scan_tensors(x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
-                                        C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias))
+    shape = x.shape
+    nb, T, ch = shape
+    S, G = A.shape[1], B.shape[2]
+    vec, bc = (ch,), (nb, T, G, S)
+    n, flags, nseq, cu = _seqs(nb, cu_seqlens, index)
+    tensors = gdr_scan_tensors(
+        x.data_ptr(), _like(index, dtype, shape, "dt", dt),
+        _like(index, torch.float32, (ch, S), "A", A, True), _like(index, dtype, bc, "B", B),
+        _like(index, dtype, bc, "C", C), _like(index, torch.float32, vec, "D", D, True),
+        _like(index, dtype, shape, "z", z), _like(index, torch.float32, vec, "dt_bias", dt_bias, True))
+    dims = gdr_scan_dims(nb, T, ch, S, G, n, _dtype_code(dtype), flags, 1 if softplus else 0,
+                         0 if max_seqlen is None else max_seqlen, _stride("x", x), _stride("dt", dt),
+                         0 if z is None else _stride("z", z))
+    strides = _group_strides("B", B)
+    if strides:
+        dims.b_stride[:] = strides
+    strides = _group_strides("C", C)
+    if strides:
+        dims.c_stride[:] = strides
+    return index, dims, nseq, tensors, cu
 
 
 def gdr_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seqlens=None, h0=None,
@@ -228,21 +273,19 @@ def gdr_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seql
     sequences whole, more cuts them.  Returns ``(y, ht)``; ht is ``state``, or None unless
     ``output_final_state``."""
     lib = load_library()
-    index = _index_of("gdr_selective_scan_fwd", x)
-    dims, nseq, tensors = _scan_dims(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, softplus,
-                                     max_seqlen, index)
+    index, dims, nseq, tensors, cu = _scan_call("gdr_selective_scan_fwd", x, dt, A, B, C, D, z,
+                                                dt_bias, cu_seqlens, softplus, max_seqlen)
     opt = _options(index, workspace, status, timer)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _new(x)
     else:
-        _like(index, x.dtype, x.shape, y=y)
-        dims.y_stride = _token_stride("y", y)
-    h0, ht, rows = _states(index, nseq, (dims.C, dims.S), torch.float32, h0, ht, state,
-                           state_indices, output_final_state, x.device)
+        _like(index, x.dtype, x.shape, "y", y)
+        dims.y_stride = _stride("y", y)
+    ht, rows, p0, pt, idx = _states(index, nseq, (x.shape[2], A.shape[1]), torch.float32, h0, ht,
+                                    state, state_indices, output_final_state, x)
     _call(lib.gdr_selective_scan_fwd, index, stream,
           (x, dt, A, B, C, D, z, dt_bias, cu_seqlens, h0, ht, state_indices, y, workspace), dims,
-          tensors, _addr(cu_seqlens), _addr(h0), _addr(ht), rows, _addr(state_indices),
-          y.data_ptr(), int(n_segments), opt)
+          tensors, cu, p0, pt, rows, idx, y.data_ptr(), n_segments, opt)
     return y, ht
 
 
@@ -253,24 +296,24 @@ def gdr_selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, cu_
     inputs: ``(dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0)``, each in its input's dtype; None for
     an input that is None, dh0 unless ``want_dh0``."""
     lib = load_library()
-    index = _index_of("gdr_selective_scan_bwd", x)
-    dims, nseq, tensors = _scan_dims(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, softplus,
-                                     max_seqlen, index)
+    index, dims, nseq, tensors, cu = _scan_call("gdr_selective_scan_bwd", x, dt, A, B, C, D, z,
+                                                dt_bias, cu_seqlens, softplus, max_seqlen)
     opt = _options(index, workspace, status, timer)
-    _like(index, x.dtype, x.shape, dy=dy)
-    dims.y_stride = _token_stride("dy", dy)
-    _like(index, torch.float32, (nseq, dims.C, dims.S), h0=h0, dht=dht)
-    _on(index, h0=(h0, None), dht=(dht, None))
+    g = _like(index, x.dtype, x.shape, "dy", dy)
+    dims.y_stride = _stride("dy", dy)
+    shape = (nseq, x.shape[2], A.shape[1])
+    p0 = _like(index, torch.float32, shape, "h0", h0, True)
+    gt = _like(index, torch.float32, shape, "dht", dht, True)
 
     def new(like):
-        return None if like is None else torch.empty(like.shape, dtype=like.dtype, device=x.device)
+        return None if like is None else _new(like)
 
-    dh0 = torch.empty((nseq, dims.C, dims.S), device=x.device) if want_dh0 else None
+    dh0 = torch.empty(shape, device=x.device) if want_dh0 else None
     out = (new(x), new(dt), new(A), new(B), new(C), new(D), new(z), new(dt_bias), dh0)
-    grads = gdr_scan_grads(*(_addr(t) for t in out))
+    grads = gdr_scan_grads(*[None if t is None else t.data_ptr() for t in out])
     _call(lib.gdr_selective_scan_bwd, index, stream,
           (x, dt, A, B, C, dy, D, z, dt_bias, cu_seqlens, h0, dht, workspace) + out, dims, tensors,
-          _addr(cu_seqlens), _addr(h0), dy.data_ptr(), _addr(dht), grads, opt)
+          cu, p0, g, gt, grads, opt)
     return out
 
 
@@ -305,46 +348,49 @@ def gdr_rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-6, dtype=None, gro
     :func:`gdr_cache_write` does.  Returns ``(y, r, scale)``; r is None without a residual, scale
     unless y is quantised.  ``residual_out`` may be the residual or x itself, ``y`` x (in place)."""
     lib = load_library()
-    index = _index_of("gdr_rms_norm_fwd", x)
-    D = x.shape[-1]
-    code = _dtype_code(x.dtype)
-    if dtype is None or dtype == x.dtype:
-        out, out_code = x.dtype, code
+    index, own, shape = x.get_device(), x.dtype, x.shape
+    if index < 0:
+        raise ValueError("gdr_rms_norm_fwd takes CUDA tensors")
+    code, D = _dtype_code(own), shape[-1]
+    if dtype is None or dtype is own:
+        out, out_code = own, code
     elif dtype in _OUT_DTYPES:
         out, out_code = dtype, _OUT_DTYPES[dtype]
     else:
-        raise TypeError(f"dtype must be {x.dtype}, float8_e4m3fn or int8, got {dtype}")
-    if group and (out_code < GDR_E4M3 or group != 128):
+        raise TypeError(f"dtype must be {own}, float8_e4m3fn or int8, got {dtype}")
+    if group and (out is own or group != 128):
         raise ValueError("group is 0, or 128 where y is quantised")
-    wd = code if weight is None else _weight_code("weight", weight, x.dtype)
-    if weight is not None:
-        _like(index, weight.dtype, (D,), weight=weight)
-        _on(index, weight=(weight, None))
-    _like(index, x.dtype, x.shape, residual=residual, residual_out=residual_out)
+    wd, w = (code, None) if weight is None else _weight(index, own, (D,), weight)
     if y is None:
-        y = torch.empty(x.shape, dtype=out, device=x.device)
+        y = _new(x) if out is own else torch.empty(shape, dtype=out, device=x.device)
+        ys = 0
     else:
-        _like(index, out, x.shape, y=y)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif residual is None and residual_out is not None:
-        raise ValueError("residual_out belongs to a residual")
-    if out_code >= GDR_E4M3:
-        want = x.shape[:-1] + ((D + 127) // 128,) if group else x.shape[:-1]
+        _like(index, out, shape, "y", y)
+        ys = _row_stride("y", y)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out belongs to a residual")
+        pr = po = None
+        rs = os = 0
+    else:
+        pr = _like(index, own, shape, "residual", residual)
+        rs = _row_stride("residual", residual)
+        if residual_out is None:
+            residual_out = _new(x)
+        po = _like(index, own, shape, "residual_out", residual_out)
+        os = _row_stride("residual_out", residual_out)
+    ps = None
+    if out is not own:
+        want = shape[:-1] + ((D + 127) // 128,) if group else shape[:-1]
         if scale is None:
             scale = torch.empty(want, device=x.device)
-        _like(index, torch.float32, want, scale=scale)
-        _on(index, scale=(scale, None))
+        ps = _like(index, torch.float32, want, "scale", scale, True)
     elif scale is not None:
         raise ValueError("scale belongs to a quantised y")
-    dims = gdr_norm_dims(x.numel() // D if D else 0, D, code, wd, out_code, int(group), float(eps),
-                         _row_stride("x", x), 0, 0, _row_stride("y", y))
-    if residual is not None:
-        dims.residual_stride = _row_stride("residual", residual)
-        dims.sum_stride = _row_stride("residual_out", residual_out)
+    dims = gdr_norm_dims(x.numel() // D if D else 0, D, code, wd, out_code, group, eps,
+                         _row_stride("x", x), rs, os, ys)
     _call(lib.gdr_rms_norm_fwd, index, stream, (x, residual, weight, residual_out, y, scale), dims,
-          x.data_ptr(), _addr(residual), _addr(weight), _addr(residual_out), y.data_ptr(),
-          _addr(scale), _options(index, None, None, timer))
+          x.data_ptr(), pr, w, po, y.data_ptr(), ps, _options(index, None, None, timer))
     return y, residual_out, scale
 
 
@@ -354,21 +400,19 @@ def gdr_rms_norm_bwd(dy, r, weight=None, dr=None, *, eps=1e-6, workspace=None, s
     (its r, or its x without a residual): ``(dx, dweight)``; dx is the gradient of x and of the
     residual alike, dweight float32 (None without a weight)."""
     lib = load_library()
-    index = _index_of("gdr_rms_norm_bwd", r)
-    D, code = r.shape[-1], _dtype_code(r.dtype)
-    _like(index, r.dtype, r.shape, dy=dy, dr=dr)
-    wd = code if weight is None else _weight_code("weight", weight, r.dtype)
-    if weight is not None:
-        _like(index, weight.dtype, (D,), weight=weight)
-        _on(index, weight=(weight, None))
+    index, dtype, shape = r.get_device(), r.dtype, r.shape
+    if index < 0:
+        raise ValueError("gdr_rms_norm_bwd takes CUDA tensors")
+    code, D = _dtype_code(dtype), shape[-1]
+    wd, w = (code, None) if weight is None else _weight(index, dtype, (D,), weight)
+    g, gr = _like(index, dtype, shape, "dy", dy), _like(index, dtype, shape, "dr", dr)
     opt = _options(index, workspace, None, timer)
-    dx = torch.empty(r.shape, dtype=r.dtype, device=r.device)
+    dx = _new(r)
     dw = None if weight is None else torch.empty(D, device=r.device)
-    dims = gdr_norm_dims(r.numel() // D if D else 0, D, code, wd, code, 0, float(eps),
-                         _row_stride("r", r), 0 if dr is None else _row_stride("dr", dr), 0,
-                         _row_stride("dy", dy))
+    dims = gdr_norm_dims(r.numel() // D if D else 0, D, code, wd, code, 0, eps, _row_stride("r", r),
+                         0 if dr is None else _row_stride("dr", dr), 0, _row_stride("dy", dy))
     _call(lib.gdr_rms_norm_bwd, index, stream, (dy, r, weight, dr, dx, dw, workspace), dims,
-          r.data_ptr(), _addr(weight), dy.data_ptr(), _addr(dr), dx.data_ptr(), _addr(dw), opt)
+          r.data_ptr(), w, g, gr, dx.data_ptr(), None if dw is None else dw.data_ptr(), opt)
     return dx, dw
 
 
