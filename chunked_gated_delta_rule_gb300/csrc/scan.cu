@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kNT, 4) k_scan(ScanArgs a, int tiles) {
                 const ulonglong2 b0 = B[0], b1 = B[1];
                 const F2 b[4] = {{b0.x}, {b0.y}, {b1.x}, {b1.y}};
 #pragma unroll
-                for (int i = 0; i < kPS / 2; ++i) h[i] = fma2(ex2(dd * A2[i]), h[i], dx * b[i]);
+                for (int i = 0; i < kPS / 2; ++i) h[i] = fma2(decay(dd, A2[i]), h[i], dx * b[i]);
                 if constexpr (SUM) {
                     total += d.x;
                 } else {
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(128) k_scan_join(ScanArgs a) {
                 r.narrow(h);
                 r.store(part + i * states, 16, V);
 #pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = fmaf(ex2(A2[v] * d[k]), h[v], f[v]);
+                for (int v = 0; v < V; ++v) h[v] = fmaf(decay(A2[v], d[k]), h[v], f[v]);
             }
     }
     if (back && a.dh0) {
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, int tiles) {
             v[i] = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                h4[k] = fmaf(ex2(di * A4[k]), h4[k], dxi * b[k]);
+                h4[k] = fmaf(decay(di, A4[k]), h4[k], dxi * b[k]);
                 v[i] = fmaf(h4[k], cc[k], v[i]);
             }
             h[i].narrow(h4);

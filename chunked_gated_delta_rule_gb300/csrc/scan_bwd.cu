@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kNT) k_scan_bwd_ends(ScanArgs a, int tiles) {
             const F2 b[P] = {{b0.x}, {b0.y}, {b1.x}, {b1.y}}, cc[P] = {{c0.x}, {c0.y}, {c1.x}, {c1.y}};
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const F2 w = ex2(dd * A2[i]);
+                const F2 w = decay(dd, A2[i]);
                 h[i] = fma2(w, h[i], dx * b[i]);
                 D[i] = D[i] * w;
                 R[i] = fma2(D[i], cc[i] * dv, R[i]);
@@ -284,8 +284,8 @@ __device__ __forceinline__ void step(const float4 &d, const ulonglong2 &B, const
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const F2 dk = f2(dd[k]), xk = f2(dx[k]);
-        h[k][0] = fma2(ex2(dk * A2[k][0]), h[k][0], xk * F2{B.x});
-        h[k][1] = fma2(ex2(dk * A2[k][1]), h[k][1], xk * F2{B.y});
+        h[k][0] = fma2(decay(dk, A2[k][0]), h[k][0], xk * F2{B.x});
+        h[k][1] = fma2(decay(dk, A2[k][1]), h[k][1], xk * F2{B.y});
         if constexpr (OUT) y[k] = both(fma2(h[k][0], F2{C.x}, h[k][1] * F2{C.y}));
     }
 }
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, int tiles) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         F2 &g = dh[k][j];
-                        g = g * ex2(dd * A2[k][j]);
+                        g = g * decay(dd, A2[k][j]);
                         e[j] = g * (t ? hs[t ? t - 1 : 0][k][j] : before[k][j]);
                         dA[k][j] = fma2(e[j], dd, dA[k][j]);
                     }
