@@ -39,15 +39,16 @@ struct Lay {
 // SUM: leave a piece's end from a zero start (E) and the sum of its time steps (sd).  Else: the
 // outputs, from E (pieces) or from h0 (whole sequences), and the last state into ht.
 template <typename T, int LPC, bool SUM>
-__global__ void __launch_bounds__(kNT, 4) k_scan(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kNT, 4) k_scan(ScanArgs a, Tiles tiles) {
     using L = Lay<LPC>;
     constexpr int kT = L::kT, V = L::kV, kC = L::kC;
     using O = Order<V, L::kRows>;
     __shared__ float2 sdx[kT][kC + O::kPad];  // time step and its product with x; the sums over states
     __shared__ float4 sbc[2][kT][LPC][2];
     const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC;
-    const int64_t slot = blockIdx.x / tiles;
-    const Tile tile = tile_of<kC>(a, (int)(blockIdx.x % tiles));
+    const uint32_t slot_id = blockIdx.x / tiles.all;
+    const int64_t slot = slot_id;
+    const Tile tile = tile_of<kC>(tiles, blockIdx.x - slot_id * tiles.all);
     const int tr = tid / L::kRows, lv = tid % L::kRows, cv = lv * V;
     pdl_wait();
     if (!SUM && slot == a.slots) {  // tokens of no sequence
@@ -272,14 +273,14 @@ __global__ void __launch_bounds__(128) k_scan_join(ScanArgs a) {
 // those of channels i (32 / LPC) + l / LPC), and with its own token values of channel l, whose time
 // step it forms for the others.
 template <typename T, int LPC>
-__global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, Tiles tiles) {
     constexpr int kCh = 32 / LPC;
     const int lane = threadIdx.x & 31, q = lane % LPC, cl = lane / LPC;
-    const int64_t id = (int64_t)blockIdx.x * (kNT / 32) + (threadIdx.x >> 5);
-    const int64_t n = id / tiles;
+    const uint32_t id = blockIdx.x * (kNT / 32) + (threadIdx.x >> 5), seq = id / tiles.all;
+    const int64_t n = seq;
     if (blockIdx.x == 0 && threadIdx.x < 32) check_offsets(a.r);
     if (n > a.r.N) return;
-    const Tile tile = tile_of<32>(a, (int)(id % tiles));
+    const Tile tile = tile_of<32>(tiles, id - seq * tiles.all);
     const bool mine = lane < tile.valid;
     T *y = (T *)a.y + tile.c0 + lane;
     if (n == a.r.N) {  // tokens of no sequence
@@ -299,61 +300,66 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, int tiles) {
         return;
     }
     const int s0 = q * 4, wide = a.S % 4 ? 4 : a.st_bytes;
-    const int64_t at_state = (tile.c0 + cl) * a.S + s0;
-    auto have = [&](int i) { return i * kCh + cl < tile.valid ? max(0, min(4, a.S - s0)) : 0; };
-    Row<float, 4> A[LPC], h[LPC];
-#pragma unroll
-    for (int i = 0; i < LPC; ++i) {
-        const int64_t at = at_state + (int64_t)i * kCh * a.S;
-        h[i].zero();
-        if (a.h0) h[i].load(a.h0 + row * a.C * a.S + at, wide, have(i));
-        A[i].load(a.A + at, wide, have(i));
-    }
+    const int64_t at_state = (tile.c0 + cl) * a.S + s0, row_state = row * a.C * a.S + at_state;
     const float bias = a.dt_bias && mine ? a.dt_bias[tile.c0 + lane] : 0.f;
     const float skip = a.D && mine ? a.D[tile.c0 + lane] : 0.f;
-    for (int64_t t = s; t < s + len; ++t) {
-        Row<T, 4> rb, rc;
-        const int states = max(0, min(4, a.S - s0));
-        rb.load((const T *)a.Bm + t * a.bs[0] + tile.g * a.bs[1] + s0, a.bc_bytes, states);
-        rc.load((const T *)a.Cm + t * a.cs[0] + tile.g * a.cs[1] + s0, a.bc_bytes, states);
-        float x = 0.f, d = 0.f, z = 0.f, b[4], cc[4], v[LPC];
-        if (mine) {
-            x = to_f32(((const T *)a.x)[t * a.xs + tile.c0 + lane]);
-            d = to_f32(((const T *)a.dt)[t * a.dts + tile.c0 + lane]) + bias;
-            if (a.z) z = to_f32(((const T *)a.z)[t * a.zs + tile.c0 + lane]);
-        }
-        if (a.softplus) {
-            float unused;
-            split(softplus2(f2(d)), d, unused);
-        }
-        rb.widen(b);
-        rc.widen(cc);
-        const float dx = d * x;
+    auto run = [&](auto whole) {
+        // whole: all 32 channels, all states of every lane, 16-byte loads
+        constexpr bool W = decltype(whole)::value;
+        const int states = W ? 4 : max(0, min(4, a.S - s0)), bytes = W ? 16 : wide;
+        auto have = [&](int i) { return W || i * kCh + cl < tile.valid ? states : 0; };
+        const int step = kCh * a.S;
+        Row<float, 4> A[LPC], h[LPC];
 #pragma unroll
         for (int i = 0; i < LPC; ++i) {
-            const float di = __shfl_sync(0xffffffffu, d, i * kCh + cl) * kLog2e;
-            const float dxi = __shfl_sync(0xffffffffu, dx, i * kCh + cl);
-            float A4[4], h4[4];
-            A[i].widen(A4);
-            h[i].widen(h4);
-            v[i] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h4[k] = fmaf(decay(di, A4[k]), h4[k], dxi * b[k]);
-                v[i] = fmaf(h4[k], cc[k], v[i]);
-            }
-            h[i].narrow(h4);
+            h[i].zero();
+            if (a.h0) h[i].load(a.h0 + row_state + i * step, bytes, have(i));
+            A[i].load(a.A + at_state + i * step, bytes, have(i));
         }
-        // lane q of a channel's lanes has the sum of the q-th of its channels
-        float sum = __shfl_sync(0xffffffffu, fold<LPC>(v, q), lane % kCh * LPC + lane / kCh);
-        sum = fmaf(skip, x, sum);
-        if (a.z) sum *= z * sigmoid_f(z);
-        if (mine) y[t * a.ys] = from_f32<T>(sum);
-    }
-    if (!a.ht) return;
+        for (int64_t t = s; t < s + len; ++t) {
+            Row<T, 4> rb, rc;
+            rb.load((const T *)a.Bm + t * a.bs[0] + tile.g * a.bs[1] + s0, W ? 16 : a.bc_bytes, states);
+            rc.load((const T *)a.Cm + t * a.cs[0] + tile.g * a.cs[1] + s0, W ? 16 : a.bc_bytes, states);
+            float x = 0.f, d = 0.f, z = 0.f, b[4], cc[4], v[LPC];
+            if (W || mine) {
+                x = to_f32(((const T *)a.x)[t * a.xs + tile.c0 + lane]);
+                d = to_f32(((const T *)a.dt)[t * a.dts + tile.c0 + lane]) + bias;
+                if (a.z) z = to_f32(((const T *)a.z)[t * a.zs + tile.c0 + lane]);
+            }
+            if (a.softplus) {
+                float unused;
+                split(softplus2(f2(d)), d, unused);
+            }
+            rb.widen(b);
+            rc.widen(cc);
+            const F2 b01 = f2(b[0], b[1]), b23 = f2(b[2], b[3]), c01 = f2(cc[0], cc[1]), c23 = f2(cc[2], cc[3]);
+            const float dx = d * x, d2 = d * kLog2e;
 #pragma unroll
-    for (int i = 0; i < LPC; ++i)
-        h[i].store(a.ht + row * a.C * a.S + at_state + (int64_t)i * kCh * a.S, wide, have(i));
+            for (int i = 0; i < LPC; ++i) {
+                const F2 di = f2(__shfl_sync(0xffffffffu, d2, i * kCh + cl));
+                const F2 dxi = f2(__shfl_sync(0xffffffffu, dx, i * kCh + cl));
+                float A4[4], h4[4];
+                A[i].widen(A4);
+                h[i].widen(h4);
+                const F2 h01 = fma2(decay(di, f2(A4[0], A4[1])), f2(h4[0], h4[1]), dxi * b01);
+                const F2 h23 = fma2(decay(di, f2(A4[2], A4[3])), f2(h4[2], h4[3]), dxi * b23);
+                v[i] = both(fma2(h01, c01, h23 * c23));
+                split(h01, h4[0], h4[1]);
+                split(h23, h4[2], h4[3]);
+                h[i].narrow(h4);
+            }
+            // lane q of a channel's lanes has the sum of the q-th of its channels
+            float sum = __shfl_sync(0xffffffffu, fold<LPC>(v, q), lane % kCh * LPC + lane / kCh);
+            sum = fmaf(skip, x, sum);
+            if (a.z) sum *= z * sigmoid_f(z);
+            if (W || mine) y[t * a.ys] = from_f32<T>(sum);
+        }
+        if (!a.ht) return;
+#pragma unroll
+        for (int i = 0; i < LPC; ++i) h[i].store(a.ht + row_state + i * step, bytes, have(i));
+    };
+    if (tile.valid == 32 && a.S == 4 * LPC && wide >= 16 && a.bc_bytes >= 4 * (int)sizeof(T)) run(std::true_type{});
+    else run(std::false_type{});
 }
 
 }  // namespace
@@ -362,31 +368,32 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, int tiles) {
 int scan_channels(int S) { return kNT / (S <= 8 ? 1 : S <= 16 ? 2 : S <= 32 ? 4 : 8); }
 
 cudaError_t scan_step(const ScanArgs &a, int dtype, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, 32, a.G), warps = kNT / 32;
+    const Tiles tiles = tiles_of(a, 32);
+    const int64_t warps = kNT / 32;
     return scan_type(dtype, [&](auto t) {
         return scan_lanes(a.S, 4, [&](auto l) {
             k_scan_step<decltype(t), decltype(l)::value>
-                <<<(unsigned)(((a.r.N + 1) * tiles + warps - 1) / warps), kNT, 0, st>>>(a, (int)tiles);
+                <<<(unsigned)(((a.r.N + 1) * tiles.all + warps - 1) / warps), kNT, 0, st>>>(a, tiles);
             return cudaGetLastError();
         });
     });
 }
 
 cudaError_t scan_pieces(const ScanArgs &a, int dtype, bool summary, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, scan_channels(a.S), a.G);
+    const Tiles tiles = tiles_of(a, scan_channels(a.S));
     return scan_type(dtype, [&](auto t) {
         return scan_lanes(a.S, kPS, [&](auto l) {
             using T = decltype(t);
             constexpr int LPC = decltype(l)::value;
             if constexpr (LPC <= 8) {  // S is at most 64
                 if (summary) {
-                    k_scan<T, LPC, true><<<(unsigned)(a.slots * tiles), kNT, 0, st>>>(a, (int)tiles);
+                    k_scan<T, LPC, true><<<(unsigned)(a.slots * tiles.all), kNT, 0, st>>>(a, tiles);
                     return cudaGetLastError();
                 }
-                const dim3 grid((unsigned)((a.slots + 1) * tiles));
+                const dim3 grid((unsigned)((a.slots + 1) * tiles.all));
                 if (a.piece)
-                    return launch_pdl(k_scan<T, LPC, false>, grid, dim3(kNT), 0, st, a, (int)tiles);
-                k_scan<T, LPC, false><<<grid, kNT, 0, st>>>(a, (int)tiles);
+                    return launch_pdl(k_scan<T, LPC, false>, grid, dim3(kNT), 0, st, a, tiles);
+                k_scan<T, LPC, false><<<grid, kNT, 0, st>>>(a, tiles);
             }
             return cudaGetLastError();
         });

@@ -60,19 +60,28 @@ __device__ __forceinline__ void time_steps(const ScanArgs &a, const float (&raw)
     }
 }
 
-// The channels of tile `tile`: a tile lies within one group of B and C.
+// A launch's blocks: `all` tiles of channels for each slot (or sequence), those of a group side by
+// side, each of `per` channels.
+struct Tiles {
+    uint32_t all, group, per;
+};
+inline Tiles tiles_of(const ScanArgs &a, int channels) {
+    const uint32_t per = (uint32_t)(a.C / a.G), group = (per + channels - 1) / channels;
+    return Tiles{group * (uint32_t)a.G, group, per};
+}
+
+// The channels of tile `id`: a tile lies within one group of B and C.
 struct Tile {
     int64_t c0;
     int valid, g;
 };
 template <int C>
-__device__ __forceinline__ Tile tile_of(const ScanArgs &a, int tile) {
-    const int per = (int)(a.C / a.G), tiles = (per + C - 1) / C;
+__device__ __forceinline__ Tile tile_of(const Tiles &tiles, uint32_t id) {
     Tile t;
-    t.g = tile / tiles;
-    const int at = tile % tiles * C;
-    t.c0 = (int64_t)t.g * per + at;
-    t.valid = min(C, per - at);
+    t.g = tiles.group == tiles.all ? 0 : (int)(id / tiles.group);
+    const int at = (int)(id - t.g * tiles.group) * C;
+    t.c0 = (int64_t)t.g * tiles.per + at;
+    t.valid = min(C, (int)tiles.per - at);
     return t;
 }
 

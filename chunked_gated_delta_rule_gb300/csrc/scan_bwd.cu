@@ -160,15 +160,16 @@ __device__ __forceinline__ void store_states(float *p, int64_t at, int s0, int S
 
 // 1. E, sd and R of a piece.  A thread has eight states of a channel.
 template <typename T, int LPC>
-__global__ void __launch_bounds__(kNT) k_scan_bwd_ends(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kNT) k_scan_bwd_ends(ScanArgs a, Tiles tiles) {
     using L = Ends<LPC>;
     constexpr int kT = L::kT, kC = L::kC, P = 4;
     __shared__ __align__(16) float2 sdx[kT][L::kPitch];
     __shared__ float sdv[kT][L::kPitch], sch[2 * kC];
     __shared__ __align__(16) float sbc[2 * kT * L::kS];
     const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC;
-    const int64_t slot = blockIdx.x / tiles;
-    const Tile tile = tile_of<kC>(a, (int)(blockIdx.x % tiles));
+    const uint32_t slot_id = blockIdx.x / tiles.all;
+    const int64_t slot = slot_id;
+    const Tile tile = tile_of<kC>(tiles, blockIdx.x - slot_id * tiles.all);
     if (blockIdx.x == 0 && tid < 32) check_offsets(a.r);
     const Piece p = piece_of(a, slot);
     if (p.n < 0) return;
@@ -292,15 +293,15 @@ __device__ __forceinline__ void step(const float4 &d, const ulonglong2 &B, const
 
 // 3. The gradients of a piece.  At the end E's slot holds its part of dA.
 template <typename T, int LPC>
-__global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, Tiles tiles) {
     using L = Main<LPC>;
     constexpr int kT = L::kT, V = L::kV, kC = L::kC, kS = L::kS;
     extern __shared__ __align__(16) uint8_t raw_smem[];
     Smem<LPC> &sm = *reinterpret_cast<Smem<LPC> *>(raw_smem);
     const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC, lane = tid & 31, warp = tid >> 5;
-    const int64_t slot = blockIdx.x / tiles;
-    const int tile_id = (int)(blockIdx.x % tiles);
-    const Tile tile = tile_of<kC>(a, tile_id);
+    const uint32_t slot_id = blockIdx.x / tiles.all, tile_id = blockIdx.x - slot_id * tiles.all;
+    const int64_t slot = slot_id;
+    const Tile tile = tile_of<kC>(tiles, tile_id);
     const int tr = tid / L::kRows, lv = tid % L::kRows, cv = lv * V;
     const int64_t all = total_tokens(a.r);
     float *part = a.part + (int64_t)tile_id * all * 2 * a.S;
@@ -525,12 +526,12 @@ __global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, int tiles) {
 
 // 4a. dB and dC of a token, group and state: the sums of the group's tiles.
 template <typename T>
-__global__ void __launch_bounds__(256) k_scan_bwd_bc(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(256) k_scan_bwd_bc(ScanArgs a, Tiles tiles) {
     const int64_t all = total_tokens(a.r), per = 2 * (int64_t)a.S, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     pdl_wait();
     if (id >= all * a.G * per) return;
     const int64_t t = id / (a.G * per);
-    const int g = (int)(id / per % a.G), w = (int)(id / a.S % 2), s = (int)(id % a.S), n = tiles / a.G;
+    const int g = (int)(id / per % a.G), w = (int)(id / a.S % 2), s = (int)(id % a.S), n = (int)tiles.group;
     float f = 0.f;
     const float *p = a.part + ((int64_t)g * n * all + t) * per + w * a.S + s;
     for (int k = 0; k < n; ++k) f += p[(int64_t)k * all * per];
@@ -562,8 +563,8 @@ cudaError_t scan_bwd_ends(const ScanArgs &a, int dtype, cudaStream_t st) {
             constexpr int LPC = decltype(l)::value;
             if constexpr (LPC <= 8) {  // S is at most 64
                 using T = decltype(t);
-                const int64_t tiles = scan_tiles(a.C, Ends<LPC>::kC, a.G);
-                k_scan_bwd_ends<T, LPC><<<(unsigned)(a.slots * tiles), kNT, 0, st>>>(a, (int)tiles);
+                const Tiles tiles = tiles_of(a, Ends<LPC>::kC);
+                k_scan_bwd_ends<T, LPC><<<(unsigned)(a.slots * tiles.all), kNT, 0, st>>>(a, tiles);
             }
             return cudaGetLastError();
         });
@@ -571,7 +572,7 @@ cudaError_t scan_bwd_ends(const ScanArgs &a, int dtype, cudaStream_t st) {
 }
 
 cudaError_t scan_bwd(const ScanArgs &a, int dtype, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, scan_bwd_channels(a.S), a.G);
+    const Tiles tiles = tiles_of(a, scan_bwd_channels(a.S));
     return scan_type(dtype, [&](auto t) {
         return scan_lanes(a.S, 4, [&](auto l) {
             using T = decltype(t);
@@ -583,18 +584,18 @@ cudaError_t scan_bwd(const ScanArgs &a, int dtype, cudaStream_t st) {
                                             (int)smem);
             });
             if (e != cudaSuccess) return e;
-            return launch_pdl(k_scan_bwd<T, LPC>, dim3((unsigned)((a.slots + 1) * tiles)), dim3(kNT), smem,
-                              st, a, (int)tiles);
+            return launch_pdl(k_scan_bwd<T, LPC>, dim3((unsigned)((a.slots + 1) * tiles.all)), dim3(kNT), smem,
+                              st, a, tiles);
         });
     });
 }
 
 cudaError_t scan_bwd_bc(const ScanArgs &a, int dtype, cudaStream_t st) {
-    const int64_t tiles = scan_tiles(a.C, scan_bwd_channels(a.S), a.G);
+    const Tiles tiles = tiles_of(a, scan_bwd_channels(a.S));
     const int64_t all = rows_packed(a.r) ? a.r.T : a.r.N * a.r.T, outs = all * a.G * 2 * a.S;
     return scan_type(dtype, [&](auto t) {
         return launch_pdl(k_scan_bwd_bc<decltype(t)>, dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, st,
-                          a, (int)tiles);
+                          a, tiles);
     });
 }
 
