@@ -77,14 +77,15 @@ class HybridModel:
         cu = torch.tensor([0] + lens, device=x.device).cumsum(0).to(torch.int32)
         cache.extend(lens)
         T, longest = x.shape[0], max(lens)
+        new = None  # what the last layer adds to x, added by the next one's norm
         for i, w in enumerate(self.rule):
             if i == 1:  # the attention layer lies between the rule's two
-                h = norm(x)
+                h, x = add_norm(x, new)
                 q = (h @ self.attn["q"]).view(1, T, HEADS, DIM)
                 kv = (h @ self.attn["kv"]).view(1, T, 2, KV_HEADS, DIM)
                 o = cache.attend(q, kv[:, :, 0], kv[:, :, 1], cu, longest)
-                x = x + o.reshape(T, WIDTH) @ self.attn["out"]
-            h = norm(x)
+                new = o.reshape(T, WIDTH) @ self.attn["out"]
+            h, x = add_norm(x, new)
             qkv = (h @ w["qkv"]).view(1, T, 3, HEADS, DIM)
             q, k = (norm(qkv[:, :, j]) * DIM ** -0.5 for j in (0, 1))
             gates = (h @ w["gate"]).float().view(1, T, 2, HEADS)
@@ -95,8 +96,15 @@ class HybridModel:
             else:
                 o, states[i] = gdr.gdr_chunk_fwd(q, k, qkv[:, :, 2], g, beta, cu, h0=states[i],
                                                  max_seqlen=longest)
-            x = x + o.reshape(T, WIDTH) @ w["out"]
-        return x
+            new = o.reshape(T, WIDTH) @ w["out"]
+        return x + new
+
+
+def add_norm(x, new):
+    """The norm of x + new, and x + new."""
+    if new is None:
+        return gdr.gdr_rms_norm_fwd(x)[0], x
+    return gdr.gdr_rms_norm_fwd(new, None, x)[:2]
 
 
 def norm(x):
