@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, kConvThreads / kThreads) k_conv(Conv
     while (t < t1) {
         const Seq q = seq_at(a.r, t, together);
         int64_t row = 0;
-        if (q.n >= 0 && a.h0) row = state_row(a.idx, a.n_states, q.n, a.r.status);
+        if (q.n >= 0 && (a.h0 || a.ht)) row = state_row(a.idx, a.n_states, q.n, a.r.status);
         const int64_t end = min(q.e, t1);
         if (q.n < 0 || row < 0) {  // nobody's tokens
             Row<T, V> zero;

@@ -153,10 +153,11 @@ int check_scan(const gdr_scan_dims *d) {
         (d->y_stride != 0 && d->y_stride < d->C))
         return GDR_ERR_INVALID;
     if (d->S > 64 || d->C > INT32_MAX / 64) return GDR_ERR_UNSUPPORTED;
-    // blocks of a launch: every piece (of 32 tokens at least) of every tile of channels
+    // blocks of a launch: every piece (of 32 tokens at least) of every tile of channels; 128 states of
+    // the join
     const int64_t seqs = d->N > 0 ? d->N : d->B, tiles = scan_tiles(d->C, scan_bwd_channels((int)d->S), (int)d->G);
     if (tokens_of(*d) / 32 + seqs + 1 > INT32_MAX / tiles ||
-        seqs > INT32_MAX * (int64_t)256 / (d->C * d->S) - 1)
+        seqs > INT32_MAX * (int64_t)128 / (d->C * d->S) - 1)
         return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
@@ -398,6 +399,7 @@ int gdr_selective_scan_bwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
         (tokens > 0 && (!dy || !out->dx || !out->ddt || !out->dB || !out->dC || (in->z && !out->dz))) ||
         (out->dD && !in->D) || (out->ddt_bias && !in->dt_bias) || (out->dz && !in->z))
         return GDR_ERR_INVALID;
+    if (tokens > INT32_MAX * (int64_t)128 / (d.G * d.S)) return GDR_ERR_UNSUPPORTED;  // blocks of dB, dC
     ScanArgs a = scan_args(d, *in, cu_seqlens, opt);
     a.h0 = h0; a.dy = dy; a.dht = dht;
     a.n_states = seqs;
@@ -440,6 +442,8 @@ int gdr_rms_norm_fwd(const gdr_norm_dims *dims, const void *x, const void *resid
     if ((residual != nullptr) != (sum != nullptr) ||
         (d.rows > 0 && (!x || !y || (quant && !scale))) || (!quant && scale))
         return GDR_ERR_INVALID;
+    // two outputs in one place; values of other sizes over rows that are still to be read
+    if (y && (y == sum || (quant && (y == x || y == residual)))) return GDR_ERR_INVALID;
     NormArgs a{};
     a.x = x; a.res = residual; a.r = sum; a.y = y; a.scale = scale;
     a.w = Param{weight, d.weight_dtype == GDR_F32};

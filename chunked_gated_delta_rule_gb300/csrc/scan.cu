@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kNT, 4) k_scan(ScanArgs a, Tiles tiles) {
 #pragma unroll
         for (int i = 0; i < kPS; ++i) {
             const bool in = mine && q * kPS + i < a.S;
-            fa[i] = in ? a.A[at_state + i] * kLog2e : 0.f;
+            fa[i] = in ? times_log2e(a.A[at_state + i]) : 0.f;
             fh[i] = in && from ? from[at_state + i] : 0.f;
         }
 #pragma unroll
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(128) k_scan_join(ScanArgs a) {
     r.load(a.A + at, a.st_bytes, V);
     r.widen(A2);
 #pragma unroll
-    for (int k = 0; k < V; ++k) A2[k] *= kLog2e;
+    for (int k = 0; k < V; ++k) A2[k] = times_log2e(A2[k]);
     r.zero();
     if (back) {
         if (a.dht) r.load(a.dht + n * states + at, a.st_bytes, V);
@@ -316,6 +316,13 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, Tiles tiles) {
             if (a.h0) h[i].load(a.h0 + row_state + i * step, bytes, have(i));
             A[i].load(a.A + at_state + i * step, bytes, have(i));
         }
+        float A2[LPC][4];
+#pragma unroll
+        for (int i = 0; i < LPC; ++i) {
+            A[i].widen(A2[i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) A2[i][k] = times_log2e(A2[i][k]);
+        }
         for (int64_t t = s; t < s + len; ++t) {
             Row<T, 4> rb, rc;
             rb.load((const T *)a.Bm + t * a.bs[0] + tile.g * a.bs[1] + s0, W ? 16 : a.bc_bytes, states);
@@ -333,16 +340,15 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, Tiles tiles) {
             rb.widen(b);
             rc.widen(cc);
             const F2 b01 = f2(b[0], b[1]), b23 = f2(b[2], b[3]), c01 = f2(cc[0], cc[1]), c23 = f2(cc[2], cc[3]);
-            const float dx = d * x, d2 = d * kLog2e;
+            const float dx = d * x;
 #pragma unroll
             for (int i = 0; i < LPC; ++i) {
-                const F2 di = f2(__shfl_sync(0xffffffffu, d2, i * kCh + cl));
+                const F2 di = f2(__shfl_sync(0xffffffffu, d, i * kCh + cl));
                 const F2 dxi = f2(__shfl_sync(0xffffffffu, dx, i * kCh + cl));
-                float A4[4], h4[4];
-                A[i].widen(A4);
+                float h4[4];
                 h[i].widen(h4);
-                const F2 h01 = fma2(decay(di, f2(A4[0], A4[1])), f2(h4[0], h4[1]), dxi * b01);
-                const F2 h23 = fma2(decay(di, f2(A4[2], A4[3])), f2(h4[2], h4[3]), dxi * b23);
+                const F2 h01 = fma2(decay(di, f2(A2[i][0], A2[i][1])), f2(h4[0], h4[1]), dxi * b01);
+                const F2 h23 = fma2(decay(di, f2(A2[i][2], A2[i][3])), f2(h4[2], h4[3]), dxi * b23);
                 v[i] = both(fma2(h01, c01, h23 * c23));
                 split(h01, h4[0], h4[1]);
                 split(h23, h4[2], h4[3]);

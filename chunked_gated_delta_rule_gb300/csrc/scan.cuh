@@ -27,6 +27,13 @@ constexpr float kEx2Lack = 2.9e-8f;
 __device__ __forceinline__ F2 decay(F2 d, F2 A2) { return ex2(fma2(d, A2, f2(kEx2Lack))); }
 __device__ __forceinline__ float decay(float d, float A2) { return ex2(fmaf(d, A2, kEx2Lack)); }
 
+// A log2(e), finite where A = -inf: times the zero time step of a place past a sequence's end it has to
+// give a decay of 1.
+__device__ __forceinline__ float times_log2e(float A) {
+    const float x = A * kLog2e;
+    return x < -3e38f ? -3e38f : x;
+}
+
 // log(1 + e^x) = max(x, 0) + log(1 + u), u = e^-|x|, for two values.  u is 2^-t with what rounding
 // t = |x| log2(e) lost put back.  log(1 + u) = 2 artanh(s) with 2 s = u / (1 + u / 2); artanh(s) / s
 // is a polynomial in (2 s)^2 <= 4 / 9 (fitted here, off by 5e-9 at most).

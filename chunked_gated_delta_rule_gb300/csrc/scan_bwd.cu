@@ -138,14 +138,18 @@ __device__ __forceinline__ void load_channels(const ScanArgs &a, const Tile &til
     }
 }
 
-// 2 P values of A or of a state, zeros past S and the tile.
-template <int P>
-__device__ __forceinline__ void load_states(const float *p, int64_t at, int s0, int S, bool mine, float by,
-                                            F2 (&to)[P]) {
+// 2 P values of A, as times_log2e, or of a state (none without an address), zeros past S and the
+// tile.
+template <int P, bool IS_A>
+__device__ __forceinline__ void load_states(const float *p, int64_t at, int s0, int S, bool mine, F2 (&to)[P]) {
+    float f[2 * P];
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-        to[i] = f2(p && mine && s0 + 2 * i < S ? p[at + 2 * i] * by : 0.f,
-                   p && mine && s0 + 2 * i + 1 < S ? p[at + 2 * i + 1] * by : 0.f);
+    for (int i = 0; i < 2 * P; ++i) {
+        f[i] = p && mine && s0 + i < S ? p[at + i] : 0.f;
+        if (IS_A) f[i] = times_log2e(f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) to[i] = f2(f[2 * i], f[2 * i + 1]);
 }
 template <int P>
 __device__ __forceinline__ void store_states(float *p, int64_t at, int s0, int S, const F2 (&from)[P]) {
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kNT) k_scan_bwd_ends(ScanArgs a, Tiles tiles) 
     const bool mine = ch < tile.valid;
     F2 A2[P], h[P], D[P], R[P];
     float total = 0.f;
-    load_states<P>(a.A, at_state, q * 8, a.S, mine, kLog2e, A2);
+    load_states<P, true>(a.A, at_state, q * 8, a.S, mine, A2);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         h[i] = R[i] = f2(0.f);
@@ -335,9 +339,9 @@ __global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, Tiles tiles) {
         const int ch = L::O::channel(2 * cl + k);
         at_state[k] = (tile.c0 + ch) * a.S + s0;
         mine[k] = ch < tile.valid;
-        load_states<2>(a.A, at_state[k], s0, a.S, mine[k], kLog2e, A2[k]);
-        load_states<2>(len ? a.E + slot * a.C * a.S : nullptr, at_state[k], s0, a.S, mine[k], 1.f, h[k]);
-        load_states<2>(len ? a.R + slot * a.C * a.S : nullptr, at_state[k], s0, a.S, mine[k], 1.f, dh[k]);
+        load_states<2, true>(a.A, at_state[k], s0, a.S, mine[k], A2[k]);
+        load_states<2, false>(len ? a.E + slot * a.C * a.S : nullptr, at_state[k], s0, a.S, mine[k], h[k]);
+        load_states<2, false>(len ? a.R + slot * a.C * a.S : nullptr, at_state[k], s0, a.S, mine[k], dh[k]);
         dA[k][0] = dA[k][1] = f2(0.f);
     }
     float dD[V], db[V];  // of the channels that the thread loads

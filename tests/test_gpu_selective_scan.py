@@ -248,6 +248,23 @@ def test_values_that_are_not_finite_stay_in_their_channel_and_sequence():
     assert torch.equal(ht2[[0, 2]], ht[[0, 2]])
 
 
+def test_states_that_forget_at_once():
+    """A = -inf: a decay of zero for every token, and none for the places past a sequence's end that
+    tiles and pieces are filled up with."""
+    lens = [20, 33, 100]
+    s = inputs(lens, 32, 16, dtype="f32")
+    s["A"][3, 5] = -float("inf")
+    r = want(dict(s, A=s["A"].clamp(min=-1e30)), lens)
+    for kw in (dict(max_seqlen=1), dict(n_segments=1), dict(n_segments=3, max_seqlen=100)):
+        y, ht = forward(s, h0=s["h0"], **kw)
+        close("y", y, r["y"])
+        close("ht", ht, r["ht"])
+    got = backward(s, h0=s["h0"])
+    (r["y"] * s["dy"].cpu().double()).sum().backward()
+    for k, g in zip(NAMES, got):
+        close("d" + k, g, r[k].grad)
+
+
 def test_captured_calls_and_own_scratch():
     """A captured forward (in pieces) and backward replayed on other values, the caller's
     scratch, and a second run give the same bits; too little scratch is refused."""

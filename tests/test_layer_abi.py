@@ -144,6 +144,9 @@ def test_bad_norms(lib):
     for kw in (dict(x=None), dict(y=None), dict(res=4), dict(out=4), dict(scale=5)):
         assert norm_fwd(lib, ok, **kw) == -1, kw
     assert norm_fwd(lib, q) == -1                                    # a scale is wanted
+    assert norm_fwd(lib, ok, res=4, out=3, y=3) == -1                # two outputs in one place
+    assert norm_fwd(lib, q, y=1, scale=5) == -1                      # 8 bits over rows to be read
+    assert norm_fwd(lib, q, res=4, out=6, y=4, scale=5) == -1
     assert norm_fwd(lib, norm(out_dtype=E4M3, group=64), scale=5) == -1
     bwd = lambda d, r=1, w=2, dy=3, dx=4, dw=5, opt=None: lib.gdr_rms_norm_bwd(  # noqa: E731
         d, _p(r), _p(w), _p(dy), None, _p(dx), _p(dw), opt, None)
