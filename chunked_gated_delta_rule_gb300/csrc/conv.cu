@@ -122,50 +122,66 @@ __device__ __forceinline__ void one_token(const ConvArgs &a, const Row<T, V> &r,
 template <typename T, int V, int N>
 struct Feed {
     static constexpr bool kRing = V > 1;
-    using Slot = T[kThreads][V];
+    static constexpr int kSlot = kThreads * V * (int)sizeof(T);  // a row of every thread
+    static constexpr int kBatch = kAhead * N * kSlot;
     // batches that are on their way or worked on, within 48 KB
-    static constexpr int kDepth = kAhead * N * (int)sizeof(Slot) <= 12288 ? 4 : 3;
-    static constexpr int kBytes = kRing ? kDepth * kAhead * N * (int)sizeof(Slot) : 16;
-    Slot *ring;  // [kDepth * kAhead * N]
-    const T *p[N];
-    int64_t stride[N];
+    static constexpr int kDepth = kBatch <= 12288 ? 4 : 3;
+    static constexpr int kBytes = kRing ? kDepth * kBatch : 16;
 
-    __device__ __forceinline__ T *slot(int64_t batch, int i, int n) const {
-        return ring[((int)(batch % kDepth) * kAhead + i) * N + n][threadIdx.x];
-    }
-    // Asks for batch `batch` from token t on, if it exists.
-    __device__ __forceinline__ void ask(int64_t batch, int64_t batches, int64_t t) const {
+    uint8_t *const ring;    // the thread's place in the first slot
+    const T *next[N];       // rows of the next batch to ask for
+    const int64_t stride[N];
+    int put = 0, get = 0;   // batches, in bytes from ring
+    int64_t left = 0;       // batches to ask for
+
+    __device__ __forceinline__ void ask() {
         if constexpr (kRing) {
-            if (batch < batches) {
+            if (left > 0) {
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i)
+                for (int n = 0; n < N; ++n) {
+                    const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring) + put + n * kSlot;
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot(batch, i, n));
-                        const T *from = p[n] + (t + batch * kAhead + i) * stride[n];
+                    for (int i = 0; i < kAhead; ++i) {
                         if constexpr (V * sizeof(T) == 16)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * N * kSlot),
+                                         "l"(next[n]) : "memory");
                         else
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from),
-                                         "n"(V * sizeof(T)) : "memory");
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + i * N * kSlot),
+                                         "l"(next[n]), "n"(V * sizeof(T)) : "memory");
+                        next[n] += stride[n];
                     }
+                }
+                put = put + kBatch == kBytes ? 0 : put + kBatch;
+                --left;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     }
-    __device__ __forceinline__ void start(int64_t batches, int64_t t) const {
+    // `batches` batches of the rows from p[n] on.
+    __device__ __forceinline__ void start(const T *const (&p)[N], int64_t batches) {
 #pragma unroll
-        for (int k = 0; k < kDepth - 1; ++k) ask(k, batches, t);
+        for (int n = 0; n < N; ++n) next[n] = p[n];
+        left = batches;
+        put = get = 0;
+#pragma unroll
+        for (int k = 0; k < kDepth - 1; ++k) ask();
     }
-    // The rows of batch `batch`, and the one that its place is free for behind it.
-    __device__ __forceinline__ void take(int64_t batch, int64_t batches, int64_t t, Row<T, V> (&r)[kAhead][N]) const {
+    // The rows of the next batch; the place of the one before it is free for another.
+    __device__ __forceinline__ void take(Row<T, V> (&r)[kAhead][N]) {
         if constexpr (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-            for (int n = 0; n < N; ++n)
-                r[i][n].load(kRing ? slot(batch, i, n) : p[n] + (t + batch * kAhead + i) * stride[n], 16, V);
-        ask(batch + kDepth - 1, batches, t);
+            for (int n = 0; n < N; ++n) {
+                if constexpr (kRing) {
+                    r[i][n].load(reinterpret_cast<const T *>(ring + get + (i * N + n) * kSlot), 16, V);
+                } else {
+                    r[i][n].load(next[n], 16, V);
+                    next[n] += stride[n];
+                }
+            }
+        get = get + kBatch == kBytes ? 0 : get + kBatch;
+        ask();
     }
 };
 
@@ -183,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, kConvThreads / kThreads) k_conv(Conv
     const int64_t t1 = min(t + a.run, total);
     using F = Feed<T, V, 1>;
     __shared__ __align__(16) uint8_t ring[F::kBytes];
-    const F feed{reinterpret_cast<typename F::Slot *>(ring), {(const T *)a.x + c}, {a.xs}};
+    F feed{ring + (F::kRing ? threadIdx.x * V * sizeof(T) : 0), {}, {a.xs}};
     F2 w[W][P], b[P], win[W - 1][P];
     load_taps<T, W, V>(a, c, w, b);
     while (t < t1) {
@@ -198,11 +214,11 @@ __global__ void __launch_bounds__(kThreads, kConvThreads / kThreads) k_conv(Conv
             continue;
         }
         load_window<T, W, V>(a, t, q.s, row, c, win);
-        const int64_t batches = (end - t) / kAhead, t0 = t;
-        feed.start(batches, t0);
+        const int64_t batches = (end - t) / kAhead;
+        feed.start({(const T *)a.x + t * a.xs + c}, batches);
         for (int64_t k = 0; k < batches; ++k) {
             Row<T, V> r[kAhead][1];
-            feed.take(k, batches, t0, r);
+            feed.take(r);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i, ++t) one_token<T, W, V>(a, r[i][0], t, c, w, b, win);
         }
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, kConvThreads / kThreads) k_conv_bwd(
     constexpr int P = kPairs<V>;
     using F = Feed<T, V, 2>;
     __shared__ __align__(16) uint8_t ring[F::kBytes];
-    const F feed{reinterpret_cast<typename F::Slot *>(ring), {(const T *)a.x + c, (const T *)a.dy + c}, {a.xs, a.ys}};
+    F feed{ring + (F::kRing ? threadIdx.x * V * sizeof(T) : 0), {}, {a.xs, a.ys}};
     F2 w[W][P], b[P], dw[W + 1][P];
     load_taps<T, W, V>(a, c, w, b);
 #pragma unroll
@@ -327,14 +343,17 @@ __global__ void __launch_bounds__(kThreads, kConvThreads / kThreads) k_conv_bwd(
 #pragma unroll
             for (int j = 0; j < P; ++j) pend[k][j] = f2(0.f);
         const int64_t mine = min(q.e, t1), stop = min(q.e, t1 + W - 1), first = t;
-        auto token = [&](const Row<T, V> &rx, const Row<T, V> &rd, int64_t p) {
+        const int own = (int)(mine - t);  // tokens of the run: at most a few hundred
+        T *out = (T *)a.dx + (t - (W - 1)) * a.C + c;
+        int at = 0;  // tokens done
+        auto token = [&](const Row<T, V> &rx, const Row<T, V> &rd) {
             F2 x[P], du[P];
             widen2<T, V>(rx, x);
             widen2<T, V>(rd, du);
             grad_u<W, P>(a.silu, w, b, win, x, du);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                if (p < mine) {
+                if (at < own) {
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) dw[k][j] = fma2(du[j], win[k][j], dw[k][j]);
                     dw[W - 1][j] = fma2(du[j], x[j], dw[W - 1][j]);
@@ -345,21 +364,23 @@ __global__ void __launch_bounds__(kThreads, kConvThreads / kThreads) k_conv_bwd(
                 pend[0][j] = w[W - 1][j] * du[j];
             }
             shift<W, P>(win, x);
-            if (p - (W - 1) >= first) store2<T, V>((T *)a.dx + (p - (W - 1)) * a.C + c, pend[W - 1]);
+            if (at >= W - 1) store2<T, V>(out, pend[W - 1]);
+            out += a.C;
+            ++at;
         };
         const int64_t batches = (stop - t) / kAhead;
-        feed.start(batches, first);
+        feed.start({(const T *)a.x + t * a.xs + c, (const T *)a.dy + t * a.ys + c}, batches);
         for (int64_t k = 0; k < batches; ++k) {
             Row<T, V> r[kAhead][2];
-            feed.take(k, batches, first, r);
+            feed.take(r);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i, ++t) token(r[i][0], r[i][1], t);
+            for (int i = 0; i < kAhead; ++i) token(r[i][0], r[i][1]);
         }
-        for (; t < stop; ++t) {
+        for (t += batches * kAhead; t < stop; ++t) {
             Row<T, V> rx, rd;
             rx.load((const T *)a.x + t * a.xs + c, 16, V);
             rd.load((const T *)a.dy + t * a.ys + c, 16, V);
-            token(rx, rd, t);
+            token(rx, rd);
         }
         if (stop == q.e) {  // the sequence's last tokens: what is pending is whole but for dht
 #pragma unroll
