@@ -21,27 +21,31 @@ namespace {
 
 constexpr int kWarpRows = 4;  // rows of a block whose warps take one each
 constexpr int kMaxBlock = 512, kMaxNarrow = 1024;  // threads of a row
+constexpr int kBwdThreads = 512;                   // of the backward on an SM: their registers fill it
 
 template <typename T, int V, bool WARP>
 constexpr int most_threads() {
     return WARP ? 32 * kWarpRows : V * sizeof(T) < 16 ? kMaxNarrow : kMaxBlock;
 }
 
-// Sum over the threads of a row: a warp, or the block (sh: 32 floats).
-__device__ __forceinline__ float warp_sum(float x) {
+// Sums over the threads of a row, a warp or the block (sh: 32 pairs), of two values at once.
+__device__ __forceinline__ float2 warp_sum(float2 x) {
 #pragma unroll
-    for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+    for (int i = 16; i; i >>= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, i);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, i);
+    }
     return x;
 }
 template <bool WARP>
-__device__ __forceinline__ float row_sum(float x, float *sh) {
+__device__ __forceinline__ float2 row_sum(float2 x, float2 *sh) {
     x = warp_sum(x);
     if constexpr (WARP) return x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
     __syncthreads();  // sh may still be read
     if (lane == 0) sh[warp] = x;
     __syncthreads();
-    return warp_sum(lane < n ? sh[lane] : 0.f);
+    return warp_sum(lane < n ? sh[lane] : make_float2(0.f, 0.f));
 }
 // The largest of magnitudes, NaN if one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -56,14 +60,14 @@ __device__ __forceinline__ float lanes_max(float x) {
     return x;
 }
 template <bool WARP>
-__device__ __forceinline__ float row_max(float x, float *sh) {
+__device__ __forceinline__ float row_max(float x, float2 *sh) {
     x = lanes_max<32>(x);
     if constexpr (WARP) return x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
     __syncthreads();
-    if (lane == 0) sh[warp] = x;
+    if (lane == 0) sh[warp].x = x;
     __syncthreads();
-    return lanes_max<32>(lane < n ? sh[lane] : 0.f);
+    return lanes_max<32>(lane < n ? sh[lane].x : 0.f);
 }
 
 template <typename T, int V>
@@ -142,7 +146,7 @@ struct Columns {
 template <typename T, int V, int NV, bool WARP, int OUT>
 __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a) {
     constexpr int P = kPairs<V>;
-    __shared__ float sh[32];
+    __shared__ float2 sh[32];
     const Columns<V, WARP> col;
     const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.rows) return;  // whole warps
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a)
             for (int j = 0; j < P; ++j) sum2 = fma2(f[j], f[j], sum2);
         }
     }
-    const float sum = row_sum<WARP>(both(sum2), sh);
+    const float sum = row_sum<WARP>(make_float2(both(sum2), 0.f), sh).x;
     const F2 rstd = f2(rsqrtf(sum / (float)D + a.eps));
     auto normed = [&](int i, F2(&y)[P]) {
         F2 w[P];
@@ -246,7 +250,7 @@ template <typename T, int V, int NV, bool WARP>
 __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArgs a) {
     constexpr int P = kPairs<V>;
     extern __shared__ float acc[];  // WARP: [kWarpRows][D]
-    __shared__ float sh[32];
+    __shared__ float2 sh[32];
     const Columns<V, WARP> col;
     const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x, D = a.D;
     F2 dw[NV][P];
@@ -279,9 +283,9 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
                 dot2 = fma2(f[j], g[j] * w[j], dot2);
             }
         }
-        const float sum = row_sum<WARP>(both(sum2), sh), dot = row_sum<WARP>(both(dot2), sh);
-        const float rstd = rsqrtf(sum / (float)D + a.eps);
-        const F2 rs = f2(rstd), k = f2(-dot * rstd / (float)D);  // -mean(w dy n)
+        const float2 sums = row_sum<WARP>(make_float2(both(sum2), both(dot2)), sh);
+        const float rstd = rsqrtf(sums.x / (float)D + a.eps);
+        const F2 rs = f2(rstd), k = f2(-sums.y * rstd / (float)D);  // -mean(w dy n)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = col(i);
@@ -424,7 +428,7 @@ int64_t norm_bwd_blocks(int64_t rows, int64_t D, int vec, int dtype) {
     const Shape s = shape_of(rows, D, vec, es, most_bwd(es));
     const int64_t all = s.threads == 32 ? (rows + kWarpRows - 1) / kWarpRows : rows;
     const int block = s.threads == 32 ? 32 * kWarpRows : s.threads;
-    const int64_t fit = (int64_t)device_sms() * (1024 / block);
+    const int64_t fit = (int64_t)device_sms() * (block < kBwdThreads ? kBwdThreads / block : 1);
     return all < fit ? all : fit;
 }
 
