@@ -62,6 +62,7 @@ struct ScanArgs {
     float *E, *sd;            // [slots][C][S] states, [slots][C] sums of the time steps
     float *R, *part;          // backward: [slots][C][S]; [tiles][tokens][2 S]
     float *pd;                // backward: [slots][2 C] of D and dt_bias
+    float *keep, *keep_d;     // backward: [slots][kScanBwdPiece / kScanBwdKeep][C][S] and [..][C]
     int bytes, bc_bytes;      // alignment: x, dt, z, y, dy; B and C
     int st_bytes, out_bytes;  // A, h0, ht, dht, dh0; dx, ddt, dz
 };
@@ -77,6 +78,8 @@ cudaError_t scan_bwd_params(const ScanArgs &a, cudaStream_t st);
 int scan_channels(int S);
 int scan_bwd_channels(int S);
 inline int64_t scan_tiles(int64_t C, int channels, int G) { return G * ((C / G + channels - 1) / channels); }
-constexpr int kScanBwdPiece = 64;  // the backward's
+// The backward's pieces, and the tokens between the states that its first pass leaves for the main
+// one.
+constexpr int kScanBwdPiece = 64, kScanBwdKeep = 8;
 
 }  // namespace gdr

@@ -192,7 +192,7 @@ int64_t slots_of(const gdr_scan_dims &d, int64_t piece) {
 }
 
 struct ScanScratch {
-    size_t E, R, sd, pd, part, total;
+    size_t E, R, sd, pd, part, keep, keep_d, total;
 };
 ScanScratch scan_scratch(const gdr_scan_dims &d, int64_t piece, bool backward) {
     const size_t slots = (size_t)slots_of(d, piece), C = (size_t)d.C, S = (size_t)d.S;
@@ -208,6 +208,8 @@ ScanScratch scan_scratch(const gdr_scan_dims &d, int64_t piece, bool backward) {
     if (backward) {
         s.R = take(slots * C * S);
         s.pd = take(slots * 2 * C);
+        s.keep = take(slots * (kScanBwdPiece / kScanBwdKeep) * C * S);
+        s.keep_d = take(slots * (kScanBwdPiece / kScanBwdKeep) * C);
         s.part = take((size_t)scan_tiles(d.C, scan_bwd_channels((int)d.S), (int)d.G) * (size_t)tokens_of(d) * 2 * S);
     }
     s.total = at;
@@ -419,6 +421,8 @@ int gdr_selective_scan_bwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
     a.R = reinterpret_cast<float *>(call.base + s.R);
     a.sd = reinterpret_cast<float *>(call.base + s.sd);
     a.pd = reinterpret_cast<float *>(call.base + s.pd);
+    a.keep = reinterpret_cast<float *>(call.base + s.keep);
+    a.keep_d = reinterpret_cast<float *>(call.base + s.keep_d);
     a.part = reinterpret_cast<float *>(call.base + s.part);
     call.run(kKScanBwdEnds, [&] { return scan_bwd_ends(a, d.dtype, call.st); });
     call.run(kKScanJoin, [&] { return scan_join(a, true, call.st); });

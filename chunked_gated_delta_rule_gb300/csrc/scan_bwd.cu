@@ -10,11 +10,13 @@
 // Pieces of kScanBwdPiece tokens, all at once, whatever the sequences:
 //   1. one sweep leaves each piece's end from a zero start (E), its sum of time
 //      steps, and the gradient that its outputs send to its start (R): with P the
-//      product of the decays so far, R = sum_t P_t C_t dv_t;
+//      product of the decays so far, R = sum_t P_t C_t dv_t; and every 8 tokens the
+//      state and the sum of the time steps so far;
 //   2. the join turns ends into starts, forward for E and backward for R;
-//   3. the main pass runs the piece forward from its start, keeping the state in
-//      front of every 8 tokens, then backward 4 tokens at a time: their states are
-//      formed again in registers and the gradients follow from the last token to
+//   3. the main pass goes back through the piece 4 tokens at a time: what was left
+//      of the states, and what the piece's start adds to them (its decay follows
+//      from the sum of the time steps), are the states in front of them, theirs are
+//      formed again in registers, and the gradients follow from the last token to
 //      the first.
 //   4. sums over channels (dB, dC) and over pieces (dA, dD, dbias), in a fixed order.
 // What bounds the main pass is the number of instructions, most of them for the
@@ -22,15 +24,15 @@
 // channels for dB and dC.  A thread therefore has two channels of four states (the
 // channels' sums begin in its registers), and lanes fold eight values at once, so
 // that a shuffle carries a value that is still wanted.  The decays are formed a
-// third time on the way back: an exponential costs less than the registers.
+// second time on the way back: an exponential costs less than the registers.
 #include "scan.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kU = 8;                      // tokens from one kept state to the next
+constexpr int kU = kScanBwdKeep;           // tokens from one kept state to the next
 constexpr int kG = 4;                      // tokens whose states are in registers at once
-constexpr int kKeep = kScanBwdPiece / kU;  // states kept of a piece
+constexpr int kKeep = kScanBwdPiece / kU;  // of a piece; the first is the piece's start
 constexpr int kWarps = kNT / 32;
 
 // CH channels and STATES states of a thread: channels of a block, tokens of a tile, and what a
@@ -72,25 +74,25 @@ struct Stage {
     Row<T, V> x, dt, z, dy;
     Row<T, L::kVec> bc[L::kBCper];
 
-    template <bool GRAD>
     __device__ __forceinline__ void fetch(const ScanArgs &a, const Tile &tile, int64_t t0, int len) {
         const int tid = threadIdx.x, tr = tid / L::kRows, cv = tid % L::kRows * V;
         load_row<T, V>(x, a.x, a.xs, t0, tr, len, tile, cv, a.bytes);
         load_row<T, V>(dt, a.dt, a.dts, t0, tr, len, tile, cv, a.bytes);
-        if constexpr (GRAD) {
-            load_row<T, V>(dy, a.dy, a.ys, t0, tr, len, tile, cv, a.bytes);
-            if (a.z) load_row<T, V>(z, a.z, a.zs, t0, tr, len, tile, cv, a.bytes);
-        }
+        load_row<T, V>(dy, a.dy, a.ys, t0, tr, len, tile, cv, a.bytes);
+        if (a.z) load_row<T, V>(z, a.z, a.zs, t0, tr, len, tile, cv, a.bytes);
+        fetch_bc(a, tile, t0, len);
+    }
+    __device__ __forceinline__ void fetch_bc(const ScanArgs &a, const Tile &tile, int64_t t0, int len) {
+        const int tid = threadIdx.x;
 #pragma unroll
         for (int k = 0; k < L::kBCper; ++k) {
             const int id = k * kNT + tid, which = id / (kT * LPC), t = id / LPC % kT, v = id % LPC;
-            if (id < (GRAD ? L::kBC : kT * LPC))
+            if (id < L::kBC)
                 load_bc<T, L::kVec>(bc[k], which ? a.Cm : a.Bm, which ? a.cs : a.bs, tile.g, t0, t, len,
                                     L::kVec * v, a.S, a.bc_bytes);
         }
     }
     // sbc: [2][kT][kS]; bias: of the tile's channels, in the order of their places
-    template <bool GRAD>
     __device__ __forceinline__ void put(const ScanArgs &a, const float *bias, int len, float2 (*sdx)[kP],
                                         float (*sdv)[kP], float *sbc) const {
         const int tid = threadIdx.x, tr = tid / L::kRows, lv = tid % L::kRows;
@@ -105,18 +107,16 @@ struct Stage {
             if (tr >= len) d[j] = 0.f;  // past the end the states stay as they are
             sdx[tr][O::place(lv, j)] = make_float2(d[j], d[j] * fx[j]);
         }
-        if constexpr (GRAD) {
-            float g[V], fz[V], dv[V];
-            dy.widen(g);
-            if (a.z) z.widen(fz);
-            gate_grad<V>(g, fz, a.z != nullptr, dv);
+        float g[V], fz[V], dv[V];
+        dy.widen(g);
+        if (a.z) z.widen(fz);
+        gate_grad<V>(g, fz, a.z != nullptr, dv);
 #pragma unroll
-            for (int j = 0; j < V; ++j) sdv[tr][O::place(lv, j)] = dv[j];
-        }
+        for (int j = 0; j < V; ++j) sdv[tr][O::place(lv, j)] = dv[j];
 #pragma unroll
         for (int k = 0; k < L::kBCper; ++k) {
             const int id = k * kNT + tid;
-            if (id < (GRAD ? L::kBC : kT * LPC)) {
+            if (id < L::kBC) {
                 float f[L::kVec];
                 bc[k].widen(f);
 #pragma unroll
@@ -125,6 +125,53 @@ struct Stage {
                         make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
             }
         }
+    }
+};
+
+// The rows of a tile on their way to shared memory, each thread's to places of its own: there they
+// are when the tile is staged, and again when its gradients are written.
+template <typename T, typename L>
+struct Rows {
+    static constexpr int V = L::kV;
+    using R = Row<T, V>;
+    struct alignas(R::kBytes < 16 ? R::kBytes : 16) Slot {
+        uint8_t b[R::kBytes];
+    };
+    Slot own[4][kNT];  // x, dt, dy, z
+
+    __device__ __forceinline__ void ask(const ScanArgs &a, const Tile &tile, int64_t t0, int len) {
+        const int tid = threadIdx.x, tr = tid / L::kRows, cv = tid % L::kRows * V;
+        const int valid = tr < len ? max(0, min(V, tile.valid - cv)) : 0;
+        const void *const base[4] = {a.x, a.dt, a.dy, a.z};
+        const int64_t stride[4] = {a.xs, a.dts, a.ys, a.zs};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if (n == 3 && !a.z) break;
+            const T *from = (const T *)base[n] + (t0 + tr) * stride[n] + tile.c0 + cv;
+            if (valid == V && a.bytes >= R::kNeed) {
+                constexpr int kCopy = R::kNeed;
+                const uint32_t to = (uint32_t)__cvta_generic_to_shared(&own[n][tid]);
+#pragma unroll
+                for (int i = 0; i < R::kBytes / kCopy; ++i) {
+                    if constexpr (kCopy == 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * i),
+                                     "l"((const uint8_t *)from + 16 * i) : "memory");
+                    else
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kCopy)
+                                     : "memory");
+                }
+            } else {
+                R r;
+                r.load(from, a.bytes, valid);
+                r.store(reinterpret_cast<T *>(&own[n][tid]), 16, V);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ R row(int n) const {
+        R r;
+        r.load(reinterpret_cast<const T *>(&own[n][threadIdx.x]), 16, V);
+        return r;
     }
 };
 
@@ -138,28 +185,27 @@ __device__ __forceinline__ void load_channels(const ScanArgs &a, const Tile &til
     }
 }
 
-// 2 P values of A, as times_log2e, or of a state (none without an address), zeros past S and the
-// tile.
-template <int P, bool IS_A>
-__device__ __forceinline__ void load_states(const float *p, int64_t at, int s0, int S, bool mine, F2 (&to)[P]) {
-    float f[2 * P];
-#pragma unroll
-    for (int i = 0; i < 2 * P; ++i) {
-        f[i] = p && mine && s0 + i < S ? p[at + i] : 0.f;
-        if (IS_A) f[i] = times_log2e(f[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i) to[i] = f2(f[2 * i], f[2 * i + 1]);
+// K neighbouring states of a channel from s0 on; zeros past S, where `in` does not hold, and without
+// an address.
+template <int K>
+__device__ __forceinline__ void load_states(const float *p, int s0, int S, bool in, F2 (&to)[K / 2]) {
+    Row<float, K> r;
+    r.load(p, S % 4 ? 4 : 16, p && in ? max(0, min(K, S - s0)) : 0);
+    widen2<float, K>(r, to);
 }
-template <int P>
-__device__ __forceinline__ void store_states(float *p, int64_t at, int s0, int S, const F2 (&from)[P]) {
+template <int K>
+__device__ __forceinline__ void store_states(float *p, int s0, int S, const F2 (&from)[K / 2]) {
+    Row<float, K> r;
+    narrow2<float, K>(from, r);
+    r.store(p, S % 4 ? 4 : 16, max(0, min(K, S - s0)));
+}
+template <int K>
+__device__ __forceinline__ void load_A2(const ScanArgs &a, int64_t at, int s0, bool in, F2 (&to)[K / 2]) {
+    float f[K];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        float lo, hi;
-        split(from[i], lo, hi);
-        if (s0 + 2 * i < S) p[at + 2 * i] = lo;
-        if (s0 + 2 * i + 1 < S) p[at + 2 * i + 1] = hi;
-    }
+    for (int i = 0; i < K; ++i) f[i] = in && s0 + i < a.S ? times_log2e(a.A[at + i]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < K / 2; ++i) to[i] = f2(f[2 * i], f[2 * i + 1]);
 }
 
 // 1. E, sd and R of a piece.  A thread has eight states of a channel.
@@ -182,22 +228,27 @@ __global__ void __launch_bounds__(kNT) k_scan_bwd_ends(ScanArgs a, Tiles tiles) 
     const bool mine = ch < tile.valid;
     F2 A2[P], h[P], D[P], R[P];
     float total = 0.f;
-    load_states<P, true>(a.A, at_state, q * 8, a.S, mine, A2);
+    load_A2<8>(a, at_state, q * 8, mine, A2);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         h[i] = R[i] = f2(0.f);
         D[i] = f2(1.f);
     }
     Stage<T, L> s;
-    s.template fetch<true>(a, tile, p.t0, p.len);
+    s.fetch(a, tile, p.t0, p.len);
     load_channels<L>(a, tile, sch);
     __syncthreads();
     for (int at = 0; at < p.len; at += kT) {
-        s.template put<true>(a, sch, p.len - at, sdx, sdv, sbc);
+        s.put(a, sch, p.len - at, sdx, sdv, sbc);
         __syncthreads();
-        if (at + kT < p.len) s.template fetch<true>(a, tile, p.t0 + at + kT, p.len - at - kT);
+        if (at + kT < p.len) s.fetch(a, tile, p.t0 + at + kT, p.len - at - kT);
 #pragma unroll 4
         for (int t = 0; t < kT; ++t) {
+            if (t % kU == 0 && at + t && mine) {
+                const int64_t k = slot * kKeep + (at + t) / kU;
+                store_states<8>(a.keep + k * a.C * a.S + at_state, q * 8, a.S, h);
+                if (q == 0) a.keep_d[k * a.C + c] = total;
+            }
             const float2 d = sdx[t][cl];
             const F2 dd = f2(d.x), dx = f2(d.y), dv = f2(sdv[t][cl]);
             const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(sbc + t * L::kS + q * 8);
@@ -217,8 +268,8 @@ __global__ void __launch_bounds__(kNT) k_scan_bwd_ends(ScanArgs a, Tiles tiles) 
     }
     if (!mine) return;
     if (q == 0) a.sd[slot * a.C + c] = total;
-    store_states<P>(a.E + slot * a.C * a.S, at_state, q * 8, a.S, h);
-    store_states<P>(a.R + slot * a.C * a.S, at_state, q * 8, a.S, R);
+    store_states<8>(a.E + slot * a.C * a.S + at_state, q * 8, a.S, h);
+    store_states<8>(a.R + slot * a.C * a.S + at_state, q * 8, a.S, R);
 }
 
 // Sums of eight values over a channel's LPC lanes.  A lane ends with 8 / LPC of them (at least
@@ -269,16 +320,20 @@ __device__ __forceinline__ void fold_channels(float (&v)[8], int lane) {
     }
 }
 
-template <int LPC>
+template <typename T, int LPC>
 struct Smem {
     using L = Main<LPC>;
-    float4 keep[kKeep][2][kNT];        // states in front of every kU tokens
     float sbc[2 * L::kT * L::kS];
     float2 sdx[L::kT][L::kPitch];      // time step, and its product with x
     float2 res[L::kT][L::kPitch];      // <dh, B>, <e, A> / ln 2
     float sdv[L::kT][L::kPitch];       // dv, then <C, h>
     float red[kWarps][L::kT][2 * L::kS];
     float sch[2 * L::kC];
+    // a thread's own
+    Rows<T, L> rows[2];                // of this tile and the next
+    float acc[2][L::kV][kNT];          // dD and dbias of the channels that it loads
+    float4 start[2][kNT];              // what its states start from in the piece
+    float4 base[2][kNT];               // ... and in front of the last kept place
 };
 
 // Four states of two channels, forward by a token; y: <C, h> of the two.
@@ -295,13 +350,22 @@ __device__ __forceinline__ void step(const float4 &d, const ulonglong2 &B, const
     }
 }
 
+__device__ __forceinline__ void put_own(float4 &to, const F2 (&x)[2]) {
+    *reinterpret_cast<ulonglong2 *>(&to) = make_ulonglong2(x[0].v, x[1].v);
+}
+__device__ __forceinline__ void take_own(const float4 &from, F2 (&x)[2]) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&from);
+    x[0] = F2{v.x};
+    x[1] = F2{v.y};
+}
+
 // 3. The gradients of a piece.  At the end E's slot holds its part of dA.
 template <typename T, int LPC>
-__global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, Tiles tiles) {
+__global__ void __launch_bounds__(kNT, 4) k_scan_bwd(ScanArgs a, Tiles tiles) {
     using L = Main<LPC>;
     constexpr int kT = L::kT, V = L::kV, kC = L::kC, kS = L::kS;
     extern __shared__ __align__(16) uint8_t raw_smem[];
-    Smem<LPC> &sm = *reinterpret_cast<Smem<LPC> *>(raw_smem);
+    Smem<T, LPC> &sm = *reinterpret_cast<Smem<T, LPC> *>(raw_smem);
     const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC, lane = tid & 31, warp = tid >> 5;
     const uint32_t slot_id = blockIdx.x / tiles.all, tile_id = blockIdx.x - slot_id * tiles.all;
     const int64_t slot = slot_id;
@@ -333,59 +397,79 @@ __global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, Tiles tiles) {
     const int s0 = q * 4;
     int64_t at_state[2];
     bool mine[2];
-    F2 A2[2][2], h[2][2], dh[2][2], dA[2][2];
+    F2 A2[2][2], dh[2][2], dA[2][2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int ch = L::O::channel(2 * cl + k);
         at_state[k] = (tile.c0 + ch) * a.S + s0;
         mine[k] = ch < tile.valid;
-        load_states<2, true>(a.A, at_state[k], s0, a.S, mine[k], A2[k]);
-        load_states<2, false>(len ? a.E + slot * a.C * a.S : nullptr, at_state[k], s0, a.S, mine[k], h[k]);
-        load_states<2, false>(len ? a.R + slot * a.C * a.S : nullptr, at_state[k], s0, a.S, mine[k], dh[k]);
+        load_A2<4>(a, at_state[k], s0, mine[k], A2[k]);
+        F2 start[2];
+        load_states<4>(a.E + slot * a.C * a.S + at_state[k], s0, a.S, mine[k] && len, start);
+        put_own(sm.start[k][tid], start);
+        load_states<4>(a.R + slot * a.C * a.S + at_state[k], s0, a.S, mine[k] && len, dh[k]);
         dA[k][0] = dA[k][1] = f2(0.f);
     }
-    float dD[V], db[V];  // of the channels that the thread loads
 #pragma unroll
-    for (int j = 0; j < V; ++j) dD[j] = db[j] = 0.f;
+    for (int j = 0; j < V; ++j) sm.acc[0][j][tid] = sm.acc[1][j][tid] = 0.f;
     load_channels<L>(a, tile, sm.sch);
     auto B_at = [&](int t) { return *reinterpret_cast<const ulonglong2 *>(sm.sbc + t * kS + s0); };
     auto C_at = [&](int t) { return *reinterpret_cast<const ulonglong2 *>(sm.sbc + (kT + t) * kS + s0); };
     auto d_at = [&](int t) { return *reinterpret_cast<const float4 *>(&sm.sdx[t][2 * cl]); };
 
-    Stage<T, L> s;
-    if (len) s.template fetch<false>(a, tile, p.t0, len);
-    __syncthreads();
-    for (int at = 0; at < len; at += kT) {
-        s.template put<false>(a, sm.sch, len - at, sm.sdx, sm.sdv, sm.sbc);
-        __syncthreads();
-        if (at + kT < len) s.template fetch<false>(a, tile, p.t0 + at + kT, len - at - kT);
-        else s.template fetch<true>(a, tile, p.t0 + at, len - at);  // the backward's first
+    // What was kept in front of token `at` (not the first): the states without what the piece started
+    // from, and the sum of the time steps up to there.
+    auto kept = [&](int at, Row<float, 4> (&x)[2], float (&d)[2]) {
+        const int64_t i = slot * kKeep + at / kU;
 #pragma unroll
-        for (int u = 0; u < kT; u += kU) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                *reinterpret_cast<ulonglong2 *>(&sm.keep[(at + u) / kU][k][tid]) =
-                    make_ulonglong2(h[k][0].v, h[k][1].v);
-#pragma unroll
-            for (int t = u; t < u + kU; ++t) step<false>(d_at(t), B_at(t), ulonglong2{}, A2, h, nullptr);
+        for (int k = 0; k < 2; ++k) {
+            x[k].load(a.keep + i * a.C * a.S + at_state[k], a.S % 4 ? 4 : 16, mine[k] ? max(0, min(4, a.S - s0)) : 0);
+            d[k] = mine[k] ? a.keep_d[i * a.C + tile.c0 + L::O::channel(2 * cl + k)] : 0.f;
         }
-        __syncthreads();
+    };
+
+    Stage<T, L> s;
+    const int last = (len - 1) / kT * kT;
+    int now = 0;
+    if (len) {
+        sm.rows[0].ask(a, tile, p.t0 + last, len - last);
+        s.fetch_bc(a, tile, p.t0 + last, len - last);
     }
-    for (int at = (len - 1) / kT * kT; at >= 0 && len; at -= kT) {
-        const Row<T, V> cx = s.x, cd = s.dt, cz = s.z, cy = s.dy;
-        s.template put<true>(a, sm.sch, len - at, sm.sdx, sm.sdv, sm.sbc);
+    __syncthreads();
+    for (int at = last; at >= 0 && len; at -= kT, now ^= 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        s.x = sm.rows[now].row(0);
+        s.dt = sm.rows[now].row(1);
+        s.dy = sm.rows[now].row(2);
+        if (a.z) s.z = sm.rows[now].row(3);
+        s.put(a, sm.sch, len - at, sm.sdx, sm.sdv, sm.sbc);
         __syncthreads();
-        if (at) s.template fetch<true>(a, tile, p.t0 + at - kT, len - at + kT);
+        if (at) {
+            sm.rows[now ^ 1].ask(a, tile, p.t0 + at - kT, len - at + kT);
+            s.fetch_bc(a, tile, p.t0 + at - kT, len - at + kT);
+        }
 #pragma unroll 1
         for (int u = kT - kG; u >= 0; u -= kG) {
             F2 hs[kG][2][2], before[2][2];
+            const int from = at + u - u % kU;
+            if (u % kU && from) {
+                Row<float, 4> kx[2];
+                float kd[2];
+                kept(from, kx, kd);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sm.keep[(at + u) / kU][k][tid]);
-                before[k][0] = F2{x.x};
-                before[k][1] = F2{x.y};
+                for (int k = 0; k < 2; ++k) {
+                    F2 f[2];
+                    widen2<float, 4>(kx[k], f);
+                    take_own(sm.start[k][tid], before[k]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) before[k][j] = fma2(decay(f2(kd[k]), A2[k][j]), before[k][j], f[j]);
+                    put_own(sm.base[k][tid], before[k]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) take_own(from ? sm.base[k][tid] : sm.start[k][tid], before[k]);
             }
-            if (u % kU) {  // the second half of what was kept
+            if (u % kU) {
 #pragma unroll
                 for (int t = kG; t > 0; --t) step<false>(d_at(u - t), B_at(u - t), ulonglong2{}, A2, before, nullptr);
             }
@@ -465,10 +549,10 @@ __global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, Tiles tiles) {
         if (at + tr < len) {
             const int valid = max(0, min(V, tile.valid - cv));
             float x[V], raw[V], g[V], z[V], dv[V], ox[V], ot[V], oz[V];
-            cx.widen(x);
-            cd.widen(raw);
-            cy.widen(g);
-            if (a.z) cz.widen(z);
+            sm.rows[now].row(0).widen(x);
+            sm.rows[now].row(1).widen(raw);
+            sm.rows[now].row(2).widen(g);
+            if (a.z) sm.rows[now].row(3).widen(z);
             gate_grad<V>(g, z, a.z != nullptr, dv);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -478,8 +562,8 @@ __global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, Tiles tiles) {
                 ox[j] = fmaf(r.x, sm.sdx[tr][at_j].x, dv[j] * skip);
                 ot[j] = fmaf(r.x, x[j], r.y * kLn2);
                 if (a.softplus) ot[j] *= sigmoid_f(raw[j] + sm.sch[at_j]);
-                dD[j] = fmaf(dv[j], x[j], dD[j]);
-                db[j] += ot[j];
+                sm.acc[0][j][tid] = fmaf(dv[j], x[j], sm.acc[0][j][tid]);
+                sm.acc[1][j][tid] += ot[j];
                 if (a.z) {
                     const float sg = sigmoid_f(z[j]);
                     oz[j] = g[j] * fmaf(skip, x[j], sm.sdv[tr][at_j]) * sg * fmaf(z[j], 1.f - sg, 1.f);
@@ -508,22 +592,15 @@ __global__ void __launch_bounds__(kNT, 3) k_scan_bwd(ScanArgs a, Tiles tiles) {
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-        if (mine[k]) store_states<2>(a.E + slot * a.C * a.S, at_state[k], s0, a.S, dA[k]);
+        if (mine[k]) store_states<4>(a.E + slot * a.C * a.S + at_state[k], s0, a.S, dA[k]);
     // dD and dbias: the sums of the loading threads' rows, one behind the other
-    float(*sum)[2][kC] = reinterpret_cast<float(*)[2][kC]>(&sm.keep);  // [kT]
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        sum[tr][0][cv + j] = dD[j];
-        sum[tr][1][cv + j] = db[j];
-    }
     __syncthreads();
     for (int i = tid; i < 2 * kC; i += kNT) {
         const int w = i / kC, ch = i % kC;
         if (ch >= tile.valid) continue;
         float f = 0.f;
 #pragma unroll
-        for (int t = 0; t < kT; ++t) f += sum[t][w][ch];
+        for (int t = 0; t < kT; ++t) f += sm.acc[w][ch % V][t * L::kRows + ch / V];
         a.pd[(slot * 2 + w) * a.C + tile.c0 + ch] = f;
     }
 }
@@ -581,7 +658,7 @@ cudaError_t scan_bwd(const ScanArgs &a, int dtype, cudaStream_t st) {
         return scan_lanes(a.S, 4, [&](auto l) {
             using T = decltype(t);
             constexpr int LPC = decltype(l)::value < 2 ? 2 : decltype(l)::value;
-            constexpr size_t smem = sizeof(Smem<LPC>);
+            constexpr size_t smem = sizeof(Smem<T, LPC>);
             static std::atomic<uint64_t> done{0};
             cudaError_t e = once_a_device(done, [] {
                 return cudaFuncSetAttribute(k_scan_bwd<T, LPC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
