@@ -216,8 +216,9 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// Two FP32 values in a register pair: one instruction for both, at the same
-// rate of operations but half the issue slots, which these kernels are short of.
+// Two FP32 values in a register pair, worked on by one instruction.  It holds its scheduler's port
+// for two cycles, so what it saves is the rest of an instruction's cost: the scan's inner loop takes
+// 5.5 cycles a state with pairs and 6.2 without (8 states of a channel, measured alone).
 struct F2 {
     uint64_t v;
 };

@@ -6,19 +6,22 @@
 // with B_t and C_t shared by the channels of a group.  FP32 states and sums.
 //
 // Every (token, channel, state) takes one exponential (its decay depends on all
-// three) and five FP32 operations: the exponentials bound it, not the memory.
-// So the scan runs along the tokens as it is written, each state's chain in a
-// register, and whatever else a token needs is kept off the inner loop: a tile
-// of tokens is staged in shared memory with d_t and d_t x_t computed once a
-// channel, and the D and z terms are added when a tile's sums are written out.
-// The sums over a channel's states take part of a shuffle a token: LPC tokens
-// are folded at once.
+// three) and four FP32 operations, and no matrix product does them: the
+// schedulers' ports bound it, not the memory.  So the scan runs along the tokens
+// as it is written, each state's chain in a register, and whatever else a token
+// needs is kept off the inner loop: a tile of tokens is staged in shared memory
+// with d_t and d_t x_t computed once a channel, and the D and z terms are added
+// when a tile's sums are written out.  The sums over a channel's states take part
+// of a shuffle a token: LPC tokens are folded at once.
 //
 // With too few (sequence, channel) chains to fill the device the sequences are
 // cut into pieces: a first pass leaves each piece's end from a zero start, and
 // the sum of its time steps (the piece's decay is exp(A sum d), so no products
 // of decays are kept); a join turns the ends into starts; a second pass runs
-// the pieces from those.  That doubles the exponentials.
+// the pieces from those.  That takes the exponentials twice.  One sequence of 16K
+// tokens x 2048 channels x 16 states: 112, 6 and 163 us; the passes take 8.3 and 12
+// cycles a scheduler for 32 states, of which the instructions hold the port for
+// about 80% (a packed one for two cycles); the loop alone would take 5.5.
 #include "scan.cuh"
 
 namespace gdr {

@@ -19,12 +19,16 @@
 //      formed again in registers, and the gradients follow from the last token to
 //      the first.
 //   4. sums over channels (dB, dC) and over pieces (dA, dD, dbias), in a fixed order.
-// What bounds the main pass is the number of instructions, most of them for the
+// What bounds the main pass is the number of instructions, a third of them for the
 // sums across lanes: over a channel's states for dx, dd and <C, h>, over the
 // channels for dB and dC.  A thread therefore has two channels of four states (the
 // channels' sums begin in its registers), and lanes fold eight values at once, so
 // that a shuffle carries a value that is still wanted.  The decays are formed a
-// second time on the way back: an exponential costs less than the registers.
+// second time on the way back: an exponential costs less than the registers.  Four
+// blocks an SM, and rows on their way to shared memory while a tile is worked on,
+// keep the ports about 80% busy (8 x 2048 tokens x 2048 channels x 16 states: 680 us; with
+// three blocks and a forward sweep of its own in place of what the first pass
+// leaves, 846).
 #include "scan.cuh"
 
 namespace gdr {
@@ -53,8 +57,7 @@ struct Lay {
 
 template <int LPC>
 using Ends = Lay<LPC, 1, 8, LPC == 1 ? 8 : 16>;
-// Few tokens a tile: a thread then loads few channels of one, and what it has loaded stays in its
-// registers until the tile's gradients are written (loading it again took a quarter of the pass).
+// Few tokens a tile: a thread's own rows of two tiles then take little shared memory.
 template <int LPC>
 using Main = Lay<LPC, 2, 4, LPC == 16 ? 16 : kU>;
 
@@ -334,6 +337,8 @@ struct Smem {
     float acc[2][L::kV][kNT];          // dD and dbias of the channels that it loads
     float4 start[2][kNT];              // what its states start from in the piece
     float4 base[2][kNT];               // ... and in front of the last kept place
+    float4 kept[2][2][kNT];            // what was kept in front of the tile's last kU tokens, and the next's
+    float kept_d[2][2][kNT];
 };
 
 // Four states of two channels, forward by a token; y: <C, h> of the two.
@@ -417,14 +422,27 @@ __global__ void __launch_bounds__(kNT, 4) k_scan_bwd(ScanArgs a, Tiles tiles) {
     auto C_at = [&](int t) { return *reinterpret_cast<const ulonglong2 *>(sm.sbc + (kT + t) * kS + s0); };
     auto d_at = [&](int t) { return *reinterpret_cast<const float4 *>(&sm.sdx[t][2 * cl]); };
 
-    // What was kept in front of token `at` (not the first): the states without what the piece started
-    // from, and the sum of the time steps up to there.
-    auto kept = [&](int at, Row<float, 4> (&x)[2], float (&d)[2]) {
+    // What was kept in front of token `at` (none before the first) on its way: the states without what
+    // the piece started from, and the sum of the time steps up to there.
+    const int have = max(0, min(4, a.S - s0));
+    auto ask_kept = [&](int stage, int at) {
+        if (at <= 0) return;
         const int64_t i = slot * kKeep + at / kU;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            x[k].load(a.keep + i * a.C * a.S + at_state[k], a.S % 4 ? 4 : 16, mine[k] ? max(0, min(4, a.S - s0)) : 0);
-            d[k] = mine[k] ? a.keep_d[i * a.C + tile.c0 + L::O::channel(2 * cl + k)] : 0.f;
+            const float *from = a.keep + i * a.C * a.S + at_state[k];
+            const float *from_d = a.keep_d + i * a.C + tile.c0 + L::O::channel(2 * cl + k);
+            if (mine[k] && have == 4 && a.S % 4 == 0) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::
+                             "r"((uint32_t)__cvta_generic_to_shared(&sm.kept[stage][k][tid])), "l"(from) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::
+                             "r"((uint32_t)__cvta_generic_to_shared(&sm.kept_d[stage][k][tid])), "l"(from_d) : "memory");
+            } else {
+                Row<float, 4> x;
+                x.load(from, 4, mine[k] ? have : 0);
+                x.store(reinterpret_cast<float *>(&sm.kept[stage][k][tid]), 16, 4);
+                sm.kept_d[stage][k][tid] = mine[k] ? *from_d : 0.f;
+            }
         }
     };
 
@@ -432,6 +450,7 @@ __global__ void __launch_bounds__(kNT, 4) k_scan_bwd(ScanArgs a, Tiles tiles) {
     const int last = (len - 1) / kT * kT;
     int now = 0;
     if (len) {
+        ask_kept(0, last + kT - kU);
         sm.rows[0].ask(a, tile, p.t0 + last, len - last);
         s.fetch_bc(a, tile, p.t0 + last, len - last);
     }
@@ -445,6 +464,7 @@ __global__ void __launch_bounds__(kNT, 4) k_scan_bwd(ScanArgs a, Tiles tiles) {
         s.put(a, sm.sch, len - at, sm.sdx, sm.sdv, sm.sbc);
         __syncthreads();
         if (at) {
+            ask_kept(now ^ 1, at - kU);  // the last kU tokens of the tile before this
             sm.rows[now ^ 1].ask(a, tile, p.t0 + at - kT, len - at + kT);
             s.fetch_bc(a, tile, p.t0 + at - kT, len - at + kT);
         }
@@ -453,16 +473,18 @@ __global__ void __launch_bounds__(kNT, 4) k_scan_bwd(ScanArgs a, Tiles tiles) {
             F2 hs[kG][2][2], before[2][2];
             const int from = at + u - u % kU;
             if (u % kU && from) {
-                Row<float, 4> kx[2];
-                float kd[2];
-                kept(from, kx, kd);
+                if (u < kT - kU) {  // of a tile of more than kU tokens: the first of them
+                    ask_kept(now, from);
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     F2 f[2];
-                    widen2<float, 4>(kx[k], f);
+                    take_own(sm.kept[now][k][tid], f);
                     take_own(sm.start[k][tid], before[k]);
+                    const F2 d = f2(sm.kept_d[now][k][tid]);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) before[k][j] = fma2(decay(f2(kd[k]), A2[k][j]), before[k][j], f[j]);
+                    for (int j = 0; j < 2; ++j) before[k][j] = fma2(decay(d, A2[k][j]), before[k][j], f[j]);
                     put_own(sm.base[k][tid], before[k]);
                 }
             } else {
