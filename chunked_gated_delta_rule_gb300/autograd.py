@@ -14,6 +14,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import api, layer
 
@@ -80,6 +81,7 @@ class _ShortConv(torch.autograd.Function):
         return y, ht
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dht):
         x, weight, bias, h0, cu = ctx.saved_tensors
         activation, max_seqlen = ctx.args
@@ -114,6 +116,7 @@ class _SelectiveScan(torch.autograd.Function):
         return y, ht
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dht):
         x, dt, A, B, C, D, z, dt_bias, h0, cu = ctx.saved_tensors
         softplus, max_seqlen = ctx.args
@@ -147,6 +150,7 @@ class _RmsNorm(torch.autograd.Function):
         return y, r
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dr):
         r, weight = ctx.saved_tensors
         dx, dw = layer.gdr_rms_norm_bwd(_some(dy, r), r, weight, _dense(dr), eps=ctx.eps)

@@ -50,6 +50,13 @@ int64_t longest_of(const D &d) {
 }
 constexpr int64_t kFewTokens = 8;  // a sequence of so many is one thread's work
 
+// An output in the place of one of these inputs, which other threads still read.
+bool over(const void *out, std::initializer_list<const void *> in) {
+    for (const void *p : in)
+        if (out && out == p) return true;
+    return false;
+}
+
 // A call's launches, timed where the caller wants them, and its scratch.
 struct Call {
     LaunchRecorder rec;
@@ -290,6 +297,7 @@ int gdr_short_conv_fwd(const gdr_conv_dims *dims, const void *x, const void *wei
     const int64_t tokens = tokens_of(d), seqs = d.N > 0 ? d.N : d.B;
     if (!weight || (tokens > 0 && (!x || !y)) || (cu_seqlens != nullptr) != (d.N > 0)) return GDR_ERR_INVALID;
     if ((h0 || ht) ? n_states < (state_indices ? 1 : seqs) : state_indices != nullptr) return GDR_ERR_INVALID;
+    if (over(y, {x})) return GDR_ERR_INVALID;
     ConvArgs a = conv_args(d, x, weight, bias, cu_seqlens, opt);
     a.h0 = h0; a.ht = ht; a.y = y;
     a.n_states = n_states;
@@ -319,7 +327,7 @@ int gdr_short_conv_bwd(const gdr_conv_dims *dims, const void *x, const void *wei
     const gdr_conv_dims &d = *dims;
     const int64_t tokens = tokens_of(d);
     if (!weight || !dweight || (tokens > 0 && (!x || !dy || !dx)) || (dbias && !bias) ||
-        (cu_seqlens != nullptr) != (d.N > 0))
+        (cu_seqlens != nullptr) != (d.N > 0) || over(dx, {x, dy}))
         return GDR_ERR_INVALID;
     ConvArgs a = conv_args(d, x, weight, bias, cu_seqlens, opt);
     a.h0 = h0; a.dy = dy; a.dht = dht; a.dx = dx; a.dh0 = dh0;
@@ -355,6 +363,7 @@ int gdr_selective_scan_fwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
     if (!scan_inputs(d, in) || (tokens > 0 && !y) || (cu_seqlens != nullptr) != (d.N > 0) || n_segments < 0)
         return GDR_ERR_INVALID;
     if ((h0 || ht) ? n_states < (state_indices ? 1 : seqs) : state_indices != nullptr) return GDR_ERR_INVALID;
+    if (over(y, {in->x, in->dt, in->z, in->B, in->C})) return GDR_ERR_INVALID;
     ScanArgs a = scan_args(d, *in, cu_seqlens, opt);
     a.h0 = h0; a.ht = ht; a.y = y;
     a.n_states = n_states;
@@ -401,6 +410,8 @@ int gdr_selective_scan_bwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
         (tokens > 0 && (!dy || !out->dx || !out->ddt || !out->dB || !out->dC || (in->z && !out->dz))) ||
         (out->dD && !in->D) || (out->ddt_bias && !in->dt_bias) || (out->dz && !in->z))
         return GDR_ERR_INVALID;
+    for (const void *g : {out->dx, out->ddt, out->dz, out->dB, out->dC})
+        if (over(g, {in->x, in->dt, in->z, in->B, in->C, dy})) return GDR_ERR_INVALID;
     if (tokens > INT32_MAX * (int64_t)128 / (d.G * d.S)) return GDR_ERR_UNSUPPORTED;  // blocks of dB, dC
     ScanArgs a = scan_args(d, *in, cu_seqlens, opt);
     a.h0 = h0; a.dy = dy; a.dht = dht;
@@ -447,7 +458,7 @@ int gdr_rms_norm_fwd(const gdr_norm_dims *dims, const void *x, const void *resid
         (d.rows > 0 && (!x || !y || (quant && !scale))) || (!quant && scale))
         return GDR_ERR_INVALID;
     // two outputs in one place; values of other sizes over rows that are still to be read
-    if (y && (y == sum || (quant && (y == x || y == residual)))) return GDR_ERR_INVALID;
+    if (over(y, {sum}) || (quant && over(y, {x, residual}))) return GDR_ERR_INVALID;
     NormArgs a{};
     a.x = x; a.res = residual; a.r = sum; a.y = y; a.scale = scale;
     a.w = Param{weight, d.weight_dtype == GDR_F32};
@@ -456,6 +467,10 @@ int gdr_rms_norm_fwd(const gdr_norm_dims *dims, const void *x, const void *resid
     a.ress = stride_or(d.residual_stride, d.D);
     a.rs = stride_or(d.sum_stride, d.D);
     a.ys = stride_or(d.y_stride, d.D);
+    // rows in place, but not those of other rows
+    if ((over(sum, {x}) && a.rs != a.xs) || (over(sum, {residual}) && a.rs != a.ress) ||
+        (over(y, {x}) && a.ys != a.xs) || (over(y, {residual}) && a.ys != a.ress))
+        return GDR_ERR_INVALID;
     a.eps = d.eps;
     a.group = d.group;
     const uint64_t es = (uint64_t)size_of(d.dtype);

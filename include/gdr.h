@@ -453,6 +453,7 @@ size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cach
  * outputs and gradients; such a table is reported as GDR_ERR_SEQLENS all the
  * same.  Where offsets step back or leave [0, T], what the tokens get is
  * unspecified; nothing outside the tensors is read or written.
+ * No output may overlap an input, unless it says so.
  * opt may hold status, workspace (256-byte aligned) and the launch events; the
  * rest is zero.  Results are bit-identical from run to run.
  */
@@ -568,6 +569,7 @@ size_t gdr_selective_scan_bwd_workspace_size(const gdr_scan_dims *dims);
  *                     stores its rows: s = max|y| * (1 / 448) or (1 / 127), q =
  *                     round(y / s), 0 where s = 0; s = NaN and q = 0 where a y is
  *                     not finite.  y may be x in place (same dtype).
+ * In place means the same rows at the same stride.
  * FP32 sums: rows whose sum of squares passes FP32's range get zeros.
  */
 typedef struct gdr_norm_dims {

@@ -156,6 +156,22 @@ def test_bad_norms(lib):
     assert bwd(ok, opt=_with(api.gdr_options(), workspace=0x1000000, workspace_bytes=16)) == -6
 
 
+def test_outputs_in_the_place_of_inputs(lib):
+    assert conv_fwd(lib, conv(), y=1) == -1
+    assert conv_bwd(lib, conv(), dx=1) == -1 and conv_bwd(lib, conv(), dx=3) == -1
+    ins = scan_in()
+    for name in ("x", "dt", "z", "B", "C"):
+        assert scan_fwd(lib, scan(), y=getattr(ins, name) // 0x10000) == -1, name
+        for out in ("dx", "ddt", "dB", "dC", "dz"):
+            assert scan_bwd(lib, scan(), **{out: getattr(ins, name)}) == -1, (name, out)
+    assert scan_bwd(lib, scan(), dx=0x10000 * 9) == -1               # dy
+    # rows of the norm at another stride
+    assert norm_fwd(lib, norm(x_stride=256), y=1) == -1
+    assert norm_fwd(lib, norm(sum_stride=256), res=4, out=4) == -1
+    assert norm_fwd(lib, norm(sum_stride=256), res=4, out=1) == -1
+    assert norm_fwd(lib, norm(y_stride=256), res=4, out=6, y=4) == -1
+
+
 def test_scratch_sizes(lib):
     from chunked_gated_delta_rule_gb300 import layer
     conv_ws = layer.gdr_short_conv_bwd_workspace_size
