@@ -274,9 +274,14 @@ __global__ void __launch_bounds__(128) k_scan_join(ScanArgs a) {
 // Sequences of few tokens, straight from memory: what counts is the states' row, read and
 // written once.  A warp has 32 channels of a sequence: a lane four states of LPC of them (lane l
 // those of channels i (32 / LPC) + l / LPC), and with its own token values of channel l, whose time
-// step it forms for the others.
+// step it forms for the others.  What bounds it is a warp's chain of loads (the state's index, the
+// states, all before the first product), so blocks an SM count more than a few spilled registers, and
+// what does not wait for the index is asked for before it.  256 sequences x 4096 channels, cold, of 8 /
+// 16 / 32 / 64 states: 26 / 37 / 55 / 113 us (states alone at the memory's rate 10 / 20 / 40 / 79); as many
+// blocks as fit of themselves, and the loads in their order: 28 / 42 / 59 / 126.
+constexpr int step_blocks(int lpc) { return lpc <= 2 ? 7 : lpc == 4 ? 6 : lpc == 8 ? 4 : 2; }
 template <typename T, int LPC>
-__global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, Tiles tiles) {
+__global__ void __launch_bounds__(kNT, step_blocks(LPC)) k_scan_step(ScanArgs a, Tiles tiles) {
     constexpr int kCh = 32 / LPC;
     const int lane = threadIdx.x & 31, q = lane % LPC, cl = lane / LPC;
     const uint32_t id = blockIdx.x * (kNT / 32) + (threadIdx.x >> 5), seq = id / tiles.all;
@@ -294,16 +299,10 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, Tiles tiles) {
             y[t * a.ys] = from_f32<T>(0.f);
         return;
     }
-    int64_t s, len, row = 0;
+    int64_t s, len;
     seq_span(a.r, n, s, len);
-    if (a.h0 || a.ht) row = state_row(a.idx, a.n_states, n, a.r.status);
-    if (row < 0) {
-        if (mine)
-            for (int64_t t = s; t < s + len; ++t) y[t * a.ys] = from_f32<T>(0.f);
-        return;
-    }
     const int s0 = q * 4, wide = a.S % 4 ? 4 : a.st_bytes;
-    const int64_t at_state = (tile.c0 + cl) * a.S + s0, row_state = row * a.C * a.S + at_state;
+    const int64_t at_state = (tile.c0 + cl) * a.S + s0;
     const float bias = a.dt_bias && mine ? a.dt_bias[tile.c0 + lane] : 0.f;
     const float skip = a.D && mine ? a.D[tile.c0 + lane] : 0.f;
     auto run = [&](auto whole) {
@@ -312,12 +311,34 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, Tiles tiles) {
         const int states = W ? 4 : max(0, min(4, a.S - s0)), bytes = W ? 16 : wide;
         auto have = [&](int i) { return W || i * kCh + cl < tile.valid ? states : 0; };
         const int step = kCh * a.S;
+        Row<T, 4> rb, rc;
+        T rx, rd, rz;
+        auto fetch = [&](int64_t t) {
+            rb.load((const T *)a.Bm + t * a.bs[0] + tile.g * a.bs[1] + s0, W ? 16 : a.bc_bytes, states);
+            rc.load((const T *)a.Cm + t * a.cs[0] + tile.g * a.cs[1] + s0, W ? 16 : a.bc_bytes, states);
+            rx = rd = rz = from_f32<T>(0.f);
+            if (W || mine) {
+                rx = ((const T *)a.x)[t * a.xs + tile.c0 + lane];
+                rd = ((const T *)a.dt)[t * a.dts + tile.c0 + lane];
+                if (a.z) rz = ((const T *)a.z)[t * a.zs + tile.c0 + lane];
+            }
+        };
+        // what does not wait for the row's number is asked for before it
+        if (len > 0) fetch(s);
         Row<float, 4> A[LPC], h[LPC];
+#pragma unroll
+        for (int i = 0; i < LPC; ++i) A[i].load(a.A + at_state + i * step, bytes, have(i));
+        const int64_t row = a.h0 || a.ht ? state_row(a.idx, a.n_states, n, a.r.status) : 0;
+        if (row < 0) {
+            if (mine)
+                for (int64_t t = s; t < s + len; ++t) y[t * a.ys] = from_f32<T>(0.f);
+            return;
+        }
+        const int64_t row_state = row * a.C * a.S + at_state;
 #pragma unroll
         for (int i = 0; i < LPC; ++i) {
             h[i].zero();
             if (a.h0) h[i].load(a.h0 + row_state + i * step, bytes, have(i));
-            A[i].load(a.A + at_state + i * step, bytes, have(i));
         }
         float A2[LPC][4];
 #pragma unroll
@@ -327,21 +348,15 @@ __global__ void __launch_bounds__(kNT) k_scan_step(ScanArgs a, Tiles tiles) {
             for (int k = 0; k < 4; ++k) A2[i][k] = times_log2e(A2[i][k]);
         }
         for (int64_t t = s; t < s + len; ++t) {
-            Row<T, 4> rb, rc;
-            rb.load((const T *)a.Bm + t * a.bs[0] + tile.g * a.bs[1] + s0, W ? 16 : a.bc_bytes, states);
-            rc.load((const T *)a.Cm + t * a.cs[0] + tile.g * a.cs[1] + s0, W ? 16 : a.bc_bytes, states);
-            float x = 0.f, d = 0.f, z = 0.f, b[4], cc[4], v[LPC];
-            if (W || mine) {
-                x = to_f32(((const T *)a.x)[t * a.xs + tile.c0 + lane]);
-                d = to_f32(((const T *)a.dt)[t * a.dts + tile.c0 + lane]) + bias;
-                if (a.z) z = to_f32(((const T *)a.z)[t * a.zs + tile.c0 + lane]);
-            }
+            const float x = to_f32(rx), z = to_f32(rz);
+            float d = to_f32(rd) + bias, b[4], cc[4], v[LPC];
+            rb.widen(b);
+            rc.widen(cc);
+            if (t + 1 < s + len) fetch(t + 1);
             if (a.softplus) {
                 float unused;
                 split(softplus2(f2(d)), d, unused);
             }
-            rb.widen(b);
-            rc.widen(cc);
             const F2 b01 = f2(b[0], b[1]), b23 = f2(b[2], b[3]), c01 = f2(cc[0], cc[1]), c23 = f2(cc[2], cc[3]);
             const float dx = d * x;
 #pragma unroll
