@@ -118,7 +118,7 @@ int check_conv(const gdr_conv_dims *d) {
 // Tokens of a run, at most about `most`: long ones read few rows twice and leave few sums, and the
 // threads (one for each vector of channels of a run) fill the device a whole number of times.  64K
 // tokens x 2048 channels, forward at most 32 / 64 / 128 / 256: 102 / 103 / 111 / 113 us; backward with
-// its sums 64 / 128 / 256 / 512: 222 / 204 / 192 / 186 us.
+// its sums 64 / 128 / 256 / 512: 222 / 204 / 192 / 186 us (before its addresses were counted on: now 175).
 int run_of(int64_t tokens, int64_t vectors, int most) {
     const int64_t fill = (int64_t)device_sms() * kConvThreads, all = tokens * vectors;
     const int64_t waves = ceil_div(all, fill * most);

@@ -12,6 +12,11 @@
 // registers between the sum of squares and the product.  A warp takes a row
 // alone, without waiting for others, as long as there are rows enough to fill
 // the device; with fewer rows a block takes one.
+//
+// BF16, 64K rows of 2048 with a residual into E4M3 with scales a 128 columns: 151 us (940 MB,
+// 6.2 TB/s, 0.92 of what a copy reaches).  16K rows of 4096: forward 80 us, backward 102 and its
+// sums 12 (537 MB each; 6.7 and 5.3 TB/s: three rows and the sums leave a thread 128 registers,
+// so few rows are under way while others are summed).
 #include <cuda_fp8.h>
 
 #include "layer.cuh"
