@@ -48,7 +48,10 @@ int64_t longest_of(const D &d) {
     const int64_t len = d.max_len > 0 ? d.max_len : ceil_div(d.T, d.N);
     return len < d.T ? len : d.T;
 }
-constexpr int64_t kFewTokens = 8;  // a sequence of so many is one thread's work
+// A sequence of so many is one thread's (of the scan: one warp's) work.  256 sequences of 1 / 4 / 8 / 16
+// tokens x 2048 channels: convolution 13 / 15 / 19 / 24 us so, 41 / 24 / 22 / 26 in runs; scan 27 / 38 / 53 / 83
+// against 94 / 89 / 89 / 92; 16 sequences of 8 / 16: 16 / 20 against 20 / 20, and 17 / 22 against 17 / 18.
+constexpr int64_t kFewTokens = 8;
 
 // An output in the place of one of these inputs, which other threads still read.
 bool over(const void *out, std::initializer_list<const void *> in) {

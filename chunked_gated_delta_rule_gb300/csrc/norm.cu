@@ -13,10 +13,10 @@
 // alone, without waiting for others, as long as there are rows enough to fill
 // the device; with fewer rows a block takes one.
 //
-// BF16, 64K rows of 2048 with a residual into E4M3 with scales a 128 columns: 151 us (940 MB,
-// 6.2 TB/s, 0.92 of what a copy reaches).  16K rows of 4096: forward 80 us, backward 102 and its
-// sums 12 (537 MB each; 6.7 and 5.3 TB/s: three rows and the sums leave a thread 128 registers,
-// so few rows are under way while others are summed).
+// BF16, 64K rows of 2048 with a residual into E4M3 with scales a 128 columns: 150 us (940 MB,
+// 6.3 TB/s, 0.93 of what a copy reaches).  16K rows of 4096: forward 76 us, backward 102 and its
+// sums 10 (537 MB each; 7.1 TB/s, some of it left in L2, and 5.3: three rows and the sums leave a
+// thread 128 registers, so few rows are under way while others are summed).
 #include <cuda_fp8.h>
 
 #include "layer.cuh"
@@ -76,7 +76,7 @@ __device__ __forceinline__ float row_max(float x, float2 *sh) {
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void load_weights(const NormArgs &a, int64_t c, F2 (&w)[kPairs<V>]) {
+__device__ __forceinline__ void load_weights(const NormArgs &a, int c, F2 (&w)[kPairs<V>]) {
     if (!a.w.p || c >= a.D) {
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j) w[j] = f2(1.f);
@@ -142,20 +142,21 @@ struct Columns {
     int lane, warp, warps;
     __device__ __forceinline__ Columns()
         : lane(threadIdx.x & 31), warp(WARP ? 0 : threadIdx.x >> 5), warps(WARP ? 1 : blockDim.x >> 5) {}
-    __device__ __forceinline__ int64_t operator()(int i) const {
-        return (int64_t)((((i / kRun) * warps + warp) * kRun + i % kRun) * 32 + lane) * V;
+    __device__ __forceinline__ int first(int i) const {  // of the warp
+        return (((i / kRun) * warps + warp) * kRun + i % kRun) * 32 * V;
     }
+    __device__ __forceinline__ int operator()(int i) const { return first(i) + lane * V; }
 };
 
-// OUT: 0 the call's type, 1 E4M3, 2 8-bit integers.  V: values of a thread's load; D is a multiple.
-template <typename T, int V, int NV, bool WARP, int OUT>
+// OUT: 0 the call's type, 1 E4M3, 2 8-bit integers, GROUP: with a scale each 128 columns.  V: values of a thread's load; D is a multiple.
+template <typename T, int V, int NV, bool WARP, int OUT, bool GROUP>
 __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a) {
     constexpr int P = kPairs<V>;
     __shared__ float2 sh[32];
     const Columns<V, WARP> col;
     const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.rows) return;  // whole warps
-    const int64_t D = a.D;
+    const int D = (int)a.D;
     Row<T, V> r[NV];
     F2 sum2 = f2(0.f);
     {
@@ -163,12 +164,13 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a)
         Row<T, V> s[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = col(i);
+            const int c = col(i);
             r[i].load(x + c, 16, c < D ? V : 0);
             if (a.res) s[i].load(res + c, 16, c < D ? V : 0);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            if (col.first(i) >= D) continue;
             F2 f[P];
             widen2<T, V>(r[i], f);
             if (a.res) {
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a)
 #pragma unroll
                 for (int j = 0; j < P; ++j) f[j] = f[j] + g[j];
                 narrow2<T, V>(f, r[i]);
-                const int64_t c = col(i);
+                const int c = col(i);
                 if (c < D) r[i].store((T *)a.r + row * a.rs + c, 16, V);
                 widen2<T, V>(r[i], f);
             }
@@ -207,7 +209,8 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a)
     if constexpr (OUT == 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = col(i);
+            const int c = col(i);
+            if (col.first(i) >= D) continue;
             F2 y[P];
             normed(i, y);
             if (c < D) store2<T, V>((T *)a.y + row * a.ys + c, y);
@@ -215,35 +218,38 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm(NormArgs a)
     } else {
         // values past D are zeros and, in a row without a finite rstd, NaN: they do not count
         const float inv_max = OUT == 1 ? 1.f / 448.f : 1.f / 127.f;
-        const int64_t groups = a.group ? (D + 127) / 128 : 1;
+        constexpr int kRun = Columns<V, WARP>::kRun;
+        F2 y[NV][P];
         float most = 0.f;
-        if (!a.group) {
+        if constexpr (!GROUP) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                F2 y[P];
-                normed(i, y);
-                if (col(i) < D) most = largest(y, most);
+                if (col.first(i) >= D) continue;
+                normed(i, y[i]);
+                if (col(i) < D) most = largest(y[i], most);
             }
             most = row_max<WARP>(most, sh);
+            if (threadIdx.x % (WARP ? 32 : kMaxNarrow) == 0) a.scale[row] = scale_of(most, inv_max);
         }
-        constexpr int kRun = Columns<V, WARP>::kRun;
 #pragma unroll
         for (int i0 = 0; i0 < NV; i0 += kRun) {
-            F2 y[kRun][P];
-            float m = 0.f;
+            if (col.first(i0) >= D) continue;
+            if constexpr (GROUP) {
+                most = 0.f;
 #pragma unroll
-            for (int k = 0; k < kRun; ++k) {
-                normed(i0 + k, y[k]);
-                if (col(i0 + k) < D) m = largest(y[k], m);
+                for (int k = 0; k < kRun; ++k) {
+                    normed(i0 + k, y[i0 + k]);
+                    if (col(i0 + k) < D) most = largest(y[i0 + k], most);
+                }
+                most = lanes_max<(V >= 4 ? 128 / V : 32)>(most);
             }
-            if (a.group) most = lanes_max<(V >= 4 ? 128 / V : 32)>(m);
             const float s = scale_of(most, inv_max);
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
-                const int64_t c = col(i0 + k);
+                const int c = col(i0 + k);
                 if (c >= D) continue;
-                store8<V, OUT == 1>((uint8_t *)a.y + row * a.ys + c, y[k], s);
-                if (a.group ? c % 128 == 0 : c == 0) a.scale[row * groups + (a.group ? c / 128 : 0)] = s;
+                store8<V, OUT == 1>((uint8_t *)a.y + row * a.ys + c, y[i0 + k], s);
+                if (GROUP && c % 128 == 0) a.scale[row * ((D + 127) / 128) + c / 128] = s;
             }
         }
     }
@@ -257,7 +263,8 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
     extern __shared__ float acc[];  // WARP: [kWarpRows][D]
     __shared__ float2 sh[32];
     const Columns<V, WARP> col;
-    const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x, D = a.D;
+    const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
+    const int D = (int)a.D;
     F2 dw[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
         Row<T, V> r[NV], dy[NV], dr[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = col(i);
+            const int c = col(i);
             const int valid = c < D ? V : 0;
             r[i].load((const T *)a.r + row * a.rs + c, 16, valid);
             dy[i].load((const T *)a.dy + row * a.dys + c, 16, valid);
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
         const F2 rs = f2(rstd), k = f2(-sums.y * rstd / (float)D);  // -mean(w dy n)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = col(i);
+            const int c = col(i);
             F2 f[P], g[P], w[P], e[P];
             widen2<T, V>(r[i], f);
             widen2<T, V>(dy[i], g);
@@ -309,10 +316,10 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
         }
     }
     if (!a.dw) return;
-    float *to = WARP ? acc + (threadIdx.x >> 5) * D : a.part + blockIdx.x * D;
+    float *to = WARP ? acc + (threadIdx.x >> 5) * D : a.part + (int64_t)blockIdx.x * D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t c = col(i);
+        const int c = col(i);
         if (c < D) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
@@ -325,11 +332,11 @@ __global__ void __launch_bounds__(most_threads<T, V, WARP>()) k_norm_bwd(NormArg
     }
     if constexpr (WARP) {  // the block's warps join their sums
         __syncthreads();
-        for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
+        for (int c = threadIdx.x; c < D; c += blockDim.x) {
             float s = acc[c];
 #pragma unroll
             for (int k = 1; k < kWarpRows; ++k) s += acc[k * D + c];
-            a.part[blockIdx.x * D + c] = s;
+            a.part[(int64_t)blockIdx.x * D + c] = s;
         }
     }
 }
@@ -341,10 +348,11 @@ __global__ void __launch_bounds__(kColumnThreads) k_norm_weight(NormArgs a, int6
     if (threadIdx.x < 32 && c < a.D) a.dw[c] = s;
 }
 
-// Threads of a row (32: a warp) and vectors of a thread.  With rows enough a
-// warp takes up to `most` vectors; else a row is spread over more threads until
-// they fill the device or hold a vector each.  Narrow loads (rows off 16 bytes)
-// have a block a row and 4 or 16 of them a thread.
+// Threads of a row (32: a warp) and vectors of a thread.  A row takes as few warps as hold it with
+// `most` vectors a thread (E4M3, 16K rows of 4096 / 5120: 88 / 107 us with 4 vectors, 126 / 186 with 8,
+// 100 / 171 with 2); with few rows it is spread over more, up to a vector each, until they fill the
+// device (64 / 1024 / 4096 rows of 2048 into E4M3: 12 / 14 / 24 us, 18 / 18 / 30 without).  Narrow loads
+// (rows off 16 bytes) have a block a row and 4 or 16 of them a thread.
 struct Shape {
     int threads, nv;
 };
@@ -357,15 +365,14 @@ Shape shape_of(int64_t rows, int64_t D, int vec, int es, int most) {
         while (threads < kMaxNarrow && need() > 4) threads *= 2;
         return Shape{threads, need() > 4 ? 16 : 4};
     }
-    while (need() > most) threads *= 2;
-    while (need() > 1 && threads < kMaxBlock && rows * threads < (int64_t)device_sms() * 1024) threads *= 2;
+    if (need() > most) threads = (int)((all + 32 * most - 1) / (32 * most)) * 32;
+    while (need() > 1 && 2 * threads <= kMaxBlock && rows * threads < (int64_t)device_sms() * 1024) threads *= 2;
     int k = 1;
     while (k < need()) k *= 2;
     return Shape{threads, k};
 }
-constexpr int kMostFwd = 8;  // 16384 values: 512 threads of 8 vectors of 4 values
-// Backward a thread holds three rows and the sums: 32 values of each at most.
-constexpr int most_bwd(int es) { return es == 2 ? 4 : 8; }
+// Vectors of a thread at most: 32 values, so that 512 threads hold a row of 16384.
+constexpr int most_of(int es) { return es == 2 ? 4 : 8; }
 
 // Calls f(V, NV, WARP) as constants.
 template <typename T, int MOST, typename F>
@@ -388,13 +395,14 @@ cudaError_t with_shape(const NormArgs &a, const Shape &s, F f) {
     return go(std::integral_constant<int, MOST>{});
 }
 
-template <typename T, int OUT>
+template <typename T, int OUT, bool GROUP>
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
-    const Shape s = shape_of(a.rows, a.D, a.vec, sizeof(T), kMostFwd);
-    return with_shape<T, kMostFwd>(a, s, [&](auto v, auto nv, auto w) {
+    constexpr int kMost = most_of(sizeof(T));
+    const Shape s = shape_of(a.rows, a.D, a.vec, sizeof(T), kMost);
+    return with_shape<T, kMost>(a, s, [&](auto v, auto nv, auto w) {
         constexpr bool WARP = decltype(w)::value;
         const unsigned grid = (unsigned)(WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows);
-        k_norm<T, decltype(v)::value, decltype(nv)::value, WARP, OUT>
+        k_norm<T, decltype(v)::value, decltype(nv)::value, WARP, OUT, GROUP>
             <<<grid, WARP ? 32 * kWarpRows : s.threads, 0, st>>>(a);
         return cudaGetLastError();
     });
@@ -402,7 +410,7 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_norm_bwd(const NormArgs &a, int64_t blocks, cudaStream_t st) {
-    constexpr int kMost = most_bwd(sizeof(T));
+    constexpr int kMost = most_of(sizeof(T));
     const Shape s = shape_of(a.rows, a.D, a.vec, sizeof(T), kMost);
     return with_shape<T, kMost>(a, s, [&](auto v, auto nv, auto w) {
         constexpr bool WARP = decltype(w)::value;
@@ -418,9 +426,9 @@ cudaError_t launch_norm_bwd(const NormArgs &a, int64_t blocks, cudaStream_t st) 
 cudaError_t norm_fwd(const NormArgs &a, int dtype, int out_dtype, cudaStream_t st) {
     auto go = [&](auto t) {
         using T = decltype(t);
-        if (out_dtype == GDR_E4M3) return launch_norm<T, 1>(a, st);
-        if (out_dtype == GDR_I8) return launch_norm<T, 2>(a, st);
-        return launch_norm<T, 0>(a, st);
+        if (out_dtype == GDR_E4M3) return a.group ? launch_norm<T, 1, true>(a, st) : launch_norm<T, 1, false>(a, st);
+        if (out_dtype == GDR_I8) return a.group ? launch_norm<T, 2, true>(a, st) : launch_norm<T, 2, false>(a, st);
+        return launch_norm<T, 0, false>(a, st);
     };
     if (dtype == GDR_BF16) return go(__nv_bfloat16{});
     if (dtype == GDR_F16) return go(__half{});
@@ -430,7 +438,7 @@ cudaError_t norm_fwd(const NormArgs &a, int dtype, int out_dtype, cudaStream_t s
 // Blocks of the backward pass: as many as the device holds at once, or as there are rows.
 int64_t norm_bwd_blocks(int64_t rows, int64_t D, int vec, int dtype) {
     const int es = dtype == GDR_F32 ? 4 : 2;
-    const Shape s = shape_of(rows, D, vec, es, most_bwd(es));
+    const Shape s = shape_of(rows, D, vec, es, most_of(es));
     const int64_t all = s.threads == 32 ? (rows + kWarpRows - 1) / kWarpRows : rows;
     const int block = s.threads == 32 ? 32 * kWarpRows : s.threads;
     const int64_t fit = (int64_t)device_sms() * (block < kBwdThreads ? kBwdThreads / block : 1);

@@ -216,3 +216,12 @@ def test_autograd():
     for k in leaf:
         close("d" + k, leaf[k].grad, ref[k].grad)
     assert leaf["x"].grad.data_ptr() != leaf["res"].grad.data_ptr()
+
+
+@pytest.mark.parametrize("rows,D", [(1500, 1288), (1300, 2568), (1100, 5120), (500, 12296)])
+def test_rows_of_odd_numbers_of_warps(rows, D):
+    """Rows enough that a row has as few warps as hold it, not a power of two."""
+    test_forward(rows, D)
+    for fmt, group in ((E4M3, 0), (E4M3, 128), (I8, 0)):
+        test_eight_bits(rows, D, fmt, group)
+    test_gradients(rows, D)
