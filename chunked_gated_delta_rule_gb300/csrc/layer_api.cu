@@ -176,22 +176,40 @@ constexpr int64_t kPieceUnit = 32;  // tokens: whole tiles
 
 // Tokens of a piece of the forward scan, 0 for whole sequences.
 int64_t scan_piece(const gdr_scan_dims &d, int n_segments) {
-    const int64_t longest = longest_of(d), tokens = tokens_of(d);
+    const int64_t longest = longest_of(d);
     int64_t piece = 0;
     if (n_segments > 1) {
         piece = ceil_div(longest, n_segments);
     } else if (n_segments == 0) {
         const int64_t tiles = scan_tiles(d.C, scan_channels((int)d.S), (int)d.G), sms = device_sms();
-        const int64_t seqs = d.N > 0 ? d.N : d.B;
-        // Cycles of an SM.  Whole sequences: a token of the longest takes 187 where an SM has one
-        // block, 50 more for each other until they fill it, then 100 a block.  Pieces: 163 a token
-        // of a block in both passes, four blocks an SM, and the join.  (2048 channels of 16 states,
-        // whole / in pieces: one sequence of 16384 tokens 1530 / 278 us, 4 of 4096 389 / 287, 5 of
-        // 2048 245 / 191, 8 of 2048 245 / 287, 32 of 320 112 / 197.)
+        const int64_t tokens = tokens_of(d), seqs = d.N > 0 ? d.N : d.B;
+        const bool equal = tokens == seqs * longest;
+        // Cycles of an SM.  Whole sequences: a token of the longest takes 187 where an SM has one block,
+        // 50 more for each other until they fill it, then 100 a block.
         const int64_t mine = ceil_div(seqs * tiles, sms), slow = 187 + 50 * (mine - 1);
-        const int64_t whole = longest * (slow > 100 * mine ? slow : 100 * mine);
-        const int64_t cut = tokens * tiles / sms * 163 + 25000;
-        if (cut < whole) piece = ceil_div(tokens * tiles, sms * 4);
+        int64_t least = longest * (slow > 100 * mine ? slow : 100 * mine);
+        // Pieces that fill four blocks an SM a whole number of times: 163 a token of a block in both
+        // passes, less where a last round leaves blocks out; beginnings and ends; the join.
+        // (2048 channels, whole / in pieces.  16 states: one sequence of 16384 tokens 1530 / 278 us, 4 of
+        // 4096 389 / 287, 5 of 2048 245 / 191, 8 of 2048 245 / 287, 32 of 320 112 / 197.  8 states, 8 of 2048:
+        // 291 us, in 5 pieces each, 640 blocks where 608 fit, 282, in 10 225.  64 states, one of
+        // 16384: 2850 us; in pieces of 4096 tokens 1688, 3277 2174, 1171 1355, 863 1367.)
+        for (int64_t rounds = 1; rounds <= 4; ++rounds) {
+            const int64_t blocks = rounds * 4 * sms, fit = blocks / tiles;  // pieces
+            const int64_t each = equal ? fit / seqs : fit;
+            if (each < 1) continue;
+            const int64_t cut = ceil_div(ceil_div(equal ? longest : tokens, each), kPieceUnit) * kPieceUnit;
+            if (cut >= longest) continue;
+            const int64_t pieces = equal ? seqs * ceil_div(longest, cut) : ceil_div(tokens, cut);
+            const int64_t full = pieces * tiles / (4 * sms), left = ceil_div(pieces * tiles - full * 4 * sms, sms);
+            const int64_t last = left == 0 ? 0 : left * 163 > 305 + 82 * (left - 1) ? left * 163 : 305 + 82 * (left - 1);
+            const int64_t cycles = (full * 652 + last) * cut + (full + (left > 0)) * 12000 +
+                                   longest / cut * 300 + 25000;
+            if (cycles < least) {
+                least = cycles;
+                piece = cut;
+            }
+        }
     }
     if (piece == 0) return 0;
     piece = ceil_div(piece, kPieceUnit) * kPieceUnit;

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kNT, 4) k_scan(ScanArgs a, Tiles tiles) {
     constexpr int kT = L::kT, V = L::kV, kC = L::kC;
     using O = Order<V, L::kRows>;
     __shared__ float2 sdx[kT][kC + O::kPad];  // time step and its product with x; the sums over states
-    __shared__ float4 sbc[2][kT][LPC][2];
+    __shared__ float4 sbc[2][kT][2][LPC];  // lanes' halves side by side, so that eight lanes read all banks
     const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC;
     const uint32_t slot_id = blockIdx.x / tiles.all;
     const int64_t slot = slot_id;
@@ -140,9 +140,9 @@ __global__ void __launch_bounds__(kNT, 4) k_scan(ScanArgs a, Tiles tiles) {
             if (id < kLoadBC) {
                 float f[kPS];
                 nbc[k].widen(f);
-                float4 *to = sbc[id / (kT * LPC)][id / LPC % kT][id % LPC];
+                float4 *to = &sbc[id / (kT * LPC)][id / LPC % kT][0][id % LPC];
                 to[0] = make_float4(f[0], f[1], f[2], f[3]);
-                to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                to[LPC] = make_float4(f[4], f[5], f[6], f[7]);
             }
         }
         __syncthreads();
@@ -154,16 +154,16 @@ __global__ void __launch_bounds__(kNT, 4) k_scan(ScanArgs a, Tiles tiles) {
             for (int k = 0; k < LPC; ++k) {
                 const float2 d = sdx[t0 + k][cl];
                 const F2 dd = f2(d.x), dx = f2(d.y);
-                const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(sbc[0][t0 + k][q]);
-                const ulonglong2 *C = reinterpret_cast<const ulonglong2 *>(sbc[1][t0 + k][q]);
-                const ulonglong2 b0 = B[0], b1 = B[1];
+                const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(&sbc[0][t0 + k][0][q]);
+                const ulonglong2 *C = reinterpret_cast<const ulonglong2 *>(&sbc[1][t0 + k][0][q]);
+                const ulonglong2 b0 = B[0], b1 = B[LPC];
                 const F2 b[4] = {{b0.x}, {b0.y}, {b1.x}, {b1.y}};
 #pragma unroll
                 for (int i = 0; i < kPS / 2; ++i) h[i] = fma2(decay(dd, A2[i]), h[i], dx * b[i]);
                 if constexpr (SUM) {
                     total += d.x;
                 } else {
-                    const ulonglong2 c0 = C[0], c1 = C[1];
+                    const ulonglong2 c0 = C[0], c1 = C[LPC];
                     y[k] = both(fma2(h[0], F2{c0.x}, h[1] * F2{c0.y}) +
                                 fma2(h[2], F2{c1.x}, h[3] * F2{c1.y}));
                 }

@@ -95,7 +95,7 @@ struct Stage {
                                     L::kVec * v, a.S, a.bc_bytes);
         }
     }
-    // sbc: [2][kT][kS]; bias: of the tile's channels, in the order of their places
+    // sbc: [2][kT][kS], a row's vectors' first four states behind one another, then their last; bias: of the tile's channels, in the order of their places
     __device__ __forceinline__ void put(const ScanArgs &a, const float *bias, int len, float2 (*sdx)[kP],
                                         float (*sdv)[kP], float *sbc) const {
         const int tid = threadIdx.x, tr = tid / L::kRows, lv = tid % L::kRows;
@@ -124,7 +124,7 @@ struct Stage {
                 bc[k].widen(f);
 #pragma unroll
                 for (int i = 0; i < L::kVec; i += 4)
-                    *reinterpret_cast<float4 *>(sbc + id * L::kVec + i) =
+                    *reinterpret_cast<float4 *>(sbc + id / LPC * L::kS + i * LPC + id % LPC * 4) =
                         make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
             }
         }
@@ -254,9 +254,9 @@ __global__ void __launch_bounds__(kNT) k_scan_bwd_ends(ScanArgs a, Tiles tiles) 
             }
             const float2 d = sdx[t][cl];
             const F2 dd = f2(d.x), dx = f2(d.y), dv = f2(sdv[t][cl]);
-            const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(sbc + t * L::kS + q * 8);
-            const ulonglong2 *C = reinterpret_cast<const ulonglong2 *>(sbc + (kT + t) * L::kS + q * 8);
-            const ulonglong2 b0 = B[0], b1 = B[1], c0 = C[0], c1 = C[1];
+            const ulonglong2 *B = reinterpret_cast<const ulonglong2 *>(sbc + t * L::kS + q * 4);
+            const ulonglong2 *C = reinterpret_cast<const ulonglong2 *>(sbc + (kT + t) * L::kS + q * 4);
+            const ulonglong2 b0 = B[0], b1 = B[LPC], c0 = C[0], c1 = C[LPC];
             const F2 b[P] = {{b0.x}, {b0.y}, {b1.x}, {b1.y}}, cc[P] = {{c0.x}, {c0.y}, {c1.x}, {c1.y}};
 #pragma unroll
             for (int i = 0; i < P; ++i) {
