@@ -333,8 +333,8 @@ def _row_stride(name, t):
             continue
         if step is None:
             step = need = s
-        elif s != need:
-            raise ValueError(f"{name}: rows must lie at one stride")
+        if s != need or step < 1:  # 0: a broadcast row, which is one row and not as many as there are
+            raise ValueError(f"{name}: rows must lie at one stride, and not in one place")
         need *= n
     return shape[-1] if step is None else step
 
