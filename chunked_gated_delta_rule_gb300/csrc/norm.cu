@@ -111,9 +111,11 @@ __device__ __forceinline__ void store8(uint8_t *p, const F2 (&y)[kPairs<V>], flo
                 q = fma2(nr, fma2(q, s2, minus), q);
                 split(q, lo, hi);
             } else {
+                // a scale of a few of FP32's least units may be a third too small
+                constexpr float kMost = E4M3 ? 448.f : 127.f;
                 split(y[i], lo, hi);
-                lo = __fdiv_rn(lo, s);
-                hi = __fdiv_rn(hi, s);
+                lo = fminf(fmaxf(__fdiv_rn(lo, s), -kMost), kMost);
+                hi = fminf(fmaxf(__fdiv_rn(hi, s), -kMost), kMost);
             }
             uint32_t two;
             if constexpr (E4M3) {
