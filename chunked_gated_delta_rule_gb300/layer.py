@@ -308,7 +308,7 @@ def gdr_selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, cu_
     def new(like):
         return None if like is None else _new(like)
 
-    dh0 = torch.empty(shape, device=x.device) if want_dh0 else None
+    dh0 = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dh0 else None
     out = (new(x), new(dt), new(A), new(B), new(C), new(D), new(z), new(dt_bias), dh0)
     grads = gdr_scan_grads(*[None if t is None else t.data_ptr() for t in out])
     _call(lib.gdr_selective_scan_bwd, index, stream,
@@ -383,7 +383,7 @@ def gdr_rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-6, dtype=None, gro
     if out is not own:
         want = shape[:-1] + ((D + 127) // 128,) if group else shape[:-1]
         if scale is None:
-            scale = torch.empty(want, device=x.device)
+            scale = torch.empty(want, dtype=torch.float32, device=x.device)
         ps = _like(index, torch.float32, want, "scale", scale, True)
     elif scale is not None:
         raise ValueError("scale belongs to a quantised y")
@@ -408,7 +408,7 @@ def gdr_rms_norm_bwd(dy, r, weight=None, dr=None, *, eps=1e-6, workspace=None, s
     g, gr = _like(index, dtype, shape, "dy", dy), _like(index, dtype, shape, "dr", dr)
     opt = _options(index, workspace, None, timer)
     dx = _new(r)
-    dw = None if weight is None else torch.empty(D, device=r.device)
+    dw = None if weight is None else torch.empty(D, dtype=torch.float32, device=r.device)
     dims = gdr_norm_dims(r.numel() // D if D else 0, D, code, wd, code, 0, eps, _row_stride("r", r),
                          0 if dr is None else _row_stride("dr", dr), 0, _row_stride("dy", dy))
     _call(lib.gdr_rms_norm_bwd, index, stream, (dy, r, weight, dr, dx, dw, workspace), dims,

@@ -71,3 +71,52 @@ def test_eight_bits_of_least_units(fmt, D, group):
                         v_scale=scales[1])
     assert torch.equal(scales[0].transpose(1, 2).reshape(scale.shape), scale)
     assert torch.equal(cache[0].view(torch.uint8).reshape(rows, D), q.view(torch.uint8))
+
+
+def scan_inputs(lens=(70, 1, 0, 130), C=96, S=16, seed=0):
+    T = sum(lens)
+    cu = torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32).cuda()
+    bc = randn(1, T, 2, 1, S, seed=seed)
+    return dict(x=randn(1, T, C, seed=seed + 1), dt=randn(1, T, C, seed=seed + 2) - 2.0,
+                A=-torch.exp(randn(C, S, seed=seed + 3)), B=bc[:, :, 0], C=bc[:, :, 1],
+                D=randn(C, seed=seed + 4), z=randn(1, T, C, seed=seed + 5), dt_bias=randn(C, seed=seed + 6),
+                cu_seqlens=cu, h0=randn(len(lens), C, S, seed=seed + 7))
+
+
+def every_call(s, w, taps, dy, dht, dhc, **kw):
+    """Each of the six calls on the same inputs; the outputs by name."""
+    x, cu = s["x"], s["cu_seqlens"]
+    out = {}
+    out["conv y"], out["conv ht"] = gdr.gdr_short_conv_fwd(x, taps, s["D"], cu, output_final_state=True, **kw)
+    for name, t in zip(("dx", "dweight", "dbias", "dh0"), gdr.gdr_short_conv_bwd(
+            x, taps, dy, s["D"], cu, None, dhc, want_dh0=True, **kw)):
+        out["conv " + name] = t
+    out["scan y"], out["scan ht"] = gdr.gdr_selective_scan_fwd(**s, **kw)
+    for name, t in zip(("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"),
+                       gdr.gdr_selective_scan_bwd(**s, dy=dy, dht=dht, want_dh0=True, **kw)):
+        out["scan " + name] = t
+    for name, t in zip("y r".split(), gdr.gdr_rms_norm_fwd(x, w, dy, **kw)):
+        out["norm " + name] = t
+    q, _, out["norm scale"] = gdr.gdr_rms_norm_fwd(x, w, dtype=torch.float8_e4m3fn, **kw)
+    out["norm q"] = q.view(torch.uint8)
+    out["norm dx"], out["norm dweight"] = gdr.gdr_rms_norm_bwd(dy, x, w, **kw)
+    return out
+
+
+def call_inputs():
+    s = scan_inputs()
+    return (s, randn(96, seed=20), randn(96, 4, seed=21), randn(*s["x"].shape, seed=22),
+            randn(*s["h0"].shape, seed=23), randn(4, 3, 96, seed=24))
+
+
+@pytest.mark.parametrize("default", [torch.float64, torch.bfloat16, torch.float16], ids=str)
+def test_another_default_dtype(default):
+    args = call_inputs()
+    want = every_call(*args)
+    torch.set_default_dtype(default)
+    try:
+        got = every_call(*args)
+    finally:
+        torch.set_default_dtype(torch.float32)
+    for k in want:
+        assert got[k].dtype == want[k].dtype and torch.equal(got[k], want[k]), k

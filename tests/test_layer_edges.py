@@ -26,3 +26,15 @@ def test_row_strides():
                     (torch.zeros(0, D), 0), (torch.zeros(1, D).expand(1, D), 0),
                     (torch.zeros(1, 1, D).expand(1, 1, D), 0)):
         assert layer._row_stride("x", t) == step, (t.shape, t.stride())
+
+
+def test_outputs_in_32_bits_whatever_the_default():
+    """What the library writes in FP32 is made as FP32 (with another default dtype it would be
+    written past its end): every torch.empty of the binding names its type."""
+    import ast
+    import inspect
+    calls = [n for n in ast.walk(ast.parse(inspect.getsource(layer))) if isinstance(n, ast.Call)
+             and isinstance(n.func, ast.Attribute) and n.func.attr in ("empty", "zeros", "ones", "full")]
+    assert calls
+    for n in calls:
+        assert any(k.arg == "dtype" for k in n.keywords), f"line {n.lineno}"
