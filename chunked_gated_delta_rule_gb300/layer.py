@@ -42,11 +42,24 @@ def _like(index, dtype, shape, name, t, contiguous=False):
     return t.data_ptr()
 
 
-def _new(like):
-    """A contiguous tensor of the same shape, type and device."""
-    if like.is_contiguous():
+def _empty(shape, dtype, device, stream):
+    """A new tensor that a call on ``stream`` (None: the current one) writes.  Its memory is that
+    stream's: what the current one has let go may still be in use there, which ``stream`` does not
+    wait for.  The current stream, where the caller goes on, may use it and let it go as its own."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if t.numel():
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _new(like, stream):
+    """A contiguous tensor of the same shape, type and device, for a call on ``stream``."""
+    if stream is None and like.is_contiguous():
         return torch.empty_like(like)  # the quickest of torch's ways
-    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return _empty(like.shape, like.dtype, like.device, stream)
 
 
 def _stride(name, t):
@@ -124,7 +137,7 @@ def _call(fn, index, stream, tensors, *args):
                 t.record_stream(stream)
 
 
-def _states(index, nseq, tail, dtype, h0, ht, state, state_indices, want, x):
+def _states(index, nseq, tail, dtype, h0, ht, state, state_indices, want, x, stream):
     """(ht, rows, addresses of h0, ht and the indices) of a call that goes on from ``h0`` [N, ...],
     or moves the pool ``state`` on in place."""
     if state is not None:
@@ -140,7 +153,7 @@ def _states(index, nseq, tail, dtype, h0, ht, state, state_indices, want, x):
         raise ValueError("state_indices belong to state")
     shape = (nseq,) + tail
     if ht is None and want:
-        ht = torch.empty(shape, dtype=dtype, device=x.device)
+        ht = _empty(shape, dtype, x.device, stream)
     return (ht, nseq, _like(index, dtype, shape, "h0", h0, True),
             _like(index, dtype, shape, "ht", ht, True), None)
 
@@ -191,15 +204,15 @@ def gdr_short_conv_fwd(x, weight, bias=None, cu_seqlens=None, h0=None, *, activa
                                              activation, max_seqlen)
     opt = _options(index, None, status, timer)
     if y is None:
-        y = _new(x)
+        y = _new(x, stream)
     else:
         _like(index, x.dtype, x.shape, "y", y)
         dims.y_stride = _stride("y", y)
     ht, rows, p0, pt, idx = _states(index, nseq, (weight.shape[1] - 1, x.shape[2]), x.dtype, h0, ht,
-                                    state, state_indices, output_final_state, x)
+                                    state, state_indices, output_final_state, x, stream)
     _call(lib.gdr_short_conv_fwd, index, stream,
-          (x, weight, bias, cu_seqlens, h0, ht, state_indices, y), dims, x.data_ptr(), w, b, cu, p0,
-          pt, rows, idx, y.data_ptr(), opt)
+          (x, weight, bias, cu_seqlens, h0, ht, state_indices, y), dims, x.data_ptr(), w, b,
+          cu, p0, pt, rows, idx, y.data_ptr(), opt)
     return y, ht
 
 
@@ -218,10 +231,10 @@ def gdr_short_conv_bwd(x, weight, dy, bias=None, cu_seqlens=None, h0=None, dht=N
     tail = (nseq, weight.shape[1] - 1, x.shape[2])
     p0 = _like(index, x.dtype, tail, "h0", h0, True)
     gt = _like(index, x.dtype, tail, "dht", dht, True)
-    dx = _new(x)
-    dw = torch.empty(weight.shape, dtype=torch.float32, device=x.device)
-    db = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=x.device)
-    dh0 = torch.empty(tail, dtype=x.dtype, device=x.device) if want_dh0 else None
+    dx = _new(x, stream)
+    dw = _empty(weight.shape, torch.float32, x.device, stream)
+    db = None if bias is None else _empty(bias.shape, torch.float32, x.device, stream)
+    dh0 = _empty(tail, x.dtype, x.device, stream) if want_dh0 else None
     _call(lib.gdr_short_conv_bwd, index, stream,
           (x, weight, dy, bias, cu_seqlens, h0, dht, dx, dw, db, dh0, workspace), dims,
           x.data_ptr(), w, b, cu, p0, g, gt, dx.data_ptr(), dw.data_ptr(),
@@ -277,15 +290,15 @@ def gdr_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seql
                                                 dt_bias, cu_seqlens, softplus, max_seqlen)
     opt = _options(index, workspace, status, timer)
     if y is None:
-        y = _new(x)
+        y = _new(x, stream)
     else:
         _like(index, x.dtype, x.shape, "y", y)
         dims.y_stride = _stride("y", y)
     ht, rows, p0, pt, idx = _states(index, nseq, (x.shape[2], A.shape[1]), torch.float32, h0, ht,
-                                    state, state_indices, output_final_state, x)
+                                    state, state_indices, output_final_state, x, stream)
     _call(lib.gdr_selective_scan_fwd, index, stream,
-          (x, dt, A, B, C, D, z, dt_bias, cu_seqlens, h0, ht, state_indices, y, workspace), dims,
-          tensors, cu, p0, pt, rows, idx, y.data_ptr(), n_segments, opt)
+          (x, dt, A, B, C, D, z, dt_bias, cu_seqlens, h0, ht, state_indices, y, workspace),
+          dims, tensors, cu, p0, pt, rows, idx, y.data_ptr(), n_segments, opt)
     return y, ht
 
 
@@ -306,14 +319,14 @@ def gdr_selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, cu_
     gt = _like(index, torch.float32, shape, "dht", dht, True)
 
     def new(like):
-        return None if like is None else _new(like)
+        return None if like is None else _new(like, stream)
 
-    dh0 = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dh0 else None
+    dh0 = _empty(shape, torch.float32, x.device, stream) if want_dh0 else None
     out = (new(x), new(dt), new(A), new(B), new(C), new(D), new(z), new(dt_bias), dh0)
     grads = gdr_scan_grads(*[None if t is None else t.data_ptr() for t in out])
     _call(lib.gdr_selective_scan_bwd, index, stream,
-          (x, dt, A, B, C, dy, D, z, dt_bias, cu_seqlens, h0, dht, workspace) + out, dims, tensors,
-          cu, p0, g, gt, grads, opt)
+          (x, dt, A, B, C, dy, D, z, dt_bias, cu_seqlens, h0, dht, workspace) + out, dims,
+          tensors, cu, p0, g, gt, grads, opt)
     return out
 
 
@@ -362,7 +375,7 @@ def gdr_rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-6, dtype=None, gro
         raise ValueError("group is 0, or 128 where y is quantised")
     wd, w = (code, None) if weight is None else _weight(index, own, (D,), weight)
     if y is None:
-        y = _new(x) if out is own else torch.empty(shape, dtype=out, device=x.device)
+        y = _new(x, stream) if out is own else _empty(shape, out, x.device, stream)
         ys = 0
     else:
         _like(index, out, shape, "y", y)
@@ -376,14 +389,14 @@ def gdr_rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-6, dtype=None, gro
         pr = _like(index, own, shape, "residual", residual)
         rs = _row_stride("residual", residual)
         if residual_out is None:
-            residual_out = _new(x)
+            residual_out = _new(x, stream)
         po = _like(index, own, shape, "residual_out", residual_out)
         os = _row_stride("residual_out", residual_out)
     ps = None
     if out is not own:
         want = shape[:-1] + ((D + 127) // 128,) if group else shape[:-1]
         if scale is None:
-            scale = torch.empty(want, dtype=torch.float32, device=x.device)
+            scale = _empty(want, torch.float32, x.device, stream)
         ps = _like(index, torch.float32, want, "scale", scale, True)
     elif scale is not None:
         raise ValueError("scale belongs to a quantised y")
@@ -407,8 +420,8 @@ def gdr_rms_norm_bwd(dy, r, weight=None, dr=None, *, eps=1e-6, workspace=None, s
     wd, w = (code, None) if weight is None else _weight(index, dtype, (D,), weight)
     g, gr = _like(index, dtype, shape, "dy", dy), _like(index, dtype, shape, "dr", dr)
     opt = _options(index, workspace, None, timer)
-    dx = _new(r)
-    dw = None if weight is None else torch.empty(D, dtype=torch.float32, device=r.device)
+    dx = _new(r, stream)
+    dw = None if weight is None else _empty((D,), torch.float32, r.device, stream)
     dims = gdr_norm_dims(r.numel() // D if D else 0, D, code, wd, code, 0, eps, _row_stride("r", r),
                          0 if dr is None else _row_stride("dr", dr), 0, _row_stride("dy", dy))
     _call(lib.gdr_rms_norm_bwd, index, stream, (dy, r, weight, dr, dx, dw, workspace), dims,

@@ -120,3 +120,90 @@ def test_another_default_dtype(default):
         torch.set_default_dtype(torch.float32)
     for k in want:
         assert got[k].dtype == want[k].dtype and torch.equal(got[k], want[k]), k
+
+
+SLEEP = 200_000_000  # cycles that a stream does nothing for: some 100 ms
+
+
+def warm(args):
+    """A side stream that has memory of its own, so that no call on it waits for the device to get
+    some; and what the calls give on the current one."""
+    side, want = torch.cuda.Stream(), every_call(*args)
+    torch.cuda.synchronize()
+    every_call(*args, stream=side)
+    torch.cuda.synchronize()
+    return side, want
+
+
+def spans(tensors):
+    return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors]
+
+
+def same(got, want):
+    torch.cuda.synchronize()
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+
+
+def test_outputs_on_another_stream_are_not_in_memory_that_this_one_has_let_go():
+    """Memory let go on the current stream may still be written there, which a call on another
+    stream does not wait for."""
+    args = call_inputs()
+    side, want = warm(args)
+    gone = [torch.empty_like(t) for t in want.values()]
+    old = spans(gone)
+    torch.cuda._sleep(SLEEP)
+    for t in gone:
+        t.fill_(77)
+    del gone, t
+    got = every_call(*args, stream=side)
+    for a, b in spans(got.values()):
+        assert not any(a < d and c < b for c, d in old)
+    same(got, want)
+
+
+def test_inputs_let_go_while_another_stream_has_yet_to_read_them():
+    args = call_inputs()
+    side, want = warm(args)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SLEEP)
+    shapes = [t.shape for t in list(args[0].values()) + list(args[1:]) if t.is_floating_point()]
+    got = every_call(*args, stream=side)
+    del args
+    for s in shapes:
+        torch.full(s, float("nan"), device="cuda")
+    junk = [torch.full(s, float("nan"), device="cuda") for s in shapes]
+    same(got, want)
+    assert len(junk) == len(shapes)
+
+
+def test_outputs_let_go_while_the_current_stream_has_yet_to_read_them():
+    args, other = call_inputs(), list(call_inputs())
+    side, want = warm(args)
+    other[0] = scan_inputs(seed=40)
+    here = torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    got = every_call(*args, stream=side)
+    here.wait_stream(side)
+    torch.cuda._sleep(SLEEP)
+    kept = {k: t.clone() for k, t in got.items()}
+    del got
+    again = every_call(*other, stream=side)
+    same(kept, want)
+    assert not torch.equal(again["scan y"], want["scan y"])
+
+
+def test_captured_on_another_stream():
+    args = call_inputs()
+    side, want = warm(args)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = every_call(*args, stream=side)
+        here.wait_stream(side)
+    for _ in range(2):
+        for t in got.values():
+            t.zero_()
+        graph.replay()
+        same(got, want)
