@@ -211,7 +211,7 @@ def gdr_short_conv_fwd(x, weight, bias=None, cu_seqlens=None, h0=None, *, activa
     ht, rows, p0, pt, idx = _states(index, nseq, (weight.shape[1] - 1, x.shape[2]), x.dtype, h0, ht,
                                     state, state_indices, output_final_state, x, stream)
     _call(lib.gdr_short_conv_fwd, index, stream,
-          (x, weight, bias, cu_seqlens, h0, ht, state_indices, y), dims, x.data_ptr(), w, b,
+          (x, weight, bias, cu_seqlens, h0, ht, state_indices, y, status), dims, x.data_ptr(), w, b,
           cu, p0, pt, rows, idx, y.data_ptr(), opt)
     return y, ht
 
@@ -236,7 +236,7 @@ def gdr_short_conv_bwd(x, weight, dy, bias=None, cu_seqlens=None, h0=None, dht=N
     db = None if bias is None else _empty(bias.shape, torch.float32, x.device, stream)
     dh0 = _empty(tail, x.dtype, x.device, stream) if want_dh0 else None
     _call(lib.gdr_short_conv_bwd, index, stream,
-          (x, weight, dy, bias, cu_seqlens, h0, dht, dx, dw, db, dh0, workspace), dims,
+          (x, weight, dy, bias, cu_seqlens, h0, dht, dx, dw, db, dh0, workspace, status), dims,
           x.data_ptr(), w, b, cu, p0, g, gt, dx.data_ptr(), dw.data_ptr(),
           None if db is None else db.data_ptr(), None if dh0 is None else dh0.data_ptr(), opt)
     return dx, dw, db, dh0
@@ -297,7 +297,7 @@ def gdr_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seql
     ht, rows, p0, pt, idx = _states(index, nseq, (x.shape[2], A.shape[1]), torch.float32, h0, ht,
                                     state, state_indices, output_final_state, x, stream)
     _call(lib.gdr_selective_scan_fwd, index, stream,
-          (x, dt, A, B, C, D, z, dt_bias, cu_seqlens, h0, ht, state_indices, y, workspace),
+          (x, dt, A, B, C, D, z, dt_bias, cu_seqlens, h0, ht, state_indices, y, workspace, status),
           dims, tensors, cu, p0, pt, rows, idx, y.data_ptr(), n_segments, opt)
     return y, ht
 
@@ -325,7 +325,7 @@ def gdr_selective_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, cu_
     out = (new(x), new(dt), new(A), new(B), new(C), new(D), new(z), new(dt_bias), dh0)
     grads = gdr_scan_grads(*[None if t is None else t.data_ptr() for t in out])
     _call(lib.gdr_selective_scan_bwd, index, stream,
-          (x, dt, A, B, C, dy, D, z, dt_bias, cu_seqlens, h0, dht, workspace) + out, dims,
+          (x, dt, A, B, C, dy, D, z, dt_bias, cu_seqlens, h0, dht, workspace, status) + out, dims,
           tensors, cu, p0, g, gt, grads, opt)
     return out
 

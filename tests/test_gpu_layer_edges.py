@@ -207,3 +207,25 @@ def test_captured_on_another_stream():
             t.zero_()
         graph.replay()
         same(got, want)
+
+
+def test_status_let_go():
+    """A status word that its caller has let go is not handed out again under a call."""
+    args = call_inputs()
+    s, w, taps, dy = args[:4]
+    side, _ = warm(args)
+    for call in (lambda **kw: gdr.gdr_short_conv_fwd(s["x"], taps, None, s["cu_seqlens"], **kw),
+                 lambda **kw: gdr.gdr_short_conv_bwd(s["x"], taps, dy, None, s["cu_seqlens"], **kw),
+                 lambda **kw: gdr.gdr_selective_scan_fwd(**s, **kw),
+                 lambda **kw: gdr.gdr_selective_scan_bwd(**s, dy=dy, **kw)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        at, done = status.data_ptr(), torch.cuda.Event()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(SLEEP)
+        call(status=status, stream=side)
+        done.record(side)
+        del status
+        new = [torch.empty(1, dtype=torch.int32, device="cuda") for _ in range(4)]
+        assert not done.query()
+        assert all(t.data_ptr() != at for t in new)
+        torch.cuda.synchronize()
