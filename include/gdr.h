@@ -453,7 +453,8 @@ size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cach
  * outputs and gradients; such a table is reported as GDR_ERR_SEQLENS all the
  * same.  Where offsets step back or leave [0, T], what the tokens get is
  * unspecified; nothing outside the tensors is read or written.
- * No output may overlap an input, unless it says so.
+ * No output may overlap an input or another output, unless it says so (one that
+ * begins where an input or another output does is refused).
  * opt may hold status, workspace (256-byte aligned) and the launch events; the
  * rest is zero.  Results are bit-identical from run to run.
  */

@@ -3,7 +3,7 @@ refuse before any work.  No compute call is made."""
 import pytest
 import torch
 
-from chunked_gated_delta_rule_gb300 import layer
+from chunked_gated_delta_rule_gb300 import api, layer
 
 D = 16
 
@@ -38,3 +38,67 @@ def test_outputs_in_32_bits_whatever_the_default():
     assert calls
     for n in calls:
         assert any(k.arg == "dtype" for k in n.keywords), f"line {n.lineno}"
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from chunked_gated_delta_rule_gb300 import build
+    build.build()
+    import chunked_gated_delta_rule_gb300 as pkg
+    return pkg.load_library()
+
+
+def at(i):
+    return 0x100000 * i
+
+
+SCAN_IN = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias")
+SCAN_OUT = ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")
+
+
+def scan_bwd(lib, h0=20, dy=21, dht=22, **place):
+    """The code of a backward scan whose outputs lie at 30, 31, ..., but for those in ``place``."""
+    ins = api.gdr_scan_tensors(*(at(1 + i) for i in range(8)))
+    out = api.gdr_scan_grads(*(at(place.get(n, 30 + i)) for i, n in enumerate(SCAN_OUT)))
+    dims = api.gdr_scan_dims(1, 64, 128, 16, 1, 0, api.GDR_F32, 0, 1)
+    return lib.gdr_selective_scan_bwd(dims, ins, None, at(h0), at(dy), at(dht), out, None, None)
+
+
+def test_gradients_of_the_scan_in_one_place(lib):
+    """dh0 in the place of h0: the launch that turns ends into starts reads the one and writes the
+    other, in blocks of which neither waits for the other."""
+    for i, name in enumerate(SCAN_OUT):
+        for place in list(range(1, 9)) + [20, 21, 22]:
+            assert scan_bwd(lib, **{name: place}) == -1, (name, place)
+        for j, other in enumerate(SCAN_OUT):
+            if other != name:
+                assert scan_bwd(lib, **{name: 30 + j}) == -1, (name, other)
+
+
+def conv_bwd(lib, **place):
+    dims = api.gdr_conv_dims(1, 64, 128, 4, 0, api.GDR_F32, 0, api.GDR_F32, 1)
+    out = [at(place.get(n, 30 + i)) for i, n in enumerate(("dx", "dw", "db", "dh0"))]
+    return lib.gdr_short_conv_bwd(dims, at(1), at(2), at(3), None, at(4), at(5), at(6), *out, None, None)
+
+
+def test_gradients_of_the_convolution_in_one_place(lib):
+    names = ("dx", "dw", "db", "dh0")
+    for name in names:
+        for place in range(1, 7):
+            assert conv_bwd(lib, **{name: place}) == -1, (name, place)
+        for j, other in enumerate(names):
+            if other != name:
+                assert conv_bwd(lib, **{name: 30 + j}) == -1, (name, other)
+
+
+def test_outputs_in_the_place_of_states_and_parameters(lib):
+    """Forward: y anywhere but in a place of its own, states in the place of anything but h0."""
+    dims = api.gdr_conv_dims(1, 64, 128, 4, 0, api.GDR_F32, 0, api.GDR_F32, 1)
+    for y, ht in ((2, 30), (3, 30), (4, 30), (30, 30), (31, 1), (31, 2), (31, 3)):
+        assert lib.gdr_short_conv_fwd(dims, at(1), at(2), at(3), None, at(4), at(ht), 1, None, at(y),
+                                      None, None) == -1, (y, ht)
+    ins = api.gdr_scan_tensors(*(at(1 + i) for i in range(8)))
+    dims = api.gdr_scan_dims(1, 64, 128, 16, 1, 0, api.GDR_F32, 0, 1)
+    for y, ht in [(i, 30) for i in list(range(1, 9)) + [20, 30]] + [(31, i) for i in range(1, 9)]:
+        assert lib.gdr_selective_scan_fwd(dims, ins, None, at(20), at(ht), 1, None, at(y), 0, None,
+                                          None) == -1, (y, ht)
