@@ -492,7 +492,8 @@ int gdr_rms_norm_fwd(const gdr_norm_dims *dims, const void *x, const void *resid
         (d.rows > 0 && (!x || !y || (quant && !scale))) || (!quant && scale))
         return GDR_ERR_INVALID;
     // two outputs in one place; values of other sizes over rows that are still to be read
-    if (over(y, {sum}) || (quant && over(y, {x, residual}))) return GDR_ERR_INVALID;
+    if (clash({sum, y, scale}, {weight}) || over(scale, {x, residual}) || (quant && over(y, {x, residual})))
+        return GDR_ERR_INVALID;
     NormArgs a{};
     a.x = x; a.res = residual; a.r = sum; a.y = y; a.scale = scale;
     a.w = Param{weight, d.weight_dtype == GDR_F32};
@@ -524,7 +525,8 @@ int gdr_rms_norm_bwd(const gdr_norm_dims *dims, const void *r, const void *weigh
     if (rc == GDR_OK) rc = check_options(opt);
     if (rc != GDR_OK) return rc;
     const gdr_norm_dims &d = *dims;
-    if (d.out_dtype != d.dtype || (d.rows > 0 && (!r || !dy || !dx)) || (dweight && !weight))
+    if (d.out_dtype != d.dtype || (d.rows > 0 && (!r || !dy || !dx)) || (dweight && !weight) ||
+        clash({dx, dweight}, {r, weight, dy, dsum}))
         return GDR_ERR_INVALID;
     NormArgs a{};
     a.r = const_cast<void *>(r); a.dy = dy; a.dres = dsum; a.dx = dx; a.dw = dweight;

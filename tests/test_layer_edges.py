@@ -102,3 +102,28 @@ def test_outputs_in_the_place_of_states_and_parameters(lib):
     for y, ht in [(i, 30) for i in list(range(1, 9)) + [20, 30]] + [(31, i) for i in range(1, 9)]:
         assert lib.gdr_selective_scan_fwd(dims, ins, None, at(20), at(ht), 1, None, at(y), 0, None,
                                           None) == -1, (y, ht)
+
+
+def test_norm_outputs_in_one_place(lib):
+    """Backward: dx is written as dense rows, over rows at other strides that other blocks still
+    read.  Both ways: the weight is read by every row, a scale is no row."""
+    def bwd(dx=30, dw=31, **kw):
+        dims = api.gdr_norm_dims(64, 128, api.GDR_F32, api.GDR_F32, api.GDR_F32, 0, 1e-6)
+        for k, v in kw.items():
+            setattr(dims, k, v)
+        return lib.gdr_rms_norm_bwd(dims, at(1), at(2), at(3), at(4), at(dx), at(dw), None, None)
+
+    for place in (1, 2, 3, 4):
+        assert bwd(dx=place) == -1 and bwd(dw=place) == -1, place
+    for strides in (dict(x_stride=256), dict(y_stride=256), dict(residual_stride=256)):
+        for place in (1, 3, 4):
+            assert bwd(dx=place, **strides) == -1, (place, strides)
+    assert bwd(dx=31) == -1
+
+    def fwd(out=30, y=31, scale=32):
+        dims = api.gdr_norm_dims(64, 128, api.GDR_F32, api.GDR_F32, api.GDR_I8, 0, 1e-6)
+        return lib.gdr_rms_norm_fwd(dims, at(1), at(2), at(3), at(out), at(y), at(scale), None, None)
+
+    assert fwd(out=3) == -1 and fwd(y=3) == -1
+    for place in (1, 2, 3, 30, 31):
+        assert fwd(scale=place) == -1, place
