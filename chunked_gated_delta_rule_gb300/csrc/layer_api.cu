@@ -404,7 +404,9 @@ int gdr_selective_scan_fwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
     a.bytes = (int)common_bytes({(uint64_t)a.bytes, addr(y)});
     a.st_bytes = common_bytes({addr(h0), addr(ht), addr(in->A)});
     Call call(opt, stream);
-    if (n_segments == 0 && longest_of(d) <= kFewTokens) {
+    // its kernel counts warps, of 32 channels of a sequence each, in 32 bits
+    const bool step = longest_of(d) <= kFewTokens && (seqs + 1) * scan_tiles(d.C, 32, (int)d.G) <= UINT32_MAX;
+    if (n_segments == 0 && step) {
         call.run(kKScanStep, [&] { return scan_step(a, d.dtype, call.st); });
         return call.done();
     }

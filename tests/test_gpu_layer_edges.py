@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import chunked_gated_delta_rule_gb300 as gdr
-from layer_ref import close, rms_norm
+from layer_ref import close, rms_norm, selective_scan
 
 pytestmark = pytest.mark.gpu
 
@@ -229,3 +229,20 @@ def test_status_let_go():
         assert not done.query()
         assert all(t.data_ptr() != at for t in new)
         torch.cuda.synchronize()
+
+
+def test_scan_of_single_tokens_of_more_warps_than_32_bits_count():
+    """2^21 sequences of 65536 channels, 2^32 warps of 32 channels and one more sequence's, all but
+    the first and the last empty: the last one's tokens are written too."""
+    N, C, T = 1 << 21, 65536, 3
+    cu = torch.ones(N + 1, dtype=torch.int32, device="cuda")
+    cu[0], cu[-1] = 0, T
+    x, dt, bc = randn(1, T, C), randn(1, T, C, seed=1) - 1.0, randn(1, T, 2, 1, 1, seed=2)
+    A, status = -torch.exp(randn(C, 1, seed=3)), torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.full_like(x, float("nan"))
+    gdr.gdr_selective_scan_fwd(x, dt, A, bc[:, :, 0], bc[:, :, 1], cu_seqlens=cu, max_seqlen=2, y=y,
+                               output_final_state=False, status=status)
+    want, _ = selective_scan(*(t.cpu().double() for t in (x[0], dt[0], A, bc[0, :, 0], bc[0, :, 1])),
+                             None, None, None, [1, 2])
+    close("y", y[0], want)
+    assert int(status) == 0
