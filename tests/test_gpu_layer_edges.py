@@ -246,3 +246,80 @@ def test_scan_of_single_tokens_of_more_warps_than_32_bits_count():
                              None, None, None, [1, 2])
     close("y", y[0], want)
     assert int(status) == 0
+
+
+def view_of(t, at, pitch):
+    """The same values as columns [at, at + C) of rows of ``pitch``."""
+    big = randn(*t.shape[:-1], pitch, seed=50 + at).to(t.dtype)
+    view = big[..., at:at + t.shape[-1]]
+    view.copy_(t)
+    assert not view.is_contiguous()
+    return view
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("C,at,pitch", [(48, 0, 64), (48, 16, 80), (48, 3, 64), (48, 8, 61), (45, 1, 50)])
+def test_gradients_that_come_in_as_views(C, at, pitch, dtype):
+    """dy (and x, as the layer has it) as slices of wider rows, on 16 bytes and off them: the bits
+    of contiguous tensors, packed and dense."""
+    lens = [5, 70, 0, 13, 20]
+    T = sum(lens)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    x, dy, z = (randn(1, T, C, seed=i, dtype=dtype) for i in range(3))
+    taps, bias = randn(C, 4, seed=3, dtype=dtype), randn(C, seed=4, dtype=dtype)
+    dht = randn(5, 3, C, seed=5, dtype=dtype)
+    bc = randn(1, T, 2, 1, 16, seed=6, dtype=dtype)
+    A, D = -torch.exp(randn(C, 16, seed=7)), randn(C, seed=8)
+
+    def conv(x, dy, cu, dht=None):
+        return gdr.gdr_short_conv_bwd(x, taps, dy, bias, cu, None, dht, want_dh0=True)
+
+    def scan(x, dy, z, bc, cu):
+        return gdr.gdr_selective_scan_bwd(x, x, A, bc[..., 0, :, :], bc[..., 1, :, :], dy, D, z, D, cu,
+                                          want_dh0=True)
+
+    vx, vdy, vz = (view_of(t, at, pitch) for t in (x, dy, z))
+    want = conv(x, dy, cu, dht)
+    for a, b in ((vx, vdy), (x, vdy), (vx, dy)):
+        got = conv(a, b, cu, dht)
+        # rows off 16 bytes, or of an odd number of channels, are summed in other runs
+        assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+        close("dweight", got[1], want[1])
+        close("dbias", got[2], want[2])
+    want = scan(x, dy, z, bc, cu)
+    for a, b, c in ((vx, vdy, vz), (x, vdy, z), (vx, dy, z)):
+        for got, w in zip(scan(a, b, c, bc, cu), want):
+            assert torch.equal(got, w)
+    # four dense rows of 27 tokens
+    rows = [t.reshape(4, 27, *t.shape[2:]) for t in (x, dy, z, bc)]
+    wide = [view_of(t, at, pitch) for t in rows[:3]]
+    want = scan(*rows, None)
+    for got, w in zip(scan(*wide, rows[3], None), want):
+        assert torch.equal(got, w)
+    want, got = conv(rows[0], rows[1], None), conv(wide[0], wide[1], None)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[3], want[3])
+    close("dweight", got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("D,at,pitch", [(96, 0, 128), (96, 8, 104), (96, 2, 100), (96, 1, 97), (1026, 2, 1100),
+                                        (2048, 8, 2064), (2048, 3, 2060), (5120, 2, 5200), (10001, 1, 10007)])
+def test_norm_gradients_of_views(D, at, pitch, dtype):
+    """r, dy and dr as slices of wider rows, one at a time and together: whatever width they are
+    loaded in, the gradients of 64 bits."""
+    rows = 40
+    r, dy, dr = (randn(rows, D, seed=i, dtype=dtype) for i in range(3))
+    w = randn(D, seed=3, dtype=dtype)
+    lr, lw = (t.cpu().double().requires_grad_() for t in (r, w))
+    ((rms_norm(lr, lw, 1e-6) * dy.cpu().double()).sum() + (lr * dr.cpu().double()).sum()).backward()
+    vr, vdy, vdr = (view_of(t, at, pitch) for t in (r, dy, dr))
+    for a, b, c in ((vr, vdy, vdr), (vr, dy, dr), (r, vdy, dr), (r, dy, vdr)):
+        dx, dw = gdr.gdr_rms_norm_bwd(b, a, w, c)
+        close("dx", dx, lr.grad)
+        close("dweight", dw, lw.grad)
+    x = r.clone().requires_grad_()
+    y, _ = gdr.rms_norm(x, w)
+    y.backward(vdy)
+    lr.grad = None
+    (rms_norm(lr, lw, 1e-6) * dy.cpu().double()).sum().backward()
+    close("dx", x.grad, lr.grad)
