@@ -323,3 +323,101 @@ def test_norm_gradients_of_views(D, at, pitch, dtype):
     lr.grad = None
     (rms_norm(lr, lw, 1e-6) * dy.cpu().double()).sum().backward()
     close("dx", x.grad, lr.grad)
+
+
+def big_randn(*shape):
+    """A few GB of BF16, made on the device."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    return torch.empty(*shape, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+
+
+def test_channels_at_offsets_of_more_than_32_bits():
+    """More than 2^31 values of x: the last sequence's outputs and gradients are those of a call on
+    it alone.  (The sums over all tokens, which the other sequence is part of, are left out.)"""
+    C, T, tail = 65536, 32900, 77
+    x, dy = big_randn(1, T, C), big_randn(1, T, C)
+    cu = torch.tensor([0, T - tail, T], dtype=torch.int32, device="cuda")
+    taps, bias = randn(C, 4, dtype=torch.bfloat16), randn(C, seed=1, dtype=torch.bfloat16)
+    part, part_dy = x[:, -tail:], dy[:, -tail:]
+    y, ht = gdr.gdr_short_conv_fwd(x, taps, bias, cu, output_final_state=True)
+    y1, ht1 = gdr.gdr_short_conv_fwd(part, taps, bias, output_final_state=True, max_seqlen=tail)
+    assert torch.equal(y[:, -tail:], y1) and torch.equal(ht[1:], ht1)
+    del y
+    dx = gdr.gdr_short_conv_bwd(x, taps, dy, bias, cu)[0]
+    assert torch.equal(dx[:, -tail:], gdr.gdr_short_conv_bwd(part, taps, part_dy, bias)[0])
+    del dx
+    A, bc = -torch.exp(randn(C, 1, seed=2)), randn(1, T, 2, 1, 1, seed=3, dtype=torch.bfloat16)
+    B1, C1 = bc[:, :, 0], bc[:, :, 1]
+    ends = B1[:, -tail:], C1[:, -tail:]
+    for n in (1, 40):
+        y, ht = gdr.gdr_selective_scan_fwd(x, x, A, B1, C1, cu_seqlens=cu, n_segments=n, max_seqlen=T)
+        y1, ht1 = gdr.gdr_selective_scan_fwd(part, part, A, *ends, n_segments=1)
+        close("y", y[:, -tail:], y1)
+        close("ht", ht[1:], ht1)
+        del y
+    got = gdr.gdr_selective_scan_bwd(x, x, A, B1, C1, dy, cu_seqlens=cu, want_dh0=True)
+    want = gdr.gdr_selective_scan_bwd(part, part, A, *ends, part_dy, want_dh0=True)
+    for i in (0, 1, 3, 4):  # dx, ddt, dB, dC
+        assert torch.equal(got[i][:, -tail:], want[i]), i
+    assert torch.equal(got[8][1:], want[8])
+
+
+def test_pools_at_offsets_of_more_than_32_bits():
+    C, S, rows = 4096, 64, 8300  # 2^31 values end in row 8192
+    scan = torch.zeros(rows, C, S, device="cuda")
+    conv = torch.zeros(350000, 3, 2 * C, dtype=torch.bfloat16, device="cuda")  # 8.6e9 values
+    idx = torch.tensor([8299, 8191, 8192], dtype=torch.int32, device="cuda")
+    far = torch.tensor([349999, 87381, 174763], dtype=torch.int32, device="cuda")
+    x = randn(3, 1, C)
+    bc = randn(3, 1, 2, 1, S, seed=1)
+    A = -torch.exp(randn(C, S, seed=2))
+    h = randn(3, C, S, seed=3)
+    scan[idx.long()] = h
+    y, _ = gdr.gdr_selective_scan_fwd(x, x, A, bc[:, :, 0], bc[:, :, 1], state=scan, state_indices=idx)
+    y1, h1 = gdr.gdr_selective_scan_fwd(x, x, A, bc[:, :, 0], bc[:, :, 1], h0=h)
+    assert torch.equal(y, y1) and torch.equal(scan[idx.long()], h1)
+    scan[idx.long()] = 0
+    assert not any(part.any() for part in scan.split(1024))
+    x, h = randn(3, 1, 2 * C, dtype=torch.bfloat16), randn(3, 3, 2 * C, seed=4, dtype=torch.bfloat16)
+    taps = randn(2 * C, 4, seed=5, dtype=torch.bfloat16)
+    conv[far.long()] = h
+    y, _ = gdr.gdr_short_conv_fwd(x, taps, state=conv, state_indices=far)
+    y1, h1 = gdr.gdr_short_conv_fwd(x, taps, h0=h, output_final_state=True)
+    assert torch.equal(y, y1) and torch.equal(conv[far.long()], h1)
+    conv[far.long()] = 0
+    assert not any(part.any() for part in conv.split(32768))
+
+
+def test_norm_of_rows_at_offsets_of_more_than_32_bits():
+    D, rows, tail = 8192, (1 << 18) + 100, 100
+    x, dy, w = big_randn(rows, D), big_randn(rows, D), randn(D, dtype=torch.bfloat16)
+    exact = rms_norm(x[-tail:].cpu().double(), w.cpu().double(), 1e-6)
+    close("y", gdr.gdr_rms_norm_fwd(x, w)[0][-tail:], exact)
+    q, r, scale = gdr.gdr_rms_norm_fwd(x, w, dy, dtype=torch.int8, group=128)
+    assert torch.equal(r[-tail:], (x[-tail:].float() + dy[-tail:].float()).bfloat16())
+    r1 = r[-tail:].cpu().double()
+    del r
+    back = q[-tail:].cpu().double().reshape(tail, -1, 128) * scale[-tail:].cpu().double()[..., None]
+    err = (back.reshape(tail, D) - rms_norm(r1, w.cpu().double(), 1e-6)).reshape(tail, -1, 128).abs().amax(-1)
+    assert (err <= 0.501 * scale[-tail:].cpu().double()).all()  # half a step, and FP32's arithmetic
+    del q, scale
+    dx, _ = gdr.gdr_rms_norm_bwd(dy, x, w)
+    leaf = x[-tail:].cpu().double().requires_grad_()
+    (rms_norm(leaf, w.cpu().double(), 1e-6) * dy[-tail:].cpu().double()).sum().backward()
+    close("dx", dx[-tail:], leaf.grad)
+
+
+def test_one_tensor_as_both_inputs():
+    """x as its own residual, and as the time step: its gradient is the sum of both."""
+    x, w, dy = randn(9, 64), randn(64, seed=1), randn(9, 64, seed=2)
+    leaf, ref = x.clone().requires_grad_(), x.cpu().double().requires_grad_()
+    gdr.rms_norm(leaf, w, leaf)[0].backward(dy)
+    rms_norm(ref + ref, w.cpu().double(), 1e-6).backward(dy.cpu().double())
+    close("dx", leaf.grad, ref.grad)
+    s = scan_inputs((40,))
+    leaf, ref = s["x"].clone().requires_grad_(), s["x"][0].cpu().double().requires_grad_()
+    gdr.selective_scan(leaf, leaf, s["A"], s["B"], s["B"], None, leaf)[0].square().sum().backward()
+    A, B = s["A"].cpu().double(), s["B"][0].cpu().double()
+    selective_scan(ref, ref, A, B, B, None, ref, None, [40])[0].square().sum().backward()
+    # a loss of squares: what is left of y in FP32 counts twice
+    close("dx", leaf.grad[0], ref.grad, work=2e-5)
