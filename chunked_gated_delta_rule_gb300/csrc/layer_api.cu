@@ -129,8 +129,9 @@ int check_conv(const gdr_conv_dims *d) {
 
 // Tokens of a run, at most about `most`: long ones read few rows twice and leave few sums, and the
 // threads (one for each vector of channels of a run) fill the device a whole number of times.  64K
-// tokens x 2048 channels, forward at most 32 / 64 / 128 / 256: 102 / 103 / 111 / 113 us; backward with
-// its sums 64 / 128 / 256 / 512: 222 / 204 / 192 / 186 us (before its addresses were counted on: now 175).
+// tokens x 2048 channels, by events around each launch, cold: forward at most 32 / 64 / 128 / 256: 101 /
+// 102 / 110 / 113 us; backward with its sums 64 / 128 / 256 / 512: 218 / 196 / 182 / 175 us (the kernels
+// alone, as they are: 92 and 167).
 int run_of(int64_t tokens, int64_t vectors, int most) {
     const int64_t fill = (int64_t)device_sms() * kConvThreads, all = tokens * vectors;
     const int64_t waves = ceil_div(all, fill * most);
@@ -199,7 +200,7 @@ int64_t scan_piece(const gdr_scan_dims &d, int n_segments) {
         int64_t least = longest * (slow > 100 * mine ? slow : 100 * mine);
         // Pieces that fill four blocks an SM a whole number of times: 163 a token of a block in both
         // passes, less where a last round leaves blocks out; beginnings and ends; the join.
-        // (2048 channels, whole / in pieces.  16 states: one sequence of 16384 tokens 1530 / 278 us, 4 of
+        // (2048 channels in BF16, whole / in pieces; FP32 goes by the same.  16 states: one sequence of 16384 tokens 1530 / 278 us, 4 of
         // 4096 389 / 287, 5 of 2048 245 / 191, 8 of 2048 245 / 287, 32 of 320 112 / 197.  8 states, 8 of 2048:
         // 291 us, in 5 pieces each, 640 blocks where 608 fit, 282, in 10 225.  64 states, one of
         // 16384: 2850 us; in pieces of 4096 tokens 1688, 3277 2174, 1171 1355, 863 1367.)

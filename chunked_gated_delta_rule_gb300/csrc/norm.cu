@@ -9,13 +9,14 @@
 //   dx = rstd (w dy - n mean(w dy n)) + dres with n = r rstd;  dw = sum over rows of dy n.
 //
 // Bound by memory: each value is read once and written once, r stays in
-// registers between the sum of squares and the product.  A warp takes a row
-// alone, without waiting for others, as long as there are rows enough to fill
-// the device; with fewer rows a block takes one.
+// registers between the sum of squares and the product.  A row of up to 1024
+// values (32 of a thread) is a warp's, which waits for no other, as long as there
+// are rows enough to fill the device.  Wider rows take a block of as few warps as
+// hold them, and few rows one of more.
 //
 // BF16, 64K rows of 2048 with a residual into E4M3 with scales a 128 columns: 150 us (940 MB,
-// 6.3 TB/s, 0.93 of what a copy reaches).  16K rows of 4096: forward 76 us, backward 102 and its
-// sums 10 (537 MB each; 7.1 TB/s, some of it left in L2, and 5.3: three rows and the sums leave a
+// 6.3 TB/s, 0.93 of what a copy reaches).  16K rows of 4096: forward 77 us, backward 102 and its
+// sums 12 (537 MB each; 7.0 TB/s, some of it left in L2, and 5.3: three rows and the sums leave a
 // thread 128 registers, so few rows are under way while others are summed).
 #include <cuda_fp8.h>
 

@@ -216,9 +216,11 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// Two FP32 values in a register pair, worked on by one instruction.  It holds its scheduler's port
-// for two cycles, so what it saves is the rest of an instruction's cost: the scan's inner loop takes
-// 5.5 cycles a state with pairs and 6.2 without (8 states of a channel, measured alone).
+// Two FP32 values in a register pair, worked on by one instruction.  It takes the FMA pipe for two
+// cycles, as two single ones do (2.1 cycles a scheduler either way, measured alone), so what it saves
+// is the second one's issue slot, which others take meanwhile (with one integer operation beside it 2.4
+// cycles, with two 2.9): the scan's inner loop takes 5.5 cycles a state with pairs and 6.2 without (8
+// states of a channel, measured alone).
 struct F2 {
     uint64_t v;
 };

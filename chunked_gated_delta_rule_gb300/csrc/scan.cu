@@ -6,8 +6,8 @@
 // with B_t and C_t shared by the channels of a group.  FP32 states and sums.
 //
 // Every (token, channel, state) takes one exponential (its decay depends on all
-// three) and four FP32 operations, and no matrix product does them: the
-// schedulers' ports bound it, not the memory.  So the scan runs along the tokens
+// three) and four FP32 operations, and no matrix product does them: instructions
+// and their latencies bound it, not the memory.  So the scan runs along the tokens
 // as it is written, each state's chain in a register, and whatever else a token
 // needs is kept off the inner loop: a tile of tokens is staged in shared memory
 // with d_t and d_t x_t computed once a channel, and the D and z terms are added
@@ -19,9 +19,12 @@
 // the sum of its time steps (the piece's decay is exp(A sum d), so no products
 // of decays are kept); a join turns the ends into starts; a second pass runs
 // the pieces from those.  That takes the exponentials twice.  One sequence of 16K
-// tokens x 2048 channels x 16 states: 112, 6 and 163 us; the passes take 8.3 and 12
-// cycles a scheduler for 32 states, of which the instructions hold the port for
-// about 80% (a packed one for two cycles); the loop alone would take 5.5.
+// tokens x 2048 channels x 16 states: 109, 9 and 168 us; the passes take about 8 and
+// 12.5 cycles a scheduler for 32 states, the loop alone would take 5.5.  No unit is
+// full (issue slots 59 and 60%, the FMA pipe 56 and 53%, exponentials 58 and 41%):
+// with four warps a scheduler (128 registers a thread) a warp mostly waits for the
+// result of its own last instruction, for a pipe that another has, and in the second
+// pass for shared memory.
 #include "scan.cuh"
 
 namespace gdr {

@@ -24,11 +24,13 @@
 // channels for dB and dC.  A thread therefore has two channels of four states (the
 // channels' sums begin in its registers), and lanes fold eight values at once, so
 // that a shuffle carries a value that is still wanted.  The decays are formed a
-// second time on the way back: an exponential costs less than the registers.  Four
-// blocks an SM, and rows on their way to shared memory while a tile is worked on,
-// keep the ports about 80% busy (8 x 2048 tokens x 2048 channels x 16 states: 680 us; with
-// three blocks and a forward sweep of its own in place of what the first pass
-// leaves, 846).
+// second time on the way back: an exponential costs less than the registers.  Rows
+// are on their way to shared memory while a tile is worked on, and four blocks fit an
+// SM with 9 to 32 states (three with up to 8 or over 32 in 16 bits, two in FP32: there
+// shared memory is what limits them).  8 x 2048 tokens x 2048 channels x 16 states: 680
+// us; with three blocks and a forward sweep of its own in place of what the first pass
+// leaves, 846.  Issue slots are 65% taken and no pipe more than 46%, shared memory 69%:
+// as in the forward scan, what is left are latencies that four warps a scheduler leave.
 #include "scan.cuh"
 
 namespace gdr {

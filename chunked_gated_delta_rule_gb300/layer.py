@@ -198,7 +198,8 @@ def gdr_short_conv_fwd(x, weight, bias=None, cu_seqlens=None, h0=None, *, activa
     will follow.  With ``state`` [P, W - 1, C] the rows ``state_indices`` (row n if None) of a
     pool take the place of both, in place.  Returns ``(y, ht)``; ht is ``state``, or None unless
     wanted.  ``max_seqlen`` is a planning hint, as everywhere.  Work is enqueued on ``stream``
-    (default: the current one) and not synchronised."""
+    (default: the current one) and not synchronised; outputs made here are then in memory of
+    ``stream``, which is also kept for what the current stream has to do when they are let go."""
     lib = load_library()
     index, dims, nseq, w, b, cu = _conv_call("gdr_short_conv_fwd", x, weight, bias, cu_seqlens,
                                              activation, max_seqlen)
@@ -359,7 +360,8 @@ def gdr_rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-6, dtype=None, gro
     or float32.  ``dtype`` float8_e4m3fn or int8 quantises y, with a float32 scale for each row
     (``scale`` [...]) or, with ``group`` 128, for each 128 columns ([..., ceil(D / 128)]), as
     :func:`gdr_cache_write` does.  Returns ``(y, r, scale)``; r is None without a residual, scale
-    unless y is quantised.  ``residual_out`` may be the residual or x itself, ``y`` x (in place)."""
+    unless y is quantised.  ``residual_out`` may be the residual or x itself, ``y`` x (in place).
+    Rows may be slices of wider ones; one row broadcast to many is refused."""
     lib = load_library()
     index, own, shape = x.get_device(), x.dtype, x.shape
     if index < 0:

@@ -451,7 +451,8 @@ size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cach
  * at most 2^31 - 1 tokens.
  * A token that no sequence holds (before cu[0], from cu[N] on) gets zeros as its
  * outputs and gradients; such a table is reported as GDR_ERR_SEQLENS all the
- * same.  Where offsets step back or leave [0, T], what the tokens get is
+ * same, and many such tokens take their time: the scan and the calls of few
+ * tokens a sequence clear them one row or a few after another.  Where offsets step back or leave [0, T], what the tokens get is
  * unspecified; nothing outside the tensors is read or written.
  * No output may overlap an input or another output, unless it says so (one that
  * begins where an input or another output does is refused).
@@ -571,7 +572,8 @@ size_t gdr_selective_scan_bwd_workspace_size(const gdr_scan_dims *dims);
  *                     round(y / s), 0 where s = 0; s = NaN and q = 0 where a y is
  *                     not finite.  y may be x in place (same dtype).
  * In place means the same rows at the same stride.
- * FP32 sums: rows whose sum of squares passes FP32's range get zeros.
+ * FP32 sums: rows whose sum of squares passes FP32's range get zeros, and with eps
+ * 0 rows whose squares vanish in it infinities (a row of zeros NaN).
  */
 typedef struct gdr_norm_dims {
     int64_t rows, D;
