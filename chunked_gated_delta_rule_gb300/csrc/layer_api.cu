@@ -328,7 +328,8 @@ int gdr_short_conv_fwd(const gdr_conv_dims *dims, const void *x, const void *wei
     const int64_t tokens = tokens_of(d), seqs = d.N > 0 ? d.N : d.B;
     if (!weight || (tokens > 0 && (!x || !y)) || (cu_seqlens != nullptr) != (d.N > 0)) return GDR_ERR_INVALID;
     if ((h0 || ht) ? n_states < (state_indices ? 1 : seqs) : state_indices != nullptr) return GDR_ERR_INVALID;
-    if (over(y, {h0}) || clash({y, ht}, {x, weight, bias})) return GDR_ERR_INVALID;
+    if (over(y, {h0}) || clash({y, ht}, {x, weight, bias, cu_seqlens, state_indices}))
+        return GDR_ERR_INVALID;
     ConvArgs a = conv_args(d, x, weight, bias, cu_seqlens, opt);
     a.h0 = h0; a.ht = ht; a.y = y;
     a.n_states = n_states;
@@ -359,7 +360,7 @@ int gdr_short_conv_bwd(const gdr_conv_dims *dims, const void *x, const void *wei
     const int64_t tokens = tokens_of(d);
     if (!weight || !dweight || (tokens > 0 && (!x || !dy || !dx)) || (dbias && !bias) ||
         (cu_seqlens != nullptr) != (d.N > 0) ||
-        clash({dx, dweight, dbias, dh0}, {x, weight, bias, h0, dy, dht}))
+        clash({dx, dweight, dbias, dh0}, {x, weight, bias, cu_seqlens, h0, dy, dht}))
         return GDR_ERR_INVALID;
     ConvArgs a = conv_args(d, x, weight, bias, cu_seqlens, opt);
     a.h0 = h0; a.dy = dy; a.dht = dht; a.dx = dx; a.dh0 = dh0;
@@ -396,7 +397,7 @@ int gdr_selective_scan_fwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
         return GDR_ERR_INVALID;
     if ((h0 || ht) ? n_states < (state_indices ? 1 : seqs) : state_indices != nullptr) return GDR_ERR_INVALID;
     if (over(y, {h0}) ||
-        clash({y, ht}, {in->x, in->dt, in->A, in->B, in->C, in->D, in->z, in->dt_bias}))
+        clash({y, ht}, {in->x, in->dt, in->A, in->B, in->C, in->D, in->z, in->dt_bias, cu_seqlens, state_indices}))
         return GDR_ERR_INVALID;
     ScanArgs a = scan_args(d, *in, cu_seqlens, opt);
     a.h0 = h0; a.ht = ht; a.y = y;
@@ -447,7 +448,7 @@ int gdr_selective_scan_bwd(const gdr_scan_dims *dims, const gdr_scan_tensors *in
         (out->dD && !in->D) || (out->ddt_bias && !in->dt_bias) || (out->dz && !in->z))
         return GDR_ERR_INVALID;
     if (clash({out->dx, out->ddt, out->dA, out->dB, out->dC, out->dD, out->dz, out->ddt_bias, out->dh0},
-              {in->x, in->dt, in->A, in->B, in->C, in->D, in->z, in->dt_bias, h0, dy, dht}))
+              {in->x, in->dt, in->A, in->B, in->C, in->D, in->z, in->dt_bias, cu_seqlens, h0, dy, dht}))
         return GDR_ERR_INVALID;
     if (tokens > INT32_MAX * (int64_t)128 / (d.G * d.S)) return GDR_ERR_UNSUPPORTED;  // blocks of dB, dC
     ScanArgs a = scan_args(d, *in, cu_seqlens, opt);

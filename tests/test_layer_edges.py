@@ -127,3 +127,22 @@ def test_norm_outputs_in_one_place(lib):
     assert fwd(out=3) == -1 and fwd(y=3) == -1
     for place in (1, 2, 3, 30, 31):
         assert fwd(scale=place) == -1, place
+
+
+def test_outputs_in_the_place_of_offsets_and_indices(lib):
+    f32 = api.GDR_F32
+    conv = api.gdr_conv_dims(1, 64, 128, 4, 2, f32, 0, f32, 1)
+    scan = api.gdr_scan_dims(1, 64, 128, 16, 1, 2, f32, 0, 1)
+    ins = api.gdr_scan_tensors(*(at(1 + i) for i in range(8)))
+    for y, ht in ((40, 31), (41, 31), (30, 40), (30, 41)):  # offsets at 40, indices at 41
+        assert lib.gdr_short_conv_fwd(conv, at(1), at(2), at(3), at(40), at(20), at(ht), 2, at(41), at(y),
+                                      None, None) == -1, (y, ht)
+        assert lib.gdr_selective_scan_fwd(scan, ins, at(40), at(20), at(ht), 2, at(41), at(y), 0, None,
+                                          None) == -1, (y, ht)
+    for i in range(4):
+        out = [at(40 if k == i else 30 + k) for k in range(4)]
+        assert lib.gdr_short_conv_bwd(conv, at(1), at(2), at(3), at(40), at(4), at(5), at(6), *out, None,
+                                      None) == -1, i
+    for i in range(9):
+        out = api.gdr_scan_grads(*(at(40 if k == i else 30 + k) for k in range(9)))
+        assert lib.gdr_selective_scan_bwd(scan, ins, at(40), at(20), at(21), at(22), out, None, None) == -1, i
