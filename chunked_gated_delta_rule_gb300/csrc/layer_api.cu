@@ -200,10 +200,10 @@ int64_t scan_piece(const gdr_scan_dims &d, int n_segments) {
         int64_t least = longest * (slow > 100 * mine ? slow : 100 * mine);
         // Pieces that fill four blocks an SM a whole number of times: 163 a token of a block in both
         // passes, less where a last round leaves blocks out; beginnings and ends; the join.
-        // (2048 channels in BF16, whole / in pieces; FP32 goes by the same.  16 states: one sequence of 16384 tokens 1530 / 278 us, 4 of
-        // 4096 389 / 287, 5 of 2048 245 / 191, 8 of 2048 245 / 287, 32 of 320 112 / 197.  8 states, 8 of 2048:
-        // 291 us, in 5 pieces each, 640 blocks where 608 fit, 282, in 10 225.  64 states, one of
-        // 16384: 2850 us; in pieces of 4096 tokens 1688, 3277 2174, 1171 1355, 863 1367.)
+        // (2048 channels in BF16, whole / in pieces; FP32 goes by the same.  16 states: one sequence of 16384
+        // tokens 1530 / 278 us, 4 of 4096 389 / 287, 5 of 2048 245 / 191, 8 of 2048 245 / 287, 32 of 320 112 /
+        // 197.  8 states, 8 of 2048: 291 us, in 5 pieces each, 640 blocks where 608 fit, 282, in 10 225.  64
+        // states, one of 16384: 2850 us; in pieces of 4096 tokens 1688, 3277 2174, 1171 1355, 863 1367.)
         for (int64_t rounds = 1; rounds <= 4; ++rounds) {
             const int64_t blocks = rounds * 4 * sms, fit = blocks / tiles;  // pieces
             const int64_t each = equal ? fit / seqs : fit;

@@ -452,8 +452,9 @@ size_t gdr_attn_workspace_size(const gdr_dims *dims, const gdr_paged_cache *cach
  * A token that no sequence holds (before cu[0], from cu[N] on) gets zeros as its
  * outputs and gradients; such a table is reported as GDR_ERR_SEQLENS all the
  * same, and many such tokens take their time: the scan and the calls of few
- * tokens a sequence clear them one row or a few after another.  Where offsets step back or leave [0, T], what the tokens get is
- * unspecified; nothing outside the tensors is read or written.
+ * tokens a sequence clear them one row or a few after another.  Where offsets
+ * step back or leave [0, T], what the tokens get is unspecified; nothing outside
+ * the tensors is read or written.
  * No output may overlap an input or another output, unless it says so (one that
  * begins where an input or another output does is refused).
  * opt may hold status, workspace (256-byte aligned) and the launch events; the
